@@ -1,5 +1,5 @@
 """ctypes binding of libswin_wattn (include/swin_wattn.h, swin_wattn_test.h,
-swin_block.h, swin_wattn_backward.h).
+swin_block.h, swin_wattn_backward.h, swin_rms.h).
 
 Argument marshalling only: every function here passes tensor pointers and
 sizes to the C ABI of the same name and raises on a non-OK status.  torch is
@@ -66,6 +66,12 @@ _SIGNATURES = {
                             "p", "p", "p"],
     "swin_wattn_cpb_backward": ["p", "p", "p", "p", "i", "p", "p", "p", "p", "p"],
     "swin_wattn_backward_launches": ["p"],
+    "swin_block_rms_create": ["pp", "i", "f"],
+    "swin_block_rms_forward": ["p", "p", "p", "i", "p", "p", "p", "p"],
+    "swin_block_rms_forward_q8": ["p", "p", "p", "i", "p", "p", "p", "p", "p"],
+    "swin_block_rms_backward": ["p", "p", "i", "p", "p", "p", "p", "p", "p"],
+    "swin_block_rms_last_launches": ["p"],
+    "swin_block_rms_destroy": ["p"],
 }
 
 # swin_block_params (include/swin_block.h), field for field
@@ -75,7 +81,8 @@ BLOCK_PARAM_FIELDS = ("ln1_gamma", "ln1_beta", "Wqkv", "bqkv", "bias_table", "lo
 
 class BlockParams(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in BLOCK_PARAM_FIELDS]
-_CT = {"p": ctypes.c_void_p, "pp": ctypes.POINTER(ctypes.c_void_p), "i": ctypes.c_int, "l": ctypes.c_int64}
+_CT = {"p": ctypes.c_void_p, "pp": ctypes.POINTER(ctypes.c_void_p), "i": ctypes.c_int, "l": ctypes.c_int64,
+       "f": ctypes.c_float}
 
 
 def load(build_if_missing: bool = True):
@@ -314,3 +321,73 @@ def swin_merge_forward(h, x, gamma, beta, Wm, out, stream=None):
     B, H, W, _ = x.shape
     return _check("swin_merge_forward", load().swin_merge_forward(
         h, _p(x), B, H, W, _p(gamma), _p(beta), _p(Wm), _p(out), _stream(stream)))
+
+
+# ---- swin_rms.h ------------------------------------------------------------------
+
+def _arg(name, t, dtype, *shape):
+    """Pointer of a required argument, checked: dtype, shape, contiguous, on the
+    current CUDA device."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be of shape %s, not %s" % (name, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device" % name)
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, *shape):
+    """The same for an optional argument (None -> NULL)."""
+    return None if t is None else _arg(name, t, dtype, *shape)
+
+
+def _rows(x):
+    """rows, C of x [..., C]."""
+    C = x.shape[-1]
+    return (x.numel() // C if C else 0), C
+
+
+def swin_block_rms_create(C, eps=1e-6):
+    h = ctypes.c_void_p()
+    _check("swin_block_rms_create", load().swin_block_rms_create(ctypes.byref(h), C, eps))
+    return h
+
+
+def swin_block_rms_destroy(h):
+    return _check("swin_block_rms_destroy", load().swin_block_rms_destroy(h))
+
+
+def swin_block_rms_last_launches(h):
+    return load().swin_block_rms_last_launches(h)
+
+
+def swin_block_rms_forward(h, x, gamma, out, residual=None, out_sum=None, stream=None):
+    """out = RMS norm of x + residual over the last axis of x [..., C]; out_sum
+    receives the sum."""
+    rows, C = _rows(x)
+    bf, shape = torch.bfloat16, x.shape
+    return _check("swin_block_rms_forward", load().swin_block_rms_forward(
+        h, _arg("x", x, bf, *shape), _opt("residual", residual, bf, *shape), rows, _arg("gamma", gamma, bf, C),
+        _opt("out_sum", out_sum, bf, *shape), _arg("out", out, bf, *shape), _stream(stream)))
+
+
+def swin_block_rms_forward_q8(h, x, gamma, out8, scales, residual=None, out_sum=None, stream=None):
+    """The same in e4m3 codes out8 [..., C] with one fp32 scale a row."""
+    rows, C = _rows(x)
+    bf, shape = torch.bfloat16, x.shape
+    return _check("swin_block_rms_forward_q8", load().swin_block_rms_forward_q8(
+        h, _arg("x", x, bf, *shape), _opt("residual", residual, bf, *shape), rows, _arg("gamma", gamma, bf, C),
+        _opt("out_sum", out_sum, bf, *shape), _arg("out8", out8, torch.float8_e4m3fn, *shape),
+        _arg("scales", scales, torch.float32, *shape[:-1]), _stream(stream)))
+
+
+def swin_block_rms_backward(h, s, gamma, dy, dx, dgamma, dsum=None, stream=None):
+    rows, C = _rows(s)
+    bf, shape = torch.bfloat16, s.shape
+    return _check("swin_block_rms_backward", load().swin_block_rms_backward(
+        h, _arg("s", s, bf, *shape), rows, _arg("gamma", gamma, bf, C), _arg("dy", dy, bf, *shape),
+        _opt("dsum", dsum, bf, *shape), _arg("dx", dx, bf, *shape), _arg("dgamma", dgamma, torch.float32, C),
+        _stream(stream)))

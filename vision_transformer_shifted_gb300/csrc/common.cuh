@@ -115,6 +115,36 @@ int ws_check(const void *buf, cudaStream_t stream);
 // Test hook: overwrites one byte of a guard band (side 0: before, 1: after).
 int ws_test_corrupt(const void *buf, int side);
 
+// A handle's workspace for calls on any stream.  Eager calls share one buffer
+// and are ordered by an event, whatever streams they run on; a call captured
+// into a CUDA graph gets memory of the graph's own (allocated and freed by
+// nodes of the graph), so replays share nothing with other graphs or calls.
+struct OrderedWorkspace {
+    void *buf;
+    size_t bytes;
+    cudaEvent_t done;
+};
+// Workspace of `need` bytes for the work about to be queued on `stream`:
+// *ptr, and *captured (pass both to ows_end).  SWIN_WATTN_* status.
+int ows_begin(OrderedWorkspace *w, size_t need, cudaStream_t stream, void **ptr, bool *captured);
+// After the work is queued (also after a failed launch); returns the guard
+// bands' status.
+int ows_end(OrderedWorkspace *w, cudaStream_t stream, void *ptr, bool captured);
+void ows_free(OrderedWorkspace *w);
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlaps(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const char *p = (const char *)a, *q = (const char *)b;
+    return na > 0 && nb > 0 && p < q + nb && q < p + na;
+}
+
+// The device that is current, checked against a handle's (-1: not bound yet,
+// the handle then takes it).  SWIN_WATTN_OK, EINVAL (another device) or ECUDA.
+int bind_device(int *device);
+// SM count of the current device.
+int sm_count();
+
 // ---- kernel launchers (return cudaSuccess or the error) ----------------------
 
 enum { LOAD_PLAIN = 0, LOAD_GATHER = 1 };

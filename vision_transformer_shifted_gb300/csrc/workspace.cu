@@ -10,6 +10,7 @@
 //       read back (the call then synchronises its stream), and a changed byte
 //       -- a kernel writing outside its buffer -- is reported as
 //       SWIN_WATTN_ECORRUPT.
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -107,6 +108,78 @@ int ws_check(const void *buf, cudaStream_t stream)
     for (unsigned char c : band)
         if (c != PATTERN) return SWIN_WATTN_ECORRUPT;
     return SWIN_WATTN_OK;
+}
+
+int ows_begin(OrderedWorkspace *w, size_t need, cudaStream_t stream, void **ptr, bool *captured)
+{
+    *ptr = nullptr;
+    *captured = false;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+        cudaGetLastError();
+        return SWIN_WATTN_ECUDA;
+    }
+    if (cap != cudaStreamCaptureStatusNone) {
+        if (env_on("SWIN_WATTN_FAIL_ALLOC")) return SWIN_WATTN_ENOMEM;
+        if (cudaMallocAsync(ptr, need, stream) != cudaSuccess) {
+            cudaGetLastError();
+            *ptr = nullptr;
+            return SWIN_WATTN_ENOMEM;
+        }
+        *captured = true;
+        return SWIN_WATTN_OK;
+    }
+    if (!w->done && cudaEventCreateWithFlags(&w->done, cudaEventDisableTiming) != cudaSuccess) {
+        cudaGetLastError();
+        w->done = nullptr;
+        return SWIN_WATTN_ECUDA;
+    }
+    // (growing frees the old buffer: cudaFree waits for the work that uses it)
+    const int rc = ws_ensure(&w->buf, &w->bytes, need);
+    if (rc != SWIN_WATTN_OK) return rc;
+    if (cudaStreamWaitEvent(stream, w->done, 0) != cudaSuccess) {
+        cudaGetLastError();
+        return SWIN_WATTN_ECUDA;
+    }
+    *ptr = w->buf;
+    return SWIN_WATTN_OK;
+}
+
+int ows_end(OrderedWorkspace *w, cudaStream_t stream, void *ptr, bool captured)
+{
+    if (!ptr) return SWIN_WATTN_OK;
+    if (captured) return cudaFreeAsync(ptr, stream) == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA;
+    if (cudaEventRecord(w->done, stream) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    return ws_check(ptr, stream);
+}
+
+void ows_free(OrderedWorkspace *w)
+{
+    ws_free(&w->buf, &w->bytes);
+    if (w->done) cudaEventDestroy(w->done);
+    w->done = nullptr;
+}
+
+int bind_device(int *device)
+{
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SWIN_WATTN_ECUDA;
+    }
+    if (*device < 0) *device = dev;
+    return *device == dev ? SWIN_WATTN_OK : SWIN_WATTN_EINVAL;
+}
+
+int sm_count()
+{
+    static std::atomic<int> counts[64];   // per device; 0: not asked yet
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) n = counts[dev].load();
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    if (dev < 64) counts[dev].store(n);
+    return n;
 }
 
 int ws_test_corrupt(const void *buf, int side)
