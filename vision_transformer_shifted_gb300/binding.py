@@ -1,5 +1,5 @@
 """ctypes binding of libswin_wattn (include/swin_wattn.h, swin_wattn_test.h,
-swin_block.h, swin_wattn_backward.h, swin_rms.h).
+swin_block.h, swin_wattn_backward.h, swin_rms.h, swin_gated.h).
 
 Argument marshalling only: every function here passes tensor pointers and
 sizes to the C ABI of the same name and raises on a non-OK status.  torch is
@@ -20,6 +20,7 @@ OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM, ETIMEOUT, ESCRATCH, ECORRUPT = 0, -1, -
 NOALLOC_MAX_INTERMEDIATE_BYTES = (64 << 20) - 256
 OPT_PATH, OPT_WAIT_LIMIT_US, OPT_HOST_CHUNKS, OPT_OVERLAP_CALLS = 1, 2, 3, 4
 BLOCK_OPT_OVERLAP_CALLS = 1
+BLOCK_GATED_SILU, BLOCK_GATED_GELU = 0, 1
 PATH_AUTO, PATH_THREE_KERNELS, PATH_FUSED, PATH_FP32 = 0, 1, 2, 3
 
 _lib = None
@@ -72,6 +73,13 @@ _SIGNATURES = {
     "swin_block_rms_backward": ["p", "p", "i", "p", "p", "p", "p", "p", "p"],
     "swin_block_rms_last_launches": ["p"],
     "swin_block_rms_destroy": ["p"],
+    "swin_block_gated_create": ["pp", "i", "i", "i"],
+    "swin_block_gated_forward": ["p", "p", "i", "p", "p", "p", "p"],
+    "swin_block_gated_forward_q8": ["p", "p", "p", "i", "p", "p", "p", "p"],
+    "swin_block_gated_backward": ["p", "p", "i", "p", "p", "p", "p", "p"],
+    "swin_block_gated_last_launches": ["p"],
+    "swin_block_gated_sync_status": ["p", "p"],
+    "swin_block_gated_destroy": ["p"],
 }
 
 # swin_block_params (include/swin_block.h), field for field
@@ -350,9 +358,17 @@ def _rows(x):
     return (x.numel() // C if C else 0), C
 
 
+def _rms_rows(h, x):
+    rows, C = _rows(x)
+    if C != h.C:
+        raise ValueError("the handle is for C = %d, not %d" % (h.C, C))
+    return rows, C
+
+
 def swin_block_rms_create(C, eps=1e-6):
     h = ctypes.c_void_p()
     _check("swin_block_rms_create", load().swin_block_rms_create(ctypes.byref(h), C, eps))
+    h.C = C
     return h
 
 
@@ -367,7 +383,7 @@ def swin_block_rms_last_launches(h):
 def swin_block_rms_forward(h, x, gamma, out, residual=None, out_sum=None, stream=None):
     """out = RMS norm of x + residual over the last axis of x [..., C]; out_sum
     receives the sum."""
-    rows, C = _rows(x)
+    rows, C = _rms_rows(h, x)
     bf, shape = torch.bfloat16, x.shape
     return _check("swin_block_rms_forward", load().swin_block_rms_forward(
         h, _arg("x", x, bf, *shape), _opt("residual", residual, bf, *shape), rows, _arg("gamma", gamma, bf, C),
@@ -376,7 +392,7 @@ def swin_block_rms_forward(h, x, gamma, out, residual=None, out_sum=None, stream
 
 def swin_block_rms_forward_q8(h, x, gamma, out8, scales, residual=None, out_sum=None, stream=None):
     """The same in e4m3 codes out8 [..., C] with one fp32 scale a row."""
-    rows, C = _rows(x)
+    rows, C = _rms_rows(h, x)
     bf, shape = torch.bfloat16, x.shape
     return _check("swin_block_rms_forward_q8", load().swin_block_rms_forward_q8(
         h, _arg("x", x, bf, *shape), _opt("residual", residual, bf, *shape), rows, _arg("gamma", gamma, bf, C),
@@ -385,9 +401,100 @@ def swin_block_rms_forward_q8(h, x, gamma, out8, scales, residual=None, out_sum=
 
 
 def swin_block_rms_backward(h, s, gamma, dy, dx, dgamma, dsum=None, stream=None):
-    rows, C = _rows(s)
+    rows, C = _rms_rows(h, s)
     bf, shape = torch.bfloat16, s.shape
     return _check("swin_block_rms_backward", load().swin_block_rms_backward(
         h, _arg("s", s, bf, *shape), rows, _arg("gamma", gamma, bf, C), _arg("dy", dy, bf, *shape),
         _opt("dsum", dsum, bf, *shape), _arg("dx", dx, bf, *shape), _arg("dgamma", dgamma, torch.float32, C),
         _stream(stream)))
+
+
+# ---- swin_gated.h ------------------------------------------------------------------
+
+class GatedParams(ctypes.Structure):
+    """swin_block_gated_params, field for field (also its gradients' struct)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("Wg", "bg", "Wu", "bu", "Wd", "bd")]
+
+
+class GatedParamsQ8(ctypes.Structure):
+    """swin_block_gated_params_q8, field for field."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("Wg8", "sg", "bg", "Wu8", "su", "bu", "Wd", "bd")]
+
+
+def _gated(x, p, dtype, names):
+    """rows, C, F and the checked struct of a call on x [..., C] with the tensors
+    of dict p: names of Wg, bg, Wu, bu, Wd, bd (and, between, the scales)."""
+    rows, C = _rows(x)
+    F = p[names[0]].shape[0]
+    bf = torch.bfloat16
+    vals = [_arg(names[0], p[names[0]], dtype, F, C)]
+    for n in names[1:]:
+        if n.endswith("8") or n[-2:] in ("Wg", "Wu"):
+            vals.append(_arg(n, p[n], dtype, F, C))
+        elif n.endswith("Wd"):
+            vals.append(_arg(n, p[n], bf, C, F))
+        elif n in ("sg", "su"):
+            vals.append(_arg(n, p[n], torch.float32, F))
+        else:
+            vals.append(_opt(n, p.get(n), bf, C if n.endswith("bd") else F))
+    return rows, C, F, vals
+
+
+def swin_block_gated_create(C, F, act=BLOCK_GATED_SILU):
+    h = ctypes.c_void_p()
+    _check("swin_block_gated_create", load().swin_block_gated_create(ctypes.byref(h), C, F, act))
+    h.C, h.F = C, F
+    return h
+
+
+def swin_block_gated_destroy(h):
+    return _check("swin_block_gated_destroy", load().swin_block_gated_destroy(h))
+
+
+def swin_block_gated_last_launches(h):
+    return load().swin_block_gated_last_launches(h)
+
+
+def swin_block_gated_sync_status(h, stream=None):
+    return _check("swin_block_gated_sync_status", load().swin_block_gated_sync_status(h, _stream(stream)))
+
+
+def _same_handle(h, C, F):
+    if (h.C, h.F) != (C, F):
+        raise ValueError("the handle is for C = %d, F = %d, not C = %d, F = %d" % (h.C, h.F, C, F))
+
+
+def swin_block_gated_forward(h, x, params, out, residual=None, stream=None):
+    """out = residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd for x [..., C];
+    params: dict with Wg, bg, Wu, bu, Wd, bd (biases may be None)."""
+    rows, C, F, vals = _gated(x, params, torch.bfloat16, ("Wg", "bg", "Wu", "bu", "Wd", "bd"))
+    _same_handle(h, C, F)
+    bf, shape = torch.bfloat16, x.shape
+    return _check("swin_block_gated_forward", load().swin_block_gated_forward(
+        h, _arg("x", x, bf, *shape), rows, ctypes.addressof(s := GatedParams(*vals)),
+        _opt("residual", residual, bf, *shape), _arg("out", out, bf, *shape), _stream(stream)))
+
+
+def swin_block_gated_forward_q8(h, x8, sx, params, out, residual=None, stream=None):
+    """The same from e4m3 x8 [..., C] with scales sx [...]; params: dict with Wg8,
+    sg, bg, Wu8, su, bu, Wd, bd (biases may be None)."""
+    e4m3 = torch.float8_e4m3fn
+    rows, C, F, vals = _gated(x8, params, e4m3, ("Wg8", "sg", "bg", "Wu8", "su", "bu", "Wd", "bd"))
+    _same_handle(h, C, F)
+    bf, shape = torch.bfloat16, x8.shape
+    return _check("swin_block_gated_forward_q8", load().swin_block_gated_forward_q8(
+        h, _arg("x8", x8, e4m3, *shape), _arg("sx", sx, torch.float32, *shape[:-1]), rows,
+        ctypes.addressof(s := GatedParamsQ8(*vals)), _opt("residual", residual, bf, *shape),
+        _arg("out", out, bf, *shape), _stream(stream)))
+
+
+def swin_block_gated_backward(h, x, params, dy, dx, grads, stream=None):
+    """Gradients of the bf16 form: dx and, in the tensors of dict grads, dWg, dWu,
+    dWd and (where not None) dbg, dbu, dbd, all bf16."""
+    rows, C, F, vals = _gated(x, params, torch.bfloat16, ("Wg", "bg", "Wu", "bu", "Wd", "bd"))
+    _, _, _, gvals = _gated(x, grads, torch.bfloat16, ("dWg", "dbg", "dWu", "dbu", "dWd", "dbd"))
+    _same_handle(h, C, F)
+    bf, shape = torch.bfloat16, x.shape
+    return _check("swin_block_gated_backward", load().swin_block_gated_backward(
+        h, _arg("x", x, bf, *shape), rows, ctypes.addressof(s := GatedParams(*vals)), _arg("dy", dy, bf, *shape),
+        _arg("dx", dx, bf, *shape), ctypes.addressof(g := GatedParams(*gvals)), _stream(stream)))

@@ -1,0 +1,574 @@
+// The gated feed-forward block: C ABI, plans and launches of the kernels in
+// gated.cuh, and the two small kernels that finish sums over rows.
+//   forward   h = act(x Wg^T + bg) * (x Wu^T + bu)        (one kernel)
+//             out = residual + h Wd^T + bd                 (one kernel)
+//   backward  h, dg, du from x and dy (one kernel), dx = dg Wg + du Wu, then
+//             dWg, dWu, dWd in one launch, and the bias gradients' column sums
+#include <climits>
+#include <cstring>
+#include <new>
+
+#include "swin_gated.h"
+#include "common.cuh"
+#include "gated.cuh"
+
+using namespace swin;
+
+struct swin_block_gated_s {
+    int C, F, act;
+    int device;   // -1: not bound yet
+    int *d_err;
+    int last_launches;
+    OrderedWorkspace ws;
+};
+
+namespace {
+
+constexpr int MAX_WIDTH = 65536;
+constexpr int MAX_ROWS = INT_MAX - 512;   // row coordinates of the last tile stay below 2^31
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr CUtensorMapDataType T_BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, T_U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                              T_F32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA; }
+
+bool bad_pointer(const void *p, bool required)
+{
+    return p ? (reinterpret_cast<uintptr_t>(p) & 15u) != 0 : required;
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// K-major operand [rows, k]: boxes of 128 bytes of K x box_rows.
+cudaError_t map_k(CUtensorMap *m, const void *p, int64_t rows, int k, int box_rows, bool q8 = false)
+{
+    const int e = q8 ? 1 : 2;
+    return make_tensor_map(m, q8 ? T_U8 : T_BF16, p, k, rows, (int64_t)k * e, 128 / e, box_rows, 128);
+}
+// MN-major operand, stored [k, mn]: boxes of 64 MN elements x 64 k.
+cudaError_t map_mn(CUtensorMap *m, const void *p, int64_t k, int mn)
+{
+    return make_tensor_map(m, T_BF16, p, mn, k, (int64_t)mn * 2, 64, 64, 128);
+}
+// Output [rows, cols]: a warp's boxes of 64 columns x 32 rows.
+cudaError_t map_out(CUtensorMap *m, const void *p, int64_t rows, int cols)
+{
+    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 64, 32, 128);
+}
+
+// One product of a launch_products call: D [rows, cols] = sum over K segments of
+// A B^T (+ bias + residual).
+struct Product {
+    const void *a[2], *b[2];
+    int k[2];
+    bf16 *d;
+    const bf16 *bias, *residual;
+    int64_t rows;
+    int cols;
+};
+
+// out = the sum of `slices` fp32 partial tiles [rows, cols] (+ bias + residual),
+// slice by slice.
+struct ReduceItem {
+    const float *part;
+    const bf16 *bias, *residual;
+    bf16 *out;
+    int64_t rows;
+    int cols, slices;
+};
+struct ReduceArgs {
+    ReduceItem it[3];
+};
+__global__ void __launch_bounds__(256) reduce_slices_kernel(ReduceArgs a)
+{
+    const ReduceItem &t = a.it[blockIdx.y];
+    const int64_t n = t.rows * t.cols;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int s = 0; s < t.slices; ++s) {
+            const float4 x = *reinterpret_cast<const float4 *>(t.part + s * n + i);
+            const float4 y = *reinterpret_cast<const float4 *>(t.part + s * n + i + 4);
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+        }
+        float b[8];
+        load8(t.bias, (int)(i % t.cols), t.cols, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += b[e];
+        if (t.residual) {
+            load8(t.residual + i, 0, 8, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += b[e];
+        }
+        *reinterpret_cast<uint4 *>(t.out + i) = pack8f(v);
+    }
+}
+
+// K slices of a product of `tiles` tiles and kb K blocks: as many as make the
+// most of the pairs (waves x blocks a wave, a slice costing about four more
+// blocks for its partial tile), at most 32 and at least four blocks each.
+int pick_slices(int64_t tiles, int kb)
+{
+    const int pairs = sm_count() / 2;
+    int best = 1;
+    int64_t cost = (int64_t)ceil_div(tiles, pairs) * kb;
+    for (int s = 2; s <= 32 && kb / s >= 4; ++s) {
+        const int64_t c = (int64_t)ceil_div(tiles * s, pairs) * (ceil_div(kb, s) + 4) + 4;
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
+    return best;
+}
+
+struct ProductsPlan {
+    int n, slices, units;
+    bool wide;            // 256-column tiles (else 128)
+    size_t part_bytes;    // of the partial tiles of all products
+};
+
+// Tiles of 256 x 256 where every product has more than 128 columns and there
+// are enough of them for the pairs, else 256 x 128.
+ProductsPlan plan_products(const Product *p, int n)
+{
+    ProductsPlan pl{};
+    pl.n = n;
+    const int pairs = sm_count() / 2;
+    int64_t wide_tiles = 0;
+    pl.wide = true;
+    for (int i = 0; i < n; ++i) {
+        wide_tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, 256);
+        if (p[i].cols <= 128) pl.wide = false;
+    }
+    const int kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
+    if (wide_tiles < pairs && pick_slices(wide_tiles, kb) == 1) pl.wide = false;
+    const int tn = pl.wide ? 256 : 128;
+    int64_t tiles = 0;
+    for (int i = 0; i < n; ++i) tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, tn);
+    pl.slices = pick_slices(tiles, kb);
+    pl.units = (int)(tiles * pl.slices);
+    if (pl.slices > 1)
+        for (int i = 0; i < n; ++i) pl.part_bytes += (size_t)pl.slices * p[i].rows * p[i].cols * sizeof(float);
+    return pl;
+}
+
+template <int TN, bool A_MN, bool B_MN>
+cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
+                              cudaStream_t stream, int *launches)
+{
+    typename GemmPolicy<TN, A_MN, B_MN>::Args a;
+    memset(&a, 0, sizeof(a));
+    ReduceArgs r{};
+    int64_t first = 0, most = 0;
+    for (int i = 0; i < 3; ++i) {
+        PairProblem &q = a.p[i];
+        q.first = INT_MAX;
+        if (i >= pl.n) continue;
+        const Product &p = ps[i];
+        q.rows = (int)p.rows;
+        q.cols = p.cols;
+        q.mt = ceil_div(p.rows, 256);
+        q.nt = ceil_div(p.cols, TN);
+        q.slices = pl.slices;
+        q.first = (int)first;
+        first += (int64_t)q.mt * q.nt * pl.slices;
+        cudaError_t e;
+        for (int s = 0; s < 2; ++s) {
+            q.k[s] = p.k[s];
+            q.kb[s] = p.k[s] ? ceil_div(p.k[s], 64) : 0;
+            if (!p.k[s]) continue;
+            e = A_MN ? map_mn(&q.a[s], p.a[s], p.k[s], (int)p.rows) : map_k(&q.a[s], p.a[s], p.rows, p.k[s], 128);
+            if (e != cudaSuccess) return e;
+            e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols) : map_k(&q.b[s], p.b[s], p.cols, p.k[s], TN / 2);
+            if (e != cudaSuccess) return e;
+        }
+        if (pl.slices > 1) {
+            e = make_tensor_map(&q.part, T_F32, part, p.cols, p.rows, (int64_t)p.cols * 4, 32, 32, 128, pl.slices);
+            r.it[i] = {part, p.bias, p.residual, p.d, p.rows, p.cols, pl.slices};
+            part += (size_t)pl.slices * p.rows * p.cols;
+            if (p.rows * p.cols > most) most = p.rows * p.cols;
+        } else {
+            e = map_out(&q.d, p.d, p.rows, p.cols);
+            q.bias = p.bias;
+            q.residual = p.residual;
+        }
+        if (e != cudaSuccess) return e;
+    }
+    a.units = pl.units;
+    a.st = st;
+    ++*launches;
+    cudaError_t e = launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
+    if (e != cudaSuccess || pl.slices == 1) return e;
+    int64_t blocks = ceil_div(most, 2048);
+    if (blocks > 8 * sm_count()) blocks = 8 * sm_count();
+    ++*launches;
+    reduce_slices_kernel<<<dim3((unsigned)blocks, (unsigned)pl.n), 256, 0, stream>>>(r);
+    return cudaGetLastError();
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
+                            cudaStream_t stream, int *launches)
+{
+    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches)
+                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches);
+}
+
+// Column sums of up to three bf16 matrices [rows, cols]: block (x, y, z) sums
+// every gridDim.y-th group of 32 rows of 64 columns of matrix z into a partial
+// row; then the partial rows are added in a fixed order.
+struct ColumnSums {
+    const bf16 *in[3];
+    bf16 *out[3];
+    float *part[3];   // [splits, cols]
+    int64_t rows;
+    int cols[3];
+    int splits;
+};
+__global__ void __launch_bounds__(256) column_partials_kernel(ColumnSums a)
+{
+    __shared__ float sum[32][65];
+    const int z = blockIdx.z, cols = a.cols[z];
+    const int c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
+    if (blockIdx.x * 64 >= cols) return;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < cols)
+        for (int64_t i = (int64_t)blockIdx.y * 32 + r; i < a.rows; i += (int64_t)gridDim.y * 32) {
+            float w[8];
+            load8(a.in[z] + i * cols, c, cols, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
+        }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[r][(threadIdx.x & 7) * 8 + e] = v[e];
+    __syncthreads();
+    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < cols) {
+        float t = 0.f;
+        for (int i = 0; i < 32; ++i) t += sum[i][threadIdx.x];
+        a.part[z][(int64_t)blockIdx.y * cols + blockIdx.x * 64 + threadIdx.x] = t;
+    }
+}
+__global__ void __launch_bounds__(256) column_finish_kernel(ColumnSums a)
+{
+    const int z = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.cols[z]) return;
+    float t = 0.f;
+    for (int s = 0; s < a.splits; ++s) t += a.part[z][(int64_t)s * a.cols[z] + c];
+    a.out[z][c] = __float2bfloat16_rn(t);
+}
+
+// Workspace layout: bytes of each part, 1 KB aligned.
+struct Carve {
+    char *base;
+    size_t used = 0;
+    explicit Carve(void *p) : base((char *)p) {}
+    void *take(size_t bytes)
+    {
+        void *p = base + used;
+        used += (bytes + 1023) / 1024 * 1024;
+        return p;
+    }
+};
+
+template <bool Q8>
+cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *sx, int rows, const void *wg,
+                      const float *sg, const void *bg, const void *wu, const float *su, const void *bu, bf16 *hidden,
+                      DeviceStatus st, cudaStream_t stream)
+{
+    auto run = [&](auto policy) -> cudaError_t {
+        using P = decltype(policy);
+        typename P::Args a;
+        memset(&a, 0, sizeof(a));
+        cudaError_t e;
+        if ((e = map_k(&a.x, x, rows, h->C, 128, Q8)) != cudaSuccess) return e;
+        if ((e = map_k(&a.wg, wg, h->F, h->C, 128, Q8)) != cudaSuccess) return e;
+        if ((e = map_k(&a.wu, wu, h->F, h->C, 128, Q8)) != cudaSuccess) return e;
+        if ((e = map_out(&a.h, hidden, rows, h->F)) != cudaSuccess) return e;
+        a.bg = (const bf16 *)bg;
+        a.bu = (const bf16 *)bu;
+        a.sx = sx;
+        a.sg = sg;
+        a.su = su;
+        a.rows = rows;
+        a.C = h->C;
+        a.F = h->F;
+        a.mt = ceil_div(rows, 256);
+        a.nt = ceil_div(h->F, 128);
+        a.kb = ceil_div(h->C, P::ELEMS);
+        a.units = a.mt * a.nt;
+        a.st = st;
+        return launch_pair<P>(a, stream);
+    };
+    return h->act == SWIN_BLOCK_GATED_SILU ? run(UpPolicy<ACT_SILU, Q8>{}) : run(UpPolicy<ACT_GELU, Q8>{});
+}
+
+int first_call(swin_block_gated_s *h)
+{
+    const int rc = bind_device(&h->device);
+    if (rc != SWIN_WATTN_OK || h->d_err) return rc;
+    if (cudaMalloc(&h->d_err, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        h->d_err = nullptr;
+        return SWIN_WATTN_ENOMEM;
+    }
+    return cuda_status(cudaMemset(h->d_err, 0, sizeof(int)));
+}
+
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+bool any_overlap(Span o, std::initializer_list<Span> in)
+{
+    for (const Span &s : in)
+        if (s.p && overlaps(o.p, o.bytes, s.p, s.bytes)) return true;
+    return false;
+}
+
+// The forward's checks, the hidden activation by `up` (into the workspace) and
+// the last product.
+template <class Up>
+int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, const void *residual, void *out,
+            cudaStream_t stream, Up &&up)
+{
+    int rc = first_call(h);
+    if (rc != SWIN_WATTN_OK) return rc;
+    Product down{};
+    down.k[0] = h->F;
+    down.b[0] = Wd;
+    down.d = (bf16 *)out;
+    down.bias = (const bf16 *)bd;
+    down.residual = (const bf16 *)residual;
+    down.rows = rows;
+    down.cols = h->C;
+    const ProductsPlan pl = plan_products(&down, 1);
+    Carve size(nullptr);
+    size.take((size_t)rows * h->F * 2);
+    size.take(pl.part_bytes);
+    void *ws = nullptr;
+    bool captured = false;
+    if ((rc = ows_begin(&h->ws, size.used, stream, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    Carve carve(ws);
+    bf16 *hidden = (bf16 *)carve.take((size_t)rows * h->F * 2);
+    float *part = (float *)carve.take(pl.part_bytes);
+    down.a[0] = hidden;
+    const DeviceStatus st{h->d_err, WAIT_NS};
+    h->last_launches = 1;
+    cudaError_t e = up(hidden, st);
+    if (e == cudaSuccess) e = launch_products<false, false>(&down, pl, part, st, stream, &h->last_launches);
+    const int rc2 = ows_end(&h->ws, stream, ws, captured);
+    return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
+}
+
+} // namespace
+
+extern "C" {
+
+int swin_block_gated_create(swin_block_gated_t *out, int C, int F, int act)
+{
+    if (!out) return SWIN_WATTN_EINVAL;
+    *out = nullptr;
+    if (C <= 0 || C % 8 || C > MAX_WIDTH || F <= 0 || F % 8 || F > MAX_WIDTH) return SWIN_WATTN_EINVAL;
+    if (act != SWIN_BLOCK_GATED_SILU && act != SWIN_BLOCK_GATED_GELU) return SWIN_WATTN_EINVAL;
+    swin_block_gated_s *h = new (std::nothrow) swin_block_gated_s{};
+    if (!h) return SWIN_WATTN_ENOMEM;
+    h->C = C;
+    h->F = F;
+    h->act = act;
+    h->device = -1;
+    *out = h;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_gated_destroy(swin_block_gated_t h)
+{
+    if (!h) return SWIN_WATTN_OK;
+    if (h->d_err) {
+        cudaDeviceSynchronize();
+        cudaFree(h->d_err);
+    }
+    ows_free(&h->ws);
+    delete h;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_gated_last_launches(swin_block_gated_t h) { return h ? h->last_launches : 0; }
+
+int swin_block_gated_sync_status(swin_block_gated_t h, swin_stream_t stream)
+{
+    if (!h) return SWIN_WATTN_EINVAL;
+    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    if (!h->d_err) return SWIN_WATTN_OK;
+    int err = 0;
+    if (cudaMemcpy(&err, h->d_err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    if (!err) return SWIN_WATTN_OK;
+    if (cudaMemset(h->d_err, 0, sizeof(int)) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    return SWIN_WATTN_ETIMEOUT;
+}
+
+int swin_block_gated_forward(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
+                             const void *residual, void *out, swin_stream_t stream)
+{
+    if (!h || !p || rows < 0 || rows > MAX_ROWS) return SWIN_WATTN_EINVAL;
+    if (rows == 0) return SWIN_WATTN_OK;   // (an empty tensor may have no address)
+    for (const void *q : {x, p->Wg, p->Wu, p->Wd, (const void *)out})
+        if (bad_pointer(q, true)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {p->bg, p->bu, p->bd, residual})
+        if (bad_pointer(q, false)) return SWIN_WATTN_EINVAL;
+    const int64_t n = 2 * (int64_t)rows * h->C, w = 2 * (int64_t)h->C * h->F, f = 2 * (int64_t)h->F, c = 2 * (int64_t)h->C;
+    if (any_overlap({out, n}, {{x, n}, {p->Wg, w}, {p->Wu, w}, {p->Wd, w}, {p->bg, f}, {p->bu, f}, {p->bd, c},
+                               {residual == out ? nullptr : residual, n}}))
+        return SWIN_WATTN_EINVAL;
+    return forward(h, rows, p->Wd, p->bd, residual, out, (cudaStream_t)stream, [&](bf16 *hidden, DeviceStatus st) {
+        return launch_up<false>(h, x, nullptr, rows, p->Wg, nullptr, p->bg, p->Wu, nullptr, p->bu, hidden, st,
+                                (cudaStream_t)stream);
+    });
+}
+
+int swin_block_gated_forward_q8(swin_block_gated_t h, const void *x8, const float *sx, int rows,
+                                const swin_block_gated_params_q8 *p, const void *residual, void *out,
+                                swin_stream_t stream)
+{
+    if (!h || !p || rows < 0 || rows > MAX_ROWS) return SWIN_WATTN_EINVAL;
+    if (h->C % 16) return SWIN_WATTN_EUNSUPPORTED;
+    if (rows == 0) return SWIN_WATTN_OK;
+    for (const void *q : {x8, (const void *)sx, p->Wg8, (const void *)p->sg, p->Wu8, (const void *)p->su, p->Wd,
+                          (const void *)out})
+        if (bad_pointer(q, true)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {p->bg, p->bu, p->bd, residual})
+        if (bad_pointer(q, false)) return SWIN_WATTN_EINVAL;
+    const int64_t m = (int64_t)rows * h->C, w = (int64_t)h->C * h->F, f = 2 * (int64_t)h->F, c = 2 * (int64_t)h->C;
+    if (any_overlap({out, 2 * m}, {{x8, m}, {sx, 4 * (int64_t)rows}, {p->Wg8, w}, {p->Wu8, w}, {p->sg, 2 * f},
+                                   {p->su, 2 * f}, {p->Wd, 2 * w}, {p->bg, f}, {p->bu, f}, {p->bd, c},
+                                   {residual == out ? nullptr : residual, 2 * m}}))
+        return SWIN_WATTN_EINVAL;
+    return forward(h, rows, p->Wd, p->bd, residual, out, (cudaStream_t)stream, [&](bf16 *hidden, DeviceStatus st) {
+        return launch_up<true>(h, x8, sx, rows, p->Wg8, p->sg, p->bg, p->Wu8, p->su, p->bu, hidden, st,
+                               (cudaStream_t)stream);
+    });
+}
+
+int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
+                              const void *dy, void *dx, const swin_block_gated_grads *g, swin_stream_t stream)
+{
+    if (!h || !p || !g || rows < 0 || rows > MAX_ROWS) return SWIN_WATTN_EINVAL;
+    const int64_t n = 2 * (int64_t)rows * h->C, w = 2 * (int64_t)h->C * h->F, f = 2 * (int64_t)h->F, c = 2 * (int64_t)h->C;
+    for (const void *q : {x, dy, (const void *)dx})
+        if (bad_pointer(q, rows > 0)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {p->Wg, p->Wu, p->Wd, (const void *)g->dWg, (const void *)g->dWu, (const void *)g->dWd})
+        if (bad_pointer(q, true)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {p->bg, p->bu, p->bd, (const void *)g->dbg, (const void *)g->dbu, (const void *)g->dbd})
+        if (bad_pointer(q, false)) return SWIN_WATTN_EINVAL;
+    const Span outs[] = {{dx, n}, {g->dWg, w}, {g->dWu, w}, {g->dWd, w}, {g->dbg, f}, {g->dbu, f}, {g->dbd, c}};
+    for (int i = 0; i < 7; ++i) {
+        if (!outs[i].p) continue;
+        if (any_overlap(outs[i], {{x, n}, {dy, n}, {p->Wg, w}, {p->Wu, w}, {p->Wd, w}, {p->bg, f}, {p->bu, f}, {p->bd, c}}))
+            return SWIN_WATTN_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (any_overlap(outs[i], {outs[j]})) return SWIN_WATTN_EINVAL;
+    }
+    int rc = first_call(h);
+    if (rc != SWIN_WATTN_OK) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (rows == 0) {
+        for (int i = 1; i < 7; ++i)
+            if (outs[i].p && cudaMemsetAsync(const_cast<void *>(outs[i].p), 0, outs[i].bytes, s) != cudaSuccess)
+                return SWIN_WATTN_ECUDA;
+        return SWIN_WATTN_OK;
+    }
+
+    Product dxp{}, dw[3]{};
+    dxp.k[0] = dxp.k[1] = h->F;
+    dxp.b[0] = p->Wg;
+    dxp.b[1] = p->Wu;
+    dxp.d = (bf16 *)dx;
+    dxp.rows = rows;
+    dxp.cols = h->C;
+    for (int i = 0; i < 3; ++i) {
+        dw[i].k[0] = rows;
+        dw[i].rows = i < 2 ? h->F : h->C;
+        dw[i].cols = i < 2 ? h->C : h->F;
+    }
+    dw[0].b[0] = dw[1].b[0] = x;
+    dw[2].a[0] = dy;
+    dw[0].d = (bf16 *)g->dWg;
+    dw[1].d = (bf16 *)g->dWu;
+    dw[2].d = (bf16 *)g->dWd;
+    const ProductsPlan px = plan_products(&dxp, 1), pw = plan_products(dw, 3);
+    const size_t part_bytes = px.part_bytes > pw.part_bytes ? px.part_bytes : pw.part_bytes;
+    ColumnSums cs{};
+    cs.rows = rows;
+    cs.splits = ceil_div(rows, 256) < 64 ? ceil_div(rows, 256) : 64;
+    int sums = 0, most = 0;
+    const size_t hid = (size_t)rows * h->F * 2;
+    Carve size(nullptr);
+    for (int i = 0; i < 3; ++i) size.take(hid);
+    size.take(part_bytes);
+    size.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
+    void *ws = nullptr;
+    bool captured = false;
+    if ((rc = ows_begin(&h->ws, size.used, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    Carve carve(ws);
+    bf16 *hidden = (bf16 *)carve.take(hid), *dg = (bf16 *)carve.take(hid), *du = (bf16 *)carve.take(hid);
+    float *part = (float *)carve.take(part_bytes);
+    float *sum_part = (float *)carve.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
+    dxp.a[0] = dw[0].a[0] = dg;
+    dxp.a[1] = dw[1].a[0] = du;
+    dw[2].b[0] = hidden;
+    const DeviceStatus st{h->d_err, WAIT_NS};
+
+    auto grad = [&](auto policy) -> cudaError_t {
+        using P = decltype(policy);
+        typename P::Args a;
+        memset(&a, 0, sizeof(a));
+        cudaError_t e;
+        if ((e = map_k(&a.x, x, rows, h->C, 128)) != cudaSuccess) return e;
+        if ((e = map_k(&a.dy, dy, rows, h->C, 128)) != cudaSuccess) return e;
+        if ((e = map_k(&a.wg, p->Wg, h->F, h->C, 128)) != cudaSuccess) return e;
+        if ((e = map_k(&a.wu, p->Wu, h->F, h->C, 128)) != cudaSuccess) return e;
+        if ((e = map_mn(&a.wd, p->Wd, h->C, h->F)) != cudaSuccess) return e;
+        bf16 *o[3] = {hidden, dg, du};
+        CUtensorMap *m[3] = {&a.h, &a.dg, &a.du};
+        for (int i = 0; i < 3; ++i)
+            if ((e = make_tensor_map(m[i], T_BF16, o[i], h->F, rows, (int64_t)h->F * 2, 32, 32, 64)) != cudaSuccess)
+                return e;
+        a.bg = (const bf16 *)p->bg;
+        a.bu = (const bf16 *)p->bu;
+        a.rows = rows;
+        a.C = h->C;
+        a.F = h->F;
+        a.mt = ceil_div(rows, 256);
+        a.nt = ceil_div(h->F, 128);
+        a.kb = ceil_div(h->C, 64);
+        a.units = a.mt * a.nt;
+        a.st = st;
+        return launch_pair<P>(a, s);
+    };
+    h->last_launches = 1;
+    cudaError_t e = h->act == SWIN_BLOCK_GATED_SILU ? grad(GradPolicy<ACT_SILU>{}) : grad(GradPolicy<ACT_GELU>{});
+    if (e == cudaSuccess) e = launch_products<false, true>(&dxp, px, part, st, s, &h->last_launches);
+    if (e == cudaSuccess) e = launch_products<true, true>(dw, pw, part, st, s, &h->last_launches);
+    const bf16 *in[3] = {dg, du, (const bf16 *)dy};
+    bf16 *out[3] = {(bf16 *)g->dbg, (bf16 *)g->dbu, (bf16 *)g->dbd};
+    for (int i = 0; i < 3; ++i) {
+        const int cols = i < 2 ? h->F : h->C;
+        if (!out[i]) continue;
+        cs.in[sums] = in[i];
+        cs.out[sums] = out[i];
+        cs.part[sums] = sum_part;
+        cs.cols[sums++] = cols;
+        sum_part += (size_t)cs.splits * cols;
+        if (cols > most) most = cols;
+    }
+    if (e == cudaSuccess && sums) {
+        column_partials_kernel<<<dim3(ceil_div(most, 64), cs.splits, sums), 256, 0, s>>>(cs);
+        column_finish_kernel<<<dim3(ceil_div(most, 256), sums), 256, 0, s>>>(cs);
+        h->last_launches += 2;
+        e = cudaGetLastError();
+    }
+    const int rc2 = ows_end(&h->ws, s, ws, captured);
+    return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
+}
+
+} // extern "C"

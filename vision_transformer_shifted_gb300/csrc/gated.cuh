@@ -1,0 +1,432 @@
+// Kernels of the gated feed-forward block on the CTA-pair skeleton: the two
+// first projections with the activation and the product, the general GEMM of
+// the other products, and the backward's recompute.
+#pragma once
+
+#include "gelu.cuh"
+#include "pair.cuh"
+
+namespace swin {
+
+enum { ACT_SILU = 0, ACT_GELU = 1 };
+
+// act(g), and with DERIV its derivative.
+template <int ACT, bool DERIV>
+__device__ __forceinline__ float activate(float g, float &deriv)
+{
+    if (ACT == ACT_SILU) {
+        const float p = rcp_approx(1.f + ex2_approx(g * -1.4426950408889634f));   // 1 / (1 + exp(-g))
+        if (DERIV) deriv = p * fmaf(g, 1.f - p, 1.f);
+        return g * p;
+    }
+    if (!DERIV) return gelu_exact(g);
+    // (gelu_exact's erf; its exponential is the density's)
+    const float z = g * 0.70710678118654752f, b = fabsf(z);
+    const float t = rcp_approx(fmaf(0.3275911f, b, 1.0f));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float e = ex2_approx(b * (b * -1.4426950408889634f));
+    const float phi = fmaf(0.5f, copysignf(fmaf(-q * t, e, 1.0f), z), 0.5f);
+    deriv = fmaf(g * 0.3989422804014327f, e, phi);
+    return g * phi;
+}
+
+// Eight values of a bf16 vector at column c (zero past n, and for NULL).
+__device__ __forceinline__ void load8(const bf16 *v, int c, int n, float (&f)[8])
+{
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (v && c < n) u = *reinterpret_cast<const uint4 *>(v + c);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack_bf16x2(w[e]);
+        f[2 * e] = p.x;
+        f[2 * e + 1] = p.y;
+    }
+}
+__device__ __forceinline__ void load8(const float *v, int c, int n, float (&f)[8])
+{
+    float4 x = make_float4(0, 0, 0, 0), y = x;
+    if (c < n) {
+        x = *reinterpret_cast<const float4 *>(v + c);
+        y = *reinterpret_cast<const float4 *>(v + c + 4);
+    }
+    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+}
+
+__device__ __forceinline__ uint4 pack8f(const float *v)
+{
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+// A warp's staged box to global memory: every lane has written its row; one
+// lane stores it unless it lies outside.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, bool inside, uint8_t *stage, int lane)
+{
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && inside) {
+        tma_store_2d(map, x, y, smem_u32(stage));
+        bulk_commit();
+    }
+}
+// The staging may be written again.
+__device__ __forceinline__ void staging_free(int lane)
+{
+    if (lane == 0) bulk_wait_read();
+    __syncwarp();
+}
+
+// ---- h = act(x Wg^T + bg) * (x Wu^T + bu) --------------------------------------
+//
+// A unit is 256 rows x 128 hidden columns.  CTA 0 of the pair loads 128 rows of
+// Wg as its half of B, CTA 1 the same rows of Wu: one 256 x 256 MMA then
+// leaves g in accumulator columns 0..127 and u in 128..255 of the same rows, so
+// that the thread that drains a row holds both and forms h without exchange.
+template <int ACT, bool Q8>
+struct UpPolicy {
+    struct Args {
+        CUtensorMap x, wg, wu, h;
+        const bf16 *bg, *bu;
+        const float *sx, *sg, *su;   // Q8
+        int rows, C, F, mt, nt, kb, units;
+        DeviceStatus st;
+    };
+    struct Unit {
+        int m, n;
+    };
+    static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
+    static constexpr int STAGES = 6, STAGE_BYTES = 32768, STAGING = 4096, SEGS = 1;
+    static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 256);
+
+    static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
+    static __device__ __forceinline__ int slot_use(int, int n) { return n >> 1; }
+    static __device__ __forceinline__ int slot_col(int s) { return s * 256; }
+    static __device__ __forceinline__ Unit decode(const Args &a, int u)
+    {
+        Unit r;
+        tile_order(u, a.mt, a.nt, r.m, r.n);
+        return r;
+    }
+    static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int) { return 2 * STAGE_BYTES; }
+    static __device__ __forceinline__ void load(const Args &a, const Unit &u, int, int kb, uint32_t rank, uint32_t dst,
+                                                uint32_t bar)
+    {
+        tma_load_2d_pair(dst, &a.x, kb * ELEMS, u.m * 256 + (int)rank * 128, bar);
+        tma_load_2d_pair(dst + 16384, rank ? &a.wu : &a.wg, kb * ELEMS, u.n * 128, bar);
+    }
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int, int kb, uint32_t src, uint32_t d)
+    {
+        mma_kblock<Q8 ? MMA_E4M3 : MMA_BF16, false, false>(d, src, src + 16384, IDESC, kblock_steps(a.C, kb, ELEMS),
+                                                           kb == 0);
+    }
+    template <class Release>
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
+                                                    int half, int lane, uint32_t t_lane, uint8_t *stage,
+                                                    Release &&release)
+    {
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + half * 64;
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + half * 64;
+        float sx = 1.f;
+        if (Q8) sx = row0 + lane < a.rows ? a.sx[row0 + lane] : 0.f;
+        staging_free(lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float g[32], v[32];
+            tmem_ld32(acc + 32 * j, g);
+            tmem_ld32(acc + 128 + 32 * j, v);
+            tmem_wait_ld();
+            if (j == 1) release();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = col0 + 32 * j + 8 * q;
+                if (Q8) {
+                    float s[8];
+                    load8(a.sg, c, a.F, s);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[8 * q + e] *= sx * s[e];
+                    load8(a.su, c, a.F, s);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * q + e] *= sx * s[e];
+                }
+                if (a.bg) {
+                    float b[8];
+                    load8(a.bg, c, a.F, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[8 * q + e] += b[e];
+                }
+                if (a.bu) {
+                    float b[8];
+                    load8(a.bu, c, a.F, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+                }
+                float unused;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * q + e] *= activate<ACT, false>(g[8 * q + e], unused);
+                *reinterpret_cast<uint4 *>(stage + sw128_offset(lane, 4 * j + q)) = pack8f(v + 8 * q);
+            }
+        }
+        store_box(&a.h, col0, row0, row0 < a.rows && col0 < a.F, stage, lane);
+    }
+};
+
+// ---- general product --------------------------------------------------------------
+//
+// D = A B^T over up to two K segments (dx = dg Wg + du Wu), A and B each K-major
+// or MN-major as stored: no operand is ever transposed in memory.  Up to three
+// problems run as one launch (the three weight gradients), each cut into
+// `slices` of its K blocks when its tiles would not fill the SMs: the slices
+// write fp32 partial tiles that a second kernel adds in a fixed order.
+struct PairProblem {
+    CUtensorMap a[2], b[2], d, part;
+    const bf16 *bias, *residual;   // [cols] / [rows, cols] or null (not with slices)
+    int rows, cols, k[2], kb[2];
+    int mt, nt, slices, first;     // first: this problem's first unit
+};
+
+template <int TN, bool A_MN, bool B_MN>
+struct GemmPolicy {
+    struct Args {
+        PairProblem p[3];
+        int units;
+        DeviceStatus st;
+    };
+    struct Unit {
+        int p, m, n, slice, kb0, kbn;
+    };
+    static constexpr int STAGE_BYTES = 16384 + TN * 64, STAGING = 4096, SEGS = 1;
+    static constexpr int STAGES = TN == 256 ? 6 : 7;
+    static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, TN);
+
+    static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
+    static __device__ __forceinline__ int slot_use(int, int n) { return n >> 1; }
+    static __device__ __forceinline__ int slot_col(int s) { return s * 256; }
+    static __device__ __forceinline__ Unit decode(const Args &a, int u)
+    {
+        Unit r;
+        r.p = u >= a.p[2].first ? 2 : u >= a.p[1].first ? 1 : 0;
+        const PairProblem &p = a.p[r.p];
+        const int t = u - p.first, tiles = p.mt * p.nt;
+        r.slice = t / tiles;
+        tile_order(t - r.slice * tiles, p.mt, p.nt, r.m, r.n);
+        const int64_t all = p.kb[0] + p.kb[1];
+        r.kb0 = (int)(all * r.slice / p.slices);
+        r.kbn = (int)(all * (r.slice + 1) / p.slices) - r.kb0;
+        return r;
+    }
+    static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int) { return 2 * STAGE_BYTES; }
+    template <bool MN, int ROWS>
+    static __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int k,
+                                                        uint32_t bar)
+    {
+        if (MN) {
+#pragma unroll
+            for (int i = 0; i < ROWS / 64; ++i) tma_load_2d_pair(dst + 8192 * i, map, row + 64 * i, k, bar);
+        } else {
+            tma_load_2d_pair(dst, map, k, row, bar);
+        }
+    }
+    static __device__ __forceinline__ void load(const Args &a, const Unit &u, int, int i, uint32_t rank, uint32_t dst,
+                                                uint32_t bar)
+    {
+        const PairProblem &p = a.p[u.p];
+        int kb = u.kb0 + i;
+        const int seg = kb >= p.kb[0];
+        if (seg) kb -= p.kb[0];
+        load_operand<A_MN, 128>(dst, &p.a[seg], u.m * 256 + (int)rank * 128, kb * 64, bar);
+        load_operand<B_MN, TN / 2>(dst + 16384, &p.b[seg], u.n * TN + (int)rank * (TN / 2), kb * 64, bar);
+    }
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int, int i, uint32_t src, uint32_t d)
+    {
+        const PairProblem &p = a.p[u.p];
+        int kb = u.kb0 + i;
+        const int seg = kb >= p.kb[0];
+        if (seg) kb -= p.kb[0];
+        mma_kblock<MMA_BF16, A_MN, B_MN>(d, src, src + 16384, IDESC, kblock_steps(p.k[seg], kb, 64), i == 0);
+    }
+    template <class Release>
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
+                                                    int half, int lane, uint32_t t_lane, uint8_t *stage,
+                                                    Release &&release)
+    {
+        const PairProblem &p = a.p[u.p];
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, colh = u.n * TN + half * (TN / 2);
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + half * (TN / 2);
+        if (p.slices > 1) {
+#pragma unroll 1
+            for (int j = 0; j < TN / 64; ++j) {
+                float v[32];
+                tmem_ld32(acc + 32 * j, v);
+                tmem_wait_ld();
+                if (j == TN / 64 - 1) release();
+                staging_free(lane);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<float4 *>(stage + sw128_offset(lane, q)) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && row0 < p.rows && colh + 32 * j < p.cols) {
+                    tma_store_3d(&p.part, colh + 32 * j, row0, u.slice, smem_u32(stage));
+                    bulk_commit();
+                }
+            }
+            return;
+        }
+        const bool row_ok = row0 + lane < p.rows;
+        const bf16 *res = p.residual && row_ok ? p.residual + (int64_t)(row0 + lane) * p.cols : nullptr;
+#pragma unroll 1
+        for (int j = 0; j < TN / 64; ++j) {
+            float v[32];
+            tmem_ld32(acc + 32 * j, v);
+            tmem_wait_ld();
+            if (j == TN / 64 - 1) release();
+            const int c0 = colh + 32 * j;
+            if (p.bias) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float b[8];
+                    load8(p.bias, c0 + 8 * q, p.cols, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+                }
+            }
+            if (res) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float b[8];
+                    load8(res, c0 + 8 * q, p.cols, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+                }
+            }
+            if ((j & 1) == 0) staging_free(lane);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4 *>(stage + sw128_offset(lane, 4 * (j & 1) + q)) = pack8f(v + 8 * q);
+            if (j & 1) store_box(&p.d, c0 - 32, row0, row0 < p.rows && c0 - 32 < p.cols, stage, lane);
+        }
+    }
+};
+
+// ---- the backward's recompute: h, dg, du -----------------------------------------
+//
+// A unit is 256 rows x 128 hidden columns: dh = dy Wd (K = C; Wd [C, F] as an
+// MN-major B) into 128 accumulator columns, then g | u as in the forward into
+// 256.  384 of the 512 TMEM columns do not fit twice; dh alternates between
+// two places of 128 columns, so that the next unit's dh (a third of its MMAs)
+// runs under this unit's epilogue.
+template <int ACT>
+struct GradPolicy {
+    struct Args {
+        CUtensorMap x, wg, wu, dy, wd, h, dg, du;
+        const bf16 *bg, *bu;
+        int rows, C, F, mt, nt, kb, units;
+        DeviceStatus st;
+    };
+    struct Unit {
+        int m, n;
+    };
+    static constexpr int STAGES = 5, STAGE_BYTES = 32768, STAGING = 6144, SEGS = 2;
+    static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 128);
+    static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 256);
+
+    // segment 0 (dh): slots 1 and 2 in turn; segment 1 (g | u): slot 0
+    static __device__ __forceinline__ int slot(int seg, int n) { return seg ? 0 : 1 + (n & 1); }
+    static __device__ __forceinline__ int slot_use(int seg, int n) { return seg ? n : n >> 1; }
+    static __device__ __forceinline__ int slot_col(int s) { return s == 0 ? 0 : 128 + 128 * s; }
+    static __device__ __forceinline__ Unit decode(const Args &a, int u)
+    {
+        Unit r;
+        tile_order(u, a.mt, a.nt, r.m, r.n);
+        return r;
+    }
+    static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int seg)
+    {
+        return seg ? 2 * STAGE_BYTES : 2 * (16384 + 8192);
+    }
+    static __device__ __forceinline__ void load(const Args &a, const Unit &u, int seg, int kb, uint32_t rank,
+                                                uint32_t dst, uint32_t bar)
+    {
+        const int row = u.m * 256 + (int)rank * 128;
+        if (seg == 0) {
+            tma_load_2d_pair(dst, &a.dy, kb * 64, row, bar);
+            tma_load_2d_pair(dst + 16384, &a.wd, u.n * 128 + (int)rank * 64, kb * 64, bar);
+        } else {
+            tma_load_2d_pair(dst, &a.x, kb * 64, row, bar);
+            tma_load_2d_pair(dst + 16384, rank ? &a.wu : &a.wg, kb * 64, u.n * 128, bar);
+        }
+    }
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int seg, int kb, uint32_t src, uint32_t d)
+    {
+        const int steps = kblock_steps(a.C, kb, 64);
+        if (seg == 0) mma_kblock<MMA_BF16, false, true>(d, src, src + 16384, IDESC_H, steps, kb == 0);
+        else mma_kblock<MMA_BF16, false, false>(d, src, src + 16384, IDESC_GU, steps, kb == 0);
+    }
+    template <class Release>
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
+                                                    int half, int lane, uint32_t t_lane, uint8_t *stage,
+                                                    Release &&release)
+    {
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + half * 64;
+        const uint32_t gu = t_lane + half * 64, dh = t_lane + slot_col(slot(0, n)) + half * 64;
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+            float g[32], v[32], d[32];
+            tmem_ld32(gu + 32 * j, g);
+            tmem_ld32(gu + 128 + 32 * j, v);
+            tmem_ld32(dh + 32 * j, d);
+            tmem_wait_ld();
+            if (j == 1) release();
+            staging_free(lane);
+            const int c0 = col0 + 32 * j;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (a.bg) {
+                    float b[8];
+                    load8(a.bg, c0 + 8 * q, a.F, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[8 * q + e] += b[e];
+                }
+                if (a.bu) {
+                    float b[8];
+                    load8(a.bu, c0 + 8 * q, a.F, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+                }
+                float hh[8], dg[8], du[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float deriv;
+                    const float act = activate<ACT, true>(g[8 * q + e], deriv);
+                    const float x = v[8 * q + e], y = d[8 * q + e];
+                    hh[e] = act * x;
+                    dg[e] = y * x * deriv;
+                    du[e] = y * act;
+                }
+                const uint32_t off = sw64_offset(lane, q);
+                *reinterpret_cast<uint4 *>(stage + off) = pack8f(hh);
+                *reinterpret_cast<uint4 *>(stage + 2048 + off) = pack8f(dg);
+                *reinterpret_cast<uint4 *>(stage + 4096 + off) = pack8f(du);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < a.rows && c0 < a.F) {
+                tma_store_2d(&a.h, c0, row0, smem_u32(stage));
+                tma_store_2d(&a.dg, c0, row0, smem_u32(stage + 2048));
+                tma_store_2d(&a.du, c0, row0, smem_u32(stage + 4096));
+                bulk_commit();
+            }
+        }
+    }
+};
+
+} // namespace swin

@@ -1,0 +1,334 @@
+// The CTA-pair GEMM skeleton of the gated feed-forward kernels: persistent
+// clusters of two CTAs, each pair computing 256-row tiles with
+// tcgen05.mma.cta_group::2 (each CTA holds half of the rows of A, half of the
+// rows of B and the accumulators of its 128 rows), operands staged by TMA in a
+// ring of shared-memory stages, accumulators handed to eight epilogue warps.
+//
+// Why pairs: a 256 x 256 x 64 step reads 32 KB of shared memory a CTA for 2 x
+// 256 x 256 x 64 FLOPs a pair, half of what two independent 128 x 256 tiles
+// read, which is what lets the tensor cores run at their rate.
+//
+// Roles (320 threads): warp 0 loads (one thread in each CTA, its own halves,
+// signalling the leader's barrier), warp 1 of the leader issues the MMAs, warps
+// 2..9 of both CTAs drain (warp w owns TMEM lane quarter w % 4 and one half of
+// the columns).  Every wait is bounded; on expiry the error word is set, the
+// roles leave, and the CTAs meet at the closing cluster barrier.
+//
+// A policy P describes the kernel:
+//   Args                    kernel parameters (units: work items; st: DeviceStatus)
+//   Unit / decode(a, u)     one work item (a tile, or a K slice of one)
+//   STAGES, STAGE_BYTES     the ring
+//   STAGING                 bytes of store staging per epilogue warp
+//   SEGS                    accumulation segments of a unit (each a K loop
+//                           into one slot of TMEM columns)
+//   slot(seg, n), slot_col(slot), slot_use(seg, n)   the slot of the n-th unit
+//                           of this pair, its first column, how often it was used
+//   kblocks(a, u, seg), tx(a, u, seg), load(...), mma(...), epilogue(...)
+#pragma once
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace swin {
+
+constexpr int PAIR_EPI = 8;
+constexpr int PAIR_THREADS = 64 + 32 * PAIR_EPI;
+constexpr int PAIR_SLOTS = 3;
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Cluster address of the shared-memory location `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Bounded wait (as mbar_wait) that also acquires what the other CTA released.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    uint32_t ok;
+    uint64_t t0 = 0;
+    while (true) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t t = global_timer_ns();
+        if (!t0) t0 = t;
+        else if (t - t0 > limit_ns) return false;
+    }
+}
+// 2-D TMA load into this CTA's shared memory, completing on a barrier that may
+// be the peer's (cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when the MMAs issued so
+// far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+enum { MMA_BF16 = 0, MMA_E4M3 = 1 };
+template <int KIND>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+{
+    if (KIND == MMA_BF16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// Instruction descriptor: fp32 accumulator, bf16 or e4m3 operands, each K-major
+// or MN-major (bf16 only), M x N.
+__host__ __device__ constexpr uint32_t idesc_pair(int kind, bool a_mn, bool b_mn, int M, int N)
+{
+    return (1u << 4) | (kind == MMA_BF16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+           (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Operand tiles, 128-byte swizzle.  K-major: rows of 128 bytes of K, 8-row
+// atoms stacked densely; a step of 32 bytes of K moves the start by 32.
+// MN-major: boxes of 64 MN elements (128 bytes) x 64 k, boxes 8 KB apart; a step
+// of 16 k moves the start by 16 rows.
+template <bool MN>
+__device__ __forceinline__ uint64_t desc_pair(uint32_t addr, int step)
+{
+    return MN ? smem_desc(addr + 2048u * step, 8192, 1024, SWZ_128B) : desc_kmajor_sw128(addr + 32u * step);
+}
+template <int KIND, bool A_MN, bool B_MN>
+__device__ __forceinline__ void mma_kblock(uint32_t d, uint32_t a_addr, uint32_t b_addr, uint32_t idesc, int steps,
+                                           bool first)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < steps)
+            mma_pair<KIND>(d, desc_pair<A_MN>(a_addr, k), desc_pair<B_MN>(b_addr, k), idesc, !(first && k == 0));
+}
+// MMA steps of K block kb of a K of `k` elements (block: 128 bytes, four steps).
+__device__ __forceinline__ int kblock_steps(int k, int kb, int elems)
+{
+    const int left = k - kb * elems, per = elems / 4;
+    return left >= elems ? 4 : (left + per - 1) / per;
+}
+
+template <class P>
+struct PairSmem {
+    static constexpr int BARS = 2 * P::STAGES + 2 * PAIR_SLOTS;
+    static constexpr size_t ring = (size_t)P::STAGES * P::STAGE_BYTES;
+    static constexpr size_t bytes = 1024 + ring + PAIR_EPI * P::STAGING + BARS * 8 + 16;
+    static_assert(bytes <= 227 * 1024, "shared memory");
+};
+
+// Order of an mt x nt grid of tiles: bands of eight row tiles, column by column
+// inside a band, so that the tiles in flight share rows of A and of B in L2.
+__device__ __forceinline__ void tile_order(int t, int mt, int nt, int &m, int &n)
+{
+    const int band = t / (8 * nt), r = t - band * 8 * nt;
+    const int h = mt - band * 8 < 8 ? mt - band * 8 : 8;
+    n = r / h;
+    m = band * 8 + (r - n * h);
+}
+
+template <class P>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+pair_kernel(const __grid_constant__ typename P::Args a)
+{
+    using L = PairSmem<P>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_align(smem_raw, 1024);
+    uint8_t *staging = smem + L::ring;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + PAIR_EPI * P::STAGING);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * P::STAGES, tfull = empty + 8 * P::STAGES,
+                   tempty = tfull + 8 * PAIR_SLOTS;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + L::BARS);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < PAIR_SLOTS; ++s) {
+            mbar_init(tfull + 8 * s, 1);
+            mbar_init(tempty + 8 * s, 2 * PAIR_EPI);   // (the leader's: the epilogue warps of both CTAs)
+        }
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tslot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    bool failed = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t ring = smem_u32(smem), lead_full = map_rank(full, 0);
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            for (int u = first; u < a.units && !failed; u += step) {
+                const typename P::Unit un = P::decode(a, u);
+                for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
+                    const int kb_n = P::kblocks(a, un, seg);
+                    for (int kb = 0; kb < kb_n; ++kb) {
+                        if (!mbar_wait_cluster(empty + 8 * s, ph ^ 1u, a.st.wait_ns)) {
+                            failed = true;
+                            break;
+                        }
+                        if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, P::tx(a, un, seg));
+                        P::load(a, un, seg, kb, rank, ring + s * P::STAGE_BYTES, lead_full + 8 * s);
+                        ++issued;
+                        if (++s == P::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+            }
+            // every stage given back: no commit is on its way to this CTA's
+            // barriers when it ends
+            for (int k = 0; k < P::STAGES && k < issued && !failed; ++k) {
+                failed = !mbar_wait_cluster(empty + 8 * s, ph ^ 1u, a.st.wait_ns);
+                if (++s == P::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (failed) {
+                // copies in flight land before this CTA's memory is given back:
+                // the leader's barriers say so for both CTAs
+                if (rank == 0)
+                    for (int k = 0; k < P::STAGES && k < issued; ++k) {
+                        if (--s < 0) {
+                            s = P::STAGES - 1;
+                            ph ^= 1u;
+                        }
+                        mbar_wait_cluster(full + 8 * s, ph, a.st.wait_ns);
+                    }
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            const uint32_t ring = smem_u32(smem);
+            int s = 0, n = 0;
+            uint32_t ph = 0;
+            for (int u = first; u < a.units && !failed; u += step, ++n) {
+                const typename P::Unit un = P::decode(a, u);
+                for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
+                    const int slot = P::slot(seg, n), kb_n = P::kblocks(a, un, seg);
+                    if (!mbar_wait_cluster(tempty + 8 * slot, (P::slot_use(seg, n) & 1) ^ 1, a.st.wait_ns)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + P::slot_col(slot);
+                    for (int kb = 0; kb < kb_n; ++kb) {
+                        if (!mbar_wait_cluster(full + 8 * s, ph, a.st.wait_ns)) {
+                            failed = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        P::mma(a, un, seg, kb, ring + s * P::STAGE_BYTES, d);
+                        mma_commit_pair(empty + 8 * s);
+                        if (++s == P::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    if (!failed) mma_commit_pair(tfull + 8 * slot);
+                }
+            }
+        }
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+        uint8_t *stage = staging + (warp - 2) * P::STAGING;
+        int n = 0;
+        for (int u = first; u < a.units && !failed; u += step, ++n) {
+            const typename P::Unit un = P::decode(a, u);
+            // (warp-uniform outcome: the TMEM loads below are warp-collective)
+            for (int seg = 0; seg < P::SEGS && !failed; ++seg)
+                failed = !__all_sync(0xffffffffu, mbar_wait_cluster(tfull + 8 * P::slot(seg, n),
+                                                                    P::slot_use(seg, n) & 1, a.st.wait_ns));
+            if (failed) break;
+            tc_fence_after();
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    for (int seg = 0; seg < P::SEGS; ++seg)
+                        mbar_arrive_cluster(map_rank(tempty + 8 * P::slot(seg, n), 0));
+            };
+            P::epilogue(a, un, n, rank, quad, half, lane, t_lane, stage, release);
+        }
+        // the staged stores have read shared memory, and are complete
+        if (lane == 0) bulk_wait_all();
+    }
+    if (failed && lane == 0) atomicOr(a.st.err, ERR_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+template <class P>
+cudaError_t launch_pair(const typename P::Args &a, cudaStream_t stream)
+{
+    constexpr size_t smem = PairSmem<P>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int pairs = sm_count() / 2;
+    const unsigned grid = 2u * (unsigned)(a.units < pairs ? a.units : pairs);
+    pair_kernel<P><<<grid, PAIR_THREADS, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+} // namespace swin
