@@ -333,36 +333,49 @@ def swin_merge_forward(h, x, gamma, beta, Wm, out, stream=None):
 
 # ---- swin_rms.h ------------------------------------------------------------------
 
-def _arg(name, t, dtype, *shape):
-    """Pointer of a required argument, checked: dtype, shape, contiguous, on the
-    current CUDA device."""
+def _refuse(name, t, dtype, shape):
     if t.dtype != dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must be of shape %s, not %s" % (name, shape, tuple(t.shape)))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be of shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError("%s must be on the current CUDA device" % name)
+    raise ValueError("%s must be on the current CUDA device" % name)
+
+
+def _arg(name, t, dtype, shape, dev):
+    """Pointer of a required argument, checked: dtype, shape, contiguous, on
+    device dev (-1, no device, is refused for every tensor)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+        _refuse(name, t, dtype, shape)
     return t.data_ptr()
 
 
-def _opt(name, t, dtype, *shape):
+def _opt(name, t, dtype, shape, dev):
     """The same for an optional argument (None -> NULL)."""
-    return None if t is None else _arg(name, t, dtype, *shape)
+    return None if t is None else _arg(name, t, dtype, shape, dev)
 
 
-def _rows(x):
-    """rows, C of x [..., C]."""
+def _device():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev):
+    """Raw stream of a call: the given one, or the current one of device dev."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _rows(h, x):
+    """rows of x [..., C], C; h: the handle, for C channels."""
     C = x.shape[-1]
-    return (x.numel() // C if C else 0), C
-
-
-def _rms_rows(h, x):
-    rows, C = _rows(x)
     if C != h.C:
         raise ValueError("the handle is for C = %d, not %d" % (h.C, C))
-    return rows, C
+    return x.numel() // C, C
 
 
 def swin_block_rms_create(C, eps=1e-6):
@@ -383,30 +396,32 @@ def swin_block_rms_last_launches(h):
 def swin_block_rms_forward(h, x, gamma, out, residual=None, out_sum=None, stream=None):
     """out = RMS norm of x + residual over the last axis of x [..., C]; out_sum
     receives the sum."""
-    rows, C = _rms_rows(h, x)
-    bf, shape = torch.bfloat16, x.shape
+    rows, C = _rows(h, x)
+    bf, shape, dev = torch.bfloat16, x.shape, _device()
     return _check("swin_block_rms_forward", load().swin_block_rms_forward(
-        h, _arg("x", x, bf, *shape), _opt("residual", residual, bf, *shape), rows, _arg("gamma", gamma, bf, C),
-        _opt("out_sum", out_sum, bf, *shape), _arg("out", out, bf, *shape), _stream(stream)))
+        h, _arg("x", x, bf, shape, dev), _opt("residual", residual, bf, shape, dev), rows,
+        _arg("gamma", gamma, bf, (C,), dev), _opt("out_sum", out_sum, bf, shape, dev),
+        _arg("out", out, bf, shape, dev), _stream_on(stream, dev)))
 
 
 def swin_block_rms_forward_q8(h, x, gamma, out8, scales, residual=None, out_sum=None, stream=None):
     """The same in e4m3 codes out8 [..., C] with one fp32 scale a row."""
-    rows, C = _rms_rows(h, x)
-    bf, shape = torch.bfloat16, x.shape
+    rows, C = _rows(h, x)
+    bf, shape, dev = torch.bfloat16, x.shape, _device()
     return _check("swin_block_rms_forward_q8", load().swin_block_rms_forward_q8(
-        h, _arg("x", x, bf, *shape), _opt("residual", residual, bf, *shape), rows, _arg("gamma", gamma, bf, C),
-        _opt("out_sum", out_sum, bf, *shape), _arg("out8", out8, torch.float8_e4m3fn, *shape),
-        _arg("scales", scales, torch.float32, *shape[:-1]), _stream(stream)))
+        h, _arg("x", x, bf, shape, dev), _opt("residual", residual, bf, shape, dev), rows,
+        _arg("gamma", gamma, bf, (C,), dev), _opt("out_sum", out_sum, bf, shape, dev),
+        _arg("out8", out8, torch.float8_e4m3fn, shape, dev), _arg("scales", scales, torch.float32, shape[:-1], dev),
+        _stream_on(stream, dev)))
 
 
 def swin_block_rms_backward(h, s, gamma, dy, dx, dgamma, dsum=None, stream=None):
-    rows, C = _rms_rows(h, s)
-    bf, shape = torch.bfloat16, s.shape
+    rows, C = _rows(h, s)
+    bf, shape, dev = torch.bfloat16, s.shape, _device()
     return _check("swin_block_rms_backward", load().swin_block_rms_backward(
-        h, _arg("s", s, bf, *shape), rows, _arg("gamma", gamma, bf, C), _arg("dy", dy, bf, *shape),
-        _opt("dsum", dsum, bf, *shape), _arg("dx", dx, bf, *shape), _arg("dgamma", dgamma, torch.float32, C),
-        _stream(stream)))
+        h, _arg("s", s, bf, shape, dev), rows, _arg("gamma", gamma, bf, (C,), dev), _arg("dy", dy, bf, shape, dev),
+        _opt("dsum", dsum, bf, shape, dev), _arg("dx", dx, bf, shape, dev),
+        _arg("dgamma", dgamma, torch.float32, (C,), dev), _stream_on(stream, dev)))
 
 
 # ---- swin_gated.h ------------------------------------------------------------------
@@ -421,23 +436,12 @@ class GatedParamsQ8(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("Wg8", "sg", "bg", "Wu8", "su", "bu", "Wd", "bd")]
 
 
-def _gated(x, p, dtype, names):
-    """rows, C, F and the checked struct of a call on x [..., C] with the tensors
-    of dict p: names of Wg, bg, Wu, bu, Wd, bd (and, between, the scales)."""
-    rows, C = _rows(x)
-    F = p[names[0]].shape[0]
-    bf = torch.bfloat16
-    vals = [_arg(names[0], p[names[0]], dtype, F, C)]
-    for n in names[1:]:
-        if n.endswith("8") or n[-2:] in ("Wg", "Wu"):
-            vals.append(_arg(n, p[n], dtype, F, C))
-        elif n.endswith("Wd"):
-            vals.append(_arg(n, p[n], bf, C, F))
-        elif n in ("sg", "su"):
-            vals.append(_arg(n, p[n], torch.float32, F))
-        else:
-            vals.append(_opt(n, p.get(n), bf, C if n.endswith("bd") else F))
-    return rows, C, F, vals
+def _gated_params(h, p, dev):
+    """The parameters' checked pointers, in the struct."""
+    bf, wide, F = torch.bfloat16, (h.F, h.C), (h.F,)
+    return GatedParams(_arg("Wg", p["Wg"], bf, wide, dev), _opt("bg", p.get("bg"), bf, F, dev),
+                       _arg("Wu", p["Wu"], bf, wide, dev), _opt("bu", p.get("bu"), bf, F, dev),
+                       _arg("Wd", p["Wd"], bf, (h.C, h.F), dev), _opt("bd", p.get("bd"), bf, (h.C,), dev))
 
 
 def swin_block_gated_create(C, F, act=BLOCK_GATED_SILU):
@@ -459,42 +463,42 @@ def swin_block_gated_sync_status(h, stream=None):
     return _check("swin_block_gated_sync_status", load().swin_block_gated_sync_status(h, _stream(stream)))
 
 
-def _same_handle(h, C, F):
-    if (h.C, h.F) != (C, F):
-        raise ValueError("the handle is for C = %d, F = %d, not C = %d, F = %d" % (h.C, h.F, C, F))
-
-
 def swin_block_gated_forward(h, x, params, out, residual=None, stream=None):
     """out = residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd for x [..., C];
     params: dict with Wg, bg, Wu, bu, Wd, bd (biases may be None)."""
-    rows, C, F, vals = _gated(x, params, torch.bfloat16, ("Wg", "bg", "Wu", "bu", "Wd", "bd"))
-    _same_handle(h, C, F)
-    bf, shape = torch.bfloat16, x.shape
+    rows, _ = _rows(h, x)
+    bf, shape, dev = torch.bfloat16, x.shape, _device()
+    p = _gated_params(h, params, dev)
     return _check("swin_block_gated_forward", load().swin_block_gated_forward(
-        h, _arg("x", x, bf, *shape), rows, ctypes.addressof(s := GatedParams(*vals)),
-        _opt("residual", residual, bf, *shape), _arg("out", out, bf, *shape), _stream(stream)))
+        h, _arg("x", x, bf, shape, dev), rows, ctypes.addressof(p), _opt("residual", residual, bf, shape, dev),
+        _arg("out", out, bf, shape, dev), _stream_on(stream, dev)))
 
 
 def swin_block_gated_forward_q8(h, x8, sx, params, out, residual=None, stream=None):
     """The same from e4m3 x8 [..., C] with scales sx [...]; params: dict with Wg8,
     sg, bg, Wu8, su, bu, Wd, bd (biases may be None)."""
-    e4m3 = torch.float8_e4m3fn
-    rows, C, F, vals = _gated(x8, params, e4m3, ("Wg8", "sg", "bg", "Wu8", "su", "bu", "Wd", "bd"))
-    _same_handle(h, C, F)
-    bf, shape = torch.bfloat16, x8.shape
+    rows, _ = _rows(h, x8)
+    bf, f32, e4m3, shape, dev = torch.bfloat16, torch.float32, torch.float8_e4m3fn, x8.shape, _device()
+    wide, F = (h.F, h.C), (h.F,)
+    p = GatedParamsQ8(_arg("Wg8", params["Wg8"], e4m3, wide, dev), _arg("sg", params["sg"], f32, F, dev),
+                      _opt("bg", params.get("bg"), bf, F, dev), _arg("Wu8", params["Wu8"], e4m3, wide, dev),
+                      _arg("su", params["su"], f32, F, dev), _opt("bu", params.get("bu"), bf, F, dev),
+                      _arg("Wd", params["Wd"], bf, (h.C, h.F), dev), _opt("bd", params.get("bd"), bf, (h.C,), dev))
     return _check("swin_block_gated_forward_q8", load().swin_block_gated_forward_q8(
-        h, _arg("x8", x8, e4m3, *shape), _arg("sx", sx, torch.float32, *shape[:-1]), rows,
-        ctypes.addressof(s := GatedParamsQ8(*vals)), _opt("residual", residual, bf, *shape),
-        _arg("out", out, bf, *shape), _stream(stream)))
+        h, _arg("x8", x8, e4m3, shape, dev), _arg("sx", sx, f32, shape[:-1], dev), rows, ctypes.addressof(p),
+        _opt("residual", residual, bf, shape, dev), _arg("out", out, bf, shape, dev), _stream_on(stream, dev)))
 
 
 def swin_block_gated_backward(h, x, params, dy, dx, grads, stream=None):
     """Gradients of the bf16 form: dx and, in the tensors of dict grads, dWg, dWu,
     dWd and (where not None) dbg, dbu, dbd, all bf16."""
-    rows, C, F, vals = _gated(x, params, torch.bfloat16, ("Wg", "bg", "Wu", "bu", "Wd", "bd"))
-    _, _, _, gvals = _gated(x, grads, torch.bfloat16, ("dWg", "dbg", "dWu", "dbu", "dWd", "dbd"))
-    _same_handle(h, C, F)
-    bf, shape = torch.bfloat16, x.shape
+    rows, _ = _rows(h, x)
+    bf, shape, dev = torch.bfloat16, x.shape, _device()
+    wide, F = (h.F, h.C), (h.F,)
+    p = _gated_params(h, params, dev)
+    g = GatedParams(_arg("dWg", grads["dWg"], bf, wide, dev), _opt("dbg", grads.get("dbg"), bf, F, dev),
+                    _arg("dWu", grads["dWu"], bf, wide, dev), _opt("dbu", grads.get("dbu"), bf, F, dev),
+                    _arg("dWd", grads["dWd"], bf, (h.C, h.F), dev), _opt("dbd", grads.get("dbd"), bf, (h.C,), dev))
     return _check("swin_block_gated_backward", load().swin_block_gated_backward(
-        h, _arg("x", x, bf, *shape), rows, ctypes.addressof(s := GatedParams(*vals)), _arg("dy", dy, bf, *shape),
-        _arg("dx", dx, bf, *shape), ctypes.addressof(g := GatedParams(*gvals)), _stream(stream)))
+        h, _arg("x", x, bf, shape, dev), rows, ctypes.addressof(p), _arg("dy", dy, bf, shape, dev),
+        _arg("dx", dx, bf, shape, dev), ctypes.addressof(g), _stream_on(stream, dev)))

@@ -81,6 +81,8 @@ struct ReduceArgs {
 };
 __global__ void __launch_bounds__(256) reduce_slices_kernel(ReduceArgs a)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const ReduceItem &t = a.it[blockIdx.y];
     const int64_t n = t.rows * t.cols;
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
@@ -203,8 +205,8 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     int64_t blocks = ceil_div(most, 2048);
     if (blocks > 8 * sm_count()) blocks = 8 * sm_count();
     ++*launches;
-    reduce_slices_kernel<<<dim3((unsigned)blocks, (unsigned)pl.n), 256, 0, stream>>>(r);
-    return cudaGetLastError();
+    return launch_maybe_overlapped(reduce_slices_kernel, dim3((unsigned)blocks, (unsigned)pl.n), dim3(256), 0, stream, 1,
+                                   r);
 }
 
 template <bool A_MN, bool B_MN>
@@ -229,6 +231,8 @@ struct ColumnSums {
 __global__ void __launch_bounds__(256) column_partials_kernel(ColumnSums a)
 {
     __shared__ float sum[32][65];
+    griddep_launch_dependents();
+    griddep_wait();
     const int z = blockIdx.z, cols = a.cols[z];
     const int c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
     if (blockIdx.x * 64 >= cols) return;
@@ -251,6 +255,8 @@ __global__ void __launch_bounds__(256) column_partials_kernel(ColumnSums a)
 }
 __global__ void __launch_bounds__(256) column_finish_kernel(ColumnSums a)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const int z = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
     if (c >= a.cols[z]) return;
     float t = 0.f;
@@ -562,10 +568,11 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         if (cols > most) most = cols;
     }
     if (e == cudaSuccess && sums) {
-        column_partials_kernel<<<dim3(ceil_div(most, 64), cs.splits, sums), 256, 0, s>>>(cs);
-        column_finish_kernel<<<dim3(ceil_div(most, 256), sums), 256, 0, s>>>(cs);
         h->last_launches += 2;
-        e = cudaGetLastError();
+        e = launch_maybe_overlapped(column_partials_kernel, dim3(ceil_div(most, 64), cs.splits, sums), dim3(256), 0, s, 1,
+                                    cs);
+        if (e == cudaSuccess)
+            e = launch_maybe_overlapped(column_finish_kernel, dim3(ceil_div(most, 256), sums), dim3(256), 0, s, 1, cs);
     }
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;

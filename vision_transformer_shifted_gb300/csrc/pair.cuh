@@ -26,6 +26,8 @@
 //   kblocks(a, u, seg), tx(a, u, seg), load(...), mma(...), epilogue(...)
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -205,6 +207,10 @@ pair_kernel(const __grid_constant__ typename P::Args a)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     bool failed = false;
+    // launched while the kernel before it drains: no global memory is touched
+    // until that kernel, and so every earlier one, has completed
+    griddep_launch_dependents();
+    griddep_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -323,12 +329,19 @@ template <class P>
 cudaError_t launch_pair(const typename P::Args &a, cudaStream_t stream)
 {
     constexpr size_t smem = PairSmem<P>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> ready;   // devices whose copy of the kernel may use this much shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {
+        e = cudaFuncSetAttribute(pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit);
+    }
     const int pairs = sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(a.units < pairs ? a.units : pairs);
-    pair_kernel<P><<<grid, PAIR_THREADS, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_maybe_overlapped(pair_kernel<P>, dim3(grid), dim3(PAIR_THREADS), smem, stream, 1, a);
 }
 
 } // namespace swin

@@ -68,6 +68,28 @@ __device__ __forceinline__ float row_reduce(float v, int lpr, float *red)
     return v;
 }
 
+// The sums of a and b over the lanes of a row.
+template <bool BLOCK>
+__device__ __forceinline__ void row_sum2(float &a, float &b, int lpr, float2 *red)
+{
+    const int lanes = BLOCK ? 32 : lpr;
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (BLOCK) {
+        const int warps = blockDim.x >> 5;
+        __syncthreads();   // (the previous row's sums have been read)
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+        for (int w = 0; w < warps; ++w) {
+            a += red[w].x;
+            b += red[w].y;
+        }
+    }
+}
+
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8])
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -78,6 +100,9 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8])
         v[2 * e + 1] = f.y;
     }
 }
+
+// The compiler takes u for a new value from here on.
+__device__ __forceinline__ void forget(uint4 &u) { asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)); }
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8])
 {
@@ -91,6 +116,8 @@ template <int CPL, bool BLOCK, bool Q8>
 __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs a)
 {
     __shared__ float red[16];
+    griddep_launch_dependents();
+    griddep_wait();   // (nothing is read before the kernels queued earlier are done)
     const int lane = threadIdx.x & 31;
     const int step = BLOCK ? (int)blockDim.x : a.lpr;
     const int li = BLOCK ? (int)threadIdx.x : lane % a.lpr;
@@ -125,6 +152,12 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs 
 #pragma unroll
         for (int e = 0; e < 8; ++e) sq = fmaf(v[e], v[e], sq);
     }
+    uint4 gm[CPL];   // (asked for before the row's sum is known)
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+        gm[k] = row_ok && c < a.chunks ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
+    }
     sq = row_reduce<AddOp, BLOCK>(sq, a.lpr, red);
     const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps));
     if (!Q8) {
@@ -134,7 +167,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs 
             if (!(row_ok && c < a.chunks)) continue;
             float v[8], g[8];
             unpack8(s[k], v);
-            unpack8(ld16(a.gamma + c * 8), g);
+            unpack8(gm[k], g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = v[e] * r * g[e];
             *reinterpret_cast<uint4 *>((bf16 *)a.out + base + c * 8) = pack8(v);
@@ -149,7 +182,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs 
         const bool ok = row_ok && c < a.chunks;
         float g[8];
         unpack8(s[k], y[k]);
-        unpack8(ok ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0), g);
+        unpack8(gm[k], g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             y[k][e] = y[k][e] * r * g[e];
@@ -189,13 +222,15 @@ struct RmsBwdArgs {
 // part of a warp); each thread keeps the columns it owns of dgamma in
 // registers over its rows, and the block writes one partial row at the end.
 template <int CPL, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_backward_kernel(RmsBwdArgs a)
+__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? (CPL > 2 ? 1 : 2) : 3) rms_backward_kernel(RmsBwdArgs a)
 {
     extern __shared__ float part[];   // !BLOCK: [8 warps][C]
-    __shared__ float red[16];
+    __shared__ float2 red[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int step = BLOCK ? (int)blockDim.x : a.lpr;
     const int li = BLOCK ? (int)threadIdx.x : lane % a.lpr;
+    griddep_launch_dependents();
+    griddep_wait();
     const int rpw = BLOCK ? 1 : 32 / a.lpr, rpb = BLOCK ? 1 : rpw * (int)(blockDim.x >> 5);
     float acc[CPL][8];
     uint4 g[CPL];
@@ -232,8 +267,16 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_backward_kernel(RmsBwdA
                 dot = fmaf(y[e] * w[e], v[e], dot);
             }
         }
-        sq = row_reduce<AddOp, BLOCK>(sq, a.lpr, red);
-        dot = row_reduce<AddOp, BLOCK>(dot, a.lpr, red);
+        row_sum2<BLOCK>(sq, dot, a.lpr, red);
+        // (the packed values stay, their fp32 forms are made again: registers
+        // kept across the sums would halve the rows in flight)
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            forget(s[k]);
+            forget(d[k]);
+            forget(g[k]);
+            forget(m[k]);
+        }
         const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps));
         const float q = dot * a.inv_c * r * r;   // mean(a n) / s-scale: n mean(a n) = s q
 #pragma unroll
@@ -254,7 +297,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_backward_kernel(RmsBwdA
     }
     const int C = a.chunks * 8;
     float *mine = a.partial + (int64_t)blockIdx.x * C;
-    if (BLOCK) {
+    if constexpr (BLOCK) {
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
@@ -264,42 +307,47 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_backward_kernel(RmsBwdA
                 *reinterpret_cast<float4 *>(mine + c * 8 + 4 * q) =
                     make_float4(acc[k][4 * q], acc[k][4 * q + 1], acc[k][4 * q + 2], acc[k][4 * q + 3]);
         }
-        return;
-    }
-    // the warp's rows, then the block's warps
+    } else {
+        // the warp's rows, then the block's warps
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) {
-        const int c = li + k * step;
+        for (int k = 0; k < CPL; ++k) {
+            const int c = li + k * step;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = acc[k][e];
-            for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
+            for (int e = 0; e < 8; ++e) {
+                float v = acc[k][e];
+                for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
+            }
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < C; i += blockDim.x) {
-        float v = 0.f;
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += part[w * C + i];
-        mine[i] = v;
+        __syncthreads();
+        for (int i = threadIdx.x; i < C; i += blockDim.x) {
+            float v = 0.f;
+            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += part[w * C + i];
+            mine[i] = v;
+        }
     }
 }
 
-// out[c] = the sum of n partial rows, in a fixed order: 32 columns a block,
-// eight threads a column.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float *partial, int n, int C, float *out)
+// out[c] = the sum of n partial rows, in a fixed order: 32 columns a block, 32
+// threads a column.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, int n, int C, float *out)
 {
-    __shared__ float part[8][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    griddep_launch_dependents();
+    griddep_wait();
     float v = 0.f;
-    if (c < C)
-        for (int i = w; i < n; i += 8) v += partial[(int64_t)i * C + c];
-    part[w][threadIdx.x & 31] = v;
-    __syncthreads();
-    if (w == 0 && c < C) {
-        for (int k = 1; k < 8; ++k) v += part[k][threadIdx.x];
-        out[c] = v;
+    if (c < C) {
+#pragma unroll 8
+        for (int i = w; i < n; i += 32) v += partial[(int64_t)i * C + c];
     }
+    part[w][lane] = v;
+    __syncthreads();
+    // warp w adds column w of the block
+    v = part[lane][w];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * 32 + w < C) out[blockIdx.x * 32 + w] = v;
 }
 
 // How a row of `chunks` 16-byte pieces is laid out: on the fewest lanes of a
@@ -334,15 +382,17 @@ constexpr int FWD_PIECES = 4, BWD_PIECES = 2;
 template <bool Q8>
 cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
 {
-    const RowPlan p = plan_row(a.chunks, FWD_PIECES);
+    // rows that leave SMs idle take as many threads as pieces: the latency of
+    // one row counts then (1 x 2048: 5.6 us on 64 threads)
+    const RowPlan p = plan_row(a.chunks, a.rows < sm_count() ? 1 : FWD_PIECES);
     a.lpr = p.lpr;
     const int64_t rpb = p.block ? 1 : (p.threads / 32) * (32 / p.lpr);
     const unsigned grid = (unsigned)((a.rows + rpb - 1) / rpb);
 #define SWIN_RMS_CASE(n)                                                                      \
     case n:                                                                                   \
-        if (p.block) rms_forward_kernel<n, true, Q8><<<grid, p.threads, 0, stream>>>(a);      \
-        else rms_forward_kernel<n, false, Q8><<<grid, p.threads, 0, stream>>>(a);             \
-        break;
+        return launch_maybe_overlapped(p.block ? rms_forward_kernel<n, true, Q8>              \
+                                               : rms_forward_kernel<n, false, Q8>,            \
+                                       dim3(grid), dim3(p.threads), 0, stream, 1, a);
     switch (p.cpl) {
         SWIN_RMS_CASE(1)
         SWIN_RMS_CASE(2)
@@ -352,14 +402,15 @@ cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
         return cudaErrorInvalidValue;
     }
 #undef SWIN_RMS_CASE
-    return cudaGetLastError();
 }
 
-// Blocks of the backward: enough to fill the SMs, each with several rows.
+// Blocks of the backward: as many as the SMs hold at once, each walking its
+// share of the rows.
 int backward_grid(const RowPlan &p, int rows)
 {
     const int64_t rpb = p.block ? 1 : (p.threads / 32) * (32 / p.lpr);
-    const int64_t want = (rows + rpb - 1) / rpb, most = (int64_t)sm_count() * (2048 / p.threads / 2);
+    const int64_t want = (rows + rpb - 1) / rpb, per_sm = !p.block ? 3 : p.cpl <= 2 ? 1024 / p.threads : 1;
+    const int64_t most = sm_count() * per_sm;
     return (int)(want < most ? want : most);
 }
 
@@ -368,24 +419,13 @@ cudaError_t launch_rms_backward(RmsBwdArgs a, int grid, const RowPlan &p, float 
     a.lpr = p.lpr;
     const int C = a.chunks * 8;
     const size_t smem = p.block ? 0 : (size_t)(p.threads / 32) * C * sizeof(float);
-#define SWIN_RMS_CASE(n)                                                                      \
-    case n:                                                                                   \
-        if (p.block) rms_backward_kernel<n, true><<<grid, p.threads, smem, stream>>>(a);      \
-        else rms_backward_kernel<n, false><<<grid, p.threads, smem, stream>>>(a);             \
-        break;
-    switch (p.cpl) {
-        SWIN_RMS_CASE(1)
-        SWIN_RMS_CASE(2)
-        SWIN_RMS_CASE(3)
-        SWIN_RMS_CASE(4)
-    default:
-        return cudaErrorInvalidValue;
-    }
-#undef SWIN_RMS_CASE
-    cudaError_t e = cudaGetLastError();
+    void (*kern)(RmsBwdArgs) = nullptr;
+    if (p.block) kern = p.cpl <= 2 ? rms_backward_kernel<2, true> : p.cpl == 3 ? rms_backward_kernel<3, true> : rms_backward_kernel<4, true>;
+    else kern = p.cpl == 1 ? rms_backward_kernel<1, false> : rms_backward_kernel<2, false>;
+    const cudaError_t e = launch_maybe_overlapped(kern, dim3(grid), dim3(p.threads), smem, stream, 1, a);
     if (e != cudaSuccess) return e;
-    column_sum_kernel<<<(C + 31) / 32, 256, 0, stream>>>(a.partial, grid, C, dgamma);
-    return cudaGetLastError();
+    return launch_maybe_overlapped(column_sum_kernel, dim3((C + 31) / 32), dim3(1024), 0, stream, 1,
+                                   (const float *)a.partial, grid, C, dgamma);
 }
 
 bool bad_pointer(const void *p, bool required)
