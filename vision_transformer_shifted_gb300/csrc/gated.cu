@@ -55,6 +55,11 @@ cudaError_t map_out(CUtensorMap *m, const void *p, int64_t rows, int cols)
 {
     return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 64, 32, 128);
 }
+// Hidden activations [rows, F]: boxes of 32 columns x 32 rows.
+cudaError_t map_hidden(CUtensorMap *m, const void *p, int64_t rows, int cols)
+{
+    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 32, 32, 64);
+}
 
 // One product of a launch_products call: D [rows, cols] = sum over K segments of
 // A B^T (+ bias + residual).
@@ -290,7 +295,7 @@ cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *s
         if ((e = map_k(&a.x, x, rows, h->C, 128, Q8)) != cudaSuccess) return e;
         if ((e = map_k(&a.wg, wg, h->F, h->C, 128, Q8)) != cudaSuccess) return e;
         if ((e = map_k(&a.wu, wu, h->F, h->C, 128, Q8)) != cudaSuccess) return e;
-        if ((e = map_out(&a.h, hidden, rows, h->F)) != cudaSuccess) return e;
+        if ((e = map_hidden(&a.h, hidden, rows, h->F)) != cudaSuccess) return e;
         a.bg = (const bf16 *)bg;
         a.bu = (const bf16 *)bu;
         a.sx = sx;
@@ -537,8 +542,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         bf16 *o[3] = {hidden, dg, du};
         CUtensorMap *m[3] = {&a.h, &a.dg, &a.du};
         for (int i = 0; i < 3; ++i)
-            if ((e = make_tensor_map(m[i], T_BF16, o[i], h->F, rows, (int64_t)h->F * 2, 32, 32, 64)) != cudaSuccess)
-                return e;
+            if ((e = map_hidden(m[i], o[i], rows, h->F)) != cudaSuccess) return e;
         a.bg = (const bf16 *)p->bg;
         a.bu = (const bf16 *)p->bu;
         a.rows = rows;

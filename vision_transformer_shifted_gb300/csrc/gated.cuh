@@ -10,27 +10,65 @@ namespace swin {
 
 enum { ACT_SILU = 0, ACT_GELU = 1 };
 
-// act(g), and with DERIV its derivative.
-template <int ACT, bool DERIV>
-__device__ __forceinline__ float activate(float g, float &deriv)
+// p = 1 / (1 + exp(-g)) for two values.
+__device__ __forceinline__ void sigmoid2(float g0, float g1, float &p0, float &p1)
 {
-    if (ACT == ACT_SILU) {
-        const float p = rcp_approx(1.f + ex2_approx(g * -1.4426950408889634f));   // 1 / (1 + exp(-g))
-        if (DERIV) deriv = p * fmaf(g, 1.f - p, 1.f);
-        return g * p;
+    float z0, z1;
+    g2_mul(z0, z1, g0, g1, -1.4426950408889634f, -1.4426950408889634f);
+    p0 = rcp_approx(1.f + ex2_approx(z0));
+    p1 = rcp_approx(1.f + ex2_approx(z1));
+}
+
+// act of two values, in place.
+template <int ACT>
+__device__ __forceinline__ void activate2(float &g0, float &g1)
+{
+    if (ACT == ACT_GELU) {
+        gelu_exact2(g0, g1);
+        return;
     }
-    if (!DERIV) return gelu_exact(g);
-    // (gelu_exact's erf; its exponential is the density's)
-    const float z = g * 0.70710678118654752f, b = fabsf(z);
-    const float t = rcp_approx(fmaf(0.3275911f, b, 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float e = ex2_approx(b * (b * -1.4426950408889634f));
-    const float phi = fmaf(0.5f, copysignf(fmaf(-q * t, e, 1.0f), z), 0.5f);
-    deriv = fmaf(g * 0.3989422804014327f, e, phi);
-    return g * phi;
+    float p0, p1;
+    sigmoid2(g0, g1, p0, p1);
+    g2_mul(g0, g1, g0, g1, p0, p1);
+}
+
+// act and its derivative of two values: a = g P(g), d = P + g P'(g).
+template <int ACT>
+__device__ __forceinline__ void activate_grad2(float g0, float g1, float &a0, float &a1, float &d0, float &d1)
+{
+    float p0, p1;
+    if (ACT == ACT_SILU) {
+        sigmoid2(g0, g1, p0, p1);
+        g2_mul(a0, a1, g0, g1, p0, p1);
+        // p (1 + g (1 - p)) = p + a - a p
+        float t0, t1;
+        g2_fma(t0, t1, a0, a1, -p0, -p1, a0, a1);
+        d0 = p0 + t0;
+        d1 = p1 + t1;
+        return;
+    }
+    // gelu_exact2's erf; its exponential exp(-g^2 / 2) is also the density's
+    float z0, z1, t0, t1, q0, q1, e0, e1;
+    g2_mul(z0, z1, g0, g1, 0.70710678118654752f, 0.70710678118654752f);
+    const float b0 = fabsf(z0), b1 = fabsf(z1);
+    g2_fma(t0, t1, b0, b1, 0.3275911f, 0.3275911f, 1.0f, 1.0f);
+    t0 = rcp_approx(t0);
+    t1 = rcp_approx(t1);
+    g2_fma(q0, q1, t0, t1, -1.061405429f, -1.061405429f, 1.453152027f, 1.453152027f);
+    g2_fma(q0, q1, q0, q1, t0, t1, -1.421413741f, -1.421413741f);
+    g2_fma(q0, q1, q0, q1, t0, t1, 0.284496736f, 0.284496736f);
+    g2_fma(q0, q1, q0, q1, t0, t1, -0.254829592f, -0.254829592f);
+    g2_mul(q0, q1, q0, q1, t0, t1);
+    g2_mul(e0, e1, b0, b1, -1.4426950408889634f, -1.4426950408889634f);
+    g2_mul(e0, e1, e0, e1, b0, b1);
+    e0 = ex2_approx(e0);
+    e1 = ex2_approx(e1);
+    g2_fma(q0, q1, q0, q1, e0, e1, 1.0f, 1.0f);   // erf(|z|)
+    g2_fma(p0, p1, copysignf(q0, z0), copysignf(q1, z1), 0.5f, 0.5f, 0.5f, 0.5f);
+    g2_mul(a0, a1, g0, g1, p0, p1);
+    float s0, s1;
+    g2_mul(s0, s1, g0, g1, 0.3989422804014327f, 0.3989422804014327f);
+    g2_fma(d0, d1, s0, s1, e0, e1, p0, p1);
 }
 
 // Eight values of a bf16 vector at column c (zero past n, and for NULL).
@@ -100,7 +138,7 @@ struct UpPolicy {
         int m, n;
     };
     static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
-    static constexpr int STAGES = 6, STAGE_BYTES = 32768, STAGING = 4096, SEGS = 1;
+    static constexpr int STAGES = 6, STAGE_BYTES = 32768, EPI = 16, STAGING = 2048, SEGS = 1;
     static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 256);
 
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
@@ -127,50 +165,50 @@ struct UpPolicy {
     }
     template <class Release>
     static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
-                                                    int half, int lane, uint32_t t_lane, uint8_t *stage,
+                                                    int part, int lane, uint32_t t_lane, uint8_t *stage,
                                                     Release &&release)
     {
-        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + half * 64;
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + half * 64;
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * 32;
+        float g[32], v[32];
+        tmem_ld32(acc, g);
+        tmem_ld32(acc + 128, v);
         float sx = 1.f;
         if (Q8) sx = row0 + lane < a.rows ? a.sx[row0 + lane] : 0.f;
         staging_free(lane);
+        tmem_wait_ld();
+        release();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float g[32], v[32];
-            tmem_ld32(acc + 32 * j, g);
-            tmem_ld32(acc + 128 + 32 * j, v);
-            tmem_wait_ld();
-            if (j == 1) release();
+        for (int q = 0; q < 4; ++q) {
+            const int c = col0 + 8 * q;
+            float *gq = g + 8 * q, *vq = v + 8 * q;
+            if (Q8) {
+                float s[8];
+                load8(a.sg, c, a.F, s);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = col0 + 32 * j + 8 * q;
-                if (Q8) {
-                    float s[8];
-                    load8(a.sg, c, a.F, s);
+                for (int e = 0; e < 8; ++e) gq[e] *= sx * s[e];
+                load8(a.su, c, a.F, s);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[8 * q + e] *= sx * s[e];
-                    load8(a.su, c, a.F, s);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] *= sx * s[e];
-                }
-                if (a.bg) {
-                    float b[8];
-                    load8(a.bg, c, a.F, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[8 * q + e] += b[e];
-                }
-                if (a.bu) {
-                    float b[8];
-                    load8(a.bu, c, a.F, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
-                }
-                float unused;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * q + e] *= activate<ACT, false>(g[8 * q + e], unused);
-                *reinterpret_cast<uint4 *>(stage + sw128_offset(lane, 4 * j + q)) = pack8f(v + 8 * q);
+                for (int e = 0; e < 8; ++e) vq[e] *= sx * s[e];
             }
+            if (a.bg) {
+                float b[8];
+                load8(a.bg, c, a.F, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) gq[e] += b[e];
+            }
+            if (a.bu) {
+                float b[8];
+                load8(a.bu, c, a.F, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) vq[e] += b[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                activate2<ACT>(gq[e], gq[e + 1]);
+                g2_mul(vq[e], vq[e + 1], vq[e], vq[e + 1], gq[e], gq[e + 1]);
+            }
+            *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(vq);
         }
         store_box(&a.h, col0, row0, row0 < a.rows && col0 < a.F, stage, lane);
     }
@@ -200,7 +238,7 @@ struct GemmPolicy {
     struct Unit {
         int p, m, n, slice, kb0, kbn;
     };
-    static constexpr int STAGE_BYTES = 16384 + TN * 64, STAGING = 4096, SEGS = 1;
+    static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 8, STAGING = 4096, SEGS = 1;
     static constexpr int STAGES = TN == 256 ? 6 : 7;
     static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, TN);
 
@@ -253,12 +291,12 @@ struct GemmPolicy {
     }
     template <class Release>
     static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
-                                                    int half, int lane, uint32_t t_lane, uint8_t *stage,
+                                                    int part, int lane, uint32_t t_lane, uint8_t *stage,
                                                     Release &&release)
     {
         const PairProblem &p = a.p[u.p];
-        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, colh = u.n * TN + half * (TN / 2);
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + half * (TN / 2);
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, colh = u.n * TN + part * (TN / 2);
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (TN / 2);
         if (p.slices > 1) {
 #pragma unroll 1
             for (int j = 0; j < TN / 64; ++j) {
@@ -334,7 +372,7 @@ struct GradPolicy {
     struct Unit {
         int m, n;
     };
-    static constexpr int STAGES = 5, STAGE_BYTES = 32768, STAGING = 6144, SEGS = 2;
+    static constexpr int STAGES = 4, STAGE_BYTES = 32768, EPI = 16, STAGING = 6144, SEGS = 2;
     static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 128);
     static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 256);
 
@@ -373,58 +411,59 @@ struct GradPolicy {
     }
     template <class Release>
     static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
-                                                    int half, int lane, uint32_t t_lane, uint8_t *stage,
+                                                    int part, int lane, uint32_t t_lane, uint8_t *stage,
                                                     Release &&release)
     {
-        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + half * 64;
-        const uint32_t gu = t_lane + half * 64, dh = t_lane + slot_col(slot(0, n)) + half * 64;
-#pragma unroll 1
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
+        const uint32_t gu = t_lane + part * 32, dh = t_lane + slot_col(slot(0, n)) + part * 32;
+        staging_free(lane);
+#pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float g[32], v[32], d[32];
-            tmem_ld32(gu + 32 * j, g);
-            tmem_ld32(gu + 128 + 32 * j, v);
-            tmem_ld32(dh + 32 * j, d);
+            float g[16], v[16], d[16];
+            tmem_ld16(gu + 16 * j, g);
+            tmem_ld16(gu + 128 + 16 * j, v);
+            tmem_ld16(dh + 16 * j, d);
             tmem_wait_ld();
             if (j == 1) release();
-            staging_free(lane);
-            const int c0 = col0 + 32 * j;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
+                const int c = col0 + 16 * j + 8 * q;
+                float *gq = g + 8 * q, *vq = v + 8 * q, *dq = d + 8 * q;
                 if (a.bg) {
                     float b[8];
-                    load8(a.bg, c0 + 8 * q, a.F, b);
+                    load8(a.bg, c, a.F, b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[8 * q + e] += b[e];
+                    for (int e = 0; e < 8; ++e) gq[e] += b[e];
                 }
                 if (a.bu) {
                     float b[8];
-                    load8(a.bu, c0 + 8 * q, a.F, b);
+                    load8(a.bu, c, a.F, b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+                    for (int e = 0; e < 8; ++e) vq[e] += b[e];
                 }
-                float hh[8], dg[8], du[8];
+                float hh[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float deriv;
-                    const float act = activate<ACT, true>(g[8 * q + e], deriv);
-                    const float x = v[8 * q + e], y = d[8 * q + e];
-                    hh[e] = act * x;
-                    dg[e] = y * x * deriv;
-                    du[e] = y * act;
+                for (int e = 0; e < 8; e += 2) {
+                    float a0, a1, t0, t1, s0, s1;
+                    activate_grad2<ACT>(gq[e], gq[e + 1], a0, a1, t0, t1);
+                    g2_mul(hh[e], hh[e + 1], a0, a1, vq[e], vq[e + 1]);
+                    g2_mul(s0, s1, dq[e], dq[e + 1], vq[e], vq[e + 1]);
+                    g2_mul(gq[e], gq[e + 1], s0, s1, t0, t1);               // dg = dh u act'(g)
+                    g2_mul(dq[e], dq[e + 1], dq[e], dq[e + 1], a0, a1);     // du = dh act(g)
                 }
-                const uint32_t off = sw64_offset(lane, q);
+                const uint32_t off = sw64_offset(lane, 2 * j + q);
                 *reinterpret_cast<uint4 *>(stage + off) = pack8f(hh);
-                *reinterpret_cast<uint4 *>(stage + 2048 + off) = pack8f(dg);
-                *reinterpret_cast<uint4 *>(stage + 4096 + off) = pack8f(du);
+                *reinterpret_cast<uint4 *>(stage + 2048 + off) = pack8f(gq);
+                *reinterpret_cast<uint4 *>(stage + 4096 + off) = pack8f(dq);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && row0 < a.rows && c0 < a.F) {
-                tma_store_2d(&a.h, c0, row0, smem_u32(stage));
-                tma_store_2d(&a.dg, c0, row0, smem_u32(stage + 2048));
-                tma_store_2d(&a.du, c0, row0, smem_u32(stage + 4096));
-                bulk_commit();
-            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < a.rows && col0 < a.F) {
+            tma_store_2d(&a.h, col0, row0, smem_u32(stage));
+            tma_store_2d(&a.dg, col0, row0, smem_u32(stage + 2048));
+            tma_store_2d(&a.du, col0, row0, smem_u32(stage + 4096));
+            bulk_commit();
         }
     }
 };

@@ -2,22 +2,23 @@
 // clusters of two CTAs, each pair computing 256-row tiles with
 // tcgen05.mma.cta_group::2 (each CTA holds half of the rows of A, half of the
 // rows of B and the accumulators of its 128 rows), operands staged by TMA in a
-// ring of shared-memory stages, accumulators handed to eight epilogue warps.
+// ring of shared-memory stages, accumulators handed to 8 or 16 epilogue warps.
 //
 // Why pairs: a 256 x 256 x 64 step reads 32 KB of shared memory a CTA for 2 x
 // 256 x 256 x 64 FLOPs a pair, half of what two independent 128 x 256 tiles
 // read, which is what lets the tensor cores run at their rate.
 //
-// Roles (320 threads): warp 0 loads (one thread in each CTA, its own halves,
-// signalling the leader's barrier), warp 1 of the leader issues the MMAs, warps
-// 2..9 of both CTAs drain (warp w owns TMEM lane quarter w % 4 and one half of
-// the columns).  Every wait is bounded; on expiry the error word is set, the
+// Roles: warp 0 loads (one thread in each CTA, its own halves, signalling the
+// leader's barrier), warp 1 of the leader issues the MMAs, the other warps of
+// both CTAs drain (warp w owns TMEM lane quarter w % 4 and a share of the
+// columns).  Every wait is bounded; on expiry the error word is set, the
 // roles leave, and the CTAs meet at the closing cluster barrier.
 //
 // A policy P describes the kernel:
 //   Args                    kernel parameters (units: work items; st: DeviceStatus)
 //   Unit / decode(a, u)     one work item (a tile, or a K slice of one)
 //   STAGES, STAGE_BYTES     the ring
+//   EPI                     epilogue warps (8, or 16 where arithmetic binds)
 //   STAGING                 bytes of store staging per epilogue warp
 //   SEGS                    accumulation segments of a unit (each a K loop
 //                           into one slot of TMEM columns)
@@ -33,8 +34,6 @@
 
 namespace swin {
 
-constexpr int PAIR_EPI = 8;
-constexpr int PAIR_THREADS = 64 + 32 * PAIR_EPI;
 constexpr int PAIR_SLOTS = 3;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -159,7 +158,7 @@ template <class P>
 struct PairSmem {
     static constexpr int BARS = 2 * P::STAGES + 2 * PAIR_SLOTS;
     static constexpr size_t ring = (size_t)P::STAGES * P::STAGE_BYTES;
-    static constexpr size_t bytes = 1024 + ring + PAIR_EPI * P::STAGING + BARS * 8 + 16;
+    static constexpr size_t bytes = 1024 + ring + P::EPI * P::STAGING + BARS * 8 + 16;
     static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
@@ -174,14 +173,14 @@ __device__ __forceinline__ void tile_order(int t, int mt, int nt, int &m, int &n
 }
 
 template <class P>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * P::EPI, 1)
 pair_kernel(const __grid_constant__ typename P::Args a)
 {
     using L = PairSmem<P>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_align(smem_raw, 1024);
     uint8_t *staging = smem + L::ring;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + PAIR_EPI * P::STAGING);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + P::EPI * P::STAGING);
     const uint32_t full = smem_u32(bars), empty = full + 8 * P::STAGES, tfull = empty + 8 * P::STAGES,
                    tempty = tfull + 8 * PAIR_SLOTS;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + L::BARS);
@@ -196,7 +195,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         }
         for (int s = 0; s < PAIR_SLOTS; ++s) {
             mbar_init(tfull + 8 * s, 1);
-            mbar_init(tempty + 8 * s, 2 * PAIR_EPI);   // (the leader's: the epilogue warps of both CTAs)
+            mbar_init(tempty + 8 * s, 2 * P::EPI);   // (the leader's: the epilogue warps of both CTAs)
         }
         mbar_init_fence();
     }
@@ -293,7 +292,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
             }
         }
     } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int quad = warp & 3, part = (warp - 2) >> 2;   // (part: of the columns)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         uint8_t *stage = staging + (warp - 2) * P::STAGING;
         int n = 0;
@@ -312,7 +311,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
                     for (int seg = 0; seg < P::SEGS; ++seg)
                         mbar_arrive_cluster(map_rank(tempty + 8 * P::slot(seg, n), 0));
             };
-            P::epilogue(a, un, n, rank, quad, half, lane, t_lane, stage, release);
+            P::epilogue(a, un, n, rank, quad, part, lane, t_lane, stage, release);
         }
         // the staged stores have read shared memory, and are complete
         if (lane == 0) bulk_wait_all();
@@ -341,7 +340,7 @@ cudaError_t launch_pair(const typename P::Args &a, cudaStream_t stream)
     }
     const int pairs = sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(a.units < pairs ? a.units : pairs);
-    return launch_maybe_overlapped(pair_kernel<P>, dim3(grid), dim3(PAIR_THREADS), smem, stream, 1, a);
+    return launch_maybe_overlapped(pair_kernel<P>, dim3(grid), dim3(64 + 32 * P::EPI), smem, stream, 1, a);
 }
 
 } // namespace swin
