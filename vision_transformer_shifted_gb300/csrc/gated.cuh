@@ -158,9 +158,9 @@ struct UpPolicy {
         tma_load_2d_pair(dst, &a.x, kb * ELEMS, u.m * 256 + (int)rank * 128, bar);
         tma_load_2d_pair(dst + 16384, rank ? &a.wu : &a.wg, kb * ELEMS, u.n * 128, bar);
     }
-    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int, int kb, uint32_t src, uint32_t d)
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int, int kb, uint32_t src16, uint32_t d)
     {
-        mma_kblock<Q8 ? MMA_E4M3 : MMA_BF16, false, false>(d, src, src + 16384, IDESC, kblock_steps(a.C, kb, ELEMS),
+        mma_kblock<Q8 ? MMA_E4M3 : MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC, kblock_steps(a.C, kb, ELEMS),
                                                            kb == 0);
     }
     template <class Release>
@@ -237,6 +237,7 @@ struct GemmPolicy {
     };
     struct Unit {
         int p, m, n, slice, kb0, kbn;
+        int k0, kb_first;   // the first segment's K, and its blocks
     };
     static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 8, STAGING = 4096, SEGS = 1;
     static constexpr int STAGES = TN == 256 ? 6 : 7;
@@ -256,6 +257,8 @@ struct GemmPolicy {
         const int64_t all = p.kb[0] + p.kb[1];
         r.kb0 = (int)(all * r.slice / p.slices);
         r.kbn = (int)(all * (r.slice + 1) / p.slices) - r.kb0;
+        r.k0 = p.k[0];
+        r.kb_first = p.kb[0];
         return r;
     }
     static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
@@ -276,18 +279,17 @@ struct GemmPolicy {
     {
         const PairProblem &p = a.p[u.p];
         int kb = u.kb0 + i;
-        const int seg = kb >= p.kb[0];
-        if (seg) kb -= p.kb[0];
+        const int seg = kb >= u.kb_first;
+        if (seg) kb -= u.kb_first;
         load_operand<A_MN, 128>(dst, &p.a[seg], u.m * 256 + (int)rank * 128, kb * 64, bar);
         load_operand<B_MN, TN / 2>(dst + 16384, &p.b[seg], u.n * TN + (int)rank * (TN / 2), kb * 64, bar);
     }
-    static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int, int i, uint32_t src, uint32_t d)
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int, int i, uint32_t src16, uint32_t d)
     {
-        const PairProblem &p = a.p[u.p];
+        // (two segments are of one K: dg and du)
         int kb = u.kb0 + i;
-        const int seg = kb >= p.kb[0];
-        if (seg) kb -= p.kb[0];
-        mma_kblock<MMA_BF16, A_MN, B_MN>(d, src, src + 16384, IDESC, kblock_steps(p.k[seg], kb, 64), i == 0);
+        if (kb >= u.kb_first) kb -= u.kb_first;
+        mma_kblock<MMA_BF16, A_MN, B_MN>(d, src16, src16 + 1024, IDESC, kblock_steps(u.k0, kb, 64), i == 0);
     }
     template <class Release>
     static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
@@ -403,11 +405,11 @@ struct GradPolicy {
             tma_load_2d_pair(dst + 16384, rank ? &a.wu : &a.wg, kb * 64, u.n * 128, bar);
         }
     }
-    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int seg, int kb, uint32_t src, uint32_t d)
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int seg, int kb, uint32_t src16, uint32_t d)
     {
         const int steps = kblock_steps(a.C, kb, 64);
-        if (seg == 0) mma_kblock<MMA_BF16, false, true>(d, src, src + 16384, IDESC_H, steps, kb == 0);
-        else mma_kblock<MMA_BF16, false, false>(d, src, src + 16384, IDESC_GU, steps, kb == 0);
+        if (seg == 0) mma_kblock<MMA_BF16, false, true>(d, src16, src16 + 1024, IDESC_H, steps, kb == 0);
+        else mma_kblock<MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC_GU, steps, kb == 0);
     }
     template <class Release>
     static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,

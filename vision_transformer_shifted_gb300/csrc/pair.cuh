@@ -62,6 +62,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 {
     uint32_t ok;
     uint64_t t0 = 0;
+#pragma unroll 1
     while (true) {
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -132,20 +133,34 @@ __host__ __device__ constexpr uint32_t idesc_pair(int kind, bool a_mn, bool b_mn
 // Operand tiles, 128-byte swizzle.  K-major: rows of 128 bytes of K, 8-row
 // atoms stacked densely; a step of 32 bytes of K moves the start by 32.
 // MN-major: boxes of 64 MN elements (128 bytes) x 64 k, boxes 8 KB apart; a step
-// of 16 k moves the start by 16 rows.
+// of 16 k moves the start by 16 rows.  Descriptors as two words: the upper is a
+// constant, the lower a constant plus the address in 16-byte units, so that the
+// issuing thread spends an addition per operand and MMA.
 template <bool MN>
-__device__ __forceinline__ uint64_t desc_pair(uint32_t addr, int step)
-{
-    return MN ? smem_desc(addr + 2048u * step, 8192, 1024, SWZ_128B) : desc_kmajor_sw128(addr + 32u * step);
-}
+struct PairOperand {
+    static constexpr uint32_t STEP = MN ? 128 : 2;
+    static constexpr uint32_t LO = (MN ? 8192u >> 4 : 1u) << 16;
+    static constexpr uint32_t HI = (1024u >> 4) | 1u << 14 | (uint32_t)SWZ_128B << 29;
+    static __device__ __forceinline__ uint64_t desc(uint32_t addr16, int k)
+    {
+        return (uint64_t)HI << 32 | (uint64_t)((addr16 | LO) + STEP * k);
+    }
+};
+// The MMAs of one K block: operands at a16, b16 (16-byte units), `steps` of its
+// four steps (fewer in the last block of a K that ends inside it).
 template <int KIND, bool A_MN, bool B_MN>
-__device__ __forceinline__ void mma_kblock(uint32_t d, uint32_t a_addr, uint32_t b_addr, uint32_t idesc, int steps,
-                                           bool first)
+__device__ __forceinline__ void mma_kblock(uint32_t d, uint32_t a16, uint32_t b16, uint32_t idesc, int steps, bool first)
 {
+    mma_pair<KIND>(d, PairOperand<A_MN>::desc(a16, 0), PairOperand<B_MN>::desc(b16, 0), idesc, !first);
+    if (steps == 4) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < steps)
-            mma_pair<KIND>(d, desc_pair<A_MN>(a_addr, k), desc_pair<B_MN>(b_addr, k), idesc, !(first && k == 0));
+        for (int k = 1; k < 4; ++k)
+            mma_pair<KIND>(d, PairOperand<A_MN>::desc(a16, k), PairOperand<B_MN>::desc(b16, k), idesc, 1);
+    } else {
+#pragma unroll 1
+        for (int k = 1; k < steps; ++k)
+            mma_pair<KIND>(d, PairOperand<A_MN>::desc(a16, k), PairOperand<B_MN>::desc(b16, k), idesc, 1);
+    }
 }
 // MMA steps of K block kb of a K of `k` elements (block: 128 bytes, four steps).
 __device__ __forceinline__ int kblock_steps(int k, int kb, int elems)
@@ -261,7 +276,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            const uint32_t ring = smem_u32(smem);
+            const uint32_t ring16 = smem_u32(smem) >> 4;
             int s = 0, n = 0;
             uint32_t ph = 0;
             for (int u = first; u < a.units && !failed; u += step, ++n) {
@@ -280,7 +295,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
                             break;
                         }
                         tc_fence_after();
-                        P::mma(a, un, seg, kb, ring + s * P::STAGE_BYTES, d);
+                        P::mma(a, un, seg, kb, ring16 + s * (P::STAGE_BYTES >> 4), d);
                         mma_commit_pair(empty + 8 * s);
                         if (++s == P::STAGES) {
                             s = 0;
