@@ -57,25 +57,42 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Bounded wait (as mbar_wait) that also acquires what the other CTA released.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+// Bounded waits as mbar_wait, for waits that are rarely over before they begin:
+// the suspending form at once, the clock (slow to read) only if it ran out.
+// CLUSTER: also acquires what the other CTA's threads released.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
     uint32_t ok;
     uint64_t t0 = 0;
 #pragma unroll 1
     while (true) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.b32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(1000000u)
-            : "memory");
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.b32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity), "r"(1000000u)
+                : "memory");
+        else
+            ok = mbar_try_wait_hint(bar, parity, 1000000u);
         if (ok) return true;
         const uint64_t t = global_timer_ns();
         if (!t0) t0 = t;
         else if (t - t0 > limit_ns) return false;
     }
+}
+// True in one lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
 }
 // 2-D TMA load into this CTA's shared memory, completing on a barrier that may
 // be the peer's (cluster address).
@@ -199,7 +216,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
     const uint32_t full = smem_u32(bars), empty = full + 8 * P::STAGES, tfull = empty + 8 * P::STAGES,
                    tempty = tfull + 8 * PAIR_SLOTS;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + L::BARS);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (from one lane: the compiler then knows it for the same in all of them)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -226,83 +244,97 @@ pair_kernel(const __grid_constant__ typename P::Args a)
     griddep_launch_dependents();
     griddep_wait();
 
+    // The two issuing warps run their loops as whole warps and let one lane
+    // issue: addresses and descriptors then stay in uniform registers.  (With
+    // the loops inside a one-lane branch, a K block cost its issuing thread
+    // some 500 cycles, more than the MMAs of a 256 x 128 tile take.)
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t ring = smem_u32(smem), lead_full = map_rank(full, 0);
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
-            for (int u = first; u < a.units && !failed; u += step) {
-                const typename P::Unit un = P::decode(a, u);
-                for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
-                    const int kb_n = P::kblocks(a, un, seg);
-                    for (int kb = 0; kb < kb_n; ++kb) {
-                        if (!mbar_wait_cluster(empty + 8 * s, ph ^ 1u, a.st.wait_ns)) {
-                            failed = true;
-                            break;
-                        }
-                        if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, P::tx(a, un, seg));
+        const uint32_t ring = smem_u32(smem), lead_full = map_rank(full, 0);
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+#pragma unroll 1
+        for (int u = first; u < a.units && !failed; u += step) {
+            const typename P::Unit un = P::decode(a, u);
+#pragma unroll 1
+            for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
+                const int kb_n = P::kblocks(a, un, seg);
+                const uint32_t tx = P::tx(a, un, seg);
+#pragma unroll 1
+                for (int kb = 0; kb < kb_n; ++kb) {
+                    if (!__all_sync(0xffffffffu, pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns))) {
+                        failed = true;
+                        break;
+                    }
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, tx);
                         P::load(a, un, seg, kb, rank, ring + s * P::STAGE_BYTES, lead_full + 8 * s);
-                        ++issued;
-                        if (++s == P::STAGES) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
+                    }
+                    ++issued;
+                    if (++s == P::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
                     }
                 }
-            }
-            // every stage given back: no commit is on its way to this CTA's
-            // barriers when it ends
-            for (int k = 0; k < P::STAGES && k < issued && !failed; ++k) {
-                failed = !mbar_wait_cluster(empty + 8 * s, ph ^ 1u, a.st.wait_ns);
-                if (++s == P::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            }
-            if (failed) {
-                // copies in flight land before this CTA's memory is given back:
-                // the leader's barriers say so for both CTAs
-                if (rank == 0)
-                    for (int k = 0; k < P::STAGES && k < issued; ++k) {
-                        if (--s < 0) {
-                            s = P::STAGES - 1;
-                            ph ^= 1u;
-                        }
-                        mbar_wait_cluster(full + 8 * s, ph, a.st.wait_ns);
-                    }
-                const uint64_t t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
             }
         }
+        // every stage given back: no commit is on its way to this CTA's
+        // barriers when it ends
+        for (int k = 0; k < P::STAGES && k < issued && !failed; ++k) {
+            failed = !__all_sync(0xffffffffu, pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns));
+            if (++s == P::STAGES) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (failed) {
+            // copies in flight land before this CTA's memory is given back:
+            // the leader's barriers say so for both CTAs
+            if (rank == 0)
+                for (int k = 0; k < P::STAGES && k < issued; ++k) {
+                    if (--s < 0) {
+                        s = P::STAGES - 1;
+                        ph ^= 1u;
+                    }
+                    pair_wait(full + 8 * s, ph, a.st.wait_ns);
+                }
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
+        }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t ring16 = smem_u32(smem) >> 4;
             int s = 0, n = 0;
             uint32_t ph = 0;
+#pragma unroll 1
             for (int u = first; u < a.units && !failed; u += step, ++n) {
                 const typename P::Unit un = P::decode(a, u);
+#pragma unroll 1
                 for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
                     const int slot = P::slot(seg, n), kb_n = P::kblocks(a, un, seg);
-                    if (!mbar_wait_cluster(tempty + 8 * slot, (P::slot_use(seg, n) & 1) ^ 1, a.st.wait_ns)) {
+                    if (!__all_sync(0xffffffffu, pair_wait<true>(tempty + 8 * slot, (P::slot_use(seg, n) & 1) ^ 1,
+                                                                 a.st.wait_ns))) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + P::slot_col(slot);
+#pragma unroll 1
                     for (int kb = 0; kb < kb_n; ++kb) {
-                        if (!mbar_wait_cluster(full + 8 * s, ph, a.st.wait_ns)) {
+                        if (!__all_sync(0xffffffffu, pair_wait(full + 8 * s, ph, a.st.wait_ns))) {
                             failed = true;
                             break;
                         }
                         tc_fence_after();
-                        P::mma(a, un, seg, kb, ring16 + s * (P::STAGE_BYTES >> 4), d);
-                        mma_commit_pair(empty + 8 * s);
+                        if (elect_one()) {
+                            P::mma(a, un, seg, kb, ring16 + s * (P::STAGE_BYTES >> 4), d);
+                            mma_commit_pair(empty + 8 * s);
+                            if (kb == kb_n - 1) mma_commit_pair(tfull + 8 * slot);
+                        }
                         if (++s == P::STAGES) {
                             s = 0;
                             ph ^= 1u;
                         }
                     }
-                    if (!failed) mma_commit_pair(tfull + 8 * slot);
                 }
             }
         }
@@ -315,8 +347,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
             const typename P::Unit un = P::decode(a, u);
             // (warp-uniform outcome: the TMEM loads below are warp-collective)
             for (int seg = 0; seg < P::SEGS && !failed; ++seg)
-                failed = !__all_sync(0xffffffffu, mbar_wait_cluster(tfull + 8 * P::slot(seg, n),
-                                                                    P::slot_use(seg, n) & 1, a.st.wait_ns));
+                failed = !__all_sync(0xffffffffu, pair_wait(tfull + 8 * P::slot(seg, n), P::slot_use(seg, n) & 1,
+                                                            a.st.wait_ns));
             if (failed) break;
             tc_fence_after();
             auto release = [&]() {
