@@ -72,91 +72,92 @@ struct Product {
     int cols;
 };
 
-// out = the sum of `slices` fp32 partial tiles [rows, cols] (+ bias + residual),
-// slice by slice.
-struct ReduceItem {
+// The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
+// of K (+ bias + residual).  Block (t, y): cut tile t, every gridDim.y-th 2048
+// values.
+struct JoinArgs {
     const float *part;
-    const bf16 *bias, *residual;
-    bf16 *out;
-    int64_t rows;
-    int cols, slices;
+    PairSplit split;
+    int tn;
+    struct {
+        const bf16 *bias, *residual;
+        bf16 *out;
+        int rows, cols, mt, nt, first;
+    } p[3];
 };
-struct ReduceArgs {
-    ReduceItem it[3];
-};
-__global__ void __launch_bounds__(256) reduce_slices_kernel(ReduceArgs a)
+__global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__ JoinArgs a)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const ReduceItem &t = a.it[blockIdx.y];
-    const int64_t n = t.rows * t.cols;
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int s = 0; s < t.slices; ++s) {
-            const float4 x = *reinterpret_cast<const float4 *>(t.part + s * n + i);
-            const float4 y = *reinterpret_cast<const float4 *>(t.part + s * n + i + 4);
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-        }
-        float b[8];
-        load8(t.bias, (int)(i % t.cols), t.cols, b);
+    const PairSplit &s = a.split;
+    const int c = blockIdx.x, t = s.full * s.np + c;
+    const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
+    if (p0 == p1) return;   // (one pair had the whole tile and wrote it)
+    const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
+    int m, n;
+    tile_order(t - a.p[i].first, a.p[i].mt, a.p[i].nt, m, n);
+    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / 8;
+    const int64_t size = 256 * a.tn;
+    for (int e = blockIdx.y * 256 + threadIdx.x; e < 256 * per; e += gridDim.y * 256) {
+        const int row = m * 256 + e / per, col = n * a.tn + e % per * 8;
+        if (row >= rows || col >= cols) continue;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
+        for (int p = p0; p <= p1; ++p) {
+            load8(a.part + s.slot(p, c) * size + (int64_t)e * 8, 0, 8, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += b[e];
-        if (t.residual) {
-            load8(t.residual + i, 0, 8, b);
+            for (int k = 0; k < 8; ++k) v[k] += w[k];
+        }
+        load8(a.p[i].bias, col, cols, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += b[e];
+        for (int k = 0; k < 8; ++k) v[k] += w[k];
+        const int64_t at = (int64_t)row * cols + col;
+        if (a.p[i].residual) {
+            load8(a.p[i].residual + at, 0, 8, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] += w[k];
         }
-        *reinterpret_cast<uint4 *>(t.out + i) = pack8f(v);
+        *reinterpret_cast<uint4 *>(a.p[i].out + at) = pack8f(v);
     }
-}
-
-// K slices of a product of `tiles` tiles and kb K blocks: as many as make the
-// most of the pairs (waves x blocks a wave, a slice costing about four more
-// blocks for its partial tile), at most 32 and at least four blocks each.
-int pick_slices(int64_t tiles, int kb)
-{
-    const int pairs = sm_count() / 2;
-    int best = 1;
-    int64_t cost = (int64_t)ceil_div(tiles, pairs) * kb;
-    for (int s = 2; s <= 32 && kb / s >= 4; ++s) {
-        const int64_t c = (int64_t)ceil_div(tiles * s, pairs) * (ceil_div(kb, s) + 4) + 4;
-        if (c < cost) {
-            cost = c;
-            best = s;
-        }
-    }
-    return best;
 }
 
 struct ProductsPlan {
-    int n, slices, units;
+    int n;
     bool wide;            // 256-column tiles (else 128)
-    size_t part_bytes;    // of the partial tiles of all products
+    PairSplit split;
+    size_t part_bytes;    // of the partial tiles
 };
 
-// Tiles of 256 x 256 where every product has more than 128 columns and there
-// are enough of them for the pairs, else 256 x 128.
+// Tiles of 256 x 256 where every product has more than 128 columns, else 256 x
+// 128.  The last round is cut along K where that saves more K blocks than
+// joining the partial tiles costs (a launch and their traffic, about 5 us: 16
+// blocks of a 256 x 256 tile, 24 of a narrow one); few blocks in all go to as
+// many pairs as leave each at least four.
 ProductsPlan plan_products(const Product *p, int n)
 {
     ProductsPlan pl{};
     pl.n = n;
-    const int pairs = sm_count() / 2;
-    int64_t wide_tiles = 0;
     pl.wide = true;
-    for (int i = 0; i < n; ++i) {
-        wide_tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, 256);
+    for (int i = 0; i < n; ++i)
         if (p[i].cols <= 128) pl.wide = false;
-    }
-    const int kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
-    if (wide_tiles < pairs && pick_slices(wide_tiles, kb) == 1) pl.wide = false;
     const int tn = pl.wide ? 256 : 128;
     int64_t tiles = 0;
     for (int i = 0; i < n; ++i) tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, tn);
-    pl.slices = pick_slices(tiles, kb);
-    pl.units = (int)(tiles * pl.slices);
-    if (pl.slices > 1)
-        for (int i = 0; i < n; ++i) pl.part_bytes += (size_t)pl.slices * p[i].rows * p[i].cols * sizeof(float);
+    PairSplit &s = pl.split;
+    s.tiles = (int)tiles;
+    s.kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
+    const int pairs = sm_count() / 2;
+    s.np = (int)(tiles < pairs ? tiles : pairs);
+    const int full = (int)(tiles / pairs), rest = (int)(tiles - (int64_t)full * pairs);
+    const int64_t blocks = (int64_t)rest * s.kb;
+    const int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
+    if (rest && s.kb - ceil_div(blocks, np) > (pl.wide ? 16 : 24)) {
+        s.np = (int)np;
+        s.full = full;
+        s.cut = rest;
+        s.q = (uint32_t)(blocks / np);
+        s.r = (uint32_t)(blocks % np);
+        pl.part_bytes = (size_t)np * 2 * 256 * tn * sizeof(float);
+    }
     return pl;
 }
 
@@ -166,21 +167,23 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
 {
     typename GemmPolicy<TN, A_MN, B_MN>::Args a;
     memset(&a, 0, sizeof(a));
-    ReduceArgs r{};
-    int64_t first = 0, most = 0;
+    JoinArgs r{};
+    cudaError_t e;
+    int first = 0;
     for (int i = 0; i < 3; ++i) {
         PairProblem &q = a.p[i];
-        q.first = INT_MAX;
+        q.first = r.p[i].first = INT_MAX;
         if (i >= pl.n) continue;
         const Product &p = ps[i];
         q.rows = (int)p.rows;
         q.cols = p.cols;
         q.mt = ceil_div(p.rows, 256);
         q.nt = ceil_div(p.cols, TN);
-        q.slices = pl.slices;
-        q.first = (int)first;
-        first += (int64_t)q.mt * q.nt * pl.slices;
-        cudaError_t e;
+        q.first = first;
+        first += q.mt * q.nt;
+        q.bias = p.bias;
+        q.residual = p.residual;
+        r.p[i] = {p.bias, p.residual, p.d, q.rows, q.cols, q.mt, q.nt, q.first};
         for (int s = 0; s < 2; ++s) {
             q.k[s] = p.k[s];
             q.kb[s] = p.k[s] ? ceil_div(p.k[s], 64) : 0;
@@ -190,28 +193,22 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
             e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols) : map_k(&q.b[s], p.b[s], p.cols, p.k[s], TN / 2);
             if (e != cudaSuccess) return e;
         }
-        if (pl.slices > 1) {
-            e = make_tensor_map(&q.part, T_F32, part, p.cols, p.rows, (int64_t)p.cols * 4, 32, 32, 128, pl.slices);
-            r.it[i] = {part, p.bias, p.residual, p.d, p.rows, p.cols, pl.slices};
-            part += (size_t)pl.slices * p.rows * p.cols;
-            if (p.rows * p.cols > most) most = p.rows * p.cols;
-        } else {
-            e = map_out(&q.d, p.d, p.rows, p.cols);
-            q.bias = p.bias;
-            q.residual = p.residual;
-        }
+        if ((e = map_out(&q.d, p.d, p.rows, p.cols)) != cudaSuccess) return e;
+    }
+    a.split = r.split = pl.split;
+    a.np = pl.split.np;
+    a.st = st;
+    if (pl.split.cut) {
+        e = make_tensor_map(&a.part, T_F32, part, TN, (int64_t)a.np * 2 * 256, TN * 4, 32, 32, 128);
         if (e != cudaSuccess) return e;
     }
-    a.units = pl.units;
-    a.st = st;
     ++*launches;
-    cudaError_t e = launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
-    if (e != cudaSuccess || pl.slices == 1) return e;
-    int64_t blocks = ceil_div(most, 2048);
-    if (blocks > 8 * sm_count()) blocks = 8 * sm_count();
+    e = launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
+    if (e != cudaSuccess || !pl.split.cut) return e;
+    r.part = part;
+    r.tn = TN;
     ++*launches;
-    return launch_maybe_overlapped(reduce_slices_kernel, dim3((unsigned)blocks, (unsigned)pl.n), dim3(256), 0, stream, 1,
-                                   r);
+    return launch_maybe_overlapped(join_tiles_kernel, dim3((unsigned)pl.split.cut, TN / 16), dim3(256), 0, stream, 1, r);
 }
 
 template <bool A_MN, bool B_MN>
@@ -307,7 +304,7 @@ cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *s
         a.mt = ceil_div(rows, 256);
         a.nt = ceil_div(h->F, 128);
         a.kb = ceil_div(h->C, P::ELEMS);
-        a.units = a.mt * a.nt;
+        a.np = a.mt * a.nt < sm_count() / 2 ? a.mt * a.nt : sm_count() / 2;
         a.st = st;
         return launch_pair<P>(a, stream);
     };
@@ -551,7 +548,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         a.mt = ceil_div(rows, 256);
         a.nt = ceil_div(h->F, 128);
         a.kb = ceil_div(h->C, 64);
-        a.units = a.mt * a.nt;
+        a.np = a.mt * a.nt < sm_count() / 2 ? a.mt * a.nt : sm_count() / 2;
         a.st = st;
         return launch_pair<P>(a, s);
     };

@@ -131,7 +131,7 @@ struct UpPolicy {
         CUtensorMap x, wg, wu, h;
         const bf16 *bg, *bu;
         const float *sx, *sg, *su;   // Q8
-        int rows, C, F, mt, nt, kb, units;
+        int rows, C, F, mt, nt, kb, np;
         DeviceStatus st;
     };
     struct Unit {
@@ -144,10 +144,11 @@ struct UpPolicy {
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
     static __device__ __forceinline__ int slot_use(int, int n) { return n >> 1; }
     static __device__ __forceinline__ int slot_col(int s) { return s * 256; }
-    static __device__ __forceinline__ Unit decode(const Args &a, int u)
+    static __device__ __forceinline__ int count(const Args &a, int pair) { return deal_count(a.mt * a.nt, a.np, pair); }
+    static __device__ __forceinline__ Unit decode(const Args &a, int pair, int n)
     {
         Unit r;
-        tile_order(u, a.mt, a.nt, r.m, r.n);
+        tile_order(pair + n * a.np, a.mt, a.nt, r.m, r.n);
         return r;
     }
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
@@ -218,25 +219,52 @@ struct UpPolicy {
 //
 // D = A B^T over up to two K segments (dx = dg Wg + du Wu), A and B each K-major
 // or MN-major as stored: no operand is ever transposed in memory.  Up to three
-// problems run as one launch (the three weight gradients), each cut into
-// `slices` of its K blocks when its tiles would not fill the SMs: the slices
-// write fp32 partial tiles that a second kernel adds in a fixed order.
+// problems run as one launch (the three weight gradients).
+//
+// Tiles are dealt to the pairs in rounds; a last round that would leave pairs
+// idle is instead cut along K: its tiles' K blocks, laid end to end, are split
+// evenly over the pairs, and a pair's ranges that hold only a part of a tile go
+// to fp32 partial tiles that a second kernel adds in the order of K.  (4096 x
+// 2048 x 5632's dx: 128 tiles on 76 pairs, 2 rounds of 176 blocks; cut, 1.68.)
 struct PairProblem {
-    CUtensorMap a[2], b[2], d, part;
-    const bf16 *bias, *residual;   // [cols] / [rows, cols] or null (not with slices)
+    CUtensorMap a[2], b[2], d;
+    const bf16 *bias, *residual;   // [cols] / [rows, cols] or null
     int rows, cols, k[2], kb[2];
-    int mt, nt, slices, first;     // first: this problem's first unit
+    int mt, nt, first;             // first: this problem's first tile
+};
+// The division of `tiles` tiles of kb K blocks each over np pairs.
+struct PairSplit {
+    int tiles, kb, np;
+    int full;        // rounds of whole tiles
+    int cut;         // tiles cut along K (0: the last round is whole tiles too)
+    uint32_t q, r;   // blocks a pair of the cut tiles: q, the first r pairs q + 1
+    __device__ __forceinline__ uint32_t begin(int pair) const
+    {
+        return q * pair + ((uint32_t)pair < r ? (uint32_t)pair : r);
+    }
+    __device__ __forceinline__ int owner(uint32_t block) const
+    {
+        return block < r * (q + 1) ? (int)(block / (q + 1)) : (int)(r + (block - r * (q + 1)) / q);
+    }
+    // the partial tile of a pair's range in cut tile t
+    __device__ __forceinline__ int slot(int pair, int t) const
+    {
+        return 2 * pair + ((int)(begin(pair) / (uint32_t)kb) != t);
+    }
 };
 
 template <int TN, bool A_MN, bool B_MN>
 struct GemmPolicy {
     struct Args {
         PairProblem p[3];
-        int units;
+        CUtensorMap part;   // partial tiles [2 np][256][TN] fp32
+        PairSplit split;
+        int np;
         DeviceStatus st;
     };
     struct Unit {
-        int p, m, n, slice, kb0, kbn;
+        int p, m, n, kb0, kbn;
+        int slot;           // partial tile to write (-1: the whole K, to D)
         int k0, kb_first;   // the first segment's K, and its blocks
     };
     static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 8, STAGING = 4096, SEGS = 1;
@@ -246,17 +274,33 @@ struct GemmPolicy {
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
     static __device__ __forceinline__ int slot_use(int, int n) { return n >> 1; }
     static __device__ __forceinline__ int slot_col(int s) { return s * 256; }
-    static __device__ __forceinline__ Unit decode(const Args &a, int u)
+    static __device__ __forceinline__ int count(const Args &a, int pair)
     {
+        const PairSplit &s = a.split;
+        if (s.cut == 0) return deal_count(s.tiles, s.np, pair);
+        const uint32_t b0 = s.begin(pair), b1 = s.begin(pair + 1);
+        return s.full + (b1 > b0 ? (int)((b1 - 1) / s.kb - b0 / s.kb) + 1 : 0);
+    }
+    static __device__ __forceinline__ Unit decode(const Args &a, int pair, int n)
+    {
+        const PairSplit &s = a.split;
         Unit r;
-        r.p = u >= a.p[2].first ? 2 : u >= a.p[1].first ? 1 : 0;
+        int t = pair + n * s.np;
+        r.kb0 = 0;
+        r.kbn = s.kb;
+        r.slot = -1;
+        if (s.cut && n >= s.full) {
+            const uint32_t b0 = s.begin(pair), b1 = s.begin(pair + 1), kb = s.kb;
+            const int c = (int)(b0 / kb) + n - s.full;   // cut tile
+            const uint32_t lo = c * kb > b0 ? c * kb : b0, hi = (c + 1) * kb < b1 ? (c + 1) * kb : b1;
+            r.kb0 = (int)(lo - c * kb);
+            r.kbn = (int)(hi - lo);
+            if (r.kbn < s.kb) r.slot = 2 * pair + (n > s.full);
+            t = s.full * s.np + c;
+        }
+        r.p = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
         const PairProblem &p = a.p[r.p];
-        const int t = u - p.first, tiles = p.mt * p.nt;
-        r.slice = t / tiles;
-        tile_order(t - r.slice * tiles, p.mt, p.nt, r.m, r.n);
-        const int64_t all = p.kb[0] + p.kb[1];
-        r.kb0 = (int)(all * r.slice / p.slices);
-        r.kbn = (int)(all * (r.slice + 1) / p.slices) - r.kb0;
+        tile_order(t - p.first, p.mt, p.nt, r.m, r.n);
         r.k0 = p.k[0];
         r.kb_first = p.kb[0];
         return r;
@@ -299,7 +343,7 @@ struct GemmPolicy {
         const PairProblem &p = a.p[u.p];
         const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, colh = u.n * TN + part * (TN / 2);
         const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (TN / 2);
-        if (p.slices > 1) {
+        if (u.slot >= 0) {
 #pragma unroll 1
             for (int j = 0; j < TN / 64; ++j) {
                 float v[32];
@@ -313,8 +357,9 @@ struct GemmPolicy {
                         make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && row0 < p.rows && colh + 32 * j < p.cols) {
-                    tma_store_3d(&p.part, colh + 32 * j, row0, u.slice, smem_u32(stage));
+                if (lane == 0) {
+                    tma_store_2d(&a.part, part * (TN / 2) + 32 * j, u.slot * 256 + (int)rank * 128 + quad * 32,
+                                 smem_u32(stage));
                     bulk_commit();
                 }
             }
@@ -368,13 +413,13 @@ struct GradPolicy {
     struct Args {
         CUtensorMap x, wg, wu, dy, wd, h, dg, du;
         const bf16 *bg, *bu;
-        int rows, C, F, mt, nt, kb, units;
+        int rows, C, F, mt, nt, kb, np;
         DeviceStatus st;
     };
     struct Unit {
         int m, n;
     };
-    static constexpr int STAGES = 4, STAGE_BYTES = 32768, EPI = 16, STAGING = 6144, SEGS = 2;
+    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, STAGING = 4096, SEGS = 2;
     static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 128);
     static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 256);
 
@@ -382,10 +427,11 @@ struct GradPolicy {
     static __device__ __forceinline__ int slot(int seg, int n) { return seg ? 0 : 1 + (n & 1); }
     static __device__ __forceinline__ int slot_use(int seg, int n) { return seg ? n : n >> 1; }
     static __device__ __forceinline__ int slot_col(int s) { return s == 0 ? 0 : 128 + 128 * s; }
-    static __device__ __forceinline__ Unit decode(const Args &a, int u)
+    static __device__ __forceinline__ int count(const Args &a, int pair) { return deal_count(a.mt * a.nt, a.np, pair); }
+    static __device__ __forceinline__ Unit decode(const Args &a, int pair, int n)
     {
         Unit r;
-        tile_order(u, a.mt, a.nt, r.m, r.n);
+        tile_order(pair + n * a.np, a.mt, a.nt, r.m, r.n);
         return r;
     }
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
@@ -418,6 +464,8 @@ struct GradPolicy {
     {
         const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
         const uint32_t gu = t_lane + part * 32, dh = t_lane + slot_col(slot(0, n)) + part * 32;
+        const bool inside = row0 < a.rows && col0 < a.F;
+        uint4 du[4];
         staging_free(lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -456,17 +504,20 @@ struct GradPolicy {
                 const uint32_t off = sw64_offset(lane, 2 * j + q);
                 *reinterpret_cast<uint4 *>(stage + off) = pack8f(hh);
                 *reinterpret_cast<uint4 *>(stage + 2048 + off) = pack8f(gq);
-                *reinterpret_cast<uint4 *>(stage + 4096 + off) = pack8f(dq);
+                du[2 * j + q] = pack8f(dq);
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && row0 < a.rows && col0 < a.F) {
-            tma_store_2d(&a.h, col0, row0, smem_u32(stage));
+        // two boxes of staging for three outputs: du takes h's when it is read
+        store_box(&a.h, col0, row0, inside, stage, lane);
+        if (lane == 0 && inside) {
             tma_store_2d(&a.dg, col0, row0, smem_u32(stage + 2048));
-            tma_store_2d(&a.du, col0, row0, smem_u32(stage + 4096));
             bulk_commit();
+            bulk_wait_read1();
         }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = du[q];
+        store_box(&a.du, col0, row0, inside, stage, lane);
     }
 };
 

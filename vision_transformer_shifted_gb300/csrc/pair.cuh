@@ -15,8 +15,9 @@
 // roles leave, and the CTAs meet at the closing cluster barrier.
 //
 // A policy P describes the kernel:
-//   Args                    kernel parameters (units: work items; st: DeviceStatus)
-//   Unit / decode(a, u)     one work item (a tile, or a K slice of one)
+//   Args                    kernel parameters (np: pairs launched; st: DeviceStatus)
+//   Unit, count(a, pair), decode(a, pair, n)   a pair's work items (a tile, or
+//                           a range of a tile's K blocks)
 //   STAGES, STAGE_BYTES     the ring
 //   EPI                     epilogue warps (8, or 16 where arithmetic binds)
 //   STAGING                 bytes of store staging per epilogue warp
@@ -204,6 +205,12 @@ __device__ __forceinline__ void tile_order(int t, int mt, int nt, int &m, int &n
     m = band * 8 + (r - n * h);
 }
 
+// Tiles dealt out in turn: pair, pair + np, ...
+__device__ __forceinline__ int deal_count(int tiles, int np, int pair)
+{
+    return pair < tiles ? (tiles - pair + np - 1) / np : 0;
+}
+
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * P::EPI, 1)
 pair_kernel(const __grid_constant__ typename P::Args a)
@@ -219,7 +226,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
     // (from one lane: the compiler then knows it for the same in all of them)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1, units = P::count(a, pair);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < P::STAGES; ++s) {
@@ -253,8 +260,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         int s = 0, issued = 0;
         uint32_t ph = 0;
 #pragma unroll 1
-        for (int u = first; u < a.units && !failed; u += step) {
-            const typename P::Unit un = P::decode(a, u);
+        for (int n = 0; n < units && !failed; ++n) {
+            const typename P::Unit un = P::decode(a, pair, n);
 #pragma unroll 1
             for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
                 const int kb_n = P::kblocks(a, un, seg);
@@ -306,8 +313,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
             int s = 0, n = 0;
             uint32_t ph = 0;
 #pragma unroll 1
-            for (int u = first; u < a.units && !failed; u += step, ++n) {
-                const typename P::Unit un = P::decode(a, u);
+            for (; n < units && !failed; ++n) {
+                const typename P::Unit un = P::decode(a, pair, n);
 #pragma unroll 1
                 for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
                     const int slot = P::slot(seg, n), kb_n = P::kblocks(a, un, seg);
@@ -343,8 +350,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         uint8_t *stage = staging + (warp - 2) * P::STAGING;
         int n = 0;
-        for (int u = first; u < a.units && !failed; u += step, ++n) {
-            const typename P::Unit un = P::decode(a, u);
+        for (; n < units && !failed; ++n) {
+            const typename P::Unit un = P::decode(a, pair, n);
             // (warp-uniform outcome: the TMEM loads below are warp-collective)
             for (int seg = 0; seg < P::SEGS && !failed; ++seg)
                 failed = !__all_sync(0xffffffffu, pair_wait(tfull + 8 * P::slot(seg, n), P::slot_use(seg, n) & 1,
@@ -385,9 +392,7 @@ cudaError_t launch_pair(const typename P::Args &a, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }
-    const int pairs = sm_count() / 2;
-    const unsigned grid = 2u * (unsigned)(a.units < pairs ? a.units : pairs);
-    return launch_maybe_overlapped(pair_kernel<P>, dim3(grid), dim3(64 + 32 * P::EPI), smem, stream, 1, a);
+    return launch_maybe_overlapped(pair_kernel<P>, dim3(2u * (unsigned)a.np), dim3(64 + 32 * P::EPI), smem, stream, 1, a);
 }
 
 } // namespace swin
