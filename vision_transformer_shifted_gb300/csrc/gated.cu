@@ -39,26 +39,32 @@ bool bad_pointer(const void *p, bool required)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// K-major operand [rows, k]: boxes of 128 bytes of K x box_rows.
-cudaError_t map_k(CUtensorMap *m, const void *p, int64_t rows, int k, int box_rows, bool q8 = false)
+// K-major operand [rows, k] (row stride ld elements, 0: k): boxes of 128 bytes
+// of K x box_rows.
+cudaError_t map_k(CUtensorMap *m, const void *p, int64_t rows, int k, int box_rows, bool q8 = false, int ld = 0)
 {
     const int e = q8 ? 1 : 2;
-    return make_tensor_map(m, q8 ? T_U8 : T_BF16, p, k, rows, (int64_t)k * e, 128 / e, box_rows, 128);
+    return make_tensor_map(m, q8 ? T_U8 : T_BF16, p, k, rows, (int64_t)(ld ? ld : k) * e, 128 / e, box_rows, 128);
 }
-// MN-major operand, stored [k, mn]: boxes of 64 MN elements x 64 k.
-cudaError_t map_mn(CUtensorMap *m, const void *p, int64_t k, int mn)
+// MN-major operand, stored [k, mn] (row stride ld, 0: mn): boxes of 64 MN
+// elements x 64 k.
+cudaError_t map_mn(CUtensorMap *m, const void *p, int64_t k, int mn, int ld = 0)
 {
-    return make_tensor_map(m, T_BF16, p, mn, k, (int64_t)mn * 2, 64, 64, 128);
+    return make_tensor_map(m, T_BF16, p, mn, k, (int64_t)(ld ? ld : mn) * 2, 64, 64, 128);
 }
 // Output [rows, cols]: a warp's boxes of 64 columns x 32 rows.
 cudaError_t map_out(CUtensorMap *m, const void *p, int64_t rows, int cols)
 {
     return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 64, 32, 128);
 }
-// Hidden activations [rows, F]: boxes of 32 columns x 32 rows.
+// Hidden activations in the workspace, [rows, F] with rows padded to 128 bytes:
+// a box's rows are whole lines.  (F = 1368 unpadded: five sectors in two lines
+// where four in one would do: its weight gradients took 47.7 us instead of 43.0.)
+int hidden_ld(int F) { return (F + 63) / 64 * 64; }
+// The kernels that write them: boxes of 32 columns x 32 rows.
 cudaError_t map_hidden(CUtensorMap *m, const void *p, int64_t rows, int cols)
 {
-    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 32, 32, 64);
+    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)hidden_ld(cols) * 2, 32, 32, 64);
 }
 
 // One product of a launch_products call: D [rows, cols] = sum over K segments of
@@ -66,6 +72,7 @@ cudaError_t map_hidden(CUtensorMap *m, const void *p, int64_t rows, int cols)
 struct Product {
     const void *a[2], *b[2];
     int k[2];
+    int lda, ldb;   // row strides as stored (0: dense)
     bf16 *d;
     const bf16 *bias, *residual;
     int64_t rows;
@@ -98,12 +105,16 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__
     tile_order(t - a.p[i].first, a.p[i].mt, a.p[i].nt, m, n);
     const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / 8;
     const int64_t size = 256 * a.tn;
+    const int first = s.slot(p0, c);
     for (int e = blockIdx.y * 256 + threadIdx.x; e < 256 * per; e += gridDim.y * 256) {
         const int row = m * 256 + e / per, col = n * a.tn + e % per * 8;
         if (row >= rows || col >= cols) continue;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
-        for (int p = p0; p <= p1; ++p) {
-            load8(a.part + s.slot(p, c) * size + (int64_t)e * 8, 0, 8, w);
+        float v[8], w[8];
+        const float *src = a.part + (int64_t)e * 8;
+        load8(src + first * size, 0, 8, v);
+#pragma unroll 4
+        for (int p = p0 + 1; p <= p1; ++p) {   // (these begin inside the tile: their first range)
+            load8(src + 2 * p * size, 0, 8, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += w[k];
         }
@@ -188,9 +199,11 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
             q.k[s] = p.k[s];
             q.kb[s] = p.k[s] ? ceil_div(p.k[s], 64) : 0;
             if (!p.k[s]) continue;
-            e = A_MN ? map_mn(&q.a[s], p.a[s], p.k[s], (int)p.rows) : map_k(&q.a[s], p.a[s], p.rows, p.k[s], 128);
+            e = A_MN ? map_mn(&q.a[s], p.a[s], p.k[s], (int)p.rows, p.lda)
+                     : map_k(&q.a[s], p.a[s], p.rows, p.k[s], 128, false, p.lda);
             if (e != cudaSuccess) return e;
-            e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols) : map_k(&q.b[s], p.b[s], p.cols, p.k[s], TN / 2);
+            e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols, p.ldb)
+                     : map_k(&q.b[s], p.b[s], p.cols, p.k[s], TN / 2, false, p.ldb);
             if (e != cudaSuccess) return e;
         }
         if ((e = map_out(&q.d, p.d, p.rows, p.cols)) != cudaSuccess) return e;
@@ -219,51 +232,65 @@ cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *pa
                    : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches);
 }
 
-// Column sums of up to three bf16 matrices [rows, cols]: block (x, y, z) sums
-// every gridDim.y-th group of 32 rows of 64 columns of matrix z into a partial
-// row; then the partial rows are added in a fixed order.
+// Column sums of up to three matrices [rows, cols] (fp32 or bf16): block (x, y,
+// z) sums every gridDim.y-th group of 32 rows of 64 columns of matrix z into a
+// partial row; then the partial rows are added, all in a fixed order.
 struct ColumnSums {
-    const bf16 *in[3];
-    bf16 *out[3];
-    float *part[3];   // [splits, cols]
-    int64_t rows;
-    int cols[3];
+    struct {
+        const float *f;   // fp32, or
+        const bf16 *b;
+        bf16 *out;
+        float *part;      // [splits, cols]
+        int64_t rows;
+        int cols;
+    } m[3];
     int splits;
 };
-__global__ void __launch_bounds__(256) column_partials_kernel(ColumnSums a)
+__global__ void __launch_bounds__(256) column_partials_kernel(const __grid_constant__ ColumnSums a)
 {
     __shared__ float sum[32][65];
     griddep_launch_dependents();
     griddep_wait();
-    const int z = blockIdx.z, cols = a.cols[z];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
-    if (blockIdx.x * 64 >= cols) return;
+    const auto &m = a.m[blockIdx.z];
+    const int cols = m.cols, c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
+    if ((int)blockIdx.x * 64 >= cols) return;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < cols)
-        for (int64_t i = (int64_t)blockIdx.y * 32 + r; i < a.rows; i += (int64_t)gridDim.y * 32) {
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t i = (int64_t)blockIdx.y * 32 + r; i < m.rows; i += (int64_t)gridDim.y * 32) {
             float w[8];
-            load8(a.in[z] + i * cols, c, cols, w);
+            if (m.f) load8(m.f + i * cols, c, cols, w);
+            else load8(m.b + i * cols, c, cols, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[r][(threadIdx.x & 7) * 8 + e] = v[e];
     __syncthreads();
-    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < cols) {
+    if (threadIdx.x < 64 && (int)(blockIdx.x * 64 + threadIdx.x) < cols) {
         float t = 0.f;
+#pragma unroll
         for (int i = 0; i < 32; ++i) t += sum[i][threadIdx.x];
-        a.part[z][(int64_t)blockIdx.y * cols + blockIdx.x * 64 + threadIdx.x] = t;
+        m.part[(int64_t)blockIdx.y * cols + blockIdx.x * 64 + threadIdx.x] = t;
     }
 }
-__global__ void __launch_bounds__(256) column_finish_kernel(ColumnSums a)
+__global__ void __launch_bounds__(1024) column_finish_kernel(const __grid_constant__ ColumnSums a)
 {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     griddep_launch_dependents();
     griddep_wait();
-    const int z = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.cols[z]) return;
-    float t = 0.f;
-    for (int s = 0; s < a.splits; ++s) t += a.part[z][(int64_t)s * a.cols[z] + c];
-    a.out[z][c] = __float2bfloat16_rn(t);
+    const auto &m = a.m[blockIdx.y];
+    const int c = blockIdx.x * 32 + lane;
+    float v = 0.f;
+    if (c < m.cols)
+        for (int s = w; s < a.splits; s += 32) v += m.part[(int64_t)s * m.cols + c];
+    part[w][lane] = v;
+    __syncthreads();
+    v = part[lane][w];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && (int)blockIdx.x * 32 + w < m.cols) m.out[blockIdx.x * 32 + w] = __float2bfloat16_rn(v);
 }
 
 // Workspace layout: bytes of each part, 1 KB aligned.
@@ -344,6 +371,7 @@ int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, con
     if (rc != SWIN_WATTN_OK) return rc;
     Product down{};
     down.k[0] = h->F;
+    down.lda = hidden_ld(h->F);
     down.b[0] = Wd;
     down.d = (bf16 *)out;
     down.bias = (const bf16 *)bd;
@@ -352,13 +380,13 @@ int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, con
     down.cols = h->C;
     const ProductsPlan pl = plan_products(&down, 1);
     Carve size(nullptr);
-    size.take((size_t)rows * h->F * 2);
+    size.take((size_t)rows * hidden_ld(h->F) * 2);
     size.take(pl.part_bytes);
     void *ws = nullptr;
     bool captured = false;
     if ((rc = ows_begin(&h->ws, size.used, stream, &ws, &captured)) != SWIN_WATTN_OK) return rc;
     Carve carve(ws);
-    bf16 *hidden = (bf16 *)carve.take((size_t)rows * h->F * 2);
+    bf16 *hidden = (bf16 *)carve.take((size_t)rows * hidden_ld(h->F) * 2);
     float *part = (float *)carve.take(pl.part_bytes);
     down.a[0] = hidden;
     const DeviceStatus st{h->d_err, WAIT_NS};
@@ -488,6 +516,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
 
     Product dxp{}, dw[3]{};
     dxp.k[0] = dxp.k[1] = h->F;
+    dxp.lda = hidden_ld(h->F);
     dxp.b[0] = p->Wg;
     dxp.b[1] = p->Wu;
     dxp.d = (bf16 *)dx;
@@ -498,6 +527,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         dw[i].rows = i < 2 ? h->F : h->C;
         dw[i].cols = i < 2 ? h->C : h->F;
     }
+    dw[0].lda = dw[1].lda = dw[2].ldb = hidden_ld(h->F);
     dw[0].b[0] = dw[1].b[0] = x;
     dw[2].a[0] = dy;
     dw[0].d = (bf16 *)g->dWg;
@@ -505,14 +535,18 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     dw[2].d = (bf16 *)g->dWd;
     const ProductsPlan px = plan_products(&dxp, 1), pw = plan_products(dw, 3);
     const size_t part_bytes = px.part_bytes > pw.part_bytes ? px.part_bytes : pw.part_bytes;
+    // bias gradients: dg's and du's sums over each warp's 32 rows come from the
+    // recompute kernel
     ColumnSums cs{};
-    cs.rows = rows;
+    const int row_blocks = ceil_div(rows, 256) * 8;
     cs.splits = ceil_div(rows, 256) < 64 ? ceil_div(rows, 256) : 64;
     int sums = 0, most = 0;
-    const size_t hid = (size_t)rows * h->F * 2;
+    const size_t row_sums = g->dbg || g->dbu ? (size_t)row_blocks * h->F * sizeof(float) : 0;
+    const size_t hid = (size_t)rows * hidden_ld(h->F) * 2;
     Carve size(nullptr);
     for (int i = 0; i < 3; ++i) size.take(hid);
     size.take(part_bytes);
+    for (int i = 0; i < 2; ++i) size.take(row_sums);
     size.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
     void *ws = nullptr;
     bool captured = false;
@@ -520,6 +554,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     Carve carve(ws);
     bf16 *hidden = (bf16 *)carve.take(hid), *dg = (bf16 *)carve.take(hid), *du = (bf16 *)carve.take(hid);
     float *part = (float *)carve.take(part_bytes);
+    float *dg_sums = (float *)carve.take(row_sums), *du_sums = (float *)carve.take(row_sums);
     float *sum_part = (float *)carve.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
     dxp.a[0] = dw[0].a[0] = dg;
     dxp.a[1] = dw[1].a[0] = du;
@@ -542,6 +577,10 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
             if ((e = map_hidden(m[i], o[i], rows, h->F)) != cudaSuccess) return e;
         a.bg = (const bf16 *)p->bg;
         a.bu = (const bf16 *)p->bu;
+        if (row_sums) {
+            a.dg_sums = dg_sums;
+            a.du_sums = du_sums;
+        }
         a.rows = rows;
         a.C = h->C;
         a.F = h->F;
@@ -556,24 +595,25 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     cudaError_t e = h->act == SWIN_BLOCK_GATED_SILU ? grad(GradPolicy<ACT_SILU>{}) : grad(GradPolicy<ACT_GELU>{});
     if (e == cudaSuccess) e = launch_products<false, true>(&dxp, px, part, st, s, &h->last_launches);
     if (e == cudaSuccess) e = launch_products<true, true>(dw, pw, part, st, s, &h->last_launches);
-    const bf16 *in[3] = {dg, du, (const bf16 *)dy};
     bf16 *out[3] = {(bf16 *)g->dbg, (bf16 *)g->dbu, (bf16 *)g->dbd};
     for (int i = 0; i < 3; ++i) {
-        const int cols = i < 2 ? h->F : h->C;
         if (!out[i]) continue;
-        cs.in[sums] = in[i];
-        cs.out[sums] = out[i];
-        cs.part[sums] = sum_part;
-        cs.cols[sums++] = cols;
-        sum_part += (size_t)cs.splits * cols;
-        if (cols > most) most = cols;
+        auto &m = cs.m[sums++];
+        m.f = i == 0 ? dg_sums : i == 1 ? du_sums : nullptr;
+        m.b = (const bf16 *)dy;
+        m.out = out[i];
+        m.part = sum_part;
+        m.rows = i < 2 ? row_blocks : rows;
+        m.cols = i < 2 ? h->F : h->C;
+        sum_part += (size_t)cs.splits * m.cols;
+        if (m.cols > most) most = m.cols;
     }
     if (e == cudaSuccess && sums) {
         h->last_launches += 2;
         e = launch_maybe_overlapped(column_partials_kernel, dim3(ceil_div(most, 64), cs.splits, sums), dim3(256), 0, s, 1,
                                     cs);
         if (e == cudaSuccess)
-            e = launch_maybe_overlapped(column_finish_kernel, dim3(ceil_div(most, 256), sums), dim3(256), 0, s, 1, cs);
+            e = launch_maybe_overlapped(column_finish_kernel, dim3(ceil_div(most, 32), sums), dim3(1024), 0, s, 1, cs);
     }
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;

@@ -401,6 +401,22 @@ struct GemmPolicy {
     }
 };
 
+// Column sums of a warp's 32 rows x 16 columns (a row a lane): lane l returns
+// column l % 16's.  Each exchange halves the columns a lane still sums.
+__device__ __forceinline__ float column_sum16(float (&v)[16], int lane)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const bool up = lane & o;
+            const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
 // ---- the backward's recompute: h, dg, du -----------------------------------------
 //
 // A unit is 256 rows x 128 hidden columns: dh = dy Wd (K = C; Wd [C, F] as an
@@ -413,6 +429,7 @@ struct GradPolicy {
     struct Args {
         CUtensorMap x, wg, wu, dy, wd, h, dg, du;
         const bf16 *bg, *bu;
+        float *dg_sums, *du_sums;   // [row blocks of 32][F]: sums of dg and du, or null
         int rows, C, F, mt, nt, kb, np;
         DeviceStatus st;
     };
@@ -505,6 +522,15 @@ struct GradPolicy {
                 *reinterpret_cast<uint4 *>(stage + off) = pack8f(hh);
                 *reinterpret_cast<uint4 *>(stage + 2048 + off) = pack8f(gq);
                 du[2 * j + q] = pack8f(dq);
+            }
+            if (a.dg_sums) {
+                const int c = col0 + 16 * j + (lane & 15);
+                const float sg = column_sum16(g, lane), su = column_sum16(d, lane);
+                if (lane < 16 && c < a.F) {
+                    const int64_t at = (int64_t)(u.m * 8 + (int)rank * 4 + quad) * a.F + c;
+                    a.dg_sums[at] = sg;
+                    a.du_sums[at] = su;
+                }
             }
         }
         // two boxes of staging for three outputs: du takes h's when it is read
