@@ -311,6 +311,24 @@ cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *s
                       const float *sg, const void *bg, const void *wu, const float *su, const void *bu, bf16 *hidden,
                       DeviceStatus st, cudaStream_t stream)
 {
+    if (rows <= FEW_ROWS) {
+        FewUp u{};
+        u.x = x;
+        u.wg = wg;
+        u.wu = wu;
+        u.bg = (const bf16 *)bg;
+        u.bu = (const bf16 *)bu;
+        u.sx = sx;
+        u.sg = sg;
+        u.su = su;
+        u.h = hidden;
+        u.rows = rows;
+        u.C = h->C;
+        u.F = h->F;
+        u.ldh = hidden_ld(h->F);
+        u.gelu = h->act == SWIN_BLOCK_GATED_GELU;
+        return launch_few_up(u, st, stream);
+    }
     auto run = [&](auto policy) -> cudaError_t {
         using P = decltype(policy);
         typename P::Args a;
@@ -378,7 +396,8 @@ int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, con
     down.residual = (const bf16 *)residual;
     down.rows = rows;
     down.cols = h->C;
-    const ProductsPlan pl = plan_products(&down, 1);
+    const bool few = rows <= FEW_ROWS;
+    const ProductsPlan pl = few ? ProductsPlan{} : plan_products(&down, 1);
     Carve size(nullptr);
     size.take((size_t)rows * hidden_ld(h->F) * 2);
     size.take(pl.part_bytes);
@@ -392,7 +411,13 @@ int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, con
     const DeviceStatus st{h->d_err, WAIT_NS};
     h->last_launches = 1;
     cudaError_t e = up(hidden, st);
-    if (e == cudaSuccess) e = launch_products<false, false>(&down, pl, part, st, stream, &h->last_launches);
+    if (e == cudaSuccess && few) {
+        ++h->last_launches;
+        e = launch_few_down(hidden, hidden_ld(h->F), rows, (const bf16 *)Wd, (const bf16 *)bd, (const bf16 *)residual,
+                            (bf16 *)out, h->C, h->F, st, stream);
+    } else if (e == cudaSuccess) {
+        e = launch_products<false, false>(&down, pl, part, st, stream, &h->last_launches);
+    }
     const int rc2 = ows_end(&h->ws, stream, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
 }

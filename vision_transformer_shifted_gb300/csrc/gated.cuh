@@ -547,4 +547,21 @@ struct GradPolicy {
     }
 };
 
+// ---- few rows (gated_few.cu) -------------------------------------------------------
+
+constexpr int FEW_ROWS = 128;   // most rows of these kernels
+struct FewUp {
+    const void *x, *wg, *wu;
+    const bf16 *bg, *bu;
+    const float *sx, *sg, *su;   // 8-bit form, else null
+    bf16 *h;
+    int rows, C, F, ldh;
+    bool gelu;
+};
+// h = act(x Wg^T + bg) * (x Wu^T + bu) into rows of stride ldh.
+cudaError_t launch_few_up(const FewUp &u, DeviceStatus st, cudaStream_t stream);
+// out = residual + h Wd^T + bd; queued directly behind launch_few_up.
+cudaError_t launch_few_down(const bf16 *h, int ldh, int rows, const bf16 *wd, const bf16 *bd, const bf16 *residual,
+                            bf16 *out, int C, int F, DeviceStatus st, cudaStream_t stream);
+
 } // namespace swin
