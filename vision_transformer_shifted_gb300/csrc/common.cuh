@@ -122,7 +122,9 @@ int ws_test_corrupt(const void *buf, int side);
 struct OrderedWorkspace {
     void *buf;
     size_t bytes;
-    cudaEvent_t done;
+    cudaEvent_t done;               // recorded behind the last call's work
+    unsigned long long stream_id;   // of the last call (unique for the process)
+    bool used;
 };
 // Workspace of `need` bytes for the work about to be queued on `stream`:
 // *ptr, and *captured (pass both to ows_end).  SWIN_WATTN_* status.

@@ -21,7 +21,7 @@ namespace {
 
 constexpr int FEW_THREADS = 192;   // four draining warps, a loading and an issuing one
 constexpr int ACT_NONE = -1;
-constexpr int FEW_MAX_STAGES = 8;
+constexpr int FEW_MAX_STAGES = 6;
 
 struct FewArgs {
     CUtensorMap w0, w1, x;         // ACT: Wg, Wu (boxes of 64 rows); else Wd (128 rows); x: np rows
@@ -35,11 +35,27 @@ struct FewArgs {
     DeviceStatus st;
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr)
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
+}
+__device__ __forceinline__ void add4(float (&s)[4], const float4 &v)
+{
+    s[0] += v.x;
+    s[1] += v.y;
+    s[2] += v.z;
+    s[3] += v.w;
+}
+__device__ __forceinline__ void add4(float (&s)[4], const bf16 *p)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+    add4(s, make_float4(a.x, a.y, b.x, b.y));
 }
 
 template <int KIND>
@@ -81,6 +97,11 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     if (warp == 5) {
         tmem_alloc(smem_u32(&tslot), tcols);
         tmem_relinquish();
+    }
+    if (warp == 4 && elect_one()) {
+        prefetch_map(&a.w0);
+        prefetch_map(&a.x);
+        if (ACT != ACT_NONE) prefetch_map(&a.w1);
     }
     tc_fence_before();
     __syncthreads();
@@ -193,35 +214,42 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
-    // the cluster's CTAs finish every split-th group of output values
+    if (split > 1) cluster_sync_all();
+    // the cluster's CTAs finish every split-th group of output values, four
+    // neighbours a thread
     const uint32_t base = smem_u32(smem);
-    for (int e = rank * FEW_THREADS + (int)threadIdx.x; e < a.rows * W; e += split * FEW_THREADS) {
-        const int t = e / W, i = e % W, c = tile * W + i;
-        if (c >= a.cols) continue;
-        float v = 0.f, u = 0.f;
+    const int items = a.rows * (W / 4);
+    for (int e = rank * FEW_THREADS + (int)threadIdx.x; e < items; e += split * FEW_THREADS) {
+        const int t = e / (W / 4), i = e % (W / 4) * 4, c = tile * W + i;
+        if (c >= a.cols) continue;   // (cols is a multiple of 8)
+        float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int r = 0; r < split; ++r) {
             const uint32_t at = map_rank(base + (uint32_t)(t * 128 + i) * 4, r);
-            v += ld_cluster(at);
-            if (ACT != ACT_NONE) u += ld_cluster(at + 64 * 4);
+            add4(v, ld_cluster(at));
+            if (ACT != ACT_NONE) add4(u, ld_cluster(at + 64 * 4));
         }
+        if (Q8) {
+            const float sx = a.sx[t];
+            const float4 p = *reinterpret_cast<const float4 *>(a.s0 + c), q = *reinterpret_cast<const float4 *>(a.s1 + c);
+            v[0] *= sx * p.x; v[1] *= sx * p.y; v[2] *= sx * p.z; v[3] *= sx * p.w;
+            u[0] *= sx * q.x; u[1] *= sx * q.y; u[2] *= sx * q.z; u[3] *= sx * q.w;
+        }
+        if (a.b0) add4(v, a.b0 + c);
         if (ACT == ACT_NONE) {
-            if (a.b0) v += __bfloat162float(a.b0[c]);
-            if (a.residual) v += __bfloat162float(a.residual[(int64_t)t * a.ld + c]);
+            if (a.residual) add4(v, a.residual + (int64_t)t * a.ld + c);
         } else {
-            if (Q8) {
-                v *= a.sx[t] * a.s0[c];
-                u *= a.sx[t] * a.s1[c];
+            if (a.b1) add4(u, a.b1 + c);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                activate2<ACT == ACT_NONE ? ACT_SILU : ACT>(v[k], v[k + 1]);
+                g2_mul(v[k], v[k + 1], v[k], v[k + 1], u[k], u[k + 1]);
             }
-            if (a.b0) v += __bfloat162float(a.b0[c]);
-            if (a.b1) u += __bfloat162float(a.b1[c]);
-            float w = v;
-            activate2<ACT == ACT_NONE ? ACT_SILU : ACT>(v, w);
-            v *= u;
         }
-        a.out[(int64_t)t * a.ld + c] = __float2bfloat16_rn(v);
+        *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ld + c) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
-    cluster_sync_all();   // (the others have read this CTA's sums)
+    if (split > 1) cluster_sync_all();   // (the others have read this CTA's sums)
     if (warp == 5) tmem_dealloc(tmem, tcols);
 }
 
@@ -234,10 +262,10 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     const int tiles = (width + W - 1) / W;
     a.split = 1;
     while (a.split < 8 && tiles * a.split < sm_count() && a.kb >= 4 * a.split) a.split *= 2;
-    // two CTAs an SM where four stages fit half of its shared memory
+    // two CTAs an SM (three stages with 128 rows, up to six with 16)
     a.stage_bytes = 16384 + a.np * 128;
-    a.stages = 4 * a.stage_bytes <= 110 * 1024 ? 110 * 1024 / a.stage_bytes : 220 * 1024 / a.stage_bytes;
-    if (a.stages > FEW_MAX_STAGES) a.stages = FEW_MAX_STAGES;
+    a.stages = 110 * 1024 / a.stage_bytes;
+    static_assert(110 * 1024 / (16384 + 16 * 128) <= FEW_MAX_STAGES && 3 * (16384 + 128 * 128) <= 110 * 1024, "ring");
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes;
     static std::atomic<uint64_t> ready;
     int dev = 0;
@@ -245,7 +273,7 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
-        e = cudaFuncSetAttribute(few_rows_kernel<ACT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+        e = cudaFuncSetAttribute(few_rows_kernel<ACT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 111 * 1024);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }

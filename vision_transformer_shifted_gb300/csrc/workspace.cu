@@ -137,10 +137,16 @@ int ows_begin(OrderedWorkspace *w, size_t need, cudaStream_t stream, void **ptr,
     // (growing frees the old buffer: cudaFree waits for the work that uses it)
     const int rc = ws_ensure(&w->buf, &w->bytes, need);
     if (rc != SWIN_WATTN_OK) return rc;
-    if (cudaStreamWaitEvent(stream, w->done, 0) != cudaSuccess) {
+    // (a stream's own order suffices on the stream of the last call; a wait there
+    // would keep the next kernel from starting under the last one's tail)
+    unsigned long long id = 0;
+    if (cudaStreamGetId(stream, &id) != cudaSuccess ||
+        (w->used && id != w->stream_id && cudaStreamWaitEvent(stream, w->done, 0) != cudaSuccess)) {
         cudaGetLastError();
         return SWIN_WATTN_ECUDA;
     }
+    w->stream_id = id;
+    w->used = true;
     *ptr = w->buf;
     return SWIN_WATTN_OK;
 }
