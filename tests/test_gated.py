@@ -258,6 +258,24 @@ def test_forward(rows, C, F, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", [(129, 8, 8), (257, 120, 64), (300, 64, 72), (1000, 128, 576), (20000, 8, 136),
+                                      (45001, 96, 256), (40000, 128, 200), (60001, 64, 64), (59000, 40, 328)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_forward_narrow(rows, C, F, kind):
+    """The one-kernel form: one chunk of hidden units, odd and even counts of
+    them, weights that stay and weights that stream, several tiles a pair."""
+    extra = (rows % 2 == 1) == (kind == "silu")
+    x, p, r, _ = make(rows, C, F, bias=extra, residual=not extra, seed=9)
+    ref, tol = forward_ref(x, p, r, kind)
+    out = torch.full((rows, C), float("nan"), dtype=BF, device=DEV)
+    with gated(C, F, kind) as h:
+        sw.swin_block_gated_forward(h, dev(x), dev(p), out, residual=dev(r))
+        sw.swin_block_gated_sync_status(h)
+        assert sw.swin_block_gated_last_launches(h) == 1
+    close(out, ref, tol)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,C,F", [s for s in SHAPES if s[1] % 16 == 0])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 def test_forward_q8(rows, C, F, kind):

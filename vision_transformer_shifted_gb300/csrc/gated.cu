@@ -481,6 +481,16 @@ int swin_block_gated_forward(swin_block_gated_t h, const void *x, int rows, cons
     if (any_overlap({out, n}, {{x, n}, {p->Wg, w}, {p->Wu, w}, {p->Wd, w}, {p->bg, f}, {p->bu, f}, {p->bd, c},
                                {residual == out ? nullptr : residual, n}}))
         return SWIN_WATTN_EINVAL;
+    if (rows > FEW_ROWS && gated_fused_supported(h->C)) {
+        const int rc = first_call(h);
+        if (rc != SWIN_WATTN_OK) return rc;
+        h->last_launches = 1;
+        return cuda_status(launch_gated_fused((const bf16 *)x, rows, h->C, h->F, h->act == SWIN_BLOCK_GATED_GELU,
+                                              (const bf16 *)p->Wg, (const bf16 *)p->bg, (const bf16 *)p->Wu,
+                                              (const bf16 *)p->bu, (const bf16 *)p->Wd, (const bf16 *)p->bd,
+                                              (const bf16 *)residual, (bf16 *)out, DeviceStatus{h->d_err, WAIT_NS},
+                                              (cudaStream_t)stream));
+    }
     return forward(h, rows, p->Wd, p->bd, residual, out, (cudaStream_t)stream, [&](bf16 *hidden, DeviceStatus st) {
         return launch_up<false>(h, x, nullptr, rows, p->Wg, nullptr, p->bg, p->Wu, nullptr, p->bu, hidden, st,
                                 (cudaStream_t)stream);

@@ -564,4 +564,12 @@ cudaError_t launch_few_up(const FewUp &u, DeviceStatus st, cudaStream_t stream);
 cudaError_t launch_few_down(const bf16 *h, int ldh, int rows, const bf16 *wd, const bf16 *bd, const bf16 *residual,
                             bf16 *out, int C, int F, DeviceStatus st, cudaStream_t stream);
 
+// ---- narrow tokens (gated_fused.cu) ---------------------------------------------------
+
+// The whole forward as one kernel, without a workspace.
+bool gated_fused_supported(int C);
+cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu, const bf16 *wg, const bf16 *bg,
+                               const bf16 *wu, const bf16 *bu, const bf16 *wd, const bf16 *bd, const bf16 *residual,
+                               bf16 *out, DeviceStatus st, cudaStream_t stream);
+
 } // namespace swin

@@ -1,0 +1,399 @@
+// The gated block's forward as one kernel for narrow tokens (C <= 128): out =
+// residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd with the hidden
+// activation kept on the SM.  At C = 96, F = 256 the hidden activation is 2.7
+// times as wide as a token: written and read back it would be 206 of 283 MB of
+// traffic for 200,704 tokens; here x, the residual and out remain.
+//
+// A CTA pair walks 256-row tiles.  The hidden units go in chunks of 64: one 256
+// x 128 x C MMA group leaves g in columns 0..63 and u in 64..127 of one of two
+// TMEM buffers (the halves of B again from Wg and Wu); one of two groups of
+// eight warps forms h and writes it to shared memory as the K-major A operand
+// of the last product, whose 256 x C accumulator sums over the chunks in one of
+// two more TMEM buffers.  The groups take alternate chunks, and group t mod 2
+// drains tile t's output after its first chunk of tile t + 1: neither waits for
+// the MMAs of its own last chunk.  Weights stream through a ring of chunks, or
+// stay (loaded once) where all chunks fit it.  Arithmetic per hidden value
+// binds (the activation: about 20 instructions with the drain), not HBM.
+#include <atomic>
+#include <cstring>
+
+#include "gated.cuh"
+
+namespace swin {
+
+namespace {
+
+constexpr int FUSED_GROUPS = 2, FUSED_GROUP_WARPS = 8;
+constexpr int FUSED_THREADS = 64 + 32 * FUSED_GROUPS * FUSED_GROUP_WARPS;
+constexpr int FUSED_CHUNK = 64;
+constexpr int FUSED_SLOTS = 12;   // most weight chunks in the ring
+
+struct FusedArgs {
+    CUtensorMap x, wg, wu, wd, out;
+    const bf16 *bg, *bu, *bd, *residual;
+    int rows, C, F, tiles, np;
+    int xb, n2;              // K blocks of a token; N of the last product (C rounded up to 16)
+    int chunks, slots, slot_bytes;
+    bool resident;           // every chunk has its slot: loaded once
+    DeviceStatus st;
+};
+
+struct FusedBars {
+    uint64_t xfull[2], xempty[2], gfull[2], gempty[2], hready[2], hfree[2], yfull[2], yempty[2];
+    uint64_t wfull[FUSED_SLOTS], wempty[FUSED_SLOTS];
+};
+
+// (position, phase) in a ring.
+struct RingPos {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n)
+    {
+        if (++s == n) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, uint64_t limit)
+{
+    return __all_sync(0xffffffffu, pair_wait(bar, parity, limit));
+}
+__device__ __forceinline__ bool all_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit)
+{
+    return __all_sync(0xffffffffu, pair_wait<true>(bar, parity, limit));
+}
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED_THREADS, 1)
+gated_fused_kernel(const __grid_constant__ FusedArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_align(smem_raw, 1024);
+    __shared__ FusedBars bars;
+    __shared__ uint32_t tslot;
+    // [x 2][h 2][weights slots][staging a warp]
+    const uint32_t x_bytes = (uint32_t)a.xb * 16384u;
+    uint8_t *sx = smem, *sh = sx + 2 * x_bytes, *sw = sh + 2 * 16384, *stg = sw + (size_t)a.slots * a.slot_bytes;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, my = deal_count(a.tiles, a.np, pair);
+    const uint64_t limit = a.st.wait_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars.xfull[i]), 1);
+            mbar_init(smem_u32(&bars.xempty[i]), 1);
+            mbar_init(smem_u32(&bars.gfull[i]), 1);
+            mbar_init(smem_u32(&bars.gempty[i]), 2 * FUSED_GROUP_WARPS);
+            mbar_init(smem_u32(&bars.hready[i]), 2 * FUSED_GROUP_WARPS);
+            mbar_init(smem_u32(&bars.hfree[i]), 1);
+            mbar_init(smem_u32(&bars.yfull[i]), 1);
+            mbar_init(smem_u32(&bars.yempty[i]), 2 * FUSED_GROUP_WARPS);
+        }
+        for (int i = 0; i < a.slots; ++i) {
+            mbar_init(smem_u32(&bars.wfull[i]), 1);
+            mbar_init(smem_u32(&bars.wempty[i]), 1);
+        }
+        mbar_init_fence();
+    }
+    if (warp == 0 && elect_one()) {
+        prefetch_map(&a.x);
+        prefetch_map(rank ? &a.wu : &a.wg);
+        prefetch_map(&a.wd);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&tslot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tslot;
+    const uint32_t TY = tmem + 256;   // (output accumulators; g | u at columns 0 and 128)
+    bool failed = false;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        // ---------------- loads ----------------
+        const uint32_t xfull0 = map_rank(smem_u32(&bars.xfull[0]), 0), wfull0 = map_rank(smem_u32(&bars.wfull[0]), 0);
+        RingPos w;
+#pragma unroll 1
+        for (int i = 0; i < my && !failed; ++i) {
+            const int row = (pair + i * a.np) * 256 + (int)rank * 128, b = i & 1;
+            if (!all_wait(smem_u32(&bars.xempty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, limit)) {
+                failed = true;
+                break;
+            }
+            if (elect_one()) {
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars.xfull[b]), 2 * x_bytes);
+                for (int k = 0; k < a.xb; ++k)
+                    tma_load_2d_pair(smem_u32(sx) + b * x_bytes + k * 16384, &a.x, k * 64, row, xfull0 + 8 * b);
+            }
+            if (a.resident && i > 0) continue;
+#pragma unroll 1
+            for (int c = 0; c < a.chunks; ++c) {
+                if (!all_wait(smem_u32(&bars.wempty[w.s]), w.ph ^ 1u, limit)) {
+                    failed = true;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t dst = smem_u32(sw) + w.s * a.slot_bytes, bar = wfull0 + 8 * w.s;
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars.wfull[w.s]), 2 * a.slot_bytes);
+                    for (int k = 0; k < a.xb; ++k)
+                        tma_load_2d_pair(dst + k * 8192, rank ? &a.wu : &a.wg, k * 64, c * FUSED_CHUNK, bar);
+                    tma_load_2d_pair(dst + a.xb * 8192, &a.wd, c * FUSED_CHUNK, (int)rank * (a.n2 / 2), bar);
+                }
+                w.next(a.slots);
+            }
+        }
+        // every commit on its way to this CTA's barriers has arrived
+        for (int i = my > 1 ? my - 2 : 0; i < my && !failed; ++i)
+            failed = !all_wait(smem_u32(&bars.xempty[i & 1]), (uint32_t)(i >> 1) & 1u, limit);
+        for (int k = 0; !a.resident && k < a.slots && k < my * a.chunks && !failed; ++k, w.next(a.slots))
+            failed = !all_wait(smem_u32(&bars.wempty[w.s]), w.ph ^ 1u, limit);
+        if (failed) {
+            // (copies in flight land before the memory is given back)
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMAs (the leader's) ----------------
+        if (rank == 0) {
+            const uint32_t idesc1 = idesc_pair(MMA_BF16, false, false, 256, 128);
+            const uint32_t idesc2 = idesc_pair(MMA_BF16, false, false, 256, 0) | (uint32_t)(a.n2 >> 3) << 17;
+            const uint32_t x16 = smem_u32(sx) >> 4, h16 = smem_u32(sh) >> 4, w16 = smem_u32(sw) >> 4;
+            const int total = my * a.chunks;
+            int i1 = 0, c1 = 0, i2 = 0, c2 = 0;   // tile (of this pair) and chunk of the two products
+            RingPos w1, w2;
+#pragma unroll 1
+            for (int q = 0; q <= total && !failed; ++q) {
+                if (q < total) {   // g | u of chunk q
+                    const int b = q & 1;
+                    bool ok = c1 || all_wait(smem_u32(&bars.xfull[i1 & 1]), (uint32_t)(i1 >> 1) & 1u, limit);
+                    ok = ok && all_wait(smem_u32(&bars.wfull[w1.s]), a.resident ? 0u : w1.ph, limit);
+                    ok = ok && all_wait_cluster(smem_u32(&bars.gempty[b]), ((uint32_t)(q >> 1) & 1u) ^ 1u, limit);
+                    if (!ok) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        for (int k = 0; k < a.xb; ++k)
+                            mma_kblock<MMA_BF16, false, false>(tmem + 128 * b, x16 + (i1 & 1) * (x_bytes >> 4) + k * 1024,
+                                                               w16 + w1.s * (a.slot_bytes >> 4) + k * 512, idesc1,
+                                                               kblock_steps(a.C, k, 64), k == 0);
+                        mma_commit_pair(smem_u32(&bars.gfull[b]));
+                        if (c1 == a.chunks - 1) mma_commit_pair(smem_u32(&bars.xempty[i1 & 1]));
+                    }
+                    w1.next(a.slots);
+                    if (++c1 == a.chunks) {
+                        c1 = 0;
+                        ++i1;
+                        if (a.resident) w1 = RingPos();
+                    }
+                }
+                if (q > 0) {   // the last product's part of chunk q - 1
+                    const int p = q - 1, b = p & 1, y = i2 & 1;
+                    bool ok = c2 || all_wait_cluster(smem_u32(&bars.yempty[y]), ((uint32_t)(i2 >> 1) & 1u) ^ 1u, limit);
+                    ok = ok && all_wait_cluster(smem_u32(&bars.hready[b]), (uint32_t)(p >> 1) & 1u, limit);
+                    if (!ok) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        mma_kblock<MMA_BF16, false, false>(TY + 128 * y, h16 + b * 1024,
+                                                           w16 + w2.s * (a.slot_bytes >> 4) + a.xb * 512, idesc2, 4, c2 == 0);
+                        mma_commit_pair(smem_u32(&bars.hfree[b]));
+                        if (!a.resident) mma_commit_pair(smem_u32(&bars.wempty[w2.s]));
+                        if (c2 == a.chunks - 1) mma_commit_pair(smem_u32(&bars.yfull[y]));
+                    }
+                    w2.next(a.slots);
+                    if (++c2 == a.chunks) {
+                        c2 = 0;
+                        ++i2;
+                        if (a.resident) w2 = RingPos();
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------- activations and output ----------------
+        const int e = warp - 2, grp = e / FUSED_GROUP_WARPS, quad = warp & 3, half = (e % FUSED_GROUP_WARPS) >> 2;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        uint8_t *hbuf = sh + grp * 16384, *stage = stg + e * 2048;
+        const uint32_t gempty = map_rank(smem_u32(&bars.gempty[grp]), 0), hready = map_rank(smem_u32(&bars.hready[grp]), 0);
+        const int total = my * a.chunks;
+
+        // output rows of this pair's i-th tile: bias, residual, store
+        auto drain = [&](int i) {
+            const int y = i & 1;
+            if (!all_wait(smem_u32(&bars.yfull[y]), (uint32_t)(i >> 1) & 1u, limit)) {
+                failed = true;
+                return;
+            }
+            tc_fence_after();
+            const int row0 = (pair + i * a.np) * 256 + (int)rank * 128 + quad * 32;
+            const bool row_ok = row0 + lane < a.rows;
+            const bf16 *res = a.residual && row_ok ? a.residual + (int64_t)(row0 + lane) * a.C : nullptr;
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
+                const int c0 = half * 64 + 32 * j;
+                if (c0 >= a.C) break;
+                float v[32];
+                tmem_ld32(TY + 128 * y + lanes + c0, v);
+                staging_free(lane);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float b[8];
+                    if (a.bd) {
+                        load8(a.bd, c0 + 8 * q, a.C, b);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[8 * q + k] += b[k];
+                    }
+                    if (res) {
+                        load8(res, c0 + 8 * q, a.C, b);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[8 * q + k] += b[k];
+                    }
+                    *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(v + 8 * q);
+                }
+                store_box(&a.out, c0, row0, row0 < a.rows, stage, lane);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&bars.yempty[y]), 0));
+        };
+
+        int pending = -1;   // tile whose output this group has yet to drain
+        int i = grp / a.chunks, c = grp % a.chunks;
+#pragma unroll 1
+        for (int q = grp; q < total && !failed; q += FUSED_GROUPS) {
+            const uint32_t use = (uint32_t)(q >> 1) & 1u;
+            if (!all_wait(smem_u32(&bars.gfull[grp]), use, limit)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            float g[32], v[32];
+            tmem_ld32(tmem + 128 * grp + lanes + half * 32, g);
+            tmem_ld32(tmem + 128 * grp + lanes + 64 + half * 32, v);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(gempty);
+            const int f0 = c * FUSED_CHUNK + half * 32;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int f = f0 + 8 * s;
+                float *gq = g + 8 * s, *vq = v + 8 * s;
+                float b[8];
+                if (a.bg) {
+                    load8(a.bg, f, a.F, b);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) gq[k] += b[k];
+                }
+                if (a.bu) {
+                    load8(a.bu, f, a.F, b);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) vq[k] += b[k];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    activate2<ACT>(gq[k], gq[k + 1]);
+                    g2_mul(vq[k], vq[k + 1], vq[k], vq[k + 1], gq[k], gq[k + 1]);
+                }
+            }
+            // the MMAs that read this buffer two chunks ago are done
+            if (!all_wait(smem_u32(&bars.hfree[grp]), use ^ 1u, limit)) {
+                failed = true;
+                break;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                *reinterpret_cast<uint4 *>(hbuf + sw128_offset(quad * 32 + lane, half * 4 + s)) = pack8f(v + 8 * s);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(hready);
+
+            if (pending >= 0) {
+                drain(pending);
+                pending = -1;
+            }
+            const int tile = i;
+            c += FUSED_GROUPS;
+            while (c >= a.chunks) {
+                c -= a.chunks;
+                ++i;
+            }
+            // (this group's last chunk of an own tile: drained after its next chunk)
+            if (i > tile)
+                for (int t = tile; t < i; ++t)
+                    if ((t & 1) == grp) pending = t;
+        }
+        if (!failed && pending >= 0) drain(pending);
+        const int mine = (total - grp + 1) / FUSED_GROUPS;   // chunks of this group
+        if (!failed && mine > 0) failed = !all_wait(smem_u32(&bars.hfree[grp]), (uint32_t)(mine - 1) & 1u, limit);
+        if (lane == 0) bulk_wait_all();
+    }
+    if (failed && lane == 0) atomicOr(a.st.err, ERR_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+} // namespace
+
+bool gated_fused_supported(int C) { return C <= 128; }
+
+cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu, const bf16 *wg, const bf16 *bg,
+                               const bf16 *wu, const bf16 *bu, const bf16 *wd, const bf16 *bd, const bf16 *residual,
+                               bf16 *out, DeviceStatus st, cudaStream_t stream)
+{
+    FusedArgs a;
+    memset(&a, 0, sizeof(a));
+    const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    a.n2 = (C + 15) / 16 * 16;
+    a.xb = (C + 63) / 64;
+    a.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
+    a.slot_bytes = a.xb * 8192 + a.n2 * 64;
+    const int fixed = 2 * a.xb * 16384 + 2 * 16384 + FUSED_GROUPS * FUSED_GROUP_WARPS * 2048;
+    const int room = 226 * 1024 - 1024 - fixed;   // (1 KB for the barriers, 1 KB of alignment)
+    a.slots = room / a.slot_bytes;
+    if (a.slots > FUSED_SLOTS) a.slots = FUSED_SLOTS;
+    if (a.slots > a.chunks) a.slots = a.chunks;
+    a.resident = a.slots == a.chunks;
+    const size_t smem = 1024 + (size_t)fixed + (size_t)a.slots * a.slot_bytes;
+    cudaError_t e;
+    if ((e = make_tensor_map(&a.x, type, x, C, rows, (int64_t)C * 2, 64, 128, 128)) != cudaSuccess) return e;
+    if ((e = make_tensor_map(&a.wg, type, wg, C, F, (int64_t)C * 2, 64, 64, 128)) != cudaSuccess) return e;
+    if ((e = make_tensor_map(&a.wu, type, wu, C, F, (int64_t)C * 2, 64, 64, 128)) != cudaSuccess) return e;
+    if ((e = make_tensor_map(&a.wd, type, wd, F, C, (int64_t)F * 2, 64, a.n2 / 2, 128)) != cudaSuccess) return e;
+    if ((e = make_tensor_map(&a.out, type, out, C, rows, (int64_t)C * 2, 32, 32, 64)) != cudaSuccess) return e;
+    a.bg = bg;
+    a.bu = bu;
+    a.bd = bd;
+    a.residual = residual;
+    a.rows = rows;
+    a.C = C;
+    a.F = F;
+    a.tiles = (int)(((int64_t)rows + 255) / 256);
+    a.np = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
+    a.st = st;
+    auto *kern = gelu ? gated_fused_kernel<ACT_GELU> : gated_fused_kernel<ACT_SILU>;
+    static std::atomic<uint64_t> ready[2];
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready[gelu].load() & bit)) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024)) != cudaSuccess) return e;
+        ready[gelu].fetch_or(bit);
+    }
+    return launch_maybe_overlapped(kern, dim3(2u * (unsigned)a.np), dim3(FUSED_THREADS), smem, stream, 1, a);
+}
+
+} // namespace swin
