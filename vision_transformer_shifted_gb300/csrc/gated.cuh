@@ -71,6 +71,15 @@ __device__ __forceinline__ void activate_grad2(float g0, float g1, float &a0, fl
     g2_fma(d0, d1, s0, s1, e0, e1, p0, p1);
 }
 
+// d += s, two lanes.
+__device__ __forceinline__ void g2_add(float &d0, float &d1, float s0, float s1)
+{
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(s0), "f"(s1));
+}
+
 // Eight values of a bf16 vector at column c (zero past n, and for NULL).
 __device__ __forceinline__ void load8(const bf16 *v, int c, int n, float (&f)[8])
 {
@@ -93,6 +102,27 @@ __device__ __forceinline__ void load8(const float *v, int c, int n, float (&f)[8
     }
     f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
     f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+}
+
+// A vector over the columns of a warp's accumulators (a bias, a scale): each lane
+// fetches its column's value, early; the warp spreads them through 32 floats of
+// its shared memory, and every lane reads them back eight at a time.  (Eight
+// values of the vector loaded from global memory by every lane at every use
+// took 21 us of the narrow forward's 97.)
+__device__ __forceinline__ float lane_value(const bf16 *v, int c, int n)
+{
+    return v && c < n ? __bfloat162float(v[c]) : 0.f;
+}
+__device__ __forceinline__ void spread8(const float *vec, int q, float (&f)[8])
+{
+    const float4 x = *reinterpret_cast<const float4 *>(vec + 8 * q), y = *reinterpret_cast<const float4 *>(vec + 8 * q + 4);
+    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+}
+__device__ __forceinline__ void add8(float *d, const float (&s)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) g2_add(d[e], d[e + 1], s[e], s[e + 1]);
 }
 
 __device__ __forceinline__ uint4 pack8f(const float *v)
@@ -138,7 +168,7 @@ struct UpPolicy {
         int m, n;
     };
     static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
-    static constexpr int STAGES = 6, STAGE_BYTES = 32768, EPI = 16, STAGING = 2048, SEGS = 1;
+    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, STAGING = 2560, SEGS = 1;
     static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 256);
 
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
@@ -164,45 +194,64 @@ struct UpPolicy {
         mma_kblock<Q8 ? MMA_E4M3 : MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC, kblock_steps(a.C, kb, ELEMS),
                                                            kb == 0);
     }
+    struct Pre {
+        float bg, bu, sg, su, sx;   // of this lane's column, and its row's scale
+    };
+    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int quad, int part,
+                                                   int lane)
+    {
+        const int c = u.n * 128 + part * 32 + lane, row = u.m * 256 + (int)rank * 128 + quad * 32 + lane;
+        Pre p{};
+        p.bg = lane_value(a.bg, c, a.F);
+        p.bu = lane_value(a.bu, c, a.F);
+        if (Q8) {
+            p.sg = c < a.F ? a.sg[c] : 0.f;
+            p.su = c < a.F ? a.su[c] : 0.f;
+            p.sx = row < a.rows ? a.sx[row] : 0.f;
+        }
+        return p;
+    }
     template <class Release>
-    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
-                                                    int part, int lane, uint32_t t_lane, uint8_t *stage,
-                                                    Release &&release)
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, const Pre &pre, int n, uint32_t rank,
+                                                    int warp, int quad, int part, int lane, uint32_t t_lane,
+                                                    uint8_t *staging, Release &&release)
     {
         const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
         const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * 32;
+        // the warps' boxes (aligned for their swizzle), then the warps' vectors
+        uint8_t *stage = staging + warp * 2048;
+        float *vec = reinterpret_cast<float *>(staging + EPI * 2048 + warp * 512);
         float g[32], v[32];
         tmem_ld32(acc, g);
         tmem_ld32(acc + 128, v);
-        float sx = 1.f;
-        if (Q8) sx = row0 + lane < a.rows ? a.sx[row0 + lane] : 0.f;
-        staging_free(lane);
+        vec[lane] = pre.bg;
+        vec[32 + lane] = pre.bu;
+        if (Q8) {
+            vec[64 + lane] = pre.sg;
+            vec[96 + lane] = pre.su;
+        }
+        staging_free(lane);   // (and the vectors are there)
         tmem_wait_ld();
         release();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int c = col0 + 8 * q;
             float *gq = g + 8 * q, *vq = v + 8 * q;
+            float s[8];
             if (Q8) {
-                float s[8];
-                load8(a.sg, c, a.F, s);
+                spread8(vec + 64, q, s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) gq[e] *= sx * s[e];
-                load8(a.su, c, a.F, s);
+                for (int e = 0; e < 8; ++e) gq[e] *= pre.sx * s[e];
+                spread8(vec + 96, q, s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) vq[e] *= sx * s[e];
+                for (int e = 0; e < 8; ++e) vq[e] *= pre.sx * s[e];
             }
             if (a.bg) {
-                float b[8];
-                load8(a.bg, c, a.F, b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) gq[e] += b[e];
+                spread8(vec, q, s);
+                add8(gq, s);
             }
             if (a.bu) {
-                float b[8];
-                load8(a.bu, c, a.F, b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) vq[e] += b[e];
+                spread8(vec + 32, q, s);
+                add8(vq, s);
             }
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
@@ -335,11 +384,14 @@ struct GemmPolicy {
         if (kb >= u.kb_first) kb -= u.kb_first;
         mma_kblock<MMA_BF16, A_MN, B_MN>(d, src16, src16 + 1024, IDESC, kblock_steps(u.k0, kb, 64), i == 0);
     }
+    struct Pre {};
+    static __device__ __forceinline__ Pre prefetch(const Args &, const Unit &, uint32_t, int, int, int) { return Pre{}; }
     template <class Release>
-    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
-                                                    int part, int lane, uint32_t t_lane, uint8_t *stage,
-                                                    Release &&release)
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, const Pre &, int n, uint32_t rank,
+                                                    int warp, int quad, int part, int lane, uint32_t t_lane,
+                                                    uint8_t *staging, Release &&release)
     {
+        uint8_t *stage = staging + warp * STAGING;
         const PairProblem &p = a.p[u.p];
         const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, colh = u.n * TN + part * (TN / 2);
         const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (TN / 2);
@@ -436,7 +488,7 @@ struct GradPolicy {
     struct Unit {
         int m, n;
     };
-    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, STAGING = 4096, SEGS = 2;
+    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, STAGING = 4096 + 64, SEGS = 2;
     static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 128);
     static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 256);
 
@@ -474,15 +526,34 @@ struct GradPolicy {
         if (seg == 0) mma_kblock<MMA_BF16, false, true>(d, src16, src16 + 1024, IDESC_H, steps, kb == 0);
         else mma_kblock<MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC_GU, steps, kb == 0);
     }
+    struct Pre {
+        bf16 bg, bu;   // of this lane's column
+    };
+    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t, int, int part, int lane)
+    {
+        const int c = u.n * 128 + part * 32 + lane;
+        Pre p;
+        p.bg = a.bg && c < a.F ? a.bg[c] : __float2bfloat16_rn(0.f);
+        p.bu = a.bu && c < a.F ? a.bu[c] : __float2bfloat16_rn(0.f);
+        return p;
+    }
     template <class Release>
-    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, int n, uint32_t rank, int quad,
-                                                    int part, int lane, uint32_t t_lane, uint8_t *stage,
-                                                    Release &&release)
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, const Pre &pre, int n, uint32_t rank,
+                                                    int warp, int quad, int part, int lane, uint32_t t_lane,
+                                                    uint8_t *staging, Release &&release)
     {
         const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
         const uint32_t gu = t_lane + part * 32, dh = t_lane + slot_col(slot(0, n)) + part * 32;
         const bool inside = row0 < a.rows && col0 < a.F;
         uint4 du[4];
+        // the boxes, then the biases (bf16: a KB is all that is left), shared by
+        // the four warps of the same columns, which write the same values; by
+        // units in turn, since a warp can be one unit ahead of another (not two:
+        // the MMAs of the second wait for every warp's release of the first)
+        uint8_t *stage = staging + warp * 4096;
+        bf16 *vec = reinterpret_cast<bf16 *>(staging + EPI * 4096) + ((n & 1) * 4 + part) * 64;
+        vec[lane] = pre.bg;
+        vec[32 + lane] = pre.bu;
         staging_free(lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -494,19 +565,15 @@ struct GradPolicy {
             if (j == 1) release();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int c = col0 + 16 * j + 8 * q;
                 float *gq = g + 8 * q, *vq = v + 8 * q, *dq = d + 8 * q;
+                float s[8];
                 if (a.bg) {
-                    float b[8];
-                    load8(a.bg, c, a.F, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) gq[e] += b[e];
+                    load8(vec, 8 * (2 * j + q), 32, s);
+                    add8(gq, s);
                 }
                 if (a.bu) {
-                    float b[8];
-                    load8(a.bu, c, a.F, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) vq[e] += b[e];
+                    load8(vec + 32, 8 * (2 * j + q), 32, s);
+                    add8(vq, s);
                 }
                 float hh[8];
 #pragma unroll

@@ -56,15 +56,6 @@ struct RingPos {
     }
 };
 
-__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, uint64_t limit)
-{
-    return __all_sync(0xffffffffu, pair_wait(bar, parity, limit));
-}
-__device__ __forceinline__ bool all_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit)
-{
-    return __all_sync(0xffffffffu, pair_wait<true>(bar, parity, limit));
-}
-
 template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED_THREADS, 1)
 gated_fused_kernel(const __grid_constant__ FusedArgs a)
@@ -73,6 +64,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
     uint8_t *smem = smem_align(smem_raw, 1024);
     __shared__ FusedBars bars;
     __shared__ uint32_t tslot;
+    __shared__ __align__(16) float vecs[FUSED_GROUPS * FUSED_GROUP_WARPS][64];   // a warp's biases of its 32 hidden units
     // [x 2][h 2][weights slots][staging a warp]
     const uint32_t x_bytes = (uint32_t)a.xb * 16384u;
     uint8_t *sx = smem, *sh = sx + 2 * x_bytes, *sw = sh + 2 * 16384, *stg = sw + (size_t)a.slots * a.slot_bytes;
@@ -121,7 +113,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
 #pragma unroll 1
         for (int i = 0; i < my && !failed; ++i) {
             const int row = (pair + i * a.np) * 256 + (int)rank * 128, b = i & 1;
-            if (!all_wait(smem_u32(&bars.xempty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, limit)) {
+            if (!warp_pair_wait(smem_u32(&bars.xempty[b]), ((uint32_t)(i >> 1) & 1u) ^ 1u, limit)) {
                 failed = true;
                 break;
             }
@@ -133,7 +125,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             if (a.resident && i > 0) continue;
 #pragma unroll 1
             for (int c = 0; c < a.chunks; ++c) {
-                if (!all_wait(smem_u32(&bars.wempty[w.s]), w.ph ^ 1u, limit)) {
+                if (!warp_pair_wait(smem_u32(&bars.wempty[w.s]), w.ph ^ 1u, limit)) {
                     failed = true;
                     break;
                 }
@@ -149,9 +141,9 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
         }
         // every commit on its way to this CTA's barriers has arrived
         for (int i = my > 1 ? my - 2 : 0; i < my && !failed; ++i)
-            failed = !all_wait(smem_u32(&bars.xempty[i & 1]), (uint32_t)(i >> 1) & 1u, limit);
+            failed = !warp_pair_wait(smem_u32(&bars.xempty[i & 1]), (uint32_t)(i >> 1) & 1u, limit);
         for (int k = 0; !a.resident && k < a.slots && k < my * a.chunks && !failed; ++k, w.next(a.slots))
-            failed = !all_wait(smem_u32(&bars.wempty[w.s]), w.ph ^ 1u, limit);
+            failed = !warp_pair_wait(smem_u32(&bars.wempty[w.s]), w.ph ^ 1u, limit);
         if (failed) {
             // (copies in flight land before the memory is given back)
             const uint64_t t0 = global_timer_ns();
@@ -170,9 +162,9 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             for (int q = 0; q <= total && !failed; ++q) {
                 if (q < total) {   // g | u of chunk q
                     const int b = q & 1;
-                    bool ok = c1 || all_wait(smem_u32(&bars.xfull[i1 & 1]), (uint32_t)(i1 >> 1) & 1u, limit);
-                    ok = ok && all_wait(smem_u32(&bars.wfull[w1.s]), a.resident ? 0u : w1.ph, limit);
-                    ok = ok && all_wait_cluster(smem_u32(&bars.gempty[b]), ((uint32_t)(q >> 1) & 1u) ^ 1u, limit);
+                    bool ok = c1 || warp_pair_wait(smem_u32(&bars.xfull[i1 & 1]), (uint32_t)(i1 >> 1) & 1u, limit);
+                    ok = ok && warp_pair_wait(smem_u32(&bars.wfull[w1.s]), a.resident ? 0u : w1.ph, limit);
+                    ok = ok && warp_pair_wait(smem_u32(&bars.gempty[b]), ((uint32_t)(q >> 1) & 1u) ^ 1u, limit);
                     if (!ok) {
                         failed = true;
                         break;
@@ -195,8 +187,8 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                 }
                 if (q > 0) {   // the last product's part of chunk q - 1
                     const int p = q - 1, b = p & 1, y = i2 & 1;
-                    bool ok = c2 || all_wait_cluster(smem_u32(&bars.yempty[y]), ((uint32_t)(i2 >> 1) & 1u) ^ 1u, limit);
-                    ok = ok && all_wait_cluster(smem_u32(&bars.hready[b]), (uint32_t)(p >> 1) & 1u, limit);
+                    bool ok = c2 || warp_pair_wait(smem_u32(&bars.yempty[y]), ((uint32_t)(i2 >> 1) & 1u) ^ 1u, limit);
+                    ok = ok && warp_pair_wait(smem_u32(&bars.hready[b]), (uint32_t)(p >> 1) & 1u, limit);
                     if (!ok) {
                         failed = true;
                         break;
@@ -225,11 +217,12 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
         uint8_t *hbuf = sh + grp * 16384, *stage = stg + e * 2048;
         const uint32_t gempty = map_rank(smem_u32(&bars.gempty[grp]), 0), hready = map_rank(smem_u32(&bars.hready[grp]), 0);
         const int total = my * a.chunks;
+        float *vec = vecs[e];
 
         // output rows of this pair's i-th tile: bias, residual, store
         auto drain = [&](int i) {
             const int y = i & 1;
-            if (!all_wait(smem_u32(&bars.yfull[y]), (uint32_t)(i >> 1) & 1u, limit)) {
+            if (!warp_pair_wait(smem_u32(&bars.yfull[y]), (uint32_t)(i >> 1) & 1u, limit)) {
                 failed = true;
                 return;
             }
@@ -272,7 +265,9 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
 #pragma unroll 1
         for (int q = grp; q < total && !failed; q += FUSED_GROUPS) {
             const uint32_t use = (uint32_t)(q >> 1) & 1u;
-            if (!all_wait(smem_u32(&bars.gfull[grp]), use, limit)) {
+            const int f0 = c * FUSED_CHUNK + half * 32;
+            const float bg = lane_value(a.bg, f0 + lane, a.F), bu = lane_value(a.bu, f0 + lane, a.F);
+            if (!warp_pair_wait(smem_u32(&bars.gfull[grp]), use, limit)) {
                 failed = true;
                 break;
             }
@@ -280,25 +275,23 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             float g[32], v[32];
             tmem_ld32(tmem + 128 * grp + lanes + half * 32, g);
             tmem_ld32(tmem + 128 * grp + lanes + 64 + half * 32, v);
+            vec[lane] = bg;
+            vec[32 + lane] = bu;
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(gempty);
-            const int f0 = c * FUSED_CHUNK + half * 32;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int f = f0 + 8 * s;
                 float *gq = g + 8 * s, *vq = v + 8 * s;
                 float b[8];
                 if (a.bg) {
-                    load8(a.bg, f, a.F, b);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) gq[k] += b[k];
+                    spread8(vec, s, b);
+                    add8(gq, b);
                 }
                 if (a.bu) {
-                    load8(a.bu, f, a.F, b);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) vq[k] += b[k];
+                    spread8(vec + 32, s, b);
+                    add8(vq, b);
                 }
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
@@ -307,7 +300,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                 }
             }
             // the MMAs that read this buffer two chunks ago are done
-            if (!all_wait(smem_u32(&bars.hfree[grp]), use ^ 1u, limit)) {
+            if (!warp_pair_wait(smem_u32(&bars.hfree[grp]), use ^ 1u, limit)) {
                 failed = true;
                 break;
             }
@@ -335,7 +328,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
         }
         if (!failed && pending >= 0) drain(pending);
         const int mine = (total - grp + 1) / FUSED_GROUPS;   // chunks of this group
-        if (!failed && mine > 0) failed = !all_wait(smem_u32(&bars.hfree[grp]), (uint32_t)(mine - 1) & 1u, limit);
+        if (!failed && mine > 0) failed = !warp_pair_wait(smem_u32(&bars.hfree[grp]), (uint32_t)(mine - 1) & 1u, limit);
         if (lane == 0) bulk_wait_all();
     }
     if (failed && lane == 0) atomicOr(a.st.err, ERR_TIMEOUT);
@@ -362,7 +355,7 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     a.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
     a.slot_bytes = a.xb * 8192 + a.n2 * 64;
     const int fixed = 2 * a.xb * 16384 + 2 * 16384 + FUSED_GROUPS * FUSED_GROUP_WARPS * 2048;
-    const int room = 226 * 1024 - 1024 - fixed;   // (1 KB for the barriers, 1 KB of alignment)
+    const int room = 222 * 1024 - 1024 - fixed;   // (5 KB for the barriers and biases, 1 KB of alignment)
     a.slots = room / a.slot_bytes;
     if (a.slots > FUSED_SLOTS) a.slots = FUSED_SLOTS;
     if (a.slots > a.chunks) a.slots = a.chunks;
@@ -390,7 +383,7 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready[gelu].load() & bit)) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024)) != cudaSuccess) return e;
         ready[gelu].fetch_or(bit);
     }
     return launch_maybe_overlapped(kern, dim3(2u * (unsigned)a.np), dim3(FUSED_THREADS), smem, stream, 1, a);

@@ -20,12 +20,15 @@
 //                           a range of a tile's K blocks)
 //   STAGES, STAGE_BYTES     the ring
 //   EPI                     epilogue warps (8, or 16 where arithmetic binds)
-//   STAGING                 bytes of store staging per epilogue warp
+//   STAGING                 bytes of shared memory per epilogue warp, laid out by
+//                           the epilogue (staged stores, vectors)
 //   SEGS                    accumulation segments of a unit (each a K loop
 //                           into one slot of TMEM columns)
 //   slot(seg, n), slot_col(slot), slot_use(seg, n)   the slot of the n-th unit
 //                           of this pair, its first column, how often it was used
-//   kblocks(a, u, seg), tx(a, u, seg), load(...), mma(...), epilogue(...)
+//   kblocks(a, u, seg), tx(a, u, seg), load(...), mma(...)
+//   Pre, prefetch(...), epilogue(...)   what an epilogue thread fetches before
+//                           the accumulators are ready, and the epilogue
 #pragma once
 
 #include <atomic>
@@ -54,35 +57,32 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Arrival on a barrier of either CTA.  What is handed over so lies in TMEM
+// (ordered by the tcgen05 fences) or is read by the MMAs through the async
+// proxy (ordered by the proxy fence): no generic access of the other CTA hangs
+// on it, and the cluster-wide release, which waits for all of a thread's
+// earlier writes, is not needed (it cost the narrow forward 20 of 117 us).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Bounded waits as mbar_wait, for waits that are rarely over before they begin:
+// Bounded wait as mbar_wait, for waits that are rarely over before they begin:
 // the suspending form at once, the clock (slow to read) only if it ran out.
-// CLUSTER: also acquires what the other CTA's threads released.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
-    uint32_t ok;
     uint64_t t0 = 0;
 #pragma unroll 1
     while (true) {
-        if (CLUSTER)
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                "selp.b32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(bar), "r"(parity), "r"(1000000u)
-                : "memory");
-        else
-            ok = mbar_try_wait_hint(bar, parity, 1000000u);
-        if (ok) return true;
+        if (mbar_try_wait_hint(bar, parity, 1000000u)) return true;
         const uint64_t t = global_timer_ns();
         if (!t0) t0 = t;
         else if (t - t0 > limit_ns) return false;
     }
+}
+// The same for a whole warp, with one outcome.
+__device__ __forceinline__ bool warp_pair_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    return __all_sync(0xffffffffu, pair_wait(bar, parity, limit_ns));
 }
 // True in one lane of a converged warp (the same one every time).
 __device__ __forceinline__ bool elect_one()
@@ -273,7 +273,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
                 const uint32_t tx = P::tx(a, un, seg);
 #pragma unroll 1
                 for (int kb = 0; kb < kb_n; ++kb) {
-                    if (!__all_sync(0xffffffffu, pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns))) {
+                    if (!warp_pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns)) {
                         failed = true;
                         break;
                     }
@@ -292,7 +292,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         // every stage given back: no commit is on its way to this CTA's
         // barriers when it ends
         for (int k = 0; k < P::STAGES && k < issued && !failed; ++k) {
-            failed = !__all_sync(0xffffffffu, pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns));
+            failed = !warp_pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns);
             if (++s == P::STAGES) {
                 s = 0;
                 ph ^= 1u;
@@ -323,8 +323,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
 #pragma unroll 1
                 for (int seg = 0; seg < P::SEGS && !failed; ++seg) {
                     const int slot = P::slot(seg, n), kb_n = P::kblocks(a, un, seg);
-                    if (!__all_sync(0xffffffffu, pair_wait<true>(tempty + 8 * slot, (P::slot_use(seg, n) & 1) ^ 1,
-                                                                 a.st.wait_ns))) {
+                    if (!warp_pair_wait(tempty + 8 * slot, (P::slot_use(seg, n) & 1) ^ 1,
+                                                                 a.st.wait_ns)) {
                         failed = true;
                         break;
                     }
@@ -332,7 +332,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
                     const uint32_t d = tmem + P::slot_col(slot);
 #pragma unroll 1
                     for (int kb = 0; kb < kb_n; ++kb) {
-                        if (!__all_sync(0xffffffffu, pair_wait(full + 8 * s, ph, a.st.wait_ns))) {
+                        if (!warp_pair_wait(full + 8 * s, ph, a.st.wait_ns)) {
                             failed = true;
                             break;
                         }
@@ -353,14 +353,13 @@ pair_kernel(const __grid_constant__ typename P::Args a)
     } else {
         const int quad = warp & 3, part = (warp - 2) >> 2;   // (part: of the columns)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        uint8_t *stage = staging + (warp - 2) * P::STAGING;
         int n = 0;
         for (; n < units && !failed; ++n) {
             const typename P::Unit un = P::decode(a, pair, n);
             // (warp-uniform outcome: the TMEM loads below are warp-collective)
+            const typename P::Pre pre = P::prefetch(a, un, rank, quad, part, lane);
             for (int seg = 0; seg < P::SEGS && !failed; ++seg)
-                failed = !__all_sync(0xffffffffu, pair_wait(tfull + 8 * P::slot(seg, n), P::slot_use(seg, n) & 1,
-                                                            a.st.wait_ns));
+                failed = !warp_pair_wait(tfull + 8 * P::slot(seg, n), P::slot_use(seg, n) & 1, a.st.wait_ns);
             if (failed) break;
             tc_fence_after();
             auto release = [&]() {
@@ -370,7 +369,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
                     for (int seg = 0; seg < P::SEGS; ++seg)
                         mbar_arrive_cluster(map_rank(tempty + 8 * P::slot(seg, n), 0));
             };
-            P::epilogue(a, un, n, rank, quad, part, lane, t_lane, stage, release);
+            P::epilogue(a, un, pre, n, rank, warp - 2, quad, part, lane, t_lane, staging, release);
         }
         // the staged stores have read shared memory, and are complete
         if (lane == 0) bulk_wait_all();
