@@ -158,8 +158,11 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             const int total = my * a.chunks;
             int i1 = 0, c1 = 0, i2 = 0, c2 = 0;   // tile (of this pair) and chunk of the two products
             RingPos w1, w2;
+            // g | u run two chunks ahead of the last product: their buffer is
+            // free as soon as its group has read it, and the group's next chunk
+            // is there when it is done with this one
 #pragma unroll 1
-            for (int q = 0; q <= total && !failed; ++q) {
+            for (int q = 0; q < total + 2 && !failed; ++q) {
                 if (q < total) {   // g | u of chunk q
                     const int b = q & 1;
                     bool ok = c1 || warp_pair_wait(smem_u32(&bars.xfull[i1 & 1]), (uint32_t)(i1 >> 1) & 1u, limit);
@@ -185,8 +188,8 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                         if (a.resident) w1 = RingPos();
                     }
                 }
-                if (q > 0) {   // the last product's part of chunk q - 1
-                    const int p = q - 1, b = p & 1, y = i2 & 1;
+                if (q >= 2) {   // the last product's part of chunk q - 2
+                    const int p = q - 2, b = p & 1, y = i2 & 1;
                     bool ok = c2 || warp_pair_wait(smem_u32(&bars.yempty[y]), ((uint32_t)(i2 >> 1) & 1u) ^ 1u, limit);
                     ok = ok && warp_pair_wait(smem_u32(&bars.hready[b]), (uint32_t)(p >> 1) & 1u, limit);
                     if (!ok) {
@@ -236,20 +239,20 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                 if (c0 >= a.C) break;
                 float v[32];
                 tmem_ld32(TY + 128 * y + lanes + c0, v);
+                __syncwarp();   // (the vector's last readers are done)
+                vec[lane] = lane_value(a.bd, c0 + lane, a.C);
                 staging_free(lane);
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float b[8];
                     if (a.bd) {
-                        load8(a.bd, c0 + 8 * q, a.C, b);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[8 * q + k] += b[k];
+                        spread8(vec, q, b);
+                        add8(v + 8 * q, b);
                     }
                     if (res) {
                         load8(res, c0 + 8 * q, a.C, b);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[8 * q + k] += b[k];
+                        add8(v + 8 * q, b);
                     }
                     *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(v + 8 * q);
                 }
@@ -275,6 +278,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             float g[32], v[32];
             tmem_ld32(tmem + 128 * grp + lanes + half * 32, g);
             tmem_ld32(tmem + 128 * grp + lanes + 64 + half * 32, v);
+            __syncwarp();
             vec[lane] = bg;
             vec[32 + lane] = bu;
             tmem_wait_ld();
@@ -325,6 +329,16 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             if (i > tile)
                 for (int t = tile; t < i; ++t)
                     if ((t & 1) == grp) pending = t;
+            if (pending >= 0 && a.residual && half * 64 < a.C) {
+                // its residual on the way meanwhile (a row's 64 columns: one or two lines)
+                const int64_t row = (int64_t)(pair + pending * a.np) * 256 + (int)rank * 128 + quad * 32 + lane;
+                if (row < a.rows) {
+                    const bf16 *r = a.residual + row * a.C + half * 64;
+                    const int last = (a.C - half * 64 < 64 ? a.C - half * 64 : 64) - 1;
+                    prefetch_l1(r);
+                    prefetch_l1(r + last);
+                }
+            }
         }
         if (!failed && pending >= 0) drain(pending);
         const int mine = (total - grp + 1) / FUSED_GROUPS;   // chunks of this group
@@ -359,7 +373,7 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     a.slots = room / a.slot_bytes;
     if (a.slots > FUSED_SLOTS) a.slots = FUSED_SLOTS;
     if (a.slots > a.chunks) a.slots = a.chunks;
-    a.resident = a.slots == a.chunks;
+    a.resident = a.slots == a.chunks;   // (three slots at least otherwise: g | u run two chunks ahead)
     const size_t smem = 1024 + (size_t)fixed + (size_t)a.slots * a.slot_bytes;
     cudaError_t e;
     if ((e = make_tensor_map(&a.x, type, x, C, rows, (int64_t)C * 2, 64, 128, 128)) != cudaSuccess) return e;
