@@ -222,6 +222,21 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
         const int total = my * a.chunks;
         float *vec = vecs[e];
 
+        // the residual's box j of this pair's i-th tile on its way into the warp's
+        // staging, four lanes a row (a row a lane, 32 lines an instruction, took
+        // 16 us of 67 at 200,704 x 96)
+        auto fetch_residual = [&](int i, int j) {
+            const int row0 = (pair + i * a.np) * 256 + (int)rank * 128 + quad * 32, col = half * 64 + 32 * j + 8 * (lane & 3);
+            staging_free(lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 8 * k + (lane >> 2);
+                const bool ok = row0 + r < a.rows && col < a.C;
+                cp_async16(smem_u32(stage) + sw64_offset(r, lane & 3),
+                           ok ? a.residual + (int64_t)(row0 + r) * a.C + col : a.residual, ok ? 16u : 0u);
+            }
+            cp_async_commit();
+        };
         // output rows of this pair's i-th tile: bias, residual, store
         auto drain = [&](int i) {
             const int y = i & 1;
@@ -231,8 +246,6 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             }
             tc_fence_after();
             const int row0 = (pair + i * a.np) * 256 + (int)rank * 128 + quad * 32;
-            const bool row_ok = row0 + lane < a.rows;
-            const bf16 *res = a.residual && row_ok ? a.residual + (int64_t)(row0 + lane) * a.C : nullptr;
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 const int c0 = half * 64 + 32 * j;
@@ -241,7 +254,13 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                 tmem_ld32(TY + 128 * y + lanes + c0, v);
                 __syncwarp();   // (the vector's last readers are done)
                 vec[lane] = lane_value(a.bd, c0 + lane, a.C);
-                staging_free(lane);
+                if (a.residual) {
+                    if (j) fetch_residual(i, j);   // (the first box: fetched a chunk ago)
+                    cp_async_wait<0>();
+                } else if (lane == 0) {
+                    bulk_wait_read();
+                }
+                __syncwarp();
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -250,11 +269,12 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                         spread8(vec, q, b);
                         add8(v + 8 * q, b);
                     }
-                    if (res) {
-                        load8(res, c0 + 8 * q, a.C, b);
+                    uint4 *at = reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q));
+                    if (a.residual) {
+                        load8(reinterpret_cast<const bf16 *>(at), 0, 8, b);
                         add8(v + 8 * q, b);
                     }
-                    *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(v + 8 * q);
+                    *at = pack8f(v + 8 * q);
                 }
                 store_box(&a.out, c0, row0, row0 < a.rows, stage, lane);
             }
@@ -265,11 +285,16 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
 
         int pending = -1;   // tile whose output this group has yet to drain
         int i = grp / a.chunks, c = grp % a.chunks;
+        float bg, bu;   // of this lane's hidden unit in this group's next chunk
+        auto fetch_biases = [&](int chunk) {
+            const int f = chunk * FUSED_CHUNK + half * 32 + lane;
+            bg = lane_value(a.bg, f, a.F);
+            bu = lane_value(a.bu, f, a.F);
+        };
+        fetch_biases(c);
 #pragma unroll 1
         for (int q = grp; q < total && !failed; q += FUSED_GROUPS) {
             const uint32_t use = (uint32_t)(q >> 1) & 1u;
-            const int f0 = c * FUSED_CHUNK + half * 32;
-            const float bg = lane_value(a.bg, f0 + lane, a.F), bu = lane_value(a.bu, f0 + lane, a.F);
             if (!warp_pair_wait(smem_u32(&bars.gfull[grp]), use, limit)) {
                 failed = true;
                 break;
@@ -281,6 +306,8 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             __syncwarp();
             vec[lane] = bg;
             vec[32 + lane] = bu;
+            // (the next chunk's, a chunk ahead)
+            fetch_biases((c + FUSED_GROUPS) % a.chunks);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
@@ -330,14 +357,9 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                 for (int t = tile; t < i; ++t)
                     if ((t & 1) == grp) pending = t;
             if (pending >= 0 && a.residual && half * 64 < a.C) {
-                // its residual on the way meanwhile (a row's 64 columns: one or two lines)
+                fetch_residual(pending, 0);
                 const int64_t row = (int64_t)(pair + pending * a.np) * 256 + (int)rank * 128 + quad * 32 + lane;
-                if (row < a.rows) {
-                    const bf16 *r = a.residual + row * a.C + half * 64;
-                    const int last = (a.C - half * 64 < 64 ? a.C - half * 64 : 64) - 1;
-                    prefetch_l1(r);
-                    prefetch_l1(r + last);
-                }
+                if (row < a.rows && half * 64 + 32 < a.C) prefetch_l2(a.residual + row * a.C + half * 64 + 32);
             }
         }
         if (!failed && pending >= 0) drain(pending);
