@@ -80,8 +80,8 @@ struct Product {
 };
 
 // The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
-// of K (+ bias + residual).  Block (t, y): cut tile t, every gridDim.y-th 2048
-// values.
+// of K (+ bias + residual), JOIN_BLOCKS blocks a tile.
+constexpr int JOIN_BLOCKS = 16;
 struct JoinArgs {
     const float *part;
     PairSplit split;
@@ -92,12 +92,10 @@ struct JoinArgs {
         int rows, cols, mt, nt, first;
     } p[3];
 };
-__global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__ JoinArgs a)
+__device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
 {
-    griddep_launch_dependents();
-    griddep_wait();
     const PairSplit &s = a.split;
-    const int c = blockIdx.x, t = s.full * s.np + c;
+    const int c = block / JOIN_BLOCKS, t = s.full * s.np + c;
     const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
     if (p0 == p1) return;   // (one pair had the whole tile and wrote it)
     const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
@@ -106,7 +104,7 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__
     const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / 8;
     const int64_t size = 256 * a.tn;
     const int first = s.slot(p0, c);
-    for (int e = blockIdx.y * 256 + threadIdx.x; e < 256 * per; e += gridDim.y * 256) {
+    for (int e = block % JOIN_BLOCKS * 256 + threadIdx.x; e < 256 * per; e += JOIN_BLOCKS * 256) {
         const int row = m * 256 + e / per, col = n * a.tn + e % per * 8;
         if (row >= rows || col >= cols) continue;
         float v[8], w[8];
@@ -129,6 +127,102 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__
         }
         *reinterpret_cast<uint4 *>(a.p[i].out + at) = pack8f(v);
     }
+}
+
+// Column sums of up to three matrices [rows, cols] (fp32 or bf16): a block sums
+// every splits-th group of 32 rows of 64 columns into a partial row; then the
+// partial rows are added, all in a fixed order.
+struct ColumnSums {
+    struct {
+        const float *f;   // fp32, or
+        const bf16 *b;
+        bf16 *out;
+        float *part;      // [splits, cols]
+        int64_t rows;
+        int cols;
+    } m[3];
+    int n, splits;
+    int blocks(int i) const { return (m[i].cols + 63) / 64 * splits; }
+};
+__device__ __forceinline__ void column_partials(const ColumnSums &a, int block)
+{
+    __shared__ float sum[32][65];
+    int z = 0;
+    for (; z + 1 < a.n && block >= (a.m[z].cols + 63) / 64 * a.splits; ++z) block -= (a.m[z].cols + 63) / 64 * a.splits;
+    const auto &m = a.m[z];
+    const int cols = m.cols, c0 = block / a.splits * 64, y = block % a.splits;
+    const int c = c0 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t i = (int64_t)y * 32 + r; i < m.rows; i += (int64_t)a.splits * 32) {
+            float w[8];
+            if (m.f) load8(m.f + i * cols, c, cols, w);
+            else load8(m.b + i * cols, c, cols, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[r][(threadIdx.x & 7) * 8 + e] = v[e];
+    __syncthreads();
+    if (threadIdx.x < 64 && c0 + (int)threadIdx.x < cols) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t += sum[i][threadIdx.x];
+        m.part[(int64_t)y * cols + c0 + threadIdx.x] = t;
+    }
+}
+
+// What is left of a call when its products are done, as one launch: the cut
+// tiles of up to two of them, and the first half of the column sums.  (As
+// kernels of their own behind each product they took 27 us of the 151 of the
+// backward at 12544 x 512 x 1368, most of it latency.)
+struct FinishArgs {
+    JoinArgs join[2];
+    int joins[2];   // blocks of each
+    ColumnSums cs;
+};
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    int b = blockIdx.x;
+    if (b < a.joins[0]) {
+        join_tiles(a.join[0], b);
+        return;
+    }
+    b -= a.joins[0];
+    if (b < a.joins[1]) {
+        join_tiles(a.join[1], b);
+        return;
+    }
+    column_partials(a.cs, b - a.joins[1]);
+}
+cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launches)
+{
+    int blocks = a.joins[0] + a.joins[1];
+    for (int i = 0; i < a.cs.n; ++i) blocks += a.cs.blocks(i);
+    if (!blocks) return cudaSuccess;
+    ++*launches;
+    return launch_maybe_overlapped(finish_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, 1, a);
+}
+__global__ void __launch_bounds__(1024) column_finish_kernel(const __grid_constant__ ColumnSums a)
+{
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    griddep_launch_dependents();
+    griddep_wait();
+    const auto &m = a.m[blockIdx.y];
+    const int c = blockIdx.x * 32 + lane;
+    float v = 0.f;
+    if (c < m.cols)
+        for (int s = w; s < a.splits; s += 32) v += m.part[(int64_t)s * m.cols + c];
+    part[w][lane] = v;
+    __syncthreads();
+    v = part[lane][w];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && (int)blockIdx.x * 32 + w < m.cols) m.out[blockIdx.x * 32 + w] = __float2bfloat16_rn(v);
 }
 
 struct ProductsPlan {
@@ -174,11 +268,11 @@ ProductsPlan plan_products(const Product *p, int n)
 
 template <int TN, bool A_MN, bool B_MN>
 cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                              cudaStream_t stream, int *launches)
+                              cudaStream_t stream, int *launches, FinishArgs *fin, int slot)
 {
     typename GemmPolicy<TN, A_MN, B_MN>::Args a;
     memset(&a, 0, sizeof(a));
-    JoinArgs r{};
+    JoinArgs &r = fin->join[slot];
     cudaError_t e;
     int first = 0;
     for (int i = 0; i < 3; ++i) {
@@ -216,81 +310,20 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
         if (e != cudaSuccess) return e;
     }
     ++*launches;
-    e = launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
-    if (e != cudaSuccess || !pl.split.cut) return e;
     r.part = part;
     r.tn = TN;
-    ++*launches;
-    return launch_maybe_overlapped(join_tiles_kernel, dim3((unsigned)pl.split.cut, TN / 16), dim3(256), 0, stream, 1, r);
+    fin->joins[slot] = pl.split.cut * JOIN_BLOCKS;
+    return launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
 }
 
+// Queues the products; what is left to do for their cut tiles goes into
+// fin->join[slot].
 template <bool A_MN, bool B_MN>
 cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                            cudaStream_t stream, int *launches)
+                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot)
 {
-    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches)
-                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches);
-}
-
-// Column sums of up to three matrices [rows, cols] (fp32 or bf16): block (x, y,
-// z) sums every gridDim.y-th group of 32 rows of 64 columns of matrix z into a
-// partial row; then the partial rows are added, all in a fixed order.
-struct ColumnSums {
-    struct {
-        const float *f;   // fp32, or
-        const bf16 *b;
-        bf16 *out;
-        float *part;      // [splits, cols]
-        int64_t rows;
-        int cols;
-    } m[3];
-    int splits;
-};
-__global__ void __launch_bounds__(256) column_partials_kernel(const __grid_constant__ ColumnSums a)
-{
-    __shared__ float sum[32][65];
-    griddep_launch_dependents();
-    griddep_wait();
-    const auto &m = a.m[blockIdx.z];
-    const int cols = m.cols, c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
-    if ((int)blockIdx.x * 64 >= cols) return;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < cols) {
-#pragma unroll 4
-        for (int64_t i = (int64_t)blockIdx.y * 32 + r; i < m.rows; i += (int64_t)gridDim.y * 32) {
-            float w[8];
-            if (m.f) load8(m.f + i * cols, c, cols, w);
-            else load8(m.b + i * cols, c, cols, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += w[e];
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[r][(threadIdx.x & 7) * 8 + e] = v[e];
-    __syncthreads();
-    if (threadIdx.x < 64 && (int)(blockIdx.x * 64 + threadIdx.x) < cols) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t += sum[i][threadIdx.x];
-        m.part[(int64_t)blockIdx.y * cols + blockIdx.x * 64 + threadIdx.x] = t;
-    }
-}
-__global__ void __launch_bounds__(1024) column_finish_kernel(const __grid_constant__ ColumnSums a)
-{
-    __shared__ float part[32][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    griddep_launch_dependents();
-    griddep_wait();
-    const auto &m = a.m[blockIdx.y];
-    const int c = blockIdx.x * 32 + lane;
-    float v = 0.f;
-    if (c < m.cols)
-        for (int s = w; s < a.splits; s += 32) v += m.part[(int64_t)s * m.cols + c];
-    part[w][lane] = v;
-    __syncthreads();
-    v = part[lane][w];
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0 && (int)blockIdx.x * 32 + w < m.cols) m.out[blockIdx.x * 32 + w] = __float2bfloat16_rn(v);
+    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot)
+                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot);
 }
 
 // Workspace layout: bytes of each part, 1 KB aligned.
@@ -416,7 +449,9 @@ int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, con
         e = launch_few_down(hidden, hidden_ld(h->F), rows, (const bf16 *)Wd, (const bf16 *)bd, (const bf16 *)residual,
                             (bf16 *)out, h->C, h->F, st, stream);
     } else if (e == cudaSuccess) {
-        e = launch_products<false, false>(&down, pl, part, st, stream, &h->last_launches);
+        FinishArgs fin{};
+        e = launch_products<false, false>(&down, pl, part, st, stream, &h->last_launches, &fin, 0);
+        if (e == cudaSuccess) e = launch_finish(fin, stream, &h->last_launches);
     }
     const int rc2 = ows_end(&h->ws, stream, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
@@ -569,18 +604,19 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     dw[1].d = (bf16 *)g->dWu;
     dw[2].d = (bf16 *)g->dWd;
     const ProductsPlan px = plan_products(&dxp, 1), pw = plan_products(dw, 3);
-    const size_t part_bytes = px.part_bytes > pw.part_bytes ? px.part_bytes : pw.part_bytes;
     // bias gradients: dg's and du's sums over each warp's 32 rows come from the
     // recompute kernel
-    ColumnSums cs{};
+    FinishArgs fin{};
+    ColumnSums &cs = fin.cs;
     const int row_blocks = ceil_div(rows, 256) * 8;
     cs.splits = ceil_div(rows, 256) < 64 ? ceil_div(rows, 256) : 64;
-    int sums = 0, most = 0;
+    int most = 0;
     const size_t row_sums = g->dbg || g->dbu ? (size_t)row_blocks * h->F * sizeof(float) : 0;
     const size_t hid = (size_t)rows * hidden_ld(h->F) * 2;
     Carve size(nullptr);
     for (int i = 0; i < 3; ++i) size.take(hid);
-    size.take(part_bytes);
+    size.take(px.part_bytes);
+    size.take(pw.part_bytes);
     for (int i = 0; i < 2; ++i) size.take(row_sums);
     size.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
     void *ws = nullptr;
@@ -588,7 +624,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     if ((rc = ows_begin(&h->ws, size.used, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
     Carve carve(ws);
     bf16 *hidden = (bf16 *)carve.take(hid), *dg = (bf16 *)carve.take(hid), *du = (bf16 *)carve.take(hid);
-    float *part = (float *)carve.take(part_bytes);
+    float *x_part = (float *)carve.take(px.part_bytes), *w_part = (float *)carve.take(pw.part_bytes);
     float *dg_sums = (float *)carve.take(row_sums), *du_sums = (float *)carve.take(row_sums);
     float *sum_part = (float *)carve.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
     dxp.a[0] = dw[0].a[0] = dg;
@@ -628,12 +664,12 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     };
     h->last_launches = 1;
     cudaError_t e = h->act == SWIN_BLOCK_GATED_SILU ? grad(GradPolicy<ACT_SILU>{}) : grad(GradPolicy<ACT_GELU>{});
-    if (e == cudaSuccess) e = launch_products<false, true>(&dxp, px, part, st, s, &h->last_launches);
-    if (e == cudaSuccess) e = launch_products<true, true>(dw, pw, part, st, s, &h->last_launches);
+    if (e == cudaSuccess) e = launch_products<false, true>(&dxp, px, x_part, st, s, &h->last_launches, &fin, 0);
+    if (e == cudaSuccess) e = launch_products<true, true>(dw, pw, w_part, st, s, &h->last_launches, &fin, 1);
     bf16 *out[3] = {(bf16 *)g->dbg, (bf16 *)g->dbu, (bf16 *)g->dbd};
     for (int i = 0; i < 3; ++i) {
         if (!out[i]) continue;
-        auto &m = cs.m[sums++];
+        auto &m = cs.m[cs.n++];
         m.f = i == 0 ? dg_sums : i == 1 ? du_sums : nullptr;
         m.b = (const bf16 *)dy;
         m.out = out[i];
@@ -643,12 +679,10 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         sum_part += (size_t)cs.splits * m.cols;
         if (m.cols > most) most = m.cols;
     }
-    if (e == cudaSuccess && sums) {
-        h->last_launches += 2;
-        e = launch_maybe_overlapped(column_partials_kernel, dim3(ceil_div(most, 64), cs.splits, sums), dim3(256), 0, s, 1,
-                                    cs);
-        if (e == cudaSuccess)
-            e = launch_maybe_overlapped(column_finish_kernel, dim3(ceil_div(most, 32), sums), dim3(1024), 0, s, 1, cs);
+    if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
+    if (e == cudaSuccess && cs.n) {
+        ++h->last_launches;
+        e = launch_maybe_overlapped(column_finish_kernel, dim3(ceil_div(most, 32), cs.n), dim3(1024), 0, s, 1, cs);
     }
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
