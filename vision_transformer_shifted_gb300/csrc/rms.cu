@@ -7,7 +7,8 @@
 // them.  Rows of up to 1024 channels lie on part of a warp (a power of two of
 // lanes, at most four 16-byte pieces each: their loads are all in flight at
 // once and the statistics need shuffles only); longer rows take a block each.
-// (The backward, with three inputs, at most two pieces a lane.)
+// (The backward, with three inputs, at most three pieces a lane.)
+#include <climits>
 #include <cmath>
 #include <cuda_fp8.h>
 #include <new>
@@ -68,25 +69,27 @@ __device__ __forceinline__ float row_reduce(float v, int lpr, float *red)
     return v;
 }
 
-// The sums of a and b over the lanes of a row.
-template <bool BLOCK>
-__device__ __forceinline__ void row_sum2(float &a, float &b, int lpr, float2 *red)
+// The sums of a and b over `lanes` lanes of a warp.
+__device__ __forceinline__ void lane_sum2(float &a, float &b, int lanes)
 {
-    const int lanes = BLOCK ? 32 : lpr;
     for (int o = lanes >> 1; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
         b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-    if (BLOCK) {
-        const int warps = blockDim.x >> 5;
-        __syncthreads();   // (the previous row's sums have been read)
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        a = b = 0.f;
-        for (int w = 0; w < warps; ++w) {
-            a += red[w].x;
-            b += red[w].y;
-        }
+}
+// The same over group `group` of a block, of `threads` threads that meet at a
+// barrier of their own; red: two rows of 16 sums a group, used in turn.
+__device__ __forceinline__ void group_sum2(float &a, float &b, int threads, int group, int turn, float2 *red)
+{
+    lane_sum2(a, b, 32);
+    const int warps = threads >> 5, warp = (threadIdx.x - group * threads) >> 5;
+    red += (2 * group + (turn & 1)) * 16;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    a = b = 0.f;
+    for (int w = 0; w < warps; ++w) {
+        a += red[w].x;
+        b += red[w].y;
     }
 }
 
@@ -214,24 +217,52 @@ struct RmsBwdArgs {
     float *partial;   // [gridDim.x, C]: each block's share of dgamma
     int rows, chunks;
     float inv_c, eps;
-    int lpr;
+    int lanes;        // of a row: of a warp, or (wide rows) threads
 };
 
-// dx = r (a - n mean(a n)) + dsum with n = s r, a = dy gamma.  A block walks
-// rows blockIdx.x, blockIdx.x + gridDim.x, ... (groups of rows where a row is
-// part of a warp); each thread keeps the columns it owns of dgamma in
-// registers over its rows, and the block writes one partial row at the end.
-template <int CPL, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? (CPL > 2 ? 1 : 2) : 3) rms_backward_kernel(RmsBwdArgs a)
+// One thread's piece (eight channels) of a row in the backward, dx = r (a - n
+// mean(a n)) + dsum with n = s r, a = dy gamma.  First its shares of sum s^2
+// and sum a s:
+__device__ __forceinline__ void piece_sums(const uint4 &s, const uint4 &d, const uint4 &g, float &sq, float &dot)
 {
-    extern __shared__ float part[];   // !BLOCK: [8 warps][C]
-    __shared__ float2 red[16];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int step = BLOCK ? (int)blockDim.x : a.lpr;
-    const int li = BLOCK ? (int)threadIdx.x : lane % a.lpr;
+    float v[8], y[8], w[8];
+    unpack8(s, v);
+    unpack8(d, y);
+    unpack8(g, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        sq = fmaf(v[e], v[e], sq);
+        dot = fmaf(y[e] * w[e], v[e], dot);
+    }
+}
+// then, with q = mean(a n) r (so that n mean(a n) = s q), dx and its terms of dgamma.
+__device__ __forceinline__ uint4 piece_grad(const uint4 &s, const uint4 &d, const uint4 &g, const uint4 &m, float r,
+                                            float q, float (&acc)[8])
+{
+    float v[8], y[8], w[8], b[8];
+    unpack8(s, v);
+    unpack8(d, y);
+    unpack8(g, w);
+    unpack8(m, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        acc[e] = fmaf(y[e], v[e] * r, acc[e]);
+        b[e] = fmaf(r, y[e] * w[e] - v[e] * q, b[e]);
+    }
+    return pack8(b);
+}
+
+// Rows on part of a warp: a block takes 8 * (32 / lanes) rows together, then the
+// ones gridDim.x on.  Each thread keeps the columns it owns of dgamma in
+// registers over its rows; the block writes one partial row at the end.
+template <int CPL>
+__global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsBwdArgs a)
+{
+    extern __shared__ float part[];   // [8 warps][C]
     griddep_launch_dependents();
     griddep_wait();
-    const int rpw = BLOCK ? 1 : 32 / a.lpr, rpb = BLOCK ? 1 : rpw * (int)(blockDim.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = a.lanes, li = lane % step;
+    const int rpw = 32 / step, rpb = 8 * rpw;
     float acc[CPL][8];
     uint4 g[CPL];
 #pragma unroll
@@ -242,7 +273,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? (CPL > 2 ? 1 : 2) :
         for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
     }
     for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
-        const int64_t row = BLOCK ? r0 : r0 + warp * rpw + lane / a.lpr;
+        const int64_t row = r0 + warp * rpw + lane / step;
         const bool row_ok = row < a.rows;
         const int64_t base = row * a.chunks * 8;
         uint4 s[CPL], d[CPL], m[CPL];
@@ -254,20 +285,10 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? (CPL > 2 ? 1 : 2) :
             d[k] = ok ? ld16(a.dy + base + c * 8) : make_uint4(0, 0, 0, 0);
             m[k] = ok && a.dsum ? ld16(a.dsum + base + c * 8) : make_uint4(0, 0, 0, 0);
         }
-        float sq = 0.f, dot = 0.f;   // sum s^2, sum a s
+        float sq = 0.f, dot = 0.f;
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            float v[8], y[8], w[8];
-            unpack8(s[k], v);
-            unpack8(d[k], y);
-            unpack8(g[k], w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sq = fmaf(v[e], v[e], sq);
-                dot = fmaf(y[e] * w[e], v[e], dot);
-            }
-        }
-        row_sum2<BLOCK>(sq, dot, a.lpr, red);
+        for (int k = 0; k < CPL; ++k) piece_sums(s[k], d[k], g[k], sq, dot);
+        lane_sum2(sq, dot, step);
         // (the packed values stay, their fp32 forms are made again: registers
         // kept across the sums would halve the rows in flight)
 #pragma unroll
@@ -277,55 +298,117 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? (CPL > 2 ? 1 : 2) :
             forget(g[k]);
             forget(m[k]);
         }
-        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps));
-        const float q = dot * a.inv_c * r * r;   // mean(a n) / s-scale: n mean(a n) = s q
+        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
-            float v[8], y[8], w[8], b[8];
-            unpack8(s[k], v);
-            unpack8(d[k], y);
-            unpack8(g[k], w);
-            unpack8(m[k], b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[k][e] = fmaf(y[e], v[e] * r, acc[k][e]);
-                b[e] = fmaf(r, y[e] * w[e] - v[e] * q, b[e]);
-            }
-            if (row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.dx + base + c * 8) = pack8(b);
+            const uint4 o = piece_grad(s[k], d[k], g[k], m[k], r, q, acc[k]);
+            if (row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.dx + base + c * 8) = o;
         }
     }
+    // the warp's rows, then the block's warps
     const int C = a.chunks * 8;
-    float *mine = a.partial + (int64_t)blockIdx.x * C;
-    if constexpr (BLOCK) {
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float v = acc[k][e];
+            for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < C; i += 256) {
+        float v = 0.f;
+        for (int w = 0; w < 8; ++w) v += part[w * C + i];
+        a.partial[(int64_t)blockIdx.x * C + i] = v;
+    }
+}
+
+// Wider rows: a group of warps a row, several groups a block (few blocks, since
+// each writes a partial row of dgamma that is read again).  Every thread
+// fetches its own pieces of the next DEPTH - 1 rows by asynchronous copies into
+// its own place in shared memory, so that the latency of HBM is paid once, not
+// once a row; 3001 x 2744: 20.8 us with the rows loaded as they come.
+template <int CPL, int DEPTH>
+__global__ void __launch_bounds__(CPL > 2 ? 512 : 1024, 1) rms_backward_wide_kernel(RmsBwdArgs a)
+{
+    extern __shared__ __align__(16) float part[];   // the pieces; at the end [C]
+    __shared__ float2 red[2 * 16 * 16];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int step = a.lanes, group = (int)threadIdx.x / step, li = (int)threadIdx.x - group * step;
+    const int rpb = (int)blockDim.x / step, C = a.chunks * 8, arrays = a.dsum ? 3 : 2;
+    // piece k of array i of stage d, this thread's
+    uint4 *mine = reinterpret_cast<uint4 *>(part) + threadIdx.x;
+    auto piece = [&](int d, int i, int k) { return mine + ((d * arrays + i) * CPL + k) * (int)blockDim.x; };
+    auto fetch = [&](int64_t row, int d) {
+        if (row < a.rows) {
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                const int c = li + k * step;
+                if (c >= a.chunks) continue;
+                const int64_t at = row * C + c * 8;
+                cp_async16(smem_u32(piece(d, 0, k)), a.s + at, 16);
+                cp_async16(smem_u32(piece(d, 1, k)), a.dy + at, 16);
+                if (a.dsum) cp_async16(smem_u32(piece(d, 2, k)), a.dsum + at, 16);
+            }
+        }
+        cp_async_commit();
+    };
+    const int64_t first = (int64_t)blockIdx.x * rpb + group, hop = (int64_t)gridDim.x * rpb;
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fetch(first + d * hop, d);
+    float acc[CPL][8];
+    uint4 g[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+        g[k] = c < a.chunks ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+    }
+    int d = 0, turn = 0;
+    for (int64_t row = first; row < a.rows; row += hop) {   // (the same for a group's threads)
+        fetch(row + (DEPTH - 1) * hop, d == 0 ? DEPTH - 1 : d - 1);
+        cp_async_wait<DEPTH - 1>();
+        float sq = 0.f, dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k)
+            if (li + k * step < a.chunks) piece_sums(*piece(d, 0, k), *piece(d, 1, k), g[k], sq, dot);
+        group_sum2(sq, dot, step, group, turn++, red);
+        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
             if (c >= a.chunks) continue;
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<float4 *>(mine + c * 8 + 4 * q) =
-                    make_float4(acc[k][4 * q], acc[k][4 * q + 1], acc[k][4 * q + 2], acc[k][4 * q + 3]);
+            forget(g[k]);
+            const uint4 m = a.dsum ? *piece(d, 2, k) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(a.dx + row * C + c * 8) =
+                piece_grad(*piece(d, 0, k), *piece(d, 1, k), g[k], m, r, q, acc[k]);
         }
-    } else {
-        // the warp's rows, then the block's warps
-#pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            const int c = li + k * step;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = acc[k][e];
-                for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
-            }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < C; i += blockDim.x) {
-            float v = 0.f;
-            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += part[w * C + i];
-            mine[i] = v;
-        }
+        if (++d == DEPTH) d = 0;
     }
+    __syncthreads();   // (every group is done with its pieces)
+    // the groups add theirs in turn
+    for (int t = 0; t < rpb; ++t) {
+        if (group == t)
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                const int c = li + k * step;
+                if (c >= a.chunks) continue;
+                float4 *p = reinterpret_cast<float4 *>(part + c * 8);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 old = t ? p[h] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    p[h] = make_float4(old.x + acc[k][4 * h], old.y + acc[k][4 * h + 1], old.z + acc[k][4 * h + 2],
+                                       old.w + acc[k][4 * h + 3]);
+                }
+            }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < C; i += blockDim.x) a.partial[(int64_t)blockIdx.x * C + i] = part[i];
 }
 
 // out[c] = the sum of n partial rows, in a fixed order: 32 columns a block, 32
@@ -350,34 +433,38 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
     if (lane == 0 && blockIdx.x * 32 + w < C) out[blockIdx.x * 32 + w] = v;
 }
 
-// How a row of `chunks` 16-byte pieces is laid out: on the fewest lanes of a
-// warp that leave each at most `most` pieces, or on a block of as few warps as
-// leave each thread at most `most` (more, up to four, where 512 threads are
-// not enough for that).
+// How a row of `chunks` 16-byte pieces is laid out: on part of a warp where at
+// most `most` pieces a lane suffice, by the count of pieces that leaves the
+// fewest lanes idle (the larger of equals: more loads in flight a thread); else on as few warps as leave each thread at most `most`
+// (more, up to four, where 512 threads are not enough for that).
 struct RowPlan {
     bool block;
-    int lpr, threads, cpl;
+    int lanes;     // of a row: of a warp, or threads
+    int cpl;
 };
 RowPlan plan_row(int chunks, int most)
 {
     RowPlan p{};
     if (chunks <= 32 * most) {
-        p.lpr = 1;
-        while (p.lpr * most < chunks) p.lpr <<= 1;
-        p.threads = 256;
-    } else {
-        p.block = true;
-        p.lpr = 32;
-        p.threads = ((chunks + most - 1) / most + 31) / 32 * 32;
-        if (p.threads > 512) p.threads = 512;
+        int idle = INT_MAX;
+        for (int cpl = 1; cpl <= most; ++cpl) {
+            int lanes = 1;
+            while (lanes * cpl < chunks) lanes <<= 1;
+            if (lanes > 32 || lanes * cpl - chunks > idle) continue;
+            idle = lanes * cpl - chunks;
+            p.lanes = lanes;
+            p.cpl = cpl;
+        }
+        return p;
     }
-    const int per = p.block ? p.threads : p.lpr;
-    p.cpl = (chunks + per - 1) / per;
+    p.block = true;
+    p.lanes = ((chunks + most - 1) / most + 31) / 32 * 32;
+    if (p.lanes > 512) p.lanes = 512;
+    p.cpl = (chunks + p.lanes - 1) / p.lanes;
     return p;
 }
-// The backward keeps three inputs and a sum a column: two pieces a thread
-// take 127 registers, four would spill.
-constexpr int FWD_PIECES = 4, BWD_PIECES = 2;
+constexpr int FWD_PIECES = 4, BWD_PIECES = 3, BWD_BLOCK_PIECES = 2;
+constexpr int MAX_GROUPS = 15;   // row groups of a block: a block has 16 barriers, and one is everybody's
 
 template <bool Q8>
 cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
@@ -385,14 +472,15 @@ cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
     // rows that leave SMs idle take as many threads as pieces: the latency of
     // one row counts then (1 x 2048: 5.6 us on 64 threads)
     const RowPlan p = plan_row(a.chunks, a.rows < sm_count() ? 1 : FWD_PIECES);
-    a.lpr = p.lpr;
-    const int64_t rpb = p.block ? 1 : (p.threads / 32) * (32 / p.lpr);
+    a.lpr = p.block ? 32 : p.lanes;
+    const int threads = p.block ? p.lanes : 256;
+    const int64_t rpb = p.block ? 1 : 8 * (32 / p.lanes);
     const unsigned grid = (unsigned)((a.rows + rpb - 1) / rpb);
 #define SWIN_RMS_CASE(n)                                                                      \
     case n:                                                                                   \
         return launch_maybe_overlapped(p.block ? rms_forward_kernel<n, true, Q8>              \
                                                : rms_forward_kernel<n, false, Q8>,            \
-                                       dim3(grid), dim3(p.threads), 0, stream, 1, a);
+                                       dim3(grid), dim3(threads), 0, stream, 1, a);
     switch (p.cpl) {
         SWIN_RMS_CASE(1)
         SWIN_RMS_CASE(2)
@@ -404,28 +492,65 @@ cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
 #undef SWIN_RMS_CASE
 }
 
-// Blocks of the backward: as many as the SMs hold at once, each walking its
-// share of the rows.
-int backward_grid(const RowPlan &p, int rows)
+// The backward's launch: as many blocks as the SMs hold at once, each walking
+// its share of the rows.  (Registers allow four blocks of 256 threads a SM with
+// one or two pieces a lane, two with three; a wide row's block is an SM's only
+// one, of up to 1024 threads with two pieces a thread, 512 with more, and its
+// pieces' stages are what shared memory holds: three of two arrays, two of three.)
+struct BwdPlan {
+    RowPlan row;
+    int threads, grid, depth;
+    size_t smem;
+};
+BwdPlan plan_backward(int rows, int C, bool with_dsum)
 {
-    const int64_t rpb = p.block ? 1 : (p.threads / 32) * (32 / p.lpr);
-    const int64_t want = (rows + rpb - 1) / rpb, per_sm = !p.block ? 3 : p.cpl <= 2 ? 1024 / p.threads : 1;
-    const int64_t most = sm_count() * per_sm;
-    return (int)(want < most ? want : most);
+    const int chunks = C / 8;
+    BwdPlan p{};
+    p.row = plan_row(chunks, chunks <= 32 * BWD_PIECES ? BWD_PIECES : BWD_BLOCK_PIECES);
+    const RowPlan &r = p.row;
+    int64_t rpb, per_sm;
+    if (r.block) {
+        const int groups = (r.cpl > 2 ? 512 : 1024) / r.lanes;
+        rpb = groups < MAX_GROUPS ? groups : MAX_GROUPS;
+        per_sm = 1;
+        p.threads = (int)rpb * r.lanes;
+        p.depth = with_dsum ? 2 : 3;
+        const int cpl = r.cpl < 2 ? 2 : r.cpl;   // (as the kernels are built)
+        p.smem = (size_t)p.threads * p.depth * (with_dsum ? 3 : 2) * cpl * 16;   // (at most 192 KB)
+        if (p.smem < (size_t)C * sizeof(float)) p.smem = (size_t)C * sizeof(float);
+    } else {
+        rpb = 8 * (32 / r.lanes);
+        per_sm = r.cpl > 2 ? 2 : 4;
+        p.threads = 256;
+        p.smem = (size_t)8 * C * sizeof(float);
+    }
+    const int64_t want = (rows + rpb - 1) / rpb, most = sm_count() * per_sm;
+    p.grid = (int)(want < most ? want : most);
+    return p;
 }
 
-cudaError_t launch_rms_backward(RmsBwdArgs a, int grid, const RowPlan &p, float *dgamma, cudaStream_t stream)
+cudaError_t launch_rms_backward(RmsBwdArgs a, const BwdPlan &p, float *dgamma, cudaStream_t stream)
 {
-    a.lpr = p.lpr;
+    const RowPlan &r = p.row;
+    a.lanes = r.lanes;
     const int C = a.chunks * 8;
-    const size_t smem = p.block ? 0 : (size_t)(p.threads / 32) * C * sizeof(float);
     void (*kern)(RmsBwdArgs) = nullptr;
-    if (p.block) kern = p.cpl <= 2 ? rms_backward_kernel<2, true> : p.cpl == 3 ? rms_backward_kernel<3, true> : rms_backward_kernel<4, true>;
-    else kern = p.cpl == 1 ? rms_backward_kernel<1, false> : rms_backward_kernel<2, false>;
-    const cudaError_t e = launch_maybe_overlapped(kern, dim3(grid), dim3(p.threads), smem, stream, 1, a);
+    if (!r.block)
+        kern = r.cpl == 1 ? rms_backward_kernel<1> : r.cpl == 2 ? rms_backward_kernel<2> : rms_backward_kernel<3>;
+    else if (p.depth == 2)
+        kern = r.cpl <= 2 ? rms_backward_wide_kernel<2, 2> : r.cpl == 3 ? rms_backward_wide_kernel<3, 2>
+                                                                        : rms_backward_wide_kernel<4, 2>;
+    else
+        kern = r.cpl <= 2 ? rms_backward_wide_kernel<2, 3> : r.cpl == 3 ? rms_backward_wide_kernel<3, 3>
+                                                                        : rms_backward_wide_kernel<4, 3>;
+    cudaError_t e;
+    if (r.block &&
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem)) != cudaSuccess)
+        return e;
+    e = launch_maybe_overlapped(kern, dim3(p.grid), dim3(p.threads), p.smem, stream, 1, a);
     if (e != cudaSuccess) return e;
     return launch_maybe_overlapped(column_sum_kernel, dim3((C + 31) / 32), dim3(1024), 0, stream, 1,
-                                   (const float *)a.partial, grid, C, dgamma);
+                                   (const float *)a.partial, p.grid, C, dgamma);
 }
 
 bool bad_pointer(const void *p, bool required)
@@ -565,11 +690,10 @@ int swin_block_rms_backward(swin_block_rms_t h, const void *s, int rows, const v
     int rc = bind_device(&h->device);
     if (rc != SWIN_WATTN_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    const RowPlan p = plan_row(h->C / 8, BWD_PIECES);
-    const int grid = backward_grid(p, rows);
+    const BwdPlan p = plan_backward(rows, h->C, dsum != nullptr);
     void *ws = nullptr;
     bool captured = false;
-    if ((rc = ows_begin(&h->ws, (size_t)grid * h->C * sizeof(float), st, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    if ((rc = ows_begin(&h->ws, (size_t)p.grid * h->C * sizeof(float), st, &ws, &captured)) != SWIN_WATTN_OK) return rc;
     RmsBwdArgs a{};
     a.s = (const bf16 *)s;
     a.dy = (const bf16 *)dy;
@@ -582,7 +706,7 @@ int swin_block_rms_backward(swin_block_rms_t h, const void *s, int rows, const v
     a.inv_c = 1.f / (float)h->C;
     a.eps = h->eps;
     h->last_launches = 2;
-    rc = cuda_status(launch_rms_backward(a, grid, p, dgamma, st));
+    rc = cuda_status(launch_rms_backward(a, p, dgamma, st));
     const int rc2 = ows_end(&h->ws, st, ws, captured);
     return rc != SWIN_WATTN_OK ? rc : rc2;
 }
