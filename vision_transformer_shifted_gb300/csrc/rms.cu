@@ -15,6 +15,7 @@
 
 #include "swin_rms.h"
 #include "common.cuh"
+#include "gelu.cuh"
 #include "ptx.cuh"
 
 using namespace swin;
@@ -102,6 +103,13 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8])
         v[2 * e] = f.x;
         v[2 * e + 1] = f.y;
     }
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 u;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr) : "memory");
+    return u;
 }
 
 // The compiler takes u for a new value from here on.
@@ -223,16 +231,17 @@ struct RmsBwdArgs {
 // One thread's piece (eight channels) of a row in the backward, dx = r (a - n
 // mean(a n)) + dsum with n = s r, a = dy gamma.  First its shares of sum s^2
 // and sum a s:
-__device__ __forceinline__ void piece_sums(const uint4 &s, const uint4 &d, const uint4 &g, float &sq, float &dot)
+__device__ __forceinline__ void piece_sums(const uint4 &s, const uint4 &d, const uint4 &g, float2 &sq, float2 &dot)
 {
     float v[8], y[8], w[8];
     unpack8(s, v);
     unpack8(d, y);
     unpack8(g, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        sq = fmaf(v[e], v[e], sq);
-        dot = fmaf(y[e] * w[e], v[e], dot);
+    for (int e = 0; e < 8; e += 2) {
+        g2_fma(sq.x, sq.y, v[e], v[e + 1], v[e], v[e + 1], sq.x, sq.y);
+        g2_mul(y[e], y[e + 1], y[e], y[e + 1], w[e], w[e + 1]);
+        g2_fma(dot.x, dot.y, y[e], y[e + 1], v[e], v[e + 1], dot.x, dot.y);
     }
 }
 // then, with q = mean(a n) r (so that n mean(a n) = s q), dx and its terms of dgamma.
@@ -245,9 +254,13 @@ __device__ __forceinline__ uint4 piece_grad(const uint4 &s, const uint4 &d, cons
     unpack8(g, w);
     unpack8(m, b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        acc[e] = fmaf(y[e], v[e] * r, acc[e]);
-        b[e] = fmaf(r, y[e] * w[e] - v[e] * q, b[e]);
+    for (int e = 0; e < 8; e += 2) {
+        float n0, n1, t0, t1;
+        g2_mul(n0, n1, v[e], v[e + 1], r, r);
+        g2_fma(acc[e], acc[e + 1], y[e], y[e + 1], n0, n1, acc[e], acc[e + 1]);
+        g2_mul(t0, t1, y[e], y[e + 1], w[e], w[e + 1]);
+        g2_fma(t0, t1, v[e], v[e + 1], -q, -q, t0, t1);
+        g2_fma(b[e], b[e + 1], t0, t1, r, r, b[e], b[e + 1]);
     }
     return pack8(b);
 }
@@ -285,9 +298,10 @@ __global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsB
             d[k] = ok ? ld16(a.dy + base + c * 8) : make_uint4(0, 0, 0, 0);
             m[k] = ok && a.dsum ? ld16(a.dsum + base + c * 8) : make_uint4(0, 0, 0, 0);
         }
-        float sq = 0.f, dot = 0.f;
+        float2 sq2 = make_float2(0.f, 0.f), dot2 = sq2;
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) piece_sums(s[k], d[k], g[k], sq, dot);
+        for (int k = 0; k < CPL; ++k) piece_sums(s[k], d[k], g[k], sq2, dot2);
+        float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
         lane_sum2(sq, dot, step);
         // (the packed values stay, their fp32 forms are made again: registers
         // kept across the sums would halve the rows in flight)
@@ -331,64 +345,76 @@ __global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsB
 // fetches its own pieces of the next DEPTH - 1 rows by asynchronous copies into
 // its own place in shared memory, so that the latency of HBM is paid once, not
 // once a row; 3001 x 2744: 20.8 us with the rows loaded as they come.
-template <int CPL, int DEPTH>
-__global__ void __launch_bounds__(CPL > 2 ? 512 : 1024, 1) rms_backward_wide_kernel(RmsBwdArgs a)
+template <int CPL, bool DSUM>
+__global__ void __launch_bounds__(512, 1) rms_backward_wide_kernel(RmsBwdArgs a)
 {
+    constexpr int ARRAYS = DSUM ? 3 : 2, DEPTH = DSUM ? 2 : 3;
     extern __shared__ __align__(16) float part[];   // the pieces; at the end [C]
     __shared__ float2 red[2 * 16 * 16];
     griddep_launch_dependents();
     griddep_wait();
     const int step = a.lanes, group = (int)threadIdx.x / step, li = (int)threadIdx.x - group * step;
-    const int rpb = (int)blockDim.x / step, C = a.chunks * 8, arrays = a.dsum ? 3 : 2;
-    // piece k of array i of stage d, this thread's
-    uint4 *mine = reinterpret_cast<uint4 *>(part) + threadIdx.x;
-    auto piece = [&](int d, int i, int k) { return mine + ((d * arrays + i) * CPL + k) * (int)blockDim.x; };
-    auto fetch = [&](int64_t row, int d) {
-        if (row < a.rows) {
+    const int rpb = (int)blockDim.x / step, C = a.chunks * 8;
+    // this thread's piece k of array i in a stage at `at`: place(at, i, k)
+    const uint32_t stride = blockDim.x * 16, stage = ARRAYS * CPL * stride;
+    const uint32_t ring = smem_u32(part) + threadIdx.x * 16, ring_end = ring + DEPTH * stage;
+    auto place = [&](uint32_t at, int i, int k) { return at + (uint32_t)(i * CPL + k) * stride; };
+    bool have[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) have[k] = li + k * step < a.chunks;
+    const int64_t first = (int64_t)blockIdx.x * rpb + group, hop = (int64_t)gridDim.x * rpb;
+    int64_t ahead = first;   // the next row to fetch, and its stage
+    uint32_t ahead_at = ring;
+    auto fetch = [&]() {
+        if (ahead < a.rows) {
+            const int64_t off = ahead * C + li * 8;
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
-                const int c = li + k * step;
-                if (c >= a.chunks) continue;
-                const int64_t at = row * C + c * 8;
-                cp_async16(smem_u32(piece(d, 0, k)), a.s + at, 16);
-                cp_async16(smem_u32(piece(d, 1, k)), a.dy + at, 16);
-                if (a.dsum) cp_async16(smem_u32(piece(d, 2, k)), a.dsum + at, 16);
+                if (!have[k]) continue;
+                cp_async16(place(ahead_at, 0, k), a.s + off + k * step * 8, 16);
+                cp_async16(place(ahead_at, 1, k), a.dy + off + k * step * 8, 16);
+                if (DSUM) cp_async16(place(ahead_at, 2, k), a.dsum + off + k * step * 8, 16);
             }
         }
         cp_async_commit();
+        ahead += hop;
+        ahead_at += stage;
+        if (ahead_at == ring_end) ahead_at = ring;
     };
-    const int64_t first = (int64_t)blockIdx.x * rpb + group, hop = (int64_t)gridDim.x * rpb;
 #pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d) fetch(first + d * hop, d);
+    for (int d = 0; d < DEPTH - 1; ++d) fetch();
     float acc[CPL][8];
     uint4 g[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
-        const int c = li + k * step;
-        g[k] = c < a.chunks ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
+        g[k] = have[k] ? ld16(a.gamma + (li + k * step) * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
     }
-    int d = 0, turn = 0;
+    uint32_t at = ring;
+    int turn = 0;
+#pragma unroll 1
     for (int64_t row = first; row < a.rows; row += hop) {   // (the same for a group's threads)
-        fetch(row + (DEPTH - 1) * hop, d == 0 ? DEPTH - 1 : d - 1);
+        fetch();
         cp_async_wait<DEPTH - 1>();
-        float sq = 0.f, dot = 0.f;
+        float2 sq2 = make_float2(0.f, 0.f), dot2 = sq2;
 #pragma unroll
         for (int k = 0; k < CPL; ++k)
-            if (li + k * step < a.chunks) piece_sums(*piece(d, 0, k), *piece(d, 1, k), g[k], sq, dot);
+            if (have[k]) piece_sums(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], sq2, dot2);
+        float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
         group_sum2(sq, dot, step, group, turn++, red);
         const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r;
+        bf16 *dx = a.dx + row * C + li * 8;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
-            const int c = li + k * step;
-            if (c >= a.chunks) continue;
+            if (!have[k]) continue;
             forget(g[k]);
-            const uint4 m = a.dsum ? *piece(d, 2, k) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(a.dx + row * C + c * 8) =
-                piece_grad(*piece(d, 0, k), *piece(d, 1, k), g[k], m, r, q, acc[k]);
+            const uint4 m = DSUM ? lds16(place(at, 2, k)) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(dx + k * step * 8) =
+                piece_grad(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], m, r, q, acc[k]);
         }
-        if (++d == DEPTH) d = 0;
+        at += stage;
+        if (at == ring_end) at = ring;
     }
     __syncthreads();   // (every group is done with its pieces)
     // the groups add theirs in turn
@@ -442,7 +468,7 @@ struct RowPlan {
     int lanes;     // of a row: of a warp, or threads
     int cpl;
 };
-RowPlan plan_row(int chunks, int most)
+RowPlan plan_row(int chunks, int most, int block_most)
 {
     RowPlan p{};
     if (chunks <= 32 * most) {
@@ -458,12 +484,12 @@ RowPlan plan_row(int chunks, int most)
         return p;
     }
     p.block = true;
-    p.lanes = ((chunks + most - 1) / most + 31) / 32 * 32;
+    p.lanes = ((chunks + block_most - 1) / block_most + 31) / 32 * 32;
     if (p.lanes > 512) p.lanes = 512;
     p.cpl = (chunks + p.lanes - 1) / p.lanes;
     return p;
 }
-constexpr int FWD_PIECES = 4, BWD_PIECES = 3, BWD_BLOCK_PIECES = 2;
+constexpr int FWD_PIECES = 4, BWD_PIECES = 3, BWD_BLOCK_PIECES = 4;
 constexpr int MAX_GROUPS = 15;   // row groups of a block: a block has 16 barriers, and one is everybody's
 
 template <bool Q8>
@@ -471,7 +497,8 @@ cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
 {
     // rows that leave SMs idle take as many threads as pieces: the latency of
     // one row counts then (1 x 2048: 5.6 us on 64 threads)
-    const RowPlan p = plan_row(a.chunks, a.rows < sm_count() ? 1 : FWD_PIECES);
+    const int most = a.rows < sm_count() ? 1 : FWD_PIECES;
+    const RowPlan p = plan_row(a.chunks, most, most);
     a.lpr = p.block ? 32 : p.lanes;
     const int threads = p.block ? p.lanes : 256;
     const int64_t rpb = p.block ? 1 : 8 * (32 / p.lanes);
@@ -495,28 +522,26 @@ cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
 // The backward's launch: as many blocks as the SMs hold at once, each walking
 // its share of the rows.  (Registers allow four blocks of 256 threads a SM with
 // one or two pieces a lane, two with three; a wide row's block is an SM's only
-// one, of up to 1024 threads with two pieces a thread, 512 with more, and its
-// pieces' stages are what shared memory holds: three of two arrays, two of three.)
+// one, of up to 512 threads with three or four pieces each: with two on 1024
+// threads, what a thread spends on a row beside its pieces took 1 of 18 us.)
 struct BwdPlan {
     RowPlan row;
-    int threads, grid, depth;
+    int threads, grid;
     size_t smem;
 };
 BwdPlan plan_backward(int rows, int C, bool with_dsum)
 {
     const int chunks = C / 8;
     BwdPlan p{};
-    p.row = plan_row(chunks, chunks <= 32 * BWD_PIECES ? BWD_PIECES : BWD_BLOCK_PIECES);
+    p.row = plan_row(chunks, BWD_PIECES, BWD_BLOCK_PIECES);
     const RowPlan &r = p.row;
     int64_t rpb, per_sm;
     if (r.block) {
-        const int groups = (r.cpl > 2 ? 512 : 1024) / r.lanes;
+        const int groups = 512 / r.lanes;
         rpb = groups < MAX_GROUPS ? groups : MAX_GROUPS;
         per_sm = 1;
         p.threads = (int)rpb * r.lanes;
-        p.depth = with_dsum ? 2 : 3;
-        const int cpl = r.cpl < 2 ? 2 : r.cpl;   // (as the kernels are built)
-        p.smem = (size_t)p.threads * p.depth * (with_dsum ? 3 : 2) * cpl * 16;   // (at most 192 KB)
+        p.smem = (size_t)p.threads * (with_dsum ? 2 * 3 : 3 * 2) * r.cpl * 16;   // (at most 192 KB)
         if (p.smem < (size_t)C * sizeof(float)) p.smem = (size_t)C * sizeof(float);
     } else {
         rpb = 8 * (32 / r.lanes);
@@ -537,12 +562,10 @@ cudaError_t launch_rms_backward(RmsBwdArgs a, const BwdPlan &p, float *dgamma, c
     void (*kern)(RmsBwdArgs) = nullptr;
     if (!r.block)
         kern = r.cpl == 1 ? rms_backward_kernel<1> : r.cpl == 2 ? rms_backward_kernel<2> : rms_backward_kernel<3>;
-    else if (p.depth == 2)
-        kern = r.cpl <= 2 ? rms_backward_wide_kernel<2, 2> : r.cpl == 3 ? rms_backward_wide_kernel<3, 2>
-                                                                        : rms_backward_wide_kernel<4, 2>;
+    else if (a.dsum)
+        kern = r.cpl == 3 ? rms_backward_wide_kernel<3, true> : rms_backward_wide_kernel<4, true>;
     else
-        kern = r.cpl <= 2 ? rms_backward_wide_kernel<2, 3> : r.cpl == 3 ? rms_backward_wide_kernel<3, 3>
-                                                                        : rms_backward_wide_kernel<4, 3>;
+        kern = r.cpl == 3 ? rms_backward_wide_kernel<3, false> : rms_backward_wide_kernel<4, false>;
     cudaError_t e;
     if (r.block &&
         (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem)) != cudaSuccess)
