@@ -10,26 +10,44 @@ namespace swin {
 
 enum { ACT_SILU = 0, ACT_GELU = 1 };
 
-// d = a + b, two lanes.
-__device__ __forceinline__ void g2_add(float &d0, float &d1, float a0, float a1, float b0, float b1)
+// Two fp32 values as one 64-bit register pair, and the operations on both.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b)
 {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pack2(float a) { return pack2(a, a); }
+__device__ __forceinline__ void unpack2(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 1 / (1 + 2^z).
+__device__ __forceinline__ f2 logistic2(f2 z)
+{
+    float a, b;
+    unpack2(z, a, b);
+    unpack2(add2(pack2(ex2_approx(a), ex2_approx(b)), pack2(1.f)), a, b);
+    return pack2(rcp_approx(a), rcp_approx(b));
 }
 
-// p = 1 / (1 + exp(-g)) for two values.
-__device__ __forceinline__ void sigmoid2(float g0, float g1, float &p0, float &p1)
-{
-    float z0, z1;
-    g2_mul(z0, z1, g0, g1, -1.4426950408889634f, -1.4426950408889634f);
-    g2_add(z0, z1, ex2_approx(z0), ex2_approx(z1), 1.f, 1.f);
-    p0 = rcp_approx(z0);
-    p1 = rcp_approx(z1);
-}
-
-// act of two values, in place.
+// act of two values.
 //
 // GELU as x / (1 + 2^(x P(x^2))): the logit of the normal distribution function
 // is odd and smooth, and P, of degree 6, was fitted to it here by reweighted
@@ -38,25 +56,17 @@ __device__ __forceinline__ void sigmoid2(float g0, float g1, float &p0, float &p
 // operations and no sign handling against fourteen and four more; its last
 // coefficient is negative, so that far from zero Phi goes to 0 and 1.
 template <int ACT>
-__device__ __forceinline__ void activate2(float &g0, float &g1)
+__device__ __forceinline__ f2 activate2(f2 g)
 {
-    if (ACT == ACT_GELU) {
-        float t0, t1, z0, z1;
-        g2_mul(t0, t1, g0, g1, g0, g1);
-        g2_fma(z0, z1, t0, t1, -5.23388088e-9f, -5.23388088e-9f, 3.860164099e-7f, 3.860164099e-7f);
-        g2_fma(z0, z1, z0, z1, t0, t1, -1.1466739124e-5f, -1.1466739124e-5f);
-        g2_fma(z0, z1, z0, z1, t0, t1, 1.59485251061e-4f, 1.59485251061e-4f);
-        g2_fma(z0, z1, z0, z1, t0, t1, 9.5295035863e-5f, 9.5295035863e-5f);
-        g2_fma(z0, z1, z0, z1, t0, t1, -0.10483819246f, -0.10483819246f);
-        g2_fma(z0, z1, z0, z1, t0, t1, -2.30220746994f, -2.30220746994f);
-        g2_mul(z0, z1, z0, z1, g0, g1);
-        g2_add(z0, z1, ex2_approx(z0), ex2_approx(z1), 1.f, 1.f);
-        g2_mul(g0, g1, g0, g1, rcp_approx(z0), rcp_approx(z1));
-        return;
-    }
-    float p0, p1;
-    sigmoid2(g0, g1, p0, p1);
-    g2_mul(g0, g1, g0, g1, p0, p1);
+    if (ACT == ACT_SILU) return mul2(g, logistic2(mul2(g, pack2(-1.4426950408889634f))));
+    const f2 t = mul2(g, g);
+    f2 z = fma2(t, pack2(-5.23388088e-9f), pack2(3.860164099e-7f));
+    z = fma2(z, t, pack2(-1.1466739124e-5f));
+    z = fma2(z, t, pack2(1.59485251061e-4f));
+    z = fma2(z, t, pack2(9.5295035863e-5f));
+    z = fma2(z, t, pack2(-0.10483819246f));
+    z = fma2(z, t, pack2(-2.30220746994f));
+    return mul2(g, logistic2(mul2(z, g)));
 }
 
 // act and its derivative of two values: a = g P(g), d = P + g P'(g).
@@ -65,8 +75,9 @@ __device__ __forceinline__ void activate_grad2(float g0, float g1, float &a0, fl
 {
     float p0, p1;
     if (ACT == ACT_SILU) {
-        sigmoid2(g0, g1, p0, p1);
-        g2_mul(a0, a1, g0, g1, p0, p1);
+        const f2 g = pack2(g0, g1), p = logistic2(mul2(g, pack2(-1.4426950408889634f)));
+        unpack2(p, p0, p1);
+        unpack2(mul2(g, p), a0, a1);
         // p (1 + g (1 - p)) = p + a - a p
         float t0, t1;
         g2_fma(t0, t1, a0, a1, -p0, -p1, a0, a1);
@@ -140,7 +151,15 @@ __device__ __forceinline__ void spread8(const float *vec, int q, float (&f)[8])
 __device__ __forceinline__ void add8(float *d, const float (&s)[8])
 {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) g2_add(d[e], d[e + 1], d[e], d[e + 1], s[e], s[e + 1]);
+    for (int e = 0; e < 8; e += 2) unpack2(add2(pack2(d[e], d[e + 1]), pack2(s[e], s[e + 1])), d[e], d[e + 1]);
+}
+// v = act(g) v, eight values.
+template <int ACT>
+__device__ __forceinline__ void gate8(const float *g, float *v)
+{
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        unpack2(mul2(activate2<ACT>(pack2(g[e], g[e + 1])), pack2(v[e], v[e + 1])), v[e], v[e + 1]);
 }
 
 __device__ __forceinline__ uint4 pack8f(const float *v)
@@ -271,11 +290,7 @@ struct UpPolicy {
                 spread8(vec + 32, q, s);
                 add8(vq, s);
             }
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                activate2<ACT>(gq[e], gq[e + 1]);
-                g2_mul(vq[e], vq[e + 1], vq[e], vq[e + 1], gq[e], gq[e + 1]);
-            }
+            gate8<ACT>(gq, vq);
             *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(vq);
         }
         store_box(&a.h, col0, row0, row0 < a.rows && col0 < a.F, stage, lane);

@@ -241,10 +241,8 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
         } else {
             if (a.b1) add4(u, a.b1 + c);
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                activate2<ACT == ACT_NONE ? ACT_SILU : ACT>(v[k], v[k + 1]);
-                g2_mul(v[k], v[k + 1], v[k], v[k + 1], u[k], u[k + 1]);
-            }
+            for (int k = 0; k < 4; k += 2)
+                unpack2(mul2(activate2<ACT>(pack2(v[k], v[k + 1])), pack2(u[k], u[k + 1])), v[k], v[k + 1]);
         }
         *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ld + c) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));

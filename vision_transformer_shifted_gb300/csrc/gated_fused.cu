@@ -324,11 +324,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
                     spread8(vec + 32, s, b);
                     add8(vq, b);
                 }
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    activate2<ACT>(gq[k], gq[k + 1]);
-                    g2_mul(vq[k], vq[k + 1], vq[k], vq[k + 1], gq[k], gq[k + 1]);
-                }
+                gate8<ACT>(gq, vq);
             }
             // the MMAs that read this buffer two chunks ago are done
             if (!warp_pair_wait(smem_u32(&bars.hfree[grp]), use ^ 1u, limit)) {
