@@ -52,10 +52,10 @@ cudaError_t map_mn(CUtensorMap *m, const void *p, int64_t k, int mn, int ld = 0)
 {
     return make_tensor_map(m, T_BF16, p, mn, k, (int64_t)(ld ? ld : mn) * 2, 64, 64, 128);
 }
-// Output [rows, cols]: a warp's boxes of 64 columns x 32 rows.
+// Output [rows, cols]: a warp's boxes of 32 columns x 32 rows.
 cudaError_t map_out(CUtensorMap *m, const void *p, int64_t rows, int cols)
 {
-    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 64, 32, 128);
+    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 32, 32, 64);
 }
 // Hidden activations in the workspace, [rows, F] with rows padded to 128 bytes:
 // a box's rows are whole lines.  (F = 1368 unpadded: five sectors in two lines
@@ -306,7 +306,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     a.np = pl.split.np;
     a.st = st;
     if (pl.split.cut) {
-        e = make_tensor_map(&a.part, T_F32, part, TN, (int64_t)a.np * 2 * 256, TN * 4, 32, 32, 128);
+        e = make_tensor_map(&a.part, T_F32, part, TN, (int64_t)a.np * 2 * 256, TN * 4, 16, 32, 64);
         if (e != cudaSuccess) return e;
     }
     ++*launches;

@@ -234,8 +234,8 @@ struct UpPolicy {
     struct Pre {
         float bg, bu, sg, su, sx;   // of this lane's column, and its row's scale
     };
-    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int quad, int part,
-                                                   int lane)
+    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int, int quad, int part,
+                                                   int lane, uint8_t *)
     {
         const int c = u.n * 128 + part * 32 + lane, row = u.m * 256 + (int)rank * 128 + quad * 32 + lane;
         Pre p{};
@@ -349,8 +349,9 @@ struct GemmPolicy {
         int slot;           // partial tile to write (-1: the whole K, to D)
         int k0, kb_first;   // the first segment's K, and its blocks
     };
-    static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 8, STAGING = 4096, SEGS = 1;
-    static constexpr int STAGES = TN == 256 ? 6 : 7;
+    static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 16, STAGING = 4096, SEGS = 1;
+    static constexpr int STAGES = TN == 256 ? 5 : 6;
+    static constexpr int BOXES = TN / 128;   // a warp's share of the columns: boxes of 32
     static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, TN);
 
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
@@ -417,71 +418,100 @@ struct GemmPolicy {
         if (kb >= u.kb_first) kb -= u.kb_first;
         mma_kblock<MMA_BF16, A_MN, B_MN>(d, src16, src16 + 1024, IDESC, kblock_steps(u.k0, kb, 64), i == 0);
     }
-    struct Pre {};
-    static __device__ __forceinline__ Pre prefetch(const Args &, const Unit &, uint32_t, int, int, int) { return Pre{}; }
+    // Of a warp's two 2 KB boxes of staging, box j takes its columns 32 j ...:
+    // before the accumulators are ready, the residual.
+    struct Pre {
+        float bias[BOXES];   // of this lane's column of each box
+    };
+    static __device__ __forceinline__ int row_of(const Unit &u, uint32_t rank, int quad)
+    {
+        return u.m * 256 + (int)rank * 128 + quad * 32;
+    }
+    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.n * TN + part * (TN / 4) + 32 * j; }
+    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int warp, int quad,
+                                                   int part, int lane, uint8_t *staging)
+    {
+        const PairProblem &p = a.p[u.p];
+        Pre pre{};
+        if (u.slot >= 0) return pre;
+        if (p.residual) {
+            const int row0 = row_of(u, rank, quad);
+            staging_free(lane);
+#pragma unroll
+            for (int j = 0; j < BOXES; ++j) {
+                const int col = col_of(u, part, j) + 8 * (lane & 3);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2);
+                    const bool ok = row0 + r < p.rows && col < p.cols;
+                    cp_async16(smem_u32(staging + warp * STAGING + j * 2048) + sw64_offset(r, lane & 3),
+                               ok ? p.residual + (int64_t)(row0 + r) * p.cols + col : p.residual, ok ? 16u : 0u);
+                }
+            }
+            cp_async_commit();
+        }
+#pragma unroll
+        for (int j = 0; j < BOXES; ++j) pre.bias[j] = lane_value(p.bias, col_of(u, part, j) + lane, p.cols);
+        return pre;
+    }
     template <class Release>
-    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, const Pre &, int n, uint32_t rank,
+    static __device__ __forceinline__ void epilogue(const Args &a, const Unit &u, const Pre &pre, int n, uint32_t rank,
                                                     int warp, int quad, int part, int lane, uint32_t t_lane,
                                                     uint8_t *staging, Release &&release)
     {
-        uint8_t *stage = staging + warp * STAGING;
         const PairProblem &p = a.p[u.p];
-        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, colh = u.n * TN + part * (TN / 2);
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (TN / 2);
-        if (u.slot >= 0) {
+        uint8_t *stage = staging + warp * STAGING;
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (TN / 4);
+        if (u.slot >= 0) {   // fp32 boxes of 16 columns, the two stagings in turn
 #pragma unroll 1
-            for (int j = 0; j < TN / 64; ++j) {
-                float v[32];
-                tmem_ld32(acc + 32 * j, v);
-                tmem_wait_ld();
-                if (j == TN / 64 - 1) release();
-                staging_free(lane);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<float4 *>(stage + sw128_offset(lane, q)) =
-                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&a.part, part * (TN / 2) + 32 * j, u.slot * 256 + (int)rank * 128 + quad * 32,
-                                 smem_u32(stage));
-                    bulk_commit();
+            for (int j = 0; j < 2 * BOXES; ++j) {
+                float v[16];
+                tmem_ld16(acc + 16 * j, v);
+                if (lane == 0) {   // (the box written two before; at first, whatever an earlier unit stored)
+                    if (j) bulk_wait_read1();
+                    else bulk_wait_read();
                 }
+                __syncwarp();
+                tmem_wait_ld();
+                if (j == 2 * BOXES - 1) release();
+                uint8_t *box = stage + (j & 1) * 2048;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4 *>(box + sw64_offset(lane, q)) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                store_box(&a.part, part * (TN / 4) + 16 * j, u.slot * 256 + (int)rank * 128 + quad * 32, true, box, lane);
             }
             return;
         }
-        const bool row_ok = row0 + lane < p.rows;
-        const bf16 *res = p.residual && row_ok ? p.residual + (int64_t)(row0 + lane) * p.cols : nullptr;
-#pragma unroll 1
-        for (int j = 0; j < TN / 64; ++j) {
+        const int row0 = row_of(u, rank, quad);
+        if (p.residual) {
+            cp_async_wait<0>();
+            __syncwarp();
+        } else {
+            staging_free(lane);
+        }
+#pragma unroll
+        for (int j = 0; j < BOXES; ++j) {
             float v[32];
             tmem_ld32(acc + 32 * j, v);
             tmem_wait_ld();
-            if (j == TN / 64 - 1) release();
-            const int c0 = colh + 32 * j;
+            if (j == BOXES - 1) release();
+            uint8_t *box = stage + j * 2048;
             if (p.bias) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float b[8];
-                    load8(p.bias, c0 + 8 * q, p.cols, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
-                }
+                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, pre.bias[j], i);
             }
-            if (res) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 4; ++q) {
+                uint4 *at = reinterpret_cast<uint4 *>(box + sw64_offset(lane, q));
+                if (p.residual) {
                     float b[8];
-                    load8(res, c0 + 8 * q, p.cols, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] += b[e];
+                    load8(reinterpret_cast<const bf16 *>(at), 0, 8, b);
+                    add8(v + 8 * q, b);
                 }
+                *at = pack8f(v + 8 * q);
             }
-            if ((j & 1) == 0) staging_free(lane);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint4 *>(stage + sw128_offset(lane, 4 * (j & 1) + q)) = pack8f(v + 8 * q);
-            if (j & 1) store_box(&p.d, c0 - 32, row0, row0 < p.rows && c0 - 32 < p.cols, stage, lane);
+            store_box(&p.d, col_of(u, part, j), row0, row0 < p.rows && col_of(u, part, j) < p.cols, box, lane);
         }
     }
 };
@@ -562,7 +592,8 @@ struct GradPolicy {
     struct Pre {
         bf16 bg, bu;   // of this lane's column
     };
-    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t, int, int part, int lane)
+    static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t, int, int, int part, int lane,
+                                                   uint8_t *)
     {
         const int c = u.n * 128 + part * 32 + lane;
         Pre p;

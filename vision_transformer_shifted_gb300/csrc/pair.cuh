@@ -357,7 +357,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         for (; n < units && !failed; ++n) {
             const typename P::Unit un = P::decode(a, pair, n);
             // (warp-uniform outcome: the TMEM loads below are warp-collective)
-            const typename P::Pre pre = P::prefetch(a, un, rank, quad, part, lane);
+            const typename P::Pre pre = P::prefetch(a, un, rank, warp - 2, quad, part, lane, staging);
             for (int seg = 0; seg < P::SEGS && !failed; ++seg)
                 failed = !warp_pair_wait(tfull + 8 * P::slot(seg, n), P::slot_use(seg, n) & 1, a.st.wait_ns);
             if (failed) break;
