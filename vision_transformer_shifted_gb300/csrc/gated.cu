@@ -80,12 +80,12 @@ struct Product {
 };
 
 // The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
-// of K (+ bias + residual), JOIN_BLOCKS blocks a tile.
-constexpr int JOIN_BLOCKS = 16;
+// of K (+ bias + residual), `blocks` blocks a tile (16, and up to 64 where few
+// tiles have many partial tiles each).
 struct JoinArgs {
     const float *part;
     PairSplit split;
-    int tn;
+    int tn, blocks;
     struct {
         const bf16 *bias, *residual;
         bf16 *out;
@@ -95,37 +95,39 @@ struct JoinArgs {
 __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
 {
     const PairSplit &s = a.split;
-    const int c = block / JOIN_BLOCKS, t = s.full * s.np + c;
+    const int c = block / a.blocks, t = s.full * s.np + c;
     const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
     if (p0 == p1) return;   // (one pair had the whole tile and wrote it)
     const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
     int m, n;
     tile_order(t - a.p[i].first, a.p[i].mt, a.p[i].nt, m, n);
-    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / 8;
+    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / 4;
     const int64_t size = 256 * a.tn;
     const int first = s.slot(p0, c);
-    for (int e = block % JOIN_BLOCKS * 256 + threadIdx.x; e < 256 * per; e += JOIN_BLOCKS * 256) {
-        const int row = m * 256 + e / per, col = n * a.tn + e % per * 8;
+    for (int e = block % a.blocks * 256 + threadIdx.x; e < 256 * per; e += a.blocks * 256) {
+        const int row = m * 256 + e / per, col = n * a.tn + e % per * 4;
         if (row >= rows || col >= cols) continue;
-        float v[8], w[8];
-        const float *src = a.part + (int64_t)e * 8;
-        load8(src + first * size, 0, 8, v);
-#pragma unroll 4
+        const float *src = a.part + (int64_t)e * 4;
+        float4 v = *reinterpret_cast<const float4 *>(src + first * size);
+#pragma unroll 8
         for (int p = p0 + 1; p <= p1; ++p) {   // (these begin inside the tile: their first range)
-            load8(src + 2 * p * size, 0, 8, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += w[k];
+            const float4 w = *reinterpret_cast<const float4 *>(src + 2 * p * size);
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
         }
-        load8(a.p[i].bias, col, cols, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += w[k];
         const int64_t at = (int64_t)row * cols + col;
-        if (a.p[i].residual) {
-            load8(a.p[i].residual + at, 0, 8, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += w[k];
+        for (const bf16 *q : {a.p[i].bias ? a.p[i].bias + col : nullptr, a.p[i].residual ? a.p[i].residual + at : nullptr}) {
+            if (!q) continue;
+            const uint2 u = *reinterpret_cast<const uint2 *>(q);
+            const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += y.x;
+            v.w += y.y;
         }
-        *reinterpret_cast<uint4 *>(a.p[i].out + at) = pack8f(v);
+        *reinterpret_cast<uint2 *>(a.p[i].out + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
 
@@ -249,18 +251,30 @@ ProductsPlan plan_products(const Product *p, int n)
     for (int i = 0; i < n; ++i) tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, tn);
     PairSplit &s = pl.split;
     s.tiles = (int)tiles;
-    s.kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
+    s.k_blocks = s.kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
     const int pairs = sm_count() / 2;
     s.np = (int)(tiles < pairs ? tiles : pairs);
     const int full = (int)(tiles / pairs), rest = (int)(tiles - (int64_t)full * pairs);
     const int64_t blocks = (int64_t)rest * s.kb;
-    const int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
+    int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
     if (rest && s.kb - ceil_div(blocks, np) > (pl.wide ? 16 : 24)) {
+        // Equal slices of every tile, where they cost at most a tenth more blocks:
+        // pairs that share rows of an operand then walk K side by side, and each
+        // reads what another has brought into L2.  (36 tiles, the weight gradients
+        // of 44821 x 336 x 1288: 112 us, 194 by even ranges.  A slice is longer than
+        // what rounding K up to equal slices adds, so that none is empty.)
+        const int slices = pairs / rest;
+        if (!full && slices > 1 && s.kb >= 16 * slices && s.kb >= slices * slices &&
+            (int64_t)ceil_div(s.kb, slices) * 10 <= (int64_t)ceil_div(blocks, np) * 11) {
+            np = rest * slices;
+            s.kb = ceil_div(s.kb, slices) * slices;
+        }
+        const int64_t all = (int64_t)rest * s.kb;
         s.np = (int)np;
         s.full = full;
         s.cut = rest;
-        s.q = (uint32_t)(blocks / np);
-        s.r = (uint32_t)(blocks % np);
+        s.q = (uint32_t)(all / np);
+        s.r = (uint32_t)(all % np);
         pl.part_bytes = (size_t)np * 2 * 256 * tn * sizeof(float);
     }
     return pl;
@@ -312,7 +326,8 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     ++*launches;
     r.part = part;
     r.tn = TN;
-    fin->joins[slot] = pl.split.cut * JOIN_BLOCKS;
+    r.blocks = pl.split.cut >= 32 ? 16 : pl.split.cut >= 16 ? 32 : 64;
+    fin->joins[slot] = pl.split.cut * r.blocks;
     return launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
 }
 

@@ -205,7 +205,7 @@ struct UpPolicy {
         int m, n;
     };
     static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
-    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, STAGING = 2560, SEGS = 1;
+    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 2, STAGING = 2560, SEGS = 1;
     static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 256);
 
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
@@ -232,20 +232,25 @@ struct UpPolicy {
                                                            kb == 0);
     }
     struct Pre {
-        float bg, bu, sg, su, sx;   // of this lane's column, and its row's scale
+        float bg[2], bu[2], sg[2], su[2], sx;   // of this lane's column of each box of 32, and its row's scale
     };
+    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.n * 128 + part * 64 + 32 * j; }
     static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int, int quad, int part,
                                                    int lane, uint8_t *)
     {
-        const int c = u.n * 128 + part * 32 + lane, row = u.m * 256 + (int)rank * 128 + quad * 32 + lane;
         Pre p{};
-        p.bg = lane_value(a.bg, c, a.F);
-        p.bu = lane_value(a.bu, c, a.F);
-        if (Q8) {
-            p.sg = c < a.F ? a.sg[c] : 0.f;
-            p.su = c < a.F ? a.su[c] : 0.f;
-            p.sx = row < a.rows ? a.sx[row] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = col_of(u, part, j) + lane;
+            p.bg[j] = lane_value(a.bg, c, a.F);
+            p.bu[j] = lane_value(a.bu, c, a.F);
+            if (Q8) {
+                p.sg[j] = c < a.F ? a.sg[c] : 0.f;
+                p.su[j] = c < a.F ? a.su[c] : 0.f;
+            }
         }
+        const int row = u.m * 256 + (int)rank * 128 + quad * 32 + lane;
+        if (Q8) p.sx = row < a.rows ? a.sx[row] : 0.f;
         return p;
     }
     template <class Release>
@@ -253,47 +258,52 @@ struct UpPolicy {
                                                     int warp, int quad, int part, int lane, uint32_t t_lane,
                                                     uint8_t *staging, Release &&release)
     {
-        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * 32;
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32;
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * 64;
         // the warps' boxes (aligned for their swizzle), then the warps' vectors
         uint8_t *stage = staging + warp * 2048;
         float *vec = reinterpret_cast<float *>(staging + EPI * 2048 + warp * 512);
-        float g[32], v[32];
-        tmem_ld32(acc, g);
-        tmem_ld32(acc + 128, v);
-        vec[lane] = pre.bg;
-        vec[32 + lane] = pre.bu;
-        if (Q8) {
-            vec[64 + lane] = pre.sg;
-            vec[96 + lane] = pre.su;
-        }
-        staging_free(lane);   // (and the vectors are there)
-        tmem_wait_ld();
-        release();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float *gq = g + 8 * q, *vq = v + 8 * q;
-            float s[8];
+        for (int j = 0; j < 2; ++j) {
+            float g[32], v[32];
+            tmem_ld32(acc + 32 * j, g);
+            tmem_ld32(acc + 128 + 32 * j, v);
+            __syncwarp();
+            vec[lane] = pre.bg[j];
+            vec[32 + lane] = pre.bu[j];
             if (Q8) {
-                spread8(vec + 64, q, s);
+                vec[64 + lane] = pre.sg[j];
+                vec[96 + lane] = pre.su[j];
+            }
+            staging_free(lane);   // (and the vectors are there)
+            tmem_wait_ld();
+            if (j == 1) release();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) gq[e] *= pre.sx * s[e];
-                spread8(vec + 96, q, s);
+            for (int q = 0; q < 4; ++q) {
+                float *gq = g + 8 * q, *vq = v + 8 * q;
+                float s[8];
+                if (Q8) {
+                    spread8(vec + 64, q, s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) vq[e] *= pre.sx * s[e];
+                    for (int e = 0; e < 8; ++e) gq[e] *= pre.sx * s[e];
+                    spread8(vec + 96, q, s);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) vq[e] *= pre.sx * s[e];
+                }
+                if (a.bg) {
+                    spread8(vec, q, s);
+                    add8(gq, s);
+                }
+                if (a.bu) {
+                    spread8(vec + 32, q, s);
+                    add8(vq, s);
+                }
+                gate8<ACT>(gq, vq);
+                *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(vq);
             }
-            if (a.bg) {
-                spread8(vec, q, s);
-                add8(gq, s);
-            }
-            if (a.bu) {
-                spread8(vec + 32, q, s);
-                add8(vq, s);
-            }
-            gate8<ACT>(gq, vq);
-            *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(vq);
+            const int col0 = col_of(u, part, j);
+            store_box(&a.h, col0, row0, row0 < a.rows && col0 < a.F, stage, lane);
         }
-        store_box(&a.h, col0, row0, row0 < a.rows && col0 < a.F, stage, lane);
     }
 };
 
@@ -316,7 +326,9 @@ struct PairProblem {
 };
 // The division of `tiles` tiles of kb K blocks each over np pairs.
 struct PairSplit {
-    int tiles, kb, np;
+    int tiles, np;
+    int k_blocks;    // of a tile
+    int kb;          // the same, or (equal slices) a multiple of the slices a little above
     int full;        // rounds of whole tiles
     int cut;         // tiles cut along K (0: the last round is whole tiles too)
     uint32_t q, r;   // blocks a pair of the cut tiles: q, the first r pairs q + 1
@@ -349,7 +361,7 @@ struct GemmPolicy {
         int slot;           // partial tile to write (-1: the whole K, to D)
         int k0, kb_first;   // the first segment's K, and its blocks
     };
-    static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 16, STAGING = 4096, SEGS = 1;
+    static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 16, GROUPS = 1, STAGING = 4096, SEGS = 1;
     static constexpr int STAGES = TN == 256 ? 5 : 6;
     static constexpr int BOXES = TN / 128;   // a warp's share of the columns: boxes of 32
     static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, TN);
@@ -370,15 +382,15 @@ struct GemmPolicy {
         Unit r;
         int t = pair + n * s.np;
         r.kb0 = 0;
-        r.kbn = s.kb;
+        r.kbn = s.k_blocks;
         r.slot = -1;
         if (s.cut && n >= s.full) {
             const uint32_t b0 = s.begin(pair), b1 = s.begin(pair + 1), kb = s.kb;
             const int c = (int)(b0 / kb) + n - s.full;   // cut tile
             const uint32_t lo = c * kb > b0 ? c * kb : b0, hi = (c + 1) * kb < b1 ? (c + 1) * kb : b1;
             r.kb0 = (int)(lo - c * kb);
-            r.kbn = (int)(hi - lo);
-            if (r.kbn < s.kb) r.slot = 2 * pair + (n > s.full);
+            r.kbn = (int)((hi - c * kb < (uint32_t)s.k_blocks ? hi - c * kb : (uint32_t)s.k_blocks)) - r.kb0;
+            if (hi - lo < kb) r.slot = 2 * pair + (n > s.full);
             t = s.full * s.np + c;
         }
         r.p = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
@@ -551,7 +563,7 @@ struct GradPolicy {
     struct Unit {
         int m, n;
     };
-    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, STAGING = 4096 + 64, SEGS = 2;
+    static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 1, STAGING = 4096 + 64, SEGS = 2;
     static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 128);
     static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 256);
 

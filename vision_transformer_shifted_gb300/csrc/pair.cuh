@@ -19,7 +19,9 @@
 //   Unit, count(a, pair), decode(a, pair, n)   a pair's work items (a tile, or
 //                           a range of a tile's K blocks)
 //   STAGES, STAGE_BYTES     the ring
-//   EPI                     epilogue warps (8, or 16 where arithmetic binds)
+//   EPI, GROUPS             epilogue warps; they drain units all together, or as
+//                           two groups in turn (GROUPS = 2): where the epilogue
+//                           binds, one group's latencies pass under the other's work
 //   STAGING                 bytes of shared memory per epilogue warp, laid out by
 //                           the epilogue (staged stores, vectors)
 //   SEGS                    accumulation segments of a unit (each a K loop
@@ -240,7 +242,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         }
         for (int s = 0; s < PAIR_SLOTS; ++s) {
             mbar_init(tfull + 8 * s, 1);
-            mbar_init(tempty + 8 * s, 2 * P::EPI);   // (the leader's: the epilogue warps of both CTAs)
+            mbar_init(tempty + 8 * s, 2 * P::EPI / P::GROUPS);   // (the leader's: a group's warps in both CTAs)
         }
         mbar_init_fence();
     }
@@ -351,10 +353,10 @@ pair_kernel(const __grid_constant__ typename P::Args a)
             }
         }
     } else {
-        const int quad = warp & 3, part = (warp - 2) >> 2;   // (part: of the columns)
+        constexpr int TEAM = P::EPI / P::GROUPS;
+        const int quad = warp & 3, part = (warp - 2) % TEAM >> 2;   // (part: of the columns)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        int n = 0;
-        for (; n < units && !failed; ++n) {
+        for (int n = (warp - 2) / TEAM; n < units && !failed; n += P::GROUPS) {
             const typename P::Unit un = P::decode(a, pair, n);
             // (warp-uniform outcome: the TMEM loads below are warp-collective)
             const typename P::Pre pre = P::prefetch(a, un, rank, warp - 2, quad, part, lane, staging);
