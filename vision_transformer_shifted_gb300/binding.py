@@ -333,6 +333,11 @@ def swin_merge_forward(h, x, gamma, beta, Wm, out, stream=None):
 
 # ---- swin_rms.h ------------------------------------------------------------------
 
+_BF, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _refuse(name, t, dtype, shape):
     if t.dtype != dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
@@ -345,22 +350,23 @@ def _refuse(name, t, dtype, shape):
 
 def _arg(name, t, dtype, shape, dev):
     """Pointer of a required argument, checked: dtype, shape, contiguous, on
-    device dev (-1, no device, is refused for every tensor)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+    device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         _refuse(name, t, dtype, shape)
     return t.data_ptr()
 
 
-def _opt(name, t, dtype, shape, dev):
-    """The same for an optional argument (None -> NULL)."""
-    return None if t is None else _arg(name, t, dtype, shape, dev)
-
-
-def _device():
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _rows(h, x, dtype, name):
+    """rows, shape, device and pointer of the call's tokens x [..., C] (h: the
+    handle, for C channels), checked: dtype, contiguous, on the current device."""
+    shape = x.shape
+    C = shape[-1]
+    if C != h.C:
+        raise ValueError("the handle is for C = %d, not %d" % (h.C, C))
+    dev = x.get_device()
+    if x.dtype is not dtype or dev < 0 or dev != _current_device() or not x.is_contiguous():
+        _refuse(name, x, dtype, shape)
+    return x.numel() // C, shape, dev, x.data_ptr()
 
 
 def _stream_on(stream, dev):
@@ -370,18 +376,10 @@ def _stream_on(stream, dev):
     return _stream(stream)
 
 
-def _rows(h, x):
-    """rows of x [..., C], C; h: the handle, for C channels."""
-    C = x.shape[-1]
-    if C != h.C:
-        raise ValueError("the handle is for C = %d, not %d" % (h.C, C))
-    return x.numel() // C, C
-
-
 def swin_block_rms_create(C, eps=1e-6):
     h = ctypes.c_void_p()
     _check("swin_block_rms_create", load().swin_block_rms_create(ctypes.byref(h), C, eps))
-    h.C = C
+    h.C, h.vec = C, (C,)
     return h
 
 
@@ -396,32 +394,33 @@ def swin_block_rms_last_launches(h):
 def swin_block_rms_forward(h, x, gamma, out, residual=None, out_sum=None, stream=None):
     """out = RMS norm of x + residual over the last axis of x [..., C]; out_sum
     receives the sum."""
-    rows, C = _rows(h, x)
-    bf, shape, dev = torch.bfloat16, x.shape, _device()
-    return _check("swin_block_rms_forward", load().swin_block_rms_forward(
-        h, _arg("x", x, bf, shape, dev), _opt("residual", residual, bf, shape, dev), rows,
-        _arg("gamma", gamma, bf, (C,), dev), _opt("out_sum", out_sum, bf, shape, dev),
-        _arg("out", out, bf, shape, dev), _stream_on(stream, dev)))
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    rc = (_lib or load()).swin_block_rms_forward(
+        h, px, None if residual is None else _arg("residual", residual, _BF, shape, dev), rows,
+        _arg("gamma", gamma, _BF, h.vec, dev), None if out_sum is None else _arg("out_sum", out_sum, _BF, shape, dev),
+        _arg("out", out, _BF, shape, dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_rms_forward", rc)
 
 
 def swin_block_rms_forward_q8(h, x, gamma, out8, scales, residual=None, out_sum=None, stream=None):
     """The same in e4m3 codes out8 [..., C] with one fp32 scale a row."""
-    rows, C = _rows(h, x)
-    bf, shape, dev = torch.bfloat16, x.shape, _device()
-    return _check("swin_block_rms_forward_q8", load().swin_block_rms_forward_q8(
-        h, _arg("x", x, bf, shape, dev), _opt("residual", residual, bf, shape, dev), rows,
-        _arg("gamma", gamma, bf, (C,), dev), _opt("out_sum", out_sum, bf, shape, dev),
-        _arg("out8", out8, torch.float8_e4m3fn, shape, dev), _arg("scales", scales, torch.float32, shape[:-1], dev),
-        _stream_on(stream, dev)))
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    rc = (_lib or load()).swin_block_rms_forward_q8(
+        h, px, None if residual is None else _arg("residual", residual, _BF, shape, dev), rows,
+        _arg("gamma", gamma, _BF, h.vec, dev), None if out_sum is None else _arg("out_sum", out_sum, _BF, shape, dev),
+        _arg("out8", out8, _E4M3, shape, dev), _arg("scales", scales, _F32, shape[:-1], dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_rms_forward_q8", rc)
 
 
 def swin_block_rms_backward(h, s, gamma, dy, dx, dgamma, dsum=None, stream=None):
-    rows, C = _rows(h, s)
-    bf, shape, dev = torch.bfloat16, s.shape, _device()
-    return _check("swin_block_rms_backward", load().swin_block_rms_backward(
-        h, _arg("s", s, bf, shape, dev), rows, _arg("gamma", gamma, bf, (C,), dev), _arg("dy", dy, bf, shape, dev),
-        _opt("dsum", dsum, bf, shape, dev), _arg("dx", dx, bf, shape, dev),
-        _arg("dgamma", dgamma, torch.float32, (C,), dev), _stream_on(stream, dev)))
+    """dx and dgamma from s [..., C] (the forward's out_sum, or x), dy and the
+    gradient dsum that reaches the sum past the norm."""
+    rows, shape, dev, ps = _rows(h, s, _BF, "s")
+    rc = (_lib or load()).swin_block_rms_backward(
+        h, ps, rows, _arg("gamma", gamma, _BF, h.vec, dev), _arg("dy", dy, _BF, shape, dev),
+        None if dsum is None else _arg("dsum", dsum, _BF, shape, dev), _arg("dx", dx, _BF, shape, dev),
+        _arg("dgamma", dgamma, _F32, h.vec, dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_rms_backward", rc)
 
 
 # ---- swin_gated.h ------------------------------------------------------------------
@@ -436,18 +435,22 @@ class GatedParamsQ8(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("Wg8", "sg", "bg", "Wu8", "su", "bu", "Wd", "bd")]
 
 
+def _bias(name, t, shape, dev):
+    return None if t is None else _arg(name, t, _BF, shape, dev)
+
+
 def _gated_params(h, p, dev):
     """The parameters' checked pointers, in the struct."""
-    bf, wide, F = torch.bfloat16, (h.F, h.C), (h.F,)
-    return GatedParams(_arg("Wg", p["Wg"], bf, wide, dev), _opt("bg", p.get("bg"), bf, F, dev),
-                       _arg("Wu", p["Wu"], bf, wide, dev), _opt("bu", p.get("bu"), bf, F, dev),
-                       _arg("Wd", p["Wd"], bf, (h.C, h.F), dev), _opt("bd", p.get("bd"), bf, (h.C,), dev))
+    get = p.get
+    return GatedParams(_arg("Wg", p["Wg"], _BF, h.wide, dev), _bias("bg", get("bg"), h.hidden, dev),
+                       _arg("Wu", p["Wu"], _BF, h.wide, dev), _bias("bu", get("bu"), h.hidden, dev),
+                       _arg("Wd", p["Wd"], _BF, h.down, dev), _bias("bd", get("bd"), h.vec, dev))
 
 
 def swin_block_gated_create(C, F, act=BLOCK_GATED_SILU):
     h = ctypes.c_void_p()
     _check("swin_block_gated_create", load().swin_block_gated_create(ctypes.byref(h), C, F, act))
-    h.C, h.F = C, F
+    h.C, h.F, h.vec, h.hidden, h.wide, h.down = C, F, (C,), (F,), (F, C), (C, F)
     return h
 
 
@@ -466,39 +469,40 @@ def swin_block_gated_sync_status(h, stream=None):
 def swin_block_gated_forward(h, x, params, out, residual=None, stream=None):
     """out = residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd for x [..., C];
     params: dict with Wg, bg, Wu, bu, Wd, bd (biases may be None)."""
-    rows, _ = _rows(h, x)
-    bf, shape, dev = torch.bfloat16, x.shape, _device()
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
     p = _gated_params(h, params, dev)
-    return _check("swin_block_gated_forward", load().swin_block_gated_forward(
-        h, _arg("x", x, bf, shape, dev), rows, ctypes.addressof(p), _opt("residual", residual, bf, shape, dev),
-        _arg("out", out, bf, shape, dev), _stream_on(stream, dev)))
+    rc = (_lib or load()).swin_block_gated_forward(
+        h, px, rows, ctypes.addressof(p), None if residual is None else _arg("residual", residual, _BF, shape, dev),
+        _arg("out", out, _BF, shape, dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_gated_forward", rc)
 
 
 def swin_block_gated_forward_q8(h, x8, sx, params, out, residual=None, stream=None):
     """The same from e4m3 x8 [..., C] with scales sx [...]; params: dict with Wg8,
     sg, bg, Wu8, su, bu, Wd, bd (biases may be None)."""
-    rows, _ = _rows(h, x8)
-    bf, f32, e4m3, shape, dev = torch.bfloat16, torch.float32, torch.float8_e4m3fn, x8.shape, _device()
-    wide, F = (h.F, h.C), (h.F,)
-    p = GatedParamsQ8(_arg("Wg8", params["Wg8"], e4m3, wide, dev), _arg("sg", params["sg"], f32, F, dev),
-                      _opt("bg", params.get("bg"), bf, F, dev), _arg("Wu8", params["Wu8"], e4m3, wide, dev),
-                      _arg("su", params["su"], f32, F, dev), _opt("bu", params.get("bu"), bf, F, dev),
-                      _arg("Wd", params["Wd"], bf, (h.C, h.F), dev), _opt("bd", params.get("bd"), bf, (h.C,), dev))
-    return _check("swin_block_gated_forward_q8", load().swin_block_gated_forward_q8(
-        h, _arg("x8", x8, e4m3, shape, dev), _arg("sx", sx, f32, shape[:-1], dev), rows, ctypes.addressof(p),
-        _opt("residual", residual, bf, shape, dev), _arg("out", out, bf, shape, dev), _stream_on(stream, dev)))
+    rows, shape, dev, px = _rows(h, x8, _E4M3, "x8")
+    get = params.get
+    p = GatedParamsQ8(_arg("Wg8", params["Wg8"], _E4M3, h.wide, dev), _arg("sg", params["sg"], _F32, h.hidden, dev),
+                      _bias("bg", get("bg"), h.hidden, dev), _arg("Wu8", params["Wu8"], _E4M3, h.wide, dev),
+                      _arg("su", params["su"], _F32, h.hidden, dev), _bias("bu", get("bu"), h.hidden, dev),
+                      _arg("Wd", params["Wd"], _BF, h.down, dev), _bias("bd", get("bd"), h.vec, dev))
+    rc = (_lib or load()).swin_block_gated_forward_q8(
+        h, px, _arg("sx", sx, _F32, shape[:-1], dev), rows, ctypes.addressof(p),
+        None if residual is None else _arg("residual", residual, _BF, shape, dev), _arg("out", out, _BF, shape, dev),
+        _stream_on(stream, dev))
+    return rc and _check("swin_block_gated_forward_q8", rc)
 
 
 def swin_block_gated_backward(h, x, params, dy, dx, grads, stream=None):
     """Gradients of the bf16 form: dx and, in the tensors of dict grads, dWg, dWu,
     dWd and (where not None) dbg, dbu, dbd, all bf16."""
-    rows, _ = _rows(h, x)
-    bf, shape, dev = torch.bfloat16, x.shape, _device()
-    wide, F = (h.F, h.C), (h.F,)
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
     p = _gated_params(h, params, dev)
-    g = GatedParams(_arg("dWg", grads["dWg"], bf, wide, dev), _opt("dbg", grads.get("dbg"), bf, F, dev),
-                    _arg("dWu", grads["dWu"], bf, wide, dev), _opt("dbu", grads.get("dbu"), bf, F, dev),
-                    _arg("dWd", grads["dWd"], bf, (h.C, h.F), dev), _opt("dbd", grads.get("dbd"), bf, (h.C,), dev))
-    return _check("swin_block_gated_backward", load().swin_block_gated_backward(
-        h, _arg("x", x, bf, shape, dev), rows, ctypes.addressof(p), _arg("dy", dy, bf, shape, dev),
-        _arg("dx", dx, bf, shape, dev), ctypes.addressof(g), _stream_on(stream, dev)))
+    get = grads.get
+    g = GatedParams(_arg("dWg", grads["dWg"], _BF, h.wide, dev), _bias("dbg", get("dbg"), h.hidden, dev),
+                    _arg("dWu", grads["dWu"], _BF, h.wide, dev), _bias("dbu", get("dbu"), h.hidden, dev),
+                    _arg("dWd", grads["dWd"], _BF, h.down, dev), _bias("dbd", get("dbd"), h.vec, dev))
+    rc = (_lib or load()).swin_block_gated_backward(
+        h, px, rows, ctypes.addressof(p), _arg("dy", dy, _BF, shape, dev), _arg("dx", dx, _BF, shape, dev),
+        ctypes.addressof(g), _stream_on(stream, dev))
+    return rc and _check("swin_block_gated_backward", rc)
