@@ -24,7 +24,7 @@ namespace swin {
 namespace {
 
 constexpr int FUSED_GROUPS = 2, FUSED_GROUP_WARPS = 8;
-constexpr int FUSED_THREADS = 64 + 32 * FUSED_GROUPS * FUSED_GROUP_WARPS;
+constexpr int FUSED_THREADS = 128 + 32 * FUSED_GROUPS * FUSED_GROUP_WARPS;   // a loading warp, two issuing ones, one idle
 constexpr int FUSED_CHUNK = 64;
 constexpr int FUSED_SLOTS = 12;   // most weight chunks in the ring
 
@@ -150,72 +150,74 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
         }
     } else if (warp == 1) {
-        // ---------------- MMAs (the leader's) ----------------
+        // ---------------- g | u MMAs (the leader's) ----------------
+        // A warp of their own: their buffer is free as soon as its group has read
+        // it, and the group's next chunk is ready when it is done with this one,
+        // whatever the last product waits for.
         if (rank == 0) {
-            const uint32_t idesc1 = idesc_pair(MMA_BF16, false, false, 256, 128);
-            const uint32_t idesc2 = idesc_pair(MMA_BF16, false, false, 256, 0) | (uint32_t)(a.n2 >> 3) << 17;
-            const uint32_t x16 = smem_u32(sx) >> 4, h16 = smem_u32(sh) >> 4, w16 = smem_u32(sw) >> 4;
-            const int total = my * a.chunks;
-            int i1 = 0, c1 = 0, i2 = 0, c2 = 0;   // tile (of this pair) and chunk of the two products
-            RingPos w1, w2;
-            // g | u run two chunks ahead of the last product: their buffer is
-            // free as soon as its group has read it, and the group's next chunk
-            // is there when it is done with this one
+            const uint32_t idesc = idesc_pair(MMA_BF16, false, false, 256, 128);
+            const uint32_t x16 = smem_u32(sx) >> 4, w16 = smem_u32(sw) >> 4;
+            int q = 0;
+            RingPos w;
 #pragma unroll 1
-            for (int q = 0; q < total + 2 && !failed; ++q) {
-                if (q < total) {   // g | u of chunk q
+            for (int i = 0; i < my && !failed; ++i) {
+                if (!warp_pair_wait(smem_u32(&bars.xfull[i & 1]), (uint32_t)(i >> 1) & 1u, limit)) failed = true;
+                if (a.resident) w = RingPos();
+#pragma unroll 1
+                for (int c = 0; c < a.chunks && !failed; ++c, ++q, w.next(a.slots)) {
                     const int b = q & 1;
-                    bool ok = c1 || warp_pair_wait(smem_u32(&bars.xfull[i1 & 1]), (uint32_t)(i1 >> 1) & 1u, limit);
-                    ok = ok && warp_pair_wait(smem_u32(&bars.wfull[w1.s]), a.resident ? 0u : w1.ph, limit);
-                    ok = ok && warp_pair_wait(smem_u32(&bars.gempty[b]), ((uint32_t)(q >> 1) & 1u) ^ 1u, limit);
-                    if (!ok) {
+                    if (!warp_pair_wait(smem_u32(&bars.wfull[w.s]), a.resident ? 0u : w.ph, limit) ||
+                        !warp_pair_wait(smem_u32(&bars.gempty[b]), ((uint32_t)(q >> 1) & 1u) ^ 1u, limit)) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
                     if (elect_one()) {
                         for (int k = 0; k < a.xb; ++k)
-                            mma_kblock<MMA_BF16, false, false>(tmem + 128 * b, x16 + (i1 & 1) * (x_bytes >> 4) + k * 1024,
-                                                               w16 + w1.s * (a.slot_bytes >> 4) + k * 512, idesc1,
+                            mma_kblock<MMA_BF16, false, false>(tmem + 128 * b, x16 + (i & 1) * (x_bytes >> 4) + k * 1024,
+                                                               w16 + w.s * (a.slot_bytes >> 4) + k * 512, idesc,
                                                                kblock_steps(a.C, k, 64), k == 0);
                         mma_commit_pair(smem_u32(&bars.gfull[b]));
-                        if (c1 == a.chunks - 1) mma_commit_pair(smem_u32(&bars.xempty[i1 & 1]));
-                    }
-                    w1.next(a.slots);
-                    if (++c1 == a.chunks) {
-                        c1 = 0;
-                        ++i1;
-                        if (a.resident) w1 = RingPos();
+                        if (c == a.chunks - 1) mma_commit_pair(smem_u32(&bars.xempty[i & 1]));
                     }
                 }
-                if (q >= 2) {   // the last product's part of chunk q - 2
-                    const int p = q - 2, b = p & 1, y = i2 & 1;
-                    bool ok = c2 || warp_pair_wait(smem_u32(&bars.yempty[y]), ((uint32_t)(i2 >> 1) & 1u) ^ 1u, limit);
-                    ok = ok && warp_pair_wait(smem_u32(&bars.hready[b]), (uint32_t)(p >> 1) & 1u, limit);
-                    if (!ok) {
+            }
+        }
+    } else if (warp == 2) {
+        // ---------------- the last product's MMAs (the leader's) ----------------
+        if (rank == 0) {
+            const uint32_t idesc = idesc_pair(MMA_BF16, false, false, 256, 0) | (uint32_t)(a.n2 >> 3) << 17;
+            const uint32_t h16 = smem_u32(sh) >> 4, w16 = (smem_u32(sw) >> 4) + a.xb * 512;
+            int q = 0;
+            RingPos w;
+#pragma unroll 1
+            for (int i = 0; i < my && !failed; ++i) {
+                const int y = i & 1;
+                if (!warp_pair_wait(smem_u32(&bars.yempty[y]), ((uint32_t)(i >> 1) & 1u) ^ 1u, limit)) failed = true;
+                if (a.resident) w = RingPos();
+#pragma unroll 1
+                for (int c = 0; c < a.chunks && !failed; ++c, ++q, w.next(a.slots)) {
+                    const int b = q & 1;
+                    if (!warp_pair_wait(smem_u32(&bars.wfull[w.s]), a.resident ? 0u : w.ph, limit) ||
+                        !warp_pair_wait(smem_u32(&bars.hready[b]), (uint32_t)(q >> 1) & 1u, limit)) {
                         failed = true;
                         break;
                     }
                     tc_fence_after();
                     if (elect_one()) {
-                        mma_kblock<MMA_BF16, false, false>(TY + 128 * y, h16 + b * 1024,
-                                                           w16 + w2.s * (a.slot_bytes >> 4) + a.xb * 512, idesc2, 4, c2 == 0);
+                        mma_kblock<MMA_BF16, false, false>(TY + 128 * y, h16 + b * 1024, w16 + w.s * (a.slot_bytes >> 4),
+                                                           idesc, 4, c == 0);
                         mma_commit_pair(smem_u32(&bars.hfree[b]));
-                        if (!a.resident) mma_commit_pair(smem_u32(&bars.wempty[w2.s]));
-                        if (c2 == a.chunks - 1) mma_commit_pair(smem_u32(&bars.yfull[y]));
-                    }
-                    w2.next(a.slots);
-                    if (++c2 == a.chunks) {
-                        c2 = 0;
-                        ++i2;
-                        if (a.resident) w2 = RingPos();
+                        // (g and u of this chunk were done before its h was)
+                        if (!a.resident) mma_commit_pair(smem_u32(&bars.wempty[w.s]));
+                        if (c == a.chunks - 1) mma_commit_pair(smem_u32(&bars.yfull[y]));
                     }
                 }
             }
         }
-    } else {
+    } else if (warp >= 4) {
         // ---------------- activations and output ----------------
-        const int e = warp - 2, grp = e / FUSED_GROUP_WARPS, quad = warp & 3, half = (e % FUSED_GROUP_WARPS) >> 2;
+        const int e = warp - 4, grp = e / FUSED_GROUP_WARPS, quad = warp & 3, half = (e % FUSED_GROUP_WARPS) >> 2;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint8_t *hbuf = sh + grp * 16384, *stage = stg + e * 2048;
         const uint32_t gempty = map_rank(smem_u32(&bars.gempty[grp]), 0), hready = map_rank(smem_u32(&bars.hready[grp]), 0);
