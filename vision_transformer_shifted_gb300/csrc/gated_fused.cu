@@ -287,8 +287,10 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
 
         int pending = -1;   // tile whose output this group has yet to drain
         int i = grp / a.chunks, c = grp % a.chunks;
-        float bg, bu;   // of this lane's hidden unit in this group's next chunk
+        float bg = 0.f, bu = 0.f;   // of this lane's hidden unit in this group's next chunk
+        const bool biased = a.bg || a.bu;
         auto fetch_biases = [&](int chunk) {
+            if (!biased) return;
             const int f = chunk * FUSED_CHUNK + half * 32 + lane;
             bg = lane_value(a.bg, f, a.F);
             bu = lane_value(a.bu, f, a.F);
@@ -309,7 +311,9 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             vec[lane] = bg;
             vec[32 + lane] = bu;
             // (the next chunk's, a chunk ahead)
-            fetch_biases((c + FUSED_GROUPS) % a.chunks);
+            int next = c + FUSED_GROUPS;
+            while (next >= a.chunks) next -= a.chunks;
+            fetch_biases(next);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
