@@ -9,9 +9,13 @@
  * act: SWIN_BLOCK_GATED_SILU g / (1 + exp(-g)) or SWIN_BLOCK_GATED_GELU, the
  * exact GELU g Phi(g) of the block's MLP.  bf16 tensors, products on the tensor
  * cores with fp32 accumulation, activation and product in fp32; h is rounded to
- * bf16 once between the two kernels (both first projections, the activation
+ * bf16 once before the last product.  Both first projections, the activation
  * and the product are one kernel, the last projection with its bias and the
- * residual the other).  Conventions of swin_wattn.h: device pointers,
+ * residual a second (for C <= 128 and more than 128 rows all of it is one
+ * kernel and h stays on chip; up to 128 rows take kernels of their own).  The
+ * kernels may start while the kernel queued before them finishes (programmatic
+ * dependent launch) but touch no memory before it has: a call needs no
+ * guarantee about its parameters.  Conventions of swin_wattn.h: device pointers,
  * asynchronous on `stream`, caller-owned tensors, status codes SWIN_WATTN_*,
  * no CPU fallback.
  */
@@ -54,13 +58,15 @@ typedef struct swin_block_gated_grads {
 } swin_block_gated_grads;
 
 /* C and F multiples of 8, at most 65536.  *out receives the handle (NULL on
- * failure).  EINVAL for bad arguments.  The handle belongs to the device that
- * is current at its first call that launches; calls with another current
- * device return EINVAL.  One handle may be used on several streams (its calls
- * are ordered by an event: they share its workspace) but not from two host
- * threads at once.  A call captured into a CUDA graph takes its workspace from
- * the graph's own memory, so graphs share nothing with each other or with
- * eager calls; make the handle's first call before any capture. */
+ * failure).  EINVAL for bad arguments, ENOMEM if the handle's 4-byte device
+ * error word cannot be allocated.  The handle belongs to the device that is
+ * current when it is created; calls with another current device return EINVAL
+ * (without a device it can be created, and every call that would launch
+ * returns ECUDA).  One handle may be used on several streams (its calls are
+ * ordered by an event: they share its workspace) but not from two host threads
+ * at once.  A call captured into a CUDA graph takes its workspace from the
+ * graph's own memory, so graphs share nothing with each other or with eager
+ * calls. */
 int swin_block_gated_create(swin_block_gated_t *out, int C, int F, int act);
 
 /* out = residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd.

@@ -11,7 +11,7 @@
  * starts from it, differentiates the very function that ran.  8-bit output:
  * scale = max(max_c |y|, 1e-30) / 448 per row (fp32), code = y / scale in e4m3
  * (round to nearest even; 448 is its largest value), y ~ code * scale.  A row
- * of zeros gets zero codes and a positive scale; a row holding an infinity or
+ * of zeros (eps > 0) gets zero codes and a positive scale; a row holding an infinity or
  * a NaN gets NaN codes and a NaN scale.
  *
  * Beside swin_stage_norm (LayerNorm): the other norm of the residual stream,

@@ -10,6 +10,7 @@
 #ifndef SWIN_WATTN_TEST_H
 #define SWIN_WATTN_TEST_H
 
+#include "swin_gated.h"
 #include "swin_wattn.h"
 
 #ifdef __cplusplus
@@ -75,6 +76,18 @@ int swin_wattn_test_watchdog(swin_wattn_t h, swin_stream_t stream);
  * swin_wattn_forward_noalloc, with a wait limit of wait_limit_us (1 us to
  * 60 s): swin_wattn_noalloc_sync_status then returns ETIMEOUT once. */
 int swin_wattn_test_noalloc_watchdog(int64_t wait_limit_us, swin_stream_t stream);
+
+/* Runs the gated block's first kernel (swin_gated.h) for rows > 128 with loads
+ * that are announced and never issued, and a wait limit of wait_limit_us (1 us
+ * to 1 s), so that its bounded waits run out: the CTA pairs give up, free their
+ * tensor memory and return, and swin_block_gated_sync_status then returns
+ * ETIMEOUT once.  x [rows, C] and p as swin_block_gated_forward; nothing but
+ * the handle's workspace is written. */
+int swin_block_gated_test_stall(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
+                                int64_t wait_limit_us, swin_stream_t stream);
+
+/* swin_wattn_test_corrupt_workspace for a gated block's handle. */
+int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side);
 
 #ifdef __cplusplus
 }

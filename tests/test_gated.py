@@ -16,6 +16,7 @@ and du.  Those are worst cases, so the relative error in the 2-norm is held
 too: two roundings of at most 2^-8 each, the inner one averaged over a sum.
 """
 import ctypes
+import os
 
 import pytest
 import torch
@@ -402,6 +403,114 @@ def test_streams_and_captured_graphs_share_nothing(rows):
         torch.cuda.synchronize()
         sw.swin_block_gated_sync_status(h)
         assert same(graphs[0][2], want2) and same(graphs[1][2], want2) and same(eager, want)
+
+
+@pytest.mark.gpu
+def test_first_call_of_a_handle_captured():
+    """A handle's first call may be the captured one."""
+    rows, C, F = 300, 256, 384
+    x, p, r, _ = make(rows, C, F, seed=11)
+    ref, tol = forward_ref(x, p, r, "silu")
+    xd, pd, rd, out = dev(x), dev(p), dev(r), torch.zeros(rows, C, dtype=BF, device=DEV)
+    with gated(C, F) as h:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        for _ in range(2):
+            gr.replay()
+        sw.swin_block_gated_sync_status(h)
+        close(out, ref, tol)
+        del gr
+        torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """A hidden activation of more than 2^31 elements: the last rows, forward and
+    backward."""
+    rows, C, F = 33000, 136, 65536
+    g = torch.Generator(device=DEV).manual_seed(5)
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=DEV) * std).to(BF)  # noqa: E731
+    p = dict(Wg=n(F, C, std=C ** -0.5), Wu=n(F, C, std=C ** -0.5), Wd=n(C, F, std=F ** -0.5), bg=None, bu=None, bd=None)
+    x, dy = n(rows, C), n(rows, C)
+    out, dx, grads = torch.empty_like(x), torch.empty_like(x), new_grads(p)
+    with gated(C, F) as h:
+        sw.swin_block_gated_forward(h, x, p, out)
+        sw.swin_block_gated_backward(h, x, p, dy, dx, grads)
+        sw.swin_block_gated_sync_status(h)
+    host = {k: None if v is None else v.cpu() for k, v in p.items()}
+    tail = slice(rows - 9, rows)
+    ref, tol = forward_ref(x[tail].cpu(), host, None, "silu")
+    close(out[tail], ref, tol)
+    ref, tol = backward_ref(x[tail].cpu(), host, dy[tail].cpu(), "silu")
+    close(dx[tail], ref["dx"], tol["dx"])
+    assert all(torch.isfinite(v).all() for v in grads.values() if v is not None)
+
+
+class env:
+    def __init__(self, name):
+        self.name = name
+
+    def __enter__(self):
+        os.environ[self.name] = "1"
+
+    def __exit__(self, *exc):
+        del os.environ[self.name]
+
+
+@pytest.mark.gpu
+def test_simulated_allocation_failure_then_a_normal_call():
+    rows, C, F = 200, 192, 256
+    x, p, _, dy = make(rows, C, F, seed=12)
+    xd, pd, yd = dev(x), dev(p), dev(dy)
+    out, grads = torch.full_like(xd, 5.0), new_grads(p)
+    with gated(C, F) as h:
+        with env("SWIN_WATTN_FAIL_ALLOC"):
+            for call in (lambda: sw.swin_block_gated_forward(h, xd, pd, out),
+                         lambda: sw.swin_block_gated_backward(h, xd, pd, yd, out, grads)):
+                with pytest.raises(sw.SwinWAttnError) as ei:
+                    call()
+                assert ei.value.code == sw.ENOMEM
+        torch.cuda.synchronize()
+        assert (out == 5).all()
+        sw.swin_block_gated_forward(h, xd, pd, out)
+        sw.swin_block_gated_sync_status(h)
+    ref, tol = forward_ref(x, p, None, "silu")
+    close(out, ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", [(1, 96, 256), (70, 264, 520), (300, 1032, 2056), (700, 136, 264)])
+def test_guard_bands_stay_intact_and_catch_an_overwrite(rows, C, F):
+    x, p, r, dy = make(rows, C, F, seed=13)
+    xd, pd, rd, yd = dev(x), dev(p), dev(r), dev(dy)
+    out, dx, grads = torch.empty_like(xd), torch.empty_like(xd), new_grads(p)
+    with env("SWIN_WATTN_DEBUG"), gated(C, F) as h:   # the bands are read back after each call
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        sw.swin_block_gated_backward(h, xd, pd, yd, dx, grads)
+        for side in (0, 1):
+            sw.swin_block_gated_test_corrupt_workspace(h, side)
+            with pytest.raises(sw.SwinWAttnError) as ei:
+                sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+            assert ei.value.code == sw.ECORRUPT
+
+
+@pytest.mark.gpu
+def test_bounded_waits_run_out():
+    """Loads that never come: every role gives up, the status says so once, and
+    the next call on the handle is right."""
+    rows, C, F = 600, 256, 384
+    x, p, r, _ = make(rows, C, F, seed=14)
+    xd, pd, rd, out = dev(x), dev(p), dev(r), torch.empty(rows, C, dtype=BF, device=DEV)
+    with gated(C, F) as h:
+        sw.swin_block_gated_test_stall(h, xd, pd, 20000)
+        with pytest.raises(sw.SwinWAttnError) as ei:
+            sw.swin_block_gated_sync_status(h)
+        assert ei.value.code == sw.ETIMEOUT
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        assert sw.swin_block_gated_sync_status(h) == sw.OK
+    ref, tol = forward_ref(x, p, r, "silu")
+    close(out, ref, tol)
 
 
 @pytest.mark.gpu

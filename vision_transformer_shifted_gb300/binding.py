@@ -80,6 +80,8 @@ _SIGNATURES = {
     "swin_block_gated_last_launches": ["p"],
     "swin_block_gated_sync_status": ["p", "p"],
     "swin_block_gated_destroy": ["p"],
+    "swin_block_gated_test_stall": ["p", "p", "i", "p", "l", "p"],
+    "swin_block_gated_test_corrupt_workspace": ["p", "i"],
 }
 
 # swin_block_params (include/swin_block.h), field for field
@@ -506,3 +508,14 @@ def swin_block_gated_backward(h, x, params, dy, dx, grads, stream=None):
         h, px, rows, ctypes.addressof(p), _arg("dy", dy, _BF, shape, dev), _arg("dx", dx, _BF, shape, dev),
         ctypes.addressof(g), _stream_on(stream, dev))
     return rc and _check("swin_block_gated_backward", rc)
+
+
+def swin_block_gated_test_stall(h, x, params, wait_limit_us, stream=None):
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    p = _gated_params(h, params, dev)
+    return _check("swin_block_gated_test_stall", load().swin_block_gated_test_stall(
+        h, px, rows, ctypes.addressof(p), int(wait_limit_us), _stream_on(stream, dev)))
+
+
+def swin_block_gated_test_corrupt_workspace(h, side):
+    return _check("swin_block_gated_test_corrupt_workspace", load().swin_block_gated_test_corrupt_workspace(h, side))

@@ -9,6 +9,7 @@
 #include <new>
 
 #include "swin_gated.h"
+#include "swin_wattn_test.h"
 #include "common.cuh"
 #include "gated.cuh"
 
@@ -16,7 +17,7 @@ using namespace swin;
 
 struct swin_block_gated_s {
     int C, F, act;
-    int device;   // -1: not bound yet
+    int device;   // -1: created without one
     int *d_err;
     int last_launches;
     OrderedWorkspace ws;
@@ -354,10 +355,16 @@ struct Carve {
     }
 };
 
+// UpPolicy whose loads never come: a test of the bounded waits.
+struct StallPolicy : UpPolicy<ACT_SILU, false> {
+    static __device__ __forceinline__ void load(const Args &, const Unit &, int, int, uint32_t, uint32_t, uint32_t) {}
+};
+
+// (stall: with StallPolicy)
 template <bool Q8>
 cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *sx, int rows, const void *wg,
                       const float *sg, const void *bg, const void *wu, const float *su, const void *bu, bf16 *hidden,
-                      DeviceStatus st, cudaStream_t stream)
+                      DeviceStatus st, cudaStream_t stream, bool stall = false)
 {
     if (rows <= FEW_ROWS) {
         FewUp u{};
@@ -401,19 +408,16 @@ cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *s
         a.st = st;
         return launch_pair<P>(a, stream);
     };
+    if (stall) return run(StallPolicy{});
     return h->act == SWIN_BLOCK_GATED_SILU ? run(UpPolicy<ACT_SILU, Q8>{}) : run(UpPolicy<ACT_GELU, Q8>{});
 }
 
-int first_call(swin_block_gated_s *h)
+// The handle's device is the current one.
+int check_device(const swin_block_gated_s *h)
 {
-    const int rc = bind_device(&h->device);
-    if (rc != SWIN_WATTN_OK || h->d_err) return rc;
-    if (cudaMalloc(&h->d_err, sizeof(int)) != cudaSuccess) {
-        cudaGetLastError();
-        h->d_err = nullptr;
-        return SWIN_WATTN_ENOMEM;
-    }
-    return cuda_status(cudaMemset(h->d_err, 0, sizeof(int)));
+    int dev = h->device;
+    if (dev < 0) return SWIN_WATTN_ECUDA;
+    return bind_device(&dev);
 }
 
 struct Span {
@@ -433,7 +437,7 @@ template <class Up>
 int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, const void *residual, void *out,
             cudaStream_t stream, Up &&up)
 {
-    int rc = first_call(h);
+    int rc = check_device(h);
     if (rc != SWIN_WATTN_OK) return rc;
     Product down{};
     down.k[0] = h->F;
@@ -488,6 +492,14 @@ int swin_block_gated_create(swin_block_gated_t *out, int C, int F, int act)
     h->F = F;
     h->act = act;
     h->device = -1;
+    if (bind_device(&h->device) != SWIN_WATTN_OK) h->device = -1;
+    if (h->device >= 0 &&
+        (cudaMalloc(&h->d_err, sizeof(int)) != cudaSuccess || cudaMemset(h->d_err, 0, sizeof(int)) != cudaSuccess)) {
+        cudaGetLastError();
+        if (h->d_err) cudaFree(h->d_err);
+        delete h;
+        return SWIN_WATTN_ENOMEM;
+    }
     *out = h;
     return SWIN_WATTN_OK;
 }
@@ -532,7 +544,7 @@ int swin_block_gated_forward(swin_block_gated_t h, const void *x, int rows, cons
                                {residual == out ? nullptr : residual, n}}))
         return SWIN_WATTN_EINVAL;
     if (rows > FEW_ROWS && gated_fused_supported(h->C)) {
-        const int rc = first_call(h);
+        const int rc = check_device(h);
         if (rc != SWIN_WATTN_OK) return rc;
         h->last_launches = 1;
         return cuda_status(launch_gated_fused((const bf16 *)x, rows, h->C, h->F, h->act == SWIN_BLOCK_GATED_GELU,
@@ -589,7 +601,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         for (int j = 0; j < i; ++j)
             if (any_overlap(outs[i], {outs[j]})) return SWIN_WATTN_EINVAL;
     }
-    int rc = first_call(h);
+    int rc = check_device(h);
     if (rc != SWIN_WATTN_OK) return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if (rows == 0) {
@@ -701,6 +713,33 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     }
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
+}
+
+// ---- test hooks (swin_wattn_test.h) ------------------------------------------------
+
+int swin_block_gated_test_stall(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
+                                int64_t wait_limit_us, swin_stream_t stream)
+{
+    if (!h || !p || rows <= FEW_ROWS || rows > MAX_ROWS || wait_limit_us < 1 || wait_limit_us > 1000000)
+        return SWIN_WATTN_EINVAL;
+    for (const void *q : {x, p->Wg, p->Wu})
+        if (bad_pointer(q, true)) return SWIN_WATTN_EINVAL;
+    int rc = check_device(h);
+    if (rc != SWIN_WATTN_OK) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    void *ws = nullptr;
+    bool captured = false;
+    if ((rc = ows_begin(&h->ws, (size_t)rows * hidden_ld(h->F) * 2, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    const cudaError_t e = launch_up<false>(h, x, nullptr, rows, p->Wg, nullptr, nullptr, p->Wu, nullptr, nullptr, (bf16 *)ws,
+                                           DeviceStatus{h->d_err, (uint64_t)wait_limit_us * 1000}, s, true);
+    const int rc2 = ows_end(&h->ws, s, ws, captured);
+    return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
+}
+
+int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side)
+{
+    if (!h || side < 0 || side > 1) return SWIN_WATTN_EINVAL;
+    return ws_test_corrupt(h->ws.buf, side);
 }
 
 } // extern "C"
