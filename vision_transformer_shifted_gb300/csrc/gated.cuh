@@ -218,6 +218,12 @@ struct UpPolicy {
         tile_order(pair + n * a.np, a.mt, a.nt, r.m, r.n);
         return r;
     }
+    static __device__ __forceinline__ void prefetch_maps(const Args &a, int, uint32_t rank)
+    {
+        prefetch_map(&a.x);
+        prefetch_map(rank ? &a.wu : &a.wg);
+        prefetch_map(&a.h);
+    }
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int) { return 2 * STAGE_BYTES; }
     static __device__ __forceinline__ void load(const Args &a, const Unit &u, int, int kb, uint32_t rank, uint32_t dst,
@@ -400,6 +406,14 @@ struct GemmPolicy {
         r.kb_first = p.kb[0];
         return r;
     }
+    static __device__ __forceinline__ void prefetch_maps(const Args &a, int pair, uint32_t)
+    {
+        const Unit u = decode(a, pair, 0);
+        const int seg = u.kb0 >= u.kb_first;
+        prefetch_map(&a.p[u.p].a[seg]);
+        prefetch_map(&a.p[u.p].b[seg]);
+        prefetch_map(u.slot >= 0 ? &a.part : &a.p[u.p].d);
+    }
     static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int) { return 2 * STAGE_BYTES; }
     template <bool MN, int ROWS>
@@ -577,6 +591,13 @@ struct GradPolicy {
         Unit r;
         tile_order(pair + n * a.np, a.mt, a.nt, r.m, r.n);
         return r;
+    }
+    static __device__ __forceinline__ void prefetch_maps(const Args &a, int, uint32_t rank)
+    {
+        prefetch_map(&a.dy);
+        prefetch_map(&a.wd);
+        prefetch_map(&a.x);
+        prefetch_map(rank ? &a.wu : &a.wg);
     }
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int seg)

@@ -29,6 +29,7 @@
 //   slot(seg, n), slot_col(slot), slot_use(seg, n)   the slot of the n-th unit
 //                           of this pair, its first column, how often it was used
 //   kblocks(a, u, seg), tx(a, u, seg), load(...), mma(...)
+//   prefetch_maps(a, pair, rank)   fetches the tensor maps this CTA begins with
 //   Pre, prefetch(...), epilogue(...)   what an epilogue thread fetches before
 //                           the accumulators are ready, and the epilogue
 #pragma once
@@ -246,6 +247,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         }
         mbar_init_fence();
     }
+    if (warp == 0 && elect_one()) P::prefetch_maps(a, pair, rank);
     if (warp == 1) tmem_alloc_pair(smem_u32(tslot), 512);
     tc_fence_before();
     __syncthreads();
