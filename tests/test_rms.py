@@ -215,7 +215,7 @@ def test_backward(rows, C, with_dsum):
     gx, gg = torch.full_like(sd, float("nan")), torch.full((C,), float("nan"), device=DEV)
     with rms(C) as h:
         sw.swin_block_rms_backward(h, sd, gd, yd, gx, gg, dsum=md)
-        assert sw.swin_block_rms_last_launches(h) == 2
+        assert sw.swin_block_rms_last_launches(h) in (1, 2)
         again = torch.empty_like(gg)
         sw.swin_block_rms_backward(h, sd, gd, yd, gx, again, dsum=md)
     close(gx, dx, 2.0 ** -8 * dx.abs() + FP * size)

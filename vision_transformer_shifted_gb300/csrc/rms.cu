@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs 
 struct RmsBwdArgs {
     const bf16 *s, *dy, *dsum, *gamma;
     bf16 *dx;
-    float *partial;   // [gridDim.x, C]: each block's share of dgamma
+    float *partial;   // [gridDim.x, C]: each block's share of dgamma (one block: dgamma itself)
     int rows, chunks;
     float inv_c, eps;
     int lanes;        // of a row: of a warp, or (wide rows) threads
@@ -550,7 +550,9 @@ BwdPlan plan_backward(int rows, int C, bool with_dsum)
         p.smem = (size_t)8 * C * sizeof(float);
     }
     const int64_t want = (rows + rpb - 1) / rpb, most = sm_count() * per_sm;
-    p.grid = (int)(want < most ? want : most);
+    // few rows: one block, whose sums are dgamma (two turns at most: less than what
+    // the second launch would cost)
+    p.grid = want <= 2 ? 1 : (int)(want < most ? want : most);
     return p;
 }
 
@@ -571,7 +573,7 @@ cudaError_t launch_rms_backward(RmsBwdArgs a, const BwdPlan &p, float *dgamma, c
         (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem)) != cudaSuccess)
         return e;
     e = launch_maybe_overlapped(kern, dim3(p.grid), dim3(p.threads), p.smem, stream, 1, a);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.grid == 1) return e;
     return launch_maybe_overlapped(column_sum_kernel, dim3((C + 31) / 32), dim3(1024), 0, stream, 1,
                                    (const float *)a.partial, p.grid, C, dgamma);
 }
@@ -716,19 +718,21 @@ int swin_block_rms_backward(swin_block_rms_t h, const void *s, int rows, const v
     const BwdPlan p = plan_backward(rows, h->C, dsum != nullptr);
     void *ws = nullptr;
     bool captured = false;
-    if ((rc = ows_begin(&h->ws, (size_t)p.grid * h->C * sizeof(float), st, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    if (p.grid > 1 &&
+        (rc = ows_begin(&h->ws, (size_t)p.grid * h->C * sizeof(float), st, &ws, &captured)) != SWIN_WATTN_OK)
+        return rc;
     RmsBwdArgs a{};
     a.s = (const bf16 *)s;
     a.dy = (const bf16 *)dy;
     a.dsum = (const bf16 *)dsum;
     a.gamma = (const bf16 *)gamma;
     a.dx = (bf16 *)dx;
-    a.partial = (float *)ws;
+    a.partial = p.grid > 1 ? (float *)ws : dgamma;
     a.rows = rows;
     a.chunks = h->C / 8;
     a.inv_c = 1.f / (float)h->C;
     a.eps = h->eps;
-    h->last_launches = 2;
+    h->last_launches = p.grid > 1 ? 2 : 1;
     rc = cuda_status(launch_rms_backward(a, p, dgamma, st));
     const int rc2 = ows_end(&h->ws, st, ws, captured);
     return rc != SWIN_WATTN_OK ? rc : rc2;
