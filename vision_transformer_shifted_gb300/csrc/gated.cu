@@ -81,8 +81,9 @@ struct Product {
 };
 
 // The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
-// of K (+ bias + residual), `blocks` blocks a tile (16, and up to 64 where few
-// tiles have many partial tiles each).
+// of K (+ bias + residual).  `blocks` blocks a tile and VEC values a thread at a
+// time: 16 and eight, or (few tiles, of many partial tiles each) 64 and four;
+// 3 tiles of 25 partial tiles: 9 us, 15 by sixteen blocks.
 struct JoinArgs {
     const float *part;
     PairSplit split;
@@ -93,6 +94,32 @@ struct JoinArgs {
         int rows, cols, mt, nt, first;
     } p[3];
 };
+template <int VEC>
+__device__ __forceinline__ void add_vec(float (&v)[VEC], const float *p)
+{
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + k);
+        v[k] += w.x;
+        v[k + 1] += w.y;
+        v[k + 2] += w.z;
+        v[k + 3] += w.w;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void add_vec(float (&v)[VEC], const bf16 *p)
+{
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p + k);
+        const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
+        v[k] += x.x;
+        v[k + 1] += x.y;
+        v[k + 2] += y.x;
+        v[k + 3] += y.y;
+    }
+}
+template <int VEC>
 __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
 {
     const PairSplit &s = a.split;
@@ -102,33 +129,27 @@ __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
     const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
     int m, n;
     tile_order(t - a.p[i].first, a.p[i].mt, a.p[i].nt, m, n);
-    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / 4;
+    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / VEC;
     const int64_t size = 256 * a.tn;
     const int first = s.slot(p0, c);
     for (int e = block % a.blocks * 256 + threadIdx.x; e < 256 * per; e += a.blocks * 256) {
-        const int row = m * 256 + e / per, col = n * a.tn + e % per * 4;
+        const int row = m * 256 + e / per, col = n * a.tn + e % per * VEC;
         if (row >= rows || col >= cols) continue;
-        const float *src = a.part + (int64_t)e * 4;
-        float4 v = *reinterpret_cast<const float4 *>(src + first * size);
-#pragma unroll 8
-        for (int p = p0 + 1; p <= p1; ++p) {   // (these begin inside the tile: their first range)
-            const float4 w = *reinterpret_cast<const float4 *>(src + 2 * p * size);
-            v.x += w.x;
-            v.y += w.y;
-            v.z += w.z;
-            v.w += w.w;
-        }
+        const float *src = a.part + (int64_t)e * VEC;
+        float v[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = 0.f;
+        add_vec<VEC>(v, src + first * size);
+#pragma unroll 4
+        for (int p = p0 + 1; p <= p1; ++p)   // (these begin inside the tile: their first range)
+            add_vec<VEC>(v, src + 2 * p * size);
         const int64_t at = (int64_t)row * cols + col;
-        for (const bf16 *q : {a.p[i].bias ? a.p[i].bias + col : nullptr, a.p[i].residual ? a.p[i].residual + at : nullptr}) {
-            if (!q) continue;
-            const uint2 u = *reinterpret_cast<const uint2 *>(q);
-            const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
-            v.x += x.x;
-            v.y += x.y;
-            v.z += y.x;
-            v.w += y.y;
-        }
-        *reinterpret_cast<uint2 *>(a.p[i].out + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        if (a.p[i].bias) add_vec<VEC>(v, a.p[i].bias + col);
+        if (a.p[i].residual) add_vec<VEC>(v, a.p[i].residual + at);
+#pragma unroll
+        for (int k = 0; k < VEC; k += 4)
+            *reinterpret_cast<uint2 *>(a.p[i].out + at + k) =
+                make_uint2(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]));
     }
 }
 
@@ -191,16 +212,15 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
     griddep_launch_dependents();
     griddep_wait();
     int b = blockIdx.x;
-    if (b < a.joins[0]) {
-        join_tiles(a.join[0], b);
-        return;
+    for (int i = 0; i < 2; ++i) {
+        if (b < a.joins[i]) {
+            if (a.join[i].blocks == 16) join_tiles<8>(a.join[i], b);
+            else join_tiles<4>(a.join[i], b);
+            return;
+        }
+        b -= a.joins[i];
     }
-    b -= a.joins[0];
-    if (b < a.joins[1]) {
-        join_tiles(a.join[1], b);
-        return;
-    }
-    column_partials(a.cs, b - a.joins[1]);
+    column_partials(a.cs, b);
 }
 cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launches)
 {
@@ -327,7 +347,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     ++*launches;
     r.part = part;
     r.tn = TN;
-    r.blocks = pl.split.cut >= 32 ? 16 : pl.split.cut >= 16 ? 32 : 64;
+    r.blocks = pl.split.cut >= 16 ? 16 : 64;
     fin->joins[slot] = pl.split.cut * r.blocks;
     return launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
 }
@@ -404,7 +424,12 @@ cudaError_t launch_up(const swin_block_gated_s *h, const void *x, const float *s
         a.mt = ceil_div(rows, 256);
         a.nt = ceil_div(h->F, 128);
         a.kb = ceil_div(h->C, P::ELEMS);
-        a.np = a.mt * a.nt < sm_count() / 2 ? a.mt * a.nt : sm_count() / 2;
+        a.deal = deal_tiles(a.mt * a.nt, sm_count() / 2);
+        a.np = a.deal.np;
+        if (a.deal.parts > 1) {
+            if ((e = map_k(&a.wg_part, wg, h->F, h->C, 128 / a.deal.parts, Q8)) != cudaSuccess) return e;
+            if ((e = map_k(&a.wu_part, wu, h->F, h->C, 128 / a.deal.parts, Q8)) != cudaSuccess) return e;
+        }
         a.st = st;
         return launch_pair<P>(a, stream);
     };
@@ -685,7 +710,12 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         a.mt = ceil_div(rows, 256);
         a.nt = ceil_div(h->F, 128);
         a.kb = ceil_div(h->C, 64);
-        a.np = a.mt * a.nt < sm_count() / 2 ? a.mt * a.nt : sm_count() / 2;
+        a.deal = deal_tiles(a.mt * a.nt, sm_count() / 2);
+        a.np = a.deal.np;
+        if (a.deal.parts > 1) {
+            if ((e = map_k(&a.wg_part, p->Wg, h->F, h->C, 128 / a.deal.parts)) != cudaSuccess) return e;
+            if ((e = map_k(&a.wu_part, p->Wu, h->F, h->C, 128 / a.deal.parts)) != cudaSuccess) return e;
+        }
         a.st = st;
         return launch_pair<P>(a, s);
     };

@@ -196,26 +196,31 @@ template <int ACT, bool Q8>
 struct UpPolicy {
     struct Args {
         CUtensorMap x, wg, wu, h;
+        CUtensorMap wg_part, wu_part;   // boxes of a part of a tile's columns
         const bf16 *bg, *bu;
         const float *sx, *sg, *su;   // Q8
         int rows, C, F, mt, nt, kb, np;
+        PairDeal deal;
         DeviceStatus st;
     };
     struct Unit {
-        int m, n;
+        int m, col, width;   // row tile, first hidden column, columns
     };
     static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
     static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 2, STAGING = 2560, SEGS = 1;
-    static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 256);
+    static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 0);   // (N: 2 width)
 
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
     static __device__ __forceinline__ int slot_use(int, int n) { return n >> 1; }
     static __device__ __forceinline__ int slot_col(int s) { return s * 256; }
-    static __device__ __forceinline__ int count(const Args &a, int pair) { return deal_count(a.mt * a.nt, a.np, pair); }
+    static __device__ __forceinline__ int count(const Args &a, int pair) { return a.deal.count(pair); }
     static __device__ __forceinline__ Unit decode(const Args &a, int pair, int n)
     {
         Unit r;
-        tile_order(pair + n * a.np, a.mt, a.nt, r.m, r.n);
+        int col, nt;
+        const int t = a.deal.tile(pair, n, col, r.width);
+        tile_order(t, a.mt, a.nt, r.m, nt);
+        r.col = nt * 128 + col;
         return r;
     }
     static __device__ __forceinline__ void prefetch_maps(const Args &a, int, uint32_t rank)
@@ -225,22 +230,28 @@ struct UpPolicy {
         prefetch_map(&a.h);
     }
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
-    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int) { return 2 * STAGE_BYTES; }
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int) { return 2 * (16384 + 128 * u.width); }
     static __device__ __forceinline__ void load(const Args &a, const Unit &u, int, int kb, uint32_t rank, uint32_t dst,
                                                 uint32_t bar)
     {
         tma_load_2d_pair(dst, &a.x, kb * ELEMS, u.m * 256 + (int)rank * 128, bar);
-        tma_load_2d_pair(dst + 16384, rank ? &a.wu : &a.wg, kb * ELEMS, u.n * 128, bar);
+        tma_load_2d_pair(dst + 16384, weight_map(a, u, rank), kb * ELEMS, u.col, bar);
     }
-    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int, int kb, uint32_t src16, uint32_t d)
+    static __device__ __forceinline__ const CUtensorMap *weight_map(const Args &a, const Unit &u, uint32_t rank)
     {
-        mma_kblock<Q8 ? MMA_E4M3 : MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC, kblock_steps(a.C, kb, ELEMS),
-                                                           kb == 0);
+        return u.width == 128 ? (rank ? &a.wu : &a.wg) : (rank ? &a.wu_part : &a.wg_part);
+    }
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int, int kb, uint32_t src16, uint32_t d)
+    {
+        mma_kblock<Q8 ? MMA_E4M3 : MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC | (uint32_t)(u.width >> 2) << 17,
+                                                           kblock_steps(a.C, kb, ELEMS), kb == 0);
     }
     struct Pre {
         float bg[2], bu[2], sg[2], su[2], sx;   // of this lane's column of each box of 32, and its row's scale
     };
-    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.n * 128 + part * 64 + 32 * j; }
+    // a part's columns of the unit (64; in a narrower unit 32): its first, boxes of 32
+    static __device__ __forceinline__ int part_col(const Unit &u, int part) { return part * (u.width == 128 ? 64 : 32); }
+    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.col + part_col(u, part) + 32 * j; }
     static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int, int quad, int part,
                                                    int lane, uint8_t *)
     {
@@ -265,15 +276,21 @@ struct UpPolicy {
                                                     uint8_t *staging, Release &&release)
     {
         const int row0 = u.m * 256 + (int)rank * 128 + quad * 32;
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * 64;
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part_col(u, part);
+        const int boxes = u.width == 128 ? 2 : part_col(u, part) < u.width;
+        if (boxes == 0) {
+            release();
+            return;
+        }
         // the warps' boxes (aligned for their swizzle), then the warps' vectors
         uint8_t *stage = staging + warp * 2048;
         float *vec = reinterpret_cast<float *>(staging + EPI * 2048 + warp * 512);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+            if (j == boxes) break;
             float g[32], v[32];
             tmem_ld32(acc + 32 * j, g);
-            tmem_ld32(acc + 128 + 32 * j, v);
+            tmem_ld32(acc + u.width + 32 * j, v);
             __syncwarp();
             vec[lane] = pre.bg[j];
             vec[32 + lane] = pre.bu[j];
@@ -283,7 +300,7 @@ struct UpPolicy {
             }
             staging_free(lane);   // (and the vectors are there)
             tmem_wait_ld();
-            if (j == 1) release();
+            if (j == boxes - 1) release();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float *gq = g + 8 * q, *vq = v + 8 * q;
@@ -569,27 +586,32 @@ template <int ACT>
 struct GradPolicy {
     struct Args {
         CUtensorMap x, wg, wu, dy, wd, h, dg, du;
+        CUtensorMap wg_part, wu_part;   // boxes of a part of a tile's columns
         const bf16 *bg, *bu;
         float *dg_sums, *du_sums;   // [row blocks of 32][F]: sums of dg and du, or null
         int rows, C, F, mt, nt, kb, np;
+        PairDeal deal;
         DeviceStatus st;
     };
     struct Unit {
-        int m, n;
+        int m, col, width;   // row tile, first hidden column, columns
     };
     static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 1, STAGING = 4096 + 64, SEGS = 2;
-    static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 128);
-    static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 256);
+    static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 0);    // (N: width)
+    static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 0);  // (N: 2 width)
 
     // segment 0 (dh): slots 1 and 2 in turn; segment 1 (g | u): slot 0
     static __device__ __forceinline__ int slot(int seg, int n) { return seg ? 0 : 1 + (n & 1); }
     static __device__ __forceinline__ int slot_use(int seg, int n) { return seg ? n : n >> 1; }
     static __device__ __forceinline__ int slot_col(int s) { return s == 0 ? 0 : 128 + 128 * s; }
-    static __device__ __forceinline__ int count(const Args &a, int pair) { return deal_count(a.mt * a.nt, a.np, pair); }
+    static __device__ __forceinline__ int count(const Args &a, int pair) { return a.deal.count(pair); }
     static __device__ __forceinline__ Unit decode(const Args &a, int pair, int n)
     {
         Unit r;
-        tile_order(pair + n * a.np, a.mt, a.nt, r.m, r.n);
+        int col, nt;
+        const int t = a.deal.tile(pair, n, col, r.width);
+        tile_order(t, a.mt, a.nt, r.m, nt);
+        r.col = nt * 128 + col;
         return r;
     }
     static __device__ __forceinline__ void prefetch_maps(const Args &a, int, uint32_t rank)
@@ -600,9 +622,9 @@ struct GradPolicy {
         prefetch_map(rank ? &a.wu : &a.wg);
     }
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
-    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int seg)
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int seg)
     {
-        return seg ? 2 * STAGE_BYTES : 2 * (16384 + 8192);
+        return 2 * (16384 + (seg ? 128 * u.width : 8192));   // (Wd: 64 columns are loaded whatever the unit uses)
     }
     static __device__ __forceinline__ void load(const Args &a, const Unit &u, int seg, int kb, uint32_t rank,
                                                 uint32_t dst, uint32_t bar)
@@ -610,17 +632,19 @@ struct GradPolicy {
         const int row = u.m * 256 + (int)rank * 128;
         if (seg == 0) {
             tma_load_2d_pair(dst, &a.dy, kb * 64, row, bar);
-            tma_load_2d_pair(dst + 16384, &a.wd, u.n * 128 + (int)rank * 64, kb * 64, bar);
+            tma_load_2d_pair(dst + 16384, &a.wd, u.col + (int)rank * (u.width / 2), kb * 64, bar);
         } else {
             tma_load_2d_pair(dst, &a.x, kb * 64, row, bar);
-            tma_load_2d_pair(dst + 16384, rank ? &a.wu : &a.wg, kb * 64, u.n * 128, bar);
+            tma_load_2d_pair(dst + 16384, u.width == 128 ? (rank ? &a.wu : &a.wg) : (rank ? &a.wu_part : &a.wg_part), kb * 64,
+                             u.col, bar);
         }
     }
-    static __device__ __forceinline__ void mma(const Args &a, const Unit &, int seg, int kb, uint32_t src16, uint32_t d)
+    static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int seg, int kb, uint32_t src16, uint32_t d)
     {
         const int steps = kblock_steps(a.C, kb, 64);
-        if (seg == 0) mma_kblock<MMA_BF16, false, true>(d, src16, src16 + 1024, IDESC_H, steps, kb == 0);
-        else mma_kblock<MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC_GU, steps, kb == 0);
+        const uint32_t w = (uint32_t)(u.width >> 3) << 17;
+        if (seg == 0) mma_kblock<MMA_BF16, false, true>(d, src16, src16 + 1024, IDESC_H | w, steps, kb == 0);
+        else mma_kblock<MMA_BF16, false, false>(d, src16, src16 + 1024, IDESC_GU | 2 * w, steps, kb == 0);
     }
     struct Pre {
         bf16 bg, bu;   // of this lane's column
@@ -628,7 +652,7 @@ struct GradPolicy {
     static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t, int, int, int part, int lane,
                                                    uint8_t *)
     {
-        const int c = u.n * 128 + part * 32 + lane;
+        const int c = u.col + part * 32 + lane;
         Pre p;
         p.bg = a.bg && c < a.F ? a.bg[c] : __float2bfloat16_rn(0.f);
         p.bu = a.bu && c < a.F ? a.bu[c] : __float2bfloat16_rn(0.f);
@@ -639,7 +663,11 @@ struct GradPolicy {
                                                     int warp, int quad, int part, int lane, uint32_t t_lane,
                                                     uint8_t *staging, Release &&release)
     {
-        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.n * 128 + part * 32;
+        if (part * 32 >= u.width) {   // (a narrow unit: the last of its pair)
+            release();
+            return;
+        }
+        const int row0 = u.m * 256 + (int)rank * 128 + quad * 32, col0 = u.col + part * 32;
         const uint32_t gu = t_lane + part * 32, dh = t_lane + slot_col(slot(0, n)) + part * 32;
         const bool inside = row0 < a.rows && col0 < a.F;
         uint4 du[4];
@@ -656,7 +684,7 @@ struct GradPolicy {
         for (int j = 0; j < 2; ++j) {
             float g[16], v[16], d[16];
             tmem_ld16(gu + 16 * j, g);
-            tmem_ld16(gu + 128 + 16 * j, v);
+            tmem_ld16(gu + u.width + 16 * j, v);
             tmem_ld16(dh + 16 * j, d);
             tmem_wait_ld();
             if (j == 1) release();

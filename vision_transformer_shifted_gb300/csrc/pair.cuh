@@ -219,6 +219,35 @@ __device__ __forceinline__ int deal_count(int tiles, int np, int pair)
     return pair < tiles ? (tiles - pair + np - 1) / np : 0;
 }
 
+// The same with a last round that would leave half of the pairs idle or more
+// dealt out as halves or quarters of its tiles' columns (`parts`): unit n of a
+// pair is tile t, from column `col` on, `width` of 128 columns.
+struct PairDeal {
+    int tiles, np;
+    int full, parts;   // rounds of whole tiles; parts of a tile in the round after them
+    __device__ __forceinline__ int count(int pair) const
+    {
+        return parts == 1 ? deal_count(tiles, np, pair) : full + (pair < (tiles - full * np) * parts);
+    }
+    __device__ __forceinline__ int tile(int pair, int n, int &col, int &width) const
+    {
+        const bool whole = parts == 1 || n < full;
+        width = whole ? 128 : 128 / parts;
+        col = whole ? 0 : pair % parts * width;
+        return whole ? pair + n * np : full * np + pair / parts;
+    }
+};
+inline PairDeal deal_tiles(int tiles, int pairs)
+{
+    PairDeal d{};
+    d.tiles = tiles;
+    d.full = tiles / pairs;
+    const int rest = tiles - d.full * pairs;
+    d.parts = rest == 0 ? 1 : 4 * rest <= pairs ? 4 : 2 * rest <= pairs ? 2 : 1;
+    d.np = d.full ? pairs : rest * d.parts;
+    return d;
+}
+
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * P::EPI, 1)
 pair_kernel(const __grid_constant__ typename P::Args a)
