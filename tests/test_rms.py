@@ -347,3 +347,31 @@ def test_streams_and_captured_graphs_share_nothing():
         for _, _, o in graphs:   # both on the second inputs
             assert torch.equal(o[0], want2[0]) and torch.equal(o[1], want2[1])
         assert torch.equal(eager[0], want[0]) and torch.equal(eager[1], want[1])
+
+
+@pytest.mark.gpu
+def test_two_host_threads_with_a_handle_each():
+    """Handles of different widths used from two threads at once: what one call
+    asks of a kernel (its shared memory) does not take from the other's."""
+    import threading
+    failures = []
+
+    def work(C, rows):
+        try:
+            s, _, g, dy = dev(*inputs(rows, C, False, seed=C))
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            with rms(C) as h, torch.cuda.stream(stream):
+                dx, dg = torch.empty_like(s), torch.empty(C, device=DEV)
+                for _ in range(400):
+                    sw.swin_block_rms_backward(h, s, g, dy, dx, dg)
+                stream.synchronize()
+        except Exception as e:
+            failures.append((C, e))
+
+    threads = [threading.Thread(target=work, args=a) for a in ((1000, 8), (16384, 8), (10000, 3))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures

@@ -569,8 +569,10 @@ cudaError_t launch_rms_backward(RmsBwdArgs a, const BwdPlan &p, float *dgamma, c
     else
         kern = r.cpl == 3 ? rms_backward_wide_kernel<3, false> : rms_backward_wide_kernel<4, false>;
     cudaError_t e;
+    // (always the most any call needs: another thread may be between its setting
+    // and its launch)
     if (r.block &&
-        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem)) != cudaSuccess)
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 6 * r.cpl * 16)) != cudaSuccess)
         return e;
     e = launch_maybe_overlapped(kern, dim3(p.grid), dim3(p.threads), p.smem, stream, 1, a);
     if (e != cudaSuccess || p.grid == 1) return e;
