@@ -32,7 +32,7 @@ struct FusedArgs {
     CUtensorMap x, wg, wu, wd, out;
     const bf16 *bg, *bu, *bd, *residual;
     int rows, C, F, tiles, np;
-    int xb, n2;              // K blocks of a token; N of the last product (C rounded up to 16)
+    int xb, n2;              // K blocks of a token; N of the last product (C rounded up to 32: a pair's step)
     int chunks, slots, slot_bytes;
     bool resident;           // every chunk has its slot: loaded once
     DeviceStatus st;
@@ -388,7 +388,7 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     FusedArgs a;
     memset(&a, 0, sizeof(a));
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    a.n2 = (C + 15) / 16 * 16;
+    a.n2 = (C + 31) / 32 * 32;
     a.xb = (C + 63) / 64;
     a.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
     a.slot_bytes = a.xb * 8192 + a.n2 * 64;
