@@ -563,3 +563,52 @@ def test_run_of_norm_and_gated_block(q8):
             for got, want in [(ds, ss.grad), (dgamma, gg.grad)] + [(grads["d" + k], v.grad) for k, v in leaves.items()]:
                 assert float((got.double().cpu() - want).norm() / want.norm()) <= 4 * HALF
     sw.swin_block_rms_destroy(hn)
+
+
+@pytest.mark.gpu
+def test_bias_gradients_of_infinite_units_leave_out_the_rows_behind():
+    """A hidden unit whose u is infinite for every token: its dg is +inf in every
+    row, and so is their sum; the zero rows that fill the last tile are not in
+    it (there zero times infinity would be NaN)."""
+    rows, C, F = 130, 64, 128
+    x, p, _, dy = make(rows, C, F, seed=15)
+    x, dy, p["Wd"] = x.abs() + 0.5, dy.abs() + 0.5, p["Wd"].abs() + 0.1
+    p["Wg"] = p["Wg"].abs()   # act'(g) > 0 for every g of a positive row
+    p["bg"].zero_()
+    p["Wu"][5], p["bu"][9] = float("inf"), float("inf")
+    p["Wu"][5] = p["Wu"][5].abs()
+    dx, grads = torch.empty_like(dev(x)), new_grads(p)
+    with gated(C, F) as h:
+        sw.swin_block_gated_backward(h, dev(x), dev(p), dev(dy), dx, grads)
+        sw.swin_block_gated_sync_status(h)
+    dbg = grads["dbg"].cpu()
+    assert dbg[5] == float("inf") and dbg[9] == float("inf")
+    assert torch.isfinite(dbg[[i for i in range(F) if i not in (5, 9)]]).all()
+    assert torch.isfinite(grads["dbu"]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", [(5001, 144, 520), (5100, 144, 512), (19700, 144, 2056)])
+def test_rounds_of_whole_tiles_and_a_last_one_in_parts(rows, C, F):
+    """More tiles than CTA pairs, the last round thin: dealt out by halves and by
+    quarters of tiles, or (the last product of the third) cut along K."""
+    x, p, r, dy = make(rows, C, F, seed=16)
+    ref, tol = forward_ref(x, p, r, "silu")
+    xd, pd, rd, yd = dev(x), dev(p), dev(r), dev(dy)
+    out, dx, grads = torch.full_like(xd, float("nan")), torch.full_like(xd, float("nan")), new_grads(p)
+    x8, sx = quantise(x)
+    q = dict(bg=p["bg"], bu=p["bu"], Wd=p["Wd"], bd=p["bd"])
+    (q["Wg8"], q["sg"]), (q["Wu8"], q["su"]) = quantise(p["Wg"]), quantise(p["Wu"])
+    exact = dict(p, Wg=q["Wg8"].double() * q["sg"].double()[:, None], Wu=q["Wu8"].double() * q["su"].double()[:, None])
+    ref8, tol8 = forward_ref(x8.double() * sx.double()[:, None], exact, r, "silu")
+    out8 = torch.full_like(xd, float("nan"))
+    with gated(C, F) as h:
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        sw.swin_block_gated_forward_q8(h, dev(x8), dev(sx), dev(q), out8, residual=rd)
+        sw.swin_block_gated_backward(h, xd, pd, yd, dx, grads)
+        sw.swin_block_gated_sync_status(h)
+    close(out, ref, tol)
+    close(out8, ref8, tol8)
+    ref, tol = backward_ref(x, p, dy, "silu")
+    for k, v in dict(grads, dx=dx).items():
+        close(v, ref[k], tol[k])

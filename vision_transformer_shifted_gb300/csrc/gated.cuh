@@ -716,6 +716,10 @@ struct GradPolicy {
                 du[2 * j + q] = pack8f(dq);
             }
             if (a.dg_sums) {
+                if (row0 + lane >= a.rows) {   // (no token: zero times an infinite parameter is not zero)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) g[e] = d[e] = 0.f;
+                }
                 const int c = col0 + 16 * j + (lane & 15);
                 const float sg = column_sum16(g, lane), su = column_sum16(d, lane);
                 if (lane < 16 && c < a.F) {
