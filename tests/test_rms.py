@@ -349,6 +349,28 @@ def test_streams_and_captured_graphs_share_nothing():
         assert torch.equal(eager[0], want[0]) and torch.equal(eager[1], want[1])
 
 
+def test_binding_refuses_more_rows_than_an_int_holds(monkeypatch):
+    """2^32 + 1 rows would reach the C side as one."""
+    class Tall:   # (what the check asks of a tensor: no such tensor fits here)
+        shape, dtype = torch.Size([(1 << 32) + 1, 8]), BF
+
+        def numel(self):
+            return 8 * ((1 << 32) + 1)
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return 0
+
+        def data_ptr(self):
+            return 1 << 24
+
+    monkeypatch.setattr(sw, "_current_device", lambda: 0)
+    with rms(8) as h, pytest.raises(ValueError, match="rows"):
+        sw.swin_block_rms_forward(h, Tall(), None, None)
+
+
 @pytest.mark.gpu
 def test_two_host_threads_with_a_handle_each():
     """Handles of different widths used from two threads at once: what one call

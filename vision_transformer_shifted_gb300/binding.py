@@ -368,7 +368,10 @@ def _rows(h, x, dtype, name):
     dev = x.get_device()
     if x.dtype is not dtype or dev < 0 or dev != _current_device() or not x.is_contiguous():
         _refuse(name, x, dtype, shape)
-    return x.numel() // C, shape, dev, x.data_ptr()
+    rows = x.numel() // C
+    if rows > 0x7fffffff:   # (the C side's int would wrap)
+        raise ValueError("%s has %d rows, more than 2^31 - 1" % (name, rows))
+    return rows, shape, dev, x.data_ptr()
 
 
 def _stream_on(stream, dev):
