@@ -11,8 +11,9 @@
  * cores with fp32 accumulation, activation and product in fp32; h is rounded to
  * bf16 once before the last product.  Both first projections, the activation
  * and the product are one kernel, the last projection with its bias and the
- * residual a second (for C <= 128 and more than 128 rows all of it is one
- * kernel and h stays on chip; up to 128 rows take kernels of their own).  The
+ * residual a second, sometimes with a third that joins tiles cut along F (the
+ * bf16 form for C <= 128 and more than 128 rows is one kernel, and h stays on
+ * chip; up to 128 rows take kernels of their own).  The
  * kernels may start while the kernel queued before them finishes (programmatic
  * dependent launch) but touch no memory before it has: a call needs no
  * guarantee about its parameters.  Conventions of swin_wattn.h: device pointers,
@@ -62,11 +63,11 @@ typedef struct swin_block_gated_grads {
  * error word cannot be allocated.  The handle belongs to the device that is
  * current when it is created; calls with another current device return EINVAL
  * (without a device it can be created, and every call that would launch
- * returns ECUDA).  One handle may be used on several streams (its calls are
+ * returns ECUDA); creating it allocates, so not while a stream is captured.  One handle may be used on several streams (its calls are
  * ordered by an event: they share its workspace) but not from two host threads
  * at once.  A call captured into a CUDA graph takes its workspace from the
  * graph's own memory, so graphs share nothing with each other or with eager
- * calls. */
+ * calls but the error word: a graph is replayed only while its handle lives. */
 int swin_block_gated_create(swin_block_gated_t *out, int C, int F, int act);
 
 /* out = residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd.

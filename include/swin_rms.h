@@ -7,7 +7,8 @@
  *   s = x + residual (rounded to bf16; s = x without a residual)
  *   r = 1 / sqrt(mean_c s^2 + eps)
  *   y = s r gamma
- * The norm sees the stored (rounded) sum, so that the backward pass, which
+ * (fp32: a row whose squares add up to more than 3.4e38 has r = 0.)  The norm
+ * sees the stored (rounded) sum, so that the backward pass, which
  * starts from it, differentiates the very function that ran.  8-bit output:
  * scale = max(max_c |y|, 1e-30) / 448 per row (fp32), code = y / scale in e4m3
  * (round to nearest even; 448 is its largest value), y ~ code * scale.  A row
