@@ -80,6 +80,10 @@ struct Product {
     int cols;
 };
 
+// A K block of half a tile (256 x 128) in hundredths of a whole one's: it loads
+// three quarters as much for half of the MMAs.
+constexpr int HALF_COST = 60;
+
 // The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
 // of K (+ bias + residual).  `blocks` blocks a tile and VEC values a thread at a
 // time: 16 and eight, or (few tiles, of many partial tiles each) 64 and four;
@@ -163,23 +167,24 @@ struct ColumnSums {
         bf16 *out;
         float *part;      // [splits, cols]
         int64_t rows;
-        int cols;
+        int cols, splits;
     } m[3];
-    int n, splits;
-    int blocks(int i) const { return (m[i].cols + 63) / 64 * splits; }
+    int n;
+    __host__ __device__ int blocks(int i) const { return (m[i].cols + 63) / 64 * m[i].splits; }
 };
+int column_splits(int64_t rows) { return rows < 64 * 32 ? ceil_div(rows, 32) : 64; }
 __device__ __forceinline__ void column_partials(const ColumnSums &a, int block)
 {
     __shared__ float sum[32][65];
     int z = 0;
-    for (; z + 1 < a.n && block >= (a.m[z].cols + 63) / 64 * a.splits; ++z) block -= (a.m[z].cols + 63) / 64 * a.splits;
+    for (; z + 1 < a.n && block >= a.blocks(z); ++z) block -= a.blocks(z);
     const auto &m = a.m[z];
-    const int cols = m.cols, c0 = block / a.splits * 64, y = block % a.splits;
+    const int cols = m.cols, c0 = block / m.splits * 64, y = block % m.splits;
     const int c = c0 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (c < cols) {
 #pragma unroll 4
-        for (int64_t i = (int64_t)y * 32 + r; i < m.rows; i += (int64_t)a.splits * 32) {
+        for (int64_t i = (int64_t)y * 32 + r; i < m.rows; i += (int64_t)m.splits * 32) {
             float w[8];
             if (m.f) load8(m.f + i * cols, c, cols, w);
             else load8(m.b + i * cols, c, cols, w);
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(1024) column_finish_kernel(const __grid_consta
     const int c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < m.cols)
-        for (int s = w; s < a.splits; s += 32) v += m.part[(int64_t)s * m.cols + c];
+        for (int s = w; s < m.splits; s += 32) v += m.part[(int64_t)s * m.cols + c];
     part[w][lane] = v;
     __syncthreads();
     v = part[lane][w];
@@ -259,7 +264,10 @@ struct ProductsPlan {
 // 128.  The last round is cut along K where that saves more K blocks than
 // joining the partial tiles costs (a launch and their traffic, about 5 us: 16
 // blocks of a 256 x 256 tile, 24 of a narrow one); few blocks in all go to as
-// many pairs as leave each at least four.
+// many pairs as leave each at least four.  A last round of at most half of the
+// pairs goes out as half tiles where that costs less: no join (1024 x 2048 x
+// 5632 forward 61.7 us cut, 57.5 in halves; 12544 x 512 x 1368 backward 140.6,
+// 135).
 ProductsPlan plan_products(const Product *p, int n)
 {
     ProductsPlan pl{};
@@ -278,7 +286,12 @@ ProductsPlan plan_products(const Product *p, int n)
     const int full = (int)(tiles / pairs), rest = (int)(tiles - (int64_t)full * pairs);
     const int64_t blocks = (int64_t)rest * s.kb;
     int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
-    if (rest && s.kb - ceil_div(blocks, np) > (pl.wide ? 16 : 24)) {
+    const int cut_cost = ceil_div(blocks, np) + (pl.wide ? 16 : 24);
+    if (pl.wide && rest && 2 * rest <= pairs && HALF_COST * s.kb <= 100 * (s.kb < cut_cost ? s.kb : cut_cost)) {
+        s.full = full;
+        s.halves = 2 * rest;
+        s.np = full ? pairs : s.halves;
+    } else if (rest && s.kb > cut_cost) {
         // Equal slices of every tile, where they cost at most a tenth more blocks:
         // pairs that share rows of an operand then walk K side by side, and each
         // reads what another has brought into L2.  (36 tiles, the weight gradients
@@ -334,6 +347,10 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
             e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols, p.ldb)
                      : map_k(&q.b[s], p.b[s], p.cols, p.k[s], TN / 2, false, p.ldb);
             if (e != cudaSuccess) return e;
+            if (!B_MN && pl.split.halves) {
+                e = map_k(&q.b_half[s], p.b[s], p.cols, p.k[s], TN / 4, false, p.ldb);
+                if (e != cudaSuccess) return e;
+            }
         }
         if ((e = map_out(&q.d, p.d, p.rows, p.cols)) != cudaSuccess) return e;
     }
@@ -661,7 +678,8 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     FinishArgs fin{};
     ColumnSums &cs = fin.cs;
     const int row_blocks = ceil_div(rows, 256) * 8;
-    cs.splits = ceil_div(rows, 256) < 64 ? ceil_div(rows, 256) : 64;
+    const int splits[3] = {column_splits(row_blocks), column_splits(row_blocks), column_splits(rows)};
+    const size_t sum_bytes = ((size_t)2 * splits[0] * h->F + (size_t)splits[2] * h->C) * sizeof(float);
     int most = 0;
     const size_t row_sums = g->dbg || g->dbu ? (size_t)row_blocks * h->F * sizeof(float) : 0;
     const size_t hid = (size_t)rows * hidden_ld(h->F) * 2;
@@ -670,7 +688,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     size.take(px.part_bytes);
     size.take(pw.part_bytes);
     for (int i = 0; i < 2; ++i) size.take(row_sums);
-    size.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
+    size.take(sum_bytes);
     void *ws = nullptr;
     bool captured = false;
     if ((rc = ows_begin(&h->ws, size.used, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
@@ -678,7 +696,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     bf16 *hidden = (bf16 *)carve.take(hid), *dg = (bf16 *)carve.take(hid), *du = (bf16 *)carve.take(hid);
     float *x_part = (float *)carve.take(px.part_bytes), *w_part = (float *)carve.take(pw.part_bytes);
     float *dg_sums = (float *)carve.take(row_sums), *du_sums = (float *)carve.take(row_sums);
-    float *sum_part = (float *)carve.take((size_t)cs.splits * (2 * h->F + h->C) * sizeof(float));
+    float *sum_part = (float *)carve.take(sum_bytes);
     dxp.a[0] = dw[0].a[0] = dg;
     dxp.a[1] = dw[1].a[0] = du;
     dw[2].b[0] = hidden;
@@ -733,7 +751,8 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         m.part = sum_part;
         m.rows = i < 2 ? row_blocks : rows;
         m.cols = i < 2 ? h->F : h->C;
-        sum_part += (size_t)cs.splits * m.cols;
+        m.splits = splits[i];
+        sum_part += (size_t)m.splits * m.cols;
         if (m.cols > most) most = m.cols;
     }
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);

@@ -337,12 +337,13 @@ struct UpPolicy {
 // problems run as one launch (the three weight gradients).
 //
 // Tiles are dealt to the pairs in rounds; a last round that would leave pairs
-// idle is instead cut along K: its tiles' K blocks, laid end to end, are split
+// idle is instead dealt out as half tiles, or cut along K: its tiles' K blocks, laid end to end, are split
 // evenly over the pairs, and a pair's ranges that hold only a part of a tile go
 // to fp32 partial tiles that a second kernel adds in the order of K.  (4096 x
 // 2048 x 5632's dx: 128 tiles on 76 pairs, 2 rounds of 176 blocks; cut, 1.68.)
 struct PairProblem {
     CUtensorMap a[2], b[2], d;
+    CUtensorMap b_half[2];         // K-major B: boxes for a half tile
     const bf16 *bias, *residual;   // [cols] / [rows, cols] or null
     int rows, cols, k[2], kb[2];
     int mt, nt, first;             // first: this problem's first tile
@@ -350,6 +351,7 @@ struct PairProblem {
 // The division of `tiles` tiles of kb K blocks each over np pairs.
 struct PairSplit {
     int tiles, np;
+    int halves;      // the round after the whole ones is tiles' halves (of their columns): how many
     int k_blocks;    // of a tile
     int kb;          // the same, or (equal slices) a multiple of the slices a little above
     int full;        // rounds of whole tiles
@@ -380,14 +382,15 @@ struct GemmPolicy {
         DeviceStatus st;
     };
     struct Unit {
-        int p, m, n, kb0, kbn;
+        int p, m, col, kb0, kbn;
+        int width;          // columns, from col: TN, or half of it
         int slot;           // partial tile to write (-1: the whole K, to D)
         int k0, kb_first;   // the first segment's K, and its blocks
     };
     static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 16, GROUPS = 1, STAGING = 4096, SEGS = 1;
     static constexpr int STAGES = TN == 256 ? 5 : 6;
     static constexpr int BOXES = TN / 128;   // a warp's share of the columns: boxes of 32
-    static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, TN);
+    static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, 0);   // (N: width)
 
     static __device__ __forceinline__ int slot(int, int n) { return n & 1; }
     static __device__ __forceinline__ int slot_use(int, int n) { return n >> 1; }
@@ -395,7 +398,7 @@ struct GemmPolicy {
     static __device__ __forceinline__ int count(const Args &a, int pair)
     {
         const PairSplit &s = a.split;
-        if (s.cut == 0) return deal_count(s.tiles, s.np, pair);
+        if (s.cut == 0) return s.full + (pair < s.halves) + (s.halves ? 0 : deal_count(s.tiles - s.full * s.np, s.np, pair));
         const uint32_t b0 = s.begin(pair), b1 = s.begin(pair + 1);
         return s.full + (b1 > b0 ? (int)((b1 - 1) / s.kb - b0 / s.kb) + 1 : 0);
     }
@@ -416,9 +419,14 @@ struct GemmPolicy {
             if (hi - lo < kb) r.slot = 2 * pair + (n > s.full);
             t = s.full * s.np + c;
         }
+        const bool half = s.halves && n >= s.full;
+        if (half) t = s.full * s.np + pair / 2;
         r.p = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
         const PairProblem &p = a.p[r.p];
-        tile_order(t - p.first, p.mt, p.nt, r.m, r.n);
+        int nt;
+        tile_order(t - p.first, p.mt, p.nt, r.m, nt);
+        r.width = half ? TN / 2 : TN;
+        r.col = nt * TN + (half ? pair % 2 * (TN / 2) : 0);
         r.k0 = p.k[0];
         r.kb_first = p.kb[0];
         return r;
@@ -432,7 +440,7 @@ struct GemmPolicy {
         prefetch_map(u.slot >= 0 ? &a.part : &a.p[u.p].d);
     }
     static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
-    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &, int) { return 2 * STAGE_BYTES; }
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int) { return 2 * (16384 + u.width * 64); }
     template <bool MN, int ROWS>
     static __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int k,
                                                         uint32_t bar)
@@ -452,25 +460,29 @@ struct GemmPolicy {
         const int seg = kb >= u.kb_first;
         if (seg) kb -= u.kb_first;
         load_operand<A_MN, 128>(dst, &p.a[seg], u.m * 256 + (int)rank * 128, kb * 64, bar);
-        load_operand<B_MN, TN / 2>(dst + 16384, &p.b[seg], u.n * TN + (int)rank * (TN / 2), kb * 64, bar);
+        const int row = u.col + (int)rank * (u.width / 2);
+        if (u.width == TN) load_operand<B_MN, TN / 2>(dst + 16384, &p.b[seg], row, kb * 64, bar);
+        else load_operand<B_MN, TN / 4>(dst + 16384, B_MN ? &p.b[seg] : &p.b_half[seg], row, kb * 64, bar);
     }
     static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int, int i, uint32_t src16, uint32_t d)
     {
         // (two segments are of one K: dg and du)
         int kb = u.kb0 + i;
         if (kb >= u.kb_first) kb -= u.kb_first;
-        mma_kblock<MMA_BF16, A_MN, B_MN>(d, src16, src16 + 1024, IDESC, kblock_steps(u.k0, kb, 64), i == 0);
+        mma_kblock<MMA_BF16, A_MN, B_MN>(d, src16, src16 + 1024, IDESC | (uint32_t)(u.width >> 3) << 17,
+                                         kblock_steps(u.k0, kb, 64), i == 0);
     }
     // Of a warp's two 2 KB boxes of staging, box j takes its columns 32 j ...:
     // before the accumulators are ready, the residual.
     struct Pre {
         float bias[BOXES];   // of this lane's column of each box
     };
+    static __device__ __forceinline__ int boxes(const Unit &u) { return u.width == TN ? BOXES : BOXES / 2; }
     static __device__ __forceinline__ int row_of(const Unit &u, uint32_t rank, int quad)
     {
         return u.m * 256 + (int)rank * 128 + quad * 32;
     }
-    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.n * TN + part * (TN / 4) + 32 * j; }
+    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.col + part * (u.width / 4) + 32 * j; }
     static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int warp, int quad,
                                                    int part, int lane, uint8_t *staging)
     {
@@ -482,6 +494,7 @@ struct GemmPolicy {
             staging_free(lane);
 #pragma unroll
             for (int j = 0; j < BOXES; ++j) {
+                if (j == boxes(u)) break;
                 const int col = col_of(u, part, j) + 8 * (lane & 3);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -504,7 +517,7 @@ struct GemmPolicy {
     {
         const PairProblem &p = a.p[u.p];
         uint8_t *stage = staging + warp * STAGING;
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (TN / 4);
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (u.width / 4);
         if (u.slot >= 0) {   // fp32 boxes of 16 columns, the two stagings in turn
 #pragma unroll 1
             for (int j = 0; j < 2 * BOXES; ++j) {
@@ -535,10 +548,11 @@ struct GemmPolicy {
         }
 #pragma unroll
         for (int j = 0; j < BOXES; ++j) {
+            if (j == boxes(u)) break;
             float v[32];
             tmem_ld32(acc + 32 * j, v);
             tmem_wait_ld();
-            if (j == BOXES - 1) release();
+            if (j == boxes(u) - 1) release();
             uint8_t *box = stage + j * 2048;
             if (p.bias) {
 #pragma unroll
