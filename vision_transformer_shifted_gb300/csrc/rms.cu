@@ -229,61 +229,76 @@ struct RmsBwdArgs {
 };
 
 // One thread's piece (eight channels) of a row in the backward, dx = r (a - n
-// mean(a n)) + dsum with n = s r, a = dy gamma.  First its shares of sum s^2
-// and sum a s:
-__device__ __forceinline__ void piece_sums(const uint4 &s, const uint4 &d, const uint4 &g, float2 &sq, float2 &dot)
+// mean(a n)) + dsum with n = s r, a = dy gamma, as pairs of channels.
+struct Piece {
+    f2 v[4];
+};
+__device__ __forceinline__ Piece piece(const uint4 &u)
 {
-    float v[8], y[8], w[8];
-    unpack8(s, v);
-    unpack8(d, y);
-    unpack8(g, w);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    Piece p;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        g2_fma(sq.x, sq.y, v[e], v[e + 1], v[e], v[e + 1], sq.x, sq.y);
-        g2_mul(y[e], y[e + 1], y[e], y[e + 1], w[e], w[e + 1]);
-        g2_fma(dot.x, dot.y, y[e], y[e + 1], v[e], v[e + 1], dot.x, dot.y);
+    for (int e = 0; e < 4; ++e) p.v[e] = pack2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+    return p;
+}
+// First its shares of sum s^2 and sum a s:
+__device__ __forceinline__ void piece_sums(const Piece &s, const Piece &d, const Piece &g, f2 &sq, f2 &dot)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sq = fma2(s.v[e], s.v[e], sq);
+        dot = fma2(mul2(d.v[e], g.v[e]), s.v[e], dot);
     }
 }
-// then, with q = mean(a n) r (so that n mean(a n) = s q), dx and its terms of dgamma.
-__device__ __forceinline__ uint4 piece_grad(const uint4 &s, const uint4 &d, const uint4 &g, const uint4 &m, float r,
-                                            float q, float (&acc)[8])
+// then, with q = mean(a n) r^2 (so that r n mean(a n) = s q), dx and its terms of
+// dgamma (dy r s).
+template <bool DSUM>
+__device__ __forceinline__ uint4 piece_grad(const Piece &s, const Piece &d, const Piece &g, const Piece &m, f2 r, f2 minus_q,
+                                            Piece &acc)
 {
-    float v[8], y[8], w[8], b[8];
-    unpack8(s, v);
-    unpack8(d, y);
-    unpack8(g, w);
-    unpack8(m, b);
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        float n0, n1, t0, t1;
-        g2_mul(n0, n1, v[e], v[e + 1], r, r);
-        g2_fma(acc[e], acc[e + 1], y[e], y[e + 1], n0, n1, acc[e], acc[e + 1]);
-        g2_mul(t0, t1, y[e], y[e + 1], w[e], w[e + 1]);
-        g2_fma(t0, t1, v[e], v[e + 1], -q, -q, t0, t1);
-        g2_fma(b[e], b[e + 1], t0, t1, r, r, b[e], b[e + 1]);
+    for (int e = 0; e < 4; ++e) {
+        const f2 dr = mul2(d.v[e], r);
+        acc.v[e] = fma2(dr, s.v[e], acc.v[e]);
+        const f2 t = DSUM ? fma2(dr, g.v[e], m.v[e]) : mul2(dr, g.v[e]);
+        float lo, hi;
+        unpack2(fma2(s.v[e], minus_q, t), lo, hi);
+        w[e] = pack_bf16x2(lo, hi);
     }
-    return pack8(b);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ float sum2(f2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return a + b;
+}
+
+// Blocks of 256 threads on an SM: enough bytes of loads in flight, and no more
+// (200000 x 512 with dsum, two pieces a lane: 130.5 us with two blocks, 131.5
+// with three, 142 with four; without dsum 114, 103 and 96; 589824 x 192 without
+// dsum, three pieces: 112 with two, 125 with three).
+constexpr int blocks_per_sm(int cpl, bool dsum) { return cpl > 2 || (cpl == 2 && dsum) ? 2 : 4; }
 
 // Rows on part of a warp: a block takes 8 * (32 / lanes) rows together, then the
 // ones gridDim.x on.  Each thread keeps the columns it owns of dgamma in
 // registers over its rows; the block writes one partial row at the end.
-template <int CPL>
-__global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsBwdArgs a)
+template <int CPL, bool DSUM>
+__global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) rms_backward_kernel(RmsBwdArgs a)
 {
     extern __shared__ float part[];   // [8 warps][C]
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = a.lanes, li = lane % step;
     const int rpw = 32 / step, rpb = 8 * rpw;
-    float acc[CPL][8];
+    Piece acc[CPL];
     uint4 g[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
         const int c = li + k * step;
         g[k] = c < a.chunks ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+        acc[k] = Piece{};
     }
     for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
         const int64_t row = r0 + warp * rpw + lane / step;
@@ -296,12 +311,12 @@ __global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsB
             const bool ok = row_ok && c < a.chunks;
             s[k] = ok ? ld16(a.s + base + c * 8) : make_uint4(0, 0, 0, 0);
             d[k] = ok ? ld16(a.dy + base + c * 8) : make_uint4(0, 0, 0, 0);
-            m[k] = ok && a.dsum ? ld16(a.dsum + base + c * 8) : make_uint4(0, 0, 0, 0);
+            if (DSUM) m[k] = ok ? ld16(a.dsum + base + c * 8) : make_uint4(0, 0, 0, 0);
         }
-        float2 sq2 = make_float2(0.f, 0.f), dot2 = sq2;
+        f2 sq2 = 0, dot2 = 0;
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) piece_sums(s[k], d[k], g[k], sq2, dot2);
-        float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
+        for (int k = 0; k < CPL; ++k) piece_sums(piece(s[k]), piece(d[k]), piece(g[k]), sq2, dot2);
+        float sq = sum2(sq2), dot = sum2(dot2);
         lane_sum2(sq, dot, step);
         // (the packed values stay, their fp32 forms are made again: registers
         // kept across the sums would halve the rows in flight)
@@ -310,13 +325,14 @@ __global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsB
             forget(s[k]);
             forget(d[k]);
             forget(g[k]);
-            forget(m[k]);
+            if (DSUM) forget(m[k]);
         }
-        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r;
+        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r * r;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
-            const uint4 o = piece_grad(s[k], d[k], g[k], m[k], r, q, acc[k]);
+            const uint4 o = piece_grad<DSUM>(piece(s[k]), piece(d[k]), piece(g[k]), DSUM ? piece(m[k]) : Piece{}, pack2(r),
+                                             pack2(-q), acc[k]);
             if (row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.dx + base + c * 8) = o;
         }
     }
@@ -325,9 +341,12 @@ __global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsB
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
         const int c = li + k * step;
+        float sums[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unpack2(acc[k].v[e], sums[2 * e], sums[2 * e + 1]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v = acc[k][e];
+            float v = sums[e];
             for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
         }
@@ -342,13 +361,14 @@ __global__ void __launch_bounds__(256, CPL > 2 ? 2 : 4) rms_backward_kernel(RmsB
 
 // Wider rows: a group of warps a row, several groups a block (few blocks, since
 // each writes a partial row of dgamma that is read again).  Every thread
-// fetches its own pieces of the next DEPTH - 1 rows by asynchronous copies into
-// its own place in shared memory, so that the latency of HBM is paid once, not
-// once a row; 3001 x 2744: 20.8 us with the rows loaded as they come.
+// fetches its own pieces of the next row by asynchronous copies into its own
+// place in shared memory, so that the latency of HBM is paid once, not once a
+// row (3001 x 2744: 15.5 us; 20.8 with the rows loaded as they come, and 30010
+// rows: 84.7 us one row ahead, 91 two).
 template <int CPL, bool DSUM>
 __global__ void __launch_bounds__(512, 1) rms_backward_wide_kernel(RmsBwdArgs a)
 {
-    constexpr int ARRAYS = DSUM ? 3 : 2, DEPTH = DSUM ? 2 : 3;
+    constexpr int ARRAYS = DSUM ? 3 : 2, DEPTH = 2;   // stages: a row, and the next
     extern __shared__ __align__(16) float part[];   // the pieces; at the end [C]
     __shared__ float2 red[2 * 16 * 16];
     griddep_launch_dependents();
@@ -383,13 +403,11 @@ __global__ void __launch_bounds__(512, 1) rms_backward_wide_kernel(RmsBwdArgs a)
     };
 #pragma unroll
     for (int d = 0; d < DEPTH - 1; ++d) fetch();
-    float acc[CPL][8];
-    uint4 g[CPL];
+    Piece acc[CPL], g[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
-        g[k] = have[k] ? ld16(a.gamma + (li + k * step) * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+        g[k] = piece(have[k] ? ld16(a.gamma + (li + k * step) * 8) : make_uint4(0, 0, 0, 0));
+        acc[k] = Piece{};
     }
     uint32_t at = ring;
     int turn = 0;
@@ -397,21 +415,20 @@ __global__ void __launch_bounds__(512, 1) rms_backward_wide_kernel(RmsBwdArgs a)
     for (int64_t row = first; row < a.rows; row += hop) {   // (the same for a group's threads)
         fetch();
         cp_async_wait<DEPTH - 1>();
-        float2 sq2 = make_float2(0.f, 0.f), dot2 = sq2;
+        f2 sq2 = 0, dot2 = 0;
 #pragma unroll
         for (int k = 0; k < CPL; ++k)
-            if (have[k]) piece_sums(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], sq2, dot2);
-        float sq = sq2.x + sq2.y, dot = dot2.x + dot2.y;
+            if (have[k]) piece_sums(piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), g[k], sq2, dot2);
+        float sq = sum2(sq2), dot = sum2(dot2);
         group_sum2(sq, dot, step, group, turn++, red);
-        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r;
+        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r * r;
         bf16 *dx = a.dx + row * C + li * 8;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             if (!have[k]) continue;
-            forget(g[k]);
-            const uint4 m = DSUM ? lds16(place(at, 2, k)) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(dx + k * step * 8) =
-                piece_grad(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], m, r, q, acc[k]);
+            const Piece m = DSUM ? piece(lds16(place(at, 2, k))) : Piece{};
+            *reinterpret_cast<uint4 *>(dx + k * step * 8) = piece_grad<DSUM>(
+                piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), g[k], m, pack2(r), pack2(-q), acc[k]);
         }
         at += stage;
         if (at == ring_end) at = ring;
@@ -427,9 +444,11 @@ __global__ void __launch_bounds__(512, 1) rms_backward_wide_kernel(RmsBwdArgs a)
                 float4 *p = reinterpret_cast<float4 *>(part + c * 8);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    float4 v;
+                    unpack2(acc[k].v[2 * h], v.x, v.y);
+                    unpack2(acc[k].v[2 * h + 1], v.z, v.w);
                     const float4 old = t ? p[h] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    p[h] = make_float4(old.x + acc[k][4 * h], old.y + acc[k][4 * h + 1], old.z + acc[k][4 * h + 2],
-                                       old.w + acc[k][4 * h + 3]);
+                    p[h] = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
                 }
             }
         __syncthreads();
@@ -520,10 +539,9 @@ cudaError_t launch_rms_forward(RmsArgs a, cudaStream_t stream)
 }
 
 // The backward's launch: as many blocks as the SMs hold at once, each walking
-// its share of the rows.  (Registers allow four blocks of 256 threads a SM with
-// one or two pieces a lane, two with three; a wide row's block is an SM's only
-// one, of up to 512 threads with three or four pieces each: with two on 1024
-// threads, what a thread spends on a row beside its pieces took 1 of 18 us.)
+// its share of the rows.  (A wide row's block is an SM's only one, of up to 512
+// threads with three or four pieces each: with two on 1024 threads, what a
+// thread spends on a row beside its pieces took 1 of 18 us.)
 struct BwdPlan {
     RowPlan row;
     int threads, grid;
@@ -541,11 +559,11 @@ BwdPlan plan_backward(int rows, int C, bool with_dsum)
         rpb = groups < MAX_GROUPS ? groups : MAX_GROUPS;
         per_sm = 1;
         p.threads = (int)rpb * r.lanes;
-        p.smem = (size_t)p.threads * (with_dsum ? 2 * 3 : 3 * 2) * r.cpl * 16;   // (at most 192 KB)
+        p.smem = (size_t)p.threads * (with_dsum ? 3 : 2) * 2 * r.cpl * 16;   // (at most 192 KB)
         if (p.smem < (size_t)C * sizeof(float)) p.smem = (size_t)C * sizeof(float);
     } else {
         rpb = 8 * (32 / r.lanes);
-        per_sm = r.cpl > 2 ? 2 : 4;
+        per_sm = blocks_per_sm(r.cpl, with_dsum);
         p.threads = 256;
         p.smem = (size_t)8 * C * sizeof(float);
     }
@@ -562,12 +580,14 @@ cudaError_t launch_rms_backward(RmsBwdArgs a, const BwdPlan &p, float *dgamma, c
     a.lanes = r.lanes;
     const int C = a.chunks * 8;
     void (*kern)(RmsBwdArgs) = nullptr;
-    if (!r.block)
-        kern = r.cpl == 1 ? rms_backward_kernel<1> : r.cpl == 2 ? rms_backward_kernel<2> : rms_backward_kernel<3>;
+    if (r.block)
+        kern = a.dsum ? (r.cpl == 3 ? rms_backward_wide_kernel<3, true> : rms_backward_wide_kernel<4, true>)
+                      : (r.cpl == 3 ? rms_backward_wide_kernel<3, false> : rms_backward_wide_kernel<4, false>);
     else if (a.dsum)
-        kern = r.cpl == 3 ? rms_backward_wide_kernel<3, true> : rms_backward_wide_kernel<4, true>;
+        kern = r.cpl == 1 ? rms_backward_kernel<1, true> : r.cpl == 2 ? rms_backward_kernel<2, true> : rms_backward_kernel<3, true>;
     else
-        kern = r.cpl == 3 ? rms_backward_wide_kernel<3, false> : rms_backward_wide_kernel<4, false>;
+        kern = r.cpl == 1 ? rms_backward_kernel<1, false>
+                          : r.cpl == 2 ? rms_backward_kernel<2, false> : rms_backward_kernel<3, false>;
     cudaError_t e;
     // (always the most any call needs: another thread may be between its setting
     // and its launch)
