@@ -612,3 +612,24 @@ def test_rounds_of_whole_tiles_and_a_last_one_in_parts(rows, C, F):
     ref, tol = backward_ref(x, p, dy, "silu")
     for k, v in dict(grads, dx=dx).items():
         close(v, ref[k], tol[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", [(300, 264, 8200), (300, 120, 8200), (9000, 136, 264), (20000, 136, 264)])
+def test_products_cut_along_k(rows, C, F):
+    """Few tiles of a long K: the forward's last product, dx (also in narrow
+    tiles), the weight gradients by even ranges and by equal slices."""
+    x, p, r, dy = make(rows, C, F, seed=17)
+    xd, pd, rd, yd = dev(x), dev(p), dev(r), dev(dy)
+    out, dx, grads = torch.full_like(xd, float("nan")), torch.full_like(xd, float("nan")), new_grads(p)
+    with gated(C, F) as h:
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        if F > 8000 and C > 128:
+            assert sw.swin_block_gated_last_launches(h) == 3   # (the third adds the partial tiles)
+        sw.swin_block_gated_backward(h, xd, pd, yd, dx, grads)
+        sw.swin_block_gated_sync_status(h)
+    ref, tol = forward_ref(x, p, r, "silu")
+    close(out, ref, tol)
+    ref, tol = backward_ref(x, p, dy, "silu")
+    for k, v in dict(grads, dx=dx).items():
+        close(v, ref[k], tol[k])

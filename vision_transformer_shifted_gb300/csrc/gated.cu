@@ -80,9 +80,15 @@ struct Product {
     int cols;
 };
 
-// A K block of half a tile (256 x 128) in hundredths of a whole one's: it loads
-// three quarters as much for half of the MMAs.
-constexpr int HALF_COST = 60;
+// What joining the tiles of a cut round costs, in K blocks of a whole tile: the
+// launch, the partial tiles' traffic and their second epilogue, some 10 us.
+// (Products of 1537 x 4104 x 1536, 42 tiles: the forward took 60 us with their 65
+// blocks cut to 36, 55 whole; 3000 x 4096 x 1024: 67 cut, 59 in halves.)
+constexpr int WIDE_JOIN = 32, NARROW_JOIN = 36;
+// A K block of half a tile (256 x 128) in hundredths of a whole one's, with
+// `halves` pairs at it: half of the MMAs and a little, or (many pairs) its share
+// of what L2 delivers, three quarters of a whole tile's operands a pair.
+int half_cost(int halves, int pairs) { return halves * 75 > 55 * pairs ? halves * 75 / pairs : 55; }
 
 // The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
 // of K (+ bias + residual).  `blocks` blocks a tile and VEC values a thread at a
@@ -261,13 +267,12 @@ struct ProductsPlan {
 };
 
 // Tiles of 256 x 256 where every product has more than 128 columns, else 256 x
-// 128.  The last round is cut along K where that saves more K blocks than
-// joining the partial tiles costs (a launch and their traffic, about 5 us: 16
-// blocks of a 256 x 256 tile, 24 of a narrow one); few blocks in all go to as
-// many pairs as leave each at least four.  A last round of at most half of the
-// pairs goes out as half tiles where that costs less: no join (1024 x 2048 x
-// 5632 forward 61.7 us cut, 57.5 in halves; 12544 x 512 x 1368 backward 140.6,
-// 135).
+// 128.  The last round is cut along K where that saves more K blocks than the
+// join costs; few blocks in all go to as many pairs as leave each at least four.
+// A last round of at most half of the pairs goes out as half tiles where that
+// costs less than either: no join (1024 x 2048 x 5632 forward 61.7 us cut, 57.5
+// in halves; 12544 x 512 x 1368 backward, dx's last 22 tiles, 140.6 and 135; its
+// weight gradients' 36 tiles of 196 blocks stay cut: in halves 11 us more).
 ProductsPlan plan_products(const Product *p, int n)
 {
     ProductsPlan pl{};
@@ -286,8 +291,8 @@ ProductsPlan plan_products(const Product *p, int n)
     const int full = (int)(tiles / pairs), rest = (int)(tiles - (int64_t)full * pairs);
     const int64_t blocks = (int64_t)rest * s.kb;
     int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
-    const int cut_cost = ceil_div(blocks, np) + (pl.wide ? 16 : 24);
-    if (pl.wide && rest && 2 * rest <= pairs && HALF_COST * s.kb <= 100 * (s.kb < cut_cost ? s.kb : cut_cost)) {
+    const int cut_cost = ceil_div(blocks, np) + (pl.wide ? WIDE_JOIN : NARROW_JOIN), least = s.kb < cut_cost ? s.kb : cut_cost;
+    if (pl.wide && rest && 2 * rest <= pairs && (int64_t)half_cost(2 * rest, pairs) * s.kb <= 100ll * least) {
         s.full = full;
         s.halves = 2 * rest;
         s.np = full ? pairs : s.halves;
