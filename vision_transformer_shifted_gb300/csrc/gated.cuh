@@ -19,18 +19,18 @@ __device__ __forceinline__ f2 logistic2(f2 z)
     return pack2(rcp_approx(a), rcp_approx(b));
 }
 
-// act of two values.
+// What stands in front of g in act(g) = g P(g), for two values.
 //
-// GELU as x / (1 + 2^(x P(x^2))): the logit of the normal distribution function
-// is odd and smooth, and P, of degree 6, was fitted to it here by reweighted
+// GELU's P as 1 / (1 + 2^(x Q(x^2))): the logit of the normal distribution function
+// is odd and smooth, and Q, of degree 6, was fitted to it here by reweighted
 // least squares for the smallest largest error of x Phi(x) on [0, 9] (6.6e-8;
 // 5.9e-7 evaluated in fp32, as good as gelu_exact's 4.7e-7).  Ten two-lane
 // operations and no sign handling against fourteen and four more; its last
 // coefficient is negative, so that far from zero Phi goes to 0 and 1.
 template <int ACT>
-__device__ __forceinline__ f2 activate2(f2 g)
+__device__ __forceinline__ f2 gate2(f2 g)
 {
-    if (ACT == ACT_SILU) return mul2(g, logistic2(mul2(g, pack2(-1.4426950408889634f))));
+    if (ACT == ACT_SILU) return logistic2(mul2(g, pack2(-1.4426950408889634f)));
     const f2 t = mul2(g, g);
     f2 z = fma2(t, pack2(-5.23388088e-9f), pack2(3.860164099e-7f));
     z = fma2(z, t, pack2(-1.1466739124e-5f));
@@ -38,47 +38,27 @@ __device__ __forceinline__ f2 activate2(f2 g)
     z = fma2(z, t, pack2(9.5295035863e-5f));
     z = fma2(z, t, pack2(-0.10483819246f));
     z = fma2(z, t, pack2(-2.30220746994f));
-    return mul2(g, logistic2(mul2(z, g)));
+    return logistic2(mul2(z, g));
 }
-
-// act and its derivative of two values: a = g P(g), d = P + g P'(g).
 template <int ACT>
-__device__ __forceinline__ void activate_grad2(float g0, float g1, float &a0, float &a1, float &d0, float &d1)
+__device__ __forceinline__ f2 activate2(f2 g)
 {
-    float p0, p1;
-    if (ACT == ACT_SILU) {
-        const f2 g = pack2(g0, g1), p = logistic2(mul2(g, pack2(-1.4426950408889634f)));
-        unpack2(p, p0, p1);
-        unpack2(mul2(g, p), a0, a1);
-        // p (1 + g (1 - p)) = p + a - a p
-        float t0, t1;
-        g2_fma(t0, t1, a0, a1, -p0, -p1, a0, a1);
-        d0 = p0 + t0;
-        d1 = p1 + t1;
+    return mul2(g, gate2<ACT>(g));
+}
+// act of two values and its derivative d = P + g P'(g).
+template <int ACT>
+__device__ __forceinline__ void activate_grad2(f2 g, f2 &a, f2 &d)
+{
+    const f2 p = gate2<ACT>(g);
+    a = mul2(g, p);
+    if (ACT == ACT_SILU) {   // p + g p (1 - p) = p + p (g - a)
+        d = fma2(p, fma2(a, pack2(-1.f), g), p);
         return;
     }
-    // gelu_exact2's erf; its exponential exp(-g^2 / 2) is also the density's
-    float z0, z1, t0, t1, q0, q1, e0, e1;
-    g2_mul(z0, z1, g0, g1, 0.70710678118654752f, 0.70710678118654752f);
-    const float b0 = fabsf(z0), b1 = fabsf(z1);
-    g2_fma(t0, t1, b0, b1, 0.3275911f, 0.3275911f, 1.0f, 1.0f);
-    t0 = rcp_approx(t0);
-    t1 = rcp_approx(t1);
-    g2_fma(q0, q1, t0, t1, -1.061405429f, -1.061405429f, 1.453152027f, 1.453152027f);
-    g2_fma(q0, q1, q0, q1, t0, t1, -1.421413741f, -1.421413741f);
-    g2_fma(q0, q1, q0, q1, t0, t1, 0.284496736f, 0.284496736f);
-    g2_fma(q0, q1, q0, q1, t0, t1, -0.254829592f, -0.254829592f);
-    g2_mul(q0, q1, q0, q1, t0, t1);
-    g2_mul(e0, e1, b0, b1, -1.4426950408889634f, -1.4426950408889634f);
-    g2_mul(e0, e1, e0, e1, b0, b1);
-    e0 = ex2_approx(e0);
-    e1 = ex2_approx(e1);
-    g2_fma(q0, q1, q0, q1, e0, e1, 1.0f, 1.0f);   // erf(|z|)
-    g2_fma(p0, p1, copysignf(q0, z0), copysignf(q1, z1), 0.5f, 0.5f, 0.5f, 0.5f);
-    g2_mul(a0, a1, g0, g1, p0, p1);
-    float s0, s1;
-    g2_mul(s0, s1, g0, g1, 0.3989422804014327f, 0.3989422804014327f);
-    g2_fma(d0, d1, s0, s1, e0, e1, p0, p1);
+    // g P'(g): g times the density exp(-g^2 / 2) / sqrt(2 pi)
+    float e0, e1;
+    unpack2(mul2(mul2(g, g), pack2(-0.72134752044448170f)), e0, e1);
+    d = fma2(mul2(g, pack2(0.3989422804014327f)), pack2(ex2_approx(e0), ex2_approx(e1)), p);
 }
 
 // Eight values of a bf16 vector at column c (zero past n, and for NULL).
@@ -545,20 +525,32 @@ struct GemmPolicy {
     }
 };
 
-// Column sums of a warp's 32 rows x 16 columns (a row a lane): lane l returns
-// column l % 16's.  Each exchange halves the columns a lane still sums.
-__device__ __forceinline__ float column_sum16(float (&v)[16], int lane)
+// Column sums of a warp's staged box of 32 rows x 32 bf16: lane l < 16 gets columns
+// 2 l and 2 l + 1's.  A product with ones from the left, by the warp's own MMAs
+// (the box is their B as it lies): 12 instructions, where exchanges between lanes
+// took 250.
+__device__ __forceinline__ float2 box_sums(uint32_t stage, int lane)
 {
+    const uint32_t ones = 0x3f803f80u;
+    float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
+    for (int q = 0; q < 4; ++q) {
+        uint32_t b[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                     : "r"(stage + sw64_offset(lane, q))
+                     : "memory");
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const bool up = lane & o;
-            const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
+        for (int k = 0; k < 2; ++k)
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %4, %4, %4}, {%5, %6}, {%0, %1, "
+                "%2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(ones), "r"(b[2 * k]), "r"(b[2 * k + 1]));
+        if ((lane >> 2) == q) mine = make_float2(c[0], c[1]);
     }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    return mine;
 }
 
 // ---- the backward's recompute: h, dg, du -----------------------------------------
@@ -689,30 +681,20 @@ struct GradPolicy {
                 float hh[8];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    float a0, a1, t0, t1, s0, s1;
-                    activate_grad2<ACT>(gq[e], gq[e + 1], a0, a1, t0, t1);
-                    g2_mul(hh[e], hh[e + 1], a0, a1, vq[e], vq[e + 1]);
-                    g2_mul(s0, s1, dq[e], dq[e + 1], vq[e], vq[e + 1]);
-                    g2_mul(gq[e], gq[e + 1], s0, s1, t0, t1);               // dg = dh u act'(g)
-                    g2_mul(dq[e], dq[e + 1], dq[e], dq[e + 1], a0, a1);     // du = dh act(g)
+                    const f2 u2 = pack2(vq[e], vq[e + 1]), dh2 = pack2(dq[e], dq[e + 1]);
+                    f2 act2, grad2;
+                    activate_grad2<ACT>(pack2(gq[e], gq[e + 1]), act2, grad2);
+                    unpack2(mul2(act2, u2), hh[e], hh[e + 1]);
+                    unpack2(mul2(mul2(dh2, u2), grad2), gq[e], gq[e + 1]);   // dg = dh u act'(g)
+                    unpack2(mul2(dh2, act2), dq[e], dq[e + 1]);              // du = dh act(g)
                 }
                 const uint32_t off = sw64_offset(lane, 2 * j + q);
+                uint4 dg8 = pack8f(gq), du8 = pack8f(dq);
+                // (no token: zero times an infinite parameter is not zero)
+                if (row0 + 32 > a.rows && row0 + lane >= a.rows) dg8 = du8 = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(stage + off) = pack8f(hh);
-                *reinterpret_cast<uint4 *>(stage + 2048 + off) = pack8f(gq);
-                du[2 * j + q] = pack8f(dq);
-            }
-            if (a.dg_sums) {
-                if (row0 + lane >= a.rows) {   // (no token: zero times an infinite parameter is not zero)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) g[e] = d[e] = 0.f;
-                }
-                const int c = col0 + 16 * j + (lane & 15);
-                const float sg = column_sum16(g, lane), su = column_sum16(d, lane);
-                if (lane < 16 && c < a.F) {
-                    const int64_t at = (int64_t)(u.m * 8 + (int)rank * 4 + quad) * a.F + c;
-                    a.dg_sums[at] = sg;
-                    a.du_sums[at] = su;
-                }
+                *reinterpret_cast<uint4 *>(stage + 2048 + off) = dg8;
+                du[2 * j + q] = du8;
             }
         }
         // two boxes of staging for three outputs: du takes h's when it is read
@@ -720,12 +702,22 @@ struct GradPolicy {
         if (lane == 0 && inside) {
             tma_store_2d(&a.dg, col0, row0, smem_u32(stage + 2048));
             bulk_commit();
-            bulk_wait_read1();
         }
+        const bool sums = a.dg_sums && lane < 16 && col0 + 2 * lane < a.F;
+        const int64_t at = (int64_t)(u.m * 8 + (int)rank * 4 + quad) * a.F + col0 + 2 * lane;
+        if (a.dg_sums) {
+            const float2 sg = box_sums(smem_u32(stage + 2048), lane);
+            if (sums) *reinterpret_cast<float2 *>(a.dg_sums + at) = sg;
+        }
+        if (lane == 0 && inside) bulk_wait_read1();
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = du[q];
         store_box(&a.du, col0, row0, inside, stage, lane);
+        if (a.dg_sums) {
+            const float2 su = box_sums(smem_u32(stage), lane);
+            if (sums) *reinterpret_cast<float2 *>(a.du_sums + at) = su;
+        }
     }
 };
 
