@@ -163,63 +163,25 @@ __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
     }
 }
 
-// Column sums of up to three matrices [rows, cols] (fp32 or bf16): a block sums
-// every splits-th group of 32 rows of 64 columns into a partial row; then the
-// partial rows are added, all in a fixed order.
-struct ColumnSums {
-    struct {
-        const float *f;   // fp32, or
-        const bf16 *b;
-        bf16 *out;
-        float *part;      // [splits, cols]
-        int64_t rows;
-        int cols, splits;
-    } m[3];
-    int n;
-    __host__ __device__ int blocks(int i) const { return (m[i].cols + 63) / 64 * m[i].splits; }
-};
-int column_splits(int64_t rows) { return rows < 64 * 32 ? ceil_div(rows, 32) : 64; }
-__device__ __forceinline__ void column_partials(const ColumnSums &a, int block)
-{
-    __shared__ float sum[32][65];
-    int z = 0;
-    for (; z + 1 < a.n && block >= a.blocks(z); ++z) block -= a.blocks(z);
-    const auto &m = a.m[z];
-    const int cols = m.cols, c0 = block / m.splits * 64, y = block % m.splits;
-    const int c = c0 + (threadIdx.x & 7) * 8, r = threadIdx.x >> 3;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < cols) {
-#pragma unroll 4
-        for (int64_t i = (int64_t)y * 32 + r; i < m.rows; i += (int64_t)m.splits * 32) {
-            float w[8];
-            if (m.f) load8(m.f + i * cols, c, cols, w);
-            else load8(m.b + i * cols, c, cols, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += w[e];
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[r][(threadIdx.x & 7) * 8 + e] = v[e];
-    __syncthreads();
-    if (threadIdx.x < 64 && c0 + (int)threadIdx.x < cols) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t += sum[i][threadIdx.x];
-        m.part[(int64_t)y * cols + c0 + threadIdx.x] = t;
-    }
-}
-
 // What is left of a call when its products are done, as one launch: the cut
-// tiles of up to two of them, and the first half of the column sums.  (As
-// kernels of their own behind each product they took 27 us of the 151 of the
-// backward at 12544 x 512 x 1368, most of it latency.)
+// tiles of up to two of them, and the last additions of the column sums, eight
+// columns a block and 32 threads a column.
 struct FinishArgs {
     JoinArgs join[2];
     int joins[2];   // blocks of each
     ColumnSums cs;
 };
+__host__ __device__ inline int column_blocks(const ColumnSums &cs, int i) { return (cs.m[i].cols + 7) / 8; }
+// Partial rows of a column sum: 16 rows or more each, and not more than 98 (a
+// warp takes them eight at a time, some 12 us for 98) up to 2048 partial rows.
+int column_slices(int64_t rows)
+{
+    const int few = rows < 128 * 16 ? ceil_div(rows, 16) : 128, many = rows < 2048 * 98 ? ceil_div(rows, 98) : 2048;
+    return few > many ? few : many;
+}
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a)
 {
+    __shared__ float sum[32][8];
     griddep_launch_dependents();
     griddep_wait();
     int b = blockIdx.x;
@@ -231,34 +193,28 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
         }
         b -= a.joins[i];
     }
-    column_partials(a.cs, b);
+    int z = 0;
+    for (; z + 1 < a.cs.n && b >= column_blocks(a.cs, z); ++z) b -= column_blocks(a.cs, z);
+    const auto &m = a.cs.m[z];
+    const int k = threadIdx.x & 7, w = threadIdx.x >> 3, c = b * 8 + k;   // (cols is a multiple of 8)
+    float v = 0.f;
+#pragma unroll 8
+    for (int s = w; s < m.slices; s += 32) v += m.part[(int64_t)s * m.cols + c];
+    sum[w][k] = v;
+    __syncthreads();
+    if (threadIdx.x >= 8) return;
+#pragma unroll
+    for (int i = 1; i < 32; ++i) v += sum[i][k];
+    m.out[c] = __float2bfloat16_rn(v);
 }
 cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launches)
 {
     int blocks = a.joins[0] + a.joins[1];
-    for (int i = 0; i < a.cs.n; ++i) blocks += a.cs.blocks(i);
+    for (int i = 0; i < a.cs.n; ++i) blocks += column_blocks(a.cs, i);
     if (!blocks) return cudaSuccess;
     ++*launches;
     return launch_maybe_overlapped(finish_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, 1, a);
 }
-__global__ void __launch_bounds__(1024) column_finish_kernel(const __grid_constant__ ColumnSums a)
-{
-    __shared__ float part[32][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    griddep_launch_dependents();
-    griddep_wait();
-    const auto &m = a.m[blockIdx.y];
-    const int c = blockIdx.x * 32 + lane;
-    float v = 0.f;
-    if (c < m.cols)
-        for (int s = w; s < m.splits; s += 32) v += m.part[(int64_t)s * m.cols + c];
-    part[w][lane] = v;
-    __syncthreads();
-    v = part[lane][w];
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0 && (int)blockIdx.x * 32 + w < m.cols) m.out[blockIdx.x * 32 + w] = __float2bfloat16_rn(v);
-}
-
 struct ProductsPlan {
     int n;
     bool wide;            // 256-column tiles (else 128)
@@ -360,6 +316,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
         if ((e = map_out(&q.d, p.d, p.rows, p.cols)) != cudaSuccess) return e;
     }
     a.split = r.split = pl.split;
+    if (A_MN) a.sums = fin->cs;
     a.np = pl.split.np;
     a.st = st;
     if (pl.split.cut) {
@@ -683,10 +640,20 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     FinishArgs fin{};
     ColumnSums &cs = fin.cs;
     const int row_blocks = ceil_div(rows, 256) * 8;
-    const int splits[3] = {column_splits(row_blocks), column_splits(row_blocks), column_splits(rows)};
-    const size_t sum_bytes = ((size_t)2 * splits[0] * h->F + (size_t)splits[2] * h->C) * sizeof(float);
-    int most = 0;
     const size_t row_sums = g->dbg || g->dbu ? (size_t)row_blocks * h->F * sizeof(float) : 0;
+    void *const bias_grads[3] = {g->dbg, g->dbu, g->dbd};
+    size_t sum_bytes = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!bias_grads[i]) continue;
+        auto &m = cs.m[cs.n++];
+        m.out = (bf16 *)bias_grads[i];
+        m.b = i < 2 ? nullptr : (const bf16 *)dy;
+        m.rows = i < 2 ? row_blocks : rows;
+        m.cols = i < 2 ? h->F : h->C;
+        m.slices = column_slices(m.rows);
+        m.tasks = ceil_div(m.cols, m.b ? 256 : 128) * m.slices;
+        sum_bytes += (size_t)m.slices * m.cols * sizeof(float);
+    }
     const size_t hid = (size_t)rows * hidden_ld(h->F) * 2;
     Carve size(nullptr);
     for (int i = 0; i < 3; ++i) size.take(hid);
@@ -705,6 +672,12 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     dxp.a[0] = dw[0].a[0] = dg;
     dxp.a[1] = dw[1].a[0] = du;
     dw[2].b[0] = hidden;
+    for (int i = 0; i < cs.n; ++i) {
+        auto &m = cs.m[i];
+        if (!m.b) m.f = m.out == g->dbg ? dg_sums : du_sums;
+        m.part = sum_part;
+        sum_part += (size_t)m.slices * m.cols;
+    }
     const DeviceStatus st{h->d_err, WAIT_NS};
 
     auto grad = [&](auto policy) -> cudaError_t {
@@ -746,25 +719,7 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
     cudaError_t e = h->act == SWIN_BLOCK_GATED_SILU ? grad(GradPolicy<ACT_SILU>{}) : grad(GradPolicy<ACT_GELU>{});
     if (e == cudaSuccess) e = launch_products<false, true>(&dxp, px, x_part, st, s, &h->last_launches, &fin, 0);
     if (e == cudaSuccess) e = launch_products<true, true>(dw, pw, w_part, st, s, &h->last_launches, &fin, 1);
-    bf16 *out[3] = {(bf16 *)g->dbg, (bf16 *)g->dbu, (bf16 *)g->dbd};
-    for (int i = 0; i < 3; ++i) {
-        if (!out[i]) continue;
-        auto &m = cs.m[cs.n++];
-        m.f = i == 0 ? dg_sums : i == 1 ? du_sums : nullptr;
-        m.b = (const bf16 *)dy;
-        m.out = out[i];
-        m.part = sum_part;
-        m.rows = i < 2 ? row_blocks : rows;
-        m.cols = i < 2 ? h->F : h->C;
-        m.splits = splits[i];
-        sum_part += (size_t)m.splits * m.cols;
-        if (m.cols > most) most = m.cols;
-    }
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
-    if (e == cudaSuccess && cs.n) {
-        ++h->last_launches;
-        e = launch_maybe_overlapped(column_finish_kernel, dim3(ceil_div(most, 32), cs.n), dim3(1024), 0, s, 1, cs);
-    }
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
 }

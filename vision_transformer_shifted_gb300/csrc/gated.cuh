@@ -74,16 +74,6 @@ __device__ __forceinline__ void load8(const bf16 *v, int c, int n, float (&f)[8]
         f[2 * e + 1] = p.y;
     }
 }
-__device__ __forceinline__ void load8(const float *v, int c, int n, float (&f)[8])
-{
-    float4 x = make_float4(0, 0, 0, 0), y = x;
-    if (c < n) {
-        x = *reinterpret_cast<const float4 *>(v + c);
-        y = *reinterpret_cast<const float4 *>(v + c + 4);
-    }
-    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-}
 
 // A vector over the columns of a warp's accumulators (a bias, a scale): each lane
 // fetches its column's value, early; the warp spreads them through 32 floats of
@@ -181,6 +171,7 @@ struct UpPolicy {
         prefetch_map(rank ? &a.wu : &a.wg);
         prefetch_map(&a.h);
     }
+    static __device__ __forceinline__ void side(const Args &, int, int) {}
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int) { return 2 * (16384 + 128 * u.width); }
     static __device__ __forceinline__ void load(const Args &a, const Unit &u, int, int kb, uint32_t rank, uint32_t dst,
@@ -324,12 +315,77 @@ struct PairSplit {
     }
 };
 
+// Column sums of up to three matrices [rows, cols], bf16 or fp32 (the bias
+// gradients): a warp adds every slices-th row of 256 or 128 columns (16 bytes a
+// lane) into a partial row, eight rows in flight; the partial rows are added
+// later, all in a fixed order.  The weight gradients' epilogue warps do it, which
+// wait for their first tile's MMAs.
+struct ColumnSums {
+    struct {
+        const bf16 *b;    // bf16, or
+        const float *f;   // fp32
+        bf16 *out;
+        float *part;      // [slices, cols]
+        int64_t rows;
+        int cols, slices, tasks;   // tasks: slices of every group of columns
+    } m[3];
+    int n;
+};
+template <class T>
+__device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols, int c, int slice, int slices, float *part)
+{
+    constexpr int V = 16 / sizeof(T);
+    if (c >= cols) return;
+    float v[V] = {};
+    int64_t i = slice;
+    auto add = [&](const uint4 &u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (V == 4) {
+                v[e] += __uint_as_float(w[e]);
+            } else {
+                v[2 * e % V] += __uint_as_float(w[e] << 16);
+                v[(2 * e + 1) % V] += __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+    };
+#pragma unroll 1
+    for (; i + 7 * (int64_t)slices < rows; i += 8 * (int64_t)slices) {
+        uint4 u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(p + (i + k * (int64_t)slices) * cols + c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add(u[k]);
+    }
+#pragma unroll 1
+    for (; i < rows; i += slices) add(*reinterpret_cast<const uint4 *>(p + i * cols + c));
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+        *reinterpret_cast<float4 *>(part + (int64_t)slice * cols + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+}
+// Warp w's share, of `warps`.
+__device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int warps, int lane)
+{
+    int t = w;
+    for (int z = 0; z < a.n; ++z) {
+        const auto &m = a.m[z];
+        for (; t < m.tasks; t += warps) {
+            const int slice = t % m.slices, g = t / m.slices;
+            if (m.b) column_slice(m.b, m.rows, m.cols, g * 256 + lane * 8, slice, m.slices, m.part);
+            else column_slice(m.f, m.rows, m.cols, g * 128 + lane * 4, slice, m.slices, m.part);
+        }
+        t -= m.tasks;
+    }
+}
+
 template <int TN, bool A_MN, bool B_MN>
 struct GemmPolicy {
     struct Args {
         PairProblem p[3];
         CUtensorMap part;   // partial tiles [2 np][256][TN] fp32
         PairSplit split;
+        ColumnSums sums;    // with A_MN: summed under the first tile's MMAs
         int np;
         DeviceStatus st;
     };
@@ -390,6 +446,10 @@ struct GemmPolicy {
         prefetch_map(&a.p[u.p].a[seg]);
         prefetch_map(&a.p[u.p].b[seg]);
         prefetch_map(u.slot >= 0 ? &a.part : &a.p[u.p].d);
+    }
+    static __device__ __forceinline__ void side(const Args &a, int w, int lane)
+    {
+        if (A_MN) column_partials(a.sums, w, 2 * a.np * EPI, lane);   // (the weight gradients)
     }
     static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int) { return 2 * (16384 + u.width * 64); }
@@ -599,6 +659,7 @@ struct GradPolicy {
         prefetch_map(&a.x);
         prefetch_map(rank ? &a.wu : &a.wg);
     }
+    static __device__ __forceinline__ void side(const Args &, int, int) {}
     static __device__ __forceinline__ int kblocks(const Args &a, const Unit &, int) { return a.kb; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int seg)
     {

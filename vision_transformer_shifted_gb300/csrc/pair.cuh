@@ -30,6 +30,8 @@
 //                           of this pair, its first column, how often it was used
 //   kblocks(a, u, seg), tx(a, u, seg), load(...), mma(...)
 //   prefetch_maps(a, pair, rank)   fetches the tensor maps this CTA begins with
+//   side(a, w, lane)        what epilogue warp w of the launch does before its first
+//                           accumulators are ready, if anything
 //   Pre, prefetch(...), epilogue(...)   what an epilogue thread fetches before
 //                           the accumulators are ready, and the epilogue
 #pragma once
@@ -387,6 +389,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         constexpr int TEAM = P::EPI / P::GROUPS;
         const int quad = warp & 3, part = (warp - 2) % TEAM >> 2;   // (part: of the columns)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+        P::side(a, (int)blockIdx.x * P::EPI + warp - 2, lane);
         for (int n = (warp - 2) / TEAM; n < units && !failed; n += P::GROUPS) {
             const typename P::Unit un = P::decode(a, pair, n);
             // (warp-uniform outcome: the TMEM loads below are warp-collective)
