@@ -94,8 +94,8 @@ int swin_block_gated_forward_q8(swin_block_gated_t h, const void *x8, const floa
  *   dWg = dg^T x; dWu = du^T x; dWd = dy^T h; dbg, dbu, dbd = the row sums of
  *   dg, du, dy
  * x, dy, dx [rows, C] bf16; g, u and h are recomputed from x (nothing of the
- * forward is kept); dg, du and h are rounded to bf16 before the products and
- * row sums that read them; every sum over rows is taken in a fixed order.  No output
+ * forward is kept); dg, du and h are rounded to bf16 before the products that
+ * read them; every sum over rows is taken in a fixed order.  No output
  * overlaps an input or another output.  Errors as above; the workspace is
  * 3 * rows * F bf16 plus fp32 partial sums.  rows = 0 zeroes the parameter
  * gradients. */
