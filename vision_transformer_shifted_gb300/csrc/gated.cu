@@ -98,6 +98,7 @@ struct JoinArgs {
     const float *part;
     PairSplit split;
     int tn, blocks;
+    bool from_last;   // (tile_place)
     struct {
         const bf16 *bias, *residual;
         bf16 *out;
@@ -138,7 +139,7 @@ __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
     if (p0 == p1) return;   // (one pair had the whole tile and wrote it)
     const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
     int m, n;
-    tile_order(t - a.p[i].first, a.p[i].mt, a.p[i].nt, m, n);
+    tile_order(tile_place(t - a.p[i].first, a.p[i].mt, a.p[i].nt, a.from_last), a.p[i].mt, a.p[i].nt, m, n);
     const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / VEC;
     const int64_t size = 256 * a.tn;
     const int first = s.slot(p0, c);
@@ -326,6 +327,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     ++*launches;
     r.part = part;
     r.tn = TN;
+    r.from_last = !A_MN;
     r.blocks = pl.split.cut >= 16 ? 16 : 64;
     fin->joins[slot] = pl.split.cut * r.blocks;
     return launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);

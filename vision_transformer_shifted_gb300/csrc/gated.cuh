@@ -379,6 +379,12 @@ __device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int 
     }
 }
 
+// Place in the order of tiles of the t-th tile worked on.  Products of the hidden
+// activations' rows (not their weight gradients) go through the rows from the
+// last: the kernel before wrote those last, and L2 still has them (118162 x 192 x
+// 672 forward 113 -> 110.4 us, 200704 x 96 x 256 backward 213 -> 209).
+__host__ __device__ inline int tile_place(int t, int mt, int nt, bool from_last) { return from_last ? mt * nt - 1 - t : t; }
+
 template <int TN, bool A_MN, bool B_MN>
 struct GemmPolicy {
     struct Args {
@@ -432,7 +438,7 @@ struct GemmPolicy {
         r.p = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
         const PairProblem &p = a.p[r.p];
         int nt;
-        tile_order(t - p.first, p.mt, p.nt, r.m, nt);
+        tile_order(tile_place(t - p.first, p.mt, p.nt, !A_MN), p.mt, p.nt, r.m, nt);
         r.width = half ? TN / 2 : TN;
         r.col = nt * TN + (half ? pair % 2 * (TN / 2) : 0);
         r.k0 = p.k[0];
