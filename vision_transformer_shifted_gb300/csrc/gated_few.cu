@@ -8,8 +8,9 @@
 // eight), which spreads few tiles over the SMs without partial sums in global
 // memory: each CTA leaves its fp32 tile in shared memory and the cluster's CTAs
 // add their shares of it through distributed shared memory, in rank order.
-// Weights stream through a TMA ring of about 100 KB a CTA, two CTAs an SM:
-// HBM bounds it.
+// Weights stream through a TMA ring of about 100 KB a CTA, two CTAs an SM: HBM
+// bounds it, and the latency of two launches (9 us + bytes / 7.07 TB/s over the
+// sizes; 1 x 2048 x 5632: 20 us, 24 rows from e4m3 4096 x 11264: 37).
 #include <atomic>
 #include <cstring>
 

@@ -7,7 +7,9 @@
 // them.  Rows of up to 1024 channels lie on part of a warp (a power of two of
 // lanes, at most four 16-byte pieces each: their loads are all in flight at
 // once and the statistics need shuffles only); longer rows take a block each.
-// (The backward, with three inputs, at most three pieces a lane.)
+// (The backward, with three inputs, at most three pieces a lane.)  With residual,
+// 200704 x 96: 23.6 us, 6.5 TB/s; to e4m3, 8191 x 4096: 36.9 us, 6.4 TB/s;
+// backward 589824 x 192 with dsum: 135 us, 6.7 TB/s.
 #include <climits>
 #include <cmath>
 #include <cuda_fp8.h>
