@@ -633,3 +633,22 @@ def test_products_cut_along_k(rows, C, F):
     ref, tol = backward_ref(x, p, dy, "silu")
     for k, v in dict(grads, dx=dx).items():
         close(v, ref[k], tol[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", [(1300, 2048, 264), (2800, 1000, 136)])
+def test_products_in_tiles_of_192_columns(rows, C, F):
+    """Tiles of 256 columns for half of the CTA pairs and a few more: one round of
+    narrower ones instead (the last product, dx, the weight gradients)."""
+    x, p, r, dy = make(rows, C, F, seed=18)
+    xd, pd, rd, yd = dev(x), dev(p), dev(r), dev(dy)
+    out, dx, grads = torch.full_like(xd, float("nan")), torch.full_like(xd, float("nan")), new_grads(p)
+    with gated(C, F, "gelu") as h:
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        sw.swin_block_gated_backward(h, xd, pd, yd, dx, grads)
+        sw.swin_block_gated_sync_status(h)
+    ref, tol = forward_ref(x, p, r, "gelu")
+    close(out, ref, tol)
+    ref, tol = backward_ref(x, p, dy, "gelu")
+    for k, v in dict(grads, dx=dx).items():
+        close(v, ref[k], tol[k])

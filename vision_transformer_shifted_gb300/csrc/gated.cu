@@ -85,6 +85,11 @@ struct Product {
 // (Products of 1537 x 4104 x 1536, 42 tiles: the forward took 60 us with their 65
 // blocks cut to 36, 55 whole; 3000 x 4096 x 1024: 67 cut, 59 in halves.)
 constexpr int WIDE_JOIN = 32, NARROW_JOIN = 36;
+// A K block of a 256 x 192 tile in hundredths of a whole one's: tiles of that width
+// where they come out cheaper, as a round that leaves a third of the pairs idle
+// with 256 columns (1300 x 2048 x 5632 forward: 48 tiles 71 us, 66 of them 68;
+// 3000 x 1024 x 2736 backward 106 and 102.5).
+constexpr int COST_192 = 82;
 // A K block of half a tile (256 x 128) in hundredths of a whole one's, with
 // `halves` pairs at it: half of the MMAs and a little, or (many pairs) its share
 // of what L2 delivers, three quarters of a whole tile's operands a pair.
@@ -219,6 +224,7 @@ cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launche
 struct ProductsPlan {
     int n;
     bool wide;            // 256-column tiles (else 128)
+    int wn;               // columns of a tile: 256, 192 or 128
     PairSplit split;
     size_t part_bytes;    // of the partial tiles
 };
@@ -237,9 +243,13 @@ ProductsPlan plan_products(const Product *p, int n)
     pl.wide = true;
     for (int i = 0; i < n; ++i)
         if (p[i].cols <= 128) pl.wide = false;
-    const int tn = pl.wide ? 256 : 128;
-    int64_t tiles = 0;
-    for (int i = 0; i < n; ++i) tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, tn);
+    const int tn = pl.wn = pl.wide ? 256 : 128;
+    auto count = [&](int wn) {
+        int64_t tiles = 0;
+        for (int i = 0; i < n; ++i) tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, wn);
+        return tiles;
+    };
+    int64_t tiles = count(tn);
     PairSplit &s = pl.split;
     s.tiles = (int)tiles;
     s.k_blocks = s.kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
@@ -249,7 +259,14 @@ ProductsPlan plan_products(const Product *p, int n)
     const int64_t blocks = (int64_t)rest * s.kb;
     int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
     const int cut_cost = ceil_div(blocks, np) + (pl.wide ? WIDE_JOIN : NARROW_JOIN), least = s.kb < cut_cost ? s.kb : cut_cost;
-    if (pl.wide && rest && 2 * rest <= pairs && (int64_t)half_cost(2 * rest, pairs) * s.kb <= 100ll * least) {
+    const bool halves = pl.wide && rest && 2 * rest <= pairs && (int64_t)half_cost(2 * rest, pairs) * s.kb <= 100ll * least;
+    const int64_t here = 100ll * full * s.kb + (halves ? (int64_t)half_cost(2 * rest, pairs) * s.kb : rest ? 100ll * least : 0);
+    const int64_t tiles192 = count(192);
+    if (pl.wide && (int64_t)ceil_div(tiles192, pairs) * COST_192 * s.kb < here) {
+        pl.wn = 192;
+        s.tiles = (int)tiles192;
+        s.np = (int)(tiles192 < pairs ? tiles192 : pairs);
+    } else if (halves) {
         s.full = full;
         s.halves = 2 * rest;
         s.np = full ? pairs : s.halves;
@@ -293,7 +310,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
         q.rows = (int)p.rows;
         q.cols = p.cols;
         q.mt = ceil_div(p.rows, 256);
-        q.nt = ceil_div(p.cols, TN);
+        q.nt = ceil_div(p.cols, pl.wn);
         q.first = first;
         first += q.mt * q.nt;
         q.bias = p.bias;
@@ -307,7 +324,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
                      : map_k(&q.a[s], p.a[s], p.rows, p.k[s], 128, false, p.lda);
             if (e != cudaSuccess) return e;
             e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols, p.ldb)
-                     : map_k(&q.b[s], p.b[s], p.cols, p.k[s], TN / 2, false, p.ldb);
+                     : map_k(&q.b[s], p.b[s], p.cols, p.k[s], pl.wn / 2, false, p.ldb);
             if (e != cudaSuccess) return e;
             if (!B_MN && pl.split.halves) {
                 e = map_k(&q.b_half[s], p.b[s], p.cols, p.k[s], TN / 4, false, p.ldb);
@@ -318,6 +335,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     }
     a.split = r.split = pl.split;
     if (A_MN) a.sums = fin->cs;
+    a.wn = pl.wn;
     a.np = pl.split.np;
     a.st = st;
     if (pl.split.cut) {

@@ -397,12 +397,13 @@ struct GemmPolicy {
         CUtensorMap part;   // partial tiles [2 np][256][TN] fp32
         PairSplit split;
         ColumnSums sums;    // with A_MN: summed under the first tile's MMAs
+        int wn;             // columns of a tile: TN, or 192 of 256
         int np;
         DeviceStatus st;
     };
     struct Unit {
         int p, m, col, kb0, kbn;
-        int width;          // columns, from col: TN, or half of it
+        int width;          // columns, from col: a tile's, or half of them
         int slot;           // partial tile to write (-1: the whole K, to D)
         int k0, kb_first;   // the first segment's K, and its blocks
     };
@@ -444,8 +445,8 @@ struct GemmPolicy {
         const PairProblem &p = a.p[r.p];
         int nt;
         tile_order(tile_place(t - p.first, p.mt, p.nt, !A_MN), p.mt, p.nt, r.m, nt);
-        r.width = half ? TN / 2 : TN;
-        r.col = nt * TN + (half ? pair % 2 * (TN / 2) : 0);
+        r.width = half ? TN / 2 : a.wn;
+        r.col = nt * a.wn + (half ? pair % 2 * (TN / 2) : 0);
         r.k0 = p.k[0];
         r.kb_first = p.kb[0];
         return r;
@@ -463,14 +464,18 @@ struct GemmPolicy {
         if (A_MN) column_partials(a.sums, w, 2 * a.np * EPI, lane);   // (the weight gradients)
     }
     static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
-    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int) { return 2 * (16384 + u.width * 64); }
-    template <bool MN, int ROWS>
-    static __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int k,
+    static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int)
+    {
+        return 2 * (16384 + (B_MN ? mn_boxes(u.width / 2) * 8192 : u.width * 64));
+    }
+    static __device__ __forceinline__ int mn_boxes(int rows) { return rows > 64 ? 2 : 1; }
+    template <bool MN>
+    static __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int row, int rows, int k,
                                                         uint32_t bar)
     {
         if (MN) {
-#pragma unroll
-            for (int i = 0; i < ROWS / 64; ++i) tma_load_2d_pair(dst + 8192 * i, map, row + 64 * i, k, bar);
+            tma_load_2d_pair(dst, map, row, k, bar);
+            if (mn_boxes(rows) > 1) tma_load_2d_pair(dst + 8192, map, row + 64, k, bar);
         } else {
             tma_load_2d_pair(dst, map, k, row, bar);
         }
@@ -482,10 +487,9 @@ struct GemmPolicy {
         int kb = u.kb0 + i;
         const int seg = kb >= u.kb_first;
         if (seg) kb -= u.kb_first;
-        load_operand<A_MN, 128>(dst, &p.a[seg], u.m * 256 + (int)rank * 128, kb * 64, bar);
-        const int row = u.col + (int)rank * (u.width / 2);
-        if (u.width == TN) load_operand<B_MN, TN / 2>(dst + 16384, &p.b[seg], row, kb * 64, bar);
-        else load_operand<B_MN, TN / 4>(dst + 16384, B_MN ? &p.b[seg] : &p.b_half[seg], row, kb * 64, bar);
+        load_operand<A_MN>(dst, &p.a[seg], u.m * 256 + (int)rank * 128, 128, kb * 64, bar);
+        load_operand<B_MN>(dst + 16384, B_MN || u.width == a.wn ? &p.b[seg] : &p.b_half[seg],
+                           u.col + (int)rank * (u.width / 2), u.width / 2, kb * 64, bar);
     }
     static __device__ __forceinline__ void mma(const Args &a, const Unit &u, int, int i, uint32_t src16, uint32_t d)
     {
@@ -500,12 +504,17 @@ struct GemmPolicy {
     struct Pre {
         float bias[BOXES];   // of this lane's column of each box
     };
-    static __device__ __forceinline__ int boxes(const Unit &u) { return u.width == TN ? BOXES : BOXES / 2; }
+    // columns of a warp's part of the unit, and boxes of 32 of them
+    static __device__ __forceinline__ int part_cols(const Unit &u) { return u.width > 128 ? 64 : 32; }
+    static __device__ __forceinline__ int boxes(const Unit &u, int part)
+    {
+        return part * part_cols(u) < u.width ? part_cols(u) / 32 : 0;
+    }
     static __device__ __forceinline__ int row_of(const Unit &u, uint32_t rank, int quad)
     {
         return u.m * 256 + (int)rank * 128 + quad * 32;
     }
-    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.col + part * (u.width / 4) + 32 * j; }
+    static __device__ __forceinline__ int col_of(const Unit &u, int part, int j) { return u.col + part * part_cols(u) + 32 * j; }
     static __device__ __forceinline__ Pre prefetch(const Args &a, const Unit &u, uint32_t rank, int warp, int quad,
                                                    int part, int lane, uint8_t *staging)
     {
@@ -517,7 +526,7 @@ struct GemmPolicy {
             staging_free(lane);
 #pragma unroll
             for (int j = 0; j < BOXES; ++j) {
-                if (j == boxes(u)) break;
+                if (j == boxes(u, part)) break;
                 const int col = col_of(u, part, j) + 8 * (lane & 3);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -540,7 +549,7 @@ struct GemmPolicy {
     {
         const PairProblem &p = a.p[u.p];
         uint8_t *stage = staging + warp * STAGING;
-        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * (u.width / 4);
+        const uint32_t acc = t_lane + slot_col(slot(0, n)) + part * part_cols(u);
         if (u.slot >= 0) {   // fp32 boxes of 16 columns, the two stagings in turn
 #pragma unroll 1
             for (int j = 0; j < 2 * BOXES; ++j) {
@@ -562,6 +571,10 @@ struct GemmPolicy {
             }
             return;
         }
+        if (boxes(u, part) == 0) {
+            release();
+            return;
+        }
         const int row0 = row_of(u, rank, quad);
         if (p.residual) {
             cp_async_wait<0>();
@@ -571,11 +584,11 @@ struct GemmPolicy {
         }
 #pragma unroll
         for (int j = 0; j < BOXES; ++j) {
-            if (j == boxes(u)) break;
+            if (j == boxes(u, part)) break;
             float v[32];
             tmem_ld32(acc + 32 * j, v);
             tmem_wait_ld();
-            if (j == boxes(u) - 1) release();
+            if (j == boxes(u, part) - 1) release();
             uint8_t *box = stage + j * 2048;
             if (p.bias) {
 #pragma unroll
