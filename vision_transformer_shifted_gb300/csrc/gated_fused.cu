@@ -36,12 +36,14 @@ struct FusedArgs {
     int xb, n2;              // K blocks of a token; N of the last product (C rounded up to 32: a pair's step)
     int chunks, slots, slot_bytes;
     bool resident;           // every chunk has its slot: loaded once
+    bool shared_staging;     // the two groups drain through one staging, in turn
     DeviceStatus st;
 };
 
 struct FusedBars {
     uint64_t xfull[2], xempty[2], gfull[2], gempty[2], hready[2], hfree[2], yfull[2], yempty[2];
     uint64_t wfull[FUSED_SLOTS], wempty[FUSED_SLOTS];
+    uint64_t sfree[FUSED_GROUP_WARPS];   // a staging's tiles, in turn by the two groups
 };
 
 // (position, phase) in a ring.
@@ -66,7 +68,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
     __shared__ FusedBars bars;
     __shared__ uint32_t tslot;
     __shared__ __align__(16) float vecs[FUSED_GROUPS * FUSED_GROUP_WARPS][64];   // a warp's biases of its 32 hidden units
-    // [x 2][h 2][weights slots][staging a warp]
+    // [x 2][h 2][weights slots][staging a warp of a group]
     const uint32_t x_bytes = (uint32_t)a.xb * 16384u;
     uint8_t *sx = smem, *sh = sx + 2 * x_bytes, *sw = sh + 2 * 16384, *stg = sw + (size_t)a.slots * a.slot_bytes;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -85,6 +87,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             mbar_init(smem_u32(&bars.yfull[i]), 1);
             mbar_init(smem_u32(&bars.yempty[i]), 2 * FUSED_GROUP_WARPS);
         }
+        for (int i = 0; i < FUSED_GROUP_WARPS; ++i) mbar_init(smem_u32(&bars.sfree[i]), 1);
         for (int i = 0; i < a.slots; ++i) {
             mbar_init(smem_u32(&bars.wfull[i]), 1);
             mbar_init(smem_u32(&bars.wempty[i]), 1);
@@ -220,67 +223,86 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
         // ---------------- activations and output ----------------
         const int e = warp - 4, grp = e / FUSED_GROUP_WARPS, quad = warp & 3, half = (e % FUSED_GROUP_WARPS) >> 2;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        uint8_t *hbuf = sh + grp * 16384, *stage = stg + e * 2048;
+        uint8_t *hbuf = sh + grp * 16384, *stage = stg + (a.shared_staging ? e % FUSED_GROUP_WARPS : e) * 4096;
         const uint32_t gempty = map_rank(smem_u32(&bars.gempty[grp]), 0), hready = map_rank(smem_u32(&bars.hready[grp]), 0);
         const int total = my * a.chunks;
         float *vec = vecs[e];
 
-        // the residual's box j of this pair's i-th tile on its way into the warp's
+        // The staging (two boxes of 32 columns), where it is shared, goes from group
+        // to group with the tiles they drain: tile i's warp takes it when tile i -
+        // 1's stores have read it (over a tile ago, as a rule).
+        const int boxes = half * 64 + 32 < a.C ? 2 : half * 64 < a.C;
+        const uint32_t sfree = smem_u32(&bars.sfree[e % FUSED_GROUP_WARPS]);
+        bool owed = false;   // this warp's last stores may still read the staging
+        auto pass_on = [&]() {
+            if (!owed || !a.shared_staging) return;
+            if (lane == 0) {
+                bulk_wait_read();
+                mbar_arrive(sfree);
+            }
+            owed = false;
+        };
+        auto take = [&](int i) {
+            if (!a.shared_staging) staging_free(lane);
+            else if (i > 0 && boxes && !warp_pair_wait(sfree, (uint32_t)(i - 1) & 1u, limit)) failed = true;
+        };
+        // the residual's boxes of this pair's i-th tile on their way into the
         // staging, four lanes a row (a row a lane, 32 lines an instruction, took
         // 16 us of 67 at 200,704 x 96)
-        auto fetch_residual = [&](int i, int j) {
-            const int row0 = (pair + i * a.np) * 256 + (int)rank * 128 + quad * 32, col = half * 64 + 32 * j + 8 * (lane & 3);
-            staging_free(lane);
+        auto fetch_residual = [&](int i) {
+            take(i);
+            if (failed) return;
+            const int row0 = (pair + i * a.np) * 256 + (int)rank * 128 + quad * 32;
+#pragma unroll 1
+            for (int j = 0; j < boxes; ++j) {
+                const int col = half * 64 + 32 * j + 8 * (lane & 3);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 8 * k + (lane >> 2);
-                const bool ok = row0 + r < a.rows && col < a.C;
-                cp_async16(smem_u32(stage) + sw64_offset(r, lane & 3),
-                           ok ? a.residual + (int64_t)(row0 + r) * a.C + col : a.residual, ok ? 16u : 0u);
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2);
+                    const bool ok = row0 + r < a.rows && col < a.C;
+                    cp_async16(smem_u32(stage) + j * 2048 + sw64_offset(r, lane & 3),
+                               ok ? a.residual + (int64_t)(row0 + r) * a.C + col : a.residual, ok ? 16u : 0u);
+                }
             }
             cp_async_commit();
         };
         // output rows of this pair's i-th tile: bias, residual, store
         auto drain = [&](int i) {
             const int y = i & 1;
-            if (!warp_pair_wait(smem_u32(&bars.yfull[y]), (uint32_t)(i >> 1) & 1u, limit)) {
+            if (!a.residual) take(i);
+            if (failed || !warp_pair_wait(smem_u32(&bars.yfull[y]), (uint32_t)(i >> 1) & 1u, limit)) {
                 failed = true;
                 return;
             }
             tc_fence_after();
             const int row0 = (pair + i * a.np) * 256 + (int)rank * 128 + quad * 32;
+            if (a.residual) cp_async_wait<0>();
+            __syncwarp();   // (the vector's last readers are done; the residual is there)
 #pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < boxes; ++j) {
                 const int c0 = half * 64 + 32 * j;
-                if (c0 >= a.C) break;
                 float v[32];
                 tmem_ld32(TY + 128 * y + lanes + c0, v);
-                __syncwarp();   // (the vector's last readers are done)
-                vec[lane] = lane_value(a.bd, c0 + lane, a.C);
-                if (a.residual) {
-                    if (j) fetch_residual(i, j);   // (the first box: fetched a chunk ago)
-                    cp_async_wait<0>();
-                } else if (lane == 0) {
-                    bulk_wait_read();
-                }
+                vec[32 * j + lane] = lane_value(a.bd, c0 + lane, a.C);
                 __syncwarp();
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float b[8];
                     if (a.bd) {
-                        spread8(vec, q, b);
+                        spread8(vec + 32 * j, q, b);
                         add8(v + 8 * q, b);
                     }
-                    uint4 *at = reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q));
+                    uint4 *at = reinterpret_cast<uint4 *>(stage + j * 2048 + sw64_offset(lane, q));
                     if (a.residual) {
                         load8(reinterpret_cast<const bf16 *>(at), 0, 8, b);
                         add8(v + 8 * q, b);
                     }
                     *at = pack8f(v + 8 * q);
                 }
-                store_box(&a.out, c0, row0, row0 < a.rows, stage, lane);
+                store_box(&a.out, c0, row0, row0 < a.rows, stage + j * 2048, lane);
             }
+            owed = boxes > 0;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&bars.yempty[y]), 0));
@@ -300,6 +322,7 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
 #pragma unroll 1
         for (int q = grp; q < total && !failed; q += FUSED_GROUPS) {
             const uint32_t use = (uint32_t)(q >> 1) & 1u;
+            pass_on();
             if (!warp_pair_wait(smem_u32(&bars.gfull[grp]), use, limit)) {
                 failed = true;
                 break;
@@ -359,13 +382,16 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
             if (i > tile)
                 for (int t = tile; t < i; ++t)
                     if ((t & 1) == grp) pending = t;
-            if (pending >= 0 && a.residual && half * 64 < a.C) {
-                fetch_residual(pending, 0);
-                const int64_t row = (int64_t)(pair + pending * a.np) * 256 + (int)rank * 128 + quad * 32 + lane;
-                if (row < a.rows && half * 64 + 32 < a.C) prefetch_l2(a.residual + row * a.C + half * 64 + 32);
+            if (pending >= 0 && a.residual) {
+                pass_on();   // (the other group may need it to get to where it passes on the one awaited here)
+                fetch_residual(pending);
             }
         }
-        if (!failed && pending >= 0) drain(pending);
+        if (!failed && pending >= 0) {
+            pass_on();
+            drain(pending);
+        }
+        pass_on();
         const int mine = (total - grp + 1) / FUSED_GROUPS;   // chunks of this group
         if (!failed && mine > 0) failed = !warp_pair_wait(smem_u32(&bars.hfree[grp]), (uint32_t)(mine - 1) & 1u, limit);
         if (lane == 0) bulk_wait_all();
@@ -393,8 +419,15 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     a.xb = (C + 63) / 64;
     a.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
     a.slot_bytes = a.xb * 8192 + a.n2 * 64;
-    const int fixed = 2 * a.xb * 16384 + 2 * 16384 + FUSED_GROUPS * FUSED_GROUP_WARPS * 2048;
-    const int room = 222 * 1024 - 1024 - fixed;   // (5 KB for the barriers and biases, 1 KB of alignment)
+    // A staging a group where it leaves room for every chunk's weights (400000 x 64
+    // x 128: 55 us, 63 shared), else one for both (200704 x 96 x 256: 51 us; 54
+    // with halves of it, where the second box waits for the first one's store).
+    constexpr int STAGING = FUSED_GROUP_WARPS * 4096;
+    const int most = 222 * 1024 - 1024;   // (5 KB for the barriers and biases, 1 KB of alignment)
+    int fixed = 2 * a.xb * 16384 + 2 * 16384 + FUSED_GROUPS * STAGING;
+    a.shared_staging = a.chunks > FUSED_SLOTS || fixed + a.chunks * a.slot_bytes > most;
+    if (a.shared_staging) fixed -= STAGING;
+    const int room = most - fixed;
     a.slots = room / a.slot_bytes;
     if (a.slots > FUSED_SLOTS) a.slots = FUSED_SLOTS;
     if (a.slots > a.chunks) a.slots = a.chunks;
