@@ -14,7 +14,7 @@
 // the MMAs of its own last chunk.  Weights stream through a ring of chunks, or
 // stay (loaded once) where all chunks fit it.  Arithmetic per hidden value
 // binds (the activation: about 20 instructions with the drain), not HBM: 200704 x
-// 96 x 256 with biases and residual takes 52.4 us, 118 as two kernels.
+// 96 x 256 with biases and residual takes 49.8 us, 118 as two kernels.
 #include <atomic>
 #include <cstring>
 
