@@ -7,9 +7,11 @@
  *   s = x + residual (rounded to bf16; s = x without a residual)
  *   r = 1 / sqrt(mean_c s^2 + eps)
  *   y = s r gamma
- * (fp32: a row whose squares add up to more than 3.4e38 has r = 0.)  The norm
- * sees the stored (rounded) sum, so that the backward pass, which
- * starts from it, differentiates the very function that ran.  8-bit output:
+ * (fp32: a row whose squares add up to more than 3.4e38 has r = 0; with eps = 0,
+ * one whose squares add up to less than 1.2e-38 has an inexact r, and a row of
+ * zeros gives NaN, in the backward pass also in dgamma.)  The norm sees the
+ * stored (rounded) sum, so that the backward pass, which starts from it,
+ * differentiates the very function that ran.  8-bit output:
  * scale = max(max_c |y|, 1e-30) / 448 per row (fp32), code = y / scale in e4m3
  * (round to nearest even; 448 is its largest value), y ~ code * scale.  A row
  * of zeros (eps > 0) gets zero codes and a positive scale; a row holding an infinity or

@@ -397,3 +397,21 @@ def test_two_host_threads_with_a_handle_each():
     for t in threads:
         t.join()
     assert not failures, failures
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [8, 96, 192, 768, 2744])
+@pytest.mark.parametrize("rows", [1, 3, 300, 5003])
+@pytest.mark.parametrize("with_dsum", [True, False])
+def test_backward_without_eps(rows, C, with_dsum):
+    """eps = 0 and no row of zeros: every gradient is finite, whatever part of a
+    block the rows leave empty (there the mean of the squares is zero, and one
+    over its root infinite)."""
+    s, dsum, g, dy = inputs(rows, C, with_dsum, seed=9)
+    dx, dgamma, size, gsize = gradients(s, g, dy, dsum, eps=0.0)
+    sd, md, gd, yd = dev(s, dsum, g, dy)
+    gx, gg = torch.full_like(sd, float("nan")), torch.full((C,), float("nan"), device=DEV)
+    with rms(C, 0.0) as h:
+        sw.swin_block_rms_backward(h, sd, gd, yd, gx, gg, dsum=md)
+    close(gx, dx, 2.0 ** -8 * dx.abs() + FP * size)
+    close(gg, dgamma, FP * gsize)

@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) rms_backward_ke
             forget(g[k]);
             if (DSUM) forget(m[k]);
         }
-        const float r = rsqrtf(fmaf(sq, a.inv_c, a.eps)), q = dot * a.inv_c * r * r * r;
+        // (no row: r = 0, since its columns' sums get zero times r, and with eps = 0
+        // one over the root of its mean is infinite)
+        const float r = row_ok ? rsqrtf(fmaf(sq, a.inv_c, a.eps)) : 0.f, q = dot * a.inv_c * r * r * r;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
