@@ -12,10 +12,10 @@
  * zeros gives NaN, in the backward pass also in dgamma.)  The norm sees the
  * stored (rounded) sum, so that the backward pass, which starts from it,
  * differentiates the very function that ran.  8-bit output:
- * scale = max(max_c |y|, 1e-30) / 448 per row (fp32), code = y / scale in e4m3
- * (round to nearest even; 448 is its largest value), y ~ code * scale.  A row
- * of zeros (eps > 0) gets zero codes and a positive scale; a row holding an infinity or
- * a NaN gets NaN codes and a NaN scale.
+ * scale = max(max_c |y|, 1e-30) / 448 per row, code = y / scale (both fp32
+ * quotients) rounded to nearest even in e4m3 (448 is its largest value), y ~
+ * code * scale.  A row of zeros (eps > 0) gets zero codes and a positive scale;
+ * a row holding an infinity or a NaN gets NaN codes and a NaN scale.
  *
  * Beside swin_stage_norm (LayerNorm): the other norm of the residual stream,
  * in front of swin_block_gated_forward (swin_gated.h), whose 8-bit form reads

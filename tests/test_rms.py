@@ -415,3 +415,80 @@ def test_backward_without_eps(rows, C, with_dsum):
         sw.swin_block_rms_backward(h, sd, gd, yd, gx, gg, dsum=md)
     close(gx, dx, 2.0 ** -8 * dx.abs() + FP * size)
     close(gg, dgamma, FP * gsize)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [512, 4096])
+@pytest.mark.parametrize("amax", [1.53125, 1.078125, 1.625, 1.75])
+def test_codes_are_the_rounded_quotients(C, amax):
+    """Rows of +-1 with eps = 0: r is 1 and y = s gamma exactly, so that code and
+    scale are known to the last bit.  gamma holds every bf16 value of four
+    octaves up to amax; some of their quotients lie on the middle between two
+    codes, where y times 1 / scale rounds to the other one."""
+    v = torch.arange(0x3e00, 0x4000, dtype=torch.int32).to(torch.int16).view(BF)   # 0.125 to 2
+    v = v[v.float() <= amax]
+    gamma = torch.full((C,), amax, dtype=BF)
+    gamma[:v.numel()] = v
+    sign = torch.randint(0, 2, (9, C), generator=torch.Generator().manual_seed(C)) * 2 - 1
+    x = sign.to(BF)
+    xd, gd = dev(x, gamma)
+    codes, scales = torch.empty(9, C, dtype=E4M3, device=DEV), torch.empty(9, device=DEV)
+    with rms(C, 0.0) as h:
+        sw.swin_block_rms_forward_q8(h, xd, gd, codes, scales)
+    scale = torch.tensor(amax) / 448
+    assert (scales.cpu() == scale).all()
+    assert torch.equal(codes.cpu().float(), (x.float() * gamma.float() / scale).to(E4M3).float())
+
+
+@pytest.mark.gpu
+def test_codes_of_products_are_the_rounded_quotients():
+    """The same with y of 16 bits: rows of multiples of 1/128 whose mean square is
+    one (eight squares of whole numbers with the sum 8 * 128^2, time and again),
+    where the sums are exact and r is 1."""
+    import random
+    rng = random.Random(5)
+    C, rows, squares = 512, 400, {i * i: i for i in range(1, 256)}
+
+    def eight():
+        while True:
+            v = [rng.randint(1, 200) for _ in range(7)]
+            left = 8 * 128 * 128 - sum(i * i for i in v)
+            if left in squares:
+                return v + [squares[left]]
+
+    some = [eight() for _ in range(300)]
+    x = torch.tensor([[i * rng.choice((-1, 1)) for _ in range(C // 8) for i in rng.choice(some)]
+                      for _ in range(rows)]).double().div(128).to(BF)
+    assert (x.double().pow(2).mean(-1) == 1).all()
+    gamma = (1 + 0.2 * torch.randn(C, generator=torch.Generator().manual_seed(6))).to(BF)
+    y = x.float() * gamma.float()
+    scale = y.abs().amax(-1) / 448
+    want = (y / scale[:, None]).to(E4M3).float()
+    assert not torch.equal(want, (y * (1 / scale)[:, None]).to(E4M3).float())
+    codes, scales = torch.empty(rows, C, dtype=E4M3, device=DEV), torch.empty(rows, device=DEV)
+    with rms(C, 0.0) as h:
+        sw.swin_block_rms_forward_q8(h, *dev(x, gamma), codes, scales)
+    assert torch.equal(scales.cpu(), scale)
+    assert torch.equal(codes.cpu().float(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("factor", [2.0 ** -120, 2.0 ** -95, 2.0 ** -60, 2.0 ** 100, float("inf")])
+def test_codes_of_very_small_and_large_rows(factor):
+    """y from gamma (x of +-1, eps = 0) down to where a row's scale stands at its
+    floor, up to 2^101, and infinite."""
+    C = 256
+    gamma = torch.randn(C, generator=torch.Generator().manual_seed(7)).to(BF)
+    if factor == float("inf"):
+        gamma[3] = factor
+    else:
+        gamma = (gamma.float() * factor).to(BF)
+    x = torch.ones(3, C, dtype=BF)
+    x[1] = -1
+    codes, scales = torch.empty(3, C, dtype=E4M3, device=DEV), torch.empty(3, device=DEV)
+    with rms(C, 0.0) as h:
+        sw.swin_block_rms_forward_q8(h, *dev(x, gamma), codes, scales)
+    scale = gamma.float().abs().amax().clamp_min(1e-30) / 448
+    assert (scales.cpu() == scale).all()
+    want = (x.float() * gamma.float() / scale).to(E4M3).float()
+    assert torch.equal(codes.cpu().float().nan_to_num(nan=7e7), want.nan_to_num(nan=7e7))

@@ -8,8 +8,9 @@
 // lanes, at most four 16-byte pieces each: their loads are all in flight at
 // once and the statistics need shuffles only); longer rows take a block each.
 // (The backward, with three inputs, at most three pieces a lane.)  With residual,
-// 200704 x 96: 23.6 us, 6.5 TB/s; to e4m3, 8191 x 4096: 36.9 us, 6.4 TB/s;
+// 200704 x 96: 23.6 us, 6.5 TB/s; to e4m3, 8191 x 4096: 37.4 us, 6.3 TB/s;
 // backward 589824 x 192 with dsum: 135 us, 6.7 TB/s.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cuda_fp8.h>
@@ -43,6 +44,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
 {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// The same of three magnitudes.
+__device__ __forceinline__ float max_abs(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -96,17 +105,6 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, int threads, int 
     }
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8])
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack_bf16x2(w[e]);
-        v[2 * e] = f.x;
-        v[2 * e + 1] = f.y;
-    }
-}
-
 __device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
     uint4 u;
@@ -117,13 +115,52 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr)
 // The compiler takes u for a new value from here on.
 __device__ __forceinline__ void forget(uint4 &u) { asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)); }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8])
+__device__ __forceinline__ const uint4 &ld16(const bf16 *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// One thread's piece of a row, eight channels, as pairs.
+struct Piece {
+    f2 v[4];
+};
+__device__ __forceinline__ Piece piece(const uint4 &u)
 {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    Piece p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p.v[e] = pack2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+    return p;
+}
+__device__ __forceinline__ uint4 pack(const Piece &p)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        unpack2(p.v[e], lo, hi);
+        w[e] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float sum2(f2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return a + b;
 }
 
-__device__ __forceinline__ const uint4 &ld16(const bf16 *p) { return *reinterpret_cast<const uint4 *>(p); }
+// y / b for two values, correctly rounded, with inv = 1 / b correctly rounded:
+// y inv is within 1.5 units of the last place; one correction by the remainder y
+// - q b makes that less than one, and the next is then exact (P. W. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor,
+// 1990).  For b from 1e-24, where the remainder of every quotient that is not
+// rounded to zero is a number with all of its bits, to the largest finite one.
+// (A product with inv alone gives a neighbouring code once in 20,000 values, 36.9
+// us at 8191 x 4096; with the corrections 37.4, with divisions 46.5.)
+__device__ __forceinline__ f2 quotient2(f2 y, f2 minus_b, f2 inv)
+{
+    f2 q = mul2(y, inv);
+    q = fma2(fma2(q, minus_b, y), inv, q);
+    return fma2(fma2(q, minus_b, y), inv, q);
+}
 
 template <int CPL, bool BLOCK, bool Q8>
 __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs a)
@@ -147,24 +184,23 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs 
         s[k] = ok ? ld16(a.x + base + c * 8) : make_uint4(0, 0, 0, 0);
         if (a.residual) t[k] = ok ? ld16(a.residual + base + c * 8) : make_uint4(0, 0, 0, 0);
     }
-    float sq = 0.f;
+    f2 sq2 = 0;
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
         const int c = li + k * step;
-        float v[8];
-        unpack8(s[k], v);
+        Piece v = piece(s[k]);
         if (a.residual) {
-            float w[8];
-            unpack8(t[k], w);
+            const Piece w = piece(t[k]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += w[e];
-            s[k] = pack8(v);
-            unpack8(s[k], v);   // the stored (rounded) sum is what the norm sees
+            for (int e = 0; e < 4; ++e) v.v[e] = add2(v.v[e], w.v[e]);
+            s[k] = pack(v);
+            v = piece(s[k]);   // the stored (rounded) sum is what the norm sees
             if (a.out_sum && row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.out_sum + base + c * 8) = s[k];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(v[e], v[e], sq);
+        for (int e = 0; e < 4; ++e) sq2 = fma2(v.v[e], v.v[e], sq2);
     }
+    float sq = sum2(sq2);
     uint4 gm[CPL];   // (asked for before the row's sum is known)
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
@@ -178,46 +214,54 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) rms_forward_kernel(RmsArgs 
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
             if (!(row_ok && c < a.chunks)) continue;
-            float v[8], g[8];
-            unpack8(s[k], v);
-            unpack8(gm[k], g);
+            Piece v = piece(s[k]);
+            const Piece g = piece(gm[k]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * g[e];
-            *reinterpret_cast<uint4 *>((bf16 *)a.out + base + c * 8) = pack8(v);
+            for (int e = 0; e < 4; ++e) v.v[e] = mul2(mul2(v.v[e], pack2(r)), g.v[e]);
+            *reinterpret_cast<uint4 *>((bf16 *)a.out + base + c * 8) = pack(v);
         }
         return;
     }
-    float y[CPL][8];
+    f2 y[CPL][4];
     float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) {
-        const int c = li + k * step;
-        const bool ok = row_ok && c < a.chunks;
-        float g[8];
-        unpack8(s[k], y[k]);
-        unpack8(gm[k], g);
+    for (int k = 0; k < CPL; ++k) {   // (pieces behind the row are zeros)
+        const Piece v = piece(s[k]), g = piece(gm[k]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            y[k][e] = y[k][e] * r * g[e];
-            if (ok) amax = max_nan(amax, fabsf(y[k][e]));
+        for (int e = 0; e < 4; ++e) {
+            y[k][e] = mul2(mul2(v.v[e], pack2(r)), g.v[e]);
+            float lo, hi;
+            unpack2(y[k][e], lo, hi);
+            amax = max_abs(amax, lo, hi);
         }
     }
     amax = row_reduce<MaxOp, BLOCK>(amax, a.lpr, red);
-    const float scale = max_nan(amax, MIN_AMAX) / E4M3_MAX, inv = 1.f / scale;
+    float scale = max_nan(amax, MIN_AMAX) / E4M3_MAX;
     if (row_ok && li == 0) a.scales[row] = scale;
+    // (outside quotient2's range: a small scale and its row times 2^64, exactly; an
+    // infinite scale makes finite values zero, NaN everything NaN)
+    if (!(scale >= 1e-24f && scale <= FLT_MAX)) {
+        const bool small = scale < 1e-24f;
+        const f2 up = pack2(small ? 0x1p64f : scale > FLT_MAX ? 0.f : scale);
+#pragma unroll
+        for (int k = 0; k < CPL; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[k][e] = mul2(y[k][e], up);
+        scale = small ? scale * 0x1p64f : 1.f;
+    }
+    const f2 minus_b = pack2(-scale), inv = pack2(1.f / scale);
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
         const int c = li + k * step;
         if (!(row_ok && c < a.chunks)) continue;
-        uint32_t w[2];
+        uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float *v = &y[k][4 * q];
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
-            w[q] = lo | (hi << 16);
+        for (int e = 0; e < 4; ++e) {
+            float2 q;
+            unpack2(quotient2(y[k][e], minus_b, inv), q.x, q.y);
+            w[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
         }
-        *reinterpret_cast<uint2 *>((uint8_t *)a.out + base + c * 8) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>((uint8_t *)a.out + base + c * 8) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
     }
 }
 
@@ -230,20 +274,8 @@ struct RmsBwdArgs {
     int lanes;        // of a row: of a warp, or (wide rows) threads
 };
 
-// One thread's piece (eight channels) of a row in the backward, dx = r (a - n
-// mean(a n)) + dsum with n = s r, a = dy gamma, as pairs of channels.
-struct Piece {
-    f2 v[4];
-};
-__device__ __forceinline__ Piece piece(const uint4 &u)
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    Piece p;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p.v[e] = pack2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-    return p;
-}
-// First its shares of sum s^2 and sum a s:
+// The backward, dx = r (a - n mean(a n)) + dsum with n = s r, a = dy gamma, of a
+// thread's piece of a row.  First its shares of sum s^2 and sum a s:
 __device__ __forceinline__ void piece_sums(const Piece &s, const Piece &d, const Piece &g, f2 &sq, f2 &dot)
 {
 #pragma unroll
@@ -270,13 +302,6 @@ __device__ __forceinline__ uint4 piece_grad(const Piece &s, const Piece &d, cons
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ float sum2(f2 v)
-{
-    float a, b;
-    unpack2(v, a, b);
-    return a + b;
-}
-
 // Blocks of 256 threads on an SM: enough bytes of loads in flight, and no more
 // (200000 x 512 with dsum, two pieces a lane: 130.5 us with two blocks, 131.5
 // with three, 142 with four; without dsum 114, 103 and 96; 589824 x 192 without
