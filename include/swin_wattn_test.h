@@ -86,6 +86,12 @@ int swin_wattn_test_noalloc_watchdog(int64_t wait_limit_us, swin_stream_t stream
 int swin_block_gated_test_stall(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
                                 int64_t wait_limit_us, swin_stream_t stream);
 
+/* What the gated block's loading warp waits for before it ends, having loaded
+ * `issued` K blocks through a ring of `stages`: *stage and the *parity of the
+ * phase that the k-th of the last min(stages, issued) releases completes (k from
+ * 0).  On the host alone; EINVAL for another k. */
+int swin_block_gated_test_last_use(int stages, int issued, int k, int *stage, int *parity);
+
 /* swin_wattn_test_corrupt_workspace for a gated block's handle. */
 int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side);
 

@@ -652,3 +652,23 @@ def test_products_in_tiles_of_192_columns(rows, C, F):
     ref, tol = backward_ref(x, p, dy, "gelu")
     for k, v in dict(grads, dx=dx).items():
         close(v, ref[k], tol[k])
+
+
+@pytest.mark.parametrize("stages", [5, 6])
+def test_closing_waits_cover_every_release(stages):
+    """Before a CTA ends, its loading warp waits for the last release of every
+    stage that it filled, also where it filled fewer than there are.  Modelled on
+    a barrier's rule: a wait for parity p passes once the phase of that parity
+    has completed, and at once for parity 1 on a fresh barrier."""
+    def passes(completed, parity):
+        return (completed - 1) % 2 == parity   # (the phase that completed last; -1 before the first)
+
+    for issued in range(0, 4 * stages + 2):
+        uses = [len(range(s, issued, stages)) for s in range(stages)]   # releases of each stage's barrier
+        seen = [sw.swin_block_gated_test_last_use(stages, issued, k) for k in range(min(stages, issued))]
+        assert sorted(s for s, _ in seen) == [s for s in range(stages) if uses[s]]
+        for s, parity in seen:
+            assert passes(uses[s], parity), (issued, s)
+            assert not passes(uses[s] - 1, parity), (issued, s)   # not before the last one
+        with pytest.raises(sw.SwinWAttnError):
+            sw.swin_block_gated_test_last_use(stages, issued, min(stages, issued))

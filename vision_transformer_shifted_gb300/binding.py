@@ -82,6 +82,7 @@ _SIGNATURES = {
     "swin_block_gated_destroy": ["p"],
     "swin_block_gated_test_stall": ["p", "p", "i", "p", "l", "p"],
     "swin_block_gated_test_corrupt_workspace": ["p", "i"],
+    "swin_block_gated_test_last_use": ["i", "i", "i", "p", "p"],
 }
 
 # swin_block_params (include/swin_block.h), field for field
@@ -522,3 +523,10 @@ def swin_block_gated_test_stall(h, x, params, wait_limit_us, stream=None):
 
 def swin_block_gated_test_corrupt_workspace(h, side):
     return _check("swin_block_gated_test_corrupt_workspace", load().swin_block_gated_test_corrupt_workspace(h, side))
+
+
+def swin_block_gated_test_last_use(stages, issued, k):
+    stage, parity = ctypes.c_int(), ctypes.c_int()
+    _check("swin_block_gated_test_last_use", load().swin_block_gated_test_last_use(
+        stages, issued, k, ctypes.addressof(stage), ctypes.addressof(parity)))
+    return stage.value, parity.value

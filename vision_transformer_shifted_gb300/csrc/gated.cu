@@ -765,6 +765,15 @@ int swin_block_gated_test_stall(swin_block_gated_t h, const void *x, int rows, c
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
 }
 
+int swin_block_gated_test_last_use(int stages, int issued, int k, int *stage, int *parity)
+{
+    if (stages < 1 || issued < 0 || k < 0 || k >= stages || k >= issued || !stage || !parity) return SWIN_WATTN_EINVAL;
+    const RingUse u = last_use(stages, issued, k);
+    *stage = u.stage;
+    *parity = (int)u.parity;
+    return SWIN_WATTN_OK;
+}
+
 int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side)
 {
     if (!h || side < 0 || side > 1) return SWIN_WATTN_EINVAL;

@@ -250,6 +250,18 @@ inline PairDeal deal_tiles(int tiles, int pairs)
     return d;
 }
 
+// The k-th of the last min(stages, issued) uses of a ring's stages by `issued` K
+// blocks: its stage, and the parity of the phase that its release completes.
+struct RingUse {
+    int stage;
+    uint32_t parity;
+};
+__host__ __device__ inline RingUse last_use(int stages, int issued, int k)
+{
+    const int i = issued - (issued < stages ? issued : stages) + k;
+    return {i % stages, (uint32_t)(i / stages) & 1u};
+}
+
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * P::EPI, 1)
 pair_kernel(const __grid_constant__ typename P::Args a)
@@ -327,11 +339,8 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         // every stage given back: no commit is on its way to this CTA's
         // barriers when it ends
         for (int k = 0; k < P::STAGES && k < issued && !failed; ++k) {
-            failed = !warp_pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns);
-            if (++s == P::STAGES) {
-                s = 0;
-                ph ^= 1u;
-            }
+            const RingUse u = last_use(P::STAGES, issued, k);
+            failed = !warp_pair_wait(empty + 8 * u.stage, u.parity, a.st.wait_ns);
         }
         if (failed) {
             // copies in flight land before this CTA's memory is given back:
