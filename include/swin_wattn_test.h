@@ -92,6 +92,21 @@ int swin_block_gated_test_stall(swin_block_gated_t h, const void *x, int rows, c
  * 0).  On the host alone; EINVAL for another k. */
 int swin_block_gated_test_last_use(int stages, int issued, int k, int *stage, int *parity);
 
+/* How the gated block divides a call for more than 128 rows, on the current
+ * device or, without one, for 152 SMs; six ints.  A product (the forward's last
+ * one, dx, the three weight gradients together): {tiles of 256 rows, CTA pairs,
+ * columns of a tile, half tiles of the last round, its tiles cut along K, 1 if
+ * into equal slices}.  The one-kernel forward (C <= 128): {tiles, pairs, chunks
+ * of 64 hidden units, weight chunks held, 1 if that is all, 1 if the two groups
+ * of warps share a staging}.  EINVAL for other sizes. */
+enum {
+    SWIN_BLOCK_GATED_PLAN_DOWN = 0,
+    SWIN_BLOCK_GATED_PLAN_DX = 1,
+    SWIN_BLOCK_GATED_PLAN_WEIGHTS = 2,
+    SWIN_BLOCK_GATED_PLAN_NARROW = 3
+};
+int swin_block_gated_test_plan(int C, int F, int rows, int which, int *plan);
+
 /* swin_wattn_test_corrupt_workspace for a gated block's handle. */
 int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side);
 

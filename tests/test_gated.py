@@ -672,3 +672,82 @@ def test_closing_waits_cover_every_release(stages):
             assert not passes(uses[s] - 1, parity), (issued, s)   # not before the last one
         with pytest.raises(sw.SwinWAttnError):
             sw.swin_block_gated_test_last_use(stages, issued, min(stages, issued))
+
+
+# How the sizes of the tests above and below are divided (on 76 CTA pairs): per
+# product (tiles, pairs, columns of a tile, half tiles, tiles cut along K, equal
+# slices).
+PLANS = {
+    (5001, 144, 520): ((20, 40, 256, 40, 0, 0), (20, 40, 256, 40, 0, 0), (9, 76, 256, 0, 9, 0)),
+    (19700, 144, 2056): ((77, 76, 256, 2, 0, 0), (77, 76, 256, 0, 1, 0), (27, 76, 256, 0, 27, 0)),
+    (19700, 144, 4104): ((77, 76, 256, 0, 1, 0), (77, 76, 256, 0, 1, 0), (51, 76, 256, 0, 51, 0)),
+    (300, 264, 8200): ((4, 76, 256, 0, 4, 0), (4, 76, 256, 0, 4, 0), (218, 76, 192, 0, 0, 0)),
+    (300, 120, 8200): ((2, 64, 128, 0, 2, 0), (2, 76, 128, 0, 2, 0), (131, 76, 128, 0, 0, 0)),
+    (20000, 136, 264): ((79, 76, 256, 6, 0, 0), (79, 76, 256, 6, 0, 0), (6, 72, 256, 0, 6, 1)),
+    (1300, 2048, 264): ((66, 66, 192, 0, 0, 0), (66, 66, 192, 0, 0, 0), (60, 60, 192, 0, 0, 0)),
+    (2800, 1000, 136): ((66, 66, 192, 0, 0, 0), (66, 66, 192, 0, 0, 0), (12, 24, 256, 24, 0, 0)),
+}
+# The one-kernel forward: (tiles, pairs, chunks, chunks held, all of them, one staging)
+NARROW_PLANS = {
+    (20000, 8, 136): (79, 76, 3, 3, 1, 0), (40000, 128, 136): (157, 76, 3, 3, 1, 1),
+    (40000, 128, 200): (157, 76, 4, 3, 0, 1), (45001, 96, 256): (176, 76, 4, 4, 1, 1),
+    (45000, 96, 320): (176, 76, 5, 4, 0, 1), (60001, 64, 64): (235, 76, 1, 1, 1, 0),
+    (59000, 40, 328): (231, 76, 6, 6, 1, 0),
+}
+
+
+def test_the_tested_sizes_reach_the_plans_they_are_for():
+    for (rows, C, F), want in PLANS.items():
+        for which, w in zip((sw.BLOCK_GATED_PLAN_DOWN, sw.BLOCK_GATED_PLAN_DX, sw.BLOCK_GATED_PLAN_WEIGHTS), want):
+            assert sw.swin_block_gated_test_plan(C, F, rows, which) == w, (rows, C, F, which)
+    for (rows, C, F), w in NARROW_PLANS.items():
+        assert sw.swin_block_gated_test_plan(C, F, rows, sw.BLOCK_GATED_PLAN_NARROW) == w, (rows, C, F)
+    for bad in ((144, 64, 300, sw.BLOCK_GATED_PLAN_NARROW), (96, 64, 128, 0), (96, 12, 300, 0), (96, 64, 300, 4)):
+        with pytest.raises(sw.SwinWAttnError):
+            sw.swin_block_gated_test_plan(*bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F,launches", [(19700, 144, 2056, 2), (19700, 144, 4104, 3)])
+def test_last_product_after_whole_rounds(rows, C, F, launches):
+    """A whole round of tiles, then one tile as halves, or cut along K and joined
+    by a third kernel, which adds bias and residual; from 16 and 8 bits, in place."""
+    assert sw.swin_block_gated_test_plan(C, F, rows, sw.BLOCK_GATED_PLAN_DOWN) == PLANS[rows, C, F][0]
+    x, p, r, _ = make(rows, C, F, seed=19)
+    x8, sx = quantise(x)
+    q = dict(bg=p["bg"], bu=p["bu"], Wd=p["Wd"], bd=p["bd"])
+    (q["Wg8"], q["sg"]), (q["Wu8"], q["su"]) = quantise(p["Wg"]), quantise(p["Wu"])
+    exact = dict(p, Wg=q["Wg8"].double() * q["sg"].double()[:, None], Wu=q["Wu8"].double() * q["su"].double()[:, None])
+    xd, pd, rd = dev(x), dev(p), dev(r)
+    out, out8, place = torch.full_like(xd, float("nan")), torch.full_like(xd, float("nan")), rd.clone()
+    with gated(C, F) as h:
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        assert sw.swin_block_gated_last_launches(h) == launches
+        sw.swin_block_gated_forward(h, xd, pd, place, residual=place)
+        sw.swin_block_gated_forward_q8(h, dev(x8), dev(sx), dev(q), out8, residual=rd)
+        assert sw.swin_block_gated_last_launches(h) == launches
+        sw.swin_block_gated_sync_status(h)
+    for got, a, w in ((out, x, p), (out8, x8.double() * sx.double()[:, None], exact)):
+        ref, tol = forward_ref(dev(a), dev(w), rd, "silu")
+        close(got, ref.cpu(), tol.cpu())
+    assert torch.equal(place, out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", sorted(NARROW_PLANS))
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_narrow_tiles_with_biases_and_residual(rows, C, F, kind):
+    """The one-kernel form with both over several tiles a pair: one staging or two,
+    odd and even counts of chunks, weights that stay and that stream; in place."""
+    assert sw.swin_block_gated_test_plan(C, F, rows, sw.BLOCK_GATED_PLAN_NARROW) == NARROW_PLANS[rows, C, F]
+    x, p, r, _ = make(rows, C, F, seed=20)
+    xd, pd, rd = dev(x), dev(p), dev(r)
+    out, place = torch.full_like(xd, float("nan")), rd.clone()
+    with gated(C, F, kind) as h:
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        assert sw.swin_block_gated_last_launches(h) == 1
+        sw.swin_block_gated_forward(h, xd, pd, place, residual=place)
+        sw.swin_block_gated_sync_status(h)
+    ref, tol = forward_ref(xd, pd, rd, kind)
+    close(out, ref.cpu(), tol.cpu())
+    assert torch.equal(place, out)

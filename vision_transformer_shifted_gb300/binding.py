@@ -21,6 +21,7 @@ NOALLOC_MAX_INTERMEDIATE_BYTES = (64 << 20) - 256
 OPT_PATH, OPT_WAIT_LIMIT_US, OPT_HOST_CHUNKS, OPT_OVERLAP_CALLS = 1, 2, 3, 4
 BLOCK_OPT_OVERLAP_CALLS = 1
 BLOCK_GATED_SILU, BLOCK_GATED_GELU = 0, 1
+BLOCK_GATED_PLAN_DOWN, BLOCK_GATED_PLAN_DX, BLOCK_GATED_PLAN_WEIGHTS, BLOCK_GATED_PLAN_NARROW = 0, 1, 2, 3
 PATH_AUTO, PATH_THREE_KERNELS, PATH_FUSED, PATH_FP32 = 0, 1, 2, 3
 
 _lib = None
@@ -82,6 +83,7 @@ _SIGNATURES = {
     "swin_block_gated_destroy": ["p"],
     "swin_block_gated_test_stall": ["p", "p", "i", "p", "l", "p"],
     "swin_block_gated_test_corrupt_workspace": ["p", "i"],
+    "swin_block_gated_test_plan": ["i", "i", "i", "i", "p"],
     "swin_block_gated_test_last_use": ["i", "i", "i", "p", "p"],
 }
 
@@ -530,3 +532,9 @@ def swin_block_gated_test_last_use(stages, issued, k):
     _check("swin_block_gated_test_last_use", load().swin_block_gated_test_last_use(
         stages, issued, k, ctypes.addressof(stage), ctypes.addressof(parity)))
     return stage.value, parity.value
+
+
+def swin_block_gated_test_plan(C, F, rows, which):
+    plan = (ctypes.c_int * 6)()
+    _check("swin_block_gated_test_plan", load().swin_block_gated_test_plan(C, F, rows, which, ctypes.addressof(plan)))
+    return tuple(plan)

@@ -80,6 +80,33 @@ struct Product {
     int cols;
 };
 
+// The shapes of a call's products: the forward's last one, dx, and dWg, dWu, dWd.
+Product down_product(int C, int F, int rows)
+{
+    Product p{};
+    p.k[0] = F;
+    p.lda = hidden_ld(F);
+    p.rows = rows;
+    p.cols = C;
+    return p;
+}
+Product dx_product(int C, int F, int rows)
+{
+    Product p = down_product(C, F, rows);
+    p.k[1] = F;
+    return p;
+}
+void weight_products(int C, int F, int rows, Product (&p)[3])
+{
+    for (int i = 0; i < 3; ++i) {
+        p[i] = Product{};
+        p[i].k[0] = rows;
+        p[i].rows = i < 2 ? F : C;
+        p[i].cols = i < 2 ? C : F;
+        (i < 2 ? p[i].lda : p[i].ldb) = hidden_ld(F);
+    }
+}
+
 // What joining the tiles of a cut round costs, in K blocks of a whole tile: the
 // launch, the partial tiles' traffic and their second epilogue, some 10 us.
 // (Products of 1537 x 4104 x 1536, 42 tiles: the forward took 60 us with their 65
@@ -463,15 +490,11 @@ int forward(swin_block_gated_s *h, int rows, const void *Wd, const void *bd, con
 {
     int rc = check_device(h);
     if (rc != SWIN_WATTN_OK) return rc;
-    Product down{};
-    down.k[0] = h->F;
-    down.lda = hidden_ld(h->F);
+    Product down = down_product(h->C, h->F, rows);
     down.b[0] = Wd;
     down.d = (bf16 *)out;
     down.bias = (const bf16 *)bd;
     down.residual = (const bf16 *)residual;
-    down.rows = rows;
-    down.cols = h->C;
     const bool few = rows <= FEW_ROWS;
     const ProductsPlan pl = few ? ProductsPlan{} : plan_products(&down, 1);
     Carve size(nullptr);
@@ -635,20 +658,11 @@ int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, con
         return SWIN_WATTN_OK;
     }
 
-    Product dxp{}, dw[3]{};
-    dxp.k[0] = dxp.k[1] = h->F;
-    dxp.lda = hidden_ld(h->F);
+    Product dxp = dx_product(h->C, h->F, rows), dw[3];
+    weight_products(h->C, h->F, rows, dw);
     dxp.b[0] = p->Wg;
     dxp.b[1] = p->Wu;
     dxp.d = (bf16 *)dx;
-    dxp.rows = rows;
-    dxp.cols = h->C;
-    for (int i = 0; i < 3; ++i) {
-        dw[i].k[0] = rows;
-        dw[i].rows = i < 2 ? h->F : h->C;
-        dw[i].cols = i < 2 ? h->C : h->F;
-    }
-    dw[0].lda = dw[1].lda = dw[2].ldb = hidden_ld(h->F);
     dw[0].b[0] = dw[1].b[0] = x;
     dw[2].a[0] = dy;
     dw[0].d = (bf16 *)g->dWg;
@@ -771,6 +785,29 @@ int swin_block_gated_test_last_use(int stages, int issued, int k, int *stage, in
     const RingUse u = last_use(stages, issued, k);
     *stage = u.stage;
     *parity = (int)u.parity;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_gated_test_plan(int C, int F, int rows, int which, int *plan)
+{
+    if (C <= 0 || C % 8 || C > MAX_WIDTH || F <= 0 || F % 8 || F > MAX_WIDTH || rows <= FEW_ROWS || rows > MAX_ROWS || !plan)
+        return SWIN_WATTN_EINVAL;
+    if (which == SWIN_BLOCK_GATED_PLAN_NARROW) {
+        if (!gated_fused_supported(C)) return SWIN_WATTN_EINVAL;
+        const FusedPlan f = plan_gated_fused(C, F, rows);
+        const int v[] = {f.tiles, f.np, f.chunks, f.slots, f.resident, f.shared_staging};
+        memcpy(plan, v, sizeof(v));
+        return SWIN_WATTN_OK;
+    }
+    Product p[3];
+    int n = 1;
+    if (which == SWIN_BLOCK_GATED_PLAN_DOWN) p[0] = down_product(C, F, rows);
+    else if (which == SWIN_BLOCK_GATED_PLAN_DX) p[0] = dx_product(C, F, rows);
+    else if (which == SWIN_BLOCK_GATED_PLAN_WEIGHTS) weight_products(C, F, rows, p), n = 3;
+    else return SWIN_WATTN_EINVAL;
+    const ProductsPlan pl = plan_products(p, n);
+    const int v[] = {pl.split.tiles, pl.split.np, pl.wn, pl.split.halves, pl.split.cut, pl.split.kb != pl.split.k_blocks};
+    memcpy(plan, v, sizeof(v));
     return SWIN_WATTN_OK;
 }
 

@@ -820,6 +820,14 @@ cudaError_t launch_few_down(const bf16 *h, int ldh, int rows, const bf16 *wd, co
 
 // The whole forward as one kernel, without a workspace.
 bool gated_fused_supported(int C);
+struct FusedPlan {
+    int tiles, np;           // of 256 rows, pairs that walk them
+    int chunks, slots;       // of hidden units, weight chunks in the ring
+    bool resident;           // every chunk has its slot: loaded once
+    bool shared_staging;     // the two groups drain through one staging, in turn
+    size_t smem;
+};
+FusedPlan plan_gated_fused(int C, int F, int rows);
 cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu, const bf16 *wg, const bf16 *bg,
                                const bf16 *wu, const bf16 *bu, const bf16 *wd, const bf16 *bd, const bf16 *residual,
                                bf16 *out, DeviceStatus st, cudaStream_t stream);

@@ -404,9 +404,36 @@ gated_fused_kernel(const __grid_constant__ FusedArgs a)
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// N of the last product: C rounded up to a pair's step.
+int last_n(int C) { return (C + 31) / 32 * 32; }
+// Bytes of a CTA's part of a chunk's weights.
+int slot_bytes(int C) { return (C + 63) / 64 * 8192 + last_n(C) * 64; }
+
 } // namespace
 
 bool gated_fused_supported(int C) { return C <= 128; }
+
+FusedPlan plan_gated_fused(int C, int F, int rows)
+{
+    FusedPlan p{};
+    p.tiles = (int)(((int64_t)rows + 255) / 256);
+    p.np = p.tiles < sm_count() / 2 ? p.tiles : sm_count() / 2;
+    p.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
+    // A staging a group where it leaves room for every chunk's weights (400000 x 64
+    // x 128: 55 us, 63 shared), else one for both (200704 x 96 x 256: 51 us; 54
+    // with halves of it, where the second box waits for the first one's store).
+    constexpr int STAGING = FUSED_GROUP_WARPS * 4096;
+    const int most = 222 * 1024 - 1024;   // (5 KB for the barriers and biases, 1 KB of alignment)
+    int fixed = 2 * ((C + 63) / 64) * 16384 + 2 * 16384 + FUSED_GROUPS * STAGING;
+    p.shared_staging = p.chunks > FUSED_SLOTS || fixed + p.chunks * slot_bytes(C) > most;
+    if (p.shared_staging) fixed -= STAGING;
+    p.slots = (most - fixed) / slot_bytes(C);
+    if (p.slots > FUSED_SLOTS) p.slots = FUSED_SLOTS;
+    if (p.slots > p.chunks) p.slots = p.chunks;
+    p.resident = p.slots == p.chunks;   // (three slots at least otherwise: g | u run two chunks ahead)
+    p.smem = 1024 + (size_t)fixed + (size_t)p.slots * slot_bytes(C);
+    return p;
+}
 
 cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu, const bf16 *wg, const bf16 *bg,
                                const bf16 *wu, const bf16 *bu, const bf16 *wd, const bf16 *bd, const bf16 *residual,
@@ -415,24 +442,16 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     FusedArgs a;
     memset(&a, 0, sizeof(a));
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    a.n2 = (C + 31) / 32 * 32;
+    const FusedPlan pl = plan_gated_fused(C, F, rows);
+    a.n2 = last_n(C);
     a.xb = (C + 63) / 64;
-    a.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
-    a.slot_bytes = a.xb * 8192 + a.n2 * 64;
-    // A staging a group where it leaves room for every chunk's weights (400000 x 64
-    // x 128: 55 us, 63 shared), else one for both (200704 x 96 x 256: 51 us; 54
-    // with halves of it, where the second box waits for the first one's store).
-    constexpr int STAGING = FUSED_GROUP_WARPS * 4096;
-    const int most = 222 * 1024 - 1024;   // (5 KB for the barriers and biases, 1 KB of alignment)
-    int fixed = 2 * a.xb * 16384 + 2 * 16384 + FUSED_GROUPS * STAGING;
-    a.shared_staging = a.chunks > FUSED_SLOTS || fixed + a.chunks * a.slot_bytes > most;
-    if (a.shared_staging) fixed -= STAGING;
-    const int room = most - fixed;
-    a.slots = room / a.slot_bytes;
-    if (a.slots > FUSED_SLOTS) a.slots = FUSED_SLOTS;
-    if (a.slots > a.chunks) a.slots = a.chunks;
-    a.resident = a.slots == a.chunks;   // (three slots at least otherwise: g | u run two chunks ahead)
-    const size_t smem = 1024 + (size_t)fixed + (size_t)a.slots * a.slot_bytes;
+    a.chunks = pl.chunks;
+    a.slot_bytes = slot_bytes(C);
+    a.slots = pl.slots;
+    a.resident = pl.resident;
+    a.shared_staging = pl.shared_staging;
+    a.tiles = pl.tiles;
+    a.np = pl.np;
     cudaError_t e;
     if ((e = make_tensor_map(&a.x, type, x, C, rows, (int64_t)C * 2, 64, 128, 128)) != cudaSuccess) return e;
     if ((e = make_tensor_map(&a.wg, type, wg, C, F, (int64_t)C * 2, 64, 64, 128)) != cudaSuccess) return e;
@@ -446,8 +465,6 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
     a.rows = rows;
     a.C = C;
     a.F = F;
-    a.tiles = (int)(((int64_t)rows + 255) / 256);
-    a.np = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
     a.st = st;
     auto *kern = gelu ? gated_fused_kernel<ACT_GELU> : gated_fused_kernel<ACT_SILU>;
     static std::atomic<uint64_t> ready[2];
@@ -458,7 +475,7 @@ cudaError_t launch_gated_fused(const bf16 *x, int rows, int C, int F, bool gelu,
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024)) != cudaSuccess) return e;
         ready[gelu].fetch_or(bit);
     }
-    return launch_maybe_overlapped(kern, dim3(2u * (unsigned)a.np), dim3(FUSED_THREADS), smem, stream, 1, a);
+    return launch_maybe_overlapped(kern, dim3(2u * (unsigned)a.np), dim3(FUSED_THREADS), pl.smem, stream, 1, a);
 }
 
 } // namespace swin
