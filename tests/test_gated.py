@@ -751,3 +751,81 @@ def test_narrow_tiles_with_biases_and_residual(rows, C, F, kind):
     ref, tol = forward_ref(xd, pd, rd, kind)
     close(out, ref.cpu(), tol.cpu())
     assert torch.equal(place, out)
+
+
+@pytest.mark.gpu
+def test_sums_over_more_than_32_bits_of_hidden_elements():
+    """The workspace of the offsets test (33000 x 65536 a matrix) with biases: rows at
+    the beginning, where the 2^31st element lies and at the end of out and dx,
+    and every gradient of hidden units at both ends and between, whose sums go
+    over all rows."""
+    rows, C, F = 33000, 136, 65536
+    g = torch.Generator(device=DEV).manual_seed(6)
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=DEV) * std).to(BF)  # noqa: E731
+    p = dict(Wg=n(F, C, std=C ** -0.5), Wu=n(F, C, std=C ** -0.5), Wd=n(C, F, std=F ** -0.5), bg=n(F, std=0.3),
+             bu=n(F, std=0.3), bd=n(C, std=0.3))
+    x, dy = n(rows, C), n(rows, C)
+    out, dx, grads = torch.empty_like(x), torch.empty_like(x), new_grads(p)
+    with gated(C, F) as h:
+        sw.swin_block_gated_forward(h, x, p, out)
+        sw.swin_block_gated_backward(h, x, p, dy, dx, grads)
+        sw.swin_block_gated_sync_status(h)
+    some = [0, 1, 255, 256, 20000, 32766, 32767, 32768, 32769, 32999]
+    ref, tol = forward_ref(x[some], p, None, "silu")
+    close(out[some], ref.cpu(), tol.cpu())
+    ref, tol = backward_ref(x[some], p, dy[some], "silu")
+    close(dx[some], ref["dx"].cpu(), tol["dx"].cpu())
+    units = list(range(8)) + list(range(127, 129)) + list(range(32760, 32776)) + list(range(50000, 50007))
+    units += list(range(F - 64, F))
+    part = dict(Wg=p["Wg"][units], Wu=p["Wu"][units], Wd=p["Wd"][:, units], bg=p["bg"][units], bu=p["bu"][units],
+                bd=p["bd"])
+    ref, tol = backward_ref(x, part, dy, "silu")
+    got = dict(dWg=grads["dWg"][units], dWu=grads["dWu"][units], dWd=grads["dWd"][:, units], dbg=grads["dbg"][units],
+               dbu=grads["dbu"][units], dbd=grads["dbd"])
+    for k, v in got.items():
+        close(v, ref[k].cpu(), tol[k].cpu())
+
+
+@pytest.mark.gpu
+def test_two_host_threads_compute_what_one_does():
+    """A handle a thread, on streams of their own, at once: every result is the one
+    that the same call gives alone."""
+    import threading
+    cases = [(1, 256, 640), (700, 256, 640), (300, 96, 256), (1000, 512, 1368)]
+    wrong = []
+
+    def call(h, x, p, dy):
+        out, dx, g = torch.empty_like(x), torch.empty_like(x), new_grads(p)
+        sw.swin_block_gated_forward(h, x, p, out)
+        sw.swin_block_gated_backward(h, x, p, dy, dx, g)
+        return [out, dx] + [g[k] for k in sorted(g)]
+
+    data = []
+    for rows, C, F in cases:
+        x, p, _, dy = make(rows, C, F, seed=21)
+        x, p, dy = dev(x), dev(p), dev(dy)
+        with gated(C, F) as h:
+            want = call(h, x, p, dy)
+            sw.swin_block_gated_sync_status(h)
+        data.append((C, F, x, p, dy, want))
+    torch.cuda.synchronize()
+
+    def work(C, F, x, p, dy, want):
+        try:
+            stream = torch.cuda.Stream()
+            with gated(C, F) as h, torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = call(h, x, p, dy)
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        wrong.append((C, F))
+                sw.swin_block_gated_sync_status(h)
+        except Exception as e:
+            wrong.append((C, F, e))
+
+    threads = [threading.Thread(target=work, args=a) for a in data]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong

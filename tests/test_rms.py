@@ -492,3 +492,67 @@ def test_codes_of_very_small_and_large_rows(factor):
     assert (scales.cpu() == scale).all()
     want = (x.float() * gamma.float() / scale).to(E4M3).float()
     assert torch.equal(codes.cpu().float().nan_to_num(nan=7e7), want.nan_to_num(nan=7e7))
+
+
+@pytest.mark.gpu
+def test_backward_and_codes_past_32_bits_of_elements():
+    """rows * C > 2^31: rows at the beginning, around the 2^31st element and at the
+    end; dgamma over all of them.  Its sums in fp32: some 863 rows a block one
+    after the other and 152 partial rows, each addition off by 2^-24 at most."""
+    C, rows = 16384, (1 << 17) + 5
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    n = lambda *s: torch.randn(*s, generator=gen, device=DEV, dtype=BF)  # noqa: E731
+    s, dy, g = n(rows, C), n(rows, C), 1 + 0.2 * n(C)
+    dx, dgamma = torch.full_like(s, float("nan")), torch.full((C,), float("nan"), device=DEV)
+    codes, scales = torch.empty(rows, C, dtype=E4M3, device=DEV), torch.full((rows,), float("nan"), device=DEV)
+    with rms(C) as h:
+        sw.swin_block_rms_backward(h, s, g, dy, dx, dgamma)
+        sw.swin_block_rms_forward_q8(h, s, g, codes, scales)
+    some = [0, 1, 65535, 131070, 131071, 131072, 131073, rows - 1]
+    ref, _, size, _ = gradients(s[some].cpu(), g.cpu(), dy[some].cpu(), None)
+    close(dx[some], ref, 2.0 ** -8 * ref.abs() + FP * size)
+    _, y = reference(s[some].cpu(), None, g.cpu())
+    scale = y.abs().amax(-1) / 448
+    close(scales[some], scale, FP * scale)
+    got = codes[some].float().double().cpu() * scales[some].double().cpu()[:, None]
+    close(got, y, (2.0 ** -4 + FP) * y.abs() + 2.0 ** -10 * scale[:, None])
+    ref, size = torch.zeros(C, dtype=torch.float64), torch.zeros(C, dtype=torch.float64)
+    for i in range(0, rows, 8192):
+        _, d, _, m = gradients(s[i:i + 8192], g, dy[i:i + 8192], None)
+        ref += d.cpu()
+        size += m.cpu()
+    close(dgamma, ref, ((863 + 152) * 2.0 ** -24 + FP) * size)
+
+
+@pytest.mark.gpu
+def test_two_host_threads_compute_what_one_does():
+    """A handle a thread at once: every result is the one that the call gives alone."""
+    import threading
+    wrong, data = [], []
+    for C, rows in ((1000, 8), (16384, 8), (10000, 3), (96, 3001), (2744, 1500)):
+        s, _, g, dy = dev(*inputs(rows, C, False, seed=C))
+        dx, dg = torch.empty_like(s), torch.empty(C, device=DEV)
+        with rms(C) as h:
+            sw.swin_block_rms_backward(h, s, g, dy, dx, dg)
+        data.append((C, s, g, dy, dx, dg))
+    torch.cuda.synchronize()
+
+    def work(C, s, g, dy, dx, dg):
+        try:
+            stream = torch.cuda.Stream()
+            with rms(C) as h, torch.cuda.stream(stream):
+                for _ in range(100):
+                    one, two = torch.empty_like(dx), torch.empty_like(dg)
+                    sw.swin_block_rms_backward(h, s, g, dy, one, two)
+                    stream.synchronize()
+                    if not (torch.equal(one, dx) and torch.equal(two, dg)):
+                        wrong.append(C)
+        except Exception as e:
+            wrong.append((C, e))
+
+    threads = [threading.Thread(target=work, args=a) for a in data]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
