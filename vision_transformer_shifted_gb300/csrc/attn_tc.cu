@@ -375,16 +375,15 @@ cudaError_t make_tensor_map_sw64_3d(CUtensorMap *map, const void *ptr, int64_t r
 }
 
 cudaError_t make_tensor_map(CUtensorMap *map, CUtensorMapDataType type, const void *ptr, int64_t inner, int64_t outer,
-                            int64_t ld, int box_inner, int box_outer, int swizzle_bytes, int64_t depth)
+                            int64_t ld, int box_inner, int box_outer, int swizzle_bytes)
 {
     const EncodeTiledFn encode = encode_fn();
     if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)depth};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld * (cuuint64_t)outer};
-    const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer, 1};
-    const cuuint32_t elem[3] = {1, 1, 1};
-    CUresult r = encode(map, type, depth > 0 ? 3 : 2, const_cast<void *>(ptr), dims, strides, box, elem,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
+    const cuuint32_t elem[2] = {1, 1};
+    CUresult r = encode(map, type, 2, const_cast<void *>(ptr), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;

@@ -273,12 +273,11 @@ cudaError_t make_tensor_map_sw128(CUtensorMap *map, const void *ptr, int64_t row
 cudaError_t make_tensor_map_sw64_3d(CUtensorMap *map, const void *ptr, int64_t rows, int width, int cols, int box_w,
                                     int box_h);
 
-// Tensor map over row-major elements (16-byte aligned base, row stride ld bytes,
-// a multiple of 16): [outer, inner] or, with depth > 0, [depth, outer, inner]
-// densely stacked; boxes of box_outer rows x box_inner elements, 128- or
-// 64-byte swizzle (box_inner bytes), zero fill outside.
+// Tensor map over row-major elements [outer, inner] (16-byte aligned base, row
+// stride ld bytes, a multiple of 16): boxes of box_outer rows x box_inner elements,
+// 128- or 64-byte swizzle (box_inner bytes), zero fill outside.
 cudaError_t make_tensor_map(CUtensorMap *map, CUtensorMapDataType type, const void *ptr, int64_t inner, int64_t outer,
-                            int64_t ld, int box_inner, int box_outer, int swizzle_bytes, int64_t depth = 0);
+                            int64_t ld, int box_inner, int box_outer, int swizzle_bytes);
 
 cudaError_t launch_cpb_table(const float *W1, const float *b1, const float *W2, int hidden, int M,
                              int heads, bool out_bf16, void *table, cudaStream_t stream);
