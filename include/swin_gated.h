@@ -13,7 +13,7 @@
  * and the product are one kernel, the last projection with its bias and the
  * residual a second, sometimes with a third that joins tiles cut along F (the
  * bf16 form for C <= 128 and more than 128 rows is one kernel, and h stays on
- * chip; up to 128 rows take kernels of their own).  The
+ * chip, but for few rows with a long F; up to 128 rows take kernels of their own).  The
  * kernels may start while the kernel queued before them finishes (programmatic
  * dependent launch) but touch no memory before it has: a call needs no
  * guarantee about its parameters.  Conventions of swin_wattn.h: device pointers,

@@ -96,7 +96,7 @@ int swin_block_gated_test_last_use(int stages, int issued, int k, int *stage, in
  * device or, without one, for 152 SMs; six ints.  A product (the forward's last
  * one, dx, the three weight gradients together): {tiles of 256 rows, CTA pairs,
  * columns of a tile, half tiles of the last round, its tiles cut along K, 1 if
- * into equal slices}.  The one-kernel forward (C <= 128): {tiles, pairs, chunks
+ * into equal slices}.  The one-kernel forward, where it is taken: {tiles, pairs, chunks
  * of 64 hidden units, weight chunks held, 1 if that is all, 1 if the two groups
  * of warps share a staging}.  EINVAL for other sizes. */
 enum {

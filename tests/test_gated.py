@@ -829,3 +829,38 @@ def test_two_host_threads_compute_what_one_does():
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+TWO_KERNEL_NARROW = [(129, 128, 4096), (263, 40, 992), (700, 24, 20000), (1180, 8, 6152), (3000, 8, 4096),
+                     (20000, 128, 4096)]
+
+
+def test_few_narrow_tiles_of_a_long_hidden_width_are_spread_over_the_pairs():
+    """The one kernel walks all of F in the pair of a row tile: with few tiles (or a
+    last round of few) two kernels are up to nine times faster."""
+    for rows, C, F in TWO_KERNEL_NARROW:
+        with pytest.raises(sw.SwinWAttnError):
+            sw.swin_block_gated_test_plan(C, F, rows, sw.BLOCK_GATED_PLAN_NARROW)
+    for rows, C, F in ((129, 128, 512), (1000, 128, 576), (30000, 64, 4096), (75936, 104, 3896), (200704, 128, 2048)):
+        sw.swin_block_gated_test_plan(C, F, rows, sw.BLOCK_GATED_PLAN_NARROW)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,F", TWO_KERNEL_NARROW)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_narrow_tokens_by_two_kernels(rows, C, F, kind):
+    """With biases and residual, without either, and in place."""
+    x, p, r, _ = make(rows, C, F, seed=22)
+    xd, pd, rd = dev(x), dev(p), dev(r)
+    bare = {k: None if k.startswith("b") else v for k, v in pd.items()}
+    out, plain, place = torch.full_like(xd, float("nan")), torch.full_like(xd, float("nan")), rd.clone()
+    with gated(C, F, kind) as h:
+        sw.swin_block_gated_forward(h, xd, pd, out, residual=rd)
+        assert sw.swin_block_gated_last_launches(h) in (2, 3)
+        sw.swin_block_gated_forward(h, xd, bare, plain)
+        sw.swin_block_gated_forward(h, xd, pd, place, residual=place)
+        sw.swin_block_gated_sync_status(h)
+    for got, w, res in ((out, pd, rd), (plain, bare, None)):
+        ref, tol = forward_ref(xd, w, res, kind)
+        close(got, ref.cpu(), tol.cpu())
+    assert torch.equal(place, out)

@@ -590,7 +590,7 @@ int swin_block_gated_forward(swin_block_gated_t h, const void *x, int rows, cons
     if (any_overlap({out, n}, {{x, n}, {p->Wg, w}, {p->Wu, w}, {p->Wd, w}, {p->bg, f}, {p->bu, f}, {p->bd, c},
                                {residual == out ? nullptr : residual, n}}))
         return SWIN_WATTN_EINVAL;
-    if (rows > FEW_ROWS && gated_fused_supported(h->C)) {
+    if (rows > FEW_ROWS && gated_fused_chosen(h->C, h->F, rows)) {
         const int rc = check_device(h);
         if (rc != SWIN_WATTN_OK) return rc;
         h->last_launches = 1;
@@ -793,7 +793,7 @@ int swin_block_gated_test_plan(int C, int F, int rows, int which, int *plan)
     if (C <= 0 || C % 8 || C > MAX_WIDTH || F <= 0 || F % 8 || F > MAX_WIDTH || rows <= FEW_ROWS || rows > MAX_ROWS || !plan)
         return SWIN_WATTN_EINVAL;
     if (which == SWIN_BLOCK_GATED_PLAN_NARROW) {
-        if (!gated_fused_supported(C)) return SWIN_WATTN_EINVAL;
+        if (!gated_fused_chosen(C, F, rows)) return SWIN_WATTN_EINVAL;
         const FusedPlan f = plan_gated_fused(C, F, rows);
         const int v[] = {f.tiles, f.np, f.chunks, f.slots, f.resident, f.shared_staging};
         memcpy(plan, v, sizeof(v));

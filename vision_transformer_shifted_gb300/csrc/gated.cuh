@@ -819,7 +819,7 @@ cudaError_t launch_few_down(const bf16 *h, int ldh, int rows, const bf16 *wd, co
 // ---- narrow tokens (gated_fused.cu) ---------------------------------------------------
 
 // The whole forward as one kernel, without a workspace.
-bool gated_fused_supported(int C);
+bool gated_fused_chosen(int C, int F, int rows);   // rather than two kernels
 struct FusedPlan {
     int tiles, np;           // of 256 rows, pairs that walk them
     int chunks, slots;       // of hidden units, weight chunks in the ring

@@ -411,7 +411,22 @@ int slot_bytes(int C) { return (C + 63) / 64 * 8192 + last_n(C) * 64; }
 
 } // namespace
 
-bool gated_fused_supported(int C) { return C <= 128; }
+// Tokens narrow enough for the accumulators to fit TMEM, and not so few tiles of
+// such a long F that the pairs that have none would be missed.  Both forms' times,
+// in hundredths of a us beyond what they share, from 60 sizes (129 to 200704 rows,
+// F from 88 to 16384; the choice costs 0.5% against the better of each): a chunk
+// 0.85 and a tile 0.6 a round; two kernels 8 more and 2.3 for a pair's tile of 256
+// rows x 128 hidden units.  (129 x 128 x 4096: 52 us as one kernel, 15.9 as two;
+// 20000 x 128 x 4096, two rounds of which the second has three tiles: 107, 90;
+// 100000 x 128 x 4096: 357, 421; 200704 x 96 x 256: 49.9, 70.5.)
+bool gated_fused_chosen(int C, int F, int rows)
+{
+    if (C > 128) return false;
+    const FusedPlan p = plan_gated_fused(C, F, rows);
+    const int64_t pairs = sm_count() / 2, rounds = (p.tiles + pairs - 1) / pairs;
+    const int64_t units = (int64_t)p.tiles * ((F + 127) / 128);
+    return rounds * (85 * p.chunks + 60) <= 800 + 230 * units / pairs;
+}
 
 FusedPlan plan_gated_fused(int C, int F, int rows)
 {
