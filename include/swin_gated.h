@@ -13,12 +13,12 @@
  * and the product are one kernel, the last projection with its bias and the
  * residual a second, sometimes with a third that joins tiles cut along F (the
  * bf16 form for C <= 128 and more than 128 rows is one kernel, and h stays on
- * chip, but for few rows with a long F; up to 128 rows take kernels of their own).  The
- * kernels may start while the kernel queued before them finishes (programmatic
- * dependent launch) but touch no memory before it has: a call needs no
- * guarantee about its parameters.  Conventions of swin_wattn.h: device pointers,
- * asynchronous on `stream`, caller-owned tensors, status codes SWIN_WATTN_*,
- * no CPU fallback.
+ * chip, but for few rows with a long F; up to 128 rows take kernels of their
+ * own).  The kernels may start while the kernel queued before them finishes
+ * (programmatic dependent launch) but touch no memory before it has: a call
+ * needs no guarantee about its parameters.  Conventions of swin_wattn.h: device
+ * pointers, asynchronous on `stream`, caller-owned tensors, status codes
+ * SWIN_WATTN_*, no CPU fallback.
  */
 #ifndef SWIN_GATED_H
 #define SWIN_GATED_H
@@ -63,27 +63,29 @@ typedef struct swin_block_gated_grads {
  * error word cannot be allocated.  The handle belongs to the device that is
  * current when it is created; calls with another current device return EINVAL
  * (without a device it can be created, and every call that would launch
- * returns ECUDA); creating it allocates, so not while a stream is captured.  One handle may be used on several streams (its calls are
- * ordered by an event: they share its workspace) but not from two host threads
- * at once.  A call captured into a CUDA graph takes its workspace from the
- * graph's own memory, so graphs share nothing with each other or with eager
- * calls but the error word: a graph is replayed only while its handle lives. */
+ * returns ECUDA); creating it allocates, so not while a stream is captured.  One
+ * handle may be used on several streams (its calls are ordered by an event: they
+ * share its workspace, which grows to the largest call's and then synchronises
+ * the device) but not from two host threads at once.  A call captured into a CUDA
+ * graph takes its workspace from the graph's own memory, so graphs share nothing
+ * with each other or with eager calls but the error word: a graph is replayed
+ * only while its handle lives. */
 int swin_block_gated_create(swin_block_gated_t *out, int C, int F, int act);
 
 /* out = residual + (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd.
  * x, out [rows, C], residual [rows, C] or NULL.  out may be residual itself
  * (in place), not a partial overlap, and overlaps no other tensor.  Every
  * pointer 16-byte aligned.  EINVAL for NULL, misaligned or overlapping
- * pointers or rows < 0 (or above 2^31 - 513); ENOMEM if the workspace (rows * F bf16, for few tiles
- * also fp32 partial sums) cannot be allocated; ECUDA for a launch failure.
- * rows = 0 is a no-op. */
+ * pointers or rows < 0 (or above 2^31 - 513); ENOMEM if the workspace (rows * F bf16 with F rounded
+ * up to a multiple of 64, for few tiles also fp32 partial sums) cannot be
+ * allocated; ECUDA for a launch failure.  rows = 0 is a no-op. */
 int swin_block_gated_forward(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
                              const void *residual, void *out, swin_stream_t stream);
 
 /* The same from 8-bit inputs: x8 [rows, C] e4m3 with a scale a row, sx [rows]
  * fp32 (as swin_block_rms_forward_q8 writes them); g = (x8 . Wg8) sx sg + bg,
- * likewise u; h and the last projection in bf16 (a row's scale of h is known
- * only once all of it is).  C must be a multiple of 16 (EUNSUPPORTED
+ * likewise u; h in bf16 (a row's scale is known only once all of it is) and so Wd
+ * too (one matrix instruction takes operands of 16 or of 8 bits).  C must be a multiple of 16 (EUNSUPPORTED
  * otherwise). */
 int swin_block_gated_forward_q8(swin_block_gated_t h, const void *x8, const float *sx, int rows,
                                 const swin_block_gated_params_q8 *p, const void *residual, void *out,
@@ -96,8 +98,8 @@ int swin_block_gated_forward_q8(swin_block_gated_t h, const void *x8, const floa
  * x, dy, dx [rows, C] bf16; g, u and h are recomputed from x (nothing of the
  * forward is kept); dg, du and h are rounded to bf16 before the products that
  * read them; every sum over rows is taken in a fixed order.  No output
- * overlaps an input or another output.  Errors as above; the workspace is
- * 3 * rows * F bf16 plus fp32 partial sums.  rows = 0 zeroes the parameter
+ * overlaps an input or another output.  Errors as above; the workspace is 3 *
+ * rows * F bf16, F rounded up as above, plus fp32 partial sums.  rows = 0 zeroes the parameter
  * gradients. */
 int swin_block_gated_backward(swin_block_gated_t h, const void *x, int rows, const swin_block_gated_params *p,
                               const void *dy, void *dx, const swin_block_gated_grads *grads, swin_stream_t stream);

@@ -109,13 +109,15 @@ void weight_products(int C, int F, int rows, Product (&p)[3])
 
 // What joining the tiles of a cut round costs, in K blocks of a whole tile: the
 // launch, the partial tiles' traffic and their second epilogue, some 10 us.
-// (Products of 1537 x 4104 x 1536, 42 tiles: the forward took 60 us with their 65
-// blocks cut to 36, 55 whole; 3000 x 4096 x 1024: 67 cut, 59 in halves.)
+// (Forward 1537 x 1536 x 4104, 42 tiles: 57.5 us with their 65 blocks cut to 36,
+// 53.3 whole; 3000 x 1024 x 4096: 63.7 cut, 55.5 whole; 12544 x 512 x 1368
+// backward: 147 whole, 131 with the cuts that this cost allows, 135 with every cut
+// that saves a block.)
 constexpr int WIDE_JOIN = 32, NARROW_JOIN = 36;
 // A K block of a 256 x 192 tile in hundredths of a whole one's: tiles of that width
 // where they come out cheaper, as a round that leaves a third of the pairs idle
-// with 256 columns (1300 x 2048 x 5632 forward: 48 tiles 71 us, 66 of them 68;
-// 3000 x 1024 x 2736 backward 106 and 102.5).
+// with 256 columns (1300 x 2048 x 5632 forward: 48 tiles 70.5 us, 66 of them 69.5;
+// e4m3 1537 x 1536 x 4104 41.1 and 39.1; 3000 x 1024 x 2736 backward 105 and 103.8).
 constexpr int COST_192 = 82;
 // A K block of half a tile (256 x 128) in hundredths of a whole one's, with
 // `halves` pairs at it: half of the MMAs and a little, or (many pairs) its share
@@ -260,9 +262,9 @@ struct ProductsPlan {
 // 128.  The last round is cut along K where that saves more K blocks than the
 // join costs; few blocks in all go to as many pairs as leave each at least four.
 // A last round of at most half of the pairs goes out as half tiles where that
-// costs less than either: no join (1024 x 2048 x 5632 forward 61.7 us cut, 57.5
-// in halves; 12544 x 512 x 1368 backward, dx's last 22 tiles, 140.6 and 135; its
-// weight gradients' 36 tiles of 196 blocks stay cut: in halves 11 us more).
+// costs less than either: no join (1024 x 2048 x 5632 forward 61 us cut or whole,
+// 57 in halves; 12544 x 512 x 1368 backward, dx's last 22 tiles, 131 cut, 129; its
+// weight gradients' 36 tiles of 196 blocks stay cut: in halves 9 us more).
 ProductsPlan plan_products(const Product *p, int n)
 {
     ProductsPlan pl{};
@@ -301,8 +303,9 @@ ProductsPlan plan_products(const Product *p, int n)
         // Equal slices of every tile, where they cost at most a tenth more blocks:
         // pairs that share rows of an operand then walk K side by side, and each
         // reads what another has brought into L2.  (36 tiles, the weight gradients
-        // of 44821 x 336 x 1288: 112 us, 194 by even ranges.  A slice is longer than
-        // what rounding K up to equal slices adds, so that none is empty.)
+        // of 44821 x 336 x 1288: the backward takes 330 us, 400 by even ranges.  A
+        // slice is longer than what rounding K up to equal slices adds, so that none
+        // is empty.)
         const int slices = pairs / rest;
         if (!full && slices > 1 && s.kb >= 16 * slices && s.kb >= slices * slices &&
             (int64_t)ceil_div(s.kb, slices) * 10 <= (int64_t)ceil_div(blocks, np) * 11) {

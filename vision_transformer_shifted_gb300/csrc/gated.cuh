@@ -134,8 +134,8 @@ __device__ __forceinline__ void staging_free(int lane)
 // Wg as its half of B, CTA 1 the same rows of Wu: one 256 x 256 MMA then
 // leaves g in accumulator columns 0..127 and u in 128..255 of the same rows, so
 // that the thread that drains a row holds both and forms h without exchange.
-// The tensor cores bind it (8192 x 2048 x 8192: 270 us, 2.03 PFLOP/s, busy in 96%
-// of the cycles) until K is short (118162 x 192 x 672: 67 us, 57% of the issue
+// The tensor cores bind it (8192 x 2048 x 8192: 271 us alone, 2.03 PFLOP/s, busy in
+// 96% of the cycles) until K is short (118162 x 192 x 672: 67 us, 57% of the issue
 // slots with the activation).
 template <int ACT, bool Q8>
 struct UpPolicy {
@@ -281,14 +281,16 @@ struct UpPolicy {
 // D = A B^T over up to two K segments (dx = dg Wg + du Wu), A and B each K-major
 // or MN-major as stored: no operand is ever transposed in memory.  Up to three
 // problems run as one launch (the three weight gradients).  The tensor cores bind
-// it (8192 x 8192 x 2048 with the residual: 150 us, 1.8 PFLOP/s); with K of a few
+// it (8192 x 8192 x 2048 with the residual: 156 us, 1.76 PFLOP/s); with K of a few
 // hundred its operands' way from L2 does (12544 x 2736 x 512: 30 us at 10 TB/s).
 //
 // Tiles are dealt to the pairs in rounds; a last round that would leave pairs
 // idle is instead dealt out as half tiles, or cut along K: its tiles' K blocks, laid end to end, are split
 // evenly over the pairs, and a pair's ranges that hold only a part of a tile go
 // to fp32 partial tiles that a second kernel adds in the order of K.  (4096 x
-// 2048 x 5632's dx: 128 tiles on 76 pairs, 2 rounds of 176 blocks; cut, 1.68.)
+// 2048 x 5632's dx: 128 tiles on 76 pairs, 2 rounds of 176 blocks; cut, 1.68: at
+// the board's power limit no gain, the backward took 494 us cut and 481 whole;
+// 12544 x 512 x 1368, below it: 131 cut, 147 whole.)
 struct PairProblem {
     CUtensorMap a[2], b[2], d;
     CUtensorMap b_half[2];         // K-major B: boxes for a half tile
@@ -387,7 +389,7 @@ __device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int 
 // Place in the order of tiles of the t-th tile worked on.  Products of the hidden
 // activations' rows (not their weight gradients) go through the rows from the
 // last: the kernel before wrote those last, and L2 still has them (118162 x 192 x
-// 672 forward 113 -> 110.4 us, 200704 x 96 x 256 backward 213 -> 209).
+// 672 forward 104.3 us from the first, 101.8; 200704 x 96 x 256 backward 210.7, 207.6).
 __host__ __device__ inline int tile_place(int t, int mt, int nt, bool from_last) { return from_last ? mt * nt - 1 - t : t; }
 
 template <int TN, bool A_MN, bool B_MN>

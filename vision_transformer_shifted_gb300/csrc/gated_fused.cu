@@ -12,9 +12,10 @@
 // two more TMEM buffers.  The groups take alternate chunks, and group t mod 2
 // drains tile t's output after its first chunk of tile t + 1: neither waits for
 // the MMAs of its own last chunk.  Weights stream through a ring of chunks, or
-// stay (loaded once) where all chunks fit it.  Arithmetic per hidden value
-// binds (the activation: about 20 instructions with the drain), not HBM: 200704 x
-// 96 x 256 with biases and residual takes 49.8 us, 118 as two kernels.
+// stay (loaded once) where all chunks fit it.  The activation warps bind, not HBM:
+// four a scheduler, some 21 instructions a hidden value with the drain, waiting
+// on TMEM and on their own chains in 39% of the issue slots.  200704 x 96 x 256
+// with biases and residual takes 49.9 us, 70.5 as two kernels.
 #include <atomic>
 #include <cstring>
 
@@ -435,8 +436,9 @@ FusedPlan plan_gated_fused(int C, int F, int rows)
     p.np = p.tiles < sm_count() / 2 ? p.tiles : sm_count() / 2;
     p.chunks = (F + FUSED_CHUNK - 1) / FUSED_CHUNK;
     // A staging a group where it leaves room for every chunk's weights (400000 x 64
-    // x 128: 55 us, 63 shared), else one for both (200704 x 96 x 256: 51 us; 54
-    // with halves of it, where the second box waits for the first one's store).
+    // x 128 with biases and residual: 52 us, 62 shared), else one for both (200704
+    // x 96 x 256: 49.9 us; 52.4 with halves of it, where the second box waits for
+    // the first one's store).
     constexpr int STAGING = FUSED_GROUP_WARPS * 4096;
     const int most = 222 * 1024 - 1024;   // (5 KB for the barriers and biases, 1 KB of alignment)
     int fixed = 2 * ((C + 63) / 64) * 16384 + 2 * 16384 + FUSED_GROUPS * STAGING;
