@@ -1,5 +1,5 @@
 """ctypes binding of libswin_wattn (include/swin_wattn.h, swin_wattn_test.h,
-swin_block.h, swin_wattn_backward.h, swin_rms.h, swin_gated.h).
+swin_block.h, swin_wattn_backward.h, swin_rms.h, swin_gated.h, swin_layernorm.h).
 
 Argument marshalling only: every function here passes tensor pointers and
 sizes to the C ABI of the same name and raises on a non-OK status.  torch is
@@ -74,6 +74,13 @@ _SIGNATURES = {
     "swin_block_rms_backward": ["p", "p", "i", "p", "p", "p", "p", "p", "p"],
     "swin_block_rms_last_launches": ["p"],
     "swin_block_rms_destroy": ["p"],
+    "swin_block_layernorm_create": ["pp", "i", "f"],
+    "swin_block_layernorm_forward": ["p", "p", "p", "i", "p", "p", "p", "p", "p"],
+    "swin_block_layernorm_forward_post": ["p", "p", "p", "i", "p", "p", "p", "p"],
+    "swin_block_layernorm_forward_q8": ["p", "p", "p", "i", "p", "p", "p", "p", "p", "p"],
+    "swin_block_layernorm_backward": ["p", "p", "i", "p", "p", "p", "p", "p", "p", "p"],
+    "swin_block_layernorm_last_launches": ["p"],
+    "swin_block_layernorm_destroy": ["p"],
     "swin_block_gated_create": ["pp", "i", "i", "i"],
     "swin_block_gated_forward": ["p", "p", "i", "p", "p", "p", "p"],
     "swin_block_gated_forward_q8": ["p", "p", "p", "i", "p", "p", "p", "p"],
@@ -429,6 +436,69 @@ def swin_block_rms_backward(h, s, gamma, dy, dx, dgamma, dsum=None, stream=None)
         None if dsum is None else _arg("dsum", dsum, _BF, shape, dev), _arg("dx", dx, _BF, shape, dev),
         _arg("dgamma", dgamma, _F32, h.vec, dev), _stream_on(stream, dev))
     return rc and _check("swin_block_rms_backward", rc)
+
+
+# ---- swin_layernorm.h ---------------------------------------------------------------
+
+def swin_block_layernorm_create(C, eps=1e-5):
+    h = ctypes.c_void_p()
+    _check("swin_block_layernorm_create", load().swin_block_layernorm_create(ctypes.byref(h), C, eps))
+    h.C, h.vec = C, (C,)
+    return h
+
+
+def swin_block_layernorm_destroy(h):
+    return _check("swin_block_layernorm_destroy", load().swin_block_layernorm_destroy(h))
+
+
+def swin_block_layernorm_last_launches(h):
+    return load().swin_block_layernorm_last_launches(h)
+
+
+def swin_block_layernorm_forward(h, x, gamma, beta, out, residual=None, out_sum=None, stream=None):
+    """out = layer norm of x + residual over the last axis of x [..., C]; out_sum
+    receives the sum; beta may be None."""
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    rc = (_lib or load()).swin_block_layernorm_forward(
+        h, px, None if residual is None else _arg("residual", residual, _BF, shape, dev), rows,
+        _arg("gamma", gamma, _BF, h.vec, dev), None if beta is None else _arg("beta", beta, _BF, h.vec, dev),
+        None if out_sum is None else _arg("out_sum", out_sum, _BF, shape, dev), _arg("out", out, _BF, shape, dev),
+        _stream_on(stream, dev))
+    return rc and _check("swin_block_layernorm_forward", rc)
+
+
+def swin_block_layernorm_forward_post(h, x, gamma, beta, residual, out, stream=None):
+    """out = residual + layer norm of x over the last axis of x [..., C]."""
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    rc = (_lib or load()).swin_block_layernorm_forward_post(
+        h, px, _arg("residual", residual, _BF, shape, dev), rows, _arg("gamma", gamma, _BF, h.vec, dev),
+        None if beta is None else _arg("beta", beta, _BF, h.vec, dev), _arg("out", out, _BF, shape, dev),
+        _stream_on(stream, dev))
+    return rc and _check("swin_block_layernorm_forward_post", rc)
+
+
+def swin_block_layernorm_forward_q8(h, x, gamma, beta, out8, scales, residual=None, out_sum=None, stream=None):
+    """swin_block_layernorm_forward in e4m3 codes out8 [..., C] with one fp32 scale
+    a row."""
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    rc = (_lib or load()).swin_block_layernorm_forward_q8(
+        h, px, None if residual is None else _arg("residual", residual, _BF, shape, dev), rows,
+        _arg("gamma", gamma, _BF, h.vec, dev), None if beta is None else _arg("beta", beta, _BF, h.vec, dev),
+        None if out_sum is None else _arg("out_sum", out_sum, _BF, shape, dev), _arg("out8", out8, _E4M3, shape, dev),
+        _arg("scales", scales, _F32, shape[:-1], dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_layernorm_forward_q8", rc)
+
+
+def swin_block_layernorm_backward(h, s, gamma, dy, dx, dgamma, dbeta=None, dsum=None, stream=None):
+    """dx, dgamma and (where not None) dbeta from s [..., C] (the forward's out_sum,
+    or x), dy and the gradient dsum that reaches the sum past the norm."""
+    rows, shape, dev, ps = _rows(h, s, _BF, "s")
+    rc = (_lib or load()).swin_block_layernorm_backward(
+        h, ps, rows, _arg("gamma", gamma, _BF, h.vec, dev), _arg("dy", dy, _BF, shape, dev),
+        None if dsum is None else _arg("dsum", dsum, _BF, shape, dev), _arg("dx", dx, _BF, shape, dev),
+        _arg("dgamma", dgamma, _F32, h.vec, dev), None if dbeta is None else _arg("dbeta", dbeta, _F32, h.vec, dev),
+        _stream_on(stream, dev))
+    return rc and _check("swin_block_layernorm_backward", rc)
 
 
 # ---- swin_gated.h ------------------------------------------------------------------

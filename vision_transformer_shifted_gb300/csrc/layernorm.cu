@@ -1,0 +1,746 @@
+// Layer norm of the residual stream: s = x + residual (stored in bf16), y = (s -
+// mu) r gamma + beta with r = 1 / sqrt(var + eps); output in bf16, in e4m3 with
+// one scale a row, or added to the residual (post-norm); backward.
+//
+// As the root-mean-square norm (rms.cu): every input is read once and every
+// output written once, the row stays in registers (the wide backward: shared
+// memory) between the statistics and the output, and HBM bounds it.  The
+// statistics take two sums a row one after the other, the mean and then the
+// squared deviations from it: sum s^2 - C mu^2 would lose what a row's mean has
+// above its spread, and a row of one large value would not come out as zeros.
+// The second sum also yields the deviations' own mean, what the first one's
+// rounding left.
+#include <cmath>
+#include <new>
+
+#include "swin_layernorm.h"
+#include "norm.cuh"
+
+using namespace swin;
+
+namespace {
+
+enum { FORM_BF16 = 0, FORM_POST = 1, FORM_Q8 = 2 };
+
+struct LnArgs {
+    const bf16 *x, *residual, *gamma, *beta;
+    bf16 *out_sum;
+    void *out;       // bf16 [rows, C], or e4m3 codes
+    float *scales;   // e4m3: [rows]
+    int rows, chunks;   // chunks = C / 8
+    float inv_c, eps;
+    int lpr;         // lanes per row (rows on part of a warp)
+};
+
+// The sums of a and b over a row's lanes (a block: red holds a pair a warp; the
+// next sum takes another red, so that one barrier a sum is enough).
+template <bool BLOCK>
+__device__ __forceinline__ void row_sum2(float &a, float &b, int lpr, float2 *red)
+{
+    lane_sum2(a, b, BLOCK ? 32 : lpr);
+    if (!BLOCK) return;
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+    for (int w = 0; w < warps; ++w) {
+        a += red[w].x;
+        b += red[w].y;
+    }
+}
+
+// 1 / sqrt(var + eps) from the sums of the deviations from nearly the mean and of
+// their squares; mean: the deviations' own.
+__device__ __forceinline__ float deviation(float sum, float squares, float inv_c, float eps, float &mean)
+{
+    mean = sum * inv_c;
+    return rsqrtf(max_nan(fmaf(-mean, mean, squares * inv_c), 0.f) + eps);   // (infinite squares: r = 0)
+}
+
+template <int CPL, bool BLOCK, int FORM>
+__global__ void __launch_bounds__(BLOCK ? 512 : 256) layernorm_forward_kernel(LnArgs a)
+{
+    __shared__ float2 red[2][16];
+    griddep_launch_dependents();
+    griddep_wait();   // (nothing is read before the kernels queued earlier are done)
+    const int lane = threadIdx.x & 31;
+    const int step = BLOCK ? (int)blockDim.x : a.lpr;
+    const int li = BLOCK ? (int)threadIdx.x : lane % a.lpr;
+    const int64_t row = BLOCK ? (int64_t)blockIdx.x
+                              : ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * (32 / a.lpr) +
+                                    lane / a.lpr;
+    const bool row_ok = row < a.rows;
+    const int64_t base = row * a.chunks * 8;
+    uint4 s[CPL], t[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+        const bool ok = row_ok && c < a.chunks;
+        s[k] = ok ? ld16(a.x + base + c * 8) : make_uint4(0, 0, 0, 0);
+        if (FORM == FORM_POST || a.residual) t[k] = ok ? ld16(a.residual + base + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+    f2 sum2v = 0;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+        Piece v = piece(s[k]);
+        if (FORM != FORM_POST && a.residual) {
+            const Piece w = piece(t[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v.v[e] = add2(v.v[e], w.v[e]);
+            s[k] = pack(v);
+            v = piece(s[k]);   // the stored (rounded) sum is what the norm sees
+            if (a.out_sum && row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.out_sum + base + c * 8) = s[k];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum2v = add2(sum2v, v.v[e]);
+    }
+    uint4 gm[CPL], bt[CPL];   // (asked for before the row's sums are known)
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+        const bool ok = row_ok && c < a.chunks;
+        gm[k] = ok ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
+        bt[k] = ok && a.beta ? ld16(a.beta + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+    float sum = sum2(sum2v), sq = 0.f;
+    row_sum2<BLOCK>(sum, sq, a.lpr, red[0]);
+    const float mu = sum * a.inv_c;
+    auto minus_mu = [&](int k) { return li + k * step < a.chunks ? pack2(-mu) : pack2(0.f); };   // (behind the row: zeros)
+    f2 sq2v = 0;
+    sum2v = 0;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const Piece v = piece(s[k]);
+        const f2 m = minus_mu(k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f2 d = add2(v.v[e], m);
+            sum2v = add2(sum2v, d);
+            sq2v = fma2(d, d, sq2v);
+        }
+    }
+    sum = sum2(sum2v);
+    sq = sum2(sq2v);
+    row_sum2<BLOCK>(sum, sq, a.lpr, red[1]);
+    float mean;
+    const float r = deviation(sum, sq, a.inv_c, a.eps, mean);
+    const f2 r2 = pack2(r), shift = pack2(-mean * r);
+    if (FORM != FORM_Q8) {
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const int c = li + k * step;
+            if (!(row_ok && c < a.chunks)) continue;
+            Piece v = piece(s[k]);
+            const Piece g = piece(gm[k]), b = piece(bt[k]), w = piece(FORM == FORM_POST ? t[k] : make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v.v[e] = fma2(fma2(add2(v.v[e], pack2(-mu)), r2, shift), g.v[e], b.v[e]);
+                if (FORM == FORM_POST) v.v[e] = add2(v.v[e], w.v[e]);
+            }
+            *reinterpret_cast<uint4 *>((bf16 *)a.out + base + c * 8) = pack(v);
+        }
+        return;
+    }
+    f2 y[CPL][4];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {   // (pieces behind the row: gamma and beta are zeros)
+        const Piece v = piece(s[k]), g = piece(gm[k]), b = piece(bt[k]);
+        const f2 m = minus_mu(k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[k][e] = fma2(fma2(add2(v.v[e], m), r2, shift), g.v[e], b.v[e]);
+            float lo, hi;
+            unpack2(y[k][e], lo, hi);
+            amax = max_abs(amax, lo, hi);
+        }
+    }
+    amax = row_reduce<MaxOp, BLOCK>(amax, a.lpr, reinterpret_cast<float *>(red[0]));
+    store_codes<CPL>(y, amax, a.scales + row, row_ok, li, step, a.chunks, (uint8_t *)a.out + base);
+}
+
+struct LnBwdArgs {
+    const bf16 *s, *dy, *dsum, *gamma;
+    bf16 *dx;
+    float *partial;   // [gridDim.x, cols]: each block's shares of dgamma and (from column C) dbeta
+    float *dgamma, *dbeta;   // one block: written by it
+    int rows, chunks;
+    float inv_c, eps;
+    int lanes;        // of a row: of a warp, or (wide rows) threads
+};
+
+// The backward, dx = r (a - mean a - n mean(a n)) + dsum with a = dy gamma, of a
+// thread's piece of a row: its shares of the row's sum of s and of a,
+__device__ __forceinline__ void piece_sums(const Piece &s, const Piece &d, const Piece &g, f2 &sum, f2 &asum)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sum = add2(sum, s.v[e]);
+        asum = fma2(d.v[e], g.v[e], asum);
+    }
+}
+// of the deviations s - mu, their squares and their products with a,
+__device__ __forceinline__ void piece_moments(const Piece &s, const Piece &d, const Piece &g, f2 minus_mu, f2 &sum, f2 &sq, f2 &dot)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f2 v = add2(s.v[e], minus_mu);
+        sum = add2(sum, v);
+        sq = fma2(v, v, sq);
+        dot = fma2(mul2(d.v[e], g.v[e]), v, dot);
+    }
+}
+// and, from the row's sums, dx and the terms of dgamma and dbeta.
+struct RowGrad {
+    f2 minus_mu, r, shift;        // n = (s - mu) r + shift
+    f2 minus_ra, minus_rn;        // -r mean a, -r mean(a n)
+};
+__device__ __forceinline__ RowGrad row_grad(float mu, float sum, float sq, float asum, float dot, float inv_c, float eps,
+                                            bool ok)
+{
+    float mean;
+    // (no row: r = 0, since its terms get zero times r, and with eps = 0 one over
+    // the root of its variance is infinite)
+    const float r = ok ? deviation(sum, sq, inv_c, eps, mean) : (mean = 0.f);
+    const float ma = asum * inv_c, mn = r * fmaf(-mean, ma, dot * inv_c);
+    return {pack2(-mu), pack2(r), pack2(-mean * r), pack2(-r * ma), pack2(-r * mn)};
+}
+template <bool DSUM>
+__device__ __forceinline__ uint4 piece_grad(const Piece &s, const Piece &d, const Piece &g, const Piece &m, const RowGrad &w,
+                                            Piece &dg, Piece &db)
+{
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f2 n = fma2(add2(s.v[e], w.minus_mu), w.r, w.shift);
+        dg.v[e] = fma2(d.v[e], n, dg.v[e]);
+        db.v[e] = add2(db.v[e], d.v[e]);
+        f2 t = fma2(mul2(d.v[e], g.v[e]), w.r, w.minus_ra);
+        t = fma2(n, w.minus_rn, t);
+        if (DSUM) t = add2(t, m.v[e]);
+        float lo, hi;
+        unpack2(t, lo, hi);
+        o[e] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A block's columns of dgamma and dbeta: partial rows, or (one block) the result.
+__device__ __forceinline__ float *block_columns(const LnBwdArgs &a, int which)
+{
+    const int C = a.chunks * 8;
+    if (gridDim.x == 1) return which ? a.dbeta : a.dgamma;
+    return a.partial + (int64_t)blockIdx.x * C * (a.dbeta ? 2 : 1) + which * C;
+}
+
+constexpr int blocks_per_sm(int cpl, bool dsum) { return cpl > 1 ? 2 : 4; }
+
+// Rows on part of a warp: a block takes 8 * (32 / lanes) rows together, then the
+// ones gridDim.x on.  Each thread keeps the columns it owns of dgamma and dbeta
+// in registers over its rows; the block writes one partial row at the end.
+template <int CPL, bool DSUM>
+__global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) layernorm_backward_kernel(LnBwdArgs a)
+{
+    extern __shared__ float part[];   // [8 warps][C]
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = a.lanes, li = lane % step;
+    const int rpw = 32 / step, rpb = 8 * rpw;
+    Piece acc[2][CPL];
+    uint4 g[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const int c = li + k * step;
+        g[k] = c < a.chunks ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
+        acc[0][k] = acc[1][k] = Piece{};
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
+        const int64_t row = r0 + warp * rpw + lane / step;
+        const bool row_ok = row < a.rows;
+        const int64_t base = row * a.chunks * 8;
+        uint4 s[CPL], d[CPL], m[CPL];
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const int c = li + k * step;
+            const bool ok = row_ok && c < a.chunks;
+            s[k] = ok ? ld16(a.s + base + c * 8) : make_uint4(0, 0, 0, 0);
+            d[k] = ok ? ld16(a.dy + base + c * 8) : make_uint4(0, 0, 0, 0);
+            if (DSUM) m[k] = ok ? ld16(a.dsum + base + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+        // (the packed values stay, their fp32 forms are made again: registers
+        // kept across the sums would halve the rows in flight)
+        auto keep_packed = [&]() {
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                forget(s[k]);
+                forget(d[k]);
+                forget(g[k]);
+                if (DSUM) forget(m[k]);
+            }
+        };
+        f2 sum2v = 0, asum2 = 0, sq2 = 0, dot2 = 0;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) piece_sums(piece(s[k]), piece(d[k]), piece(g[k]), sum2v, asum2);
+        float sum = sum2(sum2v), asum = sum2(asum2);
+        lane_sum2(sum, asum, step);
+        keep_packed();
+        const float mu = sum * a.inv_c;
+        sum2v = 0;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k)
+            piece_moments(piece(s[k]), piece(d[k]), piece(g[k]), li + k * step < a.chunks ? pack2(-mu) : pack2(0.f), sum2v, sq2,
+                          dot2);
+        sum = sum2(sum2v);
+        float sq = sum2(sq2), dot = sum2(dot2);
+        lane_sum2(sum, sq, step);
+        for (int o = step >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        keep_packed();
+        const RowGrad w = row_grad(mu, sum, sq, asum, dot, a.inv_c, a.eps, row_ok);
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const int c = li + k * step;
+            const uint4 o = piece_grad<DSUM>(piece(s[k]), piece(d[k]), piece(g[k]), DSUM ? piece(m[k]) : Piece{}, w,
+                                             acc[0][k], acc[1][k]);
+            if (row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.dx + base + c * 8) = o;
+        }
+    }
+    // the warp's rows, then the block's warps
+    const int C = a.chunks * 8;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+        if (z && !a.dbeta) break;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const int c = li + k * step;
+            float sums[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) unpack2(acc[z][k].v[e], sums[2 * e], sums[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v = sums[e];
+                for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
+            }
+        }
+        __syncthreads();
+        float *out = block_columns(a, z);
+        for (int i = threadIdx.x; i < C; i += 256) {
+            float v = 0.f;
+            for (int w = 0; w < 8; ++w) v += part[w * C + i];
+            out[i] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// Three sums over a group of a block, of `threads` threads that meet at a barrier
+// of their own; red: two rows of 16 a group, used in turn.
+__device__ __forceinline__ void group_sum3(float &a, float &b, float &c, int threads, int group, int turn, float4 *red)
+{
+    lane_sum2(a, b, 32);
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    const int warps = threads >> 5, warp = (threadIdx.x - group * threads) >> 5;
+    red += (2 * group + (turn & 1)) * 16;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float4(a, b, c, 0.f);
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    a = b = c = 0.f;
+    for (int w = 0; w < warps; ++w) {
+        const float4 v = red[w];
+        a += v.x;
+        b += v.y;
+        c += v.z;
+    }
+}
+
+// Wider rows: a group of warps a row, several groups a block (few blocks, since
+// each writes partial rows that are read again).  Every thread fetches its own
+// pieces of the next row by asynchronous copies into its own place in shared
+// memory, so that the latency of HBM is paid once, not once a row.
+template <int CPL, bool DSUM>
+__global__ void __launch_bounds__(512, 1) layernorm_backward_wide_kernel(LnBwdArgs a)
+{
+    constexpr int ARRAYS = DSUM ? 3 : 2, DEPTH = 2;   // stages: a row, and the next
+    extern __shared__ __align__(16) float part[];   // the pieces; at the end [C]
+    __shared__ float4 red[2 * 16 * 16];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int step = a.lanes, group = (int)threadIdx.x / step, li = (int)threadIdx.x - group * step;
+    const int rpb = (int)blockDim.x / step, C = a.chunks * 8;
+    // this thread's piece k of array i in a stage at `at`: place(at, i, k)
+    const uint32_t stride = blockDim.x * 16, stage = ARRAYS * CPL * stride;
+    const uint32_t ring = smem_u32(part) + threadIdx.x * 16, ring_end = ring + DEPTH * stage;
+    auto place = [&](uint32_t at, int i, int k) { return at + (uint32_t)(i * CPL + k) * stride; };
+    bool have[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) have[k] = li + k * step < a.chunks;
+    const int64_t first = (int64_t)blockIdx.x * rpb + group, hop = (int64_t)gridDim.x * rpb;
+    int64_t ahead = first;   // the next row to fetch, and its stage
+    uint32_t ahead_at = ring;
+    auto fetch = [&]() {
+        if (ahead < a.rows) {
+            const int64_t off = ahead * C + li * 8;
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                if (!have[k]) continue;
+                cp_async16(place(ahead_at, 0, k), a.s + off + k * step * 8, 16);
+                cp_async16(place(ahead_at, 1, k), a.dy + off + k * step * 8, 16);
+                if (DSUM) cp_async16(place(ahead_at, 2, k), a.dsum + off + k * step * 8, 16);
+            }
+        }
+        cp_async_commit();
+        ahead += hop;
+        ahead_at += stage;
+        if (ahead_at == ring_end) ahead_at = ring;
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fetch();
+    Piece acc[2][CPL];
+    uint4 g[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        g[k] = have[k] ? ld16(a.gamma + (li + k * step) * 8) : make_uint4(0, 0, 0, 0);
+        acc[0][k] = acc[1][k] = Piece{};
+    }
+    uint32_t at = ring;
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t row = first; row < a.rows; row += hop) {   // (the same for a group's threads)
+        fetch();
+        cp_async_wait<DEPTH - 1>();
+        f2 sum2v = 0, asum2 = 0, sq2 = 0, dot2 = 0;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            forget(g[k]);   // (kept packed)
+            if (have[k]) piece_sums(piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), piece(g[k]), sum2v, asum2);
+        }
+        float sum = sum2(sum2v), asum = sum2(asum2), sq = 0.f;
+        group_sum3(sum, asum, sq, step, group, turn++, red);
+        const float mu = sum * a.inv_c;
+        sum2v = 0;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            forget(g[k]);
+            if (have[k])
+                piece_moments(piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), piece(g[k]), pack2(-mu), sum2v, sq2,
+                              dot2);
+        }
+        sum = sum2(sum2v);
+        sq = sum2(sq2);
+        float dot = sum2(dot2);
+        group_sum3(sum, sq, dot, step, group, turn++, red);
+        const RowGrad w = row_grad(mu, sum, sq, asum, dot, a.inv_c, a.eps, true);
+        bf16 *dx = a.dx + row * C + li * 8;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            forget(g[k]);
+            if (!have[k]) continue;
+            const Piece m = DSUM ? piece(lds16(place(at, 2, k))) : Piece{};
+            *reinterpret_cast<uint4 *>(dx + k * step * 8) = piece_grad<DSUM>(
+                piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), piece(g[k]), m, w, acc[0][k], acc[1][k]);
+        }
+        at += stage;
+        if (at == ring_end) at = ring;
+    }
+    __syncthreads();   // (every group is done with its pieces)
+    // the groups add theirs in turn
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+        if (z && !a.dbeta) break;
+        for (int t = 0; t < rpb; ++t) {
+            if (group == t)
+#pragma unroll
+                for (int k = 0; k < CPL; ++k) {
+                    const int c = li + k * step;
+                    if (c >= a.chunks) continue;
+                    float4 *p = reinterpret_cast<float4 *>(part + c * 8);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float4 v;
+                        unpack2(acc[z][k].v[2 * h], v.x, v.y);
+                        unpack2(acc[z][k].v[2 * h + 1], v.z, v.w);
+                        const float4 old = t ? p[h] : make_float4(0.f, 0.f, 0.f, 0.f);
+                        p[h] = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+                    }
+                }
+            __syncthreads();
+        }
+        float *out = block_columns(a, z);
+        for (int i = threadIdx.x; i < C; i += blockDim.x) out[i] = part[i];
+        __syncthreads();
+    }
+}
+
+constexpr int FWD_PIECES = 4, BWD_PIECES = 3, BWD_BLOCK_PIECES = 4;
+constexpr int MAX_GROUPS = 15;   // row groups of a block: a block has 16 barriers, and one is everybody's
+
+template <int FORM>
+cudaError_t launch_forward(LnArgs a, cudaStream_t stream)
+{
+    // rows that leave SMs idle take as many threads as pieces: the latency of
+    // one row counts then
+    const int most = a.rows < sm_count() ? 1 : FWD_PIECES;
+    const RowPlan p = plan_row(a.chunks, most, most);
+    a.lpr = p.block ? 32 : p.lanes;
+    const int threads = p.block ? p.lanes : 256;
+    const int64_t rpb = p.block ? 1 : 8 * (32 / p.lanes);
+    const unsigned grid = (unsigned)((a.rows + rpb - 1) / rpb);
+#define SWIN_LN_CASE(n)                                                                       \
+    case n:                                                                                   \
+        return launch_maybe_overlapped(p.block ? layernorm_forward_kernel<n, true, FORM>      \
+                                               : layernorm_forward_kernel<n, false, FORM>,    \
+                                       dim3(grid), dim3(threads), 0, stream, 1, a);
+    switch (p.cpl) {
+        SWIN_LN_CASE(1)
+        SWIN_LN_CASE(2)
+        SWIN_LN_CASE(3)
+        SWIN_LN_CASE(4)
+    default:
+        return cudaErrorInvalidValue;
+    }
+#undef SWIN_LN_CASE
+}
+
+// The backward's launch: as many blocks as the SMs hold at once, each walking
+// its share of the rows.
+struct BwdPlan {
+    RowPlan row;
+    int threads, grid;
+    size_t smem;
+};
+BwdPlan plan_backward(int rows, int C, bool with_dsum)
+{
+    const int chunks = C / 8;
+    BwdPlan p{};
+    p.row = plan_row(chunks, BWD_PIECES, BWD_BLOCK_PIECES);
+    const RowPlan &r = p.row;
+    int64_t rpb, per_sm;
+    if (r.block) {
+        const int groups = 512 / r.lanes;
+        rpb = groups < MAX_GROUPS ? groups : MAX_GROUPS;
+        per_sm = 1;
+        p.threads = (int)rpb * r.lanes;
+        p.smem = (size_t)p.threads * (with_dsum ? 3 : 2) * 2 * r.cpl * 16;   // (at most 192 KB)
+        if (p.smem < (size_t)C * sizeof(float)) p.smem = (size_t)C * sizeof(float);
+    } else {
+        rpb = 8 * (32 / r.lanes);
+        per_sm = blocks_per_sm(r.cpl, with_dsum);
+        p.threads = 256;
+        p.smem = (size_t)8 * C * sizeof(float);
+    }
+    const int64_t want = (rows + rpb - 1) / rpb, most = sm_count() * per_sm;
+    // few rows: one block, whose sums are the result (two turns at most: less than
+    // what the second launch would cost)
+    p.grid = want <= 2 ? 1 : (int)(want < most ? want : most);
+    return p;
+}
+
+cudaError_t launch_backward(LnBwdArgs a, const BwdPlan &p, cudaStream_t stream)
+{
+    const RowPlan &r = p.row;
+    a.lanes = r.lanes;
+    const int C = a.chunks * 8, cols = a.dbeta ? 2 * C : C;
+    void (*kern)(LnBwdArgs) = nullptr;
+    if (r.block)
+        kern = a.dsum ? (r.cpl == 3 ? layernorm_backward_wide_kernel<3, true> : layernorm_backward_wide_kernel<4, true>)
+                      : (r.cpl == 3 ? layernorm_backward_wide_kernel<3, false> : layernorm_backward_wide_kernel<4, false>);
+    else if (a.dsum)
+        kern = r.cpl == 1 ? layernorm_backward_kernel<1, true>
+                          : r.cpl == 2 ? layernorm_backward_kernel<2, true> : layernorm_backward_kernel<3, true>;
+    else
+        kern = r.cpl == 1 ? layernorm_backward_kernel<1, false>
+                          : r.cpl == 2 ? layernorm_backward_kernel<2, false> : layernorm_backward_kernel<3, false>;
+    cudaError_t e;
+    // (always the most any call needs: another thread may be between its setting
+    // and its launch)
+    if (r.block &&
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 6 * r.cpl * 16)) != cudaSuccess)
+        return e;
+    e = launch_maybe_overlapped(kern, dim3(p.grid), dim3(p.threads), p.smem, stream, 1, a);
+    if (e != cudaSuccess || p.grid == 1) return e;
+    return launch_maybe_overlapped(column_sum_kernel, dim3((cols + 31) / 32), dim3(1024), 0, stream, 1,
+                                   (const float *)a.partial, p.grid, cols, a.dgamma, C, a.dbeta);
+}
+
+bool bad_pointer(const void *p, bool required)
+{
+    return p ? (reinterpret_cast<uintptr_t>(p) & 15u) != 0 : required;
+}
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA; }
+
+} // namespace
+
+struct swin_block_layernorm_s {
+    int C;
+    float eps;
+    int device;   // -1: not bound yet
+    int last_launches;
+    OrderedWorkspace ws;   // the backward's partial sums of dgamma and dbeta
+};
+
+namespace {
+
+// Checks shared by the forward forms; `out_bytes` of one output element.
+int check_forward(const swin_block_layernorm_s *h, const void *x, const void *residual, int rows, const void *gamma,
+                  const void *beta, const void *out_sum, const void *out, int64_t out_bytes)
+{
+    if (!h || rows < 0) return SWIN_WATTN_EINVAL;
+    if (rows == 0) return SWIN_WATTN_OK;   // (an empty tensor may have no address)
+    if (bad_pointer(x, true) || bad_pointer(residual, false) || bad_pointer(gamma, true) || bad_pointer(beta, false) ||
+        bad_pointer(out_sum, false) || bad_pointer(out, true) || (out_sum && !residual))
+        return SWIN_WATTN_EINVAL;
+    const int64_t n = (int64_t)rows * h->C, in = 2 * n, on = out_bytes * n, vec = 2 * (int64_t)h->C;
+    const bool same_type = out_bytes == 2;
+    // in place (the very same tensor) is fine, any other overlap is not
+    for (const void *p : {x, residual}) {
+        if (!p) continue;
+        if (overlaps(p, in, out, on) && !(same_type && p == out)) return SWIN_WATTN_EINVAL;
+        if (out_sum && overlaps(p, in, out_sum, in) && p != out_sum) return SWIN_WATTN_EINVAL;
+    }
+    for (const void *p : {gamma, beta})
+        if (p && (overlaps(p, vec, out, on) || (out_sum && overlaps(p, vec, out_sum, in)))) return SWIN_WATTN_EINVAL;
+    if (out_sum && overlaps(out_sum, in, out, on)) return SWIN_WATTN_EINVAL;
+    return SWIN_WATTN_OK;
+}
+
+LnArgs forward_args(const swin_block_layernorm_s *h, const void *x, const void *residual, int rows, const void *gamma,
+                    const void *beta, void *out_sum, void *out, float *scales)
+{
+    LnArgs a{};
+    a.x = (const bf16 *)x;
+    a.residual = (const bf16 *)residual;
+    a.gamma = (const bf16 *)gamma;
+    a.beta = (const bf16 *)beta;
+    a.out_sum = (bf16 *)out_sum;
+    a.out = out;
+    a.scales = scales;
+    a.rows = rows;
+    a.chunks = h->C / 8;
+    a.inv_c = 1.f / (float)h->C;
+    a.eps = h->eps;
+    return a;
+}
+
+} // namespace
+
+extern "C" {
+
+int swin_block_layernorm_create(swin_block_layernorm_t *out, int C, float eps)
+{
+    if (!out) return SWIN_WATTN_EINVAL;
+    *out = nullptr;
+    if (C <= 0 || C % 8 || C > NORM_MAX_C || !(eps >= 0.f) || std::isinf(eps)) return SWIN_WATTN_EINVAL;
+    swin_block_layernorm_s *h = new (std::nothrow) swin_block_layernorm_s{};
+    if (!h) return SWIN_WATTN_ENOMEM;
+    h->C = C;
+    h->eps = eps;
+    h->device = -1;
+    *out = h;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_layernorm_destroy(swin_block_layernorm_t h)
+{
+    if (!h) return SWIN_WATTN_OK;
+    ows_free(&h->ws);
+    delete h;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_layernorm_last_launches(swin_block_layernorm_t h) { return h ? h->last_launches : 0; }
+
+int swin_block_layernorm_forward(swin_block_layernorm_t h, const void *x, const void *residual, int rows,
+                                 const void *gamma, const void *beta, void *out_sum, void *out, swin_stream_t stream)
+{
+    int rc = check_forward(h, x, residual, rows, gamma, beta, out_sum, out, 2);
+    if (rc != SWIN_WATTN_OK || rows == 0) return rc;
+    if ((rc = bind_device(&h->device)) != SWIN_WATTN_OK) return rc;
+    h->last_launches = 1;
+    return cuda_status(launch_forward<FORM_BF16>(forward_args(h, x, residual, rows, gamma, beta, out_sum, out, nullptr),
+                                                 (cudaStream_t)stream));
+}
+
+int swin_block_layernorm_forward_post(swin_block_layernorm_t h, const void *x, const void *residual, int rows,
+                                      const void *gamma, const void *beta, void *out, swin_stream_t stream)
+{
+    int rc = check_forward(h, x, residual, rows, gamma, beta, nullptr, out, 2);
+    if (rc != SWIN_WATTN_OK || rows == 0) return rc;
+    if (!residual) return SWIN_WATTN_EINVAL;
+    if ((rc = bind_device(&h->device)) != SWIN_WATTN_OK) return rc;
+    h->last_launches = 1;
+    return cuda_status(launch_forward<FORM_POST>(forward_args(h, x, residual, rows, gamma, beta, nullptr, out, nullptr),
+                                                 (cudaStream_t)stream));
+}
+
+int swin_block_layernorm_forward_q8(swin_block_layernorm_t h, const void *x, const void *residual, int rows,
+                                    const void *gamma, const void *beta, void *out_sum, void *out8, float *scales,
+                                    swin_stream_t stream)
+{
+    int rc = check_forward(h, x, residual, rows, gamma, beta, out_sum, out8, 1);
+    if (rc != SWIN_WATTN_OK || rows == 0) return rc;
+    if (bad_pointer(scales, true)) return SWIN_WATTN_EINVAL;
+    const int64_t n = (int64_t)rows * h->C, sn = 4 * (int64_t)rows, vec = 2 * (int64_t)h->C;
+    if (overlaps(scales, sn, x, 2 * n) || overlaps(scales, sn, residual, residual ? 2 * n : 0) ||
+        overlaps(scales, sn, out_sum, out_sum ? 2 * n : 0) || overlaps(scales, sn, out8, n) ||
+        overlaps(scales, sn, gamma, vec) || overlaps(scales, sn, beta, beta ? vec : 0))
+        return SWIN_WATTN_EINVAL;
+    if ((rc = bind_device(&h->device)) != SWIN_WATTN_OK) return rc;
+    h->last_launches = 1;
+    return cuda_status(launch_forward<FORM_Q8>(forward_args(h, x, residual, rows, gamma, beta, out_sum, out8, scales),
+                                               (cudaStream_t)stream));
+}
+
+int swin_block_layernorm_backward(swin_block_layernorm_t h, const void *s, int rows, const void *gamma, const void *dy,
+                                  const void *dsum, void *dx, float *dgamma, float *dbeta, swin_stream_t stream)
+{
+    if (!h || rows < 0 || bad_pointer(dgamma, true) || bad_pointer(dbeta, false)) return SWIN_WATTN_EINVAL;
+    const int64_t n = 2 * (int64_t)rows * h->C, vec = 2 * (int64_t)h->C;
+    if (dbeta && overlaps(dgamma, 2 * vec, dbeta, 2 * vec)) return SWIN_WATTN_EINVAL;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 0) {
+        const int rc = bind_device(&h->device);
+        if (rc != SWIN_WATTN_OK) return rc;
+        const cudaError_t e = cudaMemsetAsync(dgamma, 0, 2 * (size_t)vec, st);
+        return cuda_status(e != cudaSuccess || !dbeta ? e : cudaMemsetAsync(dbeta, 0, 2 * (size_t)vec, st));
+    }
+    if (bad_pointer(s, true) || bad_pointer(gamma, true) || bad_pointer(dy, true) || bad_pointer(dsum, false) ||
+        bad_pointer(dx, true))
+        return SWIN_WATTN_EINVAL;
+    if (overlaps(s, n, dx, n) || (overlaps(dy, n, dx, n) && dy != dx) ||
+        (dsum && overlaps(dsum, n, dx, n) && dsum != dx) || overlaps(gamma, vec, dx, n))
+        return SWIN_WATTN_EINVAL;
+    for (const void *o : {(const void *)dgamma, (const void *)dbeta}) {
+        if (!o) continue;
+        for (const void *p : {s, dy, dsum, (const void *)dx})
+            if (p && overlaps(p, n, o, 2 * vec)) return SWIN_WATTN_EINVAL;
+        if (overlaps(gamma, vec, o, 2 * vec)) return SWIN_WATTN_EINVAL;
+    }
+    int rc = bind_device(&h->device);
+    if (rc != SWIN_WATTN_OK) return rc;
+    const BwdPlan p = plan_backward(rows, h->C, dsum != nullptr);
+    void *ws = nullptr;
+    bool captured = false;
+    if (p.grid > 1 && (rc = ows_begin(&h->ws, (size_t)p.grid * h->C * (dbeta ? 2 : 1) * sizeof(float), st, &ws, &captured)) !=
+                          SWIN_WATTN_OK)
+        return rc;
+    LnBwdArgs a{};
+    a.s = (const bf16 *)s;
+    a.dy = (const bf16 *)dy;
+    a.dsum = (const bf16 *)dsum;
+    a.gamma = (const bf16 *)gamma;
+    a.dx = (bf16 *)dx;
+    a.partial = (float *)ws;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.rows = rows;
+    a.chunks = h->C / 8;
+    a.inv_c = 1.f / (float)h->C;
+    a.eps = h->eps;
+    h->last_launches = p.grid > 1 ? 2 : 1;
+    rc = cuda_status(launch_backward(a, p, st));
+    const int rc2 = ows_end(&h->ws, st, ws, captured);
+    return rc != SWIN_WATTN_OK ? rc : rc2;
+}
+
+} // extern "C"
