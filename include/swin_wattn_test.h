@@ -11,6 +11,7 @@
 #define SWIN_WATTN_TEST_H
 
 #include "swin_gated.h"
+#include "swin_linear.h"
 #include "swin_wattn.h"
 
 #ifdef __cplusplus
@@ -109,6 +110,20 @@ int swin_block_gated_test_plan(int C, int F, int rows, int which, int *plan);
 
 /* swin_wattn_test_corrupt_workspace for a gated block's handle. */
 int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side);
+
+/* How the linear operator (swin_linear.h) divides a product, as
+ * swin_block_gated_test_plan does: the forward (bf16 or 8-bit, more than 128
+ * rows), dx or dW. */
+enum {
+    SWIN_BLOCK_LINEAR_PLAN_FORWARD = 0,
+    SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8 = 1,
+    SWIN_BLOCK_LINEAR_PLAN_DX = 2,
+    SWIN_BLOCK_LINEAR_PLAN_WEIGHT = 3
+};
+int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan);
+
+/* swin_wattn_test_corrupt_workspace for a linear operator's handle. */
+int swin_block_linear_test_corrupt_workspace(swin_block_linear_t h, int side);
 
 #ifdef __cplusplus
 }

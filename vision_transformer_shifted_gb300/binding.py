@@ -1,5 +1,6 @@
 """ctypes binding of libswin_wattn (include/swin_wattn.h, swin_wattn_test.h,
-swin_block.h, swin_wattn_backward.h, swin_rms.h, swin_gated.h, swin_layernorm.h).
+swin_block.h, swin_wattn_backward.h, swin_rms.h, swin_gated.h, swin_layernorm.h,
+swin_linear.h).
 
 Argument marshalling only: every function here passes tensor pointers and
 sizes to the C ABI of the same name and raises on a non-OK status.  torch is
@@ -21,6 +22,8 @@ NOALLOC_MAX_INTERMEDIATE_BYTES = (64 << 20) - 256
 OPT_PATH, OPT_WAIT_LIMIT_US, OPT_HOST_CHUNKS, OPT_OVERLAP_CALLS = 1, 2, 3, 4
 BLOCK_OPT_OVERLAP_CALLS = 1
 BLOCK_GATED_SILU, BLOCK_GATED_GELU = 0, 1
+BLOCK_LINEAR_NONE, BLOCK_LINEAR_SILU, BLOCK_LINEAR_GELU = 0, 1, 2
+BLOCK_LINEAR_PLAN_FORWARD, BLOCK_LINEAR_PLAN_FORWARD_Q8, BLOCK_LINEAR_PLAN_DX, BLOCK_LINEAR_PLAN_WEIGHT = 0, 1, 2, 3
 BLOCK_GATED_PLAN_DOWN, BLOCK_GATED_PLAN_DX, BLOCK_GATED_PLAN_WEIGHTS, BLOCK_GATED_PLAN_NARROW = 0, 1, 2, 3
 PATH_AUTO, PATH_THREE_KERNELS, PATH_FUSED, PATH_FP32 = 0, 1, 2, 3
 
@@ -91,6 +94,15 @@ _SIGNATURES = {
     "swin_block_gated_test_stall": ["p", "p", "i", "p", "l", "p"],
     "swin_block_gated_test_corrupt_workspace": ["p", "i"],
     "swin_block_gated_test_plan": ["i", "i", "i", "i", "p"],
+    "swin_block_linear_create": ["pp", "i", "i", "i"],
+    "swin_block_linear_forward": ["p", "p", "i", "p", "p", "p", "p", "p", "p"],
+    "swin_block_linear_forward_q8": ["p", "p", "p", "i", "p", "p", "p", "p", "p", "p"],
+    "swin_block_linear_backward": ["p", "p", "i", "p", "p", "p", "p", "p", "p", "p"],
+    "swin_block_linear_last_launches": ["p"],
+    "swin_block_linear_sync_status": ["p", "p"],
+    "swin_block_linear_destroy": ["p"],
+    "swin_block_linear_test_plan": ["i", "i", "i", "i", "p"],
+    "swin_block_linear_test_corrupt_workspace": ["p", "i"],
     "swin_block_gated_test_last_use": ["i", "i", "i", "p", "p"],
 }
 
@@ -608,3 +620,70 @@ def swin_block_gated_test_plan(C, F, rows, which):
     plan = (ctypes.c_int * 6)()
     _check("swin_block_gated_test_plan", load().swin_block_gated_test_plan(C, F, rows, which, ctypes.addressof(plan)))
     return tuple(plan)
+
+
+# ---- swin_linear.h -----------------------------------------------------------------
+
+def swin_block_linear_create(C, N, act=BLOCK_LINEAR_NONE):
+    h = ctypes.c_void_p()
+    _check("swin_block_linear_create", load().swin_block_linear_create(ctypes.byref(h), C, N, act))
+    h.C, h.N, h.vec, h.weight = C, N, (N,), (N, C)
+    return h
+
+
+def swin_block_linear_destroy(h):
+    return _check("swin_block_linear_destroy", load().swin_block_linear_destroy(h))
+
+
+def swin_block_linear_last_launches(h):
+    return load().swin_block_linear_last_launches(h)
+
+
+def swin_block_linear_sync_status(h, stream=None):
+    return _check("swin_block_linear_sync_status", load().swin_block_linear_sync_status(h, _stream(stream)))
+
+
+def swin_block_linear_forward(h, x, W, b, out, residual=None, z=None, stream=None):
+    """out = residual + act(x W^T + b) for x [..., C], W [N, C]; b may be None; z
+    receives the value before the activation."""
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    shape = shape[:-1] + h.vec
+    rc = (_lib or load()).swin_block_linear_forward(
+        h, px, rows, _arg("W", W, _BF, h.weight, dev), _bias("b", b, h.vec, dev), _bias("residual", residual, shape, dev),
+        _bias("z", z, shape, dev), _arg("out", out, _BF, shape, dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_linear_forward", rc)
+
+
+def swin_block_linear_forward_q8(h, x8, sx, W8, sw, b, out, residual=None, stream=None):
+    """The same from e4m3 x8 [..., C] with scales sx [...] and W8 [N, C] with scales
+    sw [N]."""
+    rows, shape, dev, px = _rows(h, x8, _E4M3, "x8")
+    scales, shape = shape[:-1], shape[:-1] + h.vec
+    rc = (_lib or load()).swin_block_linear_forward_q8(
+        h, px, _arg("sx", sx, _F32, scales, dev), rows, _arg("W8", W8, _E4M3, h.weight, dev),
+        _arg("sw", sw, _F32, h.vec, dev), _bias("b", b, h.vec, dev), _bias("residual", residual, shape, dev),
+        _arg("out", out, _BF, shape, dev), _stream_on(stream, dev))
+    return rc and _check("swin_block_linear_forward_q8", rc)
+
+
+def swin_block_linear_backward(h, x, W, dy, dx, dW, db=None, z=None, stream=None):
+    """dx [..., C], dW [N, C] and db [N] (bf16; None: not computed) from x, W, dy [...,
+    N] and, with an activation, the forward's z."""
+    rows, shape, dev, px = _rows(h, x, _BF, "x")
+    wide = shape[:-1] + h.vec
+    rc = (_lib or load()).swin_block_linear_backward(
+        h, px, rows, _arg("W", W, _BF, h.weight, dev), _bias("z", z, wide, dev), _arg("dy", dy, _BF, wide, dev),
+        _bias("dx", dx, shape, dev), _bias("dW", dW, h.weight, dev), _bias("db", db, h.vec, dev),
+        _stream_on(stream, dev))
+    return rc and _check("swin_block_linear_backward", rc)
+
+
+def swin_block_linear_test_plan(C, N, rows, which):
+    plan = (ctypes.c_int * 6)()
+    _check("swin_block_linear_test_plan",
+           load().swin_block_linear_test_plan(C, N, rows, which, ctypes.addressof(plan)))
+    return tuple(plan)
+
+
+def swin_block_linear_test_corrupt_workspace(h, side):
+    return _check("swin_block_linear_test_corrupt_workspace", load().swin_block_linear_test_corrupt_workspace(h, side))

@@ -1,5 +1,5 @@
-// The gated feed-forward block: C ABI, plans and launches of the kernels in
-// gated.cuh, and the two small kernels that finish sums over rows.
+// The gated feed-forward block: C ABI and launches of the kernels in gated.cuh
+// and of its products (products.cuh).
 //   forward   h = act(x Wg^T + bg) * (x Wu^T + bu)        (one kernel)
 //             out = residual + h Wd^T + bd                 (one kernel)
 //   backward  h, dg, du from x and dy (one kernel), dx = dg Wg + du Wu, then
@@ -28,8 +28,6 @@ namespace {
 constexpr int MAX_WIDTH = 65536;
 constexpr int MAX_ROWS = INT_MAX - 512;   // row coordinates of the last tile stay below 2^31
 constexpr uint64_t WAIT_NS = 2000000000ull;
-constexpr CUtensorMapDataType T_BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, T_U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                              T_F32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA; }
 
@@ -37,48 +35,6 @@ bool bad_pointer(const void *p, bool required)
 {
     return p ? (reinterpret_cast<uintptr_t>(p) & 15u) != 0 : required;
 }
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// K-major operand [rows, k] (row stride ld elements, 0: k): boxes of 128 bytes
-// of K x box_rows.
-cudaError_t map_k(CUtensorMap *m, const void *p, int64_t rows, int k, int box_rows, bool q8 = false, int ld = 0)
-{
-    const int e = q8 ? 1 : 2;
-    return make_tensor_map(m, q8 ? T_U8 : T_BF16, p, k, rows, (int64_t)(ld ? ld : k) * e, 128 / e, box_rows, 128);
-}
-// MN-major operand, stored [k, mn] (row stride ld, 0: mn): boxes of 64 MN
-// elements x 64 k.
-cudaError_t map_mn(CUtensorMap *m, const void *p, int64_t k, int mn, int ld = 0)
-{
-    return make_tensor_map(m, T_BF16, p, mn, k, (int64_t)(ld ? ld : mn) * 2, 64, 64, 128);
-}
-// Output [rows, cols]: a warp's boxes of 32 columns x 32 rows.
-cudaError_t map_out(CUtensorMap *m, const void *p, int64_t rows, int cols)
-{
-    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)cols * 2, 32, 32, 64);
-}
-// Hidden activations in the workspace, [rows, F] with rows padded to 128 bytes:
-// a box's rows are whole lines.  (F = 1368 unpadded: five sectors in two lines
-// where four in one would do: its weight gradients took 47.7 us instead of 43.0.)
-int hidden_ld(int F) { return (F + 63) / 64 * 64; }
-// The kernels that write them: boxes of 32 columns x 32 rows.
-cudaError_t map_hidden(CUtensorMap *m, const void *p, int64_t rows, int cols)
-{
-    return make_tensor_map(m, T_BF16, p, cols, rows, (int64_t)hidden_ld(cols) * 2, 32, 32, 64);
-}
-
-// One product of a launch_products call: D [rows, cols] = sum over K segments of
-// A B^T (+ bias + residual).
-struct Product {
-    const void *a[2], *b[2];
-    int k[2];
-    int lda, ldb;   // row strides as stored (0: dense)
-    bf16 *d;
-    const bf16 *bias, *residual;
-    int64_t rows;
-    int cols;
-};
 
 // The shapes of a call's products: the forward's last one, dx, and dWg, dWu, dWd.
 Product down_product(int C, int F, int rows)
@@ -106,303 +62,6 @@ void weight_products(int C, int F, int rows, Product (&p)[3])
         (i < 2 ? p[i].lda : p[i].ldb) = hidden_ld(F);
     }
 }
-
-// What joining the tiles of a cut round costs, in K blocks of a whole tile: the
-// launch, the partial tiles' traffic and their second epilogue, some 10 us.
-// (Forward 1537 x 1536 x 4104, 42 tiles: 57.5 us with their 65 blocks cut to 36,
-// 53.3 whole; 3000 x 1024 x 4096: 63.7 cut, 55.5 whole; 12544 x 512 x 1368
-// backward: 147 whole, 131 with the cuts that this cost allows, 135 with every cut
-// that saves a block.)
-constexpr int WIDE_JOIN = 32, NARROW_JOIN = 36;
-// A K block of a 256 x 192 tile in hundredths of a whole one's: tiles of that width
-// where they come out cheaper, as a round that leaves a third of the pairs idle
-// with 256 columns (1300 x 2048 x 5632 forward: 48 tiles 70.5 us, 66 of them 69.5;
-// e4m3 1537 x 1536 x 4104 41.1 and 39.1; 3000 x 1024 x 2736 backward 105 and 103.8).
-constexpr int COST_192 = 82;
-// A K block of half a tile (256 x 128) in hundredths of a whole one's, with
-// `halves` pairs at it: half of the MMAs and a little, or (many pairs) its share
-// of what L2 delivers, three quarters of a whole tile's operands a pair.
-int half_cost(int halves, int pairs) { return halves * 75 > 55 * pairs ? halves * 75 / pairs : 55; }
-
-// The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
-// of K (+ bias + residual).  `blocks` blocks a tile and VEC values a thread at a
-// time: 16 and eight, or (few tiles, of many partial tiles each) 64 and four;
-// 3 tiles of 25 partial tiles: 9 us, 15 by sixteen blocks.
-struct JoinArgs {
-    const float *part;
-    PairSplit split;
-    int tn, blocks;
-    bool from_last;   // (tile_place)
-    struct {
-        const bf16 *bias, *residual;
-        bf16 *out;
-        int rows, cols, mt, nt, first;
-    } p[3];
-};
-template <int VEC>
-__device__ __forceinline__ void add_vec(float (&v)[VEC], const float *p)
-{
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-        const float4 w = *reinterpret_cast<const float4 *>(p + k);
-        v[k] += w.x;
-        v[k + 1] += w.y;
-        v[k + 2] += w.z;
-        v[k + 3] += w.w;
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void add_vec(float (&v)[VEC], const bf16 *p)
-{
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p + k);
-        const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
-        v[k] += x.x;
-        v[k + 1] += x.y;
-        v[k + 2] += y.x;
-        v[k + 3] += y.y;
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
-{
-    const PairSplit &s = a.split;
-    const int c = block / a.blocks, t = s.full * s.np + c;
-    const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
-    if (p0 == p1) return;   // (one pair had the whole tile and wrote it)
-    const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
-    int m, n;
-    tile_order(tile_place(t - a.p[i].first, a.p[i].mt, a.p[i].nt, a.from_last), a.p[i].mt, a.p[i].nt, m, n);
-    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / VEC;
-    const int64_t size = 256 * a.tn;
-    const int first = s.slot(p0, c);
-    for (int e = block % a.blocks * 256 + threadIdx.x; e < 256 * per; e += a.blocks * 256) {
-        const int row = m * 256 + e / per, col = n * a.tn + e % per * VEC;
-        if (row >= rows || col >= cols) continue;
-        const float *src = a.part + (int64_t)e * VEC;
-        float v[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) v[k] = 0.f;
-        add_vec<VEC>(v, src + first * size);
-#pragma unroll 4
-        for (int p = p0 + 1; p <= p1; ++p)   // (these begin inside the tile: their first range)
-            add_vec<VEC>(v, src + 2 * p * size);
-        const int64_t at = (int64_t)row * cols + col;
-        if (a.p[i].bias) add_vec<VEC>(v, a.p[i].bias + col);
-        if (a.p[i].residual) add_vec<VEC>(v, a.p[i].residual + at);
-#pragma unroll
-        for (int k = 0; k < VEC; k += 4)
-            *reinterpret_cast<uint2 *>(a.p[i].out + at + k) =
-                make_uint2(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]));
-    }
-}
-
-// What is left of a call when its products are done, as one launch: the cut
-// tiles of up to two of them, and the last additions of the column sums, eight
-// columns a block and 32 threads a column.
-struct FinishArgs {
-    JoinArgs join[2];
-    int joins[2];   // blocks of each
-    ColumnSums cs;
-};
-__host__ __device__ inline int column_blocks(const ColumnSums &cs, int i) { return (cs.m[i].cols + 7) / 8; }
-// Partial rows of a column sum: 16 rows or more each, and not more than 98 (a
-// warp takes them eight at a time, some 12 us for 98) up to 2048 partial rows.
-int column_slices(int64_t rows)
-{
-    const int few = rows < 128 * 16 ? ceil_div(rows, 16) : 128, many = rows < 2048 * 98 ? ceil_div(rows, 98) : 2048;
-    return few > many ? few : many;
-}
-__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a)
-{
-    __shared__ float sum[32][8];
-    griddep_launch_dependents();
-    griddep_wait();
-    int b = blockIdx.x;
-    for (int i = 0; i < 2; ++i) {
-        if (b < a.joins[i]) {
-            if (a.join[i].blocks == 16) join_tiles<8>(a.join[i], b);
-            else join_tiles<4>(a.join[i], b);
-            return;
-        }
-        b -= a.joins[i];
-    }
-    int z = 0;
-    for (; z + 1 < a.cs.n && b >= column_blocks(a.cs, z); ++z) b -= column_blocks(a.cs, z);
-    const auto &m = a.cs.m[z];
-    const int k = threadIdx.x & 7, w = threadIdx.x >> 3, c = b * 8 + k;   // (cols is a multiple of 8)
-    float v = 0.f;
-#pragma unroll 8
-    for (int s = w; s < m.slices; s += 32) v += m.part[(int64_t)s * m.cols + c];
-    sum[w][k] = v;
-    __syncthreads();
-    if (threadIdx.x >= 8) return;
-#pragma unroll
-    for (int i = 1; i < 32; ++i) v += sum[i][k];
-    m.out[c] = __float2bfloat16_rn(v);
-}
-cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launches)
-{
-    int blocks = a.joins[0] + a.joins[1];
-    for (int i = 0; i < a.cs.n; ++i) blocks += column_blocks(a.cs, i);
-    if (!blocks) return cudaSuccess;
-    ++*launches;
-    return launch_maybe_overlapped(finish_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, 1, a);
-}
-struct ProductsPlan {
-    int n;
-    bool wide;            // 256-column tiles (else 128)
-    int wn;               // columns of a tile: 256, 192 or 128
-    PairSplit split;
-    size_t part_bytes;    // of the partial tiles
-};
-
-// Tiles of 256 x 256 where every product has more than 128 columns, else 256 x
-// 128.  The last round is cut along K where that saves more K blocks than the
-// join costs; few blocks in all go to as many pairs as leave each at least four.
-// A last round of at most half of the pairs goes out as half tiles where that
-// costs less than either: no join (1024 x 2048 x 5632 forward 61 us cut or whole,
-// 57 in halves; 12544 x 512 x 1368 backward, dx's last 22 tiles, 131 cut, 129; its
-// weight gradients' 36 tiles of 196 blocks stay cut: in halves 9 us more).
-ProductsPlan plan_products(const Product *p, int n)
-{
-    ProductsPlan pl{};
-    pl.n = n;
-    pl.wide = true;
-    for (int i = 0; i < n; ++i)
-        if (p[i].cols <= 128) pl.wide = false;
-    const int tn = pl.wn = pl.wide ? 256 : 128;
-    auto count = [&](int wn) {
-        int64_t tiles = 0;
-        for (int i = 0; i < n; ++i) tiles += (int64_t)ceil_div(p[i].rows, 256) * ceil_div(p[i].cols, wn);
-        return tiles;
-    };
-    int64_t tiles = count(tn);
-    PairSplit &s = pl.split;
-    s.tiles = (int)tiles;
-    s.k_blocks = s.kb = ceil_div(p[0].k[0], 64) + (p[0].k[1] ? ceil_div(p[0].k[1], 64) : 0);
-    const int pairs = sm_count() / 2;
-    s.np = (int)(tiles < pairs ? tiles : pairs);
-    const int full = (int)(tiles / pairs), rest = (int)(tiles - (int64_t)full * pairs);
-    const int64_t blocks = (int64_t)rest * s.kb;
-    int64_t np = full || blocks / 4 >= pairs ? pairs : blocks / 4 > rest ? blocks / 4 : rest;
-    const int cut_cost = ceil_div(blocks, np) + (pl.wide ? WIDE_JOIN : NARROW_JOIN), least = s.kb < cut_cost ? s.kb : cut_cost;
-    const bool halves = pl.wide && rest && 2 * rest <= pairs && (int64_t)half_cost(2 * rest, pairs) * s.kb <= 100ll * least;
-    const int64_t here = 100ll * full * s.kb + (halves ? (int64_t)half_cost(2 * rest, pairs) * s.kb : rest ? 100ll * least : 0);
-    const int64_t tiles192 = count(192);
-    if (pl.wide && (int64_t)ceil_div(tiles192, pairs) * COST_192 * s.kb < here) {
-        pl.wn = 192;
-        s.tiles = (int)tiles192;
-        s.np = (int)(tiles192 < pairs ? tiles192 : pairs);
-    } else if (halves) {
-        s.full = full;
-        s.halves = 2 * rest;
-        s.np = full ? pairs : s.halves;
-    } else if (rest && s.kb > cut_cost) {
-        // Equal slices of every tile, where they cost at most a tenth more blocks:
-        // pairs that share rows of an operand then walk K side by side, and each
-        // reads what another has brought into L2.  (36 tiles, the weight gradients
-        // of 44821 x 336 x 1288: the backward takes 330 us, 400 by even ranges.  A
-        // slice is longer than what rounding K up to equal slices adds, so that none
-        // is empty.)
-        const int slices = pairs / rest;
-        if (!full && slices > 1 && s.kb >= 16 * slices && s.kb >= slices * slices &&
-            (int64_t)ceil_div(s.kb, slices) * 10 <= (int64_t)ceil_div(blocks, np) * 11) {
-            np = rest * slices;
-            s.kb = ceil_div(s.kb, slices) * slices;
-        }
-        const int64_t all = (int64_t)rest * s.kb;
-        s.np = (int)np;
-        s.full = full;
-        s.cut = rest;
-        s.q = (uint32_t)(all / np);
-        s.r = (uint32_t)(all % np);
-        pl.part_bytes = (size_t)np * 2 * 256 * tn * sizeof(float);
-    }
-    return pl;
-}
-
-template <int TN, bool A_MN, bool B_MN>
-cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                              cudaStream_t stream, int *launches, FinishArgs *fin, int slot)
-{
-    typename GemmPolicy<TN, A_MN, B_MN>::Args a;
-    memset(&a, 0, sizeof(a));
-    JoinArgs &r = fin->join[slot];
-    cudaError_t e;
-    int first = 0;
-    for (int i = 0; i < 3; ++i) {
-        PairProblem &q = a.p[i];
-        q.first = r.p[i].first = INT_MAX;
-        if (i >= pl.n) continue;
-        const Product &p = ps[i];
-        q.rows = (int)p.rows;
-        q.cols = p.cols;
-        q.mt = ceil_div(p.rows, 256);
-        q.nt = ceil_div(p.cols, pl.wn);
-        q.first = first;
-        first += q.mt * q.nt;
-        q.bias = p.bias;
-        q.residual = p.residual;
-        r.p[i] = {p.bias, p.residual, p.d, q.rows, q.cols, q.mt, q.nt, q.first};
-        for (int s = 0; s < 2; ++s) {
-            q.k[s] = p.k[s];
-            q.kb[s] = p.k[s] ? ceil_div(p.k[s], 64) : 0;
-            if (!p.k[s]) continue;
-            e = A_MN ? map_mn(&q.a[s], p.a[s], p.k[s], (int)p.rows, p.lda)
-                     : map_k(&q.a[s], p.a[s], p.rows, p.k[s], 128, false, p.lda);
-            if (e != cudaSuccess) return e;
-            e = B_MN ? map_mn(&q.b[s], p.b[s], p.k[s], p.cols, p.ldb)
-                     : map_k(&q.b[s], p.b[s], p.cols, p.k[s], pl.wn / 2, false, p.ldb);
-            if (e != cudaSuccess) return e;
-            if (!B_MN && pl.split.halves) {
-                e = map_k(&q.b_half[s], p.b[s], p.cols, p.k[s], TN / 4, false, p.ldb);
-                if (e != cudaSuccess) return e;
-            }
-        }
-        if ((e = map_out(&q.d, p.d, p.rows, p.cols)) != cudaSuccess) return e;
-    }
-    a.split = r.split = pl.split;
-    if (A_MN) a.sums = fin->cs;
-    a.wn = pl.wn;
-    a.np = pl.split.np;
-    a.st = st;
-    if (pl.split.cut) {
-        e = make_tensor_map(&a.part, T_F32, part, TN, (int64_t)a.np * 2 * 256, TN * 4, 16, 32, 64);
-        if (e != cudaSuccess) return e;
-    }
-    ++*launches;
-    r.part = part;
-    r.tn = TN;
-    r.from_last = !A_MN;
-    r.blocks = pl.split.cut >= 16 ? 16 : 64;
-    fin->joins[slot] = pl.split.cut * r.blocks;
-    return launch_pair<GemmPolicy<TN, A_MN, B_MN>>(a, stream);
-}
-
-// Queues the products; what is left to do for their cut tiles goes into
-// fin->join[slot].
-template <bool A_MN, bool B_MN>
-cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot)
-{
-    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot)
-                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot);
-}
-
-// Workspace layout: bytes of each part, 1 KB aligned.
-struct Carve {
-    char *base;
-    size_t used = 0;
-    explicit Carve(void *p) : base((char *)p) {}
-    void *take(size_t bytes)
-    {
-        void *p = base + used;
-        used += (bytes + 1023) / 1024 * 1024;
-        return p;
-    }
-};
 
 // UpPolicy whose loads never come: a test of the bounded waits.
 struct StallPolicy : UpPolicy<ACT_SILU, false> {

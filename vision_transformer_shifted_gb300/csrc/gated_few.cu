@@ -1,4 +1,5 @@
-// The gated block's forward for few rows (single tokens, small batches), where
+// The gated block's forward and the linear operator's for few rows (single
+// tokens, small batches), where
 // the weights' one trip from HBM is the work: each product with the weights as
 // the MMA's A operand (128 weight rows) and the rows of x as its narrow B (16 to
 // 128 columns), so that no row of the tensor-core tile is idle weight traffic.
@@ -21,15 +22,19 @@ namespace swin {
 namespace {
 
 constexpr int FEW_THREADS = 192;   // four draining warps, a loading and an issuing one
-constexpr int ACT_NONE = -1;
+// What a launch computes: the gated block's first products with the activation
+// (FORM_UP + ACT_*), its last product, or the linear operator.
+enum { FORM_UP = 0, FORM_DOWN = -1, FORM_LINEAR = -2 };
 constexpr int FEW_MAX_STAGES = 6;
 
 struct FewArgs {
-    CUtensorMap w0, w1, x;         // ACT: Wg, Wu (boxes of 64 rows); else Wd (128 rows); x: np rows
-    const bf16 *b0, *b1;           // ACT: bg, bu; else bd
-    const float *sx, *s0, *s1;     // 8-bit: scales of x, Wg, Wu
+    CUtensorMap w0, w1, x;         // up: Wg, Wu (boxes of 64 rows); else Wd or W (128 rows); x: np rows
+    const bf16 *b0, *b1;           // up: bg, bu; else bd or b
+    const float *sx, *s0, *s1;     // 8-bit: scales of x, Wg (W), Wu
     const bf16 *residual;
-    bf16 *out;                     // [rows, ld]: h, or the block's output
+    bf16 *out;                     // [rows, ld]: h, or the output
+    bf16 *z;                       // linear: as out, the value before the activation, or null
+    int act;                       // linear: ACT_*
     int rows, np;                  // np: rows rounded up to 16
     int cols, ld;                  // columns of out
     int k, kb, split, stages, stage_bytes;
@@ -72,12 +77,12 @@ __device__ __forceinline__ void mma_one(uint32_t d, uint64_t adesc, uint64_t bde
             : "memory");
 }
 
-template <int ACT, bool Q8>
+template <int FORM, bool Q8>
 __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_constant__ FewArgs a)
 {
     constexpr int ELEMS = Q8 ? 128 : 64;            // K elements of a block
-    constexpr int W = ACT == ACT_NONE ? 128 : 64;   // output columns of a tile
-    constexpr bool EARLY = ACT == ACT_NONE;
+    constexpr int W = FORM < FORM_UP ? 128 : 64;   // output columns of a tile
+    constexpr bool EARLY = FORM == FORM_DOWN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_align(smem_raw, 1024);
     __shared__ uint64_t bars[2 * FEW_MAX_STAGES + 1];
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     if (warp == 4 && elect_one()) {
         prefetch_map(&a.w0);
         prefetch_map(&a.x);
-        if (ACT != ACT_NONE) prefetch_map(&a.w1);
+        if (FORM >= FORM_UP) prefetch_map(&a.w1);
     }
     tc_fence_before();
     __syncthreads();
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
         int s = 0;
         uint32_t ph = 0;
         auto load_w = [&](int kb, uint32_t dst, uint32_t bar) {
-            if (ACT == ACT_NONE) {
+            if (FORM < FORM_UP) {
                 tma_load_2d(dst, &a.w0, kb * ELEMS, tile * 128, bar);
             } else {
                 tma_load_2d(dst, &a.w0, kb * ELEMS, tile * 64, bar);
@@ -228,22 +233,36 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
         for (int r = 0; r < split; ++r) {
             const uint32_t at = map_rank(base + (uint32_t)(t * 128 + i) * 4, r);
             add4(v, ld_cluster(at));
-            if (ACT != ACT_NONE) add4(u, ld_cluster(at + 64 * 4));
+            if (FORM >= FORM_UP) add4(u, ld_cluster(at + 64 * 4));
         }
         if (Q8) {
             const float sx = a.sx[t];
-            const float4 p = *reinterpret_cast<const float4 *>(a.s0 + c), q = *reinterpret_cast<const float4 *>(a.s1 + c);
+            const float4 p = *reinterpret_cast<const float4 *>(a.s0 + c);
             v[0] *= sx * p.x; v[1] *= sx * p.y; v[2] *= sx * p.z; v[3] *= sx * p.w;
-            u[0] *= sx * q.x; u[1] *= sx * q.y; u[2] *= sx * q.z; u[3] *= sx * q.w;
+            if (FORM >= FORM_UP) {
+                const float4 q = *reinterpret_cast<const float4 *>(a.s1 + c);
+                u[0] *= sx * q.x; u[1] *= sx * q.y; u[2] *= sx * q.z; u[3] *= sx * q.w;
+            }
         }
         if (a.b0) add4(v, a.b0 + c);
-        if (ACT == ACT_NONE) {
+        if (FORM == FORM_LINEAR) {
+            if (a.z)
+                *reinterpret_cast<uint2 *>(a.z + (int64_t)t * a.ld + c) =
+                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const f2 g = pack2(v[k], v[k + 1]);
+                unpack2(a.act == ACT_SILU ? activate2<ACT_SILU>(g) : a.act == ACT_GELU ? activate2<ACT_GELU>(g) : g, v[k],
+                        v[k + 1]);
+            }
+        }
+        if (FORM < FORM_UP) {
             if (a.residual) add4(v, a.residual + (int64_t)t * a.ld + c);
         } else {
             if (a.b1) add4(u, a.b1 + c);
 #pragma unroll
             for (int k = 0; k < 4; k += 2)
-                unpack2(mul2(activate2<ACT>(pack2(v[k], v[k + 1])), pack2(u[k], u[k + 1])), v[k], v[k + 1]);
+                unpack2(mul2(activate2<(FORM < FORM_UP ? ACT_NONE : FORM)>(pack2(v[k], v[k + 1])), pack2(u[k], u[k + 1])), v[k], v[k + 1]);
         }
         *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ld + c) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
@@ -252,10 +271,10 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     if (warp == 5) tmem_dealloc(tmem, tcols);
 }
 
-template <int ACT, bool Q8>
+template <int FORM, bool Q8>
 cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
 {
-    constexpr int W = ACT == ACT_NONE ? 128 : 64;
+    constexpr int W = FORM < FORM_UP ? 128 : 64;
     a.kb = (a.k + (Q8 ? 127 : 63)) / (Q8 ? 128 : 64);
     // CTAs a tile: until there is one for every SM, with two K blocks each at least
     const int tiles = (width + W - 1) / W;
@@ -272,7 +291,7 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
-        e = cudaFuncSetAttribute(few_rows_kernel<ACT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 111 * 1024);
+        e = cudaFuncSetAttribute(few_rows_kernel<FORM, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 111 * 1024);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }
@@ -289,7 +308,7 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, few_rows_kernel<ACT, Q8>, a);
+    return cudaLaunchKernelEx(&cfg, few_rows_kernel<FORM, Q8>, a);
 }
 
 } // namespace
@@ -316,8 +335,8 @@ cudaError_t launch_few_up(const FewUp &u, DeviceStatus st, cudaStream_t stream)
     a.ld = u.ldh;
     a.k = u.C;
     a.st = st;
-    if (u.gelu) return u.sx ? launch_few<ACT_GELU, true>(a, u.F, stream) : launch_few<ACT_GELU, false>(a, u.F, stream);
-    return u.sx ? launch_few<ACT_SILU, true>(a, u.F, stream) : launch_few<ACT_SILU, false>(a, u.F, stream);
+    if (u.gelu) return u.sx ? launch_few<FORM_UP + ACT_GELU, true>(a, u.F, stream) : launch_few<FORM_UP + ACT_GELU, false>(a, u.F, stream);
+    return u.sx ? launch_few<FORM_UP + ACT_SILU, true>(a, u.F, stream) : launch_few<FORM_UP + ACT_SILU, false>(a, u.F, stream);
 }
 
 cudaError_t launch_few_down(const bf16 *h, int ldh, int rows, const bf16 *wd, const bf16 *bd, const bf16 *residual,
@@ -337,7 +356,31 @@ cudaError_t launch_few_down(const bf16 *h, int ldh, int rows, const bf16 *wd, co
     a.cols = a.ld = C;
     a.k = F;
     a.st = st;
-    return launch_few<ACT_NONE, false>(a, C, stream);
+    return launch_few<FORM_DOWN, false>(a, C, stream);
+}
+
+cudaError_t launch_few_linear(const FewLinear &u, DeviceStatus st, cudaStream_t stream)
+{
+    FewArgs a;
+    memset(&a, 0, sizeof(a));
+    const int e8 = u.sx ? 1 : 2;
+    const CUtensorMapDataType type = u.sx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    a.rows = u.rows;
+    a.np = (u.rows + 15) / 16 * 16;
+    cudaError_t e;
+    if ((e = make_tensor_map(&a.w0, type, u.w, u.C, u.N, (int64_t)u.C * e8, 128 / e8, 128, 128)) != cudaSuccess) return e;
+    if ((e = make_tensor_map(&a.x, type, u.x, u.C, u.rows, (int64_t)u.C * e8, 128 / e8, a.np, 128)) != cudaSuccess) return e;
+    a.b0 = u.bias;
+    a.sx = u.sx;
+    a.s0 = u.sw;
+    a.residual = u.residual;
+    a.out = u.out;
+    a.z = u.z;
+    a.act = u.act;
+    a.cols = a.ld = u.N;
+    a.k = u.C;
+    a.st = st;
+    return u.sx ? launch_few<FORM_LINEAR, true>(a, u.N, stream) : launch_few<FORM_LINEAR, false>(a, u.N, stream);
 }
 
 } // namespace swin

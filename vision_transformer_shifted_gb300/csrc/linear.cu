@@ -1,0 +1,452 @@
+// The linear operator: C ABI, launches, and the kernel of an activation's
+// gradient.
+//   forward   out = residual + act(x W^T + b)      (one kernel; linear.cuh, or for
+//             few rows gated_few.cu; a second joins tiles cut along K)
+//   backward  dz = dy act'(z) with its column sums (one kernel, where there is an
+//             activation), dx = dz W, dW = dz^T x, and the sums' last additions
+#include <climits>
+#include <cstring>
+#include <new>
+
+#include "swin_linear.h"
+#include "swin_wattn_test.h"
+#include "linear.cuh"
+
+using namespace swin;
+
+struct swin_block_linear_s {
+    int C, N, act;   // act: ACT_*
+    int device;      // -1: created without one
+    int *d_err;
+    int last_launches;
+    OrderedWorkspace ws;
+};
+
+namespace {
+
+constexpr int MAX_WIDTH = 65536;
+constexpr int MAX_ROWS = INT_MAX - 512;   // row coordinates of the last tile stay below 2^31
+constexpr uint64_t WAIT_NS = 2000000000ull;
+
+bool bad_pointer(const void *p, bool required)
+{
+    return p ? (reinterpret_cast<uintptr_t>(p) & 15u) != 0 : required;
+}
+
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+bool any_overlap(Span o, std::initializer_list<Span> in)
+{
+    if (!o.p) return false;
+    for (const Span &s : in)
+        if (s.p && overlaps(o.p, o.bytes, s.p, s.bytes)) return true;
+    return false;
+}
+
+// The handle's device is the current one.
+int check_device(const swin_block_linear_s *h)
+{
+    int dev = h->device;
+    if (dev < 0) return SWIN_WATTN_ECUDA;
+    return bind_device(&dev);
+}
+
+// ---- forward -----------------------------------------------------------------------
+
+struct Forward {
+    const void *x, *w;
+    const float *sx, *sw;   // 8-bit form, else null
+    const bf16 *bias, *residual;
+    bf16 *z, *out;
+    int rows;
+};
+constexpr int elems(bool q8) { return q8 ? 128 : 64; }
+Product forward_product(int C, int N, int rows)
+{
+    Product p{};
+    p.k[0] = C;
+    p.rows = rows;
+    p.cols = N;
+    return p;
+}
+
+template <int ACT, bool Q8>
+cudaError_t launch_linear(const Forward &f, int C, int N, const ProductsPlan &pl, float *part, DeviceStatus st,
+                          cudaStream_t stream, FinishArgs *fin)
+{
+    using P = LinearPolicy<ACT, Q8>;
+    typename P::Args a;
+    memset(&a, 0, sizeof(a));
+    cudaError_t e;
+    if ((e = map_k(&a.x, f.x, f.rows, C, 128, Q8)) != cudaSuccess) return e;
+    if ((e = map_k(&a.w, f.w, N, C, pl.wn / 2, Q8)) != cudaSuccess) return e;
+    if (pl.split.halves && (e = map_k(&a.w_half, f.w, N, C, pl.wn / 4, Q8)) != cudaSuccess) return e;
+    if ((e = map_out(&a.out, f.out, f.rows, N)) != cudaSuccess) return e;
+    if (f.z && (e = map_out(&a.z, f.z, f.rows, N)) != cudaSuccess) return e;
+    a.split = pl.split;
+    a.bias = f.bias;
+    a.residual = f.residual;
+    a.sx = f.sx;
+    a.sw = f.sw;
+    a.rows = f.rows;
+    a.cols = N;
+    a.k = C;
+    a.mt = ceil_div(f.rows, 256);
+    a.nt = ceil_div(N, pl.wn);
+    a.wn = pl.wn;
+    a.np = pl.split.np;
+    a.keep = f.z != nullptr;
+    a.st = st;
+    if (pl.split.cut) {
+        e = make_tensor_map(&a.part, T_F32, part, pl.wn, (int64_t)a.np * 2 * 256, (int64_t)pl.wn * 4, 16, 32, 64);
+        if (e != cudaSuccess) return e;
+        JoinArgs &j = fin->join[0];
+        j.part = part;
+        j.split = pl.split;
+        j.tn = pl.wn;
+        j.blocks = pl.split.cut >= 16 ? 16 : 64;
+        j.linear = {true, ACT, f.sx, f.sw, f.z};
+        j.p[0] = {f.bias, f.residual, f.out, f.rows, N, a.mt, a.nt, 0};
+        j.p[1].first = j.p[2].first = INT_MAX;
+        fin->joins[0] = pl.split.cut * j.blocks;
+    }
+    return launch_pair<P>(a, stream);
+}
+
+int forward(swin_block_linear_s *h, const Forward &f, cudaStream_t stream)
+{
+    int rc = check_device(h);
+    if (rc != SWIN_WATTN_OK) return rc;
+    const DeviceStatus st{h->d_err, WAIT_NS};
+    const bool q8 = f.sx != nullptr;
+    if (f.rows <= FEW_ROWS) {
+        h->last_launches = 1;
+        const FewLinear u{f.x, f.w, f.bias, f.residual, f.sx, f.sw, f.out, f.z, f.rows, h->C, h->N, h->act};
+        return launch_few_linear(u, st, stream) == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA;
+    }
+    const Product p = forward_product(h->C, h->N, f.rows);
+    const ProductsPlan pl = plan_products(&p, 1, elems(q8));
+    void *ws = nullptr;
+    bool captured = false;
+    if (pl.part_bytes && (rc = ows_begin(&h->ws, pl.part_bytes, stream, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    FinishArgs fin{};
+    auto run = [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        return q8 ? launch_linear<A, true>(f, h->C, h->N, pl, (float *)ws, st, stream, &fin)
+                  : launch_linear<A, false>(f, h->C, h->N, pl, (float *)ws, st, stream, &fin);
+    };
+    h->last_launches = 1;
+    cudaError_t e = h->act == ACT_SILU   ? run(std::integral_constant<int, ACT_SILU>{})
+                    : h->act == ACT_GELU ? run(std::integral_constant<int, ACT_GELU>{})
+                                         : run(std::integral_constant<int, ACT_NONE>{});
+    if (e == cudaSuccess) e = launch_finish(fin, stream, &h->last_launches);
+    const int rc2 = ows_end(&h->ws, stream, ws, captured);
+    return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
+}
+
+// ---- dz = dy act'(z) ------------------------------------------------------------------
+//
+// Elementwise, HBM (or, from a layer just run, L2) bounds it.  A thread takes
+// eight columns and every rows_at_once * slices-th row, four rows of loads in
+// flight, and adds up its columns of the unrounded dz; a block's sums are a
+// partial row.
+struct GradArgs {
+    const bf16 *z, *dy;
+    bf16 *dz;
+    float *part;   // [slices, N], or null
+    int64_t rows;
+    int N, ld;     // ld: of dz
+    int across, at_once, slices;   // threads across a row (of eight columns each), rows a block takes at once
+};
+template <int ACT>
+__global__ void __launch_bounds__(256) act_grad_kernel(const GradArgs a)
+{
+    __shared__ float sums[256][9];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int t = (int)threadIdx.x % a.across, r = (int)threadIdx.x / a.across;
+    const int c = ((int)blockIdx.x * a.across + t) * 8;
+    const bool on = r < a.at_once && c < a.N;
+    f2 sum[4] = {0, 0, 0, 0};
+    if (on) {
+        const int64_t step = (int64_t)a.at_once * a.slices;
+        auto grad = [&](int64_t row, const uint4 &zu, const uint4 &du) {
+            const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w}, dw[4] = {du.x, du.y, du.z, du.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 zf = unpack_bf16x2(zw[e]), df = unpack_bf16x2(dw[e]);
+                f2 act, slope;
+                activate_grad2<ACT>(pack2(zf.x, zf.y), act, slope);
+                const f2 v = mul2(pack2(df.x, df.y), slope);
+                sum[e] = add2(sum[e], v);
+                float lo, hi;
+                unpack2(v, lo, hi);
+                o[e] = pack_bf16x2(lo, hi);
+            }
+            *reinterpret_cast<uint4 *>(a.dz + row * a.ld + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        };
+        int64_t row = (int64_t)blockIdx.y * a.at_once + r;
+#pragma unroll 1
+        for (; row + 3 * step < a.rows; row += 4 * step) {
+            uint4 z[4], d[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                z[k] = *reinterpret_cast<const uint4 *>(a.z + (row + k * step) * a.N + c);
+                d[k] = *reinterpret_cast<const uint4 *>(a.dy + (row + k * step) * a.N + c);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) grad(row + k * step, z[k], d[k]);
+        }
+#pragma unroll 1
+        for (; row < a.rows; row += step)
+            grad(row, *reinterpret_cast<const uint4 *>(a.z + row * a.N + c),
+                 *reinterpret_cast<const uint4 *>(a.dy + row * a.N + c));
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) unpack2(sum[e], sums[threadIdx.x][2 * e], sums[threadIdx.x][2 * e + 1]);
+    __syncthreads();
+    if (r > 0 || !on) return;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = sums[t][e];
+    for (int i = 1; i < a.at_once; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += sums[i * a.across + t][e];
+    float *out = a.part + (int64_t)blockIdx.y * a.N + c;
+    *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+// Threads across a row: all of its pieces where a block holds them, else even
+// shares; rows: about six blocks an SM in all, at least four rows a thread.
+struct GradPlan {
+    int across, at_once, columns, slices;   // columns: blocks across a row
+};
+GradPlan plan_grad(int N, int64_t rows)
+{
+    GradPlan p{};
+    const int pieces = N / 8;
+    p.columns = ceil_div(pieces, 256);
+    p.across = ceil_div(pieces, p.columns);
+    p.at_once = 256 / p.across;
+    const int64_t most = ceil_div(6 * sm_count(), p.columns), want = ceil_div(rows, 4 * (int64_t)p.at_once);
+    p.slices = (int)(want < most ? want : most);
+    return p;
+}
+
+// The shapes of the backward's products.
+Product dx_product(int C, int N, int rows, int ld)
+{
+    Product p{};
+    p.k[0] = N;
+    p.lda = ld;
+    p.rows = rows;
+    p.cols = C;
+    return p;
+}
+Product weight_product(int C, int N, int rows, int ld)
+{
+    Product p{};
+    p.k[0] = rows;
+    p.lda = ld;
+    p.rows = N;
+    p.cols = C;
+    return p;
+}
+
+} // namespace
+
+extern "C" {
+
+int swin_block_linear_create(swin_block_linear_t *out, int C, int N, int act)
+{
+    if (!out) return SWIN_WATTN_EINVAL;
+    *out = nullptr;
+    if (C <= 0 || C % 8 || C > MAX_WIDTH || N <= 0 || N % 8 || N > MAX_WIDTH) return SWIN_WATTN_EINVAL;
+    if (act != SWIN_BLOCK_LINEAR_NONE && act != SWIN_BLOCK_LINEAR_SILU && act != SWIN_BLOCK_LINEAR_GELU)
+        return SWIN_WATTN_EINVAL;
+    swin_block_linear_s *h = new (std::nothrow) swin_block_linear_s{};
+    if (!h) return SWIN_WATTN_ENOMEM;
+    h->C = C;
+    h->N = N;
+    h->act = act == SWIN_BLOCK_LINEAR_SILU ? ACT_SILU : act == SWIN_BLOCK_LINEAR_GELU ? ACT_GELU : ACT_NONE;
+    h->device = -1;
+    if (bind_device(&h->device) != SWIN_WATTN_OK) h->device = -1;
+    if (h->device >= 0 &&
+        (cudaMalloc(&h->d_err, sizeof(int)) != cudaSuccess || cudaMemset(h->d_err, 0, sizeof(int)) != cudaSuccess)) {
+        cudaGetLastError();
+        if (h->d_err) cudaFree(h->d_err);
+        delete h;
+        return SWIN_WATTN_ENOMEM;
+    }
+    *out = h;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_linear_destroy(swin_block_linear_t h)
+{
+    if (!h) return SWIN_WATTN_OK;
+    if (h->d_err) {
+        cudaDeviceSynchronize();
+        cudaFree(h->d_err);
+    }
+    ows_free(&h->ws);
+    delete h;
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_linear_last_launches(swin_block_linear_t h) { return h ? h->last_launches : 0; }
+
+int swin_block_linear_sync_status(swin_block_linear_t h, swin_stream_t stream)
+{
+    if (!h) return SWIN_WATTN_EINVAL;
+    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    if (!h->d_err) return SWIN_WATTN_OK;
+    int err = 0;
+    if (cudaMemcpy(&err, h->d_err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    if (!err) return SWIN_WATTN_OK;
+    if (cudaMemset(h->d_err, 0, sizeof(int)) != cudaSuccess) return SWIN_WATTN_ECUDA;
+    return SWIN_WATTN_ETIMEOUT;
+}
+
+int swin_block_linear_forward(swin_block_linear_t h, const void *x, int rows, const void *W, const void *b,
+                              const void *residual, void *z, void *out, swin_stream_t stream)
+{
+    if (!h || rows < 0 || rows > MAX_ROWS || (z && h->act == ACT_NONE)) return SWIN_WATTN_EINVAL;
+    if (rows == 0) return SWIN_WATTN_OK;   // (an empty tensor may have no address)
+    for (const void *q : {x, W, (const void *)out})
+        if (bad_pointer(q, true)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {b, residual, (const void *)z})
+        if (bad_pointer(q, false)) return SWIN_WATTN_EINVAL;
+    const int64_t in = 2 * (int64_t)rows * h->C, on = 2 * (int64_t)rows * h->N, w = 2 * (int64_t)h->C * h->N, v = 2 * (int64_t)h->N;
+    if (any_overlap({out, on}, {{x, in}, {W, w}, {b, v}, {z, on}, {residual == out ? nullptr : residual, on}}) ||
+        any_overlap({z, on}, {{x, in}, {W, w}, {b, v}, {residual, on}}))
+        return SWIN_WATTN_EINVAL;
+    return forward(h, {x, W, nullptr, nullptr, (const bf16 *)b, (const bf16 *)residual, (bf16 *)z, (bf16 *)out, rows},
+                   (cudaStream_t)stream);
+}
+
+int swin_block_linear_forward_q8(swin_block_linear_t h, const void *x8, const float *sx, int rows, const void *W8,
+                                 const float *sw, const void *b, const void *residual, void *out, swin_stream_t stream)
+{
+    if (!h || rows < 0 || rows > MAX_ROWS) return SWIN_WATTN_EINVAL;
+    if (h->C % 16) return SWIN_WATTN_EUNSUPPORTED;
+    if (rows == 0) return SWIN_WATTN_OK;
+    for (const void *q : {x8, (const void *)sx, W8, (const void *)sw, (const void *)out})
+        if (bad_pointer(q, true)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {b, residual})
+        if (bad_pointer(q, false)) return SWIN_WATTN_EINVAL;
+    const int64_t in = (int64_t)rows * h->C, on = 2 * (int64_t)rows * h->N, w = (int64_t)h->C * h->N, v = 2 * (int64_t)h->N;
+    if (any_overlap({out, on}, {{x8, in}, {sx, 4 * (int64_t)rows}, {W8, w}, {sw, 2 * v}, {b, v},
+                                {residual == out ? nullptr : residual, on}}))
+        return SWIN_WATTN_EINVAL;
+    return forward(h, {x8, W8, sx, sw, (const bf16 *)b, (const bf16 *)residual, nullptr, (bf16 *)out, rows},
+                   (cudaStream_t)stream);
+}
+
+int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, const void *W, const void *z,
+                               const void *dy, void *dx, void *dW, void *db, swin_stream_t stream)
+{
+    if (!h || rows < 0 || rows > MAX_ROWS || (!dx && !dW) || (db && !dW) || (z && h->act == ACT_NONE))
+        return SWIN_WATTN_EINVAL;
+    const bool act = h->act != ACT_NONE;
+    const int64_t in = 2 * (int64_t)rows * h->C, on = 2 * (int64_t)rows * h->N, w = 2 * (int64_t)h->C * h->N, v = 2 * (int64_t)h->N;
+    for (const void *q : {x, dy})
+        if (bad_pointer(q, rows > 0)) return SWIN_WATTN_EINVAL;
+    if (bad_pointer(z, act && rows > 0) || bad_pointer(W, true)) return SWIN_WATTN_EINVAL;
+    for (const void *q : {dx, dW, db})
+        if (bad_pointer(q, false)) return SWIN_WATTN_EINVAL;
+    const Span outs[] = {{dx, in}, {dW, w}, {db, v}};
+    for (int i = 0; i < 3; ++i) {
+        if (any_overlap(outs[i], {{x, in}, {W, w}, {z, on}, {dy, on}})) return SWIN_WATTN_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (any_overlap(outs[i], {outs[j]})) return SWIN_WATTN_EINVAL;
+    }
+    int rc = check_device(h);
+    if (rc != SWIN_WATTN_OK) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (rows == 0) {
+        for (int i = 1; i < 3; ++i)
+            if (outs[i].p && cudaMemsetAsync(const_cast<void *>(outs[i].p), 0, outs[i].bytes, s) != cudaSuccess)
+                return SWIN_WATTN_ECUDA;
+        return SWIN_WATTN_OK;
+    }
+    const int ld = act ? hidden_ld(h->N) : h->N;
+    Product px = dx_product(h->C, h->N, rows, ld), pw = weight_product(h->C, h->N, rows, ld);
+    const ProductsPlan plx = dx ? plan_products(&px, 1) : ProductsPlan{}, plw = dW ? plan_products(&pw, 1) : ProductsPlan{};
+    const GradPlan pg = plan_grad(h->N, rows);
+    FinishArgs fin{};
+    size_t sum_bytes = 0;
+    if (db) {
+        // from dz's kernel, or (dz is dy) by the weight gradient's waiting warps
+        auto &m = fin.cs.m[fin.cs.n++];
+        m.out = (bf16 *)db;
+        m.b = act ? nullptr : (const bf16 *)dy;
+        m.rows = rows;
+        m.cols = h->N;
+        m.slices = act ? pg.slices : column_slices(rows);
+        m.tasks = act ? 0 : ceil_div(h->N, 256) * m.slices;
+        sum_bytes = (size_t)m.slices * h->N * sizeof(float);
+    }
+    Carve size(nullptr);
+    size.take(act ? (size_t)rows * ld * 2 : 0);
+    size.take(plx.part_bytes);
+    size.take(plw.part_bytes);
+    size.take(sum_bytes);
+    void *ws = nullptr;
+    bool captured = false;
+    if (size.used && (rc = ows_begin(&h->ws, size.used, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
+    Carve carve(ws);
+    bf16 *dz = (bf16 *)carve.take(act ? (size_t)rows * ld * 2 : 0);
+    float *x_part = (float *)carve.take(plx.part_bytes), *w_part = (float *)carve.take(plw.part_bytes);
+    float *sum_part = (float *)carve.take(sum_bytes);
+    if (db) fin.cs.m[0].part = sum_part;
+    px.a[0] = pw.a[0] = act ? (const void *)dz : dy;
+    px.b[0] = W;
+    px.d = (bf16 *)dx;
+    pw.b[0] = x;
+    pw.d = (bf16 *)dW;
+    const DeviceStatus st{h->d_err, WAIT_NS};
+    h->last_launches = 0;
+    cudaError_t e = cudaSuccess;
+    if (act) {
+        const GradArgs a{(const bf16 *)z, (const bf16 *)dy, dz, db ? sum_part : nullptr, rows, h->N, ld, pg.across, pg.at_once,
+                         pg.slices};
+        ++h->last_launches;
+        e = launch_maybe_overlapped(h->act == ACT_SILU ? act_grad_kernel<ACT_SILU> : act_grad_kernel<ACT_GELU>,
+                                    dim3((unsigned)pg.columns, (unsigned)pg.slices), dim3(256), 0, s, 1, a);
+    }
+    if (e == cudaSuccess && dx) e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0);
+    if (e == cudaSuccess && dW) e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
+    if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
+    const int rc2 = ows_end(&h->ws, s, ws, captured);
+    return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
+}
+
+// ---- test hooks (swin_wattn_test.h) ------------------------------------------------
+
+int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan)
+{
+    if (C <= 0 || C % 8 || C > MAX_WIDTH || N <= 0 || N % 8 || N > MAX_WIDTH || rows <= 0 || rows > MAX_ROWS || !plan)
+        return SWIN_WATTN_EINVAL;
+    Product p;
+    if (which == SWIN_BLOCK_LINEAR_PLAN_FORWARD || which == SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8) p = forward_product(C, N, rows);
+    else if (which == SWIN_BLOCK_LINEAR_PLAN_DX) p = dx_product(C, N, rows, N);
+    else if (which == SWIN_BLOCK_LINEAR_PLAN_WEIGHT) p = weight_product(C, N, rows, N);
+    else return SWIN_WATTN_EINVAL;
+    const ProductsPlan pl = plan_products(&p, 1, elems(which == SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8));
+    const int v[] = {pl.split.tiles, pl.split.np, pl.wn, pl.split.halves, pl.split.cut, pl.split.kb != pl.split.k_blocks};
+    memcpy(plan, v, sizeof(v));
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_linear_test_corrupt_workspace(swin_block_linear_t h, int side)
+{
+    if (!h || side < 0 || side > 1) return SWIN_WATTN_EINVAL;
+    return ws_test_corrupt(h->ws.buf, side);
+}
+
+} // extern "C"
