@@ -3,13 +3,18 @@
 // one scale a row, or added to the residual (post-norm); backward.
 //
 // As the root-mean-square norm (rms.cu): every input is read once and every
-// output written once, the row stays in registers (the wide backward: shared
-// memory) between the statistics and the output, and HBM bounds it.  The
-// statistics take two sums a row one after the other, the mean and then the
-// squared deviations from it: sum s^2 - C mu^2 would lose what a row's mean has
-// above its spread, and a row of one large value would not come out as zeros.
-// The second sum also yields the deviations' own mean, what the first one's
-// rounding left.
+// output written once, the row stays in registers (the backward: shared memory)
+// between the statistics and the output, and HBM bounds it: 200704 x 96 with the
+// residual 23.7 us, 6.5 TB/s; post-norm 589824 x 192 103.7 us, 6.55 TB/s; e4m3
+// 8191 x 4096 39 us, 6.0 TB/s; backward 589824 x 192 with dsum 140 us, 6.45 TB/s
+// (57% of the issue slots).  The
+// statistics are one sum a row, of s - p and of its square, p being the mean of
+// the row's first eight values: sum s^2 - C mu^2 (p = 0) would lose what a row's
+// mean has above its spread; of values around p the variance keeps all but
+// log2(1 + k^2) of fp32's bits, p lying k standard deviations from the mean (k^2 is
+// C / 8 at most, whatever the row holds, and some 0.1 as a rule), and a row of one
+// value gives exact zeros.  (Two sums one after the other, the mean first: e4m3
+// 8191 x 4096 43.0 us, backward 589824 x 192 151.)
 #include <cmath>
 #include <new>
 
@@ -32,8 +37,7 @@ struct LnArgs {
     int lpr;         // lanes per row (rows on part of a warp)
 };
 
-// The sums of a and b over a row's lanes (a block: red holds a pair a warp; the
-// next sum takes another red, so that one barrier a sum is enough).
+// The sums of a and b over a row's lanes (a block: red holds a pair a warp).
 template <bool BLOCK>
 __device__ __forceinline__ void row_sum2(float &a, float &b, int lpr, float2 *red)
 {
@@ -49,18 +53,25 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, int lpr, float2 *re
     }
 }
 
-// 1 / sqrt(var + eps) from the sums of the deviations from nearly the mean and of
-// their squares; mean: the deviations' own.
+// The sum of a piece's eight values.
+__device__ __forceinline__ float piece_sum(const Piece &v) { return sum2(add2(add2(v.v[0], v.v[1]), add2(v.v[2], v.v[3]))); }
+
+// 1 / sqrt(var + eps) from the row's sums of s - p and of its square; mean: of s - p.
 __device__ __forceinline__ float deviation(float sum, float squares, float inv_c, float eps, float &mean)
 {
     mean = sum * inv_c;
     return rsqrtf(max_nan(fmaf(-mean, mean, squares * inv_c), 0.f) + eps);   // (infinite squares: r = 0)
 }
 
+// (Blocks of a row: registers for two of 512 threads an SM, more in flight: post-norm
+// 20000 x 6000 117 us, 204 without.  Rows on part of a warp: no such request, the
+// compiler's own count; asked for one block it takes up to 9 registers more, post-norm
+// 200000 x 512 93.7 us and 104.)
 template <int CPL, bool BLOCK, int FORM>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256) layernorm_forward_kernel(LnArgs a)
+__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_forward_kernel(LnArgs a)
 {
-    __shared__ float2 red[2][16];
+    __shared__ float2 red[16];
+    __shared__ float amaxes[16];
     griddep_launch_dependents();
     griddep_wait();   // (nothing is read before the kernels queued earlier are done)
     const int lane = threadIdx.x & 31;
@@ -71,29 +82,61 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) layernorm_forward_kernel(Ln
                                     lane / a.lpr;
     const bool row_ok = row < a.rows;
     const int64_t base = row * a.chunks * 8;
+    // post-norm: the residual, used last, by asynchronous copies into the thread's
+    // own places (as plain loads the compiler puts them off until they are used:
+    // 589824 x 192 113 us)
+    extern __shared__ uint4 later[];   // a block's row: [CPL][blockDim.x]
+    __shared__ uint4 later256[FORM == FORM_POST && !BLOCK ? CPL * 256 : 1];
+    const uint32_t own = smem_u32(BLOCK ? later : later256) + threadIdx.x * 16;
+    const uint32_t own_step = (BLOCK ? blockDim.x : 256) * 16;
     uint4 s[CPL], t[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
         const int c = li + k * step;
         const bool ok = row_ok && c < a.chunks;
         s[k] = ok ? ld16(a.x + base + c * 8) : make_uint4(0, 0, 0, 0);
-        if (FORM == FORM_POST || a.residual) t[k] = ok ? ld16(a.residual + base + c * 8) : make_uint4(0, 0, 0, 0);
+        if (FORM == FORM_POST) {
+            if (ok) cp_async16(own + k * own_step, a.residual + base + c * 8, 16);
+        } else if (a.residual) {
+            t[k] = ok ? ld16(a.residual + base + c * 8) : make_uint4(0, 0, 0, 0);
+        }
     }
-    f2 sum2v = 0;
+    // the stored (rounded) sum is what the norm sees
+    auto stored = [&](const uint4 &x, const uint4 &res) {
+        Piece v = piece(x);
+        const Piece w = piece(res);
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) {
-        const int c = li + k * step;
-        Piece v = piece(s[k]);
-        if (FORM != FORM_POST && a.residual) {
-            const Piece w = piece(t[k]);
+        for (int e = 0; e < 4; ++e) v.v[e] = add2(v.v[e], w.v[e]);
+        return pack(v);
+    };
+    const bool add = FORM != FORM_POST && a.residual;
+    uint4 head = make_uint4(0, 0, 0, 0);   // the row's first piece (a block: read by every thread)
+    if (BLOCK) {
+        head = ld16(a.x + base);
+        if (add) head = stored(head, ld16(a.residual + base));
+    }
+    if (add) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v.v[e] = add2(v.v[e], w.v[e]);
-            s[k] = pack(v);
-            v = piece(s[k]);   // the stored (rounded) sum is what the norm sees
+        for (int k = 0; k < CPL; ++k) {
+            const int c = li + k * step;
+            s[k] = stored(s[k], t[k]);
             if (a.out_sum && row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.out_sum + base + c * 8) = s[k];
         }
+    }
+    float p = piece_sum(piece(BLOCK ? head : s[0])) * 0.125f;
+    if (!BLOCK) p = __shfl_sync(0xffffffffu, p, lane - li);
+    auto minus_p = [&](int k) { return li + k * step < a.chunks ? pack2(-p) : pack2(0.f); };   // (behind the row: zeros)
+    f2 sum2v = 0, sq2v = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum2v = add2(sum2v, v.v[e]);
+    for (int k = 0; k < CPL; ++k) {
+        const Piece v = piece(s[k]);
+        const f2 m = minus_p(k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f2 d = add2(v.v[e], m);
+            sum2v = add2(sum2v, d);
+            sq2v = fma2(d, d, sq2v);
+        }
     }
     uint4 gm[CPL], bt[CPL];   // (asked for before the row's sums are known)
 #pragma unroll
@@ -103,39 +146,31 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) layernorm_forward_kernel(Ln
         gm[k] = ok ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
         bt[k] = ok && a.beta ? ld16(a.beta + c * 8) : make_uint4(0, 0, 0, 0);
     }
-    float sum = sum2(sum2v), sq = 0.f;
-    row_sum2<BLOCK>(sum, sq, a.lpr, red[0]);
-    const float mu = sum * a.inv_c;
-    auto minus_mu = [&](int k) { return li + k * step < a.chunks ? pack2(-mu) : pack2(0.f); };   // (behind the row: zeros)
-    f2 sq2v = 0;
-    sum2v = 0;
+    float sum = sum2(sum2v), sq = sum2(sq2v);
+    row_sum2<BLOCK>(sum, sq, a.lpr, red);
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) {
-        const Piece v = piece(s[k]);
-        const f2 m = minus_mu(k);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const f2 d = add2(v.v[e], m);
-            sum2v = add2(sum2v, d);
-            sq2v = fma2(d, d, sq2v);
-        }
+    for (int k = 0; k < CPL; ++k) {   // (kept packed: fewer registers, more rows in flight)
+        forget(s[k]);
+        forget(gm[k]);
+        forget(bt[k]);
     }
-    sum = sum2(sum2v);
-    sq = sum2(sq2v);
-    row_sum2<BLOCK>(sum, sq, a.lpr, red[1]);
     float mean;
     const float r = deviation(sum, sq, a.inv_c, a.eps, mean);
     const f2 r2 = pack2(r), shift = pack2(-mean * r);
+    if (FORM == FORM_POST) {
+        cp_async_commit();
+        cp_async_wait<0>();
+    }
     if (FORM != FORM_Q8) {
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
             if (!(row_ok && c < a.chunks)) continue;
             Piece v = piece(s[k]);
-            const Piece g = piece(gm[k]), b = piece(bt[k]), w = piece(FORM == FORM_POST ? t[k] : make_uint4(0, 0, 0, 0));
+            const Piece g = piece(gm[k]), b = piece(bt[k]), w = FORM == FORM_POST ? piece(lds16(own + k * own_step)) : Piece{};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v.v[e] = fma2(fma2(add2(v.v[e], pack2(-mu)), r2, shift), g.v[e], b.v[e]);
+                v.v[e] = fma2(fma2(add2(v.v[e], pack2(-p)), r2, shift), g.v[e], b.v[e]);
                 if (FORM == FORM_POST) v.v[e] = add2(v.v[e], w.v[e]);
             }
             *reinterpret_cast<uint4 *>((bf16 *)a.out + base + c * 8) = pack(v);
@@ -147,7 +182,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) layernorm_forward_kernel(Ln
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {   // (pieces behind the row: gamma and beta are zeros)
         const Piece v = piece(s[k]), g = piece(gm[k]), b = piece(bt[k]);
-        const f2 m = minus_mu(k);
+        const f2 m = minus_p(k);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             y[k][e] = fma2(fma2(add2(v.v[e], m), r2, shift), g.v[e], b.v[e]);
@@ -156,7 +191,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256) layernorm_forward_kernel(Ln
             amax = max_abs(amax, lo, hi);
         }
     }
-    amax = row_reduce<MaxOp, BLOCK>(amax, a.lpr, reinterpret_cast<float *>(red[0]));
+    amax = row_reduce<MaxOp, BLOCK>(amax, a.lpr, amaxes);
     store_codes<CPL>(y, amax, a.scales + row, row_ok, li, step, a.chunks, (uint8_t *)a.out + base);
 }
 
@@ -170,55 +205,73 @@ struct LnBwdArgs {
     int lanes;        // of a row: of a warp, or (wide rows) threads
 };
 
-// The backward, dx = r (a - mean a - n mean(a n)) + dsum with a = dy gamma, of a
-// thread's piece of a row: its shares of the row's sum of s and of a,
-__device__ __forceinline__ void piece_sums(const Piece &s, const Piece &d, const Piece &g, f2 &sum, f2 &asum)
+// bf16 pairs with fp32 ones, exact operands and one rounding each: w + c, and the
+// product a b.
+__device__ __forceinline__ f2 add_bf16x2(uint32_t w, f2 c)
 {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        sum = add2(sum, s.v[e]);
-        asum = fma2(d.v[e], g.v[e], asum);
-    }
+    f2 r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .f32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b64 {x, y}, %2;\n\t"
+        "add.f32.bf16 x, l, x;\n\tadd.f32.bf16 y, h, y;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "r"(w), "l"(c));
+    return r;
 }
-// of the deviations s - mu, their squares and their products with a,
-__device__ __forceinline__ void piece_moments(const Piece &s, const Piece &d, const Piece &g, f2 minus_mu, f2 &sum, f2 &sq, f2 &dot)
+__device__ __forceinline__ f2 mul_bf16x2(uint32_t a, uint32_t b)
 {
+    f2 r;
+    asm("{\n\t.reg .b16 l, h, m, n;\n\t.reg .f32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {m, n}, %2;\n\t"
+        "fma.rn.f32.bf16 x, l, m, 0f00000000;\n\tfma.rn.f32.bf16 y, h, n, 0f00000000;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
+
+// The backward, dx = r (a - mean a - n mean(a n)) + dsum with a = dy gamma, of a
+// thread's piece of a row: its shares of the row's sums of s - p, its square, a and
+// a (s - p),
+struct RowSums {
+    f2 sum, sq, a, dot;
+};
+__device__ __forceinline__ void piece_sums(const uint4 &su, const uint4 &du, const uint4 &gu, f2 minus_p, RowSums &w)
+{
+    const uint32_t s[4] = {su.x, su.y, su.z, su.w}, d[4] = {du.x, du.y, du.z, du.w}, g[4] = {gu.x, gu.y, gu.z, gu.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const f2 v = add2(s.v[e], minus_mu);
-        sum = add2(sum, v);
-        sq = fma2(v, v, sq);
-        dot = fma2(mul2(d.v[e], g.v[e]), v, dot);
+        const f2 v = add_bf16x2(s[e], minus_p), x = mul_bf16x2(d[e], g[e]);
+        w.sum = add2(w.sum, v);
+        w.sq = fma2(v, v, w.sq);
+        w.a = add2(w.a, x);
+        w.dot = fma2(x, v, w.dot);
     }
 }
 // and, from the row's sums, dx and the terms of dgamma and dbeta.
 struct RowGrad {
-    f2 minus_mu, r, shift;        // n = (s - mu) r + shift
+    f2 minus_p, r, shift;         // n = (s - p) r + shift
     f2 minus_ra, minus_rn;        // -r mean a, -r mean(a n)
 };
-__device__ __forceinline__ RowGrad row_grad(float mu, float sum, float sq, float asum, float dot, float inv_c, float eps,
-                                            bool ok)
+__device__ __forceinline__ RowGrad row_grad(float p, const float4 &w, float inv_c, float eps)
 {
     float mean;
-    // (no row: r = 0, since its terms get zero times r, and with eps = 0 one over
-    // the root of its variance is infinite)
-    const float r = ok ? deviation(sum, sq, inv_c, eps, mean) : (mean = 0.f);
-    const float ma = asum * inv_c, mn = r * fmaf(-mean, ma, dot * inv_c);
-    return {pack2(-mu), pack2(r), pack2(-mean * r), pack2(-r * ma), pack2(-r * mn)};
+    const float r = deviation(w.x, w.y, inv_c, eps, mean);
+    const float ma = w.z * inv_c, mn = r * fmaf(-mean, ma, w.w * inv_c);
+    return {pack2(-p), pack2(r), pack2(-mean * r), pack2(-r * ma), pack2(-r * mn)};
 }
 template <bool DSUM>
-__device__ __forceinline__ uint4 piece_grad(const Piece &s, const Piece &d, const Piece &g, const Piece &m, const RowGrad &w,
+__device__ __forceinline__ uint4 piece_grad(const uint4 &su, const uint4 &du, const uint4 &gu, const uint4 &mu, const RowGrad &w,
                                             Piece &dg, Piece &db)
 {
+    const uint32_t s[4] = {su.x, su.y, su.z, su.w}, d[4] = {du.x, du.y, du.z, du.w}, g[4] = {gu.x, gu.y, gu.z, gu.w},
+                   m[4] = {mu.x, mu.y, mu.z, mu.w};
+    const Piece y = piece(du);
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const f2 n = fma2(add2(s.v[e], w.minus_mu), w.r, w.shift);
-        dg.v[e] = fma2(d.v[e], n, dg.v[e]);
-        db.v[e] = add2(db.v[e], d.v[e]);
-        f2 t = fma2(mul2(d.v[e], g.v[e]), w.r, w.minus_ra);
+        const f2 n = fma2(add_bf16x2(s[e], w.minus_p), w.r, w.shift);
+        dg.v[e] = fma2(y.v[e], n, dg.v[e]);
+        db.v[e] = add2(db.v[e], y.v[e]);
+        f2 t = fma2(mul_bf16x2(d[e], g[e]), w.r, w.minus_ra);
         t = fma2(n, w.minus_rn, t);
-        if (DSUM) t = add2(t, m.v[e]);
+        if (DSUM) t = add_bf16x2(m[e], t);
         float lo, hi;
         unpack2(t, lo, hi);
         o[e] = pack_bf16x2(lo, hi);
@@ -234,77 +287,85 @@ __device__ __forceinline__ float *block_columns(const LnBwdArgs &a, int which)
     return a.partial + (int64_t)blockIdx.x * C * (a.dbeta ? 2 : 1) + which * C;
 }
 
-constexpr int blocks_per_sm(int cpl, bool dsum) { return cpl > 1 ? 2 : 4; }
+// Blocks of 256 threads on an SM: enough bytes of loads in flight, and no more
+// (200000 x 512, two pieces a lane: with dsum 120 us with two blocks, 129 with
+// three; without 102 and 99).
+constexpr int blocks_per_sm(int cpl, bool dsum) { return cpl > 2 || (cpl == 2 && dsum) ? 2 : cpl == 2 ? 3 : 4; }
 
 // Rows on part of a warp: a block takes 8 * (32 / lanes) rows together, then the
-// ones gridDim.x on.  Each thread keeps the columns it owns of dgamma and dbeta
-// in registers over its rows; the block writes one partial row at the end.
+// ones gridDim.x on.  Every thread fetches its pieces of the rows after these by
+// asynchronous copies into its own place in shared memory, so that loads are in
+// flight while it computes.  It keeps the columns it owns of dgamma and dbeta in
+// registers over its rows; the block writes one partial row at the end.
 template <int CPL, bool DSUM>
 __global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) layernorm_backward_kernel(LnBwdArgs a)
 {
-    extern __shared__ float part[];   // [8 warps][C]
+    constexpr uint32_t STAGE = (DSUM ? 3 : 2) * CPL * 4096;   // two: these rows, and the next
+    extern __shared__ __align__(16) float part[];   // the pieces; at the end [8 warps][C]
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = a.lanes, li = lane % step;
     const int rpw = 32 / step, rpb = 8 * rpw;
+    // this thread's piece k of array i in a stage at `at`: at + (i CPL + k) 4 KB
+    uint32_t at = smem_u32(part) + threadIdx.x * 16, other = at + STAGE;
+    bool have[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) have[k] = li + k * step < a.chunks;
+    auto fetch = [&](int64_t row, uint32_t to) {
+        if (row < a.rows) {
+            const int64_t off = (row * a.chunks + li) * 8;
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                if (!have[k]) continue;
+                cp_async16(to + k * 4096, a.s + off + k * step * 8, 16);
+                cp_async16(to + (CPL + k) * 4096, a.dy + off + k * step * 8, 16);
+                if (DSUM) cp_async16(to + (2 * CPL + k) * 4096, a.dsum + off + k * step * 8, 16);
+            }
+        }
+        cp_async_commit();
+    };
+    const int64_t hop = (int64_t)gridDim.x * rpb;
+    int64_t row = (int64_t)blockIdx.x * rpb + warp * rpw + lane / step;
+    fetch(row, at);
     Piece acc[2][CPL];
     uint4 g[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
-        const int c = li + k * step;
-        g[k] = c < a.chunks ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
+        g[k] = have[k] ? ld16(a.gamma + (li + k * step) * 8) : make_uint4(0, 0, 0, 0);
         acc[0][k] = acc[1][k] = Piece{};
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
-        const int64_t row = r0 + warp * rpw + lane / step;
-        const bool row_ok = row < a.rows;
-        const int64_t base = row * a.chunks * 8;
-        uint4 s[CPL], d[CPL], m[CPL];
+#pragma unroll 1
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += hop, row += hop) {
+        fetch(row + hop, other);
+        cp_async_wait<1>();
+        const bool row_ok = row < a.rows;   // (no row: its pieces hold whatever was there, and count for nothing)
+        const float p = __shfl_sync(0xffffffffu, piece_sum(piece(lds16(at))) * 0.125f, lane - li);
+        RowSums w{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
-            const int c = li + k * step;
-            const bool ok = row_ok && c < a.chunks;
-            s[k] = ok ? ld16(a.s + base + c * 8) : make_uint4(0, 0, 0, 0);
-            d[k] = ok ? ld16(a.dy + base + c * 8) : make_uint4(0, 0, 0, 0);
-            if (DSUM) m[k] = ok ? ld16(a.dsum + base + c * 8) : make_uint4(0, 0, 0, 0);
+            forget(g[k]);   // (kept packed)
+            if (have[k]) piece_sums(lds16(at + k * 4096), lds16(at + (CPL + k) * 4096), g[k], pack2(-p), w);
         }
-        // (the packed values stay, their fp32 forms are made again: registers
-        // kept across the sums would halve the rows in flight)
-        auto keep_packed = [&]() {
+        float4 sums = make_float4(sum2(w.sum), sum2(w.sq), sum2(w.a), sum2(w.dot));
+        lane_sum2(sums.x, sums.y, step);
+        lane_sum2(sums.z, sums.w, step);
+        if (row_ok) {
+            const RowGrad grad = row_grad(p, sums, a.inv_c, a.eps);
+            bf16 *dx = a.dx + (row * a.chunks + li) * 8;
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
-                forget(s[k]);
-                forget(d[k]);
                 forget(g[k]);
-                if (DSUM) forget(m[k]);
+                if (!have[k]) continue;
+                *reinterpret_cast<uint4 *>(dx + k * step * 8) =
+                    piece_grad<DSUM>(lds16(at + k * 4096), lds16(at + (CPL + k) * 4096), g[k],
+                                     DSUM ? lds16(at + (2 * CPL + k) * 4096) : uint4{}, grad, acc[0][k], acc[1][k]);
             }
-        };
-        f2 sum2v = 0, asum2 = 0, sq2 = 0, dot2 = 0;
-#pragma unroll
-        for (int k = 0; k < CPL; ++k) piece_sums(piece(s[k]), piece(d[k]), piece(g[k]), sum2v, asum2);
-        float sum = sum2(sum2v), asum = sum2(asum2);
-        lane_sum2(sum, asum, step);
-        keep_packed();
-        const float mu = sum * a.inv_c;
-        sum2v = 0;
-#pragma unroll
-        for (int k = 0; k < CPL; ++k)
-            piece_moments(piece(s[k]), piece(d[k]), piece(g[k]), li + k * step < a.chunks ? pack2(-mu) : pack2(0.f), sum2v, sq2,
-                          dot2);
-        sum = sum2(sum2v);
-        float sq = sum2(sq2), dot = sum2(dot2);
-        lane_sum2(sum, sq, step);
-        for (int o = step >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        keep_packed();
-        const RowGrad w = row_grad(mu, sum, sq, asum, dot, a.inv_c, a.eps, row_ok);
-#pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            const int c = li + k * step;
-            const uint4 o = piece_grad<DSUM>(piece(s[k]), piece(d[k]), piece(g[k]), DSUM ? piece(m[k]) : Piece{}, w,
-                                             acc[0][k], acc[1][k]);
-            if (row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.dx + base + c * 8) = o;
         }
+        const uint32_t was = at;
+        at = other;
+        other = was;
     }
+    __syncthreads();   // (every thread is done with its pieces)
     // the warp's rows, then the block's warps
     const int C = a.chunks * 8;
 #pragma unroll
@@ -334,22 +395,23 @@ __global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) layernorm_backw
     }
 }
 
-// Three sums over a group of a block, of `threads` threads that meet at a barrier
-// of their own; red: two rows of 16 a group, used in turn.
-__device__ __forceinline__ void group_sum3(float &a, float &b, float &c, int threads, int group, int turn, float4 *red)
+// A row's sums over a group of a block, of `threads` threads that meet at a
+// barrier of their own; red: two rows of 16 a group, used in turn.
+__device__ __forceinline__ void group_sum4(float4 &v, int threads, int group, int turn, float4 *red)
 {
-    lane_sum2(a, b, 32);
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    lane_sum2(v.x, v.y, 32);
+    lane_sum2(v.z, v.w, 32);
     const int warps = threads >> 5, warp = (threadIdx.x - group * threads) >> 5;
     red += (2 * group + (turn & 1)) * 16;
-    if ((threadIdx.x & 31) == 0) red[warp] = make_float4(a, b, c, 0.f);
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-    a = b = c = 0.f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = 0; w < warps; ++w) {
-        const float4 v = red[w];
-        a += v.x;
-        b += v.y;
-        c += v.z;
+        const float4 u = red[w];
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
     }
 }
 
@@ -361,7 +423,7 @@ template <int CPL, bool DSUM>
 __global__ void __launch_bounds__(512, 1) layernorm_backward_wide_kernel(LnBwdArgs a)
 {
     constexpr int ARRAYS = DSUM ? 3 : 2, DEPTH = 2;   // stages: a row, and the next
-    extern __shared__ __align__(16) float part[];   // the pieces; at the end [C]
+    extern __shared__ __align__(16) float part[];   // the pieces; at the end the columns' sums
     __shared__ float4 red[2 * 16 * 16];
     griddep_launch_dependents();
     griddep_wait();
@@ -377,9 +439,11 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_wide_kernel(LnBwdAr
     const int64_t first = (int64_t)blockIdx.x * rpb + group, hop = (int64_t)gridDim.x * rpb;
     int64_t ahead = first;   // the next row to fetch, and its stage
     uint32_t ahead_at = ring;
+    uint4 head = make_uint4(0, 0, 0, 0);   // its first piece, for every thread
     auto fetch = [&]() {
         if (ahead < a.rows) {
             const int64_t off = ahead * C + li * 8;
+            head = ld16(a.s + ahead * C);
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
                 if (!have[k]) continue;
@@ -406,68 +470,59 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_wide_kernel(LnBwdAr
     int turn = 0;
 #pragma unroll 1
     for (int64_t row = first; row < a.rows; row += hop) {   // (the same for a group's threads)
+        const float p = piece_sum(piece(head)) * 0.125f;
         fetch();
         cp_async_wait<DEPTH - 1>();
-        f2 sum2v = 0, asum2 = 0, sq2 = 0, dot2 = 0;
+        RowSums w{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             forget(g[k]);   // (kept packed)
-            if (have[k]) piece_sums(piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), piece(g[k]), sum2v, asum2);
+            if (have[k]) piece_sums(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], pack2(-p), w);
         }
-        float sum = sum2(sum2v), asum = sum2(asum2), sq = 0.f;
-        group_sum3(sum, asum, sq, step, group, turn++, red);
-        const float mu = sum * a.inv_c;
-        sum2v = 0;
-#pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            forget(g[k]);
-            if (have[k])
-                piece_moments(piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), piece(g[k]), pack2(-mu), sum2v, sq2,
-                              dot2);
-        }
-        sum = sum2(sum2v);
-        sq = sum2(sq2);
-        float dot = sum2(dot2);
-        group_sum3(sum, sq, dot, step, group, turn++, red);
-        const RowGrad w = row_grad(mu, sum, sq, asum, dot, a.inv_c, a.eps, true);
+        float4 sums = make_float4(sum2(w.sum), sum2(w.sq), sum2(w.a), sum2(w.dot));
+        group_sum4(sums, step, group, turn++, red);
+        const RowGrad grad = row_grad(p, sums, a.inv_c, a.eps);
         bf16 *dx = a.dx + row * C + li * 8;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             forget(g[k]);
             if (!have[k]) continue;
-            const Piece m = DSUM ? piece(lds16(place(at, 2, k))) : Piece{};
-            *reinterpret_cast<uint4 *>(dx + k * step * 8) = piece_grad<DSUM>(
-                piece(lds16(place(at, 0, k))), piece(lds16(place(at, 1, k))), piece(g[k]), m, w, acc[0][k], acc[1][k]);
+            *reinterpret_cast<uint4 *>(dx + k * step * 8) =
+                piece_grad<DSUM>(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k],
+                                 DSUM ? lds16(place(at, 2, k)) : uint4{}, grad, acc[0][k], acc[1][k]);
         }
         at += stage;
         if (at == ring_end) at = ring;
     }
     __syncthreads();   // (every group is done with its pieces)
-    // the groups add theirs in turn
+    // each thread's columns into its own places, [z][k][half][thread]; then a column
+    // piece a thread over the groups
+    float4 *own = reinterpret_cast<float4 *>(part) + threadIdx.x;
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-        if (z && !a.dbeta) break;
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int k = 0; k < CPL; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 v;
+                unpack2(acc[z][k].v[2 * h], v.x, v.y);
+                unpack2(acc[z][k].v[2 * h + 1], v.z, v.w);
+                own[((z * CPL + k) * 2 + h) * blockDim.x] = v;
+            }
+    __syncthreads();
+    const int pieces = 2 * a.chunks;   // halves of the columns' pieces
+    for (int i = threadIdx.x; i < (a.dbeta ? 2 : 1) * pieces; i += blockDim.x) {
+        const int z = i >= pieces, c = (i - z * pieces) >> 1, h = i & 1;
+        const float4 *from = reinterpret_cast<const float4 *>(part) + ((z * CPL + c / step) * 2 + h) * blockDim.x + c % step;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int t = 0; t < rpb; ++t) {
-            if (group == t)
-#pragma unroll
-                for (int k = 0; k < CPL; ++k) {
-                    const int c = li + k * step;
-                    if (c >= a.chunks) continue;
-                    float4 *p = reinterpret_cast<float4 *>(part + c * 8);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float4 v;
-                        unpack2(acc[z][k].v[2 * h], v.x, v.y);
-                        unpack2(acc[z][k].v[2 * h + 1], v.z, v.w);
-                        const float4 old = t ? p[h] : make_float4(0.f, 0.f, 0.f, 0.f);
-                        p[h] = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
-                    }
-                }
-            __syncthreads();
+            const float4 u = from[t * step];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
         }
-        float *out = block_columns(a, z);
-        for (int i = threadIdx.x; i < C; i += blockDim.x) out[i] = part[i];
-        __syncthreads();
+        *reinterpret_cast<float4 *>(block_columns(a, z) + c * 8 + h * 4) = v;
     }
 }
 
@@ -489,7 +544,8 @@ cudaError_t launch_forward(LnArgs a, cudaStream_t stream)
     case n:                                                                                   \
         return launch_maybe_overlapped(p.block ? layernorm_forward_kernel<n, true, FORM>      \
                                                : layernorm_forward_kernel<n, false, FORM>,    \
-                                       dim3(grid), dim3(threads), 0, stream, 1, a);
+                                       dim3(grid), dim3(threads), smem, stream, 1, a);
+    const size_t smem = FORM == FORM_POST && p.block ? (size_t)p.cpl * threads * 16 : 0;   // (at most 32 KB)
     switch (p.cpl) {
         SWIN_LN_CASE(1)
         SWIN_LN_CASE(2)
@@ -520,13 +576,13 @@ BwdPlan plan_backward(int rows, int C, bool with_dsum)
         rpb = groups < MAX_GROUPS ? groups : MAX_GROUPS;
         per_sm = 1;
         p.threads = (int)rpb * r.lanes;
-        p.smem = (size_t)p.threads * (with_dsum ? 3 : 2) * 2 * r.cpl * 16;   // (at most 192 KB)
-        if (p.smem < (size_t)C * sizeof(float)) p.smem = (size_t)C * sizeof(float);
+        p.smem = (size_t)p.threads * (with_dsum ? 3 : 2) * 2 * r.cpl * 16;   // (at most 192 KB; the sums need 64 B a piece)
     } else {
         rpb = 8 * (32 / r.lanes);
         per_sm = blocks_per_sm(r.cpl, with_dsum);
         p.threads = 256;
-        p.smem = (size_t)8 * C * sizeof(float);
+        p.smem = (size_t)(with_dsum ? 3 : 2) * r.cpl * 2 * 4096;   // (at most 72 KB)
+        if (p.smem < (size_t)8 * C * sizeof(float)) p.smem = (size_t)8 * C * sizeof(float);
     }
     const int64_t want = (rows + rpb - 1) / rpb, most = sm_count() * per_sm;
     // few rows: one block, whose sums are the result (two turns at most: less than
@@ -553,9 +609,8 @@ cudaError_t launch_backward(LnBwdArgs a, const BwdPlan &p, cudaStream_t stream)
     cudaError_t e;
     // (always the most any call needs: another thread may be between its setting
     // and its launch)
-    if (r.block &&
-        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 6 * r.cpl * 16)) != cudaSuccess)
-        return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (r.block ? 512 : 256) * 6 * r.cpl * 16);
+    if (e != cudaSuccess) return e;
     e = launch_maybe_overlapped(kern, dim3(p.grid), dim3(p.threads), p.smem, stream, 1, a);
     if (e != cudaSuccess || p.grid == 1) return e;
     return launch_maybe_overlapped(column_sum_kernel, dim3((cols + 31) / 32), dim3(1024), 0, stream, 1,
