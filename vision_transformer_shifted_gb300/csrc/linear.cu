@@ -104,6 +104,7 @@ cudaError_t launch_linear(const Forward &f, int C, int N, const ProductsPlan &pl
         if (e != cudaSuccess) return e;
         JoinArgs &j = fin->join[0];
         j.part = part;
+        j.slots = 2;
         j.split = pl.split;
         j.tn = pl.wn;
         j.blocks = pl.split.cut >= 16 ? 16 : 64;
@@ -377,6 +378,7 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     const int ld = act ? hidden_ld(h->N) : h->N;
     Product px = dx_product(h->C, h->N, rows, ld), pw = weight_product(h->C, h->N, rows, ld);
     const ProductsPlan plx = dx ? plan_products(&px, 1) : ProductsPlan{}, plw = dW ? plan_products(&pw, 1) : ProductsPlan{};
+    const ActWgradPlan pa = act && dW ? plan_act_wgrad(h->C, h->N, rows) : ActWgradPlan{};
     const GradPlan pg = plan_grad(h->N, rows);
     FinishArgs fin{};
     size_t sum_bytes = 0;
@@ -387,21 +389,23 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         m.b = act ? nullptr : (const bf16 *)dy;
         m.rows = rows;
         m.cols = h->N;
-        m.slices = act ? pg.slices : column_slices(rows);
+        m.slices = pa.chosen ? pa.slices : act ? pg.slices : column_slices(rows);
         m.tasks = act ? 0 : ceil_div(h->N, 256) * m.slices;
         sum_bytes = (size_t)m.slices * h->N * sizeof(float);
     }
     Carve size(nullptr);
-    size.take(act ? (size_t)rows * ld * 2 : 0);
+    const size_t dz_bytes = act && (dx || !pa.chosen) ? (size_t)rows * ld * 2 : 0,
+                 w_bytes = pa.chosen ? pa.part_bytes : plw.part_bytes;
+    size.take(dz_bytes);
     size.take(plx.part_bytes);
-    size.take(plw.part_bytes);
+    size.take(w_bytes);
     size.take(sum_bytes);
     void *ws = nullptr;
     bool captured = false;
     if (size.used && (rc = ows_begin(&h->ws, size.used, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
     Carve carve(ws);
-    bf16 *dz = (bf16 *)carve.take(act ? (size_t)rows * ld * 2 : 0);
-    float *x_part = (float *)carve.take(plx.part_bytes), *w_part = (float *)carve.take(plw.part_bytes);
+    bf16 *dz = (bf16 *)carve.take(dz_bytes);
+    float *x_part = (float *)carve.take(plx.part_bytes), *w_part = (float *)carve.take(w_bytes);
     float *sum_part = (float *)carve.take(sum_bytes);
     if (db) fin.cs.m[0].part = sum_part;
     px.a[0] = pw.a[0] = act ? (const void *)dz : dy;
@@ -412,7 +416,12 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     const DeviceStatus st{h->d_err, WAIT_NS};
     h->last_launches = 0;
     cudaError_t e = cudaSuccess;
-    if (act) {
+    if (pa.chosen) {
+        const ActWgrad w{(const bf16 *)z, (const bf16 *)dy, (const bf16 *)x, dx ? dz : nullptr, (bf16 *)dW, db ? sum_part : nullptr,
+                         w_part, rows, h->C, h->N, ld, h->act};
+        ++h->last_launches;
+        e = launch_act_wgrad(w, pa, st, s, &fin.join[1], &fin.joins[1]);
+    } else if (act) {
         const GradArgs a{(const bf16 *)z, (const bf16 *)dy, dz, db ? sum_part : nullptr, rows, h->N, ld, pg.across, pg.at_once,
                          pg.slices};
         ++h->last_launches;
@@ -420,7 +429,7 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
                                     dim3((unsigned)pg.columns, (unsigned)pg.slices), dim3(256), 0, s, 1, a);
     }
     if (e == cudaSuccess && dx) e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0);
-    if (e == cudaSuccess && dW) e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
+    if (e == cudaSuccess && dW && !pa.chosen) e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;

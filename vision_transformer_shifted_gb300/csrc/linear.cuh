@@ -235,4 +235,25 @@ struct LinearPolicy {
     }
 };
 
+// ---- the weight gradient through an activation (linear_grad.cu) ----------------------
+
+// dW = dz^T x, dz = dy act'(z) (written to dz unless null, rows of stride ld) and
+// the slices' shares of db [slices, N] (null: not computed).
+struct ActWgrad {
+    const bf16 *z, *dy, *x;
+    bf16 *dz, *dW;
+    float *sums, *part;   // part: plan.part_bytes
+    int rows, C, N, ld, act;
+};
+struct ActWgradPlan {
+    bool chosen;          // rather than dz by a kernel of its own
+    int n, tiles, slices; // columns of a tile, tiles of 256 rows of dW, slices of the tokens
+    int kb, slice_kb;
+    size_t part_bytes;
+};
+ActWgradPlan plan_act_wgrad(int C, int N, int rows);
+// Queues the kernel; the join of its partial tiles is left to launch_finish.
+cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceStatus st, cudaStream_t stream, JoinArgs *join,
+                             int *join_blocks);
+
 } // namespace swin

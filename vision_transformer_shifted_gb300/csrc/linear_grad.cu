@@ -1,0 +1,349 @@
+// The weight gradient of a linear layer with an activation, dW = dz^T x with dz =
+// dy act'(z), from z and dy themselves: for up to 512 input channels one tile holds
+// all columns of dW, so that every element of z and dy is read once, by the pair
+// whose tile it belongs to; dz is formed in shared memory, where the MMAs read it,
+// and written once for dx's product.  As a kernel of its own (act_grad_kernel) dz
+// costs a trip of z and dy through the SMs that feeds nothing, and a second one of
+// dz: 12544 x 512 x 2048 91 us, with this kernel 73.6.
+//
+// A CTA pair takes a tile of 256 output channels (128 a CTA, the rows of dW) x all
+// input channels and a slice of the tokens; TMEM holds the tile (up to 512
+// columns), the slices' partial tiles are joined by finish_kernel.  Per K block of
+// 64 tokens a CTA loads its 64 x 128 of z and of dy (its own barrier) and its half
+// of x's columns (the leader's); sixteen warps turn z into dz in place, a 1 KB atom
+// of the swizzled tile (8 tokens x 64 channels) each, add up their channels for db,
+// store dz, and release the block to the MMAs.  What binds it: HBM (z and dy in, dz
+// out), then the reciprocals and exponentials (three an element, 8192 elements a
+// block: 0.8 us of a block's 1.05).
+#include <atomic>
+#include <cstring>
+
+#include "linear.cuh"
+
+namespace swin {
+
+namespace {
+
+constexpr int WG_WARPS = 16, WG_THREADS = 64 + 32 * WG_WARPS, WG_MAX_STAGES = 4;
+constexpr int WG_A_BYTES = 32768;   // z and dy of a stage, 16 KB each (two boxes of 64 channels x 64 tokens)
+
+struct WgradArgs {
+    CUtensorMap z, dy, x, part;   // part: partial tiles [pairs][256][n] fp32
+    bf16 *dz;                     // [rows, ld], or null
+    float *sums;                  // [slices, N]: shares of db, or null
+    int rows, N, ld;
+    int n, stages, stage_bytes;   // n: C rounded up to 32, 64 at least
+    int slices, kb, slice_kb;     // K blocks of all tokens, of a slice
+    DeviceStatus st;
+};
+
+__device__ __forceinline__ uint32_t b_boxes(int n) { return n / 2 > 64 ? 2 : 1; }   // of a CTA's half of n columns
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4 &u)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 u;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr) : "memory");
+    return u;
+}
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WG_THREADS, 1)
+act_wgrad_kernel(const __grid_constant__ WgradArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_align(smem_raw, 1024);
+    __shared__ uint64_t bars[4 * WG_MAX_STAGES + 1];
+    __shared__ uint32_t tslot;
+    __shared__ float red[WG_WARPS][64];
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, tile = pair / a.slices, slice = pair % a.slices;
+    const int kb0 = slice * a.slice_kb, kb_n = (a.kb - kb0 < a.slice_kb ? a.kb - kb0 : a.slice_kb);
+    const int ch0 = tile * 256 + (int)rank * 128;   // this CTA's first output channel
+    // per stage: z and dy have landed (own), x has (the leader's, of both CTAs), dz
+    // is formed (the leader's), the MMAs are done (both); the tile is complete (both)
+    const uint32_t afull = smem_u32(bars), bfull = afull + 8 * WG_MAX_STAGES, ready = bfull + 8 * WG_MAX_STAGES,
+                   empty = ready + 8 * WG_MAX_STAGES, done = empty + 8 * WG_MAX_STAGES;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(afull + 8 * s, 1);
+            mbar_init(bfull + 8 * s, 1);
+            mbar_init(ready + 8 * s, 2 * WG_WARPS);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(done, 1);
+        mbar_init_fence();
+    }
+    if (warp == 0 && elect_one()) {
+        prefetch_map(&a.z);
+        prefetch_map(&a.dy);
+        prefetch_map(&a.x);
+        prefetch_map(&a.part);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&tslot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tslot;
+    bool failed = false;
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t ring = smem_u32(smem);
+    const int n0 = a.n < 256 ? a.n : 256, n1 = a.n - n0;   // columns of the one or two MMAs
+
+    if (warp == 0) {
+        const uint32_t lead_bfull = map_rank(bfull, 0);
+        const uint32_t b_bytes = (b_boxes(n0) + (n1 ? b_boxes(n1) : 0)) * 8192;
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+#pragma unroll 1
+        for (int i = 0; i < kb_n; ++i) {
+            if (!warp_pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns)) {
+                failed = true;
+                break;
+            }
+            if (elect_one()) {
+                const uint32_t dst = ring + s * a.stage_bytes, own = afull + 8 * s, bar = lead_bfull + 8 * s;
+                const int k = (kb0 + i) * 64;
+                mbar_arrive_expect_tx(own, WG_A_BYTES);
+                tma_load_2d(dst, &a.z, ch0, k, own);
+                tma_load_2d(dst + 8192, &a.z, ch0 + 64, k, own);
+                tma_load_2d(dst + 16384, &a.dy, ch0, k, own);
+                tma_load_2d(dst + 24576, &a.dy, ch0 + 64, k, own);
+                if (rank == 0) mbar_arrive_expect_tx(bfull + 8 * s, 2 * b_bytes);
+                const int c0 = (int)rank * (n0 / 2), c1 = 256 + (int)rank * (n1 / 2);
+                tma_load_2d_pair(dst + WG_A_BYTES, &a.x, c0, k, bar);
+                if (b_boxes(n0) > 1) tma_load_2d_pair(dst + WG_A_BYTES + 8192, &a.x, c0 + 64, k, bar);
+                if (n1) {
+                    tma_load_2d_pair(dst + WG_A_BYTES + 16384, &a.x, c1, k, bar);
+                    if (b_boxes(n1) > 1) tma_load_2d_pair(dst + WG_A_BYTES + 24576, &a.x, c1 + 64, k, bar);
+                }
+            }
+            ++issued;
+            if (++s == a.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        // every stage given back: no commit is on its way to this CTA's barriers
+        for (int k = 0; k < a.stages && k < issued && !failed; ++k) {
+            const RingUse u = last_use(a.stages, issued, k);
+            failed = !warp_pair_wait(empty + 8 * u.stage, u.parity, a.st.wait_ns);
+        }
+        if (failed) {
+            // (copies in flight land before the memory is given back)
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t idesc = idesc_pair(MMA_BF16, true, true, 256, 0);
+            const uint32_t idesc0 = idesc | (uint32_t)(n0 >> 3) << 17, idesc1 = idesc | (uint32_t)(n1 >> 3) << 17;
+            int s = 0;
+            uint32_t ph = 0;
+#pragma unroll 1
+            for (int i = 0; i < kb_n; ++i) {
+                if (!warp_pair_wait(bfull + 8 * s, ph, a.st.wait_ns) || !warp_pair_wait(ready + 8 * s, ph, a.st.wait_ns)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t a16 = (ring + s * a.stage_bytes) >> 4, b16 = a16 + (WG_A_BYTES >> 4);
+                    const int steps = kblock_steps(a.rows, kb0 + i, 64);
+                    mma_kblock<MMA_BF16, true, true>(tmem, a16, b16, idesc0, steps, i == 0);
+                    if (n1) mma_kblock<MMA_BF16, true, true>(tmem + 256, a16, b16 + 1024, idesc1, steps, i == 0);
+                    mma_commit_pair(empty + 8 * s);
+                    if (i == kb_n - 1) mma_commit_pair(done);
+                }
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else {
+        const int w = warp - 2;
+        // this lane's two 16-byte pieces of the warp's atom: tokens t, t + 4, eight
+        // channels (one logical chunk, so that its sums are of fixed channels)
+        const int box = w & 1, chunk = lane & 7, t = lane >> 3;
+        const uint32_t at0 = (uint32_t)box * 8192 + sw128_offset((w >> 1) * 8 + t, chunk),
+                       at1 = (uint32_t)box * 8192 + sw128_offset((w >> 1) * 8 + t + 4, chunk);
+        const uint32_t lead_ready = map_rank(ready, 0);
+        const int c = ch0 + box * 64 + chunk * 8;
+        const bool stored = a.dz && c < a.N;
+        f2 sum[4] = {0, 0, 0, 0};
+        int s = 0;
+        uint32_t ph = 0;
+        int64_t row = (int64_t)kb0 * 64 + (w >> 1) * 8 + t;
+#pragma unroll 1
+        for (int i = 0; i < kb_n; ++i, row += 64) {
+            if (!warp_pair_wait(afull + 8 * s, ph, a.st.wait_ns)) {
+                failed = true;
+                break;
+            }
+            const uint32_t base = ring + s * a.stage_bytes;
+            auto grad = [&](uint32_t at, int64_t r) {
+                const uint4 zu = lds16(base + at), du = lds16(base + 16384 + at);
+                const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w}, dw[4] = {du.x, du.y, du.z, du.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 zf = unpack_bf16x2(zw[e]), df = unpack_bf16x2(dw[e]);
+                    f2 act, slope;
+                    activate_grad2<ACT>(pack2(zf.x, zf.y), act, slope);
+                    const f2 v = mul2(pack2(df.x, df.y), slope);
+                    sum[e] = add2(sum[e], v);   // (behind the last token: dy is zero)
+                    float lo, hi;
+                    unpack2(v, lo, hi);
+                    o[e] = pack_bf16x2(lo, hi);
+                }
+                const uint4 u = make_uint4(o[0], o[1], o[2], o[3]);
+                sts16(base + at, u);
+                if (stored && r < a.rows) *reinterpret_cast<uint4 *>(a.dz + r * a.ld + c) = u;
+            };
+            grad(at0, row);
+            grad(at1, row + 4);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_ready + 8 * s);
+            if (++s == a.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        // the lanes' sums, then those of the eight warps of the same channels
+        if (a.sums) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v[2];
+                unpack2(sum[e], v[0], v[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[h] += __shfl_xor_sync(0xffffffffu, v[h], 8);
+                    v[h] += __shfl_xor_sync(0xffffffffu, v[h], 16);
+                    if (lane < 8) red[w][chunk * 8 + 2 * e + h] = v[h];
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * WG_WARPS) : "memory");
+            const int i = (int)threadIdx.x - 64;
+            if (i < 128 && ch0 + i < a.N) {
+                float v = 0.f;
+                for (int k = 0; k < WG_WARPS / 2; ++k) v += red[2 * k + (i >> 6)][i & 63];
+                a.sums[(int64_t)slice * a.N + ch0 + i] = v;
+            }
+        }
+        // the tile's fp32 values, boxes of 16 columns through the free stages
+        if (!failed) failed = !warp_pair_wait(done, 0, a.st.wait_ns);
+        if (!failed) {
+            tc_fence_after();
+            const int quad = warp & 3, share = w >> 2;   // (share: of the columns)
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
+            uint8_t *stage = smem + w * 4096;
+            int turn = 0;
+#pragma unroll 1
+            for (int j = share * 16; j < a.n; j += 64, ++turn) {
+                float v[16];
+                tmem_ld16(acc + j, v);
+                if (lane == 0) bulk_wait_read1();   // (the box written two before)
+                __syncwarp();
+                tmem_wait_ld();
+                uint8_t *to = stage + (turn & 1) * 2048;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4 *>(to + sw64_offset(lane, q)) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                store_box(&a.part, j, pair * 256 + (int)rank * 128 + quad * 32, true, to, lane);
+            }
+            if (lane == 0) bulk_wait_all();
+        }
+    }
+    if (failed && lane == 0) atomicOr(a.st.err, ERR_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+template <int ACT>
+cudaError_t launch(const WgradArgs &a, int pairs, cudaStream_t stream)
+{
+    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes;
+    static std::atomic<uint64_t> ready;   // devices whose copy of the kernel may use the most shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {
+        e = cudaFuncSetAttribute(act_wgrad_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + 196608);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit);
+    }
+    return launch_maybe_overlapped(act_wgrad_kernel<ACT>, dim3(2u * (unsigned)pairs), dim3(WG_THREADS), smem, stream, 1, a);
+}
+
+} // namespace
+
+ActWgradPlan plan_act_wgrad(int C, int N, int rows)
+{
+    ActWgradPlan p{};
+    const int pairs = sm_count() / 2, tiles = ceil_div(N, 256), kb = ceil_div(rows, 64);
+    if (C > 512 || 2 * tiles > pairs) return p;
+    p.n = C < 64 ? 64 : (C + 31) / 32 * 32;
+    p.tiles = tiles;
+    p.kb = kb;
+    p.slice_kb = ceil_div(kb, pairs / tiles);
+    p.slices = ceil_div(kb, p.slice_kb);
+    p.part_bytes = (size_t)tiles * p.slices * 256 * p.n * sizeof(float);
+    p.chosen = true;
+    return p;
+}
+
+cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceStatus st, cudaStream_t stream, JoinArgs *join,
+                             int *join_blocks)
+{
+    WgradArgs a;
+    memset(&a, 0, sizeof(a));
+    const int pairs = p.tiles * p.slices;
+    cudaError_t e;
+    if ((e = map_mn(&a.z, w.z, w.rows, w.N)) != cudaSuccess) return e;
+    if ((e = map_mn(&a.dy, w.dy, w.rows, w.N)) != cudaSuccess) return e;
+    if ((e = map_mn(&a.x, w.x, w.rows, w.C)) != cudaSuccess) return e;
+    e = make_tensor_map(&a.part, T_F32, w.part, p.n, (int64_t)pairs * 256, (int64_t)p.n * 4, 16, 32, 64);
+    if (e != cudaSuccess) return e;
+    a.dz = w.dz;
+    a.sums = w.sums;
+    a.rows = w.rows;
+    a.N = w.N;
+    a.ld = w.ld;
+    a.n = p.n;
+    a.stages = p.n > 256 ? 3 : 4;
+    a.stage_bytes = p.n > 256 ? 65536 : 49152;
+    a.slices = p.slices;
+    a.kb = p.kb;
+    a.slice_kb = p.slice_kb;
+    a.st = st;
+    PairSplit &s = join->split;
+    s = PairSplit{};
+    s.tiles = s.cut = p.tiles;
+    s.np = pairs;
+    s.k_blocks = p.kb;
+    s.q = (uint32_t)p.slice_kb;
+    s.kb = p.slice_kb * p.slices;
+    join->part = w.part;
+    join->slots = 1;
+    join->single = true;
+    join->tn = p.n;
+    join->blocks = p.tiles >= 16 ? 16 : 64;
+    join->p[0] = {nullptr, nullptr, w.dW, w.N, w.C, p.tiles, 1, 0};
+    join->p[1].first = join->p[2].first = 0x7fffffff;
+    *join_blocks = p.tiles * join->blocks;
+    return w.act == ACT_SILU ? launch<ACT_SILU>(a, pairs, stream) : launch<ACT_GELU>(a, pairs, stream);
+}
+
+} // namespace swin

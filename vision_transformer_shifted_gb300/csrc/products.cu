@@ -64,13 +64,13 @@ __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
     const PairSplit &s = a.split;
     const int c = block / a.blocks, t = s.full * s.np + c;
     const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
-    if (p0 == p1) return;   // (one pair had the whole tile and wrote it)
+    if (p0 == p1 && !a.single) return;   // (one pair had the whole tile and wrote it)
     const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
     int m, n;
     tile_order(tile_place(t - a.p[i].first, a.p[i].mt, a.p[i].nt, a.from_last), a.p[i].mt, a.p[i].nt, m, n);
     const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / VEC;
     const int64_t size = 256 * a.tn;
-    const int first = s.slot(p0, c);
+    const int first = a.slots == 1 ? p0 : s.slot(p0, c);
     for (int e = block % a.blocks * 256 + threadIdx.x; e < 256 * per; e += a.blocks * 256) {
         const int row = m * 256 + e / per, col = n * a.tn + e % per * VEC;
         if (row >= rows || col >= cols) continue;
@@ -81,7 +81,7 @@ __device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
         add_vec<VEC>(v, src + first * size);
 #pragma unroll 4
         for (int p = p0 + 1; p <= p1; ++p)   // (these begin inside the tile: their first range)
-            add_vec<VEC>(v, src + 2 * p * size);
+            add_vec<VEC>(v, src + a.slots * p * size);
         const int64_t at = (int64_t)row * cols + col;
         if (a.linear.sx) {
             const float sx = a.linear.sx[row];
@@ -262,6 +262,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     }
     ++*launches;
     r.part = part;
+    r.slots = 2;
     r.tn = TN;
     r.from_last = !A_MN;
     r.blocks = pl.split.cut >= 16 ? 16 : 64;

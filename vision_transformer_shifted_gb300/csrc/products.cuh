@@ -537,6 +537,8 @@ struct JoinArgs {
     PairSplit split;
     int tn, blocks;
     bool from_last;   // (tile_place)
+    int slots;        // partial tiles a pair has: 2, or 1 (its range lies in one tile)
+    bool single;      // a tile of one partial tile is joined too
     LinearJoin linear;
     struct {
         const bf16 *bias, *residual;
