@@ -428,7 +428,15 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         e = launch_maybe_overlapped(h->act == ACT_SILU ? act_grad_kernel<ACT_SILU> : act_grad_kernel<ACT_GELU>,
                                     dim3((unsigned)pg.columns, (unsigned)pg.slices), dim3(256), 0, s, 1, a);
     }
-    if (e == cudaSuccess && dx) e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0);
+    if (e == cudaSuccess && dx) {
+        // dx's epilogue warps, where they are on most SMs, join what the kernel before
+        // left, its tiles and db (12544 x 512 x 2048 60.4 us, 66 by a launch of its
+        // own; 300 x 512 x 1024, 8 pairs: 48.6 and 24)
+        const FinishArgs left = fin;
+        const bool side = pa.chosen && 8 * plx.split.np >= 3 * sm_count();
+        if (side) fin.joins[1] = fin.cs.n = 0;
+        e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0, side ? &left : nullptr);
+    }
     if (e == cudaSuccess && dW && !pa.chosen) e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
     const int rc2 = ows_end(&h->ws, s, ws, captured);

@@ -24,15 +24,34 @@ namespace swin {
 
 namespace {
 
-constexpr int WG_WARPS = 16, WG_THREADS = 64 + 32 * WG_WARPS, WG_MAX_STAGES = 4;
-constexpr int WG_A_BYTES = 32768;   // z and dy of a stage, 16 KB each (two boxes of 64 channels x 64 tokens)
+constexpr int WG_WARPS = 16, WG_THREADS = 96 + 32 * WG_WARPS;
+constexpr int WG_TILE = 16384;   // z or dy of a block (two boxes of 64 channels x 64 tokens)
+// Rings of their own: z's place (then dz's) is free when the MMAs are done, dy's as
+// soon as dz is formed, x's comes from L2 and needs the fewest.
+template <bool WIDE>   // more than 256 columns
+struct WgradRings {
+    static constexpr int Z = WIDE ? 4 : 5, Y = WIDE ? 3 : 4, X = WIDE ? 3 : 4, X_BYTES = WIDE ? 32768 : 16384;
+    static constexpr int BYTES = (Z + Y) * WG_TILE + X * X_BYTES;
+};
+// A place in a ring and the parity of its phase.
+struct RingAt {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int stages)
+    {
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
 struct WgradArgs {
     CUtensorMap z, dy, x, part;   // part: partial tiles [pairs][256][n] fp32
     bf16 *dz;                     // [rows, ld], or null
     float *sums;                  // [slices, N]: shares of db, or null
     int rows, N, ld;
-    int n, stages, stage_bytes;   // n: C rounded up to 32, 64 at least
+    int n;                        // C rounded up to 32, 64 at least
     int slices, kb, slice_kb;     // K blocks of all tokens, of a slice
     DeviceStatus st;
 };
@@ -49,13 +68,14 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr)
     return u;
 }
 
-template <int ACT>
+template <int ACT, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WG_THREADS, 1)
 act_wgrad_kernel(const __grid_constant__ WgradArgs a)
 {
+    using R = WgradRings<WIDE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_align(smem_raw, 1024);
-    __shared__ uint64_t bars[4 * WG_MAX_STAGES + 1];
+    __shared__ uint64_t bars[3 * R::Z + R::Y + 2 * R::X + 1];
     __shared__ uint32_t tslot;
     __shared__ float red[WG_WARPS][64];
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -63,16 +83,21 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
     const int pair = blockIdx.x >> 1, tile = pair / a.slices, slice = pair % a.slices;
     const int kb0 = slice * a.slice_kb, kb_n = (a.kb - kb0 < a.slice_kb ? a.kb - kb0 : a.slice_kb);
     const int ch0 = tile * 256 + (int)rank * 128;   // this CTA's first output channel
-    // per stage: z and dy have landed (own), x has (the leader's, of both CTAs), dz
-    // is formed (the leader's), the MMAs are done (both); the tile is complete (both)
-    const uint32_t afull = smem_u32(bars), bfull = afull + 8 * WG_MAX_STAGES, ready = bfull + 8 * WG_MAX_STAGES,
-                   empty = ready + 8 * WG_MAX_STAGES, done = empty + 8 * WG_MAX_STAGES;
+    // z and dy have landed (own), dz is formed (the leader's), the MMAs are done with
+    // it (both); dy has been read (own); x has landed (the leader's, of both CTAs), the
+    // MMAs are done with it (both); the tile is complete (both)
+    const uint32_t afull = smem_u32(bars), ready = afull + 8 * R::Z, zempty = ready + 8 * R::Z, yempty = zempty + 8 * R::Z,
+                   xfull = yempty + 8 * R::Y, xempty = xfull + 8 * R::X, done = xempty + 8 * R::X;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < R::Z; ++s) {
             mbar_init(afull + 8 * s, 1);
-            mbar_init(bfull + 8 * s, 1);
             mbar_init(ready + 8 * s, 2 * WG_WARPS);
-            mbar_init(empty + 8 * s, 1);
+            mbar_init(zempty + 8 * s, 1);
+        }
+        for (int s = 0; s < R::Y; ++s) mbar_init(yempty + 8 * s, WG_WARPS);
+        for (int s = 0; s < R::X; ++s) {
+            mbar_init(xfull + 8 * s, 1);
+            mbar_init(xempty + 8 * s, 1);
         }
         mbar_init(done, 1);
         mbar_init_fence();
@@ -92,47 +117,33 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
     bool failed = false;
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t ring = smem_u32(smem);
+    const uint32_t zring = smem_u32(smem), yring = zring + R::Z * WG_TILE, xring = yring + R::Y * WG_TILE;
     const int n0 = a.n < 256 ? a.n : 256, n1 = a.n - n0;   // columns of the one or two MMAs
 
     if (warp == 0) {
-        const uint32_t lead_bfull = map_rank(bfull, 0);
-        const uint32_t b_bytes = (b_boxes(n0) + (n1 ? b_boxes(n1) : 0)) * 8192;
-        int s = 0, issued = 0;
-        uint32_t ph = 0;
+        RingAt z, y;
+        int issued = 0;
 #pragma unroll 1
-        for (int i = 0; i < kb_n; ++i) {
-            if (!warp_pair_wait(empty + 8 * s, ph ^ 1u, a.st.wait_ns)) {
+        for (int i = 0; i < kb_n; ++i, ++issued, z.next(R::Z), y.next(R::Y)) {
+            if (!warp_pair_wait(zempty + 8 * z.s, z.ph ^ 1u, a.st.wait_ns) ||
+                !warp_pair_wait(yempty + 8 * y.s, y.ph ^ 1u, a.st.wait_ns)) {
                 failed = true;
                 break;
             }
             if (elect_one()) {
-                const uint32_t dst = ring + s * a.stage_bytes, own = afull + 8 * s, bar = lead_bfull + 8 * s;
+                const uint32_t zd = zring + z.s * WG_TILE, yd = yring + y.s * WG_TILE, bar = afull + 8 * z.s;
                 const int k = (kb0 + i) * 64;
-                mbar_arrive_expect_tx(own, WG_A_BYTES);
-                tma_load_2d(dst, &a.z, ch0, k, own);
-                tma_load_2d(dst + 8192, &a.z, ch0 + 64, k, own);
-                tma_load_2d(dst + 16384, &a.dy, ch0, k, own);
-                tma_load_2d(dst + 24576, &a.dy, ch0 + 64, k, own);
-                if (rank == 0) mbar_arrive_expect_tx(bfull + 8 * s, 2 * b_bytes);
-                const int c0 = (int)rank * (n0 / 2), c1 = 256 + (int)rank * (n1 / 2);
-                tma_load_2d_pair(dst + WG_A_BYTES, &a.x, c0, k, bar);
-                if (b_boxes(n0) > 1) tma_load_2d_pair(dst + WG_A_BYTES + 8192, &a.x, c0 + 64, k, bar);
-                if (n1) {
-                    tma_load_2d_pair(dst + WG_A_BYTES + 16384, &a.x, c1, k, bar);
-                    if (b_boxes(n1) > 1) tma_load_2d_pair(dst + WG_A_BYTES + 24576, &a.x, c1 + 64, k, bar);
-                }
-            }
-            ++issued;
-            if (++s == a.stages) {
-                s = 0;
-                ph ^= 1u;
+                mbar_arrive_expect_tx(bar, 2 * WG_TILE);
+                tma_load_2d(zd, &a.z, ch0, k, bar);
+                tma_load_2d(zd + 8192, &a.z, ch0 + 64, k, bar);
+                tma_load_2d(yd, &a.dy, ch0, k, bar);
+                tma_load_2d(yd + 8192, &a.dy, ch0 + 64, k, bar);
             }
         }
-        // every stage given back: no commit is on its way to this CTA's barriers
-        for (int k = 0; k < a.stages && k < issued && !failed; ++k) {
-            const RingUse u = last_use(a.stages, issued, k);
-            failed = !warp_pair_wait(empty + 8 * u.stage, u.parity, a.st.wait_ns);
+        // every place given back: no commit is on its way to this CTA's barriers
+        for (int k = 0; k < R::Z && k < issued && !failed; ++k) {
+            const RingUse u = last_use(R::Z, issued, k);
+            failed = !warp_pair_wait(zempty + 8 * u.stage, u.parity, a.st.wait_ns);
         }
         if (failed) {
             // (copies in flight land before the memory is given back)
@@ -143,31 +154,58 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
         if (rank == 0) {
             const uint32_t idesc = idesc_pair(MMA_BF16, true, true, 256, 0);
             const uint32_t idesc0 = idesc | (uint32_t)(n0 >> 3) << 17, idesc1 = idesc | (uint32_t)(n1 >> 3) << 17;
-            int s = 0;
-            uint32_t ph = 0;
+            RingAt z, x;
 #pragma unroll 1
-            for (int i = 0; i < kb_n; ++i) {
-                if (!warp_pair_wait(bfull + 8 * s, ph, a.st.wait_ns) || !warp_pair_wait(ready + 8 * s, ph, a.st.wait_ns)) {
+            for (int i = 0; i < kb_n; ++i, z.next(R::Z), x.next(R::X)) {
+                if (!warp_pair_wait(xfull + 8 * x.s, x.ph, a.st.wait_ns) || !warp_pair_wait(ready + 8 * z.s, z.ph, a.st.wait_ns)) {
                     failed = true;
                     break;
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t a16 = (ring + s * a.stage_bytes) >> 4, b16 = a16 + (WG_A_BYTES >> 4);
+                    const uint32_t a16 = (zring + z.s * WG_TILE) >> 4, b16 = (xring + x.s * R::X_BYTES) >> 4;
                     const int steps = kblock_steps(a.rows, kb0 + i, 64);
                     mma_kblock<MMA_BF16, true, true>(tmem, a16, b16, idesc0, steps, i == 0);
-                    if (n1) mma_kblock<MMA_BF16, true, true>(tmem + 256, a16, b16 + 1024, idesc1, steps, i == 0);
-                    mma_commit_pair(empty + 8 * s);
+                    if (WIDE) mma_kblock<MMA_BF16, true, true>(tmem + 256, a16, b16 + 1024, idesc1, steps, i == 0);
+                    mma_commit_pair(zempty + 8 * z.s);
+                    mma_commit_pair(xempty + 8 * x.s);
                     if (i == kb_n - 1) mma_commit_pair(done);
-                }
-                if (++s == a.stages) {
-                    s = 0;
-                    ph ^= 1u;
                 }
             }
         }
+    } else if (warp == 2) {
+        const uint32_t lead = map_rank(xfull, 0), bytes = (b_boxes(n0) + (WIDE ? b_boxes(n1) : 0)) * 8192;
+        const int c0 = (int)rank * (n0 / 2), c1 = 256 + (int)rank * (n1 / 2);
+        RingAt x;
+        int issued = 0;
+#pragma unroll 1
+        for (int i = 0; i < kb_n; ++i, ++issued, x.next(R::X)) {
+            if (!warp_pair_wait(xempty + 8 * x.s, x.ph ^ 1u, a.st.wait_ns)) {
+                failed = true;
+                break;
+            }
+            if (elect_one()) {
+                const uint32_t dst = xring + x.s * R::X_BYTES, bar = lead + 8 * x.s;
+                const int k = (kb0 + i) * 64;
+                if (rank == 0) mbar_arrive_expect_tx(xfull + 8 * x.s, 2 * bytes);
+                tma_load_2d_pair(dst, &a.x, c0, k, bar);
+                if (b_boxes(n0) > 1) tma_load_2d_pair(dst + 8192, &a.x, c0 + 64, k, bar);
+                if (WIDE) {
+                    tma_load_2d_pair(dst + 16384, &a.x, c1, k, bar);
+                    if (b_boxes(n1) > 1) tma_load_2d_pair(dst + 24576, &a.x, c1 + 64, k, bar);
+                }
+            }
+        }
+        for (int k = 0; k < R::X && k < issued && !failed; ++k) {
+            const RingUse u = last_use(R::X, issued, k);
+            failed = !warp_pair_wait(xempty + 8 * u.stage, u.parity, a.st.wait_ns);
+        }
+        if (failed) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
+        }
     } else {
-        const int w = warp - 2;
+        const int w = warp - 3;
         // this lane's two 16-byte pieces of the warp's atom: tokens t, t + 4, eight
         // channels (one logical chunk, so that its sums are of fixed channels)
         const int box = w & 1, chunk = lane & 7, t = lane >> 3;
@@ -177,18 +215,17 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
         const int c = ch0 + box * 64 + chunk * 8;
         const bool stored = a.dz && c < a.N;
         f2 sum[4] = {0, 0, 0, 0};
-        int s = 0;
-        uint32_t ph = 0;
+        RingAt z, y;
         int64_t row = (int64_t)kb0 * 64 + (w >> 1) * 8 + t;
 #pragma unroll 1
-        for (int i = 0; i < kb_n; ++i, row += 64) {
-            if (!warp_pair_wait(afull + 8 * s, ph, a.st.wait_ns)) {
+        for (int i = 0; i < kb_n; ++i, row += 64, z.next(R::Z), y.next(R::Y)) {
+            if (!warp_pair_wait(afull + 8 * z.s, z.ph, a.st.wait_ns)) {
                 failed = true;
                 break;
             }
-            const uint32_t base = ring + s * a.stage_bytes;
+            const uint32_t zat = zring + z.s * WG_TILE, yat = yring + y.s * WG_TILE;
             auto grad = [&](uint32_t at, int64_t r) {
-                const uint4 zu = lds16(base + at), du = lds16(base + 16384 + at);
+                const uint4 zu = lds16(zat + at), du = lds16(yat + at);
                 const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w}, dw[4] = {du.x, du.y, du.z, du.w};
                 uint32_t o[4];
 #pragma unroll
@@ -203,17 +240,16 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
                     o[e] = pack_bf16x2(lo, hi);
                 }
                 const uint4 u = make_uint4(o[0], o[1], o[2], o[3]);
-                sts16(base + at, u);
+                sts16(zat + at, u);
                 if (stored && r < a.rows) *reinterpret_cast<uint4 *>(a.dz + r * a.ld + c) = u;
             };
             grad(at0, row);
             grad(at1, row + 4);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_ready + 8 * s);
-            if (++s == a.stages) {
-                s = 0;
-                ph ^= 1u;
+            if (lane == 0) {
+                mbar_arrive_cluster(lead_ready + 8 * z.s);
+                mbar_arrive(yempty + 8 * y.s);
             }
         }
         // the lanes' sums, then those of the eight warps of the same channels
@@ -230,7 +266,7 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
                 }
             }
             asm volatile("bar.sync 1, %0;" ::"n"(32 * WG_WARPS) : "memory");
-            const int i = (int)threadIdx.x - 64;
+            const int i = (int)threadIdx.x - 96;
             if (i < 128 && ch0 + i < a.N) {
                 float v = 0.f;
                 for (int k = 0; k < WG_WARPS / 2; ++k) v += red[2 * k + (i >> 6)][i & 63];
@@ -270,21 +306,21 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int ACT>
+template <int ACT, bool WIDE>
 cudaError_t launch(const WgradArgs &a, int pairs, cudaStream_t stream)
 {
-    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes;
-    static std::atomic<uint64_t> ready;   // devices whose copy of the kernel may use the most shared memory
+    constexpr size_t smem = 1024 + WgradRings<WIDE>::BYTES;
+    static std::atomic<uint64_t> ready;   // devices whose copy of the kernel may use this much shared memory
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
-        e = cudaFuncSetAttribute(act_wgrad_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + 196608);
+        e = cudaFuncSetAttribute(act_wgrad_kernel<ACT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }
-    return launch_maybe_overlapped(act_wgrad_kernel<ACT>, dim3(2u * (unsigned)pairs), dim3(WG_THREADS), smem, stream, 1, a);
+    return launch_maybe_overlapped(act_wgrad_kernel<ACT, WIDE>, dim3(2u * (unsigned)pairs), dim3(WG_THREADS), smem, stream, 1, a);
 }
 
 } // namespace
@@ -322,8 +358,6 @@ cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceSta
     a.N = w.N;
     a.ld = w.ld;
     a.n = p.n;
-    a.stages = p.n > 256 ? 3 : 4;
-    a.stage_bytes = p.n > 256 ? 65536 : 49152;
     a.slices = p.slices;
     a.kb = p.kb;
     a.slice_kb = p.slice_kb;
@@ -343,7 +377,8 @@ cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceSta
     join->p[0] = {nullptr, nullptr, w.dW, w.N, w.C, p.tiles, 1, 0};
     join->p[1].first = join->p[2].first = 0x7fffffff;
     *join_blocks = p.tiles * join->blocks;
-    return w.act == ACT_SILU ? launch<ACT_SILU>(a, pairs, stream) : launch<ACT_GELU>(a, pairs, stream);
+    if (p.n > 256) return w.act == ACT_SILU ? launch<ACT_SILU, true>(a, pairs, stream) : launch<ACT_GELU, true>(a, pairs, stream);
+    return w.act == ACT_SILU ? launch<ACT_SILU, false>(a, pairs, stream) : launch<ACT_GELU, false>(a, pairs, stream);
 }
 
 } // namespace swin

@@ -26,84 +26,6 @@ constexpr int COST_192 = 82;
 // of what L2 delivers, three quarters of a whole tile's operands a pair.
 int half_cost(int halves, int pairs) { return halves * 75 > 55 * pairs ? halves * 75 / pairs : 55; }
 
-template <int VEC>
-__device__ __forceinline__ void add_vec(float (&v)[VEC], const float *p)
-{
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-        const float4 w = *reinterpret_cast<const float4 *>(p + k);
-        v[k] += w.x;
-        v[k + 1] += w.y;
-        v[k + 2] += w.z;
-        v[k + 3] += w.w;
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void add_vec(float (&v)[VEC], const bf16 *p)
-{
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p + k);
-        const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
-        v[k] += x.x;
-        v[k + 1] += x.y;
-        v[k + 2] += y.x;
-        v[k + 3] += y.y;
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void store_vec(bf16 *p, const float (&v)[VEC])
-{
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4)
-        *reinterpret_cast<uint2 *>(p + k) = make_uint2(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]));
-}
-template <int VEC>
-__device__ __forceinline__ void join_tiles(const JoinArgs &a, int block)
-{
-    const PairSplit &s = a.split;
-    const int c = block / a.blocks, t = s.full * s.np + c;
-    const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
-    if (p0 == p1 && !a.single) return;   // (one pair had the whole tile and wrote it)
-    const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
-    int m, n;
-    tile_order(tile_place(t - a.p[i].first, a.p[i].mt, a.p[i].nt, a.from_last), a.p[i].mt, a.p[i].nt, m, n);
-    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / VEC;
-    const int64_t size = 256 * a.tn;
-    const int first = a.slots == 1 ? p0 : s.slot(p0, c);
-    for (int e = block % a.blocks * 256 + threadIdx.x; e < 256 * per; e += a.blocks * 256) {
-        const int row = m * 256 + e / per, col = n * a.tn + e % per * VEC;
-        if (row >= rows || col >= cols) continue;
-        const float *src = a.part + (int64_t)e * VEC;
-        float v[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) v[k] = 0.f;
-        add_vec<VEC>(v, src + first * size);
-#pragma unroll 4
-        for (int p = p0 + 1; p <= p1; ++p)   // (these begin inside the tile: their first range)
-            add_vec<VEC>(v, src + a.slots * p * size);
-        const int64_t at = (int64_t)row * cols + col;
-        if (a.linear.sx) {
-            const float sx = a.linear.sx[row];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) v[k] *= sx * a.linear.sw[col + k];
-        }
-        if (a.p[i].bias) add_vec<VEC>(v, a.p[i].bias + col);
-        if (a.linear.on) {
-            if (a.linear.z) store_vec<VEC>(a.linear.z + at, v);
-#pragma unroll
-            for (int k = 0; k < VEC; k += 2) {
-                const f2 g = pack2(v[k], v[k + 1]);
-                unpack2(a.linear.act == ACT_SILU ? activate2<ACT_SILU>(g)
-                                                 : a.linear.act == ACT_GELU ? activate2<ACT_GELU>(g) : g,
-                        v[k], v[k + 1]);
-            }
-        }
-        if (a.p[i].residual) add_vec<VEC>(v, a.p[i].residual + at);
-        store_vec<VEC>(a.p[i].out + at, v);
-    }
-}
-
 __host__ __device__ inline int column_blocks(const ColumnSums &cs, int i) { return (cs.m[i].cols + 7) / 8; }
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a)
 {
@@ -113,8 +35,10 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
     int b = blockIdx.x;
     for (int i = 0; i < 2; ++i) {
         if (b < a.joins[i]) {
-            if (a.join[i].blocks == 16) join_tiles<8>(a.join[i], b);
-            else join_tiles<4>(a.join[i], b);
+            const JoinArgs &j = a.join[i];
+            const int first = b % j.blocks * 256 + (int)threadIdx.x;
+            if (j.blocks == 16) join_tile<8>(j, b / 16, first, 16 * 256);
+            else join_tile<4>(j, b / 64, first, 64 * 256);
             return;
         }
         b -= a.joins[i];
@@ -213,7 +137,8 @@ namespace {
 
 template <int TN, bool A_MN, bool B_MN>
 cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                              cudaStream_t stream, int *launches, FinishArgs *fin, int slot)
+                              cudaStream_t stream, int *launches, FinishArgs *fin, int slot,
+                              const FinishArgs *side)
 {
     typename GemmPolicy<TN, A_MN, B_MN>::Args a;
     memset(&a, 0, sizeof(a));
@@ -253,6 +178,11 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     }
     a.split = r.split = pl.split;
     if (A_MN) a.sums = fin->cs;
+    if (!A_MN && side) {
+        a.side = side->join[1];
+        a.joined = a.side.split.cut;
+        a.sums = side->cs;
+    }
     a.wn = pl.wn;
     a.np = pl.split.np;
     a.st = st;
@@ -274,16 +204,17 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
 
 template <bool A_MN, bool B_MN>
 cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot)
+                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot,
+                              const FinishArgs *side)
 {
-    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot)
-                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot);
+    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot, side)
+                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot, side);
 }
 template cudaError_t launch_products<false, false>(const Product *, const ProductsPlan &, float *, DeviceStatus, cudaStream_t,
-                                                   int *, FinishArgs *, int);
+                                                   int *, FinishArgs *, int, const FinishArgs *);
 template cudaError_t launch_products<false, true>(const Product *, const ProductsPlan &, float *, DeviceStatus, cudaStream_t,
-                                                  int *, FinishArgs *, int);
+                                                  int *, FinishArgs *, int, const FinishArgs *);
 template cudaError_t launch_products<true, true>(const Product *, const ProductsPlan &, float *, DeviceStatus, cudaStream_t,
-                                                 int *, FinishArgs *, int);
+                                                 int *, FinishArgs *, int, const FinishArgs *);
 
 } // namespace swin

@@ -274,13 +274,119 @@ __device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int 
 // 672 forward 104.3 us from the first, 101.8; 200704 x 96 x 256 backward 210.7, 207.6).
 __host__ __device__ inline int tile_place(int t, int mt, int nt, bool from_last) { return from_last ? mt * nt - 1 - t : t; }
 
+// What the linear operator's tiles go through beside bias and residual.
+struct LinearJoin {
+    bool on;
+    int act;                // ACT_*, after the bias
+    const float *sx, *sw;   // 8 bits: scales of rows and columns, else null
+    bf16 *z;                // where the value before the activation is kept, or null
+};
+// The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
+// of K (+ bias + residual).  `blocks` blocks a tile and VEC values a thread at a
+// time: 16 and eight, or (few tiles, of many partial tiles each) 64 and four;
+// 3 tiles of 25 partial tiles: 9 us, 15 by sixteen blocks.
+struct JoinArgs {
+    const float *part;
+    PairSplit split;
+    int tn, blocks;
+    bool from_last;   // (tile_place)
+    int slots;        // partial tiles a pair has: 2, or 1 (its range lies in one tile)
+    bool single;      // a tile of one partial tile is joined too
+    LinearJoin linear;
+    struct {
+        const bf16 *bias, *residual;
+        bf16 *out;
+        int rows, cols, mt, nt, first;
+    } p[3];
+};
+template <int VEC>
+__device__ __forceinline__ void add_vec(float (&v)[VEC], const float *p)
+{
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + k);
+        v[k] += w.x;
+        v[k + 1] += w.y;
+        v[k + 2] += w.z;
+        v[k + 3] += w.w;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void add_vec(float (&v)[VEC], const bf16 *p)
+{
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p + k);
+        const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
+        v[k] += x.x;
+        v[k + 1] += x.y;
+        v[k + 2] += y.x;
+        v[k + 3] += y.y;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(bf16 *p, const float (&v)[VEC])
+{
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4)
+        *reinterpret_cast<uint2 *>(p + k) = make_uint2(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]));
+}
+// Values e0, e0 + step, ... (VEC at a time) of cut tile c.
+template <int VEC>
+__device__ __forceinline__ void join_tile(const JoinArgs &a, int c, int e0, int step)
+{
+    const PairSplit &s = a.split;
+    const int t = s.full * s.np + c;
+    const int p0 = s.owner((uint32_t)c * s.kb), p1 = s.owner((uint32_t)(c + 1) * s.kb - 1);
+    if (p0 == p1 && !a.single) return;   // (one pair had the whole tile and wrote it)
+    const int i = t >= a.p[2].first ? 2 : t >= a.p[1].first ? 1 : 0;
+    int m, n;
+    tile_order(tile_place(t - a.p[i].first, a.p[i].mt, a.p[i].nt, a.from_last), a.p[i].mt, a.p[i].nt, m, n);
+    const int rows = a.p[i].rows, cols = a.p[i].cols, per = a.tn / VEC;
+    const int64_t size = 256 * a.tn;
+    const int first = a.slots == 1 ? p0 : s.slot(p0, c);
+    for (int e = e0; e < 256 * per; e += step) {
+        const int row = m * 256 + e / per, col = n * a.tn + e % per * VEC;
+        if (row >= rows || col >= cols) continue;
+        const float *src = a.part + (int64_t)e * VEC;
+        float v[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = 0.f;
+        add_vec<VEC>(v, src + first * size);
+#pragma unroll 8
+        for (int p = p0 + 1; p <= p1; ++p)   // (these begin inside the tile: their first range)
+            add_vec<VEC>(v, src + a.slots * p * size);
+        const int64_t at = (int64_t)row * cols + col;
+        if (a.linear.sx) {
+            const float sx = a.linear.sx[row];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[k] *= sx * a.linear.sw[col + k];
+        }
+        if (a.p[i].bias) add_vec<VEC>(v, a.p[i].bias + col);
+        if (a.linear.on) {
+            if (a.linear.z) store_vec<VEC>(a.linear.z + at, v);
+#pragma unroll
+            for (int k = 0; k < VEC; k += 2) {
+                const f2 g = pack2(v[k], v[k + 1]);
+                unpack2(a.linear.act == ACT_SILU ? activate2<ACT_SILU>(g)
+                                                 : a.linear.act == ACT_GELU ? activate2<ACT_GELU>(g) : g,
+                        v[k], v[k + 1]);
+            }
+        }
+        if (a.p[i].residual) add_vec<VEC>(v, a.p[i].residual + at);
+        store_vec<VEC>(a.p[i].out + at, v);
+    }
+}
+
 template <int TN, bool A_MN, bool B_MN>
 struct GemmPolicy {
     struct Args {
         PairProblem p[3];
         CUtensorMap part;   // partial tiles [2 np][256][TN] fp32
         PairSplit split;
-        ColumnSums sums;    // with A_MN: summed under the first tile's MMAs
+        ColumnSums sums;    // with A_MN: summed under the first tile's MMAs; else their last additions are
+        JoinArgs side;      // another product's cut tiles, joined there too (joined: how many)
+        int joined;
         int wn;             // columns of a tile: TN, or 192 of 256
         int np;
         DeviceStatus st;
@@ -327,7 +433,26 @@ struct GemmPolicy {
     }
     static __device__ __forceinline__ void side(const Args &a, int w, int lane)
     {
-        if (A_MN) column_partials(a.sums, w, 2 * a.np * EPI, lane);   // (the weight gradients)
+        if (A_MN) {
+            column_partials(a.sums, w, 2 * a.np * EPI, lane);   // (the weight gradients)
+            return;
+        }
+        if (!a.joined) return;
+        // (neighbouring warps' shares go to different CTAs: there may be few)
+        const int ctas = 2 * a.np, first = (w % EPI * ctas + w / EPI) * 32 + lane, threads = ctas * EPI * 32,
+                  per = 64 * a.side.tn;   // fours of a tile
+#pragma unroll 1
+        for (int i = first; i < a.joined * per; i += threads) join_tile<4>(a.side, i / per, i % per, per);
+        if (a.sums.n) {
+            const auto &m = a.sums.m[0];
+#pragma unroll 1
+            for (int c = first; c < m.cols; c += threads) {
+                float v = 0.f;
+#pragma unroll 4
+                for (int s = 0; s < m.slices; ++s) v += m.part[(int64_t)s * m.cols + c];
+                m.out[c] = __float2bfloat16_rn(v);
+            }
+        }
     }
     static __device__ __forceinline__ int kblocks(const Args &, const Unit &u, int) { return u.kbn; }
     static __device__ __forceinline__ uint32_t tx(const Args &, const Unit &u, int)
@@ -521,32 +646,6 @@ struct Product {
     int cols;
 };
 
-// What the linear operator's tiles go through beside bias and residual.
-struct LinearJoin {
-    bool on;
-    int act;                // ACT_*, after the bias
-    const float *sx, *sw;   // 8 bits: scales of rows and columns, else null
-    bf16 *z;                // where the value before the activation is kept, or null
-};
-// The cut tiles of a launch: out = the sum of a tile's partial tiles in the order
-// of K (+ bias + residual).  `blocks` blocks a tile and VEC values a thread at a
-// time: 16 and eight, or (few tiles, of many partial tiles each) 64 and four;
-// 3 tiles of 25 partial tiles: 9 us, 15 by sixteen blocks.
-struct JoinArgs {
-    const float *part;
-    PairSplit split;
-    int tn, blocks;
-    bool from_last;   // (tile_place)
-    int slots;        // partial tiles a pair has: 2, or 1 (its range lies in one tile)
-    bool single;      // a tile of one partial tile is joined too
-    LinearJoin linear;
-    struct {
-        const bf16 *bias, *residual;
-        bf16 *out;
-        int rows, cols, mt, nt, first;
-    } p[3];
-};
-
 // What is left of a call when its products are done, as one launch: the cut
 // tiles of up to two of them, and the last additions of the column sums, eight
 // columns a block and 32 threads a column.
@@ -574,10 +673,13 @@ struct ProductsPlan {
 // The plan of n products as one launch (elems: K elements of a block).
 ProductsPlan plan_products(const Product *p, int n, int elems = 64);
 // Queues the products (operands K- or MN-major: A, B both K; B MN; both MN); what
-// is left to do for their cut tiles goes into fin->join[slot].
+// is left to do for their cut tiles goes into fin->join[slot].  With A_MN their
+// epilogue warps begin fin's column sums.  Without, they can do what `side` leaves
+// to do of a kernel queued before, joins (of slot 1) and sums of few slices: under
+// their first tile's MMAs, so that no launch is needed for it.
 template <bool A_MN, bool B_MN>
 cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot);
+                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot, const FinishArgs *side = nullptr);
 cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launches);
 
 // Workspace layout: bytes of each part, 1 KB aligned.
