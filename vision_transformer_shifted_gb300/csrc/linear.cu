@@ -238,6 +238,8 @@ GradPlan plan_grad(int N, int64_t rows)
     return p;
 }
 
+constexpr int SIDE_SLICES = 512;   // partial rows of db that dx's warps add
+
 // The shapes of the backward's products.
 Product dx_product(int C, int N, int rows, int ld)
 {
@@ -428,16 +430,25 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         e = launch_maybe_overlapped(h->act == ACT_SILU ? act_grad_kernel<ACT_SILU> : act_grad_kernel<ACT_GELU>,
                                     dim3((unsigned)pg.columns, (unsigned)pg.slices), dim3(256), 0, s, 1, a);
     }
+    // What dW's kernel leaves, cut tiles and db's partial rows, is finished by dx's
+    // epilogue warps under their first tile's MMAs: where they are on most SMs, db's
+    // rows are few, and no launch is left to save otherwise (dx's own cut tiles).
+    // 12544 x 512 x 2048 GELU 60.2 us, 69.7 by a launch of its own, 50000 x 256 x 1024
+    // 80 and 91, 2000 x 2048 x 2048 36.4 and 42.3; 300 x 512 x 1024, on 16 SMs, 48.6
+    // and 24.
+    auto weight = [&]() {
+        if (e == cudaSuccess && dW && !pa.chosen)
+            e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
+    };
+    const bool side = dx && dW && (pa.chosen || plw.split.cut || db) && (!db || fin.cs.m[0].slices <= SIDE_SLICES) &&
+                      !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
+    if (side) weight();
     if (e == cudaSuccess && dx) {
-        // dx's epilogue warps, where they are on most SMs, join what the kernel before
-        // left, its tiles and db (12544 x 512 x 2048 60.4 us, 66 by a launch of its
-        // own; 300 x 512 x 1024, 8 pairs: 48.6 and 24)
         const FinishArgs left = fin;
-        const bool side = pa.chosen && 8 * plx.split.np >= 3 * sm_count();
         if (side) fin.joins[1] = fin.cs.n = 0;
         e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0, side ? &left : nullptr);
     }
-    if (e == cudaSuccess && dW && !pa.chosen) e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
+    if (!side) weight();
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;

@@ -180,7 +180,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     if (A_MN) a.sums = fin->cs;
     if (!A_MN && side) {
         a.side = side->join[1];
-        a.joined = a.side.split.cut;
+        a.joined = side->joins[1] ? a.side.split.cut : 0;
         a.sums = side->cs;
     }
     a.wn = pl.wn;

@@ -437,20 +437,22 @@ struct GemmPolicy {
             column_partials(a.sums, w, 2 * a.np * EPI, lane);   // (the weight gradients)
             return;
         }
-        if (!a.joined) return;
+        if (!a.joined && !a.sums.n) return;
         // (neighbouring warps' shares go to different CTAs: there may be few)
         const int ctas = 2 * a.np, first = (w % EPI * ctas + w / EPI) * 32 + lane, threads = ctas * EPI * 32,
                   per = 64 * a.side.tn;   // fours of a tile
 #pragma unroll 1
         for (int i = first; i < a.joined * per; i += threads) join_tile<4>(a.side, i / per, i % per, per);
-        if (a.sums.n) {
+        if (a.sums.n) {   // (a warp eight columns, four lanes a column)
             const auto &m = a.sums.m[0];
 #pragma unroll 1
-            for (int c = first; c < m.cols; c += threads) {
+            for (int c = first / 32 * 8 + (lane & 7); c - (lane & 7) < m.cols; c += threads / 32 * 8) {
                 float v = 0.f;
-#pragma unroll 4
-                for (int s = 0; s < m.slices; ++s) v += m.part[(int64_t)s * m.cols + c];
-                m.out[c] = __float2bfloat16_rn(v);
+#pragma unroll 8
+                for (int s = lane >> 3; s < m.slices; s += 4) v += m.part[(int64_t)s * m.cols + c];
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (lane < 8) m.out[c] = __float2bfloat16_rn(v);   // (cols is a multiple of 8)
             }
         }
     }
