@@ -275,7 +275,7 @@ def test_plan_refuses():
 # ---- GPU ---------------------------------------------------------------------------
 
 SHAPES = [   # rows, C, N
-    (1, 8, 8), (1, 96, 384), (1, 512, 1368), (2, 64, 64), (5, 136, 120), (17, 128, 264), (24, 1024, 2048),
+    (1, 8, 8), (1, 96, 384), (1, 512, 1368), (1, 8208, 40), (1, 1040, 6152), (2, 64, 64), (5, 136, 120), (17, 128, 264), (24, 1024, 2048),
     (64, 256, 640), (127, 192, 512), (128, 96, 128), (129, 328, 136), (256, 512, 512), (300, 1032, 2056),
     (515, 128, 384), (1000, 64, 1024), (3001, 96, 384), (2048, 768, 1024), (700, 4096, 120), (300, 8208, 264)]
 
@@ -401,7 +401,35 @@ def test_nan_and_infinity_stay_in_their_rows_and_columns(rows):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,behind", [(77, 51), (300, 100)])
+def test_one_row_with_nan_and_infinity():
+    """Single tokens have a kernel of their own: what is not finite stays in its
+    channel, or, in x, reaches all; e4m3 NaN codes too."""
+    C, N = 528, 136
+    x, w, b, r, _ = make(1, C, N, seed=20)
+    w[11, 5], b[13], r[0, 20] = float("inf"), float("-inf"), float("nan")
+    good = [i for i in range(N) if i not in (11, 13, 20)]
+    _, out, _, eo = forward_ref(x, w[good], b[good], r[:, good], "gelu")
+    got, kept = nans(1, N), nans(1, N)
+    (x8, sx), (w8, sc) = quantise(x), quantise(make(1, C, N, seed=20)[1])
+    w8 = w8.view(torch.uint8)
+    w8[17, 500] = 0x7f   # NaN
+    w8 = w8.view(E4M3)
+    got8 = nans(1, N)
+    with linear(C, N, "gelu") as h:
+        sw.swin_block_linear_forward(h, *dev(x, w, b), got, residual=dev(r), z=kept)
+        sw.swin_block_linear_forward_q8(h, *dev(x8, sx, w8, sc), None, got8)
+        x[0, 500] = float("nan")
+        bad = nans(1, N)
+        sw.swin_block_linear_forward(h, *dev(x, w, b), bad)
+        sw.swin_block_linear_sync_status(h)
+    close(got[:, good], out, eo)
+    assert not got[0, [11]].isfinite().any() and got[0, 20].isnan() and kept[0, 13] == float("-inf")
+    assert bad.isnan().all()
+    assert got8[0, 17].isnan() and got8.isnan().sum() == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,behind", [(1, 4), (77, 51), (300, 100)])
 def test_in_place_and_rows_behind_the_batch(rows, behind):
     C, N = 192, 520
     x, w, b, r, dy = make(rows + behind, C, N, seed=4)

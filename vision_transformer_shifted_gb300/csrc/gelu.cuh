@@ -103,4 +103,25 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
     return r;
 }
 
+// bf16 pairs with fp32 ones, exact operands and one rounding each: w + c, and the
+// product a b.
+__device__ __forceinline__ f2 add_bf16x2(uint32_t w, f2 c)
+{
+    f2 r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .f32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b64 {x, y}, %2;\n\t"
+        "add.f32.bf16 x, l, x;\n\tadd.f32.bf16 y, h, y;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "r"(w), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul_bf16x2(uint32_t a, uint32_t b)
+{
+    f2 r;
+    asm("{\n\t.reg .b16 l, h, m, n;\n\t.reg .f32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {m, n}, %2;\n\t"
+        "fma.rn.f32.bf16 x, l, m, 0f00000000;\n\tfma.rn.f32.bf16 y, h, n, 0f00000000;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
+
 } // namespace swin

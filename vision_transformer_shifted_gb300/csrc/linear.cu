@@ -125,7 +125,8 @@ int forward(swin_block_linear_s *h, const Forward &f, cudaStream_t stream)
     if (f.rows <= FEW_ROWS) {
         h->last_launches = 1;
         const FewLinear u{f.x, f.w, f.bias, f.residual, f.sx, f.sw, f.out, f.z, f.rows, h->C, h->N, h->act};
-        return launch_few_linear(u, st, stream) == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA;
+        const cudaError_t e = f.rows == 1 ? launch_token_linear(u, stream) : launch_few_linear(u, st, stream);
+        return e == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA;
     }
     const Product p = forward_product(h->C, h->N, f.rows);
     const ProductsPlan pl = plan_products(&p, 1, elems(q8));

@@ -104,6 +104,21 @@ struct LinearPolicy {
         }
         cp_async_commit();
     }
+    // p += the eight bf16 values of u; and p's eight rounded.
+    static __device__ __forceinline__ void add_words(f2 *p, const uint4 &u)
+    {
+        p[0] = add_bf16x2(u.x, p[0]);
+        p[1] = add_bf16x2(u.y, p[1]);
+        p[2] = add_bf16x2(u.z, p[2]);
+        p[3] = add_bf16x2(u.w, p[3]);
+    }
+    static __device__ __forceinline__ uint4 pack_words(const f2 *p)
+    {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unpack2(p[e], v[2 * e], v[2 * e + 1]);
+        return pack8f(v);
+    }
     struct Pre {
         float bias, sw, sx;   // of this lane's column of the first box, and its row's scale
     };
@@ -196,38 +211,37 @@ struct LinearPolicy {
             tmem_wait_ld();
             if (j == count - 1) release();
             const int col0 = col_of(u, part, j);
+            f2 p[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float s[8];
-                if (Q8) {
+            for (int e = 0; e < 16; ++e) p[e] = pack2(v[2 * e], v[2 * e + 1]);
+            if (Q8) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float s[8];
                     spread8(scales, q, s);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[8 * q + e] *= pre.sx * s[e];
+                    for (int e = 0; e < 4; ++e)
+                        p[4 * q + e] = mul2(p[4 * q + e], mul2(pack2(pre.sx), pack2(s[2 * e], s[2 * e + 1])));
                 }
-                if (a.bias) {
-                    load8(vec, 8 * q, 32, s);
-                    add8(v + 8 * q, s);
-                }
-                if (a.keep) *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack8f(v + 8 * q);
+            }
+            if (a.bias) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) add_words(p + 4 * q, *reinterpret_cast<const uint4 *>(vec + 8 * q));
             }
             if (a.keep) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(stage + sw64_offset(lane, q)) = pack_words(p + 4 * q);
                 store_box(&a.z, col0, row0, inside, stage, lane);
                 if (lane == 0) bulk_wait_read1();   // (out's box before)
                 __syncwarp();
             }
 #pragma unroll
+            for (int e = 0; e < 16; ++e) p[e] = activate2<ACT>(p[e]);
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint4 *at = reinterpret_cast<uint4 *>(box + sw64_offset(lane, q));
-#pragma unroll
-                for (int e = 0; e < 8; e += 2)
-                    unpack2(activate2<ACT>(pack2(v[8 * q + e], v[8 * q + e + 1])), v[8 * q + e], v[8 * q + e + 1]);
-                if (a.residual) {
-                    float b[8];
-                    const uint4 r = own ? res[q] : *at;
-                    load8(reinterpret_cast<const bf16 *>(&r), 0, 8, b);
-                    add8(v + 8 * q, b);
-                }
-                *at = pack8f(v + 8 * q);
+                if (a.residual) add_words(p + 4 * q, own ? res[q] : *at);
+                *at = pack_words(p + 4 * q);
             }
             store_box(&a.out, col0, row0, inside, box, lane);
         }

@@ -709,5 +709,7 @@ struct FewLinear {
     int rows, C, N, act;    // act: ACT_*
 };
 cudaError_t launch_few_linear(const FewLinear &u, DeviceStatus st, cudaStream_t stream);
+// The same for one row (linear_token.cu).
+cudaError_t launch_token_linear(const FewLinear &u, cudaStream_t stream);
 
 } // namespace swin
