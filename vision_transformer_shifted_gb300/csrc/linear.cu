@@ -96,6 +96,9 @@ cudaError_t launch_linear(const Forward &f, int C, int N, const ProductsPlan &pl
     a.mt = ceil_div(f.rows, 256);
     a.nt = ceil_div(N, pl.wn);
     a.wn = pl.wn;
+    // (t d < 2^32 for all tiles t: the product's error is then below 1 / d)
+    const int64_t d = 8ll * a.nt;
+    a.per_band = (int64_t)a.mt * a.nt * d < (1ll << 32) ? (uint32_t)(((1ll << 32) + d - 1) / d) : 0;
     a.np = pl.split.np;
     a.keep = f.z != nullptr;
     a.st = st;
