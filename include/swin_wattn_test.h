@@ -113,12 +113,15 @@ int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side);
 
 /* How the linear operator (swin_linear.h) divides a product, as
  * swin_block_gated_test_plan does: the forward (bf16 or 8-bit, more than 128
- * rows), dx or dW. */
+ * rows), dx or dW.  dW through an activation: {tiles of 256 rows, CTA pairs,
+ * columns of a tile, tiles across dW's columns, slices of the tokens, 1 if that
+ * kernel is taken rather than dz apart and the product}. */
 enum {
     SWIN_BLOCK_LINEAR_PLAN_FORWARD = 0,
     SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8 = 1,
     SWIN_BLOCK_LINEAR_PLAN_DX = 2,
-    SWIN_BLOCK_LINEAR_PLAN_WEIGHT = 3
+    SWIN_BLOCK_LINEAR_PLAN_WEIGHT = 3,
+    SWIN_BLOCK_LINEAR_PLAN_ACT_WEIGHT = 4
 };
 int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan);
 

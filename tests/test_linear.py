@@ -266,8 +266,22 @@ def test_plans_of_the_tested_sizes():
         assert (columns, halves > 0, cut > 0, equal) == want, args
 
 
+def test_plans_of_the_weight_gradient_through_an_activation():
+    """Tiles of one and of two columns' MMAs, several across, one slice and many, and
+    sizes where dz is formed apart: what the tested sizes reach on 152 SMs."""
+    plan = lambda *a: sw.swin_block_linear_test_plan(*a, sw.BLOCK_LINEAR_PLAN_ACT_WEIGHT)  # noqa: E731
+    for args, want in [   # columns of a tile, tiles across, slices
+            ((96, 384, 20000), (96, 1, 35)), ((512, 2048, 2500), (512, 1, 8)), ((768, 768, 3000), (384, 2, 12)),
+            ((1032, 1000, 4000), (352, 3, 6)), ((8, 136, 4000), (64, 1, 63)), ((24, 10008, 10000), (64, 1, 1)),
+            ((2048, 264, 5000), (512, 4, 9))]:
+        tiles, pairs, columns, across, slices, chosen = plan(*args)
+        assert chosen and (columns, across, slices) == want and pairs == tiles * slices, args
+    for args in ((512, 1368, 1), (4096, 120, 700), (1032, 2056, 300), (136, 65536, 33000), (96, 128, 128)):
+        assert not plan(*args)[5], args
+
+
 def test_plan_refuses():
-    for a in ((0, 8, 300, 0), (8, 12, 300, 0), (8, 8, 0, 0), (8, 8, 300, 4)):
+    for a in ((0, 8, 300, 0), (8, 12, 300, 0), (8, 8, 0, 0), (8, 8, 300, 5)):
         with pytest.raises(sw.SwinWAttnError):
             sw.swin_block_linear_test_plan(*a)
 
@@ -345,7 +359,7 @@ def test_backward(rows, C, N, kind):
 
 LARGE = [   # rows, C, N: more tiles than CTA pairs, thin last rounds, long K
     (2500, 512, 2048), (5001, 144, 520), (1300, 2048, 2056), (20000, 264, 336), (20000, 96, 384), (6000, 520, 1032),
-    (9000, 384, 96)]
+    (9000, 384, 96), (3000, 768, 768), (4000, 1032, 1000), (4000, 8, 136), (10000, 24, 10008), (5000, 2048, 264)]
 
 
 @pytest.mark.gpu

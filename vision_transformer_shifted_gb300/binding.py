@@ -24,6 +24,7 @@ BLOCK_OPT_OVERLAP_CALLS = 1
 BLOCK_GATED_SILU, BLOCK_GATED_GELU = 0, 1
 BLOCK_LINEAR_NONE, BLOCK_LINEAR_SILU, BLOCK_LINEAR_GELU = 0, 1, 2
 BLOCK_LINEAR_PLAN_FORWARD, BLOCK_LINEAR_PLAN_FORWARD_Q8, BLOCK_LINEAR_PLAN_DX, BLOCK_LINEAR_PLAN_WEIGHT = 0, 1, 2, 3
+BLOCK_LINEAR_PLAN_ACT_WEIGHT = 4
 BLOCK_GATED_PLAN_DOWN, BLOCK_GATED_PLAN_DX, BLOCK_GATED_PLAN_WEIGHTS, BLOCK_GATED_PLAN_NARROW = 0, 1, 2, 3
 PATH_AUTO, PATH_THREE_KERNELS, PATH_FUSED, PATH_FP32 = 0, 1, 2, 3
 

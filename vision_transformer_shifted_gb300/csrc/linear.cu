@@ -384,7 +384,7 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     const int ld = act ? hidden_ld(h->N) : h->N;
     Product px = dx_product(h->C, h->N, rows, ld), pw = weight_product(h->C, h->N, rows, ld);
     const ProductsPlan plx = dx ? plan_products(&px, 1) : ProductsPlan{}, plw = dW ? plan_products(&pw, 1) : ProductsPlan{};
-    const ActWgradPlan pa = act && dW ? plan_act_wgrad(h->C, h->N, rows) : ActWgradPlan{};
+    const ActWgradPlan pa = act && dW ? plan_act_wgrad(h->C, h->N, rows, plw) : ActWgradPlan{};
     const GradPlan pg = plan_grad(h->N, rows);
     FinishArgs fin{};
     size_t sum_bytes = 0;
@@ -465,6 +465,13 @@ int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan)
     if (C <= 0 || C % 8 || C > MAX_WIDTH || N <= 0 || N % 8 || N > MAX_WIDTH || rows <= 0 || rows > MAX_ROWS || !plan)
         return SWIN_WATTN_EINVAL;
     Product p;
+    if (which == SWIN_BLOCK_LINEAR_PLAN_ACT_WEIGHT) {
+        p = weight_product(C, N, rows, N);
+        const ActWgradPlan a = plan_act_wgrad(C, N, rows, plan_products(&p, 1));
+        const int v[] = {a.tiles, a.tiles * a.slices, a.n, a.nt, a.slices, a.chosen};
+        memcpy(plan, v, sizeof(v));
+        return SWIN_WATTN_OK;
+    }
     if (which == SWIN_BLOCK_LINEAR_PLAN_FORWARD || which == SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8) p = forward_product(C, N, rows);
     else if (which == SWIN_BLOCK_LINEAR_PLAN_DX) p = dx_product(C, N, rows, N);
     else if (which == SWIN_BLOCK_LINEAR_PLAN_WEIGHT) p = weight_product(C, N, rows, N);

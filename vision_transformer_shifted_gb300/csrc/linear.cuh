@@ -272,10 +272,11 @@ struct ActWgrad {
 struct ActWgradPlan {
     bool chosen;          // rather than dz by a kernel of its own
     int n, tiles, slices; // columns of a tile, tiles of 256 rows of dW, slices of the tokens
+    int mt, nt;           // the tiles' rows and columns
     int kb, slice_kb;
     size_t part_bytes;
 };
-ActWgradPlan plan_act_wgrad(int C, int N, int rows);
+ActWgradPlan plan_act_wgrad(int C, int N, int rows, const ProductsPlan &apart);
 // Queues the kernel; the join of its partial tiles is left to launch_finish.
 cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceStatus st, cudaStream_t stream, JoinArgs *join,
                              int *join_blocks);

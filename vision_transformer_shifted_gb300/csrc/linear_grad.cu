@@ -1,20 +1,23 @@
 // The weight gradient of a linear layer with an activation, dW = dz^T x with dz =
-// dy act'(z), from z and dy themselves: for up to 512 input channels one tile holds
-// all columns of dW, so that every element of z and dy is read once, by the pair
-// whose tile it belongs to; dz is formed in shared memory, where the MMAs read it,
-// and written once for dx's product.  As a kernel of its own (act_grad_kernel) dz
-// costs a trip of z and dy through the SMs that feeds nothing, and a second one of
-// dz: 12544 x 512 x 2048 91 us, with this kernel 73.6.
+// dy act'(z), from z and dy themselves: a tile has up to 512 columns of dW, so that
+// few pairs (up to 512 input channels: one) read an element of z and dy; dz is
+// formed in shared memory, where the MMAs read it, and written once for dx's
+// product.  As a kernel of its own (act_grad_kernel) dz costs a trip of z and dy
+// through the SMs that feeds nothing, and another one of dz.
 //
-// A CTA pair takes a tile of 256 output channels (128 a CTA, the rows of dW) x all
-// input channels and a slice of the tokens; TMEM holds the tile (up to 512
-// columns), the slices' partial tiles are joined by finish_kernel.  Per K block of
-// 64 tokens a CTA loads its 64 x 128 of z and of dy (its own barrier) and its half
-// of x's columns (the leader's); sixteen warps turn z into dz in place, a 1 KB atom
-// of the swizzled tile (8 tokens x 64 channels) each, add up their channels for db,
-// store dz, and release the block to the MMAs.  What binds it: HBM (z and dy in, dz
-// out), then the reciprocals and exponentials (three an element, 8192 elements a
-// block: 0.8 us of a block's 1.05).
+// A CTA pair takes a tile of 256 output channels (128 a CTA, the rows of dW) x up to
+// 512 input channels and a slice of the tokens; TMEM holds the tile (up to 512
+// columns), the slices' partial tiles are joined by dx's epilogue warps or
+// finish_kernel.  Per K block of 64 tokens a CTA loads its 64 x 128 of z and of dy
+// (its own barrier) and its half of x's columns (the leader's); sixteen warps turn z
+// into dz in place, a 1 KB atom of the swizzled tile (8 tokens x 64 channels) each,
+// add up their channels for db, store dz, and release the block to the MMAs.  What
+// binds it: up to 256 columns HBM (50176 x 128 x 2048, 617 MB, 96 us: 6.4 TB/s); 512
+// columns, 1.1 us a block, both that (without the stores of dz 92 of 111 us at 50176 x
+// 512 x 2048) and the formation's instructions (42 a pair of values; without the
+// activation 104 us, at 12544 x 1024 x 4096, read from L2 by the second tile, 77 of
+// 106).  (z and dy by plain loads into registers, two blocks ahead: 43 us at 12544 x
+// 512 x 2048, 36 by TMA; two groups of eight warps at alternate blocks: 36.)
 #include <atomic>
 #include <cstring>
 
@@ -51,7 +54,8 @@ struct WgradArgs {
     bf16 *dz;                     // [rows, ld], or null
     float *sums;                  // [slices, N]: shares of db, or null
     int rows, N, ld;
-    int n;                        // C rounded up to 32, 64 at least
+    int n;                        // columns of a tile, a multiple of 32
+    int mt, nt;                   // tiles of dW
     int slices, kb, slice_kb;     // K blocks of all tokens, of a slice
     DeviceStatus st;
 };
@@ -80,9 +84,12 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
     __shared__ float red[WG_WARPS][64];
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, tile = pair / a.slices, slice = pair % a.slices;
+    const int pair = blockIdx.x >> 1, slice = pair % a.slices;
+    int mtile, ntile;
+    tile_order(pair / a.slices, a.mt, a.nt, mtile, ntile);
     const int kb0 = slice * a.slice_kb, kb_n = (a.kb - kb0 < a.slice_kb ? a.kb - kb0 : a.slice_kb);
-    const int ch0 = tile * 256 + (int)rank * 128;   // this CTA's first output channel
+    const int ch0 = mtile * 256 + (int)rank * 128;   // this CTA's first output channel
+    const bool first = ntile == 0;                   // (dz and db are the first column tile's)
     // z and dy have landed (own), dz is formed (the leader's), the MMAs are done with
     // it (both); dy has been read (own); x has landed (the leader's, of both CTAs), the
     // MMAs are done with it (both); the tile is complete (both)
@@ -175,7 +182,7 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
         }
     } else if (warp == 2) {
         const uint32_t lead = map_rank(xfull, 0), bytes = (b_boxes(n0) + (WIDE ? b_boxes(n1) : 0)) * 8192;
-        const int c0 = (int)rank * (n0 / 2), c1 = 256 + (int)rank * (n1 / 2);
+        const int c0 = ntile * a.n + (int)rank * (n0 / 2), c1 = ntile * a.n + 256 + (int)rank * (n1 / 2);
         RingAt x;
         int issued = 0;
 #pragma unroll 1
@@ -213,7 +220,7 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
                        at1 = (uint32_t)box * 8192 + sw128_offset((w >> 1) * 8 + t + 4, chunk);
         const uint32_t lead_ready = map_rank(ready, 0);
         const int c = ch0 + box * 64 + chunk * 8;
-        const bool stored = a.dz && c < a.N;
+        const bool stored = first && a.dz && c < a.N;
         f2 sum[4] = {0, 0, 0, 0};
         RingAt z, y;
         int64_t row = (int64_t)kb0 * 64 + (w >> 1) * 8 + t;
@@ -253,7 +260,7 @@ act_wgrad_kernel(const __grid_constant__ WgradArgs a)
             }
         }
         // the lanes' sums, then those of the eight warps of the same channels
-        if (a.sums) {
+        if (first && a.sums) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float v[2];
@@ -325,18 +332,29 @@ cudaError_t launch(const WgradArgs &a, int pairs, cudaStream_t stream)
 
 } // namespace
 
-ActWgradPlan plan_act_wgrad(int C, int N, int rows)
+ActWgradPlan plan_act_wgrad(int C, int N, int rows, const ProductsPlan &apart)
 {
     ActWgradPlan p{};
-    const int pairs = sm_count() / 2, tiles = ceil_div(N, 256), kb = ceil_div(rows, 64);
-    if (C > 512 || 2 * tiles > pairs) return p;
-    p.n = C < 64 ? 64 : (C + 31) / 32 * 32;
+    const int pairs = sm_count() / 2, mt = ceil_div(N, 256), nt = ceil_div(C, 512), tiles = mt * nt, kb = ceil_div(rows, 64);
+    if (nt > 4 || tiles > pairs) return p;
+    p.n = C < 64 ? 64 : ceil_div(ceil_div(C, nt), 32) * 32;
+    p.mt = mt;
+    p.nt = nt;
     p.tiles = tiles;
     p.kb = kb;
     p.slice_kb = ceil_div(kb, pairs / tiles);
     p.slices = ceil_div(kb, p.slice_kb);
     p.part_bytes = (size_t)tiles * p.slices * 256 * p.n * sizeof(float);
-    p.chosen = true;
+    // Estimates in us: the trips of z, dy and dz at 6 TB/s (as a launch of their own
+    // worse), a K block of a tile here and of a whole tile in dW's own product, launches
+    // and joins.  Measured, whole backwards, dz apart and here: 12544 x 512 x 2048 88.6
+    // and 60.4, 12544 x 768 x 768 54.0 and 38.4, 5001 x 1000 x 1000 55.5 and 34.7, 3136
+    // x 384 x 1536 40.9 and 31.5, 12544 x 1024 x 4096 186 and 182; not taken: 8192 x 2048
+    // x 2048 112.5 and 114.6, 3000 x 1024 x 4096 57.3 and 63.8, 2000 x 2048 x 2048 36.6
+    // and 54.5, 300 x 512 x 1024 18.9 and 24.2; 27 sizes: 0.7% above the better
+    // of both on average.
+    const double trips = 6.0 * rows * N / 6.0e6, blocks = p.slice_kb * (0.6 + 0.5 * p.n / 512);
+    p.chosen = 13 + (blocks > trips ? blocks : trips) < 10 + 1.25 * trips + 0.00283 * (double)apart.cost;
     return p;
 }
 
@@ -358,6 +376,8 @@ cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceSta
     a.N = w.N;
     a.ld = w.ld;
     a.n = p.n;
+    a.mt = p.mt;
+    a.nt = p.nt;
     a.slices = p.slices;
     a.kb = p.kb;
     a.slice_kb = p.slice_kb;
@@ -374,7 +394,7 @@ cudaError_t launch_act_wgrad(const ActWgrad &w, const ActWgradPlan &p, DeviceSta
     join->single = true;
     join->tn = p.n;
     join->blocks = p.tiles >= 16 ? 16 : 64;
-    join->p[0] = {nullptr, nullptr, w.dW, w.N, w.C, p.tiles, 1, 0};
+    join->p[0] = {nullptr, nullptr, w.dW, w.N, w.C, p.mt, p.nt, 0};
     join->p[1].first = join->p[2].first = 0x7fffffff;
     *join_blocks = p.tiles * join->blocks;
     if (p.n > 256) return w.act == ACT_SILU ? launch<ACT_SILU, true>(a, pairs, stream) : launch<ACT_GELU, true>(a, pairs, stream);

@@ -100,8 +100,9 @@ ProductsPlan plan_products(const Product *p, int n, int elems)
     const int cut_cost = ceil_div(blocks, np) + (pl.wide ? WIDE_JOIN : NARROW_JOIN), least = s.kb < cut_cost ? s.kb : cut_cost;
     const bool halves = pl.wide && rest && 2 * rest <= pairs && (int64_t)half_cost(2 * rest, pairs) * s.kb <= 100ll * least;
     const int64_t here = 100ll * full * s.kb + (halves ? (int64_t)half_cost(2 * rest, pairs) * s.kb : rest ? 100ll * least : 0);
-    const int64_t tiles192 = count(192);
-    if (pl.wide && (int64_t)ceil_div(tiles192, pairs) * COST_192 * s.kb < here) {
+    const int64_t tiles192 = count(192), cost192 = (int64_t)ceil_div(tiles192, pairs) * COST_192 * s.kb;
+    pl.cost = (pl.wide && cost192 < here ? cost192 : here) * (pl.wide ? 100 : 55) / 100;   // (128 columns: as half a tile)
+    if (pl.wide && cost192 < here) {
         pl.wn = 192;
         s.tiles = (int)tiles192;
         s.np = (int)(tiles192 < pairs ? tiles192 : pairs);

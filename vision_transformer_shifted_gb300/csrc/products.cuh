@@ -670,6 +670,7 @@ struct ProductsPlan {
     int wn;               // columns of a tile: 256, 192 or 128
     PairSplit split;
     size_t part_bytes;    // of the partial tiles
+    int64_t cost;         // estimated, hundredths of a whole tile's K block
 };
 
 // The plan of n products as one launch (elems: K elements of a block).
