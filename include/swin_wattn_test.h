@@ -112,8 +112,8 @@ int swin_block_gated_test_plan(int C, int F, int rows, int which, int *plan);
 int swin_block_gated_test_corrupt_workspace(swin_block_gated_t h, int side);
 
 /* How the linear operator (swin_linear.h) divides a product, as
- * swin_block_gated_test_plan does: the forward (bf16 or 8-bit, more than 128
- * rows), dx or dW.  dW through an activation: {tiles of 256 rows, CTA pairs,
+ * swin_block_gated_test_plan does: the forward (bf16 or 8-bit), dx or dW (0 CTA
+ * pairs: by the few-row kernel instead).  dW through an activation: {tiles of 256 rows, CTA pairs,
  * columns of a tile, tiles across dW's columns, slices of the tokens, 1 if that
  * kernel is taken rather than dz apart and the product}. */
 enum {

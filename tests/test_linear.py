@@ -257,13 +257,16 @@ def test_plans_of_the_tested_sizes():
     SMs."""
     for args, want in [   # columns of a tile, half tiles, cut along K, into equal slices
             ((328, 136, 129, FWD), (256, 1, 0, 0)), ((2048, 2056, 1300, FWD), (192, 0, 0, 0)),
-            ((4096, 120, 700, FWD), (128, 0, 1, 0)), ((8208, 264, 300, FWD), (256, 0, 1, 0)),
+            ((8192, 1032, 1000, FWD), (256, 0, 1, 0)),
             ((512, 2048, 2500, Q8), (256, 1, 0, 0)), ((264, 336, 20000, FWD), (192, 0, 0, 0)),
-            ((264, 8200, 300, DX), (256, 0, 1, 0)), ((120, 8200, 300, DX), (128, 0, 1, 0)),
+            ((136, 6792, 4067, DX), (256, 0, 1, 0)),
             ((144, 520, 5001, DW), (256, 0, 1, 0)), ((96, 384, 20000, DW), (128, 0, 1, 0)),
             ((520, 1032, 6000, DW), (256, 0, 1, 1))]:
         tiles, pairs, columns, halves, cut, equal = sw.swin_block_linear_test_plan(*args)
-        assert (columns, halves > 0, cut > 0, equal) == want, args
+        assert pairs and (columns, halves > 0, cut > 0, equal) == want, args
+    for args in ((4096, 120, 700, FWD), (8208, 264, 300, FWD), (2968, 400, 385, FWD), (4096, 1024, 300, Q8),
+                 (264, 8200, 300, DX), (120, 8200, 300, DX)):
+        assert sw.swin_block_linear_test_plan(*args)[1] == 0, args   # (the few-row kernel, in chunks of rows)
 
 
 def test_plans_of_the_weight_gradient_through_an_activation():
@@ -291,7 +294,7 @@ def test_plan_refuses():
 SHAPES = [   # rows, C, N
     (1, 8, 8), (1, 96, 384), (1, 512, 1368), (1, 8208, 40), (1, 1040, 6152), (2, 64, 64), (5, 136, 120), (17, 128, 264), (24, 1024, 2048),
     (64, 256, 640), (127, 192, 512), (128, 96, 128), (129, 328, 136), (256, 512, 512), (300, 1032, 2056),
-    (515, 128, 384), (1000, 64, 1024), (3001, 96, 384), (2048, 768, 1024), (700, 4096, 120), (300, 8208, 264)]
+    (515, 128, 384), (385, 2968, 400), (1000, 64, 1024), (3001, 96, 384), (2048, 768, 1024), (700, 4096, 120), (300, 8208, 264)]
 
 
 @pytest.mark.gpu
@@ -359,7 +362,8 @@ def test_backward(rows, C, N, kind):
 
 LARGE = [   # rows, C, N: more tiles than CTA pairs, thin last rounds, long K
     (2500, 512, 2048), (5001, 144, 520), (1300, 2048, 2056), (20000, 264, 336), (20000, 96, 384), (6000, 520, 1032),
-    (9000, 384, 96), (3000, 768, 768), (4000, 1032, 1000), (4000, 8, 136), (10000, 24, 10008), (5000, 2048, 264)]
+    (9000, 384, 96), (3000, 768, 768), (4000, 1032, 1000), (4000, 8, 136), (10000, 24, 10008), (5000, 2048, 264),
+    (1000, 8192, 1032), (4067, 136, 6792), (300, 4096, 1024)]
 
 
 @pytest.mark.gpu
@@ -542,7 +546,7 @@ def test_streams_and_captured_graphs_share_nothing(rows, C, N):
 @pytest.mark.gpu
 def test_first_call_of_a_handle_captured():
     """A handle's first call may be the captured one (here with a workspace)."""
-    rows, C, N = 700, 4096, 120
+    rows, C, N = 1000, 8192, 1032
     x, w, b, r, _ = make(rows, C, N, seed=11)
     _, ref, _, eo = forward_ref(x, w, b, r, "silu")
     xd, wd, bd, rd = dev(x, w, b, r)
@@ -589,7 +593,7 @@ def test_offsets_past_32_bits():
 
 @pytest.mark.gpu
 def test_simulated_allocation_failure_then_a_normal_call():
-    rows, C, N = 700, 4096, 120
+    rows, C, N = 1000, 8192, 1032
     x, w, b, _, dy = make(rows, C, N, seed=12)
     xd, wd, bd, yd = dev(x, w, b, dy)
     out, dx, dW = torch.full_like(yd, 5.0), torch.full_like(xd, 5.0), nans(N, C)

@@ -1,8 +1,8 @@
-// The gated block's forward and the linear operator's for few rows (single
-// tokens, small batches), where
-// the weights' one trip from HBM is the work: each product with the weights as
-// the MMA's A operand (128 weight rows) and the rows of x as its narrow B (16 to
-// 128 columns), so that no row of the tensor-core tile is idle weight traffic.
+// The gated block's forward, the linear operator's and its dx for few rows (single
+// tokens, small batches), where the weights' one trip from HBM is the work: each
+// product with the weights as the MMA's A operand (128 weight rows) and the rows of
+// x as its narrow B (16 to 128 columns), so that no row of the tensor-core tile is
+// idle weight traffic.
 //
 // A CTA takes one tile of 128 weight rows (64 of Wg and the same 64 of Wu, or
 // 128 of Wd) and a share of K; the CTAs of a cluster share a tile's K (up to
@@ -12,6 +12,11 @@
 // Weights stream through a TMA ring of about 100 KB a CTA, two CTAs an SM: HBM
 // bounds it, and the latency of two launches (9 us + bytes / 7.07 TB/s over the
 // sizes; 1 x 2048 x 5632: 20 us, 24 rows from e4m3 4096 x 11264: 37).
+//
+// The linear operator's dx = dz W has the same form with W as stored, [K, 128
+// columns], MN-major (30 x 3992 to 1296, with dW and db: 16.3 us, 28.2 by pairs of
+// CTAs).  A few hundred rows with a long K go through in chunks of 128, each with
+// its own pass over the weights, the later ones from L2.
 #include <atomic>
 #include <cstring>
 
@@ -23,8 +28,9 @@ namespace {
 
 constexpr int FEW_THREADS = 192;   // four draining warps, a loading and an issuing one
 // What a launch computes: the gated block's first products with the activation
-// (FORM_UP + ACT_*), its last product, or the linear operator.
-enum { FORM_UP = 0, FORM_DOWN = -1, FORM_LINEAR = -2 };
+// (FORM_UP + ACT_*), its last product, the linear operator, or its dx (these two in
+// chunks of 128 rows).
+enum { FORM_UP = 0, FORM_DOWN = -1, FORM_LINEAR = -2, FORM_DX = -3 };
 constexpr int FEW_MAX_STAGES = 6;
 
 struct FewArgs {
@@ -35,7 +41,8 @@ struct FewArgs {
     bf16 *out;                     // [rows, ld]: h, or the output
     bf16 *z;                       // linear: as out, the value before the activation, or null
     int act;                       // linear: ACT_*
-    int rows, np;                  // np: rows rounded up to 16
+    int rows, np;                  // np: rows rounded up to 16 (linear: of a chunk, 128 of more rows)
+    int tiles;                     // of weight rows, in each chunk of rows
     int cols, ld;                  // columns of out
     int k, kb, split, stages, stage_bytes;
     DeviceStatus st;
@@ -82,14 +89,15 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
 {
     constexpr int ELEMS = Q8 ? 128 : 64;            // K elements of a block
     constexpr int W = FORM < FORM_UP ? 128 : 64;   // output columns of a tile
-    constexpr bool EARLY = FORM == FORM_DOWN;
+    constexpr bool EARLY = FORM == FORM_DOWN, CHUNKS = FORM <= FORM_LINEAR, A_MN = FORM == FORM_DX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_align(smem_raw, 1024);
     __shared__ uint64_t bars[2 * FEW_MAX_STAGES + 1];
     __shared__ uint32_t tslot;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * FEW_MAX_STAGES, done = empty + 8 * FEW_MAX_STAGES;
-    const int split = a.split, rank = (int)(blockIdx.x % split), tile = (int)(blockIdx.x / split);
+    const int split = a.split, rank = (int)(blockIdx.x % split);
+    const int tile = (int)(blockIdx.x / split) % a.tiles, row0 = CHUNKS ? (int)(blockIdx.x / split) / a.tiles * FEW_ROWS : 0;
     const int kb0 = (int)((int64_t)a.kb * rank / split), kb1 = (int)((int64_t)a.kb * (rank + 1) / split);
     const uint32_t tcols = a.np <= 32 ? 32 : a.np <= 64 ? 64 : 128;
     if (threadIdx.x == 0) {
@@ -124,7 +132,10 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
         int s = 0;
         uint32_t ph = 0;
         auto load_w = [&](int kb, uint32_t dst, uint32_t bar) {
-            if (FORM < FORM_UP) {
+            if (A_MN) {
+                tma_load_2d(dst, &a.w0, tile * 128, kb * ELEMS, bar);
+                tma_load_2d(dst + 8192, &a.w0, tile * 128 + 64, kb * ELEMS, bar);
+            } else if (FORM < FORM_UP) {
                 tma_load_2d(dst, &a.w0, kb * ELEMS, tile * 128, bar);
             } else {
                 tma_load_2d(dst, &a.w0, kb * ELEMS, tile * 64, bar);
@@ -156,7 +167,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
                     mbar_arrive_expect_tx(bar, a.stage_bytes);
                     load_w(kb, dst, bar);
                 }
-                tma_load_2d(dst + 16384, &a.x, kb * ELEMS, 0, bar);
+                tma_load_2d(dst + 16384, &a.x, kb * ELEMS, row0, bar);
             }
             if (++s == a.stages) {
                 s = 0;
@@ -169,8 +180,10 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
             while (global_timer_ns() - t0 < 200000) __nanosleep(1000);
         }
     } else if (warp == 5) {
-        const uint32_t ring16 = smem_u32(smem) >> 4;
-        const uint32_t idesc = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 128, 0) | (uint32_t)(a.np >> 3) << 17;
+        // (without the CTA's rank in the cluster, which a shared-memory address holds above
+        // its 18 bits: it would end up in the descriptor's leading byte offset)
+        const uint32_t ring16 = (smem_u32(smem) & 0x3ffffu) >> 4;
+        const uint32_t idesc = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, A_MN, false, 128, 0) | (uint32_t)(a.np >> 3) << 17;
         int s = 0;
         uint32_t ph = 0;
 #pragma unroll 1
@@ -186,7 +199,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (k < steps)
-                        mma_one<Q8 ? MMA_E4M3 : MMA_BF16>(tmem, PairOperand<false>::desc(a16, k),
+                        mma_one<Q8 ? MMA_E4M3 : MMA_BF16>(tmem, PairOperand<A_MN>::desc(a16, k),
                                                           PairOperand<false>::desc(a16 + 1024, k), idesc,
                                                           (kb != kb0) | (k != 0));
                 mma_commit(empty + 8 * s);
@@ -224,14 +237,14 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     // the cluster's CTAs finish every split-th group of output values, four
     // neighbours a thread
     const uint32_t base = smem_u32(smem);
-    const int items = a.rows * (W / 4);
+    const int items = (CHUNKS && a.rows - row0 > FEW_ROWS ? FEW_ROWS : a.rows - row0) * (W / 4);
     for (int e = rank * FEW_THREADS + (int)threadIdx.x; e < items; e += split * FEW_THREADS) {
-        const int t = e / (W / 4), i = e % (W / 4) * 4, c = tile * W + i;
+        const int u0 = e / (W / 4), t = row0 + u0, i = e % (W / 4) * 4, c = tile * W + i;   // (u0: row of the chunk)
         if (c >= a.cols) continue;   // (cols is a multiple of 8)
         float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int r = 0; r < split; ++r) {
-            const uint32_t at = map_rank(base + (uint32_t)(t * 128 + i) * 4, r);
+            const uint32_t at = map_rank(base + (uint32_t)(u0 * 128 + i) * 4, r);
             add4(v, ld_cluster(at));
             if (FORM >= FORM_UP) add4(u, ld_cluster(at + 64 * 4));
         }
@@ -277,12 +290,13 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     constexpr int W = FORM < FORM_UP ? 128 : 64;
     a.kb = (a.k + (Q8 ? 127 : 63)) / (Q8 ? 128 : 64);
     // CTAs a tile: until there is one for every SM, with two K blocks each at least
-    const int tiles = (width + W - 1) / W;
+    a.tiles = (width + W - 1) / W;
+    const int chunks = FORM <= FORM_LINEAR ? (a.rows + FEW_ROWS - 1) / FEW_ROWS : 1, tiles = a.tiles * chunks;
     a.split = 1;
     while (a.split < 8 && tiles * a.split < sm_count() && a.kb >= 4 * a.split) a.split *= 2;
     // (the linear operator, one kernel: as many as two an SM hold; 24 rows from e4m3
     // 4096 x 11264, 88 tiles, 12.9 us with two, 12.3 with three)
-    if (FORM == FORM_LINEAR)
+    if (FORM <= FORM_LINEAR)
         for (a.split = 1; a.split < 8 && tiles * (a.split + 1) <= 2 * sm_count() && a.kb >= 4 * (a.split + 1);) ++a.split;
     // two CTAs an SM (three stages with 128 rows, up to six with 16)
     a.stage_bytes = 16384 + a.np * 128;
@@ -370,7 +384,7 @@ cudaError_t launch_few_linear(const FewLinear &u, DeviceStatus st, cudaStream_t 
     const int e8 = u.sx ? 1 : 2;
     const CUtensorMapDataType type = u.sx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     a.rows = u.rows;
-    a.np = (u.rows + 15) / 16 * 16;
+    a.np = u.rows < FEW_ROWS ? (u.rows + 15) / 16 * 16 : FEW_ROWS;
     cudaError_t e;
     if ((e = make_tensor_map(&a.w0, type, u.w, u.C, u.N, (int64_t)u.C * e8, 128 / e8, 128, 128)) != cudaSuccess) return e;
     if ((e = make_tensor_map(&a.x, type, u.x, u.C, u.rows, (int64_t)u.C * e8, 128 / e8, a.np, 128)) != cudaSuccess) return e;
@@ -385,6 +399,24 @@ cudaError_t launch_few_linear(const FewLinear &u, DeviceStatus st, cudaStream_t 
     a.k = u.C;
     a.st = st;
     return u.sx ? launch_few<FORM_LINEAR, true>(a, u.N, stream) : launch_few<FORM_LINEAR, false>(a, u.N, stream);
+}
+
+cudaError_t launch_few_dx(const bf16 *dz, int ld, int rows, const bf16 *w, bf16 *dx, int C, int N, DeviceStatus st,
+                          cudaStream_t stream)
+{
+    FewArgs a;
+    memset(&a, 0, sizeof(a));
+    const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    a.rows = rows;
+    a.np = rows < FEW_ROWS ? (rows + 15) / 16 * 16 : FEW_ROWS;
+    cudaError_t e;
+    if ((e = make_tensor_map(&a.w0, type, w, C, N, (int64_t)C * 2, 64, 64, 128)) != cudaSuccess) return e;
+    if ((e = make_tensor_map(&a.x, type, dz, N, rows, (int64_t)ld * 2, 64, a.np, 128)) != cudaSuccess) return e;
+    a.out = dx;
+    a.cols = a.ld = C;
+    a.k = N;
+    a.st = st;
+    return launch_few<FORM_DX, false>(a, C, stream);
 }
 
 } // namespace swin

@@ -72,6 +72,29 @@ Product forward_product(int C, int N, int rows)
     return p;
 }
 
+// Whether a product of more than 128 rows goes to the few-row kernel, chunks of 128
+// rows with K shared by a cluster, rather than to pairs of CTAs: few tiles of a long
+// K.  Estimates in us, from both ways at 25 sizes: there 6.5 and its operands at 13
+// TB/s from L2 or half a microsecond a K block of a CTA, here 4.5 and 0.25 to 0.29 a K
+// block of the pairs' longest way, 13 for a join (385 x 2968 x 400 17.7 us by pairs, 10.0;
+// 800 x 8192 x 1024 26.6, 20.3; 700 x 4096 x 120 12.6, 9.1; not taken: 300 x 1032 x 2056
+// 10.2, 11.3; 3779 x 2832 x 424 16.7, 21.5).
+bool few_chosen(const Product &p, const ProductsPlan &pl, int elems)
+{
+    const int64_t tiles = (int64_t)ceil_div(p.cols, 128) * ceil_div(p.rows, FEW_ROWS);
+    if (tiles > 2 * sm_count()) return false;
+    const int kb = ceil_div(p.k[0], elems);
+    int split = (int)(2 * sm_count() / tiles);
+    split = split > 8 ? 8 : split;
+    if (4 * split > kb) split = kb / 4 > 1 ? kb / 4 : 1;
+    const double bytes = tiles * kb * 32768 / 13e6, blocks = 0.5 * ceil_div(kb, split);
+    const PairSplit &s = pl.split;
+    const double whole = pl.wn == 256 ? 1.0 : pl.wn == 192 ? 0.82 : 0.55;
+    const double pairs = s.cut ? 17.5 + 0.283 * whole * ((double)s.full * kb + s.q)
+                               : 4.5 + kb * (0.29 * whole * (s.halves ? s.full : ceil_div(s.tiles, s.np)) + (s.halves ? 0.25 : 0.0));
+    return 6.5 + (bytes > blocks ? bytes : blocks) < pairs;
+}
+
 template <int ACT, bool Q8>
 cudaError_t launch_linear(const Forward &f, int C, int N, const ProductsPlan &pl, float *part, DeviceStatus st,
                           cudaStream_t stream, FinishArgs *fin)
@@ -125,14 +148,14 @@ int forward(swin_block_linear_s *h, const Forward &f, cudaStream_t stream)
     if (rc != SWIN_WATTN_OK) return rc;
     const DeviceStatus st{h->d_err, WAIT_NS};
     const bool q8 = f.sx != nullptr;
-    if (f.rows <= FEW_ROWS) {
+    const Product p = forward_product(h->C, h->N, f.rows);
+    const ProductsPlan pl = f.rows <= FEW_ROWS ? ProductsPlan{} : plan_products(&p, 1, elems(q8));
+    if (f.rows <= FEW_ROWS || few_chosen(p, pl, elems(q8))) {
         h->last_launches = 1;
         const FewLinear u{f.x, f.w, f.bias, f.residual, f.sx, f.sw, f.out, f.z, f.rows, h->C, h->N, h->act};
         const cudaError_t e = f.rows == 1 ? launch_token_linear(u, stream) : launch_few_linear(u, st, stream);
         return e == cudaSuccess ? SWIN_WATTN_OK : SWIN_WATTN_ECUDA;
     }
-    const Product p = forward_product(h->C, h->N, f.rows);
-    const ProductsPlan pl = plan_products(&p, 1, elems(q8));
     void *ws = nullptr;
     bool captured = false;
     if (pl.part_bytes && (rc = ows_begin(&h->ws, pl.part_bytes, stream, &ws, &captured)) != SWIN_WATTN_OK) return rc;
@@ -388,6 +411,9 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     const GradPlan pg = plan_grad(h->N, rows);
     FinishArgs fin{};
     size_t sum_bytes = 0;
+    // few rows of dy are added to the end by one warp a column, no launch for a join
+    // (16 x 72 x 8432: 2 us of 20)
+    bool direct = false;
     if (db) {
         // from dz's kernel, or (dz is dy) by the weight gradient's waiting warps
         auto &m = fin.cs.m[fin.cs.n++];
@@ -395,7 +421,8 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         m.b = act ? nullptr : (const bf16 *)dy;
         m.rows = rows;
         m.cols = h->N;
-        m.slices = pa.chosen ? pa.slices : act ? pg.slices : column_slices(rows);
+        direct = !act && rows <= 64;
+        m.slices = pa.chosen ? pa.slices : act ? pg.slices : direct ? 1 : column_slices(rows);
         m.tasks = act ? 0 : ceil_div(h->N, 256) * m.slices;
         sum_bytes = (size_t)m.slices * h->N * sizeof(float);
     }
@@ -413,7 +440,7 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     bf16 *dz = (bf16 *)carve.take(dz_bytes);
     float *x_part = (float *)carve.take(plx.part_bytes), *w_part = (float *)carve.take(w_bytes);
     float *sum_part = (float *)carve.take(sum_bytes);
-    if (db) fin.cs.m[0].part = sum_part;
+    if (db) fin.cs.m[0].part = direct ? nullptr : sum_part;
     px.a[0] = pw.a[0] = act ? (const void *)dz : dy;
     px.b[0] = W;
     px.d = (bf16 *)dx;
@@ -444,15 +471,23 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         if (e == cudaSuccess && dW && !pa.chosen)
             e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
     };
-    const bool side = dx && dW && (pa.chosen || plw.split.cut || db) && (!db || fin.cs.m[0].slices <= SIDE_SLICES) &&
+    // (few rows: dx by the few-row kernel)
+    const bool few = dx && (rows <= FEW_ROWS || few_chosen(px, plx, 64));
+    const bool side = dx && !few && dW && (pa.chosen || plw.split.cut || db) && (!db || fin.cs.m[0].slices <= SIDE_SLICES) &&
                       !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
     if (side) weight();
     if (e == cudaSuccess && dx) {
         const FinishArgs left = fin;
         if (side) fin.joins[1] = fin.cs.n = 0;
-        e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0, side ? &left : nullptr);
+        if (few) {
+            ++h->last_launches;
+            e = launch_few_dx((const bf16 *)px.a[0], ld, rows, (const bf16 *)W, (bf16 *)dx, h->C, h->N, st, s);
+        } else {
+            e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0, side ? &left : nullptr);
+        }
     }
     if (!side) weight();
+    if (direct) fin.cs.n = 0;   // (done)
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
@@ -476,8 +511,10 @@ int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan)
     else if (which == SWIN_BLOCK_LINEAR_PLAN_DX) p = dx_product(C, N, rows, N);
     else if (which == SWIN_BLOCK_LINEAR_PLAN_WEIGHT) p = weight_product(C, N, rows, N);
     else return SWIN_WATTN_EINVAL;
-    const ProductsPlan pl = plan_products(&p, 1, elems(which == SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8));
-    const int v[] = {pl.split.tiles, pl.split.np, pl.wn, pl.split.halves, pl.split.cut, pl.split.kb != pl.split.k_blocks};
+    const int block = elems(which == SWIN_BLOCK_LINEAR_PLAN_FORWARD_Q8);
+    const ProductsPlan pl = plan_products(&p, 1, block);
+    const bool few = which != SWIN_BLOCK_LINEAR_PLAN_WEIGHT && (rows <= FEW_ROWS || few_chosen(p, pl, block));
+    const int v[] = {pl.split.tiles, few ? 0 : pl.split.np, pl.wn, pl.split.halves, pl.split.cut, pl.split.kb != pl.split.k_blocks};
     memcpy(plan, v, sizeof(v));
     return SWIN_WATTN_OK;
 }

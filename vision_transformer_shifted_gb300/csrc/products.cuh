@@ -214,14 +214,15 @@ struct ColumnSums {
         const bf16 *b;    // bf16, or
         const float *f;   // fp32
         bf16 *out;
-        float *part;      // [slices, cols]
+        float *part;      // [slices, cols], or (one slice) null: it goes to out
         int64_t rows;
         int cols, slices, tasks;   // tasks: slices of every group of columns
     } m[3];
     int n;
 };
 template <class T>
-__device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols, int c, int slice, int slices, float *part)
+__device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols, int c, int slice, int slices, float *part,
+                                             bf16 *out)
 {
     constexpr int V = 16 / sizeof(T);
     if (c >= cols) return;
@@ -249,6 +250,12 @@ __device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols,
     }
 #pragma unroll 1
     for (; i < rows; i += slices) add(*reinterpret_cast<const uint4 *>(p + i * cols + c));
+    if (!part) {   // (one slice, and nothing to add later)
+#pragma unroll
+        for (int e = 0; e < V; e += 4)
+            *reinterpret_cast<uint2 *>(out + c + e) = make_uint2(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]));
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < V; e += 4)
         *reinterpret_cast<float4 *>(part + (int64_t)slice * cols + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -261,8 +268,8 @@ __device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int 
         const auto &m = a.m[z];
         for (; t < m.tasks; t += warps) {
             const int slice = t % m.slices, g = t / m.slices;
-            if (m.b) column_slice(m.b, m.rows, m.cols, g * 256 + lane * 8, slice, m.slices, m.part);
-            else column_slice(m.f, m.rows, m.cols, g * 128 + lane * 4, slice, m.slices, m.part);
+            if (m.b) column_slice(m.b, m.rows, m.cols, g * 256 + lane * 8, slice, m.slices, m.part, m.out);
+            else column_slice(m.f, m.rows, m.cols, g * 128 + lane * 4, slice, m.slices, m.part, m.out);
         }
         t -= m.tasks;
     }
@@ -710,6 +717,9 @@ struct FewLinear {
     int rows, C, N, act;    // act: ACT_*
 };
 cudaError_t launch_few_linear(const FewLinear &u, DeviceStatus st, cudaStream_t stream);
+// dx = dz W for W [N, C], rows of dz of stride ld; any number of rows, as the above.
+cudaError_t launch_few_dx(const bf16 *dz, int ld, int rows, const bf16 *w, bf16 *dx, int C, int N, DeviceStatus st,
+                          cudaStream_t stream);
 // The same for one row (linear_token.cu).
 cudaError_t launch_token_linear(const FewLinear &u, cudaStream_t stream);
 
