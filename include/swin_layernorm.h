@@ -8,14 +8,17 @@
  *   s = x + residual (rounded to bf16; s = x without a residual)
  *   mu = mean_c s;  var = mean_c (s - mu)^2;  r = 1 / sqrt(var + eps);  n = (s - mu) r
  *   y = n gamma + beta
- * The variance is the mean square of the deviations from the row's mean (two
- * sums, the second corrected for the first one's rounding), not a difference of
- * large numbers: a row of one value, however large, has n = 0.  The norm sees
- * the stored (rounded) sum, so that the backward pass, which starts from it,
- * differentiates the very function that ran.  A row holding an infinity or a
- * NaN, or whose values add up to more than 3.4e38, gives NaN; one whose squared
- * deviations do has r = 0; with eps = 0, one whose channels are all alike gives
- * NaN or infinities, in the backward pass also in dgamma.  8-bit output: as
+ * The statistics are one pass over the row, of its values' differences from a
+ * pivot of its own (the mean of its first eight values), not a difference of the
+ * large numbers mean s^2 and mu^2: a row of one value has n = 0, and a row far
+ * from zero loses nothing.  r's relative error grows with the pivot's distance
+ * from the mean, k standard deviations: some (1 + k^2) 2^-24, with k^2 at most C / 8
+ * (all of a row's spread in those eight values).  The norm sees the stored
+ * (rounded) sum, so that the backward pass, which starts from it, differentiates
+ * the very function that ran.  A row holding an infinity or a NaN, or whose first
+ * eight values or differences add up to more than 3.4e38, gives NaN; one whose
+ * squared differences do has r = 0; with eps = 0, one whose channels are all alike
+ * gives NaN or infinities, in the backward pass also in dgamma.  8-bit output: as
  * swin_block_rms_forward_q8 (swin_rms.h): scale = max(max_c |y|, 1e-30) / 448
  * per row, code = y / scale (both fp32 quotients) rounded to nearest even in
  * e4m3, NaN codes and a NaN scale for a row with a NaN.

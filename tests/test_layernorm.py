@@ -12,7 +12,10 @@ step), to e4m3 by 2^-4 or, below its smallest normal number, half of 2^-9.
 The fp32 sums have at most 16384 terms in chains of at most some 100, so that a
 row's statistics are good to FP = 2^-15, n to FP (|n| + 1/16) (its mean is a
 sum of terms of order one) and, since s - mu is one fp32 subtraction whose
-operands may be larger than itself, to 2^-22 (|s| + |mu|) r beside.
+operands may be larger than itself, to 2^-22 (|s| + |mu|) r beside.  (The sums are
+of s - p, p the mean of the row's first eight values: k standard deviations from
+the row's mean, k below 2 in random rows.  Rows with their spread in those eight
+values have bounds of their own, with k in them.)
 """
 import ctypes
 
@@ -301,9 +304,9 @@ def test_backward(rows, C, with_dsum):
 @pytest.mark.parametrize("C", [40, 96, 520, 768, 2744])
 @pytest.mark.parametrize("mean", [1.0, -300.0, 1000.0, 3e4, 2.0 ** 100])
 def test_rows_of_one_value_and_far_from_zero(C, mean):
-    """A row of one value has n = 0 whatever its size (here y = beta exactly: the
-    deviations are what the mean's rounding leaves, and their own mean takes that
-    off); a row of large values with a small spread keeps its digits."""
+    """A row of one value has n = 0 whatever its size (y = beta: all its differences
+    from its first values are zero); a row of large values with a small spread keeps
+    its digits."""
     x, _, g, b, dy = inputs(5, C, False, seed=11)
     x[:3] = mean
     if abs(mean) < 1e6:
@@ -321,6 +324,50 @@ def test_rows_of_one_value_and_far_from_zero(C, mean):
             sw.swin_block_layernorm_backward(h, xd, gd, yd, dx, dg, db)
             close(dx, ref[0], HALF * ref[0].abs() + 1.01 * err[0])
             close(dg, ref[1], err[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [8, 96, 520, 2744, 16384])
+@pytest.mark.parametrize("where", [slice(3, 4), slice(0, 8)])
+def test_a_rows_spread_in_its_first_values(C, where):
+    """Large values among the row's first eight, whose mean the sums are taken about:
+    it lies k standard deviations from the row's mean, k^2 up to C / 8.
+
+    With u = 2^-24 and at most 40 additions one after the other: the sum of s - p is
+    off by 40 u sum|s - p| at most, so mu by 40 u q sigma with q^2 = 1 + k^2; the mean
+    square by 41 u q^2 sigma^2, mu's square by 2 k sigma 40 u q sigma <= 80 u q^2
+    sigma^2, so var by 122 u q^2 of itself and r by er = 61 u q^2 + 2 u.  n = (s - p) r
+    + shift: er |n| + 48 u q.  mean a: 48 u mean|a|; mean(a n), from the sum of a (s - p)
+    and mean a: er |mean(a n)| + 50 u (mean|a n| + 2 k mean|a|)."""
+    u = 2.0 ** -24
+    x, _, g, b, dy = inputs(6, C, False, seed=21)
+    x[:, where] = torch.tensor([1000., -700., 50., 3e4, -2e5, 12.]).to(BF)[:, None]
+    g_, b_, dy_ = g.double(), b.double(), dy.double()
+    mean = lambda t: t.mean(-1, keepdim=True)  # noqa: E731
+    n, r, _ = normalise(x)
+    s = x.double()
+    k = (mean(s) - mean(s[:, :8])).abs() * r
+    q = (1 + k * k).sqrt()
+    er = 61 * u * q * q + 2 * u
+    en = er * n.abs() + 48 * u * q
+    y, ey = n * g_ + b_, en * g_.abs() + 2 * u * (b_.abs() + (n * g_).abs())
+    a = dy_ * g_
+    ma, mn = mean(a), mean(a * n)
+    emn = er * mn.abs() + 50 * u * (mean((a * n).abs()) + 2 * k * mean(a.abs()))
+    (dx, dg, db), _ = gradients(x, g, dy, None)
+    ex = er * dx.abs() + r * (4 * u * (a.abs() + (n * mn).abs()) + 48 * u * mean(a.abs()) + n.abs() * emn + mn.abs() * en)
+    xd, gd, bd, yd = dev(x, g, b, dy)
+    out, codes, scales = torch.empty_like(xd), torch.empty(6, C, dtype=E4M3, device=DEV), torch.empty(6, device=DEV)
+    got = torch.empty_like(xd), torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    with layernorm(C) as h:
+        sw.swin_block_layernorm_forward(h, xd, gd, bd, out)
+        sw.swin_block_layernorm_forward_q8(h, xd, gd, bd, codes, scales)
+        sw.swin_block_layernorm_backward(h, xd, gd, yd, *got)
+    close(out, y, HALF * y.abs() + 1.01 * ey)
+    close_codes(codes, scales, y, ey)
+    close(got[0], dx, HALF * dx.abs() + 1.01 * ex)
+    close(got[1], dg, (dy_.abs() * (en + 8 * u * n.abs())).sum(0))
+    close(got[2], db, 8 * u * dy_.abs().sum(0))
 
 
 @pytest.mark.gpu
@@ -378,6 +425,26 @@ def test_in_place(C):
         close(one, ref[0], HALF * ref[0].abs() + 1.01 * err[0])
         sw.swin_block_layernorm_backward(h, rd, gd, yd, two, gg, gb, dsum=two)
         assert torch.equal(one, two)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [520, 2744, 8200, 16384])
+@pytest.mark.parametrize("rows", [100, 4000])
+def test_in_place_gives_the_very_same(rows, C):
+    """Wide rows, of which every thread reads the first piece too: the sum over x or
+    over the residual, the output over the other."""
+    x, r, g, b, _ = dev(*inputs(rows, C, True, seed=22))
+    out, s = torch.empty_like(x), torch.empty_like(x)
+    with layernorm(C) as h:
+        sw.swin_block_layernorm_forward(h, x, g, b, out, residual=r, out_sum=s)
+        for swap in (False, True):
+            one, two = x.clone(), r.clone()
+            sw.swin_block_layernorm_forward(h, one, g, b, one if swap else two, residual=two, out_sum=two if swap else one)
+            assert torch.equal(one, out if swap else s) and torch.equal(two, s if swap else out)
+        post, over = torch.empty_like(x), x.clone()
+        sw.swin_block_layernorm_forward_post(h, x, g, b, r, post)
+        sw.swin_block_layernorm_forward_post(h, over, g, b, r, over)
+        assert torch.equal(over, post)
 
 
 @pytest.mark.gpu

@@ -6,7 +6,7 @@
 // output written once, the row stays in registers (the backward: shared memory)
 // between the statistics and the output, and HBM bounds it: 200704 x 96 with the
 // residual 23.7 us, 6.5 TB/s; post-norm 589824 x 192 103.7 us, 6.55 TB/s; e4m3
-// 8191 x 4096 39 us, 6.0 TB/s; backward 589824 x 192 with dsum 140 us, 6.45 TB/s
+// 8191 x 4096 39.7 us, 5.9 TB/s; backward 589824 x 192 with dsum 140 us, 6.45 TB/s
 // (57% of the issue slots).  The
 // statistics are one sum a row, of s - p and of its square, p being the mean of
 // the row's first eight values: sum s^2 - C mu^2 (p = 0) would lose what a row's
@@ -115,14 +115,18 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_fo
         head = ld16(a.x + base);
         if (add) head = stored(head, ld16(a.residual + base));
     }
-    if (add) {
+    auto store_sum = [&]() {
+        if (!add || !a.out_sum || !row_ok) return;
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
-            s[k] = stored(s[k], t[k]);
-            if (a.out_sum && row_ok && c < a.chunks) *reinterpret_cast<uint4 *>(a.out_sum + base + c * 8) = s[k];
+            if (c < a.chunks) *reinterpret_cast<uint4 *>(a.out_sum + base + c * 8) = s[k];
         }
-    }
+    };
+    if (add)
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) s[k] = stored(s[k], t[k]);
+    if (!BLOCK) store_sum();
     float p = piece_sum(piece(BLOCK ? head : s[0])) * 0.125f;
     if (!BLOCK) p = __shfl_sync(0xffffffffu, p, lane - li);
     auto minus_p = [&](int k) { return li + k * step < a.chunks ? pack2(-p) : pack2(0.f); };   // (behind the row: zeros)
@@ -148,6 +152,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_fo
     }
     float sum = sum2(sum2v), sq = sum2(sq2v);
     row_sum2<BLOCK>(sum, sq, a.lpr, red);
+    if (BLOCK) store_sum();   // (in place: only now has every thread read the row's first piece)
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {   // (kept packed: fewer registers, more rows in flight)
         forget(s[k]);
