@@ -446,10 +446,51 @@ def test_one_row_with_nan_and_infinity():
     assert got8[0, 17].isnan() and got8.isnan().sum() == 1
 
 
+FAR = [1e30, -1e30, 3e38, -3e38, 2e19, -2e19, 100.0, -100.0]   # act is z or 0 there, act' 1 or 0
+
+
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,behind", [(1, 4), (77, 51), (300, 100)])
-def test_in_place_and_rows_behind_the_batch(rows, behind):
-    C, N = 192, 520
+@pytest.mark.parametrize("rows,C,N", [(1, 64, 264), (40, 64, 264), (300, 64, 264), (385, 2968, 400)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activation_far_from_zero(rows, C, N, kind):
+    x, w, _, r, _ = make(rows, C, N, seed=23)
+    far = torch.tensor(FAR).repeat(N // 8).to(BF)
+    (x8, sx), (w8, sc) = quantise(x), quantise(torch.zeros_like(w))
+    want = far.clamp_min(0).expand(rows, N)
+    want = want, (want.float() + r.float()).to(BF)
+    got, z, got8 = nans(rows, N), nans(rows, N), nans(rows, N)
+    with linear(C, N, kind) as h:
+        for res, ref in zip((None, dev(r)), want):
+            sw.swin_block_linear_forward(h, dev(x), torch.zeros_like(w, device=DEV), dev(far), got, residual=res, z=z)
+            assert torch.equal(got.cpu(), ref) and torch.equal(z.cpu(), far.expand(rows, N))
+            if C % 16 == 0:
+                sw.swin_block_linear_forward_q8(h, *dev(x8, sx, w8, sc, far), got8, residual=res)
+                assert torch.equal(got8.cpu(), ref)
+        sw.swin_block_linear_sync_status(h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,N", [(1, 64, 264), (40, 64, 264), (300, 1032, 2056), (2500, 512, 1024), (4000, 96, 264)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gradient_far_from_zero(rows, C, N, kind):
+    """dz is dy or 0, exactly: what is left are the products' roundings."""
+    x, w, _, _, dy = make(rows, C, N, seed=24)
+    z = torch.tensor(FAR).repeat(N // 8).to(BF).expand(rows, N).contiguous()
+    dz = dy * (z > 0)
+    ref, tol = backward_ref(x, w, None, dz, "none")
+    g = dict(dx=nans(rows, C), dW=nans(N, C), db=nans(N))
+    with linear(C, N, kind) as h:
+        sw.swin_block_linear_backward(h, *dev(x, w, dy), g["dx"], g["dW"], g["db"], z=dev(z))
+        sw.swin_block_linear_sync_status(h)
+    for k in ref:
+        close(g[k], ref[k], tol[k])
+    assert not g["dW"][z[0] < 0].any() and not g["db"][z[0] < 0].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,behind,C,N", [(1, 4, 192, 520), (77, 51, 192, 520), (300, 100, 192, 520),
+                                             (385, 127, 2960, 400), (2500, 60, 512, 1024)])
+def test_in_place_and_rows_behind_the_batch(rows, behind, C, N):
     x, w, b, r, dy = make(rows + behind, C, N, seed=4)
     _, out, _, eo = forward_ref(x[:rows], w, b, r[:rows], "gelu")
     xd, wd, bd, rd, yd = dev(x, w, b, r, dy)
@@ -501,7 +542,8 @@ def test_leading_axes():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,C,N", [(1, 256, 640), (40, 256, 640), (700, 4096, 120)])
+@pytest.mark.parametrize("rows,C,N", [(1, 256, 640), (40, 256, 640), (700, 4096, 120), (1000, 8192, 1032),
+                                      (2500, 512, 2048), (3000, 1024, 1000)])
 def test_streams_and_captured_graphs_share_nothing(rows, C, N):
     x, w, b, _, dy = make(rows, C, N, seed=5)
     x2, _, _, _, dy2 = make(rows, C, N, seed=6)
@@ -613,7 +655,8 @@ def test_simulated_allocation_failure_then_a_normal_call():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows,C,N", [(1, 96, 256), (70, 264, 520), (300, 1032, 2056), (700, 4096, 120)])
+@pytest.mark.parametrize("rows,C,N", [(1, 96, 256), (70, 264, 520), (300, 1032, 2056), (700, 4096, 120), (1000, 8192, 1032),
+                                      (2500, 512, 2048)])
 def test_guard_bands_stay_intact_and_catch_an_overwrite(rows, C, N):
     x, w, b, r, dy = make(rows, C, N, seed=13)
     xd, wd, bd, rd, yd = dev(x, w, b, r, dy)
@@ -633,7 +676,7 @@ def test_two_host_threads_compute_what_one_does():
     """A handle a thread at once: every result is the one that the call gives alone."""
     import threading
     wrong, data = [], []
-    for rows, C, N in ((1, 1000, 640), (128, 256, 1024), (700, 4096, 120), (3001, 96, 384)):
+    for rows, C, N in ((1, 1000, 640), (128, 256, 1024), (700, 4096, 120), (3001, 96, 384), (1300, 2048, 2056)):
         x, w, b, _, dy = dev(*make(rows, C, N, seed=14))
         z = (x @ w.t())
 

@@ -406,7 +406,11 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     }
     const int ld = act ? hidden_ld(h->N) : h->N;
     Product px = dx_product(h->C, h->N, rows, ld), pw = weight_product(h->C, h->N, rows, ld);
-    const ProductsPlan plx = dx ? plan_products(&px, 1) : ProductsPlan{}, plw = dW ? plan_products(&pw, 1) : ProductsPlan{};
+    ProductsPlan plx = dx ? plan_products(&px, 1) : ProductsPlan{};
+    const ProductsPlan plw = dW ? plan_products(&pw, 1) : ProductsPlan{};
+    // few rows: dx by the few-row kernel
+    const bool few = dx && (rows <= FEW_ROWS || few_chosen(px, plx, 64));
+    if (few) plx.part_bytes = 0;
     const ActWgradPlan pa = act && dW ? plan_act_wgrad(h->C, h->N, rows, plw) : ActWgradPlan{};
     const GradPlan pg = plan_grad(h->N, rows);
     FinishArgs fin{};
@@ -471,8 +475,6 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         if (e == cudaSuccess && dW && !pa.chosen)
             e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
     };
-    // (few rows: dx by the few-row kernel)
-    const bool few = dx && (rows <= FEW_ROWS || few_chosen(px, plx, 64));
     const bool side = dx && !few && dW && (pa.chosen || plw.split.cut || db) && (!db || fin.cs.m[0].slices <= SIDE_SLICES) &&
                       !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
     if (side) weight();
