@@ -266,6 +266,9 @@ GradPlan plan_grad(int N, int64_t rows)
 }
 
 constexpr int SIDE_SLICES = 512;   // partial rows of db that dx's warps add
+// Rows that one warp adds to the end (a launch less: 34 x 336 x 576 GELU 15.5 us and
+// 13.7, 300 x 1032 x 256 16.1 and 13.8; more rows a warp would be late: not tried).
+constexpr int FEW_SUMS = 64;
 
 // The shapes of the backward's products.
 Product dx_product(int C, int N, int rows, int ld)
@@ -413,23 +416,20 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     if (few) plx.part_bytes = 0;
     const ActWgradPlan pa = act && dW ? plan_act_wgrad(h->C, h->N, rows, plw) : ActWgradPlan{};
     const GradPlan pg = plan_grad(h->N, rows);
+    // What dW's kernel leaves, cut tiles and db's partial rows, is finished by dx's
+    // epilogue warps under their first tile's MMAs: where they are on most SMs, db's
+    // rows are few, and no launch is left to save otherwise (dx's own cut tiles).
+    // 12544 x 512 x 2048 GELU 60.2 us, 69.7 by a launch of its own, 50000 x 256 x 1024
+    // 80 and 91, 2000 x 2048 x 2048 36.4 and 42.3; 300 x 512 x 1024, on 16 SMs, 48.6
+    // and 24.
+    const int slices = pa.chosen ? pa.slices : act ? pg.slices : rows <= FEW_SUMS ? 1 : column_slices(rows);
+    const bool side = dx && !few && dW && (pa.chosen || plw.split.cut || db) && (!db || slices <= SIDE_SLICES) &&
+                      !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
+    // Few rows to add (of dy, or of dz's kernel's partial sums) are added to the end by
+    // the weight gradient's waiting warps, one a group of columns, no launch for that.
+    const bool direct = db && (!act ? rows <= FEW_SUMS : !pa.chosen && !side && !plw.split.cut && slices <= FEW_SUMS);
     FinishArgs fin{};
-    size_t sum_bytes = 0;
-    // few rows of dy are added to the end by one warp a column, no launch for a join
-    // (16 x 72 x 8432: 2 us of 20)
-    bool direct = false;
-    if (db) {
-        // from dz's kernel, or (dz is dy) by the weight gradient's waiting warps
-        auto &m = fin.cs.m[fin.cs.n++];
-        m.out = (bf16 *)db;
-        m.b = act ? nullptr : (const bf16 *)dy;
-        m.rows = rows;
-        m.cols = h->N;
-        direct = !act && rows <= 64;
-        m.slices = pa.chosen ? pa.slices : act ? pg.slices : direct ? 1 : column_slices(rows);
-        m.tasks = act ? 0 : ceil_div(h->N, 256) * m.slices;
-        sum_bytes = (size_t)m.slices * h->N * sizeof(float);
-    }
+    const size_t sum_bytes = db && (act || !direct) ? (size_t)slices * h->N * sizeof(float) : 0;
     Carve size(nullptr);
     const size_t dz_bytes = act && (dx || !pa.chosen) ? (size_t)rows * ld * 2 : 0,
                  w_bytes = pa.chosen ? pa.part_bytes : plw.part_bytes;
@@ -444,7 +444,17 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     bf16 *dz = (bf16 *)carve.take(dz_bytes);
     float *x_part = (float *)carve.take(plx.part_bytes), *w_part = (float *)carve.take(w_bytes);
     float *sum_part = (float *)carve.take(sum_bytes);
-    if (db) fin.cs.m[0].part = direct ? nullptr : sum_part;
+    if (db) {
+        auto &m = fin.cs.m[fin.cs.n++];
+        m.out = (bf16 *)db;
+        m.cols = h->N;
+        m.part = direct ? nullptr : sum_part;
+        m.b = act ? nullptr : (const bf16 *)dy;
+        m.f = act ? sum_part : nullptr;
+        m.rows = act ? slices : rows;
+        m.slices = direct ? 1 : slices;
+        m.tasks = !act ? ceil_div(h->N, 256) * m.slices : direct ? ceil_div(h->N, 128) : 0;
+    }
     px.a[0] = pw.a[0] = act ? (const void *)dz : dy;
     px.b[0] = W;
     px.d = (bf16 *)dx;
@@ -465,18 +475,10 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         e = launch_maybe_overlapped(h->act == ACT_SILU ? act_grad_kernel<ACT_SILU> : act_grad_kernel<ACT_GELU>,
                                     dim3((unsigned)pg.columns, (unsigned)pg.slices), dim3(256), 0, s, 1, a);
     }
-    // What dW's kernel leaves, cut tiles and db's partial rows, is finished by dx's
-    // epilogue warps under their first tile's MMAs: where they are on most SMs, db's
-    // rows are few, and no launch is left to save otherwise (dx's own cut tiles).
-    // 12544 x 512 x 2048 GELU 60.2 us, 69.7 by a launch of its own, 50000 x 256 x 1024
-    // 80 and 91, 2000 x 2048 x 2048 36.4 and 42.3; 300 x 512 x 1024, on 16 SMs, 48.6
-    // and 24.
     auto weight = [&]() {
         if (e == cudaSuccess && dW && !pa.chosen)
             e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1);
     };
-    const bool side = dx && !few && dW && (pa.chosen || plw.split.cut || db) && (!db || fin.cs.m[0].slices <= SIDE_SLICES) &&
-                      !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
     if (side) weight();
     if (e == cudaSuccess && dx) {
         const FinishArgs left = fin;
