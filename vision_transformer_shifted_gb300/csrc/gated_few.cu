@@ -6,9 +6,10 @@
 //
 // A CTA takes one tile of 128 weight rows (64 of Wg and the same 64 of Wu, or
 // 128 of Wd) and a share of K; the CTAs of a cluster share a tile's K (up to
-// eight), which spreads few tiles over the SMs without partial sums in global
-// memory: each CTA leaves its fp32 tile in shared memory and the cluster's CTAs
-// add their shares of it through distributed shared memory, in rank order.
+// eight, the linear operator's few tiles sixteen), which spreads few tiles over
+// the SMs without partial sums in global memory: each CTA leaves its fp32 tile in
+// shared memory and the cluster's CTAs add their shares of it through distributed
+// shared memory, in rank order.
 // Weights stream through a TMA ring of about 100 KB a CTA, two CTAs an SM: HBM
 // bounds it, and the latency of two launches (9 us + bytes / 7.07 TB/s over the
 // sizes; 1 x 2048 x 5632: 20 us, 24 rows from e4m3 4096 x 11264: 37).
@@ -31,7 +32,8 @@ constexpr int FEW_THREADS = 192;   // four draining warps, a loading and an issu
 // (FORM_UP + ACT_*), its last product, the linear operator, or its dx (these two in
 // chunks of 128 rows).
 enum { FORM_UP = 0, FORM_DOWN = -1, FORM_LINEAR = -2, FORM_DX = -3 };
-constexpr int FEW_MAX_STAGES = 6;
+constexpr int FEW_MAX_STAGES = 11;
+constexpr int FEW_RING = 110 * 1024, FEW_RING_ALONE = 200 * 1024;   // bytes, of two CTAs an SM and of one
 
 struct FewArgs {
     CUtensorMap w0, w1, x;         // up: Wg, Wu (boxes of 64 rows); else Wd or W (128 rows); x: np rows
@@ -296,12 +298,18 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     while (a.split < 8 && tiles * a.split < sm_count() && a.kb >= 4 * a.split) a.split *= 2;
     // (the linear operator, one kernel: as many as two an SM hold; 24 rows from e4m3
     // 4096 x 11264, 88 tiles, 12.9 us with two, 12.3 with three)
-    if (FORM <= FORM_LINEAR)
-        for (a.split = 1; a.split < 8 && tiles * (a.split + 1) <= 2 * sm_count() && a.kb >= 4 * (a.split + 1);) ++a.split;
-    // two CTAs an SM (three stages with 128 rows, up to six with 16)
+    if (FORM <= FORM_LINEAR) {
+        const int most = tiles <= FEW_WIDE_TILES ? 16 : 8;
+        for (a.split = 1; a.split < most && tiles * (a.split + 1) <= 2 * sm_count() && a.kb >= 4 * (a.split + 1);) ++a.split;
+    }
+    // Two CTAs an SM (three stages with 128 rows, up to six with 16), or, from 64 rows,
+    // where all clusters have room so, one with twice the ring (128 x 8192 x 512, 32 CTAs,
+    // 12.4 us and 11.3; 16 rows no change, and the next kernel starts later; 128 CTAs
+    // of clusters of eight do not fit at once: 385 x 2968 x 400 9.7 and 12.4).
+    const bool alone = FORM <= FORM_LINEAR && a.np >= 64 && tiles * a.split <= 16 * FEW_WIDE_TILES;
     a.stage_bytes = 16384 + a.np * 128;
-    a.stages = 110 * 1024 / a.stage_bytes;
-    static_assert(110 * 1024 / (16384 + 16 * 128) <= FEW_MAX_STAGES && 3 * (16384 + 128 * 128) <= 110 * 1024, "ring");
+    a.stages = (alone ? FEW_RING_ALONE : FEW_RING) / a.stage_bytes;
+    static_assert(FEW_RING_ALONE / (16384 + 16 * 128) <= FEW_MAX_STAGES && 3 * (16384 + 128 * 128) <= FEW_RING, "ring");
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes;
     static std::atomic<uint64_t> ready;
     int dev = 0;
@@ -309,7 +317,10 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
-        e = cudaFuncSetAttribute(few_rows_kernel<FORM, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 111 * 1024);
+        e = cudaFuncSetAttribute(few_rows_kernel<FORM, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 1024 + (FORM <= FORM_LINEAR ? FEW_RING_ALONE : FEW_RING));
+        if (e == cudaSuccess && FORM <= FORM_LINEAR)
+            e = cudaFuncSetAttribute(few_rows_kernel<FORM, Q8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }

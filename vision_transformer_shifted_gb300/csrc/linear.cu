@@ -85,7 +85,8 @@ bool few_chosen(const Product &p, const ProductsPlan &pl, int elems)
     if (tiles > 2 * sm_count()) return false;
     const int kb = ceil_div(p.k[0], elems);
     int split = (int)(2 * sm_count() / tiles);
-    split = split > 8 ? 8 : split;
+    const int most = tiles <= FEW_WIDE_TILES ? 16 : 8;
+    split = split > most ? most : split;
     if (4 * split > kb) split = kb / 4 > 1 ? kb / 4 : 1;
     const double bytes = tiles * kb * 32768 / 13e6, blocks = 0.5 * ceil_div(kb, split);
     const PairSplit &s = pl.split;
