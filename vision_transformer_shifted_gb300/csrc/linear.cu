@@ -267,9 +267,11 @@ GradPlan plan_grad(int N, int64_t rows)
 }
 
 constexpr int SIDE_SLICES = 512;   // partial rows of db that dx's warps add
-// Rows that one warp adds to the end (a launch less: 34 x 336 x 576 GELU 15.5 us and
-// 13.7, 300 x 1032 x 256 16.1 and 13.8; more rows a warp would be late: not tried).
-constexpr int FEW_SUMS = 64;
+// Rows that one warp adds to the end, no launch for a join: 34 x 336 x 576 GELU 15.5 us
+// and 13.8, 250 x 512 x 128 without activation 13.1 and 10.1, 130 x 2048 x 2048 19.4 and
+// 17.5, 600 x 512 x 1024 GELU (over 64 partial rows of dz's kernel) 22.8 and 19.1.  More
+// would keep the warp, and the tile it drains next, longer than a launch takes.
+constexpr int FEW_SUMS = 256;
 
 // The shapes of the backward's products.
 Product dx_product(int C, int N, int rows, int ld)
@@ -427,7 +429,7 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     const bool side = dx && !few && dW && (pa.chosen || plw.split.cut || db) && (!db || slices <= SIDE_SLICES) &&
                       !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
     // Few rows to add (of dy, or of dz's kernel's partial sums) are added to the end by
-    // the weight gradient's waiting warps, one a group of columns, no launch for that.
+    // the weight gradient's waiting warps.
     const bool direct = db && (!act ? rows <= FEW_SUMS : !pa.chosen && !side && !plw.split.cut && slices <= FEW_SUMS);
     FinishArgs fin{};
     const size_t sum_bytes = db && (act || !direct) ? (size_t)slices * h->N * sizeof(float) : 0;
@@ -454,7 +456,7 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         m.f = act ? sum_part : nullptr;
         m.rows = act ? slices : rows;
         m.slices = direct ? 1 : slices;
-        m.tasks = !act ? ceil_div(h->N, 256) * m.slices : direct ? ceil_div(h->N, 128) : 0;
+        m.tasks = direct ? ceil_div(h->N, act ? 16 : 32) : act ? 0 : ceil_div(h->N, 256) * m.slices;
     }
     px.a[0] = pw.a[0] = act ? (const void *)dz : dy;
     px.b[0] = W;

@@ -214,51 +214,75 @@ struct ColumnSums {
         const bf16 *b;    // bf16, or
         const float *f;   // fp32
         bf16 *out;
-        float *part;      // [slices, cols], or (one slice) null: it goes to out
+        float *part;      // [slices, cols], or (few rows) null: added to the end, to out
         int64_t rows;
         int cols, slices, tasks;   // tasks: slices of every group of columns
     } m[3];
     int n;
 };
+// Adds to v the values of 16 bytes.
+template <class T, int V>
+__device__ __forceinline__ void add16(float (&v)[V], const uint4 &u)
+{
+    static_assert(V == 16 / sizeof(T), "16 bytes");
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (V == 4) {
+            v[e] += __uint_as_float(w[e]);
+        } else {
+            v[2 * e % V] += __uint_as_float(w[e] << 16);
+            v[(2 * e + 1) % V] += __uint_as_float(w[e] & 0xffff0000u);
+        }
+    }
+}
 template <class T>
-__device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols, int c, int slice, int slices, float *part,
-                                             bf16 *out)
+__device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols, int c, int slice, int slices, float *part)
 {
     constexpr int V = 16 / sizeof(T);
     if (c >= cols) return;
     float v[V] = {};
     int64_t i = slice;
-    auto add = [&](const uint4 &u) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (V == 4) {
-                v[e] += __uint_as_float(w[e]);
-            } else {
-                v[2 * e % V] += __uint_as_float(w[e] << 16);
-                v[(2 * e + 1) % V] += __uint_as_float(w[e] & 0xffff0000u);
-            }
-        }
-    };
 #pragma unroll 1
     for (; i + 7 * (int64_t)slices < rows; i += 8 * (int64_t)slices) {
         uint4 u[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(p + (i + k * (int64_t)slices) * cols + c);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) add(u[k]);
+        for (int k = 0; k < 8; ++k) add16<T>(v, u[k]);
     }
 #pragma unroll 1
-    for (; i < rows; i += slices) add(*reinterpret_cast<const uint4 *>(p + i * cols + c));
-    if (!part) {   // (one slice, and nothing to add later)
-#pragma unroll
-        for (int e = 0; e < V; e += 4)
-            *reinterpret_cast<uint2 *>(out + c + e) = make_uint2(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]));
-        return;
-    }
+    for (; i < rows; i += slices) add16<T>(v, *reinterpret_cast<const uint4 *>(p + i * cols + c));
 #pragma unroll
     for (int e = 0; e < V; e += 4)
         *reinterpret_cast<float4 *>(part + (int64_t)slice * cols + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+}
+// Few rows to the end: four lanes across the columns, eight rows at a time.
+template <class T>
+__device__ __forceinline__ void column_few(const T *p, int rows, int cols, int c, int lane, bf16 *out)
+{
+    constexpr int V = 16 / sizeof(T);
+    c += (lane & 3) * V;
+    const bool in = c < cols;
+    float v[V] = {};
+#pragma unroll 1
+    for (int i = lane >> 2; i < rows; i += 64) {
+        uint4 u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            u[k] = in && i + 8 * k < rows ? *reinterpret_cast<const uint4 *>(p + (int64_t)(i + 8 * k) * cols + c)
+                                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add16<T>(v, u[k]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+    if (!in || lane >= 4) return;
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+        *reinterpret_cast<uint2 *>(out + c + e) = make_uint2(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]));
 }
 // Warp w's share, of `warps`.
 __device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int warps, int lane)
@@ -267,9 +291,14 @@ __device__ __forceinline__ void column_partials(const ColumnSums &a, int w, int 
     for (int z = 0; z < a.n; ++z) {
         const auto &m = a.m[z];
         for (; t < m.tasks; t += warps) {
+            if (!m.part) {
+                if (m.b) column_few(m.b, (int)m.rows, m.cols, t * 32, lane, m.out);
+                else column_few(m.f, (int)m.rows, m.cols, t * 16, lane, m.out);
+                continue;
+            }
             const int slice = t % m.slices, g = t / m.slices;
-            if (m.b) column_slice(m.b, m.rows, m.cols, g * 256 + lane * 8, slice, m.slices, m.part, m.out);
-            else column_slice(m.f, m.rows, m.cols, g * 128 + lane * 4, slice, m.slices, m.part, m.out);
+            if (m.b) column_slice(m.b, m.rows, m.cols, g * 256 + lane * 8, slice, m.slices, m.part);
+            else column_slice(m.f, m.rows, m.cols, g * 128 + lane * 4, slice, m.slices, m.part);
         }
         t -= m.tasks;
     }
