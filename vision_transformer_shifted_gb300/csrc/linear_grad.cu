@@ -347,14 +347,14 @@ ActWgradPlan plan_act_wgrad(int C, int N, int rows, const ProductsPlan &apart)
     p.part_bytes = (size_t)tiles * p.slices * 256 * p.n * sizeof(float);
     // Estimates in us: the trips of z, dy and dz at 6 TB/s (as a launch of their own
     // worse), a K block of a tile here and of a whole tile in dW's own product, launches
-    // and joins.  Measured, whole backwards, dz apart and here: 12544 x 512 x 2048 88.6
-    // and 60.4, 12544 x 768 x 768 54.0 and 38.4, 5001 x 1000 x 1000 55.5 and 34.7, 3136
-    // x 384 x 1536 40.9 and 31.5, 12544 x 1024 x 4096 186 and 182; not taken: 8192 x 2048
-    // x 2048 112.5 and 114.6, 3000 x 1024 x 4096 57.3 and 63.8, 2000 x 2048 x 2048 36.6
-    // and 54.5, 300 x 512 x 1024 18.9 and 24.2; 27 sizes: 0.7% above the better
-    // of both on average.
+    // and joins.  Measured, whole backwards, dz apart and here: 12544 x 512 x 2048 89.2
+    // and 61.9, 12544 x 768 x 768 54.2 and 40.7, 5000 x 1000 x 1000 55.7 and 36.0, 3136
+    // x 384 x 1536 40.9 and 31.4, 12544 x 1024 x 4096 188 and 182; not taken: 8192 x 2048
+    // x 2048 114.5 and 123.1, 3000 x 1024 x 4096 57.2 and 64.6, 2000 x 2048 x 2048 36.7
+    // and 54.8, 1500 x 512 x 512 20.4 and 28.1; 40 sizes: 0.8% above the better of both
+    // on average.
     const double trips = 6.0 * rows * N / 6.0e6, blocks = p.slice_kb * (0.6 + 0.5 * p.n / 512);
-    p.chosen = 13 + (blocks > trips ? blocks : trips) < 10 + 1.25 * trips + 0.00283 * (double)apart.cost;
+    p.chosen = 14 + (blocks > trips ? blocks : trips) < 10 + 1.25 * trips + 0.00283 * (double)apart.cost;
     return p;
 }
 
