@@ -20,6 +20,7 @@
 // its own pass over the weights, the later ones from L2.
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "gated.cuh"
 
@@ -66,9 +67,8 @@ __device__ __forceinline__ void add4(float (&s)[4], const float4 &v)
     s[2] += v.z;
     s[3] += v.w;
 }
-__device__ __forceinline__ void add4(float (&s)[4], const bf16 *p)
+__device__ __forceinline__ void add4(float (&s)[4], const uint2 &u)   // (bf16)
 {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
     const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
     add4(s, make_float4(a.x, a.y, b.x, b.y));
 }
@@ -235,53 +235,91 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (split > 1) cluster_sync_all();
     // the cluster's CTAs finish every split-th group of output values, four
-    // neighbours a thread
+    // neighbours a thread, always of the same columns
     const uint32_t base = smem_u32(smem);
-    const int items = (CHUNKS && a.rows - row0 > FEW_ROWS ? FEW_ROWS : a.rows - row0) * (W / 4);
-    for (int e = rank * FEW_THREADS + (int)threadIdx.x; e < items; e += split * FEW_THREADS) {
-        const int u0 = e / (W / 4), t = row0 + u0, i = e % (W / 4) * 4, c = tile * W + i;   // (u0: row of the chunk)
-        if (c >= a.cols) continue;   // (cols is a multiple of 8)
-        float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int r = 0; r < split; ++r) {
-            const uint32_t at = map_rank(base + (uint32_t)(u0 * 128 + i) * 4, r);
-            add4(v, ld_cluster(at));
-            if (FORM >= FORM_UP) add4(u, ld_cluster(at + 64 * 4));
-        }
-        if (Q8) {
-            const float sx = a.sx[t];
-            const float4 p = *reinterpret_cast<const float4 *>(a.s0 + c);
-            v[0] *= sx * p.x; v[1] *= sx * p.y; v[2] *= sx * p.z; v[3] *= sx * p.w;
-            if (FORM >= FORM_UP) {
-                const float4 q = *reinterpret_cast<const float4 *>(a.s1 + c);
-                u[0] *= sx * q.x; u[1] *= sx * q.y; u[2] *= sx * q.z; u[3] *= sx * q.w;
+    const int rows = CHUNKS && a.rows - row0 > FEW_ROWS ? FEW_ROWS : a.rows - row0;
+    const int first = rank * FEW_THREADS + (int)threadIdx.x, i = first % (W / 4) * 4, c = tile * W + i;
+    const bool in = c < a.cols;   // (cols is a multiple of 8)
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 s0 = Q8 && in ? *reinterpret_cast<const float4 *>(a.s0 + c) : zero,
+                 s1 = Q8 && FORM >= FORM_UP && in ? *reinterpret_cast<const float4 *>(a.s1 + c) : zero;
+    const uint2 none = make_uint2(0, 0);
+    const uint2 b0 = a.b0 && in ? *reinterpret_cast<const uint2 *>(a.b0 + c) : none,
+                b1 = FORM >= FORM_UP && a.b1 && in ? *reinterpret_cast<const uint2 *>(a.b1 + c) : none;
+    if (split > 1) cluster_sync_all();
+    const int step = split * FEW_THREADS / (W / 4);   // rows between a thread's
+    auto finish = [&](auto at_once) {
+        constexpr int N = decltype(at_once)::value;
+#pragma unroll 1
+        for (int r0 = first / (W / 4); in && r0 < rows; r0 += N * step) {
+            float v[N][4], u[N][4], sx[N];
+            uint2 res[N];
+            int row[N];   // (past the end the first one again)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                row[j] = r0 + j * step < rows ? r0 + j * step : r0;
+                const int64_t t = row0 + row[j];
+                res[j] = FORM < FORM_UP && a.residual ? *reinterpret_cast<const uint2 *>(a.residual + t * a.ld + c) : none;
+                sx[j] = Q8 ? a.sx[t] : 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[j][k] = u[j][k] = 0.f;
+            }
+#pragma unroll(N == 1 ? 4 : 1)
+            for (int r = 0; r < split; ++r) {
+                float4 w[N], x[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const uint32_t at = map_rank(base + (uint32_t)(row[j] * 128 + i) * 4, r);
+                    w[j] = ld_cluster(at);
+                    if (FORM >= FORM_UP) x[j] = ld_cluster(at + 64 * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    add4(v[j], w[j]);
+                    if (FORM >= FORM_UP) add4(u[j], x[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (j && r0 + j * step >= rows) break;
+                const int64_t at = (int64_t)(row0 + row[j]) * a.ld + c;
+                float *p = v[j], *q = u[j];
+                if (Q8) {
+                    p[0] *= sx[j] * s0.x; p[1] *= sx[j] * s0.y; p[2] *= sx[j] * s0.z; p[3] *= sx[j] * s0.w;
+                    if (FORM >= FORM_UP) {
+                        q[0] *= sx[j] * s1.x; q[1] *= sx[j] * s1.y; q[2] *= sx[j] * s1.z; q[3] *= sx[j] * s1.w;
+                    }
+                }
+                if (a.b0) add4(v[j], b0);
+                if (FORM == FORM_LINEAR) {
+                    if (a.z) *reinterpret_cast<uint2 *>(a.z + at) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const f2 g = pack2(p[k], p[k + 1]);
+                        unpack2(a.act == ACT_SILU ? activate2<ACT_SILU>(g) : a.act == ACT_GELU ? activate2<ACT_GELU>(g) : g, p[k],
+                                p[k + 1]);
+                    }
+                }
+                if (FORM < FORM_UP) {
+                    if (a.residual) add4(v[j], res[j]);
+                } else {
+                    if (a.b1) add4(u[j], b1);
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2)
+                        unpack2(mul2(activate2<(FORM < FORM_UP ? ACT_NONE : FORM)>(pack2(p[k], p[k + 1])), pack2(q[k], q[k + 1])),
+                                p[k], p[k + 1]);
+                }
+                *reinterpret_cast<uint2 *>(a.out + at) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
             }
         }
-        if (a.b0) add4(v, a.b0 + c);
-        if (FORM == FORM_LINEAR) {
-            if (a.z)
-                *reinterpret_cast<uint2 *>(a.z + (int64_t)t * a.ld + c) =
-                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                const f2 g = pack2(v[k], v[k + 1]);
-                unpack2(a.act == ACT_SILU ? activate2<ACT_SILU>(g) : a.act == ACT_GELU ? activate2<ACT_GELU>(g) : g, v[k],
-                        v[k + 1]);
-            }
-        }
-        if (FORM < FORM_UP) {
-            if (a.residual) add4(v, a.residual + (int64_t)t * a.ld + c);
-        } else {
-            if (a.b1) add4(u, a.b1 + c);
-#pragma unroll
-            for (int k = 0; k < 4; k += 2)
-                unpack2(mul2(activate2<(FORM < FORM_UP ? ACT_NONE : FORM)>(pack2(v[k], v[k + 1])), pack2(u[k], u[k + 1])), v[k], v[k + 1]);
-        }
-        *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ld + c) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    }
+    };
+    // The linear operator's few CTAs a tile take their many rows several at a time, so
+    // that the latencies of shared memory, the residual and the scales pass together
+    // (126 x 256 x 768 9.1 us and 6.3, 128 x 512 x 512 9.2 and 7.3; clusters of eight or
+    // sixteen have the loads of their ranks in flight: 100 x 4096 x 4096 14.5 and 20.9).
+    if (CHUNKS && split <= 2) finish(std::integral_constant<int, 4>{});
+    else finish(std::integral_constant<int, 1>{});
     if (split > 1) cluster_sync_all();   // (the others have read this CTA's sums)
     if (warp == 5) tmem_dealloc(tmem, tcols);
 }
