@@ -294,7 +294,8 @@ def test_plan_refuses():
 SHAPES = [   # rows, C, N
     (1, 8, 8), (1, 96, 384), (1, 512, 1368), (1, 8208, 40), (1, 1040, 6152), (2, 64, 64), (5, 136, 120), (17, 128, 264), (24, 1024, 2048),
     (64, 256, 640), (127, 192, 512), (128, 96, 128), (129, 328, 136), (256, 512, 512), (300, 1032, 2056),
-    (515, 128, 384), (385, 2968, 400), (1000, 64, 1024), (3001, 96, 384), (2048, 768, 1024), (700, 4096, 120), (300, 8208, 264)]
+    (515, 128, 384), (385, 2968, 400), (1000, 64, 1024), (3001, 96, 384), (2048, 768, 1024), (700, 4096, 120), (300, 8208, 264),
+    (40, 2048, 4864), (100, 520, 720)]
 
 
 @pytest.mark.gpu

@@ -324,6 +324,39 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
     if (warp == 5) tmem_dealloc(tmem, tcols);
 }
 
+// Clusters of `split` CTAs that find room at once, of one CTA an SM or two: the
+// device's processor clusters differ in size, and a cluster lies in one of them
+// (clusters of eight, two CTAs an SM: 36, not 38; of sixteen, one an SM: 7).
+// The question is put for a kernel of its own, never launched, with this one's threads
+// and shared memory: of one that allocates tensor memory the answer is one CTA an SM,
+// whatever it allocates.
+__global__ void __launch_bounds__(FEW_THREADS) few_room() {}
+int few_clusters(int split, bool alone)
+{
+    static std::atomic<int> known[2][17];
+    int n = known[alone][split].load();
+    if (n) return n;
+    const void *kern = (const void *)few_room;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr;
+    cfg.gridDim = dim3((unsigned)(split * 2 * sm_count()));
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = 2048 + (alone ? FEW_RING_ALONE : FEW_RING);   // (and the barriers)
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 + FEW_RING_ALONE) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return (alone ? 1 : 2) * sm_count() / split;   // (no device: a plan is asked for)
+    }
+    known[alone][split].store(n);
+    return n;
+}
+
 template <int FORM, bool Q8>
 cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
 {
@@ -334,17 +367,12 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     const int chunks = FORM <= FORM_LINEAR ? (a.rows + FEW_ROWS - 1) / FEW_ROWS : 1, tiles = a.tiles * chunks;
     a.split = 1;
     while (a.split < 8 && tiles * a.split < sm_count() && a.kb >= 4 * a.split) a.split *= 2;
-    // (the linear operator, one kernel: as many as two an SM hold; 24 rows from e4m3
-    // 4096 x 11264, 88 tiles, 12.9 us with two, 12.3 with three)
-    if (FORM <= FORM_LINEAR) {
-        const int most = tiles <= FEW_WIDE_TILES ? 16 : 8;
-        for (a.split = 1; a.split < most && tiles * (a.split + 1) <= 2 * sm_count() && a.kb >= 4 * (a.split + 1);) ++a.split;
-    }
+    if (FORM <= FORM_LINEAR) a.split = few_split(tiles, a.kb);
     // Two CTAs an SM (three stages with 128 rows, up to six with 16), or, from 64 rows,
-    // where all clusters have room so, one with twice the ring (128 x 8192 x 512, 32 CTAs,
-    // 12.4 us and 11.3; 16 rows no change, and the next kernel starts later; 128 CTAs
-    // of clusters of eight do not fit at once: 385 x 2968 x 400 9.7 and 12.4).
-    const bool alone = FORM <= FORM_LINEAR && a.np >= 64 && tiles * a.split <= 16 * FEW_WIDE_TILES;
+    // where all clusters find room so, one with twice the ring (128 x 8192 x 512, 32 CTAs,
+    // 12.4 us and 11.3; 16 rows no change, and the next kernel starts later; sixteen
+    // clusters of eight, of which fifteen fit: 385 x 2968 x 400 9.7 and 12.4).
+    const bool alone = FORM <= FORM_LINEAR && a.np >= 64 && tiles <= few_clusters(a.split, true);
     a.stage_bytes = 16384 + a.np * 128;
     a.stages = (alone ? FEW_RING_ALONE : FEW_RING) / a.stage_bytes;
     static_assert(FEW_RING_ALONE / (16384 + 16 * 128) <= FEW_MAX_STAGES && 3 * (16384 + 128 * 128) <= FEW_RING, "ring");
@@ -379,6 +407,21 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
 }
 
 } // namespace
+
+// As many as two an SM hold in one round (24 rows from e4m3 4096 x 11264, 88 tiles,
+// 12.9 us with two, 12.3 with three; one cluster in a second round: 100 x 4096 x 4800, 38
+// tiles by eight, 21.6, by six 14.3; 24 x 4096 x 9600, 75 by four, 23.3, by three 17.9),
+// up to sixteen where the tiles are so few that one an SM does (128 x 8192 x 512 12.3 us
+// by eight, 10.1; 64 x 8192 x 896, seven tiles, 10.4 and 8.9; eight tiles, 128 x 4096 x
+// 1024, 9.8 and 12.3), with four K blocks each at least.
+int few_split(int64_t tiles, int kb)
+{
+    const int most = tiles <= few_clusters(16, true) ? 16 : 8;
+    int split = 1;
+    for (int s = 2; s <= most && kb >= 4 * s; ++s)
+        if (tiles <= few_clusters(s, false)) split = s;
+    return split;
+}
 
 cudaError_t launch_few_up(const FewUp &u, DeviceStatus st, cudaStream_t stream)
 {

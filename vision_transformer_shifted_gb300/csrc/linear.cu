@@ -84,11 +84,7 @@ bool few_chosen(const Product &p, const ProductsPlan &pl, int elems)
     const int64_t tiles = (int64_t)ceil_div(p.cols, 128) * ceil_div(p.rows, FEW_ROWS);
     if (tiles > 2 * sm_count()) return false;
     const int kb = ceil_div(p.k[0], elems);
-    int split = (int)(2 * sm_count() / tiles);
-    const int most = tiles <= FEW_WIDE_TILES ? 16 : 8;
-    split = split > most ? most : split;
-    if (4 * split > kb) split = kb / 4 > 1 ? kb / 4 : 1;
-    const double bytes = tiles * kb * 32768 / 13e6, blocks = 0.5 * ceil_div(kb, split);
+    const double bytes = tiles * kb * 32768 / 13e6, blocks = 0.5 * ceil_div(kb, few_split(tiles, kb));
     const PairSplit &s = pl.split;
     const double whole = pl.wn == 256 ? 1.0 : pl.wn == 192 ? 0.82 : 0.55;
     const double pairs = s.cut ? 17.5 + 0.283 * whole * ((double)s.full * kb + s.q)

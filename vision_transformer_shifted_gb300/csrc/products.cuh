@@ -737,10 +737,8 @@ struct Carve {
 // ---- few rows (gated_few.cu) -------------------------------------------------------
 
 constexpr int FEW_ROWS = 128;   // most rows of the few-row kernels
-// Tiles of the linear operator whose K goes to clusters of up to sixteen CTAs, not
-// eight: seven such clusters find room at once (128 x 8192 x 512 12.3 us by eight, 10.1;
-// 64 x 8192 x 896, seven tiles, 10.4 and 8.9; eight tiles, 128 x 4096 x 1024, 9.8 and 12.3).
-constexpr int FEW_WIDE_TILES = 7;
+// CTAs that share the K (kb blocks) of each of the linear operator's tiles.
+int few_split(int64_t tiles, int kb);
 // The linear operator for few rows, one launch.
 struct FewLinear {
     const void *x, *w;
