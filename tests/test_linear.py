@@ -20,12 +20,15 @@ cases, so the relative error in the 2-norm is held too: a rounding of at most
 """
 import ctypes
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from vision_transformer_shifted_gb300 import binding as sw
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DEV = "cuda"
 BF, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 HALF = 2.0 ** -8
@@ -605,6 +608,45 @@ def test_first_call_of_a_handle_captured():
         close(out, ref, eo)
         del gr
         torch.cuda.synchronize()
+
+
+FIRST = """
+import torch
+from vision_transformer_shifted_gb300 import binding as sw
+rows, C, N = %d, %d, %d
+n = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+x, w, b, y, g, bt = n(rows, C), n(N, C), n(N), n(rows, N), n(C), n(C)
+norm, z, out, dx, ds, dW, db = n(rows, C), n(rows, N), n(rows, N), n(rows, C), n(rows, C), n(N, C), n(N)
+dg = torch.empty(2, C, device="cuda")
+h, ln = sw.swin_block_linear_create(C, N, sw.BLOCK_LINEAR_GELU), sw.swin_block_layernorm_create(C, 1e-5)
+def call():
+    sw.swin_block_layernorm_forward(ln, x, g, bt, norm)
+    sw.swin_block_linear_forward(h, norm, w, b, out, z=z)
+    sw.swin_block_linear_backward(h, norm, w, y, dx, dW, db, z=z)
+    sw.swin_block_layernorm_backward(ln, x, g, dx, ds, dg[0], dg[1])
+    return [t.clone() for t in (norm, z, out, dx, dW, db, ds, dg)]
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    got = call()
+gr.replay()
+torch.cuda.synchronize()
+sw.swin_block_linear_sync_status(h)
+assert all(torch.equal(a, b) for a, b in zip(got, call()))
+del gr
+torch.cuda.synchronize()
+sw.swin_block_linear_destroy(h)
+sw.swin_block_layernorm_destroy(ln)
+print("same")
+"""
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,N", [(1, 256, 640), (40, 4096, 640), (300, 1032, 2056), (2500, 512, 1024)])
+def test_first_call_of_a_process_captured(rows, C, N):
+    """The first call a process makes at all may be a captured one: what the library
+    asks the device, or loads, on the way is allowed there."""
+    done = subprocess.run([sys.executable, "-c", FIRST % (rows, C, N)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip() == "same", done.stderr[-2000:]
 
 
 @pytest.mark.gpu
