@@ -1,21 +1,25 @@
 """Builds libswin_wattn.so in-tree with nvcc for sm_103a.
 
 Each CUDA source is compiled to an object in parallel, then linked into a
-shared library beside this file.  No CMake, no torch extension machinery.
+shared library beside this file; the binding's argument checks (arguments.cpp)
+become a module of their own there.  No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libswin_wattn.so")
+ARGUMENTS = os.path.join(HERE, "_arguments.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
@@ -33,7 +37,7 @@ def sources():
 
 
 def _deps_mtime():
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
     inc = os.path.join(ROOT, "include")
     files += [os.path.join(inc, f) for f in os.listdir(inc)]
     files.append(os.path.abspath(__file__))
@@ -41,7 +45,7 @@ def _deps_mtime():
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, ARGUMENTS)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -56,8 +60,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(res.stdout + res.stderr)
         return obj
 
+    def arguments():
+        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+        tmp = ARGUMENTS + ".%d.tmp" % os.getpid()
+        res = subprocess.run(
+            ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+             "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include/torch/csrc/api/include"),
+             os.path.join(CSRC, "arguments.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_cpu", "-lc10"],
+            capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("g++ failed for arguments.cpp:\n" + res.stdout + res.stderr)
+        os.replace(tmp, ARGUMENTS)
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        beside = ex.submit(arguments)
         objs = list(ex.map(compile_one, sources()))
+    beside.result()
     tmp = LIB + ".%d.tmp" % os.getpid()
     res = subprocess.run([cc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp], capture_output=True, text=True)
     if res.returncode != 0:
