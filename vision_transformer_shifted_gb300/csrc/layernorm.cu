@@ -6,8 +6,8 @@
 // output written once, the row stays in registers (the backward: shared memory)
 // between the statistics and the output, and HBM bounds it: 200704 x 96 with the
 // residual 23.7 us, 6.5 TB/s; post-norm 589824 x 192 103.7 us, 6.55 TB/s; e4m3
-// 8191 x 4096 39.7 us, 5.9 TB/s; backward 589824 x 192 with dsum 140 us, 6.45 TB/s
-// (57% of the issue slots).  The
+// 8191 x 4096 39.7 us, 5.9 TB/s; backward 589824 x 192 with dsum 138.5 us, 6.54 TB/s
+// (half of the issue slots).  The
 // statistics are one sum a row, of s - p and of its square, p being the mean of
 // the row's first eight values: sum s^2 - C mu^2 (p = 0) would lose what a row's
 // mean has above its spread; of values around p the variance keeps all but
@@ -358,15 +358,37 @@ __global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) layernorm_backw
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const int c = li + k * step;
-            float sums[8];
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) unpack2(acc[z][k].v[e], sums[2 * e], sums[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) unpack2(acc[z][k].v[e], v[2 * e], v[2 * e + 1]);
+            // (two lanes share the piece's values between them, each a half, then
+            // quarters: seven shuffles for three steps, not 24; 4873 x 96 9.2 us and 6.7)
+            int first = 0, n = 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = sums[e];
-                for (int o = 16; o >= step; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane < step && c < a.chunks) part[warp * C + c * 8 + e] = v;
+            for (int s = 0; s < 5; ++s) {
+                const int o = 16 >> s;
+                if (o < step) break;
+                const bool upper = lane & o;
+                if (s < 3) {
+                    const int half = 4 >> s;
+#pragma unroll
+                    for (int e = 0; e < half; ++e) {
+                        const float give = upper ? v[e] : v[e + half];
+                        v[e] = (upper ? v[e + half] : v[e]) + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                    first += upper ? half : 0;
+                    n = half;
+                } else {
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                    if (upper) n = 0;
+                }
             }
+            if (c >= a.chunks) continue;
+            float *to = part + warp * C + c * 8 + first;
+            if (n >= 4) *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            if (n == 8) *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            if (n == 2) *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
+            if (n == 1) to[0] = v[0];
         }
         __syncthreads();
         float *out = block_columns(a, z);
