@@ -596,9 +596,10 @@ BwdPlan plan_backward(int rows, int C, bool with_dsum)
         if (p.smem < (size_t)8 * C * sizeof(float)) p.smem = (size_t)8 * C * sizeof(float);
     }
     const int64_t want = (rows + rpb - 1) / rpb, most = sm_count() * per_sm;
-    // few rows: one block, whose sums are the result (two turns at most: less than
-    // what the second launch would cost)
-    p.grid = want <= 2 ? 1 : (int)(want < most ? want : most);
+    // few rows: one block, whose sums are the result, for as many turns as cost less than
+    // a second launch (190 x 96, three turns, 6.7 us by two launches, 5.6; 250 x 96, four, 6.6
+    // both; wide rows' take longer: 15 x 2744, three, 6.7 and 9.4)
+    p.grid = want <= (r.block ? 2 : 4) ? 1 : (int)(want < most ? want : most);
     return p;
 }
 
