@@ -590,6 +590,45 @@ def test_streams_and_captured_graphs_share_nothing(rows, C, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,N", [(3, 72, 136), (60, 152, 1736), (128, 2048, 264), (300, 1032, 256), (4067, 136, 1000)])
+@pytest.mark.parametrize("kind", ["none", "gelu"])
+def test_backwards_back_to_back(rows, C, N, kind):
+    """Calls on one stream with nothing in between, in eager order and in a graph: a
+    call's kernels may run beside each other, but not into the next call's, which writes
+    the same workspace (dz, partial sums)."""
+    sets = []
+    for seed in (30, 31, 32):
+        x, w, b, _, dy = make(rows, C, N, seed=seed)
+        sets.append(dev(x, w, dy) + [None if kind == "none" else dev(stored_z(x, w, b))])
+    out = lambda: [nans(rows, C), nans(N, C), nans(N)]  # noqa: E731
+    with linear(C, N, kind) as h:
+        def call(s, o):
+            sw.swin_block_linear_backward(h, s[0], s[1], s[2], *o, z=s[3])
+
+        want = [out() for _ in sets]
+        for s, o in zip(sets, want):
+            call(s, o)
+            torch.cuda.synchronize()
+        got, graphed = ([out() for _ in range(24)] for _ in "eg")
+        torch.cuda.synchronize()
+        for i, o in enumerate(got):
+            call(sets[i % 3], o)
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr):
+            for i, o in enumerate(graphed):
+                call(sets[i % 3], o)
+        gr.replay()
+        sw.swin_block_linear_sync_status(h)
+        torch.cuda.synchronize()
+        for i in range(24):
+            for a, b, c in zip(got[i], graphed[i], want[i % 3]):
+                assert torch.equal(a, c) and torch.equal(b, c), i
+        del gr
+        torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
 def test_first_call_of_a_handle_captured():
     """A handle's first call may be the captured one (here with a workspace)."""
     rows, C, N = 1000, 8192, 1032

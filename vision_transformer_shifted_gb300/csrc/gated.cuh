@@ -31,6 +31,7 @@ struct UpPolicy {
         int m, col, width;   // row tile, first hidden column, columns
     };
     static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
+    static constexpr bool CHAIN = false;
     static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 2, STAGING = 2560, SEGS = 1;
     static constexpr uint32_t IDESC = idesc_pair(Q8 ? MMA_E4M3 : MMA_BF16, false, false, 256, 0);   // (N: 2 width)
 
@@ -197,6 +198,7 @@ struct GradPolicy {
     struct Unit {
         int m, col, width;   // row tile, first hidden column, columns
     };
+    static constexpr bool CHAIN = false;
     static constexpr int STAGES = 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 1, STAGING = 4096 + 64, SEGS = 2;
     static constexpr uint32_t IDESC_H = idesc_pair(MMA_BF16, false, true, 256, 0);    // (N: width)
     static constexpr uint32_t IDESC_GU = idesc_pair(MMA_BF16, false, false, 256, 0);  // (N: 2 width)

@@ -30,6 +30,7 @@ struct LinearPolicy {
         int slot;            // partial tile to write (-1: the whole K, to D)
     };
     static constexpr int ELEMS = Q8 ? 128 : 64;   // K elements of a block (128 bytes)
+    static constexpr bool CHAIN = false;
     static constexpr int STAGES = Q8 ? 4 : 5, STAGE_BYTES = 32768, EPI = 16, GROUPS = 2, SEGS = 1;
     static constexpr int BOX = 4096, VEC = Q8 ? 192 : 64;   // a warp's two boxes; its bias (bf16) and scales (fp32)
     static constexpr int STAGING = BOX + VEC;

@@ -24,6 +24,8 @@
 //                           binds, one group's latencies pass under the other's work
 //   STAGING                 bytes of shared memory per epilogue warp, laid out by
 //                           the epilogue (staged stores, vectors)
+//   CHAIN                   its Args have a `chain` (CHAIN_*): the kernel may be one that
+//                           runs beside the kernel before it
 //   SEGS                    accumulation segments of a unit (each a K loop
 //                           into one slot of TMEM columns)
 //   slot(seg, n), slot_col(slot), slot_use(seg, n)   the slot of the n-th unit
@@ -262,6 +264,10 @@ __host__ __device__ inline RingUse last_use(int stages, int issued, int k)
     return {i % stages, (uint32_t)(i / stages) & 1u};
 }
 
+// A kernel that reads nothing of the one before it, which let it start only after its
+// own wait (so that all before that one is complete), need not wait but at its end.
+enum { CHAIN_NONE = 0, CHAIN_EARLY = 1 };
+
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * P::EPI, 1)
 pair_kernel(const __grid_constant__ typename P::Args a)
@@ -300,8 +306,17 @@ pair_kernel(const __grid_constant__ typename P::Args a)
     bool failed = false;
     // launched while the kernel before it drains: no global memory is touched
     // until that kernel, and so every earlier one, has completed
-    griddep_launch_dependents();
-    griddep_wait();
+    bool late = false;
+    if constexpr (P::CHAIN) late = a.chain == CHAIN_EARLY;
+    if (late) {
+        griddep_launch_dependents();
+    } else if (P::CHAIN) {   // (after the wait: the next kernel may be an early one)
+        griddep_wait();
+        griddep_launch_dependents();
+    } else {
+        griddep_launch_dependents();
+        griddep_wait();
+    }
 
     // The two issuing warps run their loops as whole warps and let one lane
     // issue: addresses and descriptors then stay in uniform registers.  (With
@@ -420,6 +435,7 @@ pair_kernel(const __grid_constant__ typename P::Args a)
         if (lane == 0) bulk_wait_all();
     }
     if (failed && lane == 0) atomicOr(a.st.err, ERR_TIMEOUT);
+    if (late) griddep_wait();   // (whoever waits for this kernel waits for the one beside it too)
     __syncwarp();
     tc_fence_before();
     __syncthreads();

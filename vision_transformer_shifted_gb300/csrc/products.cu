@@ -139,7 +139,7 @@ namespace {
 template <int TN, bool A_MN, bool B_MN>
 cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
                               cudaStream_t stream, int *launches, FinishArgs *fin, int slot,
-                              const FinishArgs *side)
+                              const FinishArgs *side, int chain)
 {
     typename GemmPolicy<TN, A_MN, B_MN>::Args a;
     memset(&a, 0, sizeof(a));
@@ -186,6 +186,7 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
     }
     a.wn = pl.wn;
     a.np = pl.split.np;
+    a.chain = chain;
     a.st = st;
     if (pl.split.cut) {
         e = make_tensor_map(&a.part, T_F32, part, TN, (int64_t)a.np * 2 * 256, TN * 4, 16, 32, 64);
@@ -206,16 +207,16 @@ cudaError_t launch_products_t(const Product *ps, const ProductsPlan &pl, float *
 template <bool A_MN, bool B_MN>
 cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
                             cudaStream_t stream, int *launches, FinishArgs *fin, int slot,
-                              const FinishArgs *side)
+                            const FinishArgs *side, int chain)
 {
-    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot, side)
-                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot, side);
+    return pl.wide ? launch_products_t<256, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot, side, chain)
+                   : launch_products_t<128, A_MN, B_MN>(ps, pl, part, st, stream, launches, fin, slot, side, chain);
 }
 template cudaError_t launch_products<false, false>(const Product *, const ProductsPlan &, float *, DeviceStatus, cudaStream_t,
-                                                   int *, FinishArgs *, int, const FinishArgs *);
+                                                   int *, FinishArgs *, int, const FinishArgs *, int);
 template cudaError_t launch_products<false, true>(const Product *, const ProductsPlan &, float *, DeviceStatus, cudaStream_t,
-                                                  int *, FinishArgs *, int, const FinishArgs *);
+                                                  int *, FinishArgs *, int, const FinishArgs *, int);
 template cudaError_t launch_products<true, true>(const Product *, const ProductsPlan &, float *, DeviceStatus, cudaStream_t,
-                                                 int *, FinishArgs *, int, const FinishArgs *);
+                                                 int *, FinishArgs *, int, const FinishArgs *, int);
 
 } // namespace swin

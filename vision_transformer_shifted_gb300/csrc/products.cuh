@@ -425,6 +425,7 @@ struct GemmPolicy {
         int joined;
         int wn;             // columns of a tile: TN, or 192 of 256
         int np;
+        int chain;          // CHAIN_*
         DeviceStatus st;
     };
     struct Unit {
@@ -434,6 +435,7 @@ struct GemmPolicy {
         int k0, kb_first;   // the first segment's K, and its blocks
     };
     static constexpr int STAGE_BYTES = 16384 + TN * 64, EPI = 16, GROUPS = 1, STAGING = 4096, SEGS = 1;
+    static constexpr bool CHAIN = B_MN;   // (the backwards' products)
     static constexpr int STAGES = TN == 256 ? 5 : 6;
     static constexpr int BOXES = TN / 128;   // a warp's share of the columns: boxes of 32
     static constexpr uint32_t IDESC = idesc_pair(MMA_BF16, A_MN, B_MN, 256, 0);   // (N: width)
@@ -715,10 +717,13 @@ ProductsPlan plan_products(const Product *p, int n, int elems = 64);
 // is left to do for their cut tiles goes into fin->join[slot].  With A_MN their
 // epilogue warps begin fin's column sums.  Without, they can do what `side` leaves
 // to do of a kernel queued before, joins (of slot 1) and sums of few slices: under
-// their first tile's MMAs, so that no launch is needed for it.
+// their first tile's MMAs, so that no launch is needed for it.  chain: CHAIN_EARLY
+// behind a kernel whose results this one does not read and that lets the next kernel
+// start only after its own wait (B MN, or the few-row kernel).
 template <bool A_MN, bool B_MN>
 cudaError_t launch_products(const Product *ps, const ProductsPlan &pl, float *part, DeviceStatus st,
-                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot, const FinishArgs *side = nullptr);
+                            cudaStream_t stream, int *launches, FinishArgs *fin, int slot, const FinishArgs *side = nullptr,
+                            int chain = CHAIN_NONE);
 cudaError_t launch_finish(const FinishArgs &a, cudaStream_t stream, int *launches);
 
 // Workspace layout: bytes of each part, 1 KB aligned.
