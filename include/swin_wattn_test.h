@@ -125,6 +125,14 @@ enum {
 };
 int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan);
 
+/* Who finishes what in a backward call for the gradients `which`: plan receives {1 if
+ * dx goes to the few-row kernel, 1 if dx's epilogue finishes what dW's kernel leaves,
+ * 1 if dW's epilogue adds db to the end, 1 if dx's epilogue adds db's partial rows,
+ * how many of them there are, 1 if the workspace holds them, 1 if dW is taken through
+ * the activation, tiles of dW that are left to be joined, tiles of dx that are}. */
+enum { SWIN_BLOCK_LINEAR_GRAD_DX = 1, SWIN_BLOCK_LINEAR_GRAD_DW = 2, SWIN_BLOCK_LINEAR_GRAD_DB = 4 };
+int swin_block_linear_test_backward_plan(int C, int N, int rows, int act, int which, int *plan);
+
 /* swin_wattn_test_corrupt_workspace for a linear operator's handle. */
 int swin_block_linear_test_corrupt_workspace(swin_block_linear_t h, int side);
 

@@ -286,6 +286,57 @@ def test_plans_of_the_weight_gradient_through_an_activation():
         assert not plan(*args)[5], args
 
 
+GRADS = sw.BLOCK_LINEAR_GRAD_DX, sw.BLOCK_LINEAR_GRAD_DW, sw.BLOCK_LINEAR_GRAD_DB
+ALL = sum(GRADS)
+
+
+@pytest.mark.parametrize("kind", ["none", "gelu"])
+@pytest.mark.parametrize("which", [ALL, 3, 1, 2, 6])   # (db never without dW)
+def test_whoever_adds_the_rows_of_db_has_them(kind, which):
+    """One kernel, and one only, finishes db, and where it adds partial rows the
+    workspace holds them: dW's epilogue to the end (rows of dy, or held rows of dz's
+    sums), dx's epilogue, or a launch of its own."""
+    widths = [8, 64, 96, 264, 512, 1000, 1032, 2048, 4096, 7424, 8192, 11008, 12288, 16384, 20480, 32768, 65536]
+    lengths = [*range(1, 600, 13), 128, 129, 200, 256, 257, 1000, 2000, 5000, 20000, 70000]
+    for C in widths:
+        for N in widths:
+            for rows in lengths:
+                p = sw.swin_block_linear_test_backward_plan(C, N, rows, ACTS[kind], which)
+                at = (rows, C, N, p)
+                db = which & GRADS[2]
+                assert not (p["direct"] or p["dx_adds"]) or db, at
+                assert not (p["direct"] and p["dx_adds"]), at
+                assert not p["dx_adds"] or (p["side"] and p["held"] and p["slices"] <= 512), at
+                assert not p["direct"] or (p["slices"] if kind != "none" else rows) <= 256, at
+                assert not db or p["held"] or (p["direct"] and kind == "none"), at
+                assert not p["side"] or (which & 3 == 3 and not p["few"] and not p["dx_cut"]
+                                         and (p["through"] or p["dw_cut"] or p["dx_adds"])), at
+
+
+def test_every_way_of_finishing_a_backward_is_tested():
+    widths = [8, 64, 264, 512, 1000, 1032, 2048, 4096, 7424, 8192, 12288, 16384, 32768, 65536]
+    lengths = [1, 40, 128, 129, 200, 256, 257, 300, 500, 1000, 1300, 2000, 5000, 20000, 70000]
+
+    def way(rows, C, N, kind):
+        p = sw.swin_block_linear_test_backward_plan(C, N, rows, ACTS[kind], ALL)
+        return kind, *(k for k, v in p.items() if v and k not in ("slices", "held"))
+
+    tested = {way(*s) for s in FINISHING}
+    tested |= {way(*s, kind) for s in SHAPES + LARGE for kind in ("none", "gelu")}
+    for C in widths:
+        for N in widths:
+            for rows in lengths:
+                for kind in ("none", "gelu"):
+                    assert way(rows, C, N, kind) in tested, (rows, C, N, way(rows, C, N, kind))
+
+
+def test_backward_plan_refuses():
+    for a in ((0, 8, 300, 0, 7), (8, 12, 300, 0, 7), (8, 8, 0, 0, 7), (8, 8, 300, 0, 0), (8, 8, 300, 0, 4), (8, 8, 300, 0, 5),
+              (8, 8, 300, 0, 8)):
+        with pytest.raises(sw.SwinWAttnError):
+            sw.swin_block_linear_test_backward_plan(*a)
+
+
 def test_plan_refuses():
     for a in ((0, 8, 300, 0), (8, 12, 300, 0), (8, 8, 0, 0), (8, 8, 300, 5)):
         with pytest.raises(sw.SwinWAttnError):
@@ -396,6 +447,35 @@ def test_rounds_of_tiles_and_products_cut_along_k(rows, C, N):
     ref, tol = backward_ref(xd, wd, kept, yd, "gelu")
     for k in ref:
         close(g[k], ref[k].cpu(), tol[k].cpu(), 2 * HALF)
+
+
+FINISHING = [   # rows, C, N, kind: who finishes dx, dW and db, as SHAPES and LARGE do not have it
+    (200, 8192, 2048, "none"), (256, 12288, 4096, "none"), (129, 65536, 512, "none"), (160, 7424, 8, "none"),
+    (257, 8, 32768, "none"), (129, 8, 32768, "none"), (257, 8, 4096, "none"), (3000, 8, 2048, "none"),
+    (5000, 1000, 7424, "none"), (20000, 64, 8, "none"), (1300, 64, 1032, "gelu"), (1300, 64, 2048, "gelu"),
+    (70000, 64, 64, "gelu"), (2000, 64, 2048, "gelu"), (5000, 1000, 7424, "gelu"), (1300, 64, 4096, "gelu"),
+    (20000, 64, 8, "gelu"), (129, 8, 32768, "gelu"), (131, 7424, 8, "gelu"), (200, 8192, 2048, "gelu")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,C,N,kind", FINISHING + [(*s, "none") for s in LARGE])
+def test_who_finishes_what_of_a_backward(rows, C, N, kind):
+    x, w, b, _, dy = make(rows, C, N, seed=33)
+    xd, wd, yd, bd = dev(x, w, dy, b)
+    z = None if kind == "none" else stored_z(xd, wd, bd)
+    ref, tol = backward_ref(xd, wd, z, yd, kind)
+    got = [dict(dx=nans(rows, C), dW=nans(N, C), db=nans(N)) for _ in range(3)]
+    with linear(C, N, kind) as h:
+        for g in got[:2]:
+            sw.swin_block_linear_backward(h, xd, wd, yd, g["dx"], g["dW"], g["db"], z=z)
+        sw.swin_block_linear_backward(h, xd, wd, yd, got[2]["dx"], got[2]["dW"], z=z)   # without db
+        sw.swin_block_linear_sync_status(h)
+    for k in ref:
+        assert torch.equal(got[0][k], got[1][k]), k
+        for g in got[::2]:
+            if g is got[0] or k != "db":
+                close(g[k], ref[k].cpu(), tol[k].cpu(), 2 * HALF)
+    assert got[2]["db"].isnan().all()
 
 
 @pytest.mark.gpu

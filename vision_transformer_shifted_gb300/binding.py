@@ -25,6 +25,7 @@ BLOCK_GATED_SILU, BLOCK_GATED_GELU = 0, 1
 BLOCK_LINEAR_NONE, BLOCK_LINEAR_SILU, BLOCK_LINEAR_GELU = 0, 1, 2
 BLOCK_LINEAR_PLAN_FORWARD, BLOCK_LINEAR_PLAN_FORWARD_Q8, BLOCK_LINEAR_PLAN_DX, BLOCK_LINEAR_PLAN_WEIGHT = 0, 1, 2, 3
 BLOCK_LINEAR_PLAN_ACT_WEIGHT = 4
+BLOCK_LINEAR_GRAD_DX, BLOCK_LINEAR_GRAD_DW, BLOCK_LINEAR_GRAD_DB = 1, 2, 4
 BLOCK_GATED_PLAN_DOWN, BLOCK_GATED_PLAN_DX, BLOCK_GATED_PLAN_WEIGHTS, BLOCK_GATED_PLAN_NARROW = 0, 1, 2, 3
 PATH_AUTO, PATH_THREE_KERNELS, PATH_FUSED, PATH_FP32 = 0, 1, 2, 3
 
@@ -103,6 +104,7 @@ _SIGNATURES = {
     "swin_block_linear_sync_status": ["p", "p"],
     "swin_block_linear_destroy": ["p"],
     "swin_block_linear_test_plan": ["i", "i", "i", "i", "p"],
+    "swin_block_linear_test_backward_plan": ["i", "i", "i", "i", "i", "p"],
     "swin_block_linear_test_corrupt_workspace": ["p", "i"],
     "swin_block_gated_test_last_use": ["i", "i", "i", "p", "p"],
 }
@@ -694,6 +696,14 @@ def swin_block_linear_test_plan(C, N, rows, which):
     _check("swin_block_linear_test_plan",
            load().swin_block_linear_test_plan(C, N, rows, which, ctypes.addressof(plan)))
     return tuple(plan)
+
+
+def swin_block_linear_test_backward_plan(C, N, rows, act, which):
+    """Who finishes what in a backward for the gradients which (BLOCK_LINEAR_GRAD_*)."""
+    plan = (ctypes.c_int * 9)()
+    _check("swin_block_linear_test_backward_plan",
+           load().swin_block_linear_test_backward_plan(C, N, rows, act, which, ctypes.addressof(plan)))
+    return dict(zip(("few", "side", "direct", "dx_adds", "slices", "held", "through", "dw_cut", "dx_cut"), plan))
 
 
 def swin_block_linear_test_corrupt_workspace(h, side):

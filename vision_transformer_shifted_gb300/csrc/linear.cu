@@ -289,6 +289,52 @@ Product weight_product(int C, int N, int rows, int ld)
     return p;
 }
 
+// What a backward call queues, and which kernel finishes what.
+struct BackwardPlan {
+    int ld;                 // of dz
+    ProductsPlan dx, dw;
+    ActWgradPlan through;   // dW through an activation
+    GradPlan grad;
+    bool few;               // dx by the few-row kernel
+    bool side;              // dx's epilogue warps finish what dW's kernel leaves
+    bool direct;            // db is added to the end by dW's epilogue warps
+    bool dx_adds;           // db's partial rows are added by dx's epilogue warps
+    int slices;             // partial rows of db
+    size_t dz_bytes, dw_bytes, sum_bytes;   // of the workspace, beside dx.part_bytes
+};
+BackwardPlan plan_backward(int C, int N, int rows, bool act, bool dx, bool dW, bool db)
+{
+    BackwardPlan p{};
+    p.ld = act ? hidden_ld(N) : N;
+    const Product px = dx_product(C, N, rows, p.ld), pw = weight_product(C, N, rows, p.ld);
+    if (dx) p.dx = plan_products(&px, 1);
+    if (dW) p.dw = plan_products(&pw, 1);
+    // few rows: dx by the few-row kernel
+    p.few = dx && (rows <= FEW_ROWS || few_chosen(px, p.dx, 64));
+    if (p.few) p.dx.part_bytes = 0;
+    if (act && dW) p.through = plan_act_wgrad(C, N, rows, p.dw);
+    p.grad = plan_grad(N, rows);
+    p.slices = p.through.chosen ? p.through.slices : act ? p.grad.slices : rows <= FEW_SUMS ? 1 : column_slices(rows);
+    // Few rows of dy are added to the end by the weight gradient's waiting warps, and
+    // leave nothing of db to any other kernel.
+    const bool dy_direct = db && !act && rows <= FEW_SUMS, sums_left = db && !dy_direct;
+    // What dW's kernel leaves, cut tiles and db's partial rows, is finished by dx's
+    // epilogue warps under their first tile's MMAs: where they are on most SMs, db's
+    // rows are few, and no launch is left to save otherwise (dx's own cut tiles).
+    // 12544 x 512 x 2048 GELU 60.2 us, 69.7 by a launch of its own, 50000 x 256 x 1024
+    // 80 and 91, 2000 x 2048 x 2048 36.4 and 42.3; 300 x 512 x 1024, on 16 SMs, 48.6
+    // and 24.
+    p.side = dx && !p.few && dW && (p.through.chosen || p.dw.split.cut || sums_left) &&
+             (!sums_left || p.slices <= SIDE_SLICES) && !p.dx.split.cut && 8 * p.dx.split.np >= 3 * sm_count();
+    p.dx_adds = p.side && sums_left;
+    // So are few rows of dz's kernel's partial sums.
+    p.direct = dy_direct || (db && act && !p.through.chosen && !p.side && !p.dw.split.cut && p.slices <= FEW_SUMS);
+    p.dz_bytes = act && (dx || !p.through.chosen) ? (size_t)rows * p.ld * 2 : 0;
+    p.dw_bytes = p.through.chosen ? p.through.part_bytes : p.dw.part_bytes;
+    p.sum_bytes = db && (act || !p.direct) ? (size_t)p.slices * N * sizeof(float) : 0;
+    return p;
+}
+
 } // namespace
 
 extern "C" {
@@ -406,53 +452,32 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
                 return SWIN_WATTN_ECUDA;
         return SWIN_WATTN_OK;
     }
-    const int ld = act ? hidden_ld(h->N) : h->N;
+    const BackwardPlan pl = plan_backward(h->C, h->N, rows, act, dx != nullptr, dW != nullptr, db != nullptr);
+    const int ld = pl.ld;
     Product px = dx_product(h->C, h->N, rows, ld), pw = weight_product(h->C, h->N, rows, ld);
-    ProductsPlan plx = dx ? plan_products(&px, 1) : ProductsPlan{};
-    const ProductsPlan plw = dW ? plan_products(&pw, 1) : ProductsPlan{};
-    // few rows: dx by the few-row kernel
-    const bool few = dx && (rows <= FEW_ROWS || few_chosen(px, plx, 64));
-    if (few) plx.part_bytes = 0;
-    const ActWgradPlan pa = act && dW ? plan_act_wgrad(h->C, h->N, rows, plw) : ActWgradPlan{};
-    const GradPlan pg = plan_grad(h->N, rows);
-    // What dW's kernel leaves, cut tiles and db's partial rows, is finished by dx's
-    // epilogue warps under their first tile's MMAs: where they are on most SMs, db's
-    // rows are few, and no launch is left to save otherwise (dx's own cut tiles).
-    // 12544 x 512 x 2048 GELU 60.2 us, 69.7 by a launch of its own, 50000 x 256 x 1024
-    // 80 and 91, 2000 x 2048 x 2048 36.4 and 42.3; 300 x 512 x 1024, on 16 SMs, 48.6
-    // and 24.
-    const int slices = pa.chosen ? pa.slices : act ? pg.slices : rows <= FEW_SUMS ? 1 : column_slices(rows);
-    const bool side = dx && !few && dW && (pa.chosen || plw.split.cut || db) && (!db || slices <= SIDE_SLICES) &&
-                      !plx.split.cut && 8 * plx.split.np >= 3 * sm_count();
-    // Few rows to add (of dy, or of dz's kernel's partial sums) are added to the end by
-    // the weight gradient's waiting warps.
-    const bool direct = db && (!act ? rows <= FEW_SUMS : !pa.chosen && !side && !plw.split.cut && slices <= FEW_SUMS);
     FinishArgs fin{};
-    const size_t sum_bytes = db && (act || !direct) ? (size_t)slices * h->N * sizeof(float) : 0;
     Carve size(nullptr);
-    const size_t dz_bytes = act && (dx || !pa.chosen) ? (size_t)rows * ld * 2 : 0,
-                 w_bytes = pa.chosen ? pa.part_bytes : plw.part_bytes;
-    size.take(dz_bytes);
-    size.take(plx.part_bytes);
-    size.take(w_bytes);
-    size.take(sum_bytes);
+    size.take(pl.dz_bytes);
+    size.take(pl.dx.part_bytes);
+    size.take(pl.dw_bytes);
+    size.take(pl.sum_bytes);
     void *ws = nullptr;
     bool captured = false;
     if (size.used && (rc = ows_begin(&h->ws, size.used, s, &ws, &captured)) != SWIN_WATTN_OK) return rc;
     Carve carve(ws);
-    bf16 *dz = (bf16 *)carve.take(dz_bytes);
-    float *x_part = (float *)carve.take(plx.part_bytes), *w_part = (float *)carve.take(w_bytes);
-    float *sum_part = (float *)carve.take(sum_bytes);
+    bf16 *dz = (bf16 *)carve.take(pl.dz_bytes);
+    float *x_part = (float *)carve.take(pl.dx.part_bytes), *w_part = (float *)carve.take(pl.dw_bytes);
+    float *sum_part = (float *)carve.take(pl.sum_bytes);
     if (db) {
         auto &m = fin.cs.m[fin.cs.n++];
         m.out = (bf16 *)db;
         m.cols = h->N;
-        m.part = direct ? nullptr : sum_part;
+        m.part = pl.direct ? nullptr : sum_part;
         m.b = act ? nullptr : (const bf16 *)dy;
         m.f = act ? sum_part : nullptr;
-        m.rows = act ? slices : rows;
-        m.slices = direct ? 1 : slices;
-        m.tasks = direct ? ceil_div(h->N, act ? 16 : 32) : act ? 0 : ceil_div(h->N, 256) * m.slices;
+        m.rows = act ? pl.slices : rows;
+        m.slices = pl.direct ? 1 : pl.slices;
+        m.tasks = pl.direct ? ceil_div(h->N, act ? 16 : 32) : act ? 0 : ceil_div(h->N, 256) * m.slices;
     }
     px.a[0] = pw.a[0] = act ? (const void *)dz : dy;
     px.b[0] = W;
@@ -462,38 +487,39 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
     const DeviceStatus st{h->d_err, WAIT_NS};
     h->last_launches = 0;
     cudaError_t e = cudaSuccess;
-    if (pa.chosen) {
+    if (pl.through.chosen) {
         const ActWgrad w{(const bf16 *)z, (const bf16 *)dy, (const bf16 *)x, dx ? dz : nullptr, (bf16 *)dW, db ? sum_part : nullptr,
                          w_part, rows, h->C, h->N, ld, h->act};
         ++h->last_launches;
-        e = launch_act_wgrad(w, pa, st, s, &fin.join[1], &fin.joins[1]);
+        e = launch_act_wgrad(w, pl.through, st, s, &fin.join[1], &fin.joins[1]);
     } else if (act) {
-        const GradArgs a{(const bf16 *)z, (const bf16 *)dy, dz, db ? sum_part : nullptr, rows, h->N, ld, pg.across, pg.at_once,
-                         pg.slices};
+        const GradArgs a{(const bf16 *)z, (const bf16 *)dy, dz, db ? sum_part : nullptr, rows, h->N, ld, pl.grad.across,
+                         pl.grad.at_once, pl.grad.slices};
         ++h->last_launches;
         e = launch_maybe_overlapped(h->act == ACT_SILU ? act_grad_kernel<ACT_SILU> : act_grad_kernel<ACT_GELU>,
-                                    dim3((unsigned)pg.columns, (unsigned)pg.slices), dim3(256), 0, s, 1, a);
+                                    dim3((unsigned)pl.grad.columns, (unsigned)pl.grad.slices), dim3(256), 0, s, 1, a);
     }
     // (behind dx, whose results it does not read, it runs beside it: 60 x 152 x 1736 11.1
     // us one after the other, 8.2; 300 x 1032 x 256 GELU 13.8 and 11.2)
     auto weight = [&]() {
-        if (e == cudaSuccess && dW && !pa.chosen)
-            e = launch_products<true, true>(&pw, plw, w_part, st, s, &h->last_launches, &fin, 1, nullptr,
-                                            dx && !side ? CHAIN_EARLY : CHAIN_NONE);
+        if (e == cudaSuccess && dW && !pl.through.chosen)
+            e = launch_products<true, true>(&pw, pl.dw, w_part, st, s, &h->last_launches, &fin, 1, nullptr,
+                                            dx && !pl.side ? CHAIN_EARLY : CHAIN_NONE);
     };
-    if (side) weight();
+    if (pl.side) weight();
     if (e == cudaSuccess && dx) {
-        const FinishArgs left = fin;
-        if (side) fin.joins[1] = fin.cs.n = 0;
-        if (few) {
+        FinishArgs left = fin;
+        if (!pl.dx_adds) left.cs.n = 0;
+        if (pl.side) fin.joins[1] = fin.cs.n = 0;
+        if (pl.few) {
             ++h->last_launches;
             e = launch_few_dx((const bf16 *)px.a[0], ld, rows, (const bf16 *)W, (bf16 *)dx, h->C, h->N, st, s);
         } else {
-            e = launch_products<false, true>(&px, plx, x_part, st, s, &h->last_launches, &fin, 0, side ? &left : nullptr);
+            e = launch_products<false, true>(&px, pl.dx, x_part, st, s, &h->last_launches, &fin, 0, pl.side ? &left : nullptr);
         }
     }
-    if (!side) weight();
-    if (direct) fin.cs.n = 0;   // (done)
+    if (!pl.side) weight();
+    if (pl.direct) fin.cs.n = 0;   // (done)
     if (e == cudaSuccess) e = launch_finish(fin, s, &h->last_launches);
     const int rc2 = ows_end(&h->ws, s, ws, captured);
     return e != cudaSuccess ? SWIN_WATTN_ECUDA : rc2;
@@ -521,6 +547,19 @@ int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan)
     const ProductsPlan pl = plan_products(&p, 1, block);
     const bool few = which != SWIN_BLOCK_LINEAR_PLAN_WEIGHT && (rows <= FEW_ROWS || few_chosen(p, pl, block));
     const int v[] = {pl.split.tiles, few ? 0 : pl.split.np, pl.wn, pl.split.halves, pl.split.cut, pl.split.kb != pl.split.k_blocks};
+    memcpy(plan, v, sizeof(v));
+    return SWIN_WATTN_OK;
+}
+
+int swin_block_linear_test_backward_plan(int C, int N, int rows, int act, int which, int *plan)
+{
+    if (C <= 0 || C % 8 || C > MAX_WIDTH || N <= 0 || N % 8 || N > MAX_WIDTH || rows <= 0 || rows > MAX_ROWS || !plan)
+        return SWIN_WATTN_EINVAL;
+    const bool dx = which & SWIN_BLOCK_LINEAR_GRAD_DX, dW = which & SWIN_BLOCK_LINEAR_GRAD_DW, db = which & SWIN_BLOCK_LINEAR_GRAD_DB;
+    if (which < 0 || which > 7 || (!dx && !dW) || (db && !dW)) return SWIN_WATTN_EINVAL;
+    const BackwardPlan p = plan_backward(C, N, rows, act != SWIN_BLOCK_LINEAR_NONE, dx, dW, db);
+    const int v[] = {p.few, p.side, p.direct, p.dx_adds, p.slices, p.sum_bytes != 0, p.through.chosen,
+                     p.through.chosen ? p.through.tiles : p.dw.split.cut, p.few ? 0 : p.dx.split.cut};
     memcpy(plan, v, sizeof(v));
     return SWIN_WATTN_OK;
 }
