@@ -1,6 +1,10 @@
 """The binding's native argument checks (csrc/arguments.cpp): they pass what the
 Python functions behind them pass, with the same address, and leave the rest to
 them."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -50,6 +54,42 @@ def test_other_objects_and_counts_of_arguments():
 
 class Sub(torch.Tensor):
     pass
+
+
+THREADS = """
+import sys, threading
+import torch
+from vision_transformer_shifted_gb300 import binding as sw
+sys.setswitchinterval(1e-6)
+class Sub(torch.Tensor):
+    pass
+x = torch.zeros(4, 8, dtype=torch.bfloat16)
+gate, seen = threading.Barrier(16), []
+def work():
+    gate.wait()
+    sw.load()
+    try:   # (CPU tensors: their device is -1)
+        assert sw._arg("x", x.as_subclass(Sub), torch.bfloat16, (4, 8), -1) == x.data_ptr()
+        sw._arg("x", x, torch.bfloat16, (4, 8), 0)
+    except Exception as e:
+        seen.append(type(e).__name__)
+threads = [threading.Thread(target=work) for _ in range(16)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+print(sorted(set(seen)), len(seen))
+"""
+
+
+def test_first_load_from_many_threads():
+    """What the native checks leave to the Python functions reaches them, whoever
+    loaded the library and however often."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        done = subprocess.run([sys.executable, "-c", THREADS], cwd=root, capture_output=True, text=True, timeout=300)
+        assert done.returncode == 0 and done.stdout.strip() == "['ValueError'] 16", done.stdout + done.stderr[-2000:]
+
 
 
 @pytest.mark.gpu

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -120,11 +121,20 @@ _CT = {"p": ctypes.c_void_p, "pp": ctypes.POINTER(ctypes.c_void_p), "i": ctypes.
        "f": ctypes.c_float}
 
 
+_load_lock = threading.Lock()
+
+
 def load(build_if_missing: bool = True):
     """Loads libswin_wattn.so (building it first if it is missing)."""
     global _lib
-    if _lib is not None:
-        return _lib
+    if _lib is None:
+        with _load_lock:   # (the first calls of several threads)
+            if _lib is None:
+                _lib = _load(build_if_missing)
+    return _lib
+
+
+def _load(build_if_missing):
     path = _build.LIB
     if not os.path.exists(path) or not os.path.exists(_build.ARGUMENTS):
         if not build_if_missing:
@@ -140,7 +150,6 @@ def load(build_if_missing: bool = True):
     lib.swin_wattn_last_cuda_error.argtypes = [ctypes.c_void_p]
     lib.swin_wattn_last_cuda_error.restype = ctypes.c_char_p
     _check_natively()
-    _lib = lib
     return lib
 
 
@@ -376,7 +385,7 @@ def _refuse(name, t, dtype, shape):
     raise ValueError("%s must be on the current CUDA device" % name)
 
 
-def _arg(name, t, dtype, shape, dev):
+def _arg_python(name, t, dtype, shape, dev):
     """Pointer of a required argument, checked: dtype, shape, contiguous, on
     device dev."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
@@ -384,7 +393,7 @@ def _arg(name, t, dtype, shape, dev):
     return t.data_ptr()
 
 
-def _rows(h, x, dtype, name):
+def _rows_python(h, x, dtype, name):
     """rows, shape, device and pointer of the call's tokens x [..., C] (h: the
     handle, for C channels), checked: dtype, contiguous, on the current device."""
     shape = x.shape
@@ -400,12 +409,16 @@ def _rows(h, x, dtype, name):
     return rows, shape, dev, x.data_ptr()
 
 
+_arg, _rows = _arg_python, _rows_python
+
+
 def _check_natively():
     """Puts arguments.cpp's forms of _arg and _rows in their places: the same checks
-    of a plain tensor in a tenth of the time; anything else comes back to these."""
+    of a plain tensor in a tenth of the time; anything else goes to the functions
+    above.  (Under load()'s lock.)"""
     global _arg, _rows
     from . import _arguments
-    _arguments.setup(torch.Tensor, torch.nn.Parameter, _BF, _F32, _E4M3, _arg, _rows, _current_device)
+    _arguments.setup(torch.Tensor, torch.nn.Parameter, _BF, _F32, _E4M3, _arg_python, _rows_python, _current_device)
     _arg, _rows = _arguments.arg, _arguments.rows
 
 
