@@ -92,6 +92,60 @@ def test_first_load_from_many_threads():
 
 
 
+WITHOUT = """
+import sys, types
+import torch
+import vision_transformer_shifted_gb300 as pkg
+from vision_transformer_shifted_gb300 import binding as sw
+def setup(*a):
+    raise SystemExit("not to be asked")
+for other in (None, types.SimpleNamespace(setup=setup), types.SimpleNamespace(setup=setup, torch_version="0.1")):
+    sys.modules[pkg.__name__ + "._arguments"] = other
+    if other is not None:
+        pkg._arguments = other
+    sw._lib = None
+    assert sw.load().swin_block_rms_destroy(None) == sw.OK
+    assert sw._arg is sw._arg_python and sw._rows is sw._rows_python
+    try:
+        sw._arg("x", torch.zeros(4, 8), torch.bfloat16, (4, 8), -1)
+    except ValueError:
+        print("refused")
+"""
+
+
+def test_library_works_without_the_native_checks():
+    """Not there (not built, another Python), of a build that does not say its PyTorch,
+    of another PyTorch: the Python functions stay in their places."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", WITHOUT], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.split() == ["refused"] * 3, done.stdout + done.stderr[-2000:]
+
+
+def test_native_checks_are_of_this_python_and_torch(monkeypatch):
+    import sysconfig
+
+    from vision_transformer_shifted_gb300 import build
+    assert _arguments.torch_version == str(torch.__version__) == build.torch_version()
+    assert _arguments.__file__ == build.ARGUMENTS and build.ARGUMENTS.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(build, "_newer", lambda *a: True)
+    assert build.arguments_current()
+    monkeypatch.setattr(build, "torch_version", lambda: "0.1")
+    assert not build.arguments_current()   # (built anew)
+
+
+def test_build_without_a_compiler_for_the_checks_keeps_the_library(monkeypatch, capsys):
+    from vision_transformer_shifted_gb300 import build
+
+    def no_compiler(*a, **kw):
+        raise FileNotFoundError("g++")
+
+    monkeypatch.setattr(build, "arguments_current", lambda: False)
+    monkeypatch.setattr(build, "_library_current", lambda: True)
+    monkeypatch.setattr(build.subprocess, "run", no_compiler)
+    assert build.build() == build.LIB
+    assert "arguments.cpp" in capsys.readouterr().err
+
+
 @pytest.mark.gpu
 def test_addresses_on_the_gpu():
     sw.load()

@@ -136,7 +136,7 @@ def load(build_if_missing: bool = True):
 
 def _load(build_if_missing):
     path = _build.LIB
-    if not os.path.exists(path) or not os.path.exists(_build.ARGUMENTS):
+    if not os.path.exists(path):
         if not build_if_missing:
             raise OSError("libswin_wattn.so is not built")
         _build.build()
@@ -415,9 +415,15 @@ _arg, _rows = _arg_python, _rows_python
 def _check_natively():
     """Puts arguments.cpp's forms of _arg and _rows in their places: the same checks
     of a plain tensor in a tenth of the time; anything else goes to the functions
-    above.  (Under load()'s lock.)"""
+    above, which stay where the module is not built or is another PyTorch's.  (Under
+    load()'s lock.)"""
     global _arg, _rows
-    from . import _arguments
+    try:
+        from . import _arguments
+    except ImportError:
+        return
+    if getattr(_arguments, "torch_version", None) != str(torch.__version__):
+        return
     _arguments.setup(torch.Tensor, torch.nn.Parameter, _BF, _F32, _E4M3, _arg_python, _rows_python, _current_device)
     _arg, _rows = _arguments.arg, _arguments.rows
 

@@ -104,4 +104,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_arguments", nullptr, -1, methods,
 
 } // namespace
 
-PyMODINIT_FUNC PyInit__arguments() { return PyModule_Create(&module); }
+// (The binding uses it under the PyTorch that it was built against only: it reads the
+// tensor objects' layout from that one's headers.)
+PyMODINIT_FUNC PyInit__arguments()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_BUILT) < 0) Py_CLEAR(m);
+    return m;
+}
