@@ -133,6 +133,10 @@ int swin_block_linear_test_plan(int C, int N, int rows, int which, int *plan);
 enum { SWIN_BLOCK_LINEAR_GRAD_DX = 1, SWIN_BLOCK_LINEAR_GRAD_DW = 2, SWIN_BLOCK_LINEAR_GRAD_DB = 4 };
 int swin_block_linear_test_backward_plan(int C, int N, int rows, int act, int which, int *plan);
 
+/* How many clusters of `split` CTAs (alone: one CTA an SM, else two) a device is
+ * remembered to hold at once, where `answer` (0: none) is what it would say if asked. */
+int swin_block_linear_test_clusters_of(int device, int split, int alone, int answer);
+
 /* swin_wattn_test_corrupt_workspace for a linear operator's handle. */
 int swin_block_linear_test_corrupt_workspace(swin_block_linear_t h, int side);
 

@@ -337,6 +337,17 @@ def test_backward_plan_refuses():
             sw.swin_block_linear_test_backward_plan(*a)
 
 
+def test_clusters_that_find_room_are_a_devices_own():
+    """What one device says is not taken for another (these two are no machine's)."""
+    of = sw.swin_block_linear_test_clusters_of
+    assert of(62, 8, False, 0) == 0   # (no answer is not kept)
+    assert of(62, 8, False, 36) == 36 and of(63, 8, False, 20) == 20
+    assert of(62, 8, False, 5) == 36 and of(63, 8, False, 5) == 20
+    assert of(62, 8, True, 18) == 18 and of(62, 16, False, 7) == 7
+    assert of(64, 8, False, 11) == 11 and of(64, 8, False, 12) == 12   # (past the table: asked each time)
+    assert of(0, 17, False, 1) == of(0, 0, False, 1) == sw.EINVAL
+
+
 def test_plan_refuses():
     for a in ((0, 8, 300, 0), (8, 12, 300, 0), (8, 8, 0, 0), (8, 8, 300, 5)):
         with pytest.raises(sw.SwinWAttnError):

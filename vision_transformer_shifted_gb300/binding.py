@@ -106,6 +106,7 @@ _SIGNATURES = {
     "swin_block_linear_destroy": ["p"],
     "swin_block_linear_test_plan": ["i", "i", "i", "i", "p"],
     "swin_block_linear_test_backward_plan": ["i", "i", "i", "i", "i", "p"],
+    "swin_block_linear_test_clusters_of": ["i", "i", "i", "i"],
     "swin_block_linear_test_corrupt_workspace": ["p", "i"],
     "swin_block_gated_test_last_use": ["i", "i", "i", "p", "p"],
 }
@@ -723,6 +724,10 @@ def swin_block_linear_test_backward_plan(C, N, rows, act, which):
     _check("swin_block_linear_test_backward_plan",
            load().swin_block_linear_test_backward_plan(C, N, rows, act, which, ctypes.addressof(plan)))
     return dict(zip(("few", "side", "direct", "dx_adds", "slices", "held", "through", "dw_cut", "dx_cut"), plan))
+
+
+def swin_block_linear_test_clusters_of(device, split, alone, answer):
+    return load().swin_block_linear_test_clusters_of(device, split, int(alone), answer)
 
 
 def swin_block_linear_test_corrupt_workspace(h, side):

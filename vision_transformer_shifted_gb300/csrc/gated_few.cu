@@ -331,11 +331,9 @@ __global__ void __launch_bounds__(FEW_THREADS) few_rows_kernel(const __grid_cons
 // and shared memory: of one that allocates tensor memory the answer is one CTA an SM,
 // whatever it allocates.
 __global__ void __launch_bounds__(FEW_THREADS) few_room() {}
-int few_clusters(int split, bool alone)
+int ask_clusters(int split, bool alone)   // (0: no device, a plan is asked for)
 {
-    static std::atomic<int> known[2][17];
-    int n = known[alone][split].load();
-    if (n) return n;
+    int n = 0;
     const void *kern = (const void *)few_room;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr;
@@ -347,14 +345,31 @@ int few_clusters(int split, bool alone)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 + FEW_RING_ALONE) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return (alone ? 1 : 2) * sm_count() / split;   // (no device: a plan is asked for)
-    }
-    known[alone][split].store(n);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 + FEW_RING_ALONE) == cudaSuccess &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0)
+        return n;
+    cudaGetLastError();
+    return 0;
+}
+// ask()'s answer for a device, kept (0: asked again).
+template <class Ask>
+int clusters_of(int dev, int split, bool alone, Ask &&ask)
+{
+    static std::atomic<int> known[64][2][17];
+    const bool keep = dev >= 0 && dev < 64;
+    int n = keep ? known[dev][alone][split].load() : 0;
+    if (n) return n;
+    n = ask();
+    if (keep && n) known[dev][alone][split].store(n);
     return n;
+}
+int few_clusters(int split, bool alone)
+{
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    const int n = clusters_of(dev, split, alone, [&] { return ask_clusters(split, alone); });
+    return n ? n : (alone ? 1 : 2) * sm_count() / split;
 }
 
 template <int FORM, bool Q8>
@@ -421,6 +436,11 @@ int few_split(int64_t tiles, int kb)
     for (int s = 2; s <= most && kb >= 4 * s; ++s)
         if (tiles <= few_clusters(s, false)) split = s;
     return split;
+}
+
+int test_few_clusters_of(int dev, int split, bool alone, int answer)
+{
+    return clusters_of(dev, split, alone, [&] { return answer; });
 }
 
 cudaError_t launch_few_up(const FewUp &u, DeviceStatus st, cudaStream_t stream)

@@ -564,6 +564,12 @@ int swin_block_linear_test_backward_plan(int C, int N, int rows, int act, int wh
     return SWIN_WATTN_OK;
 }
 
+int swin_block_linear_test_clusters_of(int device, int split, int alone, int answer)
+{
+    if (split < 1 || split > 16 || answer < 0) return SWIN_WATTN_EINVAL;
+    return test_few_clusters_of(device, split, alone != 0, answer);
+}
+
 int swin_block_linear_test_corrupt_workspace(swin_block_linear_t h, int side)
 {
     if (!h || side < 0 || side > 1) return SWIN_WATTN_EINVAL;

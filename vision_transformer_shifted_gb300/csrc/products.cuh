@@ -744,6 +744,8 @@ struct Carve {
 constexpr int FEW_ROWS = 128;   // most rows of the few-row kernels
 // CTAs that share the K (kb blocks) of each of the linear operator's tiles.
 int few_split(int64_t tiles, int kb);
+// A device's count of clusters as it is kept, if `answer` is what the device says (tests).
+int test_few_clusters_of(int dev, int split, bool alone, int answer);
 // The linear operator for few rows, one launch.
 struct FewLinear {
     const void *x, *w;
