@@ -499,7 +499,8 @@ int swin_block_linear_backward(swin_block_linear_t h, const void *x, int rows, c
         e = launch_maybe_overlapped(h->act == ACT_SILU ? act_grad_kernel<ACT_SILU> : act_grad_kernel<ACT_GELU>,
                                     dim3((unsigned)pl.grad.columns, (unsigned)pl.grad.slices), dim3(256), 0, s, 1, a);
     }
-    // (behind dx, whose results it does not read, it runs beside it: 60 x 152 x 1736 11.1
+    // (behind dx, whose results it does not read, it runs beside it, reading through L2
+    // what was complete before dx's kernel let it start: see CHAIN_EARLY; 60 x 152 x 1736 11.1
     // us one after the other, 8.2; 300 x 1032 x 256 GELU 13.8 and 11.2)
     auto weight = [&]() {
         if (e == cudaSuccess && dW && !pl.through.chosen)

@@ -264,8 +264,13 @@ __host__ __device__ inline RingUse last_use(int stages, int issued, int k)
     return {i % stages, (uint32_t)(i / stages) & 1u};
 }
 
-// A kernel that reads nothing of the one before it, which let it start only after its
-// own wait (so that all before that one is complete), need not wait but at its end.
+// A kernel that reads nothing of the one before it need not wait but at its end, if
+// that one let it start only after its own wait: all that it reads was then written by
+// kernels which had completed, their writes performed, before this one's first block
+// began.  That is the order of completion; griddepcontrol.wait promises visibility to
+// the grid that waits, which is the one before.  So an early kernel reads global memory
+// through L2 only, where those writes are: tiles by TMA, everything else by loads that
+// pass L1 over (load_l2), in which lines from before them could lie.
 enum { CHAIN_NONE = 0, CHAIN_EARLY = 1 };
 
 template <class P>

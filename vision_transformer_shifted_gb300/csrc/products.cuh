@@ -236,6 +236,8 @@ __device__ __forceinline__ void add16(float (&v)[V], const uint4 &u)
         }
     }
 }
+// 16 bytes from L2 (the kernel may be an early one: CHAIN_EARLY).
+__device__ __forceinline__ uint4 load_l2(const void *p) { return __ldcg(static_cast<const uint4 *>(p)); }
 template <class T>
 __device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols, int c, int slice, int slices, float *part)
 {
@@ -247,12 +249,12 @@ __device__ __forceinline__ void column_slice(const T *p, int64_t rows, int cols,
     for (; i + 7 * (int64_t)slices < rows; i += 8 * (int64_t)slices) {
         uint4 u[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(p + (i + k * (int64_t)slices) * cols + c);
+        for (int k = 0; k < 8; ++k) u[k] = load_l2(p + (i + k * (int64_t)slices) * cols + c);
 #pragma unroll
         for (int k = 0; k < 8; ++k) add16<T>(v, u[k]);
     }
 #pragma unroll 1
-    for (; i < rows; i += slices) add16<T>(v, *reinterpret_cast<const uint4 *>(p + i * cols + c));
+    for (; i < rows; i += slices) add16<T>(v, load_l2(p + i * cols + c));
 #pragma unroll
     for (int e = 0; e < V; e += 4)
         *reinterpret_cast<float4 *>(part + (int64_t)slice * cols + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -270,8 +272,7 @@ __device__ __forceinline__ void column_few(const T *p, int rows, int cols, int c
         uint4 u[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            u[k] = in && i + 8 * k < rows ? *reinterpret_cast<const uint4 *>(p + (int64_t)(i + 8 * k) * cols + c)
-                                          : make_uint4(0, 0, 0, 0);
+            u[k] = in && i + 8 * k < rows ? load_l2(p + (int64_t)(i + 8 * k) * cols + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) add16<T>(v, u[k]);
     }
