@@ -364,10 +364,14 @@ int clusters_of(int dev, int split, bool alone, Ask &&ask)
     if (keep && n) known[dev][alone][split].store(n);
     return n;
 }
-int few_clusters(int split, bool alone)
+int current_device()   // (-1: none)
 {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    return dev;
+}
+int few_clusters(int dev, int split, bool alone)
+{
     const int n = clusters_of(dev, split, alone, [&] { return ask_clusters(split, alone); });
     return n ? n : (alone ? 1 : 2) * sm_count() / split;
 }
@@ -380,6 +384,9 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     // CTAs a tile: until there is one for every SM, with two K blocks each at least
     a.tiles = (width + W - 1) / W;
     const int chunks = FORM <= FORM_LINEAR ? (a.rows + FEW_ROWS - 1) / FEW_ROWS : 1, tiles = a.tiles * chunks;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     a.split = 1;
     while (a.split < 8 && tiles * a.split < sm_count() && a.kb >= 4 * a.split) a.split *= 2;
     if (FORM <= FORM_LINEAR) a.split = few_split(tiles, a.kb);
@@ -387,15 +394,12 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
     // where all clusters find room so, one with twice the ring (128 x 8192 x 512, 32 CTAs,
     // 12.4 us and 11.3; 16 rows no change, and the next kernel starts later; sixteen
     // clusters of eight, of which fifteen fit: 385 x 2968 x 400 9.7 and 12.4).
-    const bool alone = FORM <= FORM_LINEAR && a.np >= 64 && tiles <= few_clusters(a.split, true);
+    const bool alone = FORM <= FORM_LINEAR && a.np >= 64 && tiles <= few_clusters(dev, a.split, true);
     a.stage_bytes = 16384 + a.np * 128;
     a.stages = (alone ? FEW_RING_ALONE : FEW_RING) / a.stage_bytes;
     static_assert(FEW_RING_ALONE / (16384 + 16 * 128) <= FEW_MAX_STAGES && 3 * (16384 + 128 * 128) <= FEW_RING, "ring");
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes;
     static std::atomic<uint64_t> ready;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
         e = cudaFuncSetAttribute(few_rows_kernel<FORM, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -431,10 +435,10 @@ cudaError_t launch_few(FewArgs &a, int width, cudaStream_t stream)
 // 1024, 9.8 and 12.3), with four K blocks each at least.
 int few_split(int64_t tiles, int kb)
 {
-    const int most = tiles <= few_clusters(16, true) ? 16 : 8;
+    const int dev = current_device(), most = tiles <= few_clusters(dev, 16, true) ? 16 : 8;
     int split = 1;
     for (int s = 2; s <= most && kb >= 4 * s; ++s)
-        if (tiles <= few_clusters(s, false)) split = s;
+        if (tiles <= few_clusters(dev, s, false)) split = s;
     return split;
 }
 
