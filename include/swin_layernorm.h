@@ -8,17 +8,17 @@
  *   s = x + residual (rounded to bf16; s = x without a residual)
  *   mu = mean_c s;  var = mean_c (s - mu)^2;  r = 1 / sqrt(var + eps);  n = (s - mu) r
  *   y = n gamma + beta
- * The statistics are one pass over the row, of its values' differences from a
- * pivot of its own (the mean of its first eight values), not a difference of the
- * large numbers mean s^2 and mu^2: a row of one value has n = 0, and a row far
- * from zero loses nothing.  r's relative error grows with the pivot's distance
- * from the mean, k standard deviations: some (1 + k^2) 2^-24, with k^2 at most C / 8
- * (all of a row's spread in those eight values).  The norm sees the stored
- * (rounded) sum, so that the backward pass, which starts from it, differentiates
- * the very function that ran.  A row holding an infinity or a NaN, or whose first
- * eight values or differences add up to more than 3.4e38, gives NaN; one whose
- * squared differences do has r = 0; with eps = 0, one whose channels are all alike
- * gives NaN or infinities, in the backward pass also in dgamma.  8-bit output: as
+ * The statistics are sums of the row's differences from a pivot (the mean of its
+ * first eight values; where that lies more than sqrt 2 standard deviations from the
+ * row's mean, as beside a large channel, the sums are taken again about the mean),
+ * not a difference of the large numbers mean s^2 and mu^2: a row of one value has n
+ * = 0, a row far from zero loses nothing, and r's relative error is a few 2^-24
+ * (185 at most, from chains of 40 additions) whatever the row holds.  The norm sees
+ * the stored (rounded) sum, so that the backward pass, which starts from it,
+ * differentiates the very function that ran.  A row holding an infinity or a NaN, or
+ * whose first eight values or differences add up to more than 3.4e38, gives NaN; one
+ * whose squared differences do has r = 0; with eps = 0, one whose channels are all
+ * alike gives NaN or infinities, in the backward pass also in dgamma.  8-bit output: as
  * swin_block_rms_forward_q8 (swin_rms.h): scale = max(max_c |y|, 1e-30) / 448
  * per row, code = y / scale (both fp32 quotients) rounded to nearest even in
  * e4m3, NaN codes and a NaN scale for a row with a NaN.

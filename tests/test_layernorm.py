@@ -371,6 +371,36 @@ def test_a_rows_spread_in_its_first_values(C, where):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [8, 96, 520, 768, 2744, 4096, 8200, 16384])
+@pytest.mark.parametrize("size", [16.0, 300.0, -30000.0])
+def test_statistics_do_not_depend_on_where_a_large_channel_lies(C, size):
+    """One channel far above the others, wherever it lies: n in fp32, as dgamma gives it
+    for one row and dy = 1, and the e4m3 form's scale, max |n| / 448.
+
+    With u = 2^-24 and at most 40 additions one after the other, sums about a pivot k
+    standard deviations from the row's mean leave r off by 61 u (1 + k^2) + 2 u, and n by as
+    much of itself and 48 u sqrt(1 + k^2) (the test above).  k^2 is at most two, whatever the
+    row's first values are: else the sums are taken again about the mean."""
+    u = 2.0 ** -24
+    one, zero = torch.ones(C).to(BF), torch.zeros(C).to(BF)
+    with layernorm(C) as h:
+        for at in sorted({0, 5, 8 % C, C // 2, C - 1}):
+            x = inputs(1, C, False, seed=at)[0]
+            x[0, at] = size
+            n = normalise(x)[0]
+            en = (61 * 3 + 2) * 1.01 * u * n.abs() + 48 * 1.01 * 3 ** 0.5 * u
+            xd, gd, bd = dev(x, one, zero)
+            dg = torch.empty(C, device=DEV)
+            sw.swin_block_layernorm_backward(h, xd, gd, gd.view(1, C), torch.empty_like(xd), dg)
+            close(dg[None], n, en)   # (1.01: the sums that decide are rounded too)
+            for rows in (1, 200):
+                codes, scales = torch.empty(rows, C, dtype=E4M3, device=DEV), torch.empty(rows, device=DEV)
+                sw.swin_block_layernorm_forward_q8(h, xd.expand(rows, C).contiguous(), gd, bd, codes, scales)
+                i = int(n.abs().argmax())
+                close(scales, (n.abs()[0, i] / 448).expand(rows), (en[0, i] / 448 + 2 * u * n.abs()[0, i] / 448).expand(rows))
+
+
+@pytest.mark.gpu
 def test_rows_past_32_bits_of_elements():
     """rows * C > 2^31: rows at the beginning, around the 2^31st element and at the
     end; the parameters' sums over all of them.  In fp32: some 863 rows a block one

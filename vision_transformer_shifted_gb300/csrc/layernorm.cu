@@ -5,16 +5,19 @@
 // As the root-mean-square norm (rms.cu): every input is read once and every
 // output written once, the row stays in registers (the backward: shared memory)
 // between the statistics and the output, and HBM bounds it: 200704 x 96 with the
-// residual 23.7 us, 6.5 TB/s; post-norm 589824 x 192 103.7 us, 6.55 TB/s; e4m3
-// 8191 x 4096 39.7 us, 5.9 TB/s; backward 589824 x 192 with dsum 138.5 us, 6.54 TB/s
-// (half of the issue slots).  The
-// statistics are one sum a row, of s - p and of its square, p being the mean of
-// the row's first eight values: sum s^2 - C mu^2 (p = 0) would lose what a row's
-// mean has above its spread; of values around p the variance keeps all but
-// log2(1 + k^2) of fp32's bits, p lying k standard deviations from the mean (k^2 is
-// C / 8 at most, whatever the row holds, and some 0.1 as a rule), and a row of one
-// value gives exact zeros.  (Two sums one after the other, the mean first: e4m3
-// 8191 x 4096 43.0 us, backward 589824 x 192 151.)
+// residual 23.9 us, 6.5 TB/s; post-norm 589824 x 192 97.4 us, 7.0 TB/s; e4m3 8191 x
+// 4096 40.0 us, 5.9 TB/s; backward 589824 x 192 with dsum 137 us, 6.6 TB/s (half of the
+// issue slots).  The statistics are one sum a row, of s - p and of its square, p being
+// the mean of the row's first eight values: sum s^2 - C mu^2 (p = 0) would lose what a
+// row's mean has above its spread; of values around p the variance keeps all but
+// log2(1 + k^2) of fp32's bits, p lying k standard deviations from the mean, and a row
+// of one value gives exact zeros.  k is some 0.35 as a rule, but sqrt(C / 8) beside a
+// large channel among the eight: above sqrt 2 (one random row in 16,000) the row's sums
+// are taken again about the mean, from registers or shared memory (a large channel
+// there in every row: e4m3 8191 x 4096 44.1 us, backward 30010 x 2744 124 for 91.5).
+// (Always two sums one after the other, the mean first: e4m3 8191 x 4096 43.0 us,
+// backward 589824 x 192 151; each thread about its own values' mean, the threads'
+// variances joined: 40.7 us, backward 30010 x 2744 112.6.)
 #include <cmath>
 #include <new>
 
@@ -56,6 +59,14 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, int lpr, float2 *re
 // The sum of a piece's eight values.
 __device__ __forceinline__ float piece_sum(const Piece &v) { return sum2(add2(add2(v.v[0], v.v[1]), add2(v.v[2], v.v[3]))); }
 
+// Whether a row's sums of s - p and of its square say that p lies more than sqrt 2
+// standard deviations from the mean: they are then taken again about the mean.
+__device__ __forceinline__ bool far_pivot(float sum, float squares, float inv_c)
+{
+    const float mean = sum * inv_c;
+    return 1.5f * mean * mean > squares * inv_c;   // (not for a NaN, nor for infinite squares)
+}
+
 // 1 / sqrt(var + eps) from the row's sums of s - p and of its square; mean: of s - p.
 __device__ __forceinline__ float deviation(float sum, float squares, float inv_c, float eps, float &mean)
 {
@@ -63,12 +74,16 @@ __device__ __forceinline__ float deviation(float sum, float squares, float inv_c
     return rsqrtf(max_nan(fmaf(-mean, mean, squares * inv_c), 0.f) + eps);   // (infinite squares: r = 0)
 }
 
+// Threads of a block whose rows lie on part of a warp.  Post-norm: few, whose loads and
+// stores mix with other blocks' (589824 x 192 97.1 us, by 256 threads 102.8; 200000 x 512,
+// a power of two, 96.0 and 105 to 108 us).
+constexpr int forward_threads(int form) { return form == FORM_POST ? 64 : 256; }
+
 // (Blocks of a row: registers for two of 512 threads an SM, more in flight: post-norm
 // 20000 x 6000 117 us, 204 without.  Rows on part of a warp: no such request, the
-// compiler's own count; asked for one block it takes up to 9 registers more, post-norm
-// 200000 x 512 93.7 us and 104.)
+// compiler's own count.)
 template <int CPL, bool BLOCK, int FORM>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_forward_kernel(LnArgs a)
+__global__ void __launch_bounds__(BLOCK ? 512 : forward_threads(FORM), BLOCK ? 2 : 0) layernorm_forward_kernel(LnArgs a)
 {
     __shared__ float2 red[16];
     __shared__ float amaxes[16];
@@ -86,9 +101,10 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_fo
     // own places (as plain loads the compiler puts them off until they are used:
     // 589824 x 192 113 us)
     extern __shared__ uint4 later[];   // a block's row: [CPL][blockDim.x]
-    __shared__ uint4 later256[FORM == FORM_POST && !BLOCK ? CPL * 256 : 1];
-    const uint32_t own = smem_u32(BLOCK ? later : later256) + threadIdx.x * 16;
-    const uint32_t own_step = (BLOCK ? blockDim.x : 256) * 16;
+    constexpr int THREADS = forward_threads(FORM);
+    __shared__ uint4 warps_later[FORM == FORM_POST && !BLOCK ? CPL * THREADS : 1];
+    const uint32_t own = smem_u32(BLOCK ? later : warps_later) + threadIdx.x * 16;
+    const uint32_t own_step = (BLOCK ? blockDim.x : THREADS) * 16;
     uint4 s[CPL], t[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
@@ -130,18 +146,24 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_fo
     float p = piece_sum(piece(BLOCK ? head : s[0])) * 0.125f;
     if (!BLOCK) p = __shfl_sync(0xffffffffu, p, lane - li);
     auto minus_p = [&](int k) { return li + k * step < a.chunks ? pack2(-p) : pack2(0.f); };   // (behind the row: zeros)
-    f2 sum2v = 0, sq2v = 0;
+    auto sums = [&](float &sum, float &sq) {
+        f2 sum2v = 0, sq2v = 0;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) {
-        const Piece v = piece(s[k]);
-        const f2 m = minus_p(k);
+        for (int k = 0; k < CPL; ++k) {
+            const Piece v = piece(s[k]);
+            const f2 m = minus_p(k);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const f2 d = add2(v.v[e], m);
-            sum2v = add2(sum2v, d);
-            sq2v = fma2(d, d, sq2v);
+            for (int e = 0; e < 4; ++e) {
+                const f2 d = add2(v.v[e], m);
+                sum2v = add2(sum2v, d);
+                sq2v = fma2(d, d, sq2v);
+            }
         }
-    }
+        sum = sum2(sum2v);
+        sq = sum2(sq2v);
+    };
+    float sum, sq;
+    sums(sum, sq);
     uint4 gm[CPL], bt[CPL];   // (asked for before the row's sums are known)
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
@@ -150,22 +172,30 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 2 : 0) layernorm_fo
         gm[k] = ok ? ld16(a.gamma + c * 8) : make_uint4(0, 0, 0, 0);
         bt[k] = ok && a.beta ? ld16(a.beta + c * 8) : make_uint4(0, 0, 0, 0);
     }
-    float sum = sum2(sum2v), sq = sum2(sq2v);
     row_sum2<BLOCK>(sum, sq, a.lpr, red);
-    if (BLOCK) store_sum();   // (in place: only now has every thread read the row's first piece)
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {   // (kept packed: fewer registers, more rows in flight)
         forget(s[k]);
         forget(gm[k]);
         forget(bt[k]);
     }
-    float mean;
-    const float r = deviation(sum, sq, a.inv_c, a.eps, mean);
-    const f2 r2 = pack2(r), shift = pack2(-mean * r);
     if (FORM == FORM_POST) {
         cp_async_commit();
         cp_async_wait<0>();
     }
+    const bool far = far_pivot(sum, sq, a.inv_c);   // (the same for a row's threads)
+    if (BLOCK ? far : __any_sync(0xffffffffu, far)) {
+        if (far) p += sum * a.inv_c;
+        sums(sum, sq);
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) forget(s[k]);
+        if (BLOCK) __syncthreads();   // (the first sums have been read)
+        row_sum2<BLOCK>(sum, sq, a.lpr, red);
+    }
+    if (BLOCK) store_sum();   // (in place: only now has every thread read the row's first piece)
+    float mean;
+    const float r = deviation(sum, sq, a.inv_c, a.eps, mean);
+    const f2 r2 = pack2(r), shift = pack2(-mean * r);
     if (FORM != FORM_Q8) {
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
@@ -323,16 +353,25 @@ __global__ void __launch_bounds__(256, blocks_per_sm(CPL, DSUM)) layernorm_backw
         fetch(row + hop, other);
         cp_async_wait<1>();
         const bool row_ok = row < a.rows;   // (no row: its pieces hold whatever was there, and count for nothing)
-        const float p = __shfl_sync(0xffffffffu, piece_sum(piece(lds16(at))) * 0.125f, lane - li);
-        RowSums w{0, 0, 0, 0};
+        float p = __shfl_sync(0xffffffffu, piece_sum(piece(lds16(at))) * 0.125f, lane - li);
+        auto row_sums = [&]() {
+            RowSums w{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            forget(g[k]);   // (kept packed)
-            if (have[k]) piece_sums(lds16(at + k * 4096), lds16(at + (CPL + k) * 4096), g[k], pack2(-p), w);
+            for (int k = 0; k < CPL; ++k) {
+                forget(g[k]);   // (kept packed)
+                if (have[k]) piece_sums(lds16(at + k * 4096), lds16(at + (CPL + k) * 4096), g[k], pack2(-p), w);
+            }
+            float4 v = make_float4(sum2(w.sum), sum2(w.sq), sum2(w.a), sum2(w.dot));
+            lane_sum2(v.x, v.y, step);
+            lane_sum2(v.z, v.w, step);
+            return v;
+        };
+        float4 sums = row_sums();
+        const bool far = row_ok && far_pivot(sums.x, sums.y, a.inv_c);   // (the same for a row's lanes)
+        if (__any_sync(0xffffffffu, far)) {
+            if (far) p += sums.x * a.inv_c;
+            sums = row_sums();
         }
-        float4 sums = make_float4(sum2(w.sum), sum2(w.sq), sum2(w.a), sum2(w.dot));
-        lane_sum2(sums.x, sums.y, step);
-        lane_sum2(sums.z, sums.w, step);
         if (row_ok) {
             const RowGrad grad = row_grad(p, sums, a.inv_c, a.eps);
             bf16 *dx = a.dx + (row * a.chunks + li) * 8;
@@ -476,17 +515,25 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_wide_kernel(LnBwdAr
     int turn = 0;
 #pragma unroll 1
     for (int64_t row = first; row < a.rows; row += hop) {   // (the same for a group's threads)
-        const float p = piece_sum(piece(head)) * 0.125f;
+        float p = piece_sum(piece(head)) * 0.125f;
         fetch();
         cp_async_wait<DEPTH - 1>();
-        RowSums w{0, 0, 0, 0};
+        auto row_sums = [&]() {
+            RowSums w{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            forget(g[k]);   // (kept packed)
-            if (have[k]) piece_sums(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], pack2(-p), w);
+            for (int k = 0; k < CPL; ++k) {
+                forget(g[k]);   // (kept packed)
+                if (have[k]) piece_sums(lds16(place(at, 0, k)), lds16(place(at, 1, k)), g[k], pack2(-p), w);
+            }
+            float4 v = make_float4(sum2(w.sum), sum2(w.sq), sum2(w.a), sum2(w.dot));
+            group_sum4(v, step, group, turn++, red);
+            return v;
+        };
+        float4 sums = row_sums();
+        if (far_pivot(sums.x, sums.y, a.inv_c)) {   // (the same for the group's threads)
+            p += sums.x * a.inv_c;
+            sums = row_sums();
         }
-        float4 sums = make_float4(sum2(w.sum), sum2(w.sq), sum2(w.a), sum2(w.dot));
-        group_sum4(sums, step, group, turn++, red);
         const RowGrad grad = row_grad(p, sums, a.inv_c, a.eps);
         bf16 *dx = a.dx + row * C + li * 8;
 #pragma unroll
@@ -543,8 +590,8 @@ cudaError_t launch_forward(LnArgs a, cudaStream_t stream)
     const int most = a.rows < sm_count() ? 1 : FWD_PIECES;
     const RowPlan p = plan_row(a.chunks, most, most);
     a.lpr = p.block ? 32 : p.lanes;
-    const int threads = p.block ? p.lanes : 256;
-    const int64_t rpb = p.block ? 1 : 8 * (32 / p.lanes);
+    const int threads = p.block ? p.lanes : forward_threads(FORM);
+    const int64_t rpb = p.block ? 1 : threads / 32 * (32 / p.lanes);
     const unsigned grid = (unsigned)((a.rows + rpb - 1) / rpb);
 #define SWIN_LN_CASE(n)                                                                       \
     case n:                                                                                   \
