@@ -82,12 +82,12 @@ def _build_arguments():
     if res.returncode != 0:
         raise RuntimeError(res.stdout + res.stderr)
     os.replace(tmp, ARGUMENTS)
+    os.makedirs(BUILD, exist_ok=True)
     with open(ARGUMENTS_TORCH, "w") as f:
         f.write(version)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         beside = ex.submit(_build_arguments) if force or not arguments_current() else None
         if force or not _library_current():
@@ -101,6 +101,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
 
 def _build_library(verbose, extra_flags):
+    os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
 
     def compile_one(src):
