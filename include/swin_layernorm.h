@@ -12,8 +12,8 @@
  * first eight values; where that lies more than sqrt 2 standard deviations from the
  * row's mean, as beside a large channel, the sums are taken again about the mean),
  * not a difference of the large numbers mean s^2 and mu^2: a row of one value has n
- * = 0, a row far from zero loses nothing, and r's relative error is a few 2^-24
- * (185 at most, from chains of 40 additions) whatever the row holds.  The norm sees
+ * = 0, a row far from zero loses nothing, and r's relative error is some 2^-21
+ * (185 2^-24 at most, from chains of 40 additions) whatever the row holds.  The norm sees
  * the stored (rounded) sum, so that the backward pass, which starts from it,
  * differentiates the very function that ran.  A row holding an infinity or a NaN, or
  * whose first eight values or differences add up to more than 3.4e38, gives NaN; one

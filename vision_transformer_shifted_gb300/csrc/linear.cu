@@ -76,8 +76,8 @@ Product forward_product(int C, int N, int rows)
 // rows with K shared by a cluster, rather than to pairs of CTAs: few tiles of a long
 // K.  Estimates in us, from both ways at 25 sizes: there 6.5 and its operands at 13
 // TB/s from L2 or half a microsecond a K block of a CTA, here 4.5 and 0.25 to 0.29 a K
-// block of the pairs' longest way, 13 for a join (385 x 2968 x 400 17.7 us by pairs, 10.0;
-// 800 x 8192 x 1024 26.6, 20.3; 700 x 4096 x 120 12.6, 9.1; not taken: 300 x 1032 x 2056
+// block of the pairs' longest way, 13 for a join (385 x 2968 x 400 17.7 us by pairs, 9.7;
+// 800 x 8192 x 1024 26.4, 20.3; 700 x 4096 x 120 12.5, 9.0; not taken: 300 x 1032 x 2056
 // 10.2, 11.3; 3779 x 2832 x 424 16.7, 21.5).
 bool few_chosen(const Product &p, const ProductsPlan &pl, int elems)
 {

@@ -133,7 +133,8 @@ __device__ __forceinline__ void staging_free(int lane)
 // D = A B^T over up to two K segments (dx = dg Wg + du Wu), A and B each K-major
 // or MN-major as stored: no operand is ever transposed in memory.  Up to three
 // problems run as one launch (the three weight gradients).  The tensor cores bind
-// it (8192 x 8192 x 2048 with the residual: 156 us, 1.76 PFLOP/s); with K of a few
+// it (8192 x 8192 x 2048 with the residual: 173 to 178 us a call at the board's power
+// limit, 1.55 to 1.59 PFLOP/s; one launch alone 158); with K of a few
 // hundred its operands' way from L2 does (12544 x 2736 x 512: 30 us at 10 TB/s).
 //
 // Tiles are dealt to the pairs in rounds; a last round that would leave pairs
