@@ -401,6 +401,45 @@ def test_statistics_do_not_depend_on_where_a_large_channel_lies(C, size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [8, 40, 96, 520, 768, 2744, 8200, 16384])
+@pytest.mark.parametrize("rows", [37, 400])
+def test_rows_beside_one_with_a_large_first_channel_keep_their_bits(rows, C):
+    """Rows share warps, groups and blocks with others; each has statistics of its own,
+    also where a neighbour's are taken twice, and in place."""
+    x, r, g, b, dy = inputs(rows, C, True, seed=25)
+    big = x.clone()
+    big[5, 0] = big[rows - 1, 3] = 30000.0
+    big[7, 2] = float("nan")
+    rest = [i for i in range(rows) if i not in (5, 7, rows - 1)]
+    rd, gd, bd, yd = dev(r, g, b, dy)
+
+    def call(x, h):
+        x, o = x.to(DEV), [torch.empty(rows, C, dtype=BF, device=DEV) for _ in range(4)]
+        codes, scales = torch.empty(rows, C, dtype=E4M3, device=DEV), torch.empty(rows, device=DEV)
+        sw.swin_block_layernorm_forward(h, x, gd, bd, o[0], residual=rd, out_sum=o[1])
+        sw.swin_block_layernorm_forward_post(h, x, gd, bd, rd, o[2])
+        sw.swin_block_layernorm_forward_q8(h, x, gd, bd, codes, scales)
+        sw.swin_block_layernorm_backward(h, x, gd, yd, o[3], torch.empty(C, device=DEV), dsum=rd)
+        over, into = x.clone(), rd.clone()
+        sw.swin_block_layernorm_forward(h, over, gd, bd, into, residual=into, out_sum=over)
+        assert torch.equal(into.nan_to_num(7.0), o[0].nan_to_num(7.0))
+        assert torch.equal(over.nan_to_num(7.0), o[1].nan_to_num(7.0))
+        return *o, codes.float(), scales
+
+    with layernorm(C) as h:
+        alone, beside = call(x, h), call(big, h)
+    for p, q in zip(alone, beside):
+        assert torch.equal(p[rest], q[rest])
+    for q in beside[:1] + beside[2:]:
+        assert q[7].isnan().all() and torch.isfinite(q[5]).all()
+    some = [5, rows - 1]
+    _, y, e = reference(big[some], r[some], g, b)
+    close(beside[0][some], y, HALF * y.abs() + 1.01 * e)
+    ref, err = gradients(big[some], g, dy[some], r[some])
+    close(beside[3][some], ref[0], HALF * ref[0].abs() + 1.01 * err[0])
+
+
+@pytest.mark.gpu
 def test_rows_past_32_bits_of_elements():
     """rows * C > 2^31: rows at the beginning, around the 2^31st element and at the
     end; the parameters' sums over all of them.  In fp32: some 863 rows a block one

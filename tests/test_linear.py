@@ -807,6 +807,31 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 5, 200])
+def test_weights_past_32_bits(rows):
+    """W and dW of more than 2^31 elements: outputs on both sides of that, dx over all of
+    W's rows, dW around the 2^31st element and at its end."""
+    C, N = 65536, 32776
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=DEV) * std).to(BF)  # noqa: E731
+    x, w, b, dy = n(rows, C), n(N, C, std=C ** -0.5), n(N, std=0.3), n(rows, N)
+    some = [0, 1, 32766, 32767, 32768, 32769, N - 1]
+    out, dx, dW, db = nans(rows, N), nans(rows, C), nans(N, C), nans(N)
+    with linear(C, N) as h:
+        sw.swin_block_linear_forward(h, x, w, b, out)
+        sw.swin_block_linear_backward(h, x, w, dy, dx, dW, db)
+        sw.swin_block_linear_sync_status(h)
+    _, ref, _, tol = forward_ref(x, w[some], b[some], None, "none")
+    close(out[:, some], ref.cpu(), tol.cpu())
+    ref, tol = backward_ref(x, w[some], None, dy[:, some], "none")
+    close(dW[some], ref["dW"].cpu(), tol["dW"].cpu())
+    close(db[some], ref["db"].cpu(), tol["db"].cpu())
+    at = [0, 1, 255, 256, 40000, C - 1]   # columns of dx, over all of W's rows
+    ref, tol = backward_ref(x[:, at], w[:, at], None, dy, "none")
+    close(dx[:, at], ref["dx"].cpu(), tol["dx"].cpu())
+
+
+@pytest.mark.gpu
 def test_simulated_allocation_failure_then_a_normal_call():
     rows, C, N = 1000, 8192, 1032
     x, w, b, _, dy = make(rows, C, N, seed=12)
